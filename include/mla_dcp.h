@@ -382,6 +382,147 @@ mla_status gqa_decode_partial(const void* q, const gqa_kv_pages* kv, const int32
 mla_status gqa_shard_combine(const float* partials, const float* lses, int num_shards,
                              const gqa_shape* shape, void* out, float* lse_out, void* stream);
 
+/*
+ * Rotary positions.  Pair i < rot_dim / 2 of a head turns by position *
+ * inv_freq[i] radians:
+ *     y_a = f (x_a cos - x_b sin),  y_b = f (x_a sin + x_b cos),
+ *     f = attention_factor,
+ * with (a, b) = first_dim + (2i, 2i + 1) if interleaved, else first_dim +
+ * (i, i + rot_dim / 2).  Dims outside [first_dim, first_dim + rot_dim) pass
+ * through.  Computed in fp32 and rounded once; the angle is reduced modulo a
+ * turn in 64-bit integers, so far positions lose no accuracy.  Scalings for
+ * long contexts enter through inv_freq and attention_factor.
+ */
+typedef struct mla_rope {
+  const double* inv_freq;  /* device, [rot_dim / 2], radians per token, finite; 8-byte aligned */
+  int rot_dim;             /* multiple of 16, >= 16, at most the head's width */
+  int first_dim;           /* multiple of 8; first_dim + rot_dim <= the head's width */
+  int interleaved;         /* 0 or 1 */
+  float attention_factor;  /* finite */
+} mla_rope;
+
+/* The new tokens of a step: request b appends its last n_b = q_lens[b] (or
+ * q_len) tokens to a context that then has seq_lens[b] tokens, i.e. token i
+ * stands at position seq_lens[b] - n_b + i -- the same seq_lens and q_lens the
+ * attention calls of the step take.  Rows i >= n_b are padding: nothing is
+ * read from or written for them. */
+typedef struct mla_tokens {
+  int batch;                    /* B >= 1 */
+  int q_len;                    /* >= 1 (the padded count, see q_lens) */
+  const int32_t* seq_lens;      /* device [B] */
+  const int32_t* q_lens;        /* device [B] in [1, q_len], or NULL (all q_len); clamped */
+  const int32_t* positions;     /* device [B, q_len]: rotary positions (any int32), or NULL
+                                   (where the token stands); cache slots do not change */
+} mla_tokens;
+
+/*
+ * Rotates query heads: x bf16, token (b, i)'s heads [num_heads, head_dim]
+ * contiguous at x + (b * q_len + i) * x_stride elements; out likewise with
+ * out_stride.  out == x with equal strides rotates in place (and moves only
+ * the rotated dims); otherwise the two must not overlap.  head_dim a multiple
+ * of 8, at most 1024; strides multiples of 8, at least num_heads * head_dim.
+ * tokens->seq_lens may be NULL if positions is given.  Padding rows of out
+ * are left as they were.
+ */
+mla_status mla_rope_apply(const void* x, long long x_stride, void* out, long long out_stride,
+                          const mla_tokens* tokens, int num_heads, int head_dim,
+                          const mla_rope* rope, void* stream);
+
+/*
+ * Appends a step's latent rows to the paged latent cache, and rotates the
+ * step's queries in the same launch.
+ *   latent  bf16, row (b, i) of 576 values at latent + (b * q_len + i) *
+ *           latent_stride; rotated by `rope` (in a latent row the rope dims
+ *           are 512..575: first_dim 512), or stored as it is if rope is NULL
+ *   kv      the cache; its data (and scale) are written.  bf16: values rounded
+ *           once.  e4m3: each row gets as its scale the smallest power of two
+ *           s >= 2^-60 with max|x| <= 448 s over its finite values, and the
+ *           codes of x / s; an infinite or NaN value is stored as NaN.
+ *   q, q_out bf16 [.., num_heads, 576] rows as in mla_rope_apply (rope must be
+ *           given then), or q NULL
+ * Whole-request caches: num_shards 1, shard_id 0.  num_shards N > 1: the cache
+ * is shard shard_id's MLA_LAYOUT_INTERLEAVED_LOCAL slice; tokens of other
+ * shards are skipped.  (CONTIGUOUS_LOCAL slices move as a context grows and
+ * are not appended to.)  Only the new tokens' rows change.  The pages they
+ * fall on must belong to one request each.
+ *
+ * workspace: 256 bytes of device memory, zeroed once before its first use:
+ * MLA_ERR_DEVICE_BOUNDS (a page outside [0, num_pages): its rows are not
+ * written) and MLA_ERR_INVALID (a q_lens entry outside [1, q_len], or more new
+ * tokens than seq_lens) stay there until mla_get_device_error reads them.
+ */
+mla_status mla_cache_append(const void* latent, long long latent_stride, const mla_kv_pages* kv,
+                            const int32_t* block_table, int max_pages_per_req,
+                            const mla_tokens* tokens, const mla_rope* rope, const void* q,
+                            long long q_stride, void* q_out, long long q_out_stride,
+                            int num_heads, int shard_id, int num_shards, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
+/*
+ * A GQA cache held in e4m3 with a scale for each block of tokens and KV head
+ * (or, for gqa_cache_append, in bf16 with null scales):
+ *   k, v              e4m3 (or bf16) [num_pages, 64, Hkv, 128]
+ *   k_scale, v_scale  fp32 [num_pages, 64 / block, Hkv]: value of row r, head h
+ *                     = code * scale[page][r / block][h]
+ * Scales written by gqa_cache_append are powers of two; the attention takes
+ * any finite scale (a V scale below 2^-60 in magnitude weighs its block with
+ * that much less precision, 0 is exact).
+ */
+typedef struct gqa_block_pages {
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  mla_kv_dtype dtype;
+  int block;            /* tokens per scale: 1, 2, 4, .. 64 (ignored for bf16) */
+  int num_pages;        /* >= 1 */
+  int page_size;        /* must be 64 */
+  int num_kv_heads;
+} gqa_block_pages;
+
+/*
+ * Appends a step's K and V heads to the paged GQA cache, and rotates the
+ * step's queries in the same launch.  k, v: bf16, token (b, i)'s heads
+ * [Hkv, 128] at k + (b * q_len + i) * k_stride; k is rotated by `rope` (NULL:
+ * stored as it is), v never.  Sharding, q, workspace and errors as for
+ * mla_cache_append.
+ *
+ * e4m3: for each block of `block` token slots, KV head and cache, with a the
+ * largest finite |x| of the new tokens in it and s_new the smallest power of
+ * two >= 2^-60 with a <= 448 s_new: a block without earlier tokens (slots
+ * before the request's first new token) takes s = s_new; otherwise s = the
+ * block's scale s_old if |s_old| >= s_new (or s_old is NaN), else s = s_new
+ * and the earlier tokens' codes are rounded again, to code * s_old / s.  With
+ * power-of-two scales that is exact except for codes that become subnormal.
+ * New codes are x / s.  Slots behind the context are left as they were.
+ */
+mla_status gqa_cache_append(const void* k, long long k_stride, const void* v, long long v_stride,
+                            const gqa_block_pages* cache, const int32_t* block_table,
+                            int max_pages_per_req, const mla_tokens* tokens, const mla_rope* rope,
+                            const void* q, long long q_stride, void* q_out,
+                            long long q_out_stride, int num_heads, int shard_id, int num_shards,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes gqa_decode_partial_fp8 needs (0 for invalid or unsupported shapes). */
+size_t gqa_fp8_workspace_size(const gqa_shape* shape, int num_shards, int shard_id);
+
+/*
+ * gqa_decode_partial over an e4m3 cache with block scales (cache->dtype
+ * MLA_KV_FP8_E4M3).  Differences from gqa_decode_partial: any group H / Hkv up
+ * to 64; all four layouts (the *_LOCAL ones with one shard_id); q_lens
+ * (device [B] or NULL) as in mla_shape: rows i >= q_lens[b] give o = 0, lse =
+ * -inf, and with causal query i sees t <= L_b - q_lens[b] + i.  With
+ * INTERLEAVED num_shards must divide 64.  An inf or NaN query value of a row
+ * that attends is reported as MLA_ERR_RANGE; a block-table entry out of range
+ * reads as zeros and is reported as MLA_ERR_DEVICE_BOUNDS.
+ */
+mla_status gqa_decode_partial_fp8(const void* q, const gqa_block_pages* cache,
+                                  const int32_t* block_table, int max_pages_per_req,
+                                  const int32_t* seq_lens, const int32_t* q_lens,
+                                  const gqa_shape* shape, int shard_id, int num_shards,
+                                  mla_layout layout, float* out_partial, float* lse_partial,
+                                  void* workspace, size_t workspace_bytes, void* stream);
+
 /* Static description of a status code. */
 const char* mla_status_string(mla_status status);
 

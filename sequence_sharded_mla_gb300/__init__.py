@@ -55,6 +55,24 @@ class gqa_kv_pages(ctypes.Structure):
                 ("page_size", ctypes.c_int)]
 
 
+class mla_rope(ctypes.Structure):
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("rot_dim", ctypes.c_int),
+                ("first_dim", ctypes.c_int), ("interleaved", ctypes.c_int),
+                ("attention_factor", ctypes.c_float)]
+
+
+class mla_tokens(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int), ("q_len", ctypes.c_int), ("seq_lens", ctypes.c_void_p),
+                ("q_lens", ctypes.c_void_p), ("positions", ctypes.c_void_p)]
+
+
+class gqa_block_pages(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("dtype", ctypes.c_int), ("block", ctypes.c_int),
+                ("num_pages", ctypes.c_int), ("page_size", ctypes.c_int),
+                ("num_kv_heads", ctypes.c_int)]
+
+
 _LIB = None
 EXPORTS = ("mla_decode_partial", "mla_decode_partial_noalloc", "mla_decode_partial_dcp",
            "mla_shard_combine",
@@ -62,7 +80,9 @@ EXPORTS = ("mla_decode_partial", "mla_decode_partial_noalloc", "mla_decode_parti
            "mla_workspace_size", "mla_get_device_error", "mla_get_device_error_noalloc",
            "mla_set_wait_budget_ns", "mla_set_withhold_query", "mla_set_profile_events",
            "mla_status_string",
-           "mla_version", "gqa_workspace_size", "gqa_decode_partial", "gqa_shard_combine")
+           "mla_version", "gqa_workspace_size", "gqa_decode_partial", "gqa_shard_combine",
+           "mla_rope_apply", "mla_cache_append", "gqa_cache_append", "gqa_fp8_workspace_size",
+           "gqa_decode_partial_fp8")
 
 
 def lib():
@@ -116,6 +136,21 @@ def lib():
         L.gqa_decode_partial.restype = i32
         L.gqa_shard_combine.argtypes = [vp, vp, i32, ctypes.POINTER(gqa_shape), vp, vp, vp]
         L.gqa_shard_combine.restype = i32
+        i64, ptr = ctypes.c_longlong, ctypes.POINTER
+        L.mla_rope_apply.argtypes = [vp, i64, vp, i64, ptr(mla_tokens), i32, i32, ptr(mla_rope), vp]
+        L.mla_rope_apply.restype = i32
+        L.mla_cache_append.argtypes = [vp, i64, ptr(mla_kv_pages), vp, i32, ptr(mla_tokens),
+                                       ptr(mla_rope), vp, i64, vp, i64, i32, i32, i32, vp, sz, vp]
+        L.mla_cache_append.restype = i32
+        L.gqa_cache_append.argtypes = [vp, i64, vp, i64, ptr(gqa_block_pages), vp, i32,
+                                       ptr(mla_tokens), ptr(mla_rope), vp, i64, vp, i64, i32, i32,
+                                       i32, vp, sz, vp]
+        L.gqa_cache_append.restype = i32
+        L.gqa_fp8_workspace_size.argtypes = [ptr(gqa_shape), i32, i32]
+        L.gqa_fp8_workspace_size.restype = sz
+        L.gqa_decode_partial_fp8.argtypes = [vp, ptr(gqa_block_pages), vp, i32, vp, vp,
+                                             ptr(gqa_shape), i32, i32, i32, vp, vp, vp, sz, vp]
+        L.gqa_decode_partial_fp8.restype = i32
         _LIB = L
     return _LIB
 
@@ -521,3 +556,374 @@ def gqa_shard_combine(partials, lses, out=None, lse_out=None, stream=None):
     if st != 0:
         raise MLAError(st, "gqa_shard_combine")
     return out, lse_out
+
+
+def gqa_fp8_workspace_size(batch, q_len, num_heads, num_kv_heads, num_shards,
+                           shard_id=ALL_SHARDS, head_dim=128, causal=False) -> int:
+    sh = _gqa_shape(batch, q_len, num_heads, num_kv_heads, head_dim, causal, 1.0)
+    return int(lib().gqa_fp8_workspace_size(ctypes.byref(sh), int(num_shards), int(shard_id)))
+
+
+def _fp8_types():
+    return (torch.uint8, getattr(torch, "float8_e4m3fn", torch.uint8))
+
+
+def _shape_is(t, name, shape):
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+
+
+def _block_pages(k_cache, v_cache, k_scale, v_scale, dev):
+    """The gqa_block_pages descriptor of an e4m3 (or bf16, without scales) cache."""
+    if k_cache.dtype == torch.bfloat16:
+        types, kv_dtype, block = (torch.bfloat16,), KV_BF16, 0
+        if k_scale is not None or v_scale is not None:
+            raise ValueError("k_scale and v_scale are only for fp8 caches")
+    else:
+        types, kv_dtype, block = _fp8_types(), KV_FP8, 0
+    _check(k_cache, "k_cache", types, 4, dev)
+    _check(v_cache, "v_cache", (k_cache.dtype,), 4, dev)
+    _shape_is(v_cache, "v_cache", k_cache.shape)
+    P, page, Hkv, D = k_cache.shape
+    if D != 128:
+        raise ValueError("k_cache and v_cache must be [P, 64, Hkv, 128]")
+    if kv_dtype == KV_FP8:
+        if k_scale is None or v_scale is None:
+            raise ValueError("fp8 caches need k_scale and v_scale")
+        _check(k_scale, "k_scale", (torch.float32,), 3, dev)
+        _check(v_scale, "v_scale", (torch.float32,), 3, dev)
+        n = k_scale.shape[1]
+        if n < 1 or page % n != 0:
+            raise ValueError("k_scale must be [P, 64 / block, Hkv]")
+        block = page // n
+        _shape_is(k_scale, "k_scale", (P, n, Hkv))
+        _shape_is(v_scale, "v_scale", (P, n, Hkv))
+    return gqa_block_pages(k_cache.data_ptr(), v_cache.data_ptr(),
+                           None if k_scale is None else k_scale.data_ptr(),
+                           None if v_scale is None else v_scale.data_ptr(),
+                           kv_dtype, block, P, page, Hkv)
+
+
+def _on(dev, stream):
+    """The stream of a call on `dev`: the given one, else dev's current one."""
+    s = torch.cuda.current_stream(dev) if stream is None else stream
+    return ctypes.c_void_p(s.cuda_stream)
+
+
+def gqa_decode_partial_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens,
+                           num_shards, layout="interleaved", shard_id=ALL_SHARDS, causal=False,
+                           softmax_scale=None, out_partial=None, lse_partial=None, workspace=None,
+                           stream=None, q_lens=None):
+    """gqa_decode_partial over an e4m3 cache with a scale for each block of
+    tokens and KV head; returns (out_partial, lse_partial, workspace).
+
+    q: bf16 [B, q_len, H, 128]; k_cache, v_cache: e4m3 codes (float8_e4m3fn or
+    uint8) [P, 64, Hkv, 128]; k_scale, v_scale: fp32 [P, 64 / block, Hkv];
+    block_table: int32 [B, max_pages]; seq_lens: int32 [B] (device); q_lens:
+    optional int32 [B] (device) query tokens per request of a padded batch.
+    out_partial: fp32 [n_out, B, q_len, H, 128]; lse_partial: fp32 [n_out, B,
+    q_len, H].  softmax_scale defaults to 1/sqrt(128).
+    """
+    _check(q, "q", (torch.bfloat16,), 4)
+    dev = q.device
+    B, q_len, H, D = q.shape
+    if k_cache.dtype == torch.bfloat16:
+        raise TypeError("k_cache must hold e4m3 codes; gqa_decode_partial takes bf16 caches")
+    pages = _block_pages(k_cache, v_cache, k_scale, v_scale, dev)
+    _check(block_table, "block_table", (torch.int32,), 2, dev)
+    _check(seq_lens, "seq_lens", (torch.int32,), 1, dev)
+    if block_table.shape[0] != B or seq_lens.shape[0] != B:
+        raise ValueError("q, block_table and seq_lens disagree on the number of requests")
+    if q_lens is not None:
+        _check(q_lens, "q_lens", (torch.int32,), 1, dev)
+        _shape_is(q_lens, "q_lens", (B,))
+    scale = 1.0 / math.sqrt(D) if softmax_scale is None else softmax_scale
+    n_out = num_shards if shard_id == ALL_SHARDS else 1
+    sh = _gqa_shape(B, q_len, H, pages.num_kv_heads, D, causal, scale)
+    with torch.cuda.device(dev):
+        need = int(lib().gqa_fp8_workspace_size(ctypes.byref(sh), int(num_shards), int(shard_id)))
+        if out_partial is None:
+            out_partial = torch.empty((max(n_out, 1), B, q_len, H, D), dtype=torch.float32, device=dev)
+        if lse_partial is None:
+            lse_partial = torch.empty((max(n_out, 1), B, q_len, H), dtype=torch.float32, device=dev)
+        if workspace is None:
+            workspace = torch.empty((max(need, 256),), dtype=torch.uint8, device=dev)
+        _check(out_partial, "out_partial", (torch.float32,), 5, dev)
+        _check(lse_partial, "lse_partial", (torch.float32,), 4, dev)
+        _check(workspace, "workspace", (torch.uint8,), 1, dev)
+        _shape_is(out_partial, "out_partial", (max(n_out, 1), B, q_len, H, D))
+        _shape_is(lse_partial, "lse_partial", (max(n_out, 1), B, q_len, H))
+        st = lib().gqa_decode_partial_fp8(_ptr(q), ctypes.byref(pages), _ptr(block_table),
+                                          block_table.shape[1], _ptr(seq_lens), _ptr(q_lens),
+                                          ctypes.byref(sh), int(shard_id), int(num_shards),
+                                          LAYOUTS[layout], _ptr(out_partial), _ptr(lse_partial),
+                                          _ptr(workspace), workspace.numel(), _on(dev, stream))
+    if st != 0:
+        raise MLAError(st, "gqa_decode_partial_fp8")
+    return out_partial, lse_partial, workspace
+
+
+# ------------------------------------------------- rotary positions and append
+class Rope:
+    """Rotary positions: inv_freq float64 [rot_dim / 2] (device, radians per
+    token, e.g. from mla_rope_frequencies), the first rotated dim of a head,
+    the pair layout and the factor on the rotated values."""
+
+    def __init__(self, inv_freq, first_dim=0, interleaved=False, attention_factor=1.0):
+        _check(inv_freq, "inv_freq", (torch.float64,), 1)
+        self.inv_freq, self.first_dim = inv_freq, int(first_dim)
+        self.interleaved, self.attention_factor = bool(interleaved), float(attention_factor)
+
+    def _args(self, dev):
+        _check(self.inv_freq, "rope.inv_freq", (torch.float64,), 1, dev)
+        return mla_rope(self.inv_freq.data_ptr(), 2 * self.inv_freq.numel(), self.first_dim,
+                        int(self.interleaved), self.attention_factor)
+
+
+def mla_rope_frequencies(rot_dim, theta=10000.0, scaling=None, device="cuda"):
+    """(inv_freq float64 [rot_dim / 2] on `device`, attention factor) of rotary
+    positions with base theta: w_i = theta^(-2i / rot_dim) radians per token.
+
+    scaling: None, or a dict whose "type" names how the frequencies are
+    stretched by "factor" for contexts beyond the ones trained on:
+      "linear"      w_i / factor
+      "ntk"         the base grows to theta * factor^(rot / (rot - 2)), which
+                    stretches the slowest pair by the factor, the fastest not
+      "yarn"        w_i / factor for pairs that turn less than "beta_slow" (1)
+                    times in "original_max_position" tokens, w_i for those that
+                    turn more than "beta_fast" (32) times, a linear ramp over
+                    the pair index between; attention factor
+                    "attention_factor" (0.1 ln factor + 1)
+      "wavelength"  w_i / factor for wavelengths above original_max_position /
+                    "low_freq_factor", w_i below original_max_position /
+                    "high_freq_factor", interpolated in between
+    """
+    if rot_dim < 2 or rot_dim % 2:
+        raise ValueError("rot_dim must be even and at least 2")
+    if not (theta > 1.0 and math.isfinite(theta)):
+        raise ValueError("theta must be finite and above 1")
+    i = torch.arange(0, rot_dim, 2, dtype=torch.float64)
+    attention_factor = 1.0
+    kind = None if scaling is None else scaling["type"]
+    if kind is not None:
+        factor = float(scaling["factor"])
+        if not (factor >= 1.0 and math.isfinite(factor)):
+            raise ValueError("scaling factor must be finite and at least 1")
+    if kind == "ntk":
+        if rot_dim < 4:
+            raise ValueError("ntk scaling needs rot_dim of at least 4")
+        theta = theta * factor ** (rot_dim / (rot_dim - 2))
+    inv = torch.pow(torch.tensor(theta, dtype=torch.float64), -i / rot_dim)
+    if kind == "linear":
+        inv = inv / factor
+    elif kind == "yarn":
+        orig = float(scaling["original_max_position"])
+        fast, slow = float(scaling.get("beta_fast", 32.0)), float(scaling.get("beta_slow", 1.0))
+
+        def pair_dim(turns):   # (fractional) dim whose pair turns that often in orig tokens
+            return rot_dim * math.log(orig / (turns * 2 * math.pi)) / (2 * math.log(theta))
+
+        low = max(math.floor(pair_dim(fast)), 0)
+        high = min(math.ceil(pair_dim(slow)), rot_dim - 1)
+        ramp = ((i / 2 - low) / max(high - low, 1e-3)).clamp(0, 1)
+        inv = inv / factor * ramp + inv * (1 - ramp)
+        given = scaling.get("attention_factor")
+        attention_factor = 0.1 * math.log(factor) + 1.0 if given is None else float(given)
+    elif kind == "wavelength":
+        orig = float(scaling["original_max_position"])
+        lo, hi = float(scaling["low_freq_factor"]), float(scaling["high_freq_factor"])
+        if not hi > lo:
+            raise ValueError("high_freq_factor must be above low_freq_factor")
+        turns = orig * inv / (2 * math.pi)
+        s = ((turns - lo) / (hi - lo)).clamp(0, 1)
+        inv = (1 - s) * inv / factor + s * inv
+    elif kind not in (None, "ntk"):
+        raise ValueError(f"unknown rope scaling {kind!r}")
+    return inv.to(device), attention_factor
+
+
+def _token_stride(t, name, dims):
+    """Elements between the tokens of t [B, q_len, ...] whose last `dims`
+    dimensions are contiguous (a view of a wider projection output will do)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name}: dtype {t.dtype} is not bfloat16")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a CUDA device")
+    if t.dim() != 2 + dims:
+        raise ValueError(f"{name} must have {2 + dims} dims, got {t.dim()}")
+    width = 1
+    for d in range(t.dim() - 1, 1, -1):
+        if t.shape[d] != 1 and t.stride(d) != width:
+            raise ValueError(f"{name}: a token's values must be contiguous")
+        width *= t.shape[d]
+    B, q_len = t.shape[:2]
+    if q_len > 1:
+        step = t.stride(1)
+        if B > 1 and t.stride(0) != q_len * step:
+            raise ValueError(f"{name}: tokens must be evenly spaced")
+    else:
+        step = t.stride(0) if B > 1 else width
+    if t.numel() and step < width:
+        raise ValueError(f"{name}: tokens overlap")
+    return step
+
+
+def _tokens(B, q_len, seq_lens, q_lens, positions, dev):
+    if seq_lens is not None:
+        _check(seq_lens, "seq_lens", (torch.int32,), 1, dev)
+        _shape_is(seq_lens, "seq_lens", (B,))
+    if q_lens is not None:
+        _check(q_lens, "q_lens", (torch.int32,), 1, dev)
+        _shape_is(q_lens, "q_lens", (B,))
+    if positions is not None:
+        _check(positions, "positions", (torch.int32,), 2, dev)
+        _shape_is(positions, "positions", (B, q_len))
+    ptr = lambda t: None if t is None else t.data_ptr()
+    return mla_tokens(int(B), int(q_len), ptr(seq_lens), ptr(q_lens), ptr(positions))
+
+
+def _out_rows(x, out, name, dims):
+    """The output of a rotation of x: `out` checked (x itself, or memory of its
+    own), or a new tensor; and the two token strides."""
+    xs = _token_stride(x, name, dims)
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    ys = _token_stride(out, name + "_out", dims)
+    _shape_is(out, name + "_out", x.shape)
+    if out.device != x.device:
+        raise ValueError(f"{name}_out is on {out.device}, expected {x.device}")
+    if out.data_ptr() == x.data_ptr():
+        if xs != ys:
+            raise ValueError(f"{name}_out overlaps {name} with other strides")
+    else:
+        def span(t, step):
+            width = math.prod(t.shape[2:])
+            return t.data_ptr(), t.data_ptr() + 2 * ((t.shape[0] * t.shape[1] - 1) * step + width)
+        (a0, a1), (b0, b1) = span(x, xs), span(out, ys)
+        if a0 < b1 and b0 < a1:
+            raise ValueError(f"{name}_out overlaps {name}")
+    return out, xs, ys
+
+
+def mla_rope_apply(x, rope, seq_lens=None, q_lens=None, positions=None, out=None, stream=None):
+    """Rotates heads by their tokens' positions; returns out.
+
+    x: bf16 [B, q_len, H, D] (each token's heads contiguous; tokens evenly
+    spaced, so a slice of a fused projection will do).  Token i of request b
+    stands at seq_lens[b] - n_b + i with n_b = q_lens[b] or q_len, or at
+    positions[b, i] (int32 [B, q_len]) if given.  out: x for in place (only the
+    rotated dims move), memory of its own, or None for a new tensor.  Rows
+    i >= n_b are left as they were.
+    """
+    out, xs, ys = _out_rows(x, out, "x", 2)
+    dev = x.device
+    B, q_len, H, D = x.shape
+    if seq_lens is None and positions is None:
+        raise ValueError("give seq_lens or positions")
+    tok = _tokens(B, q_len, seq_lens, q_lens, positions, dev)
+    r = rope._args(dev)
+    with torch.cuda.device(dev):
+        st = lib().mla_rope_apply(_ptr(x), xs, _ptr(out), ys, ctypes.byref(tok), H, D,
+                                  ctypes.byref(r), _on(dev, stream))
+    if st != 0:
+        raise MLAError(st, "mla_rope_apply")
+    return out
+
+
+def _append_query(q, q_out, B, q_len, width, dev):
+    if q is None:
+        if q_out is not None:
+            raise ValueError("q_out without q")
+        return None, 0, 0, 0
+    q_out, qs, ys = _out_rows(q, q_out, "q", 2)
+    if q.device != dev:
+        raise ValueError(f"q is on {q.device}, expected {dev}")
+    _shape_is(q, "q", (B, q_len, q.shape[2], width))
+    return q_out, qs, ys, q.shape[2]
+
+
+def _append_table(block_table, seq_lens, workspace, B, dev):
+    _check(block_table, "block_table", (torch.int32,), 2, dev)
+    if seq_lens is None:
+        raise TypeError("seq_lens must be a torch.Tensor")
+    if block_table.shape[0] != B:
+        raise ValueError("block_table and the new tokens disagree on the number of requests")
+    if workspace is None:
+        return torch.zeros((256,), dtype=torch.uint8, device=dev)
+    _check(workspace, "workspace", (torch.uint8,), 1, dev)
+    return workspace
+
+
+def mla_cache_append(latent, kv, block_table, seq_lens, rope=None, q=None, q_out=None,
+                     kv_scale=None, q_lens=None, positions=None, shard_id=0, num_shards=1,
+                     workspace=None, stream=None):
+    """Appends a step's latent rows to the paged latent cache and rotates its
+    queries; returns (q_out, workspace).
+
+    latent: bf16 [B, q_len, 576], the new tokens' rows before rotation (rope:
+    first_dim 512 in a latent row; None stores them as they are).  kv: bf16 or
+    e4m3 codes [P, 64, 576] (written), with kv_scale fp32 [P, 64] (written) for
+    codes.  seq_lens: context lengths with the new tokens.  q: bf16 [B, q_len,
+    H, 576] or None; q_out: q itself, memory of its own, or None for a new
+    tensor.  num_shards > 1: the cache is shard_id's interleaved_local slice.
+    workspace: 256 bytes, zeroed before its first use; mla_get_device_error
+    reads its errors.
+    """
+    ls = _token_stride(latent, "latent", 1)
+    dev = latent.device
+    B, q_len, d = latent.shape
+    if d != D_QK:
+        raise ValueError("latent must be [B, q_len, 576]")
+    pages = _kv_pages(kv, kv_scale, dev)
+    _shape_is(kv, "kv", (kv.shape[0], PAGE, D_QK))
+    if kv_scale is not None:
+        _shape_is(kv_scale, "kv_scale", kv.shape[:2])
+    with torch.cuda.device(dev):
+        workspace = _append_table(block_table, seq_lens, workspace, B, dev)
+        tok = _tokens(B, q_len, seq_lens, q_lens, positions, dev)
+        q_out, qs, ys, H = _append_query(q, q_out, B, q_len, D_QK, dev)
+        r = None if rope is None else ctypes.byref(rope._args(dev))
+        st = lib().mla_cache_append(_ptr(latent), ls, ctypes.byref(pages), _ptr(block_table),
+                                    block_table.shape[1], ctypes.byref(tok), r, _ptr(q), qs,
+                                    _ptr(q_out), ys, H, int(shard_id), int(num_shards),
+                                    _ptr(workspace), workspace.numel(), _on(dev, stream))
+    if st != 0:
+        raise MLAError(st, "mla_cache_append")
+    return q_out, workspace
+
+
+def gqa_cache_append(k, v, k_cache, v_cache, block_table, seq_lens, rope=None, q=None, q_out=None,
+                     k_scale=None, v_scale=None, q_lens=None, positions=None, shard_id=0,
+                     num_shards=1, workspace=None, stream=None):
+    """Appends a step's K and V heads to the paged GQA cache and rotates its
+    queries; returns (q_out, workspace).
+
+    k, v: bf16 [B, q_len, Hkv, 128], k before rotation.  k_cache, v_cache: bf16
+    or e4m3 codes [P, 64, Hkv, 128] (written), with k_scale, v_scale fp32
+    [P, 64 / block, Hkv] (written) for codes.  q: bf16 [B, q_len, H, 128] or
+    None.  The rest as for mla_cache_append.
+    """
+    ks = _token_stride(k, "k", 2)
+    vs = _token_stride(v, "v", 2)
+    dev = k.device
+    B, q_len, Hkv, _ = k.shape
+    if v.device != dev:
+        raise ValueError(f"v is on {v.device}, expected {dev}")
+    _shape_is(v, "v", k.shape)
+    pages = _block_pages(k_cache, v_cache, k_scale, v_scale, dev)
+    _shape_is(k, "k", (B, q_len, pages.num_kv_heads, 128))
+    with torch.cuda.device(dev):
+        workspace = _append_table(block_table, seq_lens, workspace, B, dev)
+        tok = _tokens(B, q_len, seq_lens, q_lens, positions, dev)
+        q_out, qs, ys, H = _append_query(q, q_out, B, q_len, 128, dev)
+        r = None if rope is None else ctypes.byref(rope._args(dev))
+        st = lib().gqa_cache_append(_ptr(k), ks, _ptr(v), vs, ctypes.byref(pages),
+                                    _ptr(block_table), block_table.shape[1], ctypes.byref(tok), r,
+                                    _ptr(q), qs, _ptr(q_out), ys, H, int(shard_id),
+                                    int(num_shards), _ptr(workspace), workspace.numel(),
+                                    _on(dev, stream))
+    if st != 0:
+        raise MLAError(st, "gqa_cache_append")
+    return q_out, workspace

@@ -1,0 +1,59 @@
+// Rotary positions shared by the rotation and cache-append kernels.
+//
+// Pair i of a rotated head turns by the angle p * w_i (w_i radians per token):
+//
+//   y_a = f (x_a cos - x_b sin),   y_b = f (x_a sin + x_b cos)
+//
+// with (a, b) = (2i, 2i + 1) in the interleaved layout and (i, i + rot / 2) in
+// the half layout.  Only p * w_i modulo one turn matters.  w_i / 2 pi is held
+// as a 64-bit fraction of a turn, so the product with the integer position
+// wraps by itself: the angle of a far position is as exact as that of a near
+// one (2^-53 of w_i per token, 2^-34 of a turn in the reduction), without
+// 64-bit floating point per position.
+#pragma once
+#include <cstdint>
+
+namespace mla {
+
+struct RopeArgs {
+  const double* inv_freq;  // [rot / 2] radians per token, device
+  int rot;                 // rotated dims, multiple of 16; 0: nothing is rotated
+  int first;               // first rotated dim, multiple of 8
+  int interleaved;         // pair layout
+  float factor;            // on the rotated values
+};
+
+// Radians per token -> 2^64ths of a turn per token.
+__device__ __forceinline__ unsigned long long turn_rate(double w) {
+  const double t = w * 0.15915494309189533577;   // 1 / (2 pi)
+  return __double2ull_rn((t - floor(t)) * 18446744073709551616.0);
+}
+
+// (f cos, f sin) of position pos at `rate`.  The turn is split into the
+// nearest quarter and a rest of at most an eighth, which is exact in integers;
+// the rest goes to sincospif with the error of one fp32 rounding.
+__device__ __forceinline__ float2 turn_cs(unsigned long long rate, int pos, float f) {
+  const unsigned long long u = rate * (unsigned long long)(long long)pos;
+  const unsigned q = (unsigned)((u + (1ull << 61)) >> 62);
+  const long long r = (long long)(u - ((unsigned long long)q << 62));
+  float s, c;
+  sincospif((float)(int)(r >> 30) * 1.16415321826934814453125e-10f, &s, &c);   // 2^-33
+  if (q & 1) {
+    const float t = c;
+    c = -s;
+    s = t;
+  }
+  if (q & 2) {
+    c = -c;
+    s = -s;
+  }
+  return make_float2(f * c, f * s);
+}
+
+__device__ __forceinline__ void turn_pair(float& a, float& b, float2 cs) {
+  const float x = a;
+  a = fmaf(x, cs.x, -b * cs.y);
+  b = fmaf(x, cs.y, b * cs.x);
+}
+
+}  // namespace mla

@@ -1,0 +1,255 @@
+"""GPU parity of grouped-query attention over an e4m3 cache with block scales
+against a 64-bit reference: group sizes, blocks, shards and layouts, ragged and
+padded batches, causal rows that see nothing, poisoned unused rows, extreme
+scales and queries, NaN in seen and unseen places, bad pages, graphs, streams."""
+import math
+
+import pytest
+import torch
+
+from _block_ref import FP8, PAGE, attend, check_attention, owned
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def mla():
+    import sequence_sharded_mla_gb300 as m
+    return m
+
+
+def make(lens, H, Hkv, block=64, q_len=1, seed=0, poison=True, q_sigma=1.0, spare=2, N=1, s=0,
+         layout="interleaved"):
+    """A batch on the CPU.  Slots that hold no token are NaN codes under NaN
+    scales, except where a live token shares the block."""
+    g = torch.Generator().manual_seed(seed)
+    slots = [owned(L, s, N, layout)[1] if layout.endswith("local") else list(range(L)) for L in lens]
+    need = [-(-len(x) // PAGE) for x in slots]
+    P = sum(need) + spare
+    perm = torch.randperm(P, generator=g).to(torch.int32)
+    bt = torch.full((len(lens), max(need + [1]) + 1), -1, dtype=torch.int32)
+    off = 0
+    for b, n in enumerate(need):
+        bt[b, :n] = perm[off:off + n]
+        off += n
+    w = dict(q=(torch.randn(len(lens), q_len, H, 128, generator=g) * q_sigma).bfloat16(), bt=bt,
+             lens=torch.tensor(lens, dtype=torch.int32))
+    used = torch.zeros(P, PAGE, dtype=torch.bool)
+    for b, x in enumerate(slots):
+        for p in x:
+            used[int(bt[b, p // PAGE]), p % PAGE] = True
+    for n in "kv":
+        c = (torch.randn(P, PAGE, Hkv, 128, generator=g) * 110).clamp(-448, 448).to(FP8).view(torch.uint8)
+        sc = (torch.rand(P, PAGE // block, Hkv, generator=g) + 0.5) / 110
+        if poison:
+            c[~used] = 0x7F
+            sc[~used.view(P, PAGE // block, block).any(-1)] = math.nan
+        w[n], w[n + "s"] = c, sc
+    return w
+
+
+def call(mla, w, N=1, layout="interleaved", shard_id=-1, causal=False, q_lens=None, scale=None, **kw):
+    d = lambda t: None if t is None else t.cuda()
+    part, lse, ws = mla.gqa_decode_partial_fp8(
+        d(w["q"]), d(w["k"]).view(FP8), d(w["v"]).view(FP8), d(w["ks"]), d(w["vs"]), d(w["bt"]),
+        d(w["lens"]), N, layout, shard_id=shard_id, causal=causal, softmax_scale=scale,
+        q_lens=d(q_lens), **kw)
+    return part, lse, mla.mla_get_device_error(ws)
+
+
+def ref(w, N=1, layout="interleaved", s=0, causal=False, q_lens=None, scale=None, rows=None):
+    return attend(w["q"], w["k"], w["v"], w["ks"], w["vs"], w["bt"], w["lens"], q_lens, causal,
+                  128 ** -0.5 if scale is None else scale, N, s, layout, rows)
+
+
+def check(mla, w, N=1, layout="interleaved", causal=False, q_lens=None, scale=None, status=0):
+    part, lse, st = call(mla, w, N, layout, causal=causal, q_lens=q_lens, scale=scale)
+    assert st == status
+    for s in range(N):
+        check_attention(part[s], lse[s], ref(w, N, layout, s, causal, q_lens, scale))
+    out, lse_out = mla.gqa_shard_combine(part, lse)
+    check_attention(out, lse_out, ref(w, 1, "interleaved", -1, causal, q_lens, scale),
+                    out_rel=2.0 ** -8)
+
+
+@pytest.mark.parametrize("H,Hkv", [(8, 8), (16, 8), (20, 4), (14, 2), (8, 1), (16, 1), (32, 2),
+                                   (24, 1), (48, 1), (64, 1)])
+def test_group_sizes(mla, H, Hkv):
+    check(mla, make([1, 63, 64, 65, 127, 700], H, Hkv, seed=H + Hkv))
+
+
+@pytest.mark.parametrize("block", [1, 2, 8, 16, 32, 64])
+def test_blocks(mla, block):
+    check(mla, make([1, 129, 300], 16, 2, block, seed=30 + block))
+
+
+@pytest.mark.parametrize("N,layout", [(1, "interleaved"), (2, "interleaved"), (4, "interleaved"),
+                                      (8, "interleaved"), (1, "contiguous"), (3, "contiguous"),
+                                      (8, "contiguous")])
+def test_shards_and_layouts(mla, N, layout):
+    check(mla, make([1, 5, 400, 1300], 16, 4, 16, seed=50 + N), N, layout)
+
+
+@pytest.mark.parametrize("N,layout", [(3, "interleaved_local"), (4, "interleaved_local"),
+                                      (5, "contiguous_local"), (2, "contiguous_local")])
+def test_local_slices(mla, N, layout):
+    for s in range(N):
+        w = make([1, 300, 77], 8, 2, 32, q_len=2, seed=60 + s, N=N, s=s, layout=layout)
+        part, lse, st = call(mla, w, N, layout, shard_id=s, causal=True)
+        assert st == 0
+        check_attention(part[0], lse[0], ref(w, N, layout, s, True))
+
+
+@pytest.mark.parametrize("q_len,H,Hkv", [(3, 16, 4), (9, 64, 8), (5, 14, 2), (9, 32, 2), (2, 64, 1),
+                                         (70, 4, 2)])
+@pytest.mark.parametrize("layout", ["interleaved", "contiguous"])
+def test_causal_verify(mla, q_len, H, Hkv, layout):
+    """The second request is shorter than its query tokens: its first rows see
+    nothing."""
+    check(mla, make([200, max(1, q_len - 2), 131], H, Hkv, seed=q_len + H, q_len=q_len), 2, layout,
+          causal=True)
+
+
+@pytest.mark.parametrize("causal", [False, True])
+def test_padded_batch(mla, causal):
+    w = make([300, 40, 5, 130], 40, 4, 32, q_len=9, seed=70)
+    check(mla, w, 2, causal=causal, q_lens=torch.tensor([9, 1, 5, 4], dtype=torch.int32))
+
+
+def test_query_counts_out_of_range_are_clamped_and_reported(mla):
+    w = make([100, 40], 8, 2, q_len=3, seed=71)
+    ql = torch.tensor([7, 0], dtype=torch.int32)
+    part, lse, st = call(mla, w, causal=True, q_lens=ql)
+    assert st == -1
+    check_attention(part[0], lse[0], ref(w, causal=True, q_lens=ql.clamp(0, 3)))
+
+
+def test_no_tokens(mla):
+    w = make([0, 10, 0], 8, 2, seed=72)
+    part, lse, st = call(mla, w, 2)
+    assert st == 0
+    for s in range(2):
+        check_attention(part[s], lse[s], ref(w, 2, s=s))
+
+
+def test_long_contexts_are_split_and_joined(mla):
+    lens = [20011, 3, 70001]
+    w = make(lens, 8, 2, seed=73)
+    part, lse, st = call(mla, w, 2)
+    assert st == 0
+    for s in range(2):
+        check_attention(part[s], lse[s], ref(w, 2, s=s))
+
+
+def test_scales_of_every_size(mla):
+    """Zero, negative, far apart and tiny block scales; one block outweighs the
+    rest by 2^40 in V, and the query looks away from it."""
+    w = make([640], 8, 2, 16, seed=74, poison=False)
+    g = torch.Generator().manual_seed(75)
+    for n in ("ks", "vs"):
+        e = torch.randint(-12, -4, w[n].shape, generator=g)
+        w[n] = torch.exp2(e.float()) * (1 - 2 * torch.randint(0, 2, w[n].shape, generator=g))
+    w["vs"][0] = 0.0
+    w["vs"][1, 0] = 2.0 ** 40
+    w["ks"][1, 0] = 0.0
+    w["vs"][2, 1] = 2.0 ** -58
+    w["ks"][3, 1] = 2.0 ** -100
+    check(mla, w)
+    w["vs"][...] = 2.0 ** -40
+    check(mla, w)
+    w["vs"][...] = 0.0
+    check(mla, w)
+
+
+def test_a_flat_tail_below_one_large_weight(mla):
+    """40000 tokens whose weights are 2^-12 of the largest: together they are
+    ten times its weight."""
+    w = make([40001], 1, 1, seed=76, poison=False)
+    w["q"][...] = 0
+    w["q"][..., 0] = 1.0
+    w["k"][...] = 0
+    w["ks"][...] = 1.0
+    page, row = int(w["bt"][0, 100]), 7
+    w["k"][page, row, 0, 0] = torch.tensor(12 * math.log(2.0)).to(FP8).view(torch.uint8)
+    check(mla, w, scale=1.0)
+
+
+@pytest.mark.parametrize("size", [0.0, 1e-30, 1e-3, 300.0, 1e30])
+def test_query_magnitudes(mla, size):
+    w = make([150, 64], 8, 2, seed=77)
+    w["q"] = (w["q"].float() * size).bfloat16()
+    check(mla, w, scale=min(128 ** -0.5, 0.1 / max(size, 1e-30)))
+
+
+def test_query_rows_of_mixed_magnitude(mla):
+    w = make([150], 8, 1, seed=78)
+    w["q"] *= torch.exp2(torch.arange(8) * 3.0 - 20)[None, None, :, None].bfloat16()
+    check(mla, w)
+
+
+def test_nonfinite_query_is_reported(mla):
+    w = make([100, 80], 8, 2, q_len=2, seed=79)
+    w["q"][1, 1, 3, 5] = math.inf
+    ql = torch.tensor([2, 1], dtype=torch.int32)
+    assert call(mla, w)[2] == -7
+    part, lse, st = call(mla, w, q_lens=ql)     # the row is padding
+    assert st == 0
+    check_attention(part[0], lse[0], ref(w, q_lens=ql))
+
+
+def test_nan_reaches_the_rows_that_see_it(mla):
+    """A NaN key makes its head's rows NaN, a NaN value one dim; a NaN in a
+    drafted token reaches only the rows that see the token."""
+    w = make([200, 90], 8, 2, q_len=4, seed=80)
+    w["k"][w["bt"][0, 1].long(), 10, 1, 7] = 0x7F
+    w["v"][w["bt"][1, 0].long(), 30, 0, 9] = 0xFF
+    w["v"][w["bt"][1, 1].long(), 90 - 64 - 2, 1, 11] = 0x7F     # token L - 2: rows 2, 3
+    w["k"][w["bt"][1, 1].long(), 90 - 64 - 1, 0, 0] = 0x7F      # token L - 1: row 3
+    part, lse, st = call(mla, w, causal=True)
+    assert st == 0
+    check_attention(part[0], lse[0], ref(w, causal=True))
+
+
+def test_bad_pages_read_as_zeros(mla):
+    w = make([300, 70], 8, 2, seed=81)
+    w["bt"][0, 2] = w["k"].shape[0] + 5
+    w["bt"][1, 1] = -3
+    check(mla, w, status=-5)
+
+
+def test_same_bits_every_time_and_one_error_word_per_call(mla):
+    w = make([900, 5000, 17], 32, 4, q_len=3, seed=82)
+    a = call(mla, w, 2, causal=True)
+    b = call(mla, w, 2, causal=True)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_graph_replay_and_streams(mla):
+    w = make([900, 333], 16, 2, seed=83)
+    d = {n: t.cuda() for n, t in w.items()}
+    need = mla.gqa_fp8_workspace_size(2, 1, 16, 2, 2)
+
+    def go(stream=None, ws=None):
+        return mla.gqa_decode_partial_fp8(d["q"], d["k"], d["v"], d["ks"], d["vs"], d["bt"],
+                                          d["lens"], 2, workspace=ws, stream=stream)
+
+    p0, l0, _ = go()
+    side = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = []
+    for k in range(6):
+        got.append(go(side[k % 2], torch.empty(need, dtype=torch.uint8, device="cuda")))
+    torch.cuda.synchronize()
+    for p, l, _ in got:
+        assert torch.equal(p, p0) and torch.equal(l, l0)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        p, l, _ = go(ws=ws)
+    d["lens"].copy_(torch.tensor([20, 64], dtype=torch.int32))
+    for _ in range(3):
+        g.replay()
+    torch.cuda.synchronize()
+    w["lens"] = torch.tensor([20, 64], dtype=torch.int32)
+    for s in range(2):
+        check_attention(p[s], l[s], ref(w, 2, s=s))
