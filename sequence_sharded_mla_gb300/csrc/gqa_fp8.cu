@@ -6,12 +6,46 @@
 //
 // with K_t, V_t the codes' values and sk, sv the scales of t's block.
 //
-// One block per output row: each warp walks every fourth token of the shard
-// with a running maximum and sum, and the four are joined at the end.
+// Work unit: (request, shard, KV head, group of up to R query rows), R = 16,
+// 32 or 64 rows (position i_local, head j of the KV head's group G: row
+// i_local * G + j).  Persistent CTAs walk a stream-K list of 128-token tiles.
+// The kernel is bound by the cache's bytes as long as it feeds the tensor
+// cores from what TMA brings in, so nothing of the cache is expanded: both
+// MMAs take K and V as e4m3 codes from shared memory, as their 128-row A
+// operand, and a tile is read from there once for all query rows:
+//
+//   S^T [128 tokens, R]  = K Q^T     (A: K, K-major; B: Q, two e4m3 terms)
+//   O^T [128 dims, 3R]  += V^T P^T   (A: V, MN-major; B: P, three e5m2 terms)
+//
+//   Q: a power-of-two scale per row puts max|q| in [128, 256), then q = hi +
+//      lo in e4m3: exact for values within 2^-10 of the row's largest, off by
+//      2^-18 of it below.  The two terms are two MMA chains into one S.
+//   P: thread t holds token t of the tile for every row.  The weight carries
+//      its block's V scale: with b_t = s_t log2(e) + log2|sv|, P_t = 2^(b_t -
+//      m), and the normaliser sums P_t / |sv| = 2^(s_t log2(e) - m), so one
+//      running reference m serves rows whose scales lie far apart.  m puts the
+//      largest weight at 2^12 and moves (rescaling O) once one passes 2^15.
+//      P goes to fp16 and from there to three e5m2 terms that add up to it
+//      within 2^-9 of its value, down to 2^-17: a token 2^-29 below the row's
+//      largest weight still counts.  (Two e4m3 terms end 2^-18 below it, and a
+//      million such tokens are not nothing.)  The terms are three blocks of
+//      the MMA's columns, so V is read once for all three; the epilogue adds
+//      their sums.
+//
+// Tile g belongs to softmax group g & 1, each with its own S buffer, weights,
+// reference and O^T accumulator, joined by their references at the end of a
+// piece.  The groups never wait for one another inside a piece.
+//
+// Warps: 0 producer (block table, TMA boxes of K and V, cp.async of the
+// tokens' scales); 1 issues K Q^T; 2 issues V^T P^T; 4..7 and 8..11 the
+// softmax groups (TMEM lane quadrant = warp % 4), which also load and split
+// the piece's query rows and write its outputs.
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <math_constants.h>
 
 #include <algorithm>
+#include <climits>
 #include <cmath>
 
 #include "common.cuh"
@@ -22,115 +56,749 @@
 namespace mla {
 namespace gqa8 {
 
-constexpr int kD = 128;
-constexpr int kThreads = 128;
+constexpr int kD = 128;                    // head width
+constexpr int kTok = 128;                  // tokens of a tile
+constexpr int kHalf = kTok * kD;           // 16384 bytes: K or V of a tile
+constexpr int kStages = 4;
+constexpr int kStageBytes = 2 * kHalf;
+constexpr int kThreads = 384;
+constexpr int kGroupThreads = 128;
+constexpr uint32_t kBarAll = 1, kBarGroup = 2;   // group g: kBarGroup + g
+constexpr int kMinTilesPerCta = 2;
+constexpr int kUnitCost = 2;
+constexpr unsigned long long kTimeoutNs = 2000000000ull;
+constexpr float kTop = 12.0f;              // log2 of the largest weight at a new reference
+constexpr float kMost = 15.0f;             // log2 of the largest weight that fits fp16
+constexpr float kNoRef = -1.0e38f;         // reference of a row that has seen nothing
+constexpr float kMinScale = 8.67361737988403547e-19f;   // 2^-60
 
 struct Desc {
   int B, q_len, H, Hkv, G;
+  int ni, Gq;          // query positions per row group, row groups per (request, KV head)
   int num_shards, shard_first, n_out, layout, local, causal;
   int num_pages, max_pages, lg_block;
+  int nv;              // page boxes per 64 slots: shards of a whole-request interleaved cache, else 1
   float scale_log2;
   const uint16_t* q;
-  const uint8_t *k, *v;
   const float *ks, *vs;
   const int32_t *block_table, *seq_lens, *q_lens;
-  unsigned* err;
 };
 
-__global__ void __launch_bounds__(kThreads) gqa_fp8_row_kernel(Desc d, float* out, float* lse) {
-  __shared__ float so[4][kD], sm[4], sl[4];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int u = blockIdx.x;
-  const size_t row = u;
-  const int h = u % d.H;
-  u /= d.H;
-  const int i = u % d.q_len;
-  u /= d.q_len;
-  const int b = u % d.B, s = d.shard_first + u / d.B;
-  const int kh = h / d.G, L = max(d.seq_lens[b], 0);
-  int n = d.q_len;
-  if (d.q_lens != nullptr) {
-    n = d.q_lens[b];
-    if ((n < 1 || n > d.q_len) && threadIdx.x == 0) atomicOr(d.err, kErrQLens);
-    n = min(max(n, 0), d.q_len);
-  }
-  const int seen = i >= n ? 0 : (d.causal ? min(L, max(0, L - n + i + 1)) : L);
-  // tokens t0 + k * step, k < cnt, of the shard are seen; slot k (+ off) of the cache holds token k
-  int t0, step, cnt;
+struct Params {
+  Desc d;
+  float* out;          // [n_out, B, q_len, H, 128]
+  float* lse;          // [n_out, B, q_len, H]
+  WsHeader* hdr;
+  int* prefix;
+  float* ws_o;         // [grid * 2, 64, 128]
+  float* ws_lse;       // [grid * 2, 64]
+  unsigned long long timeout_ns;
+  int withhold_query;
+};
+
+struct Unit {
+  int b, so, s, kh, i0;
+  int L, qn;
+  int rows, live;      // rows of the group in the output; rows that attend
+  int tiles, tstart, tend, p0, npages;
+};
+
+__device__ __forceinline__ Unit make_unit(const Desc& d, int u) {
+  Unit x;
+  const int g = u % d.Gq;
+  int t = u / d.Gq;
+  x.kh = t % d.Hkv;
+  t /= d.Hkv;
+  x.so = t % d.n_out;
+  x.b = t / d.n_out;
+  x.s = d.shard_first + x.so;
+  x.L = max(d.seq_lens[x.b], 0);
+  x.qn = d.q_lens ? min(max(d.q_lens[x.b], 0), d.q_len) : d.q_len;
+  x.i0 = g * d.ni;
+  x.rows = min(d.ni, d.q_len - x.i0) * d.G;
+  x.live = min(max(x.qn - x.i0, 0) * d.G, x.rows);
+  x.tstart = x.p0 = 0;
+  x.tend = x.L;
+  const int L = x.live > 0 ? x.L : 0;
+  int n;                                       // the shard's tokens
   if (d.layout == kInterleaved) {
-    t0 = s;
-    step = d.num_shards;
-    cnt = seen > s ? (seen - 1 - s) / step + 1 : 0;
+    n = L > x.s ? (L - 1 - x.s) / d.num_shards + 1 : 0;
+    x.tiles = ceil_div(n, kTok);
   } else {
     const int c = ceil_div(L, d.num_shards);
-    t0 = s * c;
-    step = 1;
-    cnt = max(0, min(min(t0 + c, L), seen) - t0);
-  }
-  float qv[4];
-  bool bad = false;
-  {
-    const size_t qr = ((size_t)b * d.q_len + i) * d.H + h;
-    const uint2 w = reinterpret_cast<const uint2*>(d.q + qr * kD)[lane];
-    qv[0] = __uint_as_float(w.x << 16);
-    qv[1] = __uint_as_float(w.x & 0xFFFF0000u);
-    qv[2] = __uint_as_float(w.y << 16);
-    qv[3] = __uint_as_float(w.y & 0xFFFF0000u);
-    for (int e = 0; e < 4; ++e) bad |= !(fabsf(qv[e]) < INFINITY);
-  }
-  if (bad && i < n) atomicOr(d.err, kErrQRange);
-  float m = -CUDART_INF_F, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int k = warp; k < cnt; k += 4) {
-    const int slot = d.local ? k : t0 + k * step;
-    const int idx = slot / kPage, r = slot % kPage;
-    int page = idx < d.max_pages ? __ldg(d.block_table + (size_t)b * d.max_pages + idx) : -1;
-    float a = 0.f, sv = 0.f, vv[4] = {0.f, 0.f, 0.f, 0.f};
-    if (page < 0 || page >= d.num_pages) {
-      if (lane == 0) atomicOr(d.err, kErrBadPage);
+    x.tstart = min(x.s * c, L);
+    x.tend = min(x.tstart + c, L);
+    n = x.tend - x.tstart;
+    if (d.local || n == 0) {
+      x.tiles = ceil_div(n, kTok);
     } else {
-      const size_t e = (((size_t)page * kPage + r) * d.Hkv + kh) * kD;
-      const size_t si = ((size_t)page * (kPage >> d.lg_block) + (r >> d.lg_block)) * d.Hkv + kh;
-      const uint32_t kw = __ldg(reinterpret_cast<const uint32_t*>(d.k + e) + lane);
-      const uint32_t vw = __ldg(reinterpret_cast<const uint32_t*>(d.v + e) + lane);
-      float kv[4];
-      e4m3x2_to_f32x2(kw, kv[0], kv[1]);
-      e4m3x2_to_f32x2(kw >> 16, kv[2], kv[3]);
-      e4m3x2_to_f32x2(vw, vv[0], vv[1]);
-      e4m3x2_to_f32x2(vw >> 16, vv[2], vv[3]);
-      a = qv[0] * kv[0] + qv[1] * kv[1] + qv[2] * kv[2] + qv[3] * kv[3];
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1) a += __shfl_xor_sync(0xffffffffu, a, off);
-      a *= d.scale_log2 * __ldg(d.ks + si);
-      sv = __ldg(d.vs + si);
+      x.p0 = x.tstart / kPage;
+      x.tiles = ceil_div((x.tend - 1) / kPage - x.p0 + 1, kTok / kPage);
     }
-    const float mn = a > m ? a : (a != a ? a : m);
-    const float al = m == -CUDART_INF_F ? 0.f : exp2f(m - mn);
-    const float p = exp2f(a - mn);
-    m = mn;
-    l = l * al + p;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) o[e] = o[e] * al + p * (vv[e] * sv);
   }
-  reinterpret_cast<float4*>(so[warp])[lane] = make_float4(o[0], o[1], o[2], o[3]);
-  if (lane == 0) {
-    sm[warp] = m;
-    sl[warp] = l;
-  }
-  __syncthreads();
-  float M = -CUDART_INF_F;
-  for (int w = 0; w < 4; ++w) M = sl[w] != 0.f ? (sm[w] > M || sm[w] != sm[w] ? sm[w] : M) : M;
-  float tot = 0.f, acc = 0.f;
-  for (int w = 0; w < 4; ++w) {
-    if (sl[w] == 0.f) continue;
-    const float f = exp2f(sm[w] - M);
-    tot += f * sl[w];
-    acc += f * so[w][threadIdx.x];
-  }
-  out[row * kD + threadIdx.x] = tot == 0.f ? 0.f : acc / tot;
-  if (threadIdx.x == 0)
-    lse[row] = tot == 0.f ? -CUDART_INF_F : (M + log2f(tot)) * 0.69314718055994530942f;
+  x.npages = ceil_div(d.local ? n : L, kPage);
+  return x;
 }
 
+// Position of slot a of tile j.
+__device__ __forceinline__ int slot_token(const Desc& d, const Unit& x, int j, int a) {
+  const int p = j * kTok + a;
+  if (d.layout == kInterleaved) return p * d.num_shards + x.s;
+  return (d.local ? x.tstart : x.p0 * kPage) + p;
+}
+
+__device__ __forceinline__ bool slot_valid(const Unit& x, int t) {
+  return t >= x.tstart && t < x.tend;
+}
+
+// Every slot of tile j holds a token that every row of the unit sees.
+__device__ __forceinline__ bool tile_full(const Desc& d, const Unit& x, int j) {
+  const int first = slot_token(d, x, j, 0), last = slot_token(d, x, j, kTok - 1);
+  return slot_valid(x, first) && slot_valid(x, last) &&
+         (!d.causal || last <= x.L - x.qn + x.i0);
+}
+
+__device__ __forceinline__ size_t out_row(const Desc& d, const Unit& x, int r) {
+  const int i = x.i0 + r / d.G, h = x.kh * d.G + r % d.G;
+  return (((size_t)x.so * d.B + x.b) * d.q_len + i) * d.H + h;
+}
+
+struct Misc {
+  uint64_t kv_full[kStages], kv_empty[kStages];
+  uint64_t s_full[2], s_empty[2], p_full[2], pv_done[2];
+  uint64_t q_full, drain;
+  uint32_t tmem_base;
+  int abort;
+  int lim[kRows];               // last position a row sees
+  float qs[kRows];              // 1 / the row's query scale
+  float m[2][kRows];            // per group: the rows' references
+  float alpha[2][kRows];
+  int rmax[2][kRows];
+  float lpart[2][4][kRows];     // per group and warp: sums of a piece
+  float f[2][kRows];            // per group: the factor of its accumulator
+  int nan_from[kD];             // per dim: the first partly seen token whose V is NaN
+  float ksc[kStages][kTok], vsc[kStages][kTok];
+};
+
+template <int R>
+struct Smem {
+  static constexpr int kQ = 0;                              // [2][R][128]
+  static constexpr int kP = 2 * R * kD;                     // [2 groups][3][128 tokens][R]
+  static constexpr int kPGroup = 3 * R * kTok;
+  static constexpr int kStage = (kP + 2 * kPGroup + 1023) & ~1023;
+  static constexpr int kMisc = kStage + kStages * kStageBytes;
+  static constexpr int kBytes = kMisc + (int)sizeof(Misc) + 1024;   // + alignment slack
+  static_assert(kBytes <= 232448, "shared memory budget");
+};
+
+__global__ void __launch_bounds__(1024) gqa_fp8_plan_kernel(Desc d, WsHeader* hdr, int* prefix,
+                                                            int grid) {
+  griddep_launch_dependents();
+  __shared__ unsigned bad;
+  if (threadIdx.x == 0) bad = 0;
+  __syncthreads();
+  if (d.q_lens != nullptr)
+    for (int b = threadIdx.x; b < d.B; b += 1024)
+      if (d.q_lens[b] < 1 || d.q_lens[b] > d.q_len) atomicOr(&bad, kErrQLens);
+  __syncthreads();
+  plan_units(d.B * d.n_out * d.Hkv * d.Gq, [&](int u) { return make_unit(d, u).tiles; }, hdr,
+             prefix, grid, kMinTilesPerCta, kUnitCost, bad);
+}
+
+__device__ __forceinline__ int ordered(float x) {   // float order as int order
+  const int i = __float_as_int(x);
+  return i ^ ((i >> 31) & 0x7fffffff);
+}
+__device__ __forceinline__ float from_ordered(int i) {
+  return __int_as_float(i ^ ((i >> 31) & 0x7fffffff));
+}
+
+__device__ __forceinline__ float lg2_approx(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Weights of two rows as three e5m2 terms: the top bytes of the fp16 value, of
+// what that leaves, and of what is left then rounded to nearest.  Returns the
+// first two terms in the top bytes of t0, t1 and the third as a byte pair.
+__device__ __forceinline__ void split_e5m2(float a, float b, uint32_t& t0, uint32_t& t1,
+                                           uint32_t& t2) {
+  __half2 x = __floats2half2_rn(a, b);
+  t0 = *reinterpret_cast<uint32_t*>(&x);
+  uint32_t h = t0 & 0xFF00FF00u;
+  __half2 y = __hsub2(x, *reinterpret_cast<__half2*>(&h));
+  t1 = *reinterpret_cast<uint32_t*>(&y);
+  h = t1 & 0xFF00FF00u;
+  y = __hsub2(y, *reinterpret_cast<__half2*>(&h));
+  unsigned short c;
+  asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(c) : "r"(*reinterpret_cast<uint32_t*>(&y)));
+  t2 = c;
+}
+
+template <int R>
+__global__ void __launch_bounds__(kThreads, 1)
+    gqa_fp8_partial_kernel(const __grid_constant__ CUtensorMap tm_k,
+                           const __grid_constant__ CUtensorMap tm_v, Params p) {
+  using S = Smem<R>;
+  constexpr uint32_t kTmemCols = 8 * R;          // S: 2 x R, O^T: 2 x 3R
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  Misc* misc = reinterpret_cast<Misc*>(smem + S::kMisc);
+  const Desc& d = p.d;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  griddep_wait();
+  griddep_launch_dependents();
+
+  const int W = p.hdr->total_cost, per = p.hdr->per_cta;
+  const int lo = blockIdx.x * per;
+  if (lo >= W) return;
+  const int hi = min(lo + per, W);
+
+  const uint32_t sQ = smem_u32(smem + S::kQ), sP = smem_u32(smem + S::kP);
+  const uint32_t sSt = smem_u32(smem + S::kStage);
+  auto bar = [&](const uint64_t* b) { return smem_u32(b); };
+  volatile int* abort_flag = &misc->abort;
+  const uint64_t tmo = p.timeout_ns;
+  auto fail = [&]() {
+    atomicOr(&p.hdr->err, kErrTimeout);
+    *abort_flag = 1;
+  };
+  // Waits as a warp; a wait that runs out ends the kernel for every role.
+  auto wait = [&](const uint64_t* b, int parity) {
+    const bool ok = __all_sync(0xffffffffu, mbar_wait(bar(b), parity, tmo, abort_flag));
+    if (!ok && lane == 0) fail();
+    return ok;
+  };
+
+  if (threadIdx.x == 0) {
+    for (int st = 0; st < kStages; ++st) {
+      mbar_init(bar(&misc->kv_full[st]), 1 + 32);   // expect_tx + one cp.async arrival per lane
+      mbar_init(bar(&misc->kv_empty[st]), 1);
+    }
+    for (int g = 0; g < 2; ++g) {
+      mbar_init(bar(&misc->s_full[g]), 1);
+      mbar_init(bar(&misc->s_empty[g]), 4);
+      mbar_init(bar(&misc->p_full[g]), 4);
+      mbar_init(bar(&misc->pv_done[g]), 1);
+    }
+    mbar_init(bar(&misc->q_full), 8);
+    mbar_init(bar(&misc->drain), 2);
+    misc->abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&misc->tmem_base), kTmemCols);
+    tmem_relinquish();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = misc->tmem_base;
+
+  PieceIter it;
+  it.init(p.prefix, p.hdr->num_units, lo, hi, p.hdr->unit_cost);
+  int armed[kStages];
+  for (int st = 0; st < kStages; ++st) armed[st] = -1;
+  int unit, t0, t1, slot;
+  bool whole, ok = true;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    const int nb = 2 * d.nv;                     // page boxes per tile
+    const int rp = kPage / d.nv;                 // slots per box
+    const int lg_rp = 31 - __clz(rp);
+    int g = 0;
+    while (ok && it.next(unit, t0, t1, whole, slot)) {
+      const Unit x = make_unit(d, unit);
+      const int32_t* bt = d.block_table + (size_t)x.b * d.max_pages;
+      const int res = d.nv > 1 ? x.s : 0;
+      auto entry = [&](int j) {                  // page of this lane's box of tile j, or -1
+        const int idx = x.p0 + j * nb + lane;
+        return (lane < nb && idx < x.npages && idx < d.max_pages) ? __ldg(bt + idx) : -1;
+      };
+      int next = entry(t0);
+      for (int j = t0; j < t1; ++j, ++g) {
+        const int st = g % kStages, round = g / kStages;
+        int page = next;
+        if (j + 1 < t1) next = entry(j + 1);
+        const bool there = page >= 0 && page < d.num_pages;
+        if (!there) {
+          if (lane < nb && x.p0 + j * nb + lane < x.npages) atomicOr(&p.hdr->err, kErrBadPage);
+          page = d.num_pages;                    // out of the map: TMA fills zeros
+        }
+        if (round >= 1 && !(ok = wait(&misc->kv_empty[st], (round - 1) & 1))) break;
+        const uint32_t full = bar(&misc->kv_full[st]);
+        if (lane == 0) {
+          mbar_arrive_expect_tx(full, kStageBytes);
+          armed[st] = g;
+        }
+        __syncwarp();
+        if (lane < nb) {
+          const uint32_t dst = sSt + st * kStageBytes + lane * (rp * kD);
+          const int crow = (page * kPage + res) * d.Hkv + x.kh;
+          tma_load_3d(dst, &tm_k, full, 0, 0, crow);
+          tma_load_3d(dst + kHalf, &tm_v, full, 0, 0, crow);
+        }
+#pragma unroll
+        for (int h = 0; h < kTok / 32; ++h) {
+          const int a = lane + 32 * h;
+          const int pg = __shfl_sync(0xffffffffu, page, a >> lg_rp);
+          const int row = res + (a & (rp - 1)) * d.nv;
+          const bool ok_pg = pg < d.num_pages;
+          const size_t si = ok_pg ? ((size_t)pg * (kPage >> d.lg_block) + (row >> d.lg_block)) * d.Hkv + x.kh : 0;
+          cp_async_4_zfill(smem_u32(&misc->ksc[st][a]), d.ks + si, ok_pg);
+          cp_async_4_zfill(smem_u32(&misc->vsc[st][a]), d.vs + si, ok_pg);
+        }
+        cp_async_mbar_arrive_noinc(full);
+        __syncwarp();
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ K Q^T
+    const uint32_t id = idesc_e4m3_f32(kTok, R, false, false);
+    const uint64_t dk = sw128_desc(sSt, 16, 1024), dq = sw128_desc(sQ, 16, 1024);
+    int g = 0, pc = 0;
+    while (ok && it.next(unit, t0, t1, whole, slot)) {
+      if (!(ok = wait(&misc->q_full, pc & 1))) break;
+      for (int j = t0; j < t1; ++j, ++g) {
+        const int st = g % kStages, round = g / kStages, grp = g & 1, gr = g >> 1;
+        if (!(ok = wait(&misc->kv_full[st], round & 1))) break;
+        if (gr >= 1 && !(ok = wait(&misc->s_empty[grp], (gr - 1) & 1))) break;
+        tc_fence_after();
+        if (lane == 0) {
+          const uint32_t off = (uint32_t)(st * kStageBytes) >> 4;
+#pragma unroll
+          for (int term = 0; term < 2; ++term)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma_e4m3_ss(tmem + R * grp, dk + off + ((32 * k) >> 4),
+                          dq + (uint32_t)((term * R * kD + 32 * k) >> 4), id, term + k != 0);
+          mma_commit(bar(&misc->s_full[grp]));
+        }
+        __syncwarp();
+      }
+      ++pc;
+    }
+  } else if (warp == 2) {
+    // ------------------------------------------------------------ V^T P^T
+    const uint32_t id = idesc_e4m3_e5m2_f32(kD, 3 * R, true, true);
+    const uint64_t dv = sw128_desc(sSt + kHalf, 16, 1024);
+    // P: [term][token][R] bytes, MN-major; 8-token groups 8 R bytes apart
+    auto pdesc = [&](uint32_t a) {
+      if (R == 16) return sw0_desc(a, 8 * R, R * kTok);
+      if (R == 32) return sw32_desc(a, R * kTok, 8 * R);
+      return sw64_desc(a, R * kTok, 8 * R);
+    };
+    int g = 0;
+    while (ok && it.next(unit, t0, t1, whole, slot)) {
+      for (int j = t0; j < t1; ++j, ++g) {
+        const int st = g % kStages, grp = g & 1, gr = g >> 1;
+        if (!(ok = wait(&misc->p_full[grp], gr & 1))) break;
+        tc_fence_after();
+        if (lane == 0) {
+          const uint64_t dp = pdesc(sP + grp * S::kPGroup);
+          const uint32_t off = (uint32_t)(st * kStageBytes) >> 4;
+#pragma unroll
+          for (int k = 0; k < 4; ++k)   // 32 tokens each
+            mma_e4m3_ss(tmem + 2 * R + 3 * R * grp, dv + off + ((k * 4 * 1024) >> 4),
+                        dp + (uint32_t)((k * 32 * R) >> 4), id, (j >= t0 + 2 || k != 0) ? 1u : 0u);
+          mma_commit(bar(&misc->kv_empty[st]));
+          mma_commit(bar(&misc->pv_done[grp]));
+        }
+        __syncwarp();
+      }
+    }
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------ softmax
+    const int grp = (warp - 4) >> 2, quad = warp & 3;
+    const int gtid = (threadIdx.x - 128) & 127;    // 0..127 in the group: its token of a tile
+    const int tid = threadIdx.x - 128;             // 0..255
+    const uint32_t lane_off = (uint32_t)(32 * quad) << 16;
+    const uint32_t tS = tmem + lane_off + R * grp, tO = tmem + lane_off + 2 * R;
+    float* ref = misc->m[grp];
+    int g = 0, pc = 0;
+    while (ok && it.next(unit, t0, t1, whole, slot)) {
+      const Unit x = make_unit(d, unit);
+      // ------------------------------------------------- the piece's query
+      // 16 lanes a row, 8 values each; the previous piece's MMAs have read the
+      // old rows, since all of its S has been consumed
+#pragma unroll
+      for (int r0 = 0; r0 < R; r0 += 16) {
+        const int r = r0 + (tid >> 4), c = tid & 15;
+        uint4 w = make_uint4(0, 0, 0, 0);
+        if (r < x.live) {
+          const int i = x.i0 + r / d.G, h = x.kh * d.G + r % d.G;
+          w = __ldg(reinterpret_cast<const uint4*>(
+                        d.q + (((size_t)x.b * d.q_len + i) * d.H + h) * kD) + c);
+        }
+        const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+        uint32_t mx = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) mx = max(mx, max(ww[e] & 0x7FFFu, (ww[e] >> 16) & 0x7FFFu));
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        // s_r = 2^(134 - e) puts max|q| (exponent e) in [128, 256); clamped so
+        // that it and its inverse are normal
+        const uint32_t e = min(max(mx >> 7, 8u), 254u);
+        const float sc = __uint_as_float((261u - e) << 23);
+        uint32_t sp[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          sp[k] = split_e4m3x2(__uint_as_float(ww[k] << 16) * sc,
+                               __uint_as_float(ww[k] & 0xFFFF0000u) * sc);
+        uint8_t* dst = smem + S::kQ + r * kD + (((c >> 1) ^ (r & 7)) << 4) + (c & 1) * 8;
+        *reinterpret_cast<uint2*>(dst) =
+            make_uint2((sp[0] & 0xFFFFu) | (sp[1] << 16), (sp[2] & 0xFFFFu) | (sp[3] << 16));
+        *reinterpret_cast<uint2*>(dst + R * kD) =
+            make_uint2((sp[0] >> 16) | (sp[1] & 0xFFFF0000u), (sp[2] >> 16) | (sp[3] & 0xFFFF0000u));
+        if (c == 0) {
+          if ((mx >> 7) == 255u) atomicOr(&p.hdr->err, kErrQRange);
+          misc->qs[r] = __uint_as_float((e - 7u) << 23);
+          misc->lim[r] = d.causal && r < x.live ? x.L - x.qn + x.i0 + r / d.G : INT_MAX - 1;
+        }
+      }
+      if (tid < 2 * R) misc->m[tid / R][tid % R] = kNoRef;
+      if (tid < kD) misc->nan_from[tid] = INT_MAX;
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0 && !(p.withhold_query && pc == 0)) mbar_arrive(bar(&misc->q_full));
+      named_bar_sync(kBarAll, 2 * kGroupThreads);
+
+      float l[R];
+#pragma unroll
+      for (int r = 0; r < R; ++r) l[r] = 0.0f;
+      bool first = true;                           // the group's first tile of the piece
+      for (int j = t0; j < t1; ++j, ++g) {
+        if ((g & 1) != grp) continue;
+        const int st = g % kStages, gr = g >> 1;
+        // -------------------------------------------------------- logits
+        const bool ok_s = ok && wait(&misc->kv_full[st], (g / kStages) & 1) &&
+                          wait(&misc->s_full[grp], gr & 1);
+        const bool full = tile_full(d, x, j);
+        const int t = slot_token(d, x, j, gtid);
+        const bool valid = full || slot_valid(x, t);
+        float c = 0.0f, lv = 0.0f, inv = 0.0f, fv = 1.0f;
+        if (ok_s && valid) {
+          c = misc->ksc[st][gtid] * d.scale_log2;
+          const float sv = misc->vsc[st][gtid], av = fabsf(sv);
+          // |sv| below 2^-60 counts as 2^-60 in the reference and as itself in
+          // the product; a scale that is not finite goes to the product alone
+          const float ve = av < INFINITY ? fmaxf(av, kMinScale) : 1.0f;
+          lv = lg2_approx(ve);
+          inv = 1.0f / ve;
+          fv = sv / ve;
+        }
+        const bool scaled = __any_sync(0xffffffffu, fv != 1.0f);
+        // 16 rows' log2 weights (without the reference) of this token
+        auto logits = [&](int r0, float (&b)[16]) {
+          uint32_t sr[16];
+          tmem_ld16(tS + r0, sr);
+          tmem_wait_ld();
+#pragma unroll
+          for (int k = 0; k < 16; ++k)
+            b[k] = fmaf(__uint_as_float(sr[k]) * misc->qs[r0 + k], c, lv);
+          if (!full) {
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+              if (!valid || t > misc->lim[r0 + k]) b[k] = -CUDART_INF_F;
+          }
+        };
+        float b[16];
+        bool over = false;
+        if (ok_s) {
+          tc_fence_after();
+#pragma unroll
+          for (int r0 = 0; r0 < R; r0 += 16) {
+            logits(r0, b);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) over = over || b[k] - ref[r0 + k] > kMost;
+          }
+        }
+        if (named_bar_or(kBarGroup + grp, kGroupThreads, over || !ok_s)) {
+          if (named_bar_or(kBarGroup + grp, kGroupThreads, !ok_s)) {
+            ok = false;
+            break;
+          }
+          // ---------------------------------------------- new references
+          if (gtid < R) misc->rmax[grp][gtid] = INT_MIN;
+          named_bar_sync(kBarGroup + grp, kGroupThreads);
+#pragma unroll 1
+          for (int r0 = 0; r0 < R; r0 += 16) {
+            logits(r0, b);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const int mx = __reduce_max_sync(0xffffffffu,
+                                               b[k] == b[k] ? ordered(b[k]) : INT_MIN);
+              if (lane == 0) atomicMax(&misc->rmax[grp][r0 + k], mx);
+            }
+          }
+          named_bar_sync(kBarGroup + grp, kGroupThreads);
+          if (gtid < R) {
+            const int o = misc->rmax[grp][gtid];
+            const float top = o == INT_MIN ? -CUDART_INF_F : from_ordered(o), old = ref[gtid];
+            const bool up = top > old + kMost;
+            misc->alpha[grp][gtid] = up ? ex2_approx(old - (top - kTop)) : 1.0f;
+            if (up) ref[gtid] = top - kTop;
+          }
+          const bool ok_pv = first || wait(&misc->pv_done[grp], (gr - 1) & 1);
+          if (named_bar_or(kBarGroup + grp, kGroupThreads, !ok_pv)) {
+            ok = false;
+            break;
+          }
+#pragma unroll
+          for (int r = 0; r < R; ++r) l[r] *= misc->alpha[grp][r];
+          if (!first) {
+            tc_fence_after();
+#pragma unroll 1
+            for (int c0 = 0; c0 < 3 * R; c0 += 16) {
+              uint32_t v[16];
+              tmem_ld16(tO + 3 * R * grp + c0, v);
+              tmem_wait_ld();
+#pragma unroll
+              for (int k = 0; k < 16; ++k)
+                v[k] = __float_as_uint(__uint_as_float(v[k]) * misc->alpha[grp][c0 % R + k]);
+              tmem_st16(tO + 3 * R * grp + c0, v);
+            }
+            tmem_wait_st();
+          }
+        }
+        // ------------------------------------------------------- weights
+        // the group's last P V has read the weights' buffer
+        if (!first && !wait(&misc->pv_done[grp], (gr - 1) & 1)) {
+          ok = false;
+          continue;                                // the next reduction ends the piece
+        }
+        uint8_t* prow = smem + S::kP + grp * S::kPGroup + gtid * R;
+#pragma unroll
+        for (int r0 = 0; r0 < R; r0 += 16) {
+          if (R > 16) logits(r0, b);
+          uint32_t w0[4], w1[4], w2[4];
+#pragma unroll
+          for (int q4 = 0; q4 < 4; ++q4) {
+            float pw[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int r = r0 + 4 * q4 + k;
+              pw[k] = ex2_approx(b[4 * q4 + k] - ref[r]);
+              l[r] = fmaf(pw[k], inv, l[r]);
+              if (scaled) pw[k] = pw[k] > 0.0f || pw[k] != pw[k] ? pw[k] * fv : 0.0f;
+            }
+            uint32_t a0, a1, a2, b0, b1, b2;
+            split_e5m2(pw[0], pw[1], a0, a1, a2);
+            split_e5m2(pw[2], pw[3], b0, b1, b2);
+            w0[q4] = __byte_perm(a0, b0, 0x7531);
+            w1[q4] = __byte_perm(a1, b1, 0x7531);
+            w2[q4] = a2 | (b2 << 16);
+          }
+          // 16-byte unit r0 / 16 of the token's R bytes, swizzled for R > 16
+          const int u = R == 16 ? 0 : R == 32 ? (r0 >> 4) ^ ((gtid >> 2) & 1)
+                                              : (r0 >> 4) ^ ((gtid >> 1) & 3);
+          *reinterpret_cast<uint4*>(prow + 16 * u) = make_uint4(w0[0], w0[1], w0[2], w0[3]);
+          *reinterpret_cast<uint4*>(prow + R * kTok + 16 * u) = make_uint4(w1[0], w1[1], w1[2], w1[3]);
+          *reinterpret_cast<uint4*>(prow + 2 * R * kTok + 16 * u) = make_uint4(w2[0], w2[1], w2[2], w2[3]);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(&misc->s_empty[grp]));
+        if (!full) {
+          // V rows of slots without a token become zeros; a NaN code of a token
+          // that not every row sees is taken out too and comes back in the
+          // epilogue for the rows that see it (rows see a prefix)
+          uint8_t* vt = smem + S::kStage + st * kStageBytes + kHalf;
+          for (int e = gtid; e < kTok * (kD / 16); e += kGroupThreads) {
+            const int a = e >> 3, u = e & 7;
+            const int ta = slot_token(d, x, j, a);
+            uint4* v = reinterpret_cast<uint4*>(vt + a * kD + ((u ^ (a & 7)) << 4));
+            if (!slot_valid(x, ta)) {
+              *v = make_uint4(0, 0, 0, 0);
+              continue;
+            }
+            uint4 w = *v;
+            uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+            uint32_t any = 0;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) any |= ((ww[k] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+            if (any == 0) continue;
+            for (int k = 0; k < 16; ++k) {
+              const int sh = 8 * (k & 3);
+              if (((ww[k >> 2] >> sh) & 0x7Fu) == 0x7Fu) {
+                ww[k >> 2] &= ~(0xFFu << sh);
+                atomicMin(&misc->nan_from[16 * u + k], ta);
+              }
+            }
+            *v = make_uint4(ww[0], ww[1], ww[2], ww[3]);
+          }
+        }
+        first = false;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(&misc->p_full[grp]));
+      }
+      // ------------------------------------------------------------ epilogue
+      // sums over the group's threads, then over its warps, in a fixed order
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        float v = l[r];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        if (lane == 0) misc->lpart[grp][quad][r] = v;
+      }
+      // g is now the number of tiles so far; the groups' shares of them
+      const int n0 = (g + 1) >> 1, n1 = g >> 1;
+      const int has0 = t1 - t0 > 1 || (g & 1), has1 = t1 - t0 > 1 || !(g & 1);
+      bool ok_e = ok;
+      if (ok_e && has0) ok_e = wait(&misc->pv_done[0], (n0 - 1) & 1);
+      if (ok_e && has1) ok_e = wait(&misc->pv_done[1], (n1 - 1) & 1);
+      if (named_bar_or(kBarAll, 2 * kGroupThreads, !ok_e)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const size_t sl = 2 * (size_t)blockIdx.x + slot;
+      if (tid < R) {
+        const int r = tid;
+        float lg[2], M = kNoRef;
+        for (int k = 0; k < 2; ++k) {
+          lg[k] = (misc->lpart[k][0][r] + misc->lpart[k][1][r]) +
+                  (misc->lpart[k][2][r] + misc->lpart[k][3][r]);
+          M = fmaxf(M, misc->m[k][r]);
+        }
+        const float w0 = ex2_approx(misc->m[0][r] - M), w1 = ex2_approx(misc->m[1][r] - M);
+        const float tot = w0 * lg[0] + w1 * lg[1];
+        const bool none = tot == 0.0f || r >= x.live;   // not NaN
+        const float it_ = none ? 0.0f : 1.0f / tot;
+        misc->f[0][r] = w0 * it_;
+        misc->f[1][r] = w1 * it_;
+        if (r < x.rows) {
+          const float v = none ? -CUDART_INF_F : (M + log2f(tot)) * 0.69314718055994530942f;
+          if (whole) p.lse[out_row(d, x, r)] = v;
+          else p.ws_lse[sl * kRows + r] = v;
+        }
+      }
+      named_bar_sync(kBarAll, 2 * kGroupThreads);
+      // thread (quad, lane) holds dim 32 quad + lane of every row; the groups
+      // take turns over 16 rows
+      const int dim = 32 * quad + lane;
+      const int nan_from = misc->nan_from[dim];
+#pragma unroll 1
+      for (int r0 = 16 * grp; r0 < x.rows; r0 += 32) {
+        float o[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) o[k] = 0.0f;
+#pragma unroll 1
+        for (int gg = 0; gg < 2; ++gg) {
+          if (!(gg ? has1 : has0)) continue;       // its accumulator holds nothing of this piece
+          float a[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) a[k] = 0.0f;
+#pragma unroll
+          for (int term = 0; term < 3; ++term) {
+            uint32_t v[16];
+            tmem_ld16(tO + 3 * R * gg + R * term + r0, v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 16; ++k) a[k] += __uint_as_float(v[k]);
+          }
+#pragma unroll
+          for (int k = 0; k < 16; ++k) o[k] = fmaf(a[k], misc->f[gg][r0 + k], o[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const int r = r0 + k;
+          if (r >= x.rows) break;
+          float v = misc->lim[r] >= nan_from ? CUDART_NAN_F : o[k];
+          if (r >= x.live) v = 0.0f;
+          if (whole) p.out[out_row(d, x, r) * kD + dim] = v;
+          else p.ws_o[(sl * kRows + r) * kD + dim] = v;
+        }
+      }
+      tc_fence_before();
+      named_bar_sync(kBarAll, 2 * kGroupThreads);  // accumulators and exchange are free again
+      ++pc;
+    }
+  }
+
+  // ---------------------------------------------------------------- teardown
+  if (warp == 0) cp_async_wait_all();
+  tc_fence_before();
+  __syncthreads();
+  if (*abort_flag) {
+    // after a failure, let this CTA's own MMAs and copies complete first
+    int never = 0;
+    if (lane == 0 && (warp == 1 || warp == 2)) {
+      mma_commit(bar(&misc->drain));
+      mbar_wait(bar(&misc->drain), 0, kDrainNs, &never);
+    }
+    if (warp == 0 && lane == 0)
+      for (int st = 0; st < kStages; ++st)
+        if (armed[st] >= 0)
+          mbar_wait(bar(&misc->kv_full[st]), (armed[st] / kStages) & 1, kDrainNs, &never);
+    tc_fence_before();
+    __syncthreads();
+  }
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// Units not written by the partial kernel: no token in the shard (o = 0, lse =
+// -inf) and units split across CTAs (their pieces merged by LSE).  Block u,
+// warp w handles rows w, w + 4, ...; lane: dims 4 lane .. 4 lane + 3.
+__global__ void __launch_bounds__(128) gqa_fp8_merge_kernel(Desc d, const WsHeader* hdr,
+                                                            const int* prefix, const float* ws_o,
+                                                            const float* ws_lse, float* out,
+                                                            float* lse) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int u = blockIdx.x;
+  const Unit x = make_unit(d, u);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int ps = prefix[u], ue = prefix[u + 1];
+  const int us = unit_tile_start(prefix, u, hdr->unit_cost);
+  const int per = hdr->per_cta;
+  const bool empty = us == ue;
+  const int c0 = empty ? 0 : us / per, c1 = empty ? 0 : (ue - 1) / per;
+  if (!empty && c0 == c1) return;   // written by the partial kernel
+  auto slot_of = [&](int c) -> size_t {
+    return (c == c0 && c0 * per < ps) ? 2 * (size_t)c + 1 : 2 * (size_t)c;
+  };
+  const int np = c1 - c0 + 1;
+  for (int r = warp; r < x.rows; r += 4) {
+    const size_t row = out_row(d, x, r);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float M = -CUDART_INF_F, wsum = 0.f;
+    if (!empty) {
+      for (int k = lane; k < np; k += 32) M = fmaxf(M, ws_lse[slot_of(c0 + k) * kRows + r]);
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+      for (int k = 0; k < np; ++k) {
+        const size_t s = slot_of(c0 + k);
+        const float e = ws_lse[s * kRows + r];
+        if (e == -CUDART_INF_F) continue;   // a NaN goes on
+        const float w = __expf(e - M);
+        wsum += w;
+        const float4 o = reinterpret_cast<const float4*>(ws_o + (s * kRows + r) * kD)[lane];
+        acc.x += w * o.x;
+        acc.y += w * o.y;
+        acc.z += w * o.z;
+        acc.w += w * o.w;
+      }
+    }
+    const bool none = wsum == 0.f;
+    const float inv = none ? 0.f : 1.0f / wsum;
+    reinterpret_cast<float4*>(out + row * kD)[lane] =
+        make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+    if (lane == 0) lse[row] = none ? -CUDART_INF_F : M + logf(wsum);
+  }
+}
+
+// ------------------------------------------------------------------ host side
 bool shape_ok(const gqa_shape* s) {
   if (s == nullptr || s->batch < 1 || s->q_len < 1 || s->num_heads < 1 || s->num_kv_heads < 1)
     return false;
@@ -149,6 +817,55 @@ bool shards_ok(int num_shards, int shard_id) {
          (shard_id == MLA_ALL_SHARDS || (shard_id >= 0 && shard_id < num_shards));
 }
 
+// Query rows per work unit: the smallest tile that holds a KV head's rows of
+// a request, 64 at most; and the row groups that needs, of even size.
+struct Split {
+  int R, ni, Gq, units;
+};
+
+Split split_for(const gqa_shape* s, int num_shards, int shard_id) {
+  const int G = s->num_heads / s->num_kv_heads;
+  Split x;
+  x.R = (long long)s->q_len * G <= 16 ? 16 : (long long)s->q_len * G <= 32 ? 32 : 64;
+  x.Gq = ceil_div(s->q_len, x.R / G);
+  x.ni = ceil_div(s->q_len, x.Gq);
+  x.units = s->batch * (shard_id == MLA_ALL_SHARDS ? num_shards : 1) * s->num_kv_heads * x.Gq;
+  return x;
+}
+
+struct WsLayout {
+  size_t prefix, ws_o, ws_lse, total;
+};
+
+WsLayout ws_layout(int num_units, int grid) {
+  auto up = [](size_t v) { return (v + 255) & ~static_cast<size_t>(255); };
+  WsLayout w;
+  w.prefix = up(sizeof(WsHeader));
+  w.ws_o = w.prefix + up(sizeof(int) * (size_t)(num_units + 1));
+  w.ws_lse = w.ws_o + up(sizeof(float) * (size_t)grid * 2 * kRows * kD);
+  w.total = w.ws_lse + up(sizeof(float) * (size_t)grid * 2 * kRows);
+  return w;
+}
+
+int grid_size() { return std::min(host::device_sm_count(), 512); }
+
+template <int R>
+cudaError_t launch_partial(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const Params& p,
+                           int grid, cudaStream_t st) {
+  const cudaError_t e = host::ensure_dynamic_smem(
+      reinterpret_cast<const void*>(&gqa_fp8_partial_kernel<R>), Smem<R>::kBytes);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr = pdl_attribute();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Smem<R>::kBytes;
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, gqa_fp8_partial_kernel<R>, tm_k, tm_v, p);
+}
+
 }  // namespace gqa8
 }  // namespace mla
 
@@ -160,7 +877,9 @@ size_t gqa_fp8_workspace_size(const gqa_shape* shape, int num_shards, int shard_
   if (!gqa8::shape_ok(shape) || !gqa8::shape_supported(shape) ||
       !gqa8::shards_ok(num_shards, shard_id))
     return 0;
-  return sizeof(WsHeader);
+  const int grid = gqa8::grid_size();
+  if (grid <= 0) return 0;
+  return gqa8::ws_layout(gqa8::split_for(shape, num_shards, shard_id).units, grid).total;
 }
 
 mla_status gqa_decode_partial_fp8(const void* q, const gqa_block_pages* cache,
@@ -195,8 +914,13 @@ mla_status gqa_decode_partial_fp8(const void* q, const gqa_block_pages* cache,
       !aligned4(block_table) || !aligned4(seq_lens) || !aligned4(q_lens))
     return MLA_ERR_INVALID;
   if (workspace == nullptr || !aligned16(workspace)) return MLA_ERR_WORKSPACE;
-  if (workspace_bytes < gqa_fp8_workspace_size(shape, num_shards, shard_id))
-    return MLA_ERR_WORKSPACE;
+  const int grid = gqa8::grid_size();
+  if (grid <= 0) return MLA_ERR_CUDA;
+  const gqa8::Split sp = gqa8::split_for(shape, num_shards, shard_id);
+  const gqa8::WsLayout wl = gqa8::ws_layout(sp.units, grid);
+  if (workspace_bytes < wl.total) return MLA_ERR_WORKSPACE;
+  host::EncodeTiledFn encode = host::encode_fn();
+  if (encode == nullptr) return MLA_ERR_CUDA;
 
   gqa8::Desc d;
   d.B = shape->batch;
@@ -204,6 +928,8 @@ mla_status gqa_decode_partial_fp8(const void* q, const gqa_block_pages* cache,
   d.H = shape->num_heads;
   d.Hkv = shape->num_kv_heads;
   d.G = d.H / d.Hkv;
+  d.ni = sp.ni;
+  d.Gq = sp.Gq;
   d.num_shards = num_shards;
   d.shard_first = shard_id == MLA_ALL_SHARDS ? 0 : shard_id;
   d.n_out = shard_id == MLA_ALL_SHARDS ? num_shards : 1;
@@ -216,19 +942,68 @@ mla_status gqa_decode_partial_fp8(const void* q, const gqa_block_pages* cache,
   while ((1 << d.lg_block) < cache->block) ++d.lg_block;
   d.scale_log2 = shape->softmax_scale * 1.4426950408889634f;
   d.q = static_cast<const uint16_t*>(q);
-  d.k = static_cast<const uint8_t*>(cache->k);
-  d.v = static_cast<const uint8_t*>(cache->v);
   d.ks = cache->k_scale;
   d.vs = cache->v_scale;
   d.block_table = block_table;
   d.seq_lens = seq_lens;
   d.q_lens = q_lens;
-  d.err = &static_cast<WsHeader*>(workspace)->err;
+  d.nv = layout == MLA_LAYOUT_INTERLEAVED ? num_shards : 1;
+
+  // K and V [pages * 64, Hkv, 128 codes] read as (128 codes, row of one shard
+  // in a page, cache row x KV head): a box from row (page * 64 + residue) *
+  // Hkv + kh lands one page's 64 / nv slots of the shard, 128 bytes each
+  CUtensorMap tm_k, tm_v;
+  for (int which = 0; which < 2; ++which) {
+    const cuuint64_t row = (cuuint64_t)gqa8::kD * d.Hkv;
+    cuuint64_t dims[3] = {gqa8::kD, (cuuint64_t)(kPage / d.nv),
+                          (cuuint64_t)cache->num_pages * kPage * d.Hkv};
+    cuuint64_t strides[2] = {row * d.nv, gqa8::kD};
+    cuuint32_t box[3] = {gqa8::kD, (cuuint32_t)(kPage / d.nv), 1};
+    cuuint32_t es[3] = {1, 1, 1};
+    if (encode(which ? &tm_v : &tm_k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, which ? cache->v : cache->k,
+               dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return MLA_ERR_CUDA;
+  }
+
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  gqa8::Params p;
+  p.d = d;
+  p.out = out_partial;
+  p.lse = lse_partial;
+  p.hdr = reinterpret_cast<WsHeader*>(ws);
+  p.prefix = reinterpret_cast<int*>(ws + wl.prefix);
+  p.ws_o = reinterpret_cast<float*>(ws + wl.ws_o);
+  p.ws_lse = reinterpret_cast<float*>(ws + wl.ws_lse);
+  p.timeout_ns = host::wait_budget_ns(gqa8::kTimeoutNs);
+  p.withhold_query = host::g_withhold_query.load();
+
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (cudaMemsetAsync(workspace, 0, sizeof(WsHeader), st) != cudaSuccess) return MLA_ERR_CUDA;
-  gqa8::gqa_fp8_row_kernel<<<d.n_out * d.B * d.q_len * d.H, gqa8::kThreads, 0, st>>>(
-      d, out_partial, lse_partial);
-  return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+  gqa8::gqa_fp8_plan_kernel<<<1, 1024, 0, st>>>(d, p.hdr, p.prefix, grid);
+  if (cudaGetLastError() != cudaSuccess) return MLA_ERR_CUDA;
+  void* ev0 = host::g_ev_before.load();
+  void* ev1 = host::g_ev_after.load();
+  if (ev0 != nullptr && cudaEventRecord(static_cast<cudaEvent_t>(ev0), st) != cudaSuccess)
+    return MLA_ERR_CUDA;
+  const cudaError_t e = sp.R == 16   ? gqa8::launch_partial<16>(tm_k, tm_v, p, grid, st)
+                        : sp.R == 32 ? gqa8::launch_partial<32>(tm_k, tm_v, p, grid, st)
+                                     : gqa8::launch_partial<64>(tm_k, tm_v, p, grid, st);
+  if (e != cudaSuccess) return MLA_ERR_CUDA;
+  if (ev1 != nullptr && cudaEventRecord(static_cast<cudaEvent_t>(ev1), st) != cudaSuccess)
+    return MLA_ERR_CUDA;
+  cudaLaunchAttribute attr = pdl_attribute();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(sp.units);
+  cfg.blockDim = dim3(128);
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, gqa8::gqa_fp8_merge_kernel, d, (const WsHeader*)p.hdr,
+                            (const int*)p.prefix, (const float*)p.ws_o, (const float*)p.ws_lse,
+                            out_partial, lse_partial) == cudaSuccess
+             ? MLA_OK
+             : MLA_ERR_CUDA;
 }
 
 }  // extern "C"
