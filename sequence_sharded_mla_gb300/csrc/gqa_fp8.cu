@@ -59,7 +59,7 @@ namespace gqa8 {
 constexpr int kD = 128;                    // head width
 constexpr int kTok = 128;                  // tokens of a tile
 constexpr int kHalf = kTok * kD;           // 16384 bytes: K or V of a tile
-constexpr int kStages = 4;
+constexpr int kMaxStages = 6, kMaxS = 4;
 constexpr int kStageBytes = 2 * kHalf;
 constexpr int kThreads = 384;
 constexpr int kGroupThreads = 128;
@@ -77,6 +77,7 @@ struct Desc {
   int ni, Gq;          // query positions per row group, row groups per (request, KV head)
   int num_shards, shard_first, n_out, layout, local, causal;
   int num_pages, max_pages, lg_block;
+  int lg_run;          // log2 of the consecutive slots of a tile that share a scale
   int nv;              // page boxes per 64 slots: shards of a whole-request interleaved cache, else 1
   float scale_log2;
   const uint16_t* q;
@@ -164,24 +165,32 @@ __device__ __forceinline__ size_t out_row(const Desc& d, const Unit& x, int r) {
 }
 
 struct Misc {
-  uint64_t kv_full[kStages], kv_empty[kStages];
-  uint64_t s_full[2], s_empty[2], p_full[2], pv_done[2];
+  uint64_t kv_full[kMaxStages], kv_empty[kMaxStages];
+  uint64_t s_full[kMaxS], s_empty[kMaxS], p_full[2], pv_done[2];
   uint64_t q_full, drain;
   uint32_t tmem_base;
   int abort;
   int lim[kRows];               // last position a row sees
-  float qs[kRows];              // 1 / the row's query scale
-  float m[2][kRows];            // per group: the rows' references
-  float alpha[2][kRows];
+  alignas(16) float qs[kRows];        // 1 / the row's query scale
+  alignas(16) float m[2][kRows];      // per group: the rows' references
+  alignas(16) float alpha[2][kRows];
   int rmax[2][kRows];
   float lpart[2][4][kRows];     // per group and warp: sums of a piece
   float f[2][kRows];            // per group: the factor of its accumulator
   int nan_from[kD];             // per dim: the first partly seen token whose V is NaN
-  float ksc[kStages][kTok], vsc[kStages][kTok];
+  float ksc[kMaxStages][kTok], vsc[kMaxStages][kTok];   // by run of slots with one scale
 };
 
+// Stages: what fits beside the weights.  A stage lives for its load, the
+// logits, the softmax and the P V of its tile, so more of them hide more of
+// that chain.  S buffers: two per group where TMEM has room, so that a tile's
+// logits are there when the group comes back from the one before.
 template <int R>
 struct Smem {
+  static constexpr int kStages = R == 64 ? 4 : R == 32 ? 5 : 6;
+  static constexpr int kSBufs = R == 64 ? 2 : 4;
+  static constexpr uint32_t kColO = kSBufs * R;                 // O^T after the S buffers
+  static constexpr uint32_t kTmemCols = R == 16 ? 256 : 512;
   static constexpr int kQ = 0;                              // [2][R][128]
   static constexpr int kP = 2 * R * kD;                     // [2 groups][3][128 tokens][R]
   static constexpr int kPGroup = 3 * R * kTok;
@@ -241,7 +250,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     gqa_fp8_partial_kernel(const __grid_constant__ CUtensorMap tm_k,
                            const __grid_constant__ CUtensorMap tm_v, Params p) {
   using S = Smem<R>;
-  constexpr uint32_t kTmemCols = 8 * R;          // S: 2 x R, O^T: 2 x 3R
+  constexpr int kStages = S::kStages, kSBufs = S::kSBufs;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   Misc* misc = reinterpret_cast<Misc*>(smem + S::kMisc);
@@ -276,9 +285,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar(&misc->kv_full[st]), 1 + 32);   // expect_tx + one cp.async arrival per lane
       mbar_init(bar(&misc->kv_empty[st]), 1);
     }
+    for (int k = 0; k < kSBufs; ++k) {
+      mbar_init(bar(&misc->s_full[k]), 1);
+      mbar_init(bar(&misc->s_empty[k]), 4);
+    }
     for (int g = 0; g < 2; ++g) {
-      mbar_init(bar(&misc->s_full[g]), 1);
-      mbar_init(bar(&misc->s_empty[g]), 4);
       mbar_init(bar(&misc->p_full[g]), 4);
       mbar_init(bar(&misc->pv_done[g]), 1);
     }
@@ -288,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_mbar_init();
   }
   if (warp == 1) {
-    tmem_alloc(smem_u32(&misc->tmem_base), kTmemCols);
+    tmem_alloc(smem_u32(&misc->tmem_base), S::kTmemCols);
     tmem_relinquish();
   }
   if (warp == 0 && lane == 0) {
@@ -344,15 +355,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           tma_load_3d(dst, &tm_k, full, 0, 0, crow);
           tma_load_3d(dst + kHalf, &tm_v, full, 0, 0, crow);
         }
-#pragma unroll
-        for (int h = 0; h < kTok / 32; ++h) {
-          const int a = lane + 32 * h;
+        for (int h = 0; h < (kTok >> d.lg_run); h += 32) {
+          const int e = h + lane, a = min(e << d.lg_run, kTok - 1);
           const int pg = __shfl_sync(0xffffffffu, page, a >> lg_rp);
           const int row = res + (a & (rp - 1)) * d.nv;
           const bool ok_pg = pg < d.num_pages;
           const size_t si = ok_pg ? ((size_t)pg * (kPage >> d.lg_block) + (row >> d.lg_block)) * d.Hkv + x.kh : 0;
-          cp_async_4_zfill(smem_u32(&misc->ksc[st][a]), d.ks + si, ok_pg);
-          cp_async_4_zfill(smem_u32(&misc->vsc[st][a]), d.vs + si, ok_pg);
+          if (e < (kTok >> d.lg_run)) {
+            cp_async_4_zfill(smem_u32(&misc->ksc[st][e]), d.ks + si, ok_pg);
+            cp_async_4_zfill(smem_u32(&misc->vsc[st][e]), d.vs + si, ok_pg);
+          }
         }
         cp_async_mbar_arrive_noinc(full);
         __syncwarp();
@@ -366,9 +378,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (ok && it.next(unit, t0, t1, whole, slot)) {
       if (!(ok = wait(&misc->q_full, pc & 1))) break;
       for (int j = t0; j < t1; ++j, ++g) {
-        const int st = g % kStages, round = g / kStages, grp = g & 1, gr = g >> 1;
+        const int st = g % kStages, round = g / kStages, sb = g % kSBufs, sr = g / kSBufs;
         if (!(ok = wait(&misc->kv_full[st], round & 1))) break;
-        if (gr >= 1 && !(ok = wait(&misc->s_empty[grp], (gr - 1) & 1))) break;
+        if (sr >= 1 && !(ok = wait(&misc->s_empty[sb], (sr - 1) & 1))) break;
         tc_fence_after();
         if (lane == 0) {
           const uint32_t off = (uint32_t)(st * kStageBytes) >> 4;
@@ -376,9 +388,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int term = 0; term < 2; ++term)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              mma_e4m3_ss(tmem + R * grp, dk + off + ((32 * k) >> 4),
+              mma_e4m3_ss(tmem + R * sb, dk + off + ((32 * k) >> 4),
                           dq + (uint32_t)((term * R * kD + 32 * k) >> 4), id, term + k != 0);
-          mma_commit(bar(&misc->s_full[grp]));
+          mma_commit(bar(&misc->s_full[sb]));
         }
         __syncwarp();
       }
@@ -405,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t off = (uint32_t)(st * kStageBytes) >> 4;
 #pragma unroll
           for (int k = 0; k < 4; ++k)   // 32 tokens each
-            mma_e4m3_ss(tmem + 2 * R + 3 * R * grp, dv + off + ((k * 4 * 1024) >> 4),
+            mma_e4m3_ss(tmem + S::kColO + 3 * R * grp, dv + off + ((k * 4 * 1024) >> 4),
                         dp + (uint32_t)((k * 32 * R) >> 4), id, (j >= t0 + 2 || k != 0) ? 1u : 0u);
           mma_commit(bar(&misc->kv_empty[st]));
           mma_commit(bar(&misc->pv_done[grp]));
@@ -419,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int gtid = (threadIdx.x - 128) & 127;    // 0..127 in the group: its token of a tile
     const int tid = threadIdx.x - 128;             // 0..255
     const uint32_t lane_off = (uint32_t)(32 * quad) << 16;
-    const uint32_t tS = tmem + lane_off + R * grp, tO = tmem + lane_off + 2 * R;
+    const uint32_t tS = tmem + lane_off, tO = tmem + lane_off + S::kColO;
     float* ref = misc->m[grp];
     int g = 0, pc = 0;
     while (ok && it.next(unit, t0, t1, whole, slot)) {
@@ -469,23 +481,38 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0 && !(p.withhold_query && pc == 0)) mbar_arrive(bar(&misc->q_full));
       named_bar_sync(kBarAll, 2 * kGroupThreads);
 
+      // 16 rows' values of a shared array; for R = 16 the query scales and the
+      // references stay in registers
+      auto load16 = [](const float* a, float (&v)[16]) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float4 t = reinterpret_cast<const float4*>(a)[k];
+          v[4 * k] = t.x;
+          v[4 * k + 1] = t.y;
+          v[4 * k + 2] = t.z;
+          v[4 * k + 3] = t.w;
+        }
+      };
+      float qs16[16], ref16[16];
+      load16(misc->qs, qs16);
+      load16(ref, ref16);
       float l[R];
 #pragma unroll
       for (int r = 0; r < R; ++r) l[r] = 0.0f;
       bool first = true;                           // the group's first tile of the piece
       for (int j = t0; j < t1; ++j, ++g) {
         if ((g & 1) != grp) continue;
-        const int st = g % kStages, gr = g >> 1;
+        const int st = g % kStages, gr = g >> 1, sb = g % kSBufs;
         // -------------------------------------------------------- logits
         const bool ok_s = ok && wait(&misc->kv_full[st], (g / kStages) & 1) &&
-                          wait(&misc->s_full[grp], gr & 1);
+                          wait(&misc->s_full[sb], (g / kSBufs) & 1);
         const bool full = tile_full(d, x, j);
         const int t = slot_token(d, x, j, gtid);
         const bool valid = full || slot_valid(x, t);
         float c = 0.0f, lv = 0.0f, inv = 0.0f, fv = 1.0f;
         if (ok_s && valid) {
-          c = misc->ksc[st][gtid] * d.scale_log2;
-          const float sv = misc->vsc[st][gtid], av = fabsf(sv);
+          c = misc->ksc[st][gtid >> d.lg_run] * d.scale_log2;
+          const float sv = misc->vsc[st][gtid >> d.lg_run], av = fabsf(sv);
           // |sv| below 2^-60 counts as 2^-60 in the reference and as itself in
           // the product; a scale that is not finite goes to the product alone
           const float ve = av < INFINITY ? fmaxf(av, kMinScale) : 1.0f;
@@ -497,11 +524,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         // 16 rows' log2 weights (without the reference) of this token
         auto logits = [&](int r0, float (&b)[16]) {
           uint32_t sr[16];
-          tmem_ld16(tS + r0, sr);
+          tmem_ld16(tS + R * sb + r0, sr);
+          if (R > 16) load16(misc->qs + r0, qs16);
           tmem_wait_ld();
 #pragma unroll
-          for (int k = 0; k < 16; ++k)
-            b[k] = fmaf(__uint_as_float(sr[k]) * misc->qs[r0 + k], c, lv);
+          for (int k = 0; k < 16; ++k) b[k] = fmaf(__uint_as_float(sr[k]) * qs16[k], c, lv);
           if (!full) {
 #pragma unroll
             for (int k = 0; k < 16; ++k)
@@ -515,8 +542,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int r0 = 0; r0 < R; r0 += 16) {
             logits(r0, b);
+            if (R > 16) load16(ref + r0, ref16);
 #pragma unroll
-            for (int k = 0; k < 16; ++k) over = over || b[k] - ref[r0 + k] > kMost;
+            for (int k = 0; k < 16; ++k) over = over || b[k] - ref16[k] > kMost;
           }
         }
         if (named_bar_or(kBarGroup + grp, kGroupThreads, over || !ok_s)) {
@@ -550,6 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = false;
             break;
           }
+          if (R == 16) load16(ref, ref16);
 #pragma unroll
           for (int r = 0; r < R; ++r) l[r] *= misc->alpha[grp][r];
           if (!first) {
@@ -568,6 +597,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         // ------------------------------------------------------- weights
+        if (R == 16) {                             // the logits are in registers
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(&misc->s_empty[sb]));
+        }
         // the group's last P V has read the weights' buffer
         if (!first && !wait(&misc->pv_done[grp], (gr - 1) & 1)) {
           ok = false;
@@ -576,7 +610,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint8_t* prow = smem + S::kP + grp * S::kPGroup + gtid * R;
 #pragma unroll
         for (int r0 = 0; r0 < R; r0 += 16) {
-          if (R > 16) logits(r0, b);
+          if (R > 16) {
+            logits(r0, b);
+            load16(ref + r0, ref16);
+          }
           uint32_t w0[4], w1[4], w2[4];
 #pragma unroll
           for (int q4 = 0; q4 < 4; ++q4) {
@@ -584,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const int r = r0 + 4 * q4 + k;
-              pw[k] = ex2_approx(b[4 * q4 + k] - ref[r]);
+              pw[k] = ex2_approx(b[4 * q4 + k] - ref16[4 * q4 + k]);
               l[r] = fmaf(pw[k], inv, l[r]);
               if (scaled) pw[k] = pw[k] > 0.0f || pw[k] != pw[k] ? pw[k] * fv : 0.0f;
             }
@@ -602,9 +639,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           *reinterpret_cast<uint4*>(prow + R * kTok + 16 * u) = make_uint4(w1[0], w1[1], w1[2], w1[3]);
           *reinterpret_cast<uint4*>(prow + 2 * R * kTok + 16 * u) = make_uint4(w2[0], w2[1], w2[2], w2[3]);
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(&misc->s_empty[grp]));
+        if (R > 16) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(&misc->s_empty[sb]));
+        }
         if (!full) {
           // V rows of slots without a token become zeros; a NaN code of a token
           // that not every row sees is taken out too and comes back in the
@@ -636,6 +675,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         first = false;
         fence_proxy_async_smem();
+        tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(&misc->p_full[grp]));
       }
@@ -743,7 +783,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, kTmemCols);
+    tmem_dealloc(tmem, S::kTmemCols);
   }
 }
 
@@ -948,6 +988,8 @@ mla_status gqa_decode_partial_fp8(const void* q, const gqa_block_pages* cache,
   d.seq_lens = seq_lens;
   d.q_lens = q_lens;
   d.nv = layout == MLA_LAYOUT_INTERLEAVED ? num_shards : 1;
+  d.lg_run = d.lg_block;   // less the stride of a shard's rows within a page
+  for (int n = d.nv; n > 1 && d.lg_run > 0; n >>= 1) --d.lg_run;
 
   // K and V [pages * 64, Hkv, 128 codes] read as (128 codes, row of one shard
   // in a page, cache row x KV head): a box from row (page * 64 + residue) *
