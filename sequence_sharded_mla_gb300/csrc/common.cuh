@@ -143,6 +143,27 @@ struct PieceIter {
     }
     u = a;
   }
+  // init() by a whole warp: each round looks at 32 places of the range at once.
+  __device__ void init_warp(const int* pfx, int num_units, int lo_, int hi_, int unit_cost,
+                            int lane) {
+    prefix = pfx;
+    U = num_units;
+    lo = lo_;
+    hi = hi_;
+    pos = lo_;
+    uc = unit_cost;
+    first = true;
+    // last unit with prefix[u] <= lo, in [a, a + n)
+    int a = 0, n = num_units;
+    while (n > 1) {
+      const int step = (n + 31) >> 5, at = a + lane * step;
+      const bool below = at < a + n && prefix[at] <= lo_;
+      const int k = 31 - __clz(__ballot_sync(0xffffffffu, below) | 1u);
+      n = min(step, a + n - (a + k * step));
+      a += k * step;
+    }
+    u = a;
+  }
   // Next piece: unit, tile range [t0, t1), whether it is the whole unit, and
   // the workspace slot of a partial piece (0: the CTA's first piece, 1: its
   // last).  Positions of a unit's fixed-cost part hold no tile.

@@ -171,6 +171,7 @@ struct Misc {
   uint32_t tmem_base;
   int abort;
   int lim[kRows];               // last position a row sees
+  int orow[kRows];              // the row's output row
   alignas(16) float qs[kRows];        // 1 / the row's query scale
   alignas(16) float m[2][kRows];      // per group: the rows' references
   alignas(16) float alpha[2][kRows];
@@ -189,7 +190,11 @@ template <int R>
 struct Smem {
   static constexpr int kStages = R == 64 ? 4 : R == 32 ? 5 : 6;
   static constexpr int kSBufs = R == 64 ? 2 : 4;
-  static constexpr uint32_t kColO = kSBufs * R;                 // O^T after the S buffers
+  // Q's two terms side by side in one MMA of 2R columns, added when S is read,
+  // or (R = 64: TMEM is full) two chains into the same columns
+  static constexpr bool kPair = R < 64;
+  static constexpr int kSCols = kPair ? 2 * R : R;
+  static constexpr uint32_t kColO = kSBufs * kSCols;            // O^T after the S buffers
   static constexpr uint32_t kTmemCols = R == 16 ? 256 : 512;
   static constexpr int kQ = 0;                              // [2][R][128]
   static constexpr int kP = 2 * R * kD;                     // [2 groups][3][128 tokens][R]
@@ -225,6 +230,12 @@ __device__ __forceinline__ float from_ordered(int i) {
 __device__ __forceinline__ float lg2_approx(float x) {
   float y;
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ float rcp_approx(float x) {   // within 1 ulp
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 
@@ -312,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = misc->tmem_base;
 
   PieceIter it;
-  it.init(p.prefix, p.hdr->num_units, lo, hi, p.hdr->unit_cost);
+  it.init_warp(p.prefix, p.hdr->num_units, lo, hi, p.hdr->unit_cost, lane);
   int armed[kStages];
   for (int st = 0; st < kStages; ++st) armed[st] = -1;
   int unit, t0, t1, slot;
@@ -323,14 +334,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int nb = 2 * d.nv;                     // page boxes per tile
     const int rp = kPage / d.nv;                 // slots per box
     const int lg_rp = 31 - __clz(rp);
+    const int box = lane & 15;                   // lanes 0..15 load K, 16..31 V
+    const CUtensorMap* tm = lane < 16 ? &tm_k : &tm_v;
+    const uint32_t dst0 = sSt + (lane < 16 ? 0 : kHalf) + box * (rp * kD);
+    const int lg_sub = 6 - d.lg_block;           // scales per page and head
+    const int runs = kTok >> d.lg_run;
     int g = 0;
     while (ok && it.next(unit, t0, t1, whole, slot)) {
       const Unit x = make_unit(d, unit);
       const int32_t* bt = d.block_table + (size_t)x.b * d.max_pages;
       const int res = d.nv > 1 ? x.s : 0;
       auto entry = [&](int j) {                  // page of this lane's box of tile j, or -1
-        const int idx = x.p0 + j * nb + lane;
-        return (lane < nb && idx < x.npages && idx < d.max_pages) ? __ldg(bt + idx) : -1;
+        const int idx = x.p0 + j * nb + box;
+        return (box < nb && idx < x.npages && idx < d.max_pages) ? __ldg(bt + idx) : -1;
       };
       int next = entry(t0);
       for (int j = t0; j < t1; ++j, ++g) {
@@ -339,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (j + 1 < t1) next = entry(j + 1);
         const bool there = page >= 0 && page < d.num_pages;
         if (!there) {
-          if (lane < nb && x.p0 + j * nb + lane < x.npages) atomicOr(&p.hdr->err, kErrBadPage);
+          if (box < nb && x.p0 + j * nb + box < x.npages) atomicOr(&p.hdr->err, kErrBadPage);
           page = d.num_pages;                    // out of the map: TMA fills zeros
         }
         if (round >= 1 && !(ok = wait(&misc->kv_empty[st], (round - 1) & 1))) break;
@@ -349,19 +365,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           armed[st] = g;
         }
         __syncwarp();
-        if (lane < nb) {
-          const uint32_t dst = sSt + st * kStageBytes + lane * (rp * kD);
-          const int crow = (page * kPage + res) * d.Hkv + x.kh;
-          tma_load_3d(dst, &tm_k, full, 0, 0, crow);
-          tma_load_3d(dst + kHalf, &tm_v, full, 0, 0, crow);
-        }
-        for (int h = 0; h < (kTok >> d.lg_run); h += 32) {
+        if (box < nb)
+          tma_load_3d(dst0 + st * kStageBytes, tm, full, 0, 0, (page * kPage + res) * d.Hkv + x.kh);
+        for (int h = 0; h < runs; h += 32) {
           const int e = h + lane, a = min(e << d.lg_run, kTok - 1);
           const int pg = __shfl_sync(0xffffffffu, page, a >> lg_rp);
           const int row = res + (a & (rp - 1)) * d.nv;
           const bool ok_pg = pg < d.num_pages;
-          const size_t si = ok_pg ? ((size_t)pg * (kPage >> d.lg_block) + (row >> d.lg_block)) * d.Hkv + x.kh : 0;
-          if (e < (kTok >> d.lg_run)) {
+          // below 2^31, as the cache's rows are
+          const int si = ok_pg ? ((pg << lg_sub) + (row >> d.lg_block)) * d.Hkv + x.kh : 0;
+          if (e < runs) {
             cp_async_4_zfill(smem_u32(&misc->ksc[st][e]), d.ks + si, ok_pg);
             cp_async_4_zfill(smem_u32(&misc->vsc[st][e]), d.vs + si, ok_pg);
           }
@@ -372,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ K Q^T
-    const uint32_t id = idesc_e4m3_f32(kTok, R, false, false);
+    const uint32_t id = idesc_e4m3_f32(kTok, S::kSCols, false, false);
     const uint64_t dk = sw128_desc(sSt, 16, 1024), dq = sw128_desc(sQ, 16, 1024);
     int g = 0, pc = 0;
     while (ok && it.next(unit, t0, t1, whole, slot)) {
@@ -385,10 +398,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
           const uint32_t off = (uint32_t)(st * kStageBytes) >> 4;
 #pragma unroll
-          for (int term = 0; term < 2; ++term)
+          for (int term = 0; term < (S::kPair ? 1 : 2); ++term)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              mma_e4m3_ss(tmem + R * sb, dk + off + ((32 * k) >> 4),
+              mma_e4m3_ss(tmem + S::kSCols * sb, dk + off + ((32 * k) >> 4),
                           dq + (uint32_t)((term * R * kD + 32 * k) >> 4), id, term + k != 0);
           mma_commit(bar(&misc->s_full[sb]));
         }
@@ -471,6 +484,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (c == 0) {
           if ((mx >> 7) == 255u) atomicOr(&p.hdr->err, kErrQRange);
           misc->qs[r] = __uint_as_float((e - 7u) << 23);
+          if (r < x.rows) misc->orow[r] = (int)out_row(d, x, r);
           misc->lim[r] = d.causal && r < x.live ? x.L - x.qn + x.i0 + r / d.G : INT_MAX - 1;
         }
       }
@@ -504,31 +518,40 @@ __global__ void __launch_bounds__(kThreads, 1)
         if ((g & 1) != grp) continue;
         const int st = g % kStages, gr = g >> 1, sb = g % kSBufs;
         // -------------------------------------------------------- logits
-        const bool ok_s = ok && wait(&misc->kv_full[st], (g / kStages) & 1) &&
-                          wait(&misc->s_full[sb], (g / kSBufs) & 1);
         const bool full = tile_full(d, x, j);
         const int t = slot_token(d, x, j, gtid);
         const bool valid = full || slot_valid(x, t);
+        bool ok_s = ok && wait(&misc->kv_full[st], (g / kStages) & 1);
         float c = 0.0f, lv = 0.0f, inv = 0.0f, fv = 1.0f;
         if (ok_s && valid) {
           c = misc->ksc[st][gtid >> d.lg_run] * d.scale_log2;
-          const float sv = misc->vsc[st][gtid >> d.lg_run], av = fabsf(sv);
+          const float sv = misc->vsc[st][gtid >> d.lg_run];
           // |sv| below 2^-60 counts as 2^-60 in the reference and as itself in
           // the product; a scale that is not finite goes to the product alone
-          const float ve = av < INFINITY ? fmaxf(av, kMinScale) : 1.0f;
+          float ve = sv;
+          if (!(sv >= kMinScale && sv < INFINITY)) {
+            ve = fabsf(sv) < INFINITY ? fmaxf(fabsf(sv), kMinScale) : 1.0f;
+            fv = sv / ve;
+          }
           lv = lg2_approx(ve);
-          inv = 1.0f / ve;
-          fv = sv / ve;
+          inv = rcp_approx(ve);
         }
+        ok_s = ok_s && wait(&misc->s_full[sb], (g / kSBufs) & 1);
         const bool scaled = __any_sync(0xffffffffu, fv != 1.0f);
         // 16 rows' log2 weights (without the reference) of this token
         auto logits = [&](int r0, float (&b)[16]) {
           uint32_t sr[16];
-          tmem_ld16(tS + R * sb + r0, sr);
+          tmem_ld16(tS + S::kSCols * sb + r0, sr);
+          uint32_t sl[16];
+          if (S::kPair) tmem_ld16(tS + S::kSCols * sb + R + r0, sl);
           if (R > 16) load16(misc->qs + r0, qs16);
           tmem_wait_ld();
 #pragma unroll
-          for (int k = 0; k < 16; ++k) b[k] = fmaf(__uint_as_float(sr[k]) * qs16[k], c, lv);
+          for (int k = 0; k < 16; ++k) {
+            float v = __uint_as_float(sr[k]);
+            if (S::kPair) v += __uint_as_float(sl[k]);
+            b[k] = fmaf(v * qs16[k], c, lv);
+          }
           if (!full) {
 #pragma unroll
             for (int k = 0; k < 16; ++k)
@@ -716,7 +739,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         misc->f[1][r] = w1 * it_;
         if (r < x.rows) {
           const float v = none ? -CUDART_INF_F : (M + log2f(tot)) * 0.69314718055994530942f;
-          if (whole) p.lse[out_row(d, x, r)] = v;
+          if (whole) p.lse[misc->orow[r]] = v;
           else p.ws_lse[sl * kRows + r] = v;
         }
       }
@@ -753,8 +776,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (r >= x.rows) break;
           float v = misc->lim[r] >= nan_from ? CUDART_NAN_F : o[k];
           if (r >= x.live) v = 0.0f;
-          if (whole) p.out[out_row(d, x, r) * kD + dim] = v;
-          else p.ws_o[(sl * kRows + r) * kD + dim] = v;
+          (whole ? p.out + (size_t)misc->orow[r] * kD : p.ws_o + (sl * kRows + r) * kD)[dim] = v;
         }
       }
       tc_fence_before();
