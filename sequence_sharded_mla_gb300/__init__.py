@@ -160,7 +160,13 @@ def _shape(batch, q_len, num_heads, causal, softmax_scale, q_lens=None):
                      float(softmax_scale), None if q_lens is None else q_lens.data_ptr())
 
 
+# handle of a device's current stream (torch.cuda.current_stream builds an object)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream_ptr(stream):
+    if stream is None and _raw_stream is not None:
+        return ctypes.c_void_p(_raw_stream(torch.cuda.current_device()))
     s = torch.cuda.current_stream() if stream is None else stream
     return ctypes.c_void_p(s.cuda_stream)
 
@@ -569,7 +575,7 @@ def _fp8_types():
 
 
 def _shape_is(t, name, shape):
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
 
 
@@ -605,9 +611,27 @@ def _block_pages(k_cache, v_cache, k_scale, v_scale, dev):
 
 
 def _on(dev, stream):
-    """The stream of a call on `dev`: the given one, else dev's current one."""
-    s = torch.cuda.current_stream(dev) if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    """The stream handle of a call on `dev`: the given stream's, else that of
+    dev's current one."""
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(dev.index)
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
+def _enter(dev):
+    """Makes `dev` the current device; the index to go back to, or -1."""
+    current = torch.cuda.current_device()
+    if current == dev.index:
+        return -1
+    torch.cuda.set_device(dev)
+    return current
+
+
+def _leave(previous):
+    if previous >= 0:
+        torch.cuda.set_device(previous)
 
 
 def gqa_decode_partial_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens,
@@ -640,24 +664,35 @@ def gqa_decode_partial_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, s
     scale = 1.0 / math.sqrt(D) if softmax_scale is None else softmax_scale
     n_out = num_shards if shard_id == ALL_SHARDS else 1
     sh = _gqa_shape(B, q_len, H, pages.num_kv_heads, D, causal, scale)
-    with torch.cuda.device(dev):
-        need = int(lib().gqa_fp8_workspace_size(ctypes.byref(sh), int(num_shards), int(shard_id)))
-        if out_partial is None:
-            out_partial = torch.empty((max(n_out, 1), B, q_len, H, D), dtype=torch.float32, device=dev)
-        if lse_partial is None:
-            lse_partial = torch.empty((max(n_out, 1), B, q_len, H), dtype=torch.float32, device=dev)
-        if workspace is None:
-            workspace = torch.empty((max(need, 256),), dtype=torch.uint8, device=dev)
+    rows = (max(n_out, 1), B, q_len, H)
+    if out_partial is None:
+        out_partial = torch.empty(rows + (D,), dtype=torch.float32, device=dev)
+    else:
         _check(out_partial, "out_partial", (torch.float32,), 5, dev)
+        _shape_is(out_partial, "out_partial", rows + (D,))
+    if lse_partial is None:
+        lse_partial = torch.empty(rows, dtype=torch.float32, device=dev)
+    else:
         _check(lse_partial, "lse_partial", (torch.float32,), 4, dev)
-        _check(workspace, "workspace", (torch.uint8,), 1, dev)
-        _shape_is(out_partial, "out_partial", (max(n_out, 1), B, q_len, H, D))
-        _shape_is(lse_partial, "lse_partial", (max(n_out, 1), B, q_len, H))
-        st = lib().gqa_decode_partial_fp8(_ptr(q), ctypes.byref(pages), _ptr(block_table),
-                                          block_table.shape[1], _ptr(seq_lens), _ptr(q_lens),
+        _shape_is(lse_partial, "lse_partial", rows)
+    previous = _enter(dev)
+    try:
+        if workspace is None:
+            need = int(lib().gqa_fp8_workspace_size(ctypes.byref(sh), int(num_shards),
+                                                    int(shard_id)))
+            workspace = torch.empty((max(need, 256),), dtype=torch.uint8, device=dev)
+        else:
+            _check(workspace, "workspace", (torch.uint8,), 1, dev)
+        st = lib().gqa_decode_partial_fp8(q.data_ptr(), ctypes.byref(pages),
+                                          block_table.data_ptr(), block_table.shape[1],
+                                          seq_lens.data_ptr(),
+                                          None if q_lens is None else q_lens.data_ptr(),
                                           ctypes.byref(sh), int(shard_id), int(num_shards),
-                                          LAYOUTS[layout], _ptr(out_partial), _ptr(lse_partial),
-                                          _ptr(workspace), workspace.numel(), _on(dev, stream))
+                                          LAYOUTS[layout], out_partial.data_ptr(),
+                                          lse_partial.data_ptr(), workspace.data_ptr(),
+                                          workspace.numel(), _on(dev, stream))
+    finally:
+        _leave(previous)
     if st != 0:
         raise MLAError(st, "gqa_decode_partial_fp8")
     return out_partial, lse_partial, workspace
@@ -753,12 +788,15 @@ def _token_stride(t, name, dims):
         raise ValueError(f"{name} must be on a CUDA device")
     if t.dim() != 2 + dims:
         raise ValueError(f"{name} must have {2 + dims} dims, got {t.dim()}")
+    shape = t.shape
+    if t.is_contiguous():
+        return shape[2] if dims == 1 else shape[2] * shape[3]
     width = 1
     for d in range(t.dim() - 1, 1, -1):
-        if t.shape[d] != 1 and t.stride(d) != width:
+        if shape[d] != 1 and t.stride(d) != width:
             raise ValueError(f"{name}: a token's values must be contiguous")
-        width *= t.shape[d]
-    B, q_len = t.shape[:2]
+        width *= shape[d]
+    B, q_len = shape[:2]
     if q_len > 1:
         step = t.stride(1)
         if B > 1 and t.stride(0) != q_len * step:
@@ -780,29 +818,33 @@ def _tokens(B, q_len, seq_lens, q_lens, positions, dev):
     if positions is not None:
         _check(positions, "positions", (torch.int32,), 2, dev)
         _shape_is(positions, "positions", (B, q_len))
-    ptr = lambda t: None if t is None else t.data_ptr()
-    return mla_tokens(int(B), int(q_len), ptr(seq_lens), ptr(q_lens), ptr(positions))
+    return mla_tokens(B, q_len, None if seq_lens is None else seq_lens.data_ptr(),
+                      None if q_lens is None else q_lens.data_ptr(),
+                      None if positions is None else positions.data_ptr())
 
 
 def _out_rows(x, out, name, dims):
     """The output of a rotation of x: `out` checked (x itself, or memory of its
     own), or a new tensor; and the two token strides."""
     xs = _token_stride(x, name, dims)
+    if out is x:
+        return x, xs, xs
     if out is None:
         out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        return out, xs, _token_stride(out, name, dims)
     ys = _token_stride(out, name + "_out", dims)
-    _shape_is(out, name + "_out", x.shape)
+    if out.shape != x.shape:
+        _shape_is(out, name + "_out", x.shape)
     if out.device != x.device:
         raise ValueError(f"{name}_out is on {out.device}, expected {x.device}")
-    if out.data_ptr() == x.data_ptr():
+    a, b = x.data_ptr(), out.data_ptr()
+    if a == b:
         if xs != ys:
             raise ValueError(f"{name}_out overlaps {name} with other strides")
     else:
-        def span(t, step):
-            width = math.prod(t.shape[2:])
-            return t.data_ptr(), t.data_ptr() + 2 * ((t.shape[0] * t.shape[1] - 1) * step + width)
-        (a0, a1), (b0, b1) = span(x, xs), span(out, ys)
-        if a0 < b1 and b0 < a1:
+        # the bytes from the first token to the end of the last
+        tokens, width = x.shape[0] * x.shape[1] - 1, x.numel() // max(x.shape[0] * x.shape[1], 1)
+        if a < b + 2 * (tokens * ys + width) and b < a + 2 * (tokens * xs + width):
             raise ValueError(f"{name}_out overlaps {name}")
     return out, xs, ys
 
@@ -824,9 +866,12 @@ def mla_rope_apply(x, rope, seq_lens=None, q_lens=None, positions=None, out=None
         raise ValueError("give seq_lens or positions")
     tok = _tokens(B, q_len, seq_lens, q_lens, positions, dev)
     r = rope._args(dev)
-    with torch.cuda.device(dev):
-        st = lib().mla_rope_apply(_ptr(x), xs, _ptr(out), ys, ctypes.byref(tok), H, D,
+    previous = _enter(dev)
+    try:
+        st = lib().mla_rope_apply(x.data_ptr(), xs, out.data_ptr(), ys, ctypes.byref(tok), H, D,
                                   ctypes.byref(r), _on(dev, stream))
+    finally:
+        _leave(previous)
     if st != 0:
         raise MLAError(st, "mla_rope_apply")
     return out
@@ -877,18 +922,24 @@ def mla_cache_append(latent, kv, block_table, seq_lens, rope=None, q=None, q_out
     if d != D_QK:
         raise ValueError("latent must be [B, q_len, 576]")
     pages = _kv_pages(kv, kv_scale, dev)
-    _shape_is(kv, "kv", (kv.shape[0], PAGE, D_QK))
+    if kv.shape[1:] != (PAGE, D_QK):
+        raise ValueError("kv must be [P, 64, 576]")
     if kv_scale is not None:
         _shape_is(kv_scale, "kv_scale", kv.shape[:2])
-    with torch.cuda.device(dev):
-        workspace = _append_table(block_table, seq_lens, workspace, B, dev)
-        tok = _tokens(B, q_len, seq_lens, q_lens, positions, dev)
-        q_out, qs, ys, H = _append_query(q, q_out, B, q_len, D_QK, dev)
-        r = None if rope is None else ctypes.byref(rope._args(dev))
-        st = lib().mla_cache_append(_ptr(latent), ls, ctypes.byref(pages), _ptr(block_table),
-                                    block_table.shape[1], ctypes.byref(tok), r, _ptr(q), qs,
-                                    _ptr(q_out), ys, H, int(shard_id), int(num_shards),
-                                    _ptr(workspace), workspace.numel(), _on(dev, stream))
+    workspace = _append_table(block_table, seq_lens, workspace, B, dev)
+    tok = _tokens(B, q_len, seq_lens, q_lens, positions, dev)
+    q_out, qs, ys, H = _append_query(q, q_out, B, q_len, D_QK, dev)
+    r = None if rope is None else ctypes.byref(rope._args(dev))
+    previous = _enter(dev)
+    try:
+        st = lib().mla_cache_append(latent.data_ptr(), ls, ctypes.byref(pages),
+                                    block_table.data_ptr(), block_table.shape[1],
+                                    ctypes.byref(tok), r, None if q is None else q.data_ptr(), qs,
+                                    None if q is None else q_out.data_ptr(), ys, H, int(shard_id),
+                                    int(num_shards), workspace.data_ptr(), workspace.numel(),
+                                    _on(dev, stream))
+    finally:
+        _leave(previous)
     if st != 0:
         raise MLAError(st, "mla_cache_append")
     return q_out, workspace
@@ -914,16 +965,20 @@ def gqa_cache_append(k, v, k_cache, v_cache, block_table, seq_lens, rope=None, q
     _shape_is(v, "v", k.shape)
     pages = _block_pages(k_cache, v_cache, k_scale, v_scale, dev)
     _shape_is(k, "k", (B, q_len, pages.num_kv_heads, 128))
-    with torch.cuda.device(dev):
-        workspace = _append_table(block_table, seq_lens, workspace, B, dev)
-        tok = _tokens(B, q_len, seq_lens, q_lens, positions, dev)
-        q_out, qs, ys, H = _append_query(q, q_out, B, q_len, 128, dev)
-        r = None if rope is None else ctypes.byref(rope._args(dev))
-        st = lib().gqa_cache_append(_ptr(k), ks, _ptr(v), vs, ctypes.byref(pages),
-                                    _ptr(block_table), block_table.shape[1], ctypes.byref(tok), r,
-                                    _ptr(q), qs, _ptr(q_out), ys, H, int(shard_id),
-                                    int(num_shards), _ptr(workspace), workspace.numel(),
+    workspace = _append_table(block_table, seq_lens, workspace, B, dev)
+    tok = _tokens(B, q_len, seq_lens, q_lens, positions, dev)
+    q_out, qs, ys, H = _append_query(q, q_out, B, q_len, 128, dev)
+    r = None if rope is None else ctypes.byref(rope._args(dev))
+    previous = _enter(dev)
+    try:
+        st = lib().gqa_cache_append(k.data_ptr(), ks, v.data_ptr(), vs, ctypes.byref(pages),
+                                    block_table.data_ptr(), block_table.shape[1],
+                                    ctypes.byref(tok), r, None if q is None else q.data_ptr(), qs,
+                                    None if q is None else q_out.data_ptr(), ys, H, int(shard_id),
+                                    int(num_shards), workspace.data_ptr(), workspace.numel(),
                                     _on(dev, stream))
+    finally:
+        _leave(previous)
     if st != 0:
         raise MLAError(st, "gqa_cache_append")
     return q_out, workspace
