@@ -66,6 +66,8 @@ constexpr int kGroupThreads = 128;
 constexpr uint32_t kBarAll = 1, kBarGroup = 2;   // group g: kBarGroup + g
 constexpr int kMinTilesPerCta = 2;
 constexpr int kUnitCost = 2;
+constexpr int kMaxOwnPlan = 1024;          // units that every CTA plans for itself
+constexpr int kOwnPerThread = (kMaxOwnPlan + kThreads - 1) / kThreads;
 constexpr unsigned long long kTimeoutNs = 2000000000ull;
 constexpr float kTop = 12.0f;              // log2 of the largest weight at a new reference
 constexpr float kMost = 15.0f;             // log2 of the largest weight that fits fp16
@@ -93,6 +95,9 @@ struct Params {
   int* prefix;
   float* ws_o;         // [grid * 2, 64, 128]
   float* ws_lse;       // [grid * 2, 64]
+  unsigned* err;       // [grid] error bits of each CTA; the merge kernel joins them
+  int units;
+  int own_plan;        // 1: every CTA plans, CTA 0 leaves the plan for the merge kernel
   unsigned long long timeout_ns;
   int withhold_query;
 };
@@ -170,6 +175,8 @@ struct Misc {
   uint64_t q_full, drain;
   uint32_t tmem_base;
   int abort;
+  unsigned err;
+  int wsum[kThreads / 32];      // planning: the warps' sums
   int lim[kRows];               // last position a row sees
   int orow[kRows];              // the row's output row
   alignas(16) float qs[kRows];        // 1 / the row's query scale
@@ -180,6 +187,7 @@ struct Misc {
   float f[2][kRows];            // per group: the factor of its accumulator
   int nan_from[kD];             // per dim: the first partly seen token whose V is NaN
   float ksc[kMaxStages][kTok], vsc[kMaxStages][kTok];   // by run of slots with one scale
+  int prefix[kMaxOwnPlan + 1];
 };
 
 // Stages: what fits beside the weights.  A stage lives for its load, the
@@ -206,7 +214,7 @@ struct Smem {
 };
 
 __global__ void __launch_bounds__(1024) gqa_fp8_plan_kernel(Desc d, WsHeader* hdr, int* prefix,
-                                                            int grid) {
+                                                            unsigned* err, int grid) {
   griddep_launch_dependents();
   __shared__ unsigned bad;
   if (threadIdx.x == 0) bad = 0;
@@ -216,7 +224,8 @@ __global__ void __launch_bounds__(1024) gqa_fp8_plan_kernel(Desc d, WsHeader* hd
       if (d.q_lens[b] < 1 || d.q_lens[b] > d.q_len) atomicOr(&bad, kErrQLens);
   __syncthreads();
   plan_units(d.B * d.n_out * d.Hkv * d.Gq, [&](int u) { return make_unit(d, u).tiles; }, hdr,
-             prefix, grid, kMinTilesPerCta, kUnitCost, bad);
+             prefix, grid, kMinTilesPerCta, kUnitCost, 0u);
+  if (threadIdx.x == 0) *err = bad;
 }
 
 __device__ __forceinline__ int ordered(float x) {   // float order as int order
@@ -267,21 +276,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   Misc* misc = reinterpret_cast<Misc*>(smem + S::kMisc);
   const Desc& d = p.d;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  griddep_wait();
-  griddep_launch_dependents();
-
-  const int W = p.hdr->total_cost, per = p.hdr->per_cta;
-  const int lo = blockIdx.x * per;
-  if (lo >= W) return;
-  const int hi = min(lo + per, W);
-
   const uint32_t sQ = smem_u32(smem + S::kQ), sP = smem_u32(smem + S::kP);
   const uint32_t sSt = smem_u32(smem + S::kStage);
   auto bar = [&](const uint64_t* b) { return smem_u32(b); };
   volatile int* abort_flag = &misc->abort;
   const uint64_t tmo = p.timeout_ns;
   auto fail = [&]() {
-    atomicOr(&p.hdr->err, kErrTimeout);
+    atomicOr(&misc->err, kErrTimeout);
     *abort_flag = 1;
   };
   // Waits as a warp; a wait that runs out ends the kernel for every role.
@@ -307,6 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(bar(&misc->q_full), 8);
     mbar_init(bar(&misc->drain), 2);
     misc->abort = 0;
+    misc->err = 0;
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -321,9 +323,75 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = misc->tmem_base;
+  griddep_wait();                // everything before reads and writes nothing global
+  griddep_launch_dependents();
+
+  // The plan: the exclusive prefix of the units' work positions, and every
+  // CTA's share of them.  A few units are planned by every CTA for itself in
+  // shared memory, which costs less than another launch and its results'
+  // way through global memory.
+  const int* prefix = p.prefix;
+  int W, per;
+  if (p.own_plan) {
+    const int upt = ceil_div(p.units, kThreads), u0 = threadIdx.x * upt;
+    int cost[kOwnPerThread], sum = 0;
+#pragma unroll
+    for (int k = 0; k < kOwnPerThread; ++k) {
+      cost[k] = 0;
+      if (k < upt && u0 + k < p.units) {
+        const int t = make_unit(d, u0 + k).tiles;
+        cost[k] = t > 0 ? t + kUnitCost : 0;
+      }
+      sum += cost[k];
+    }
+    int run = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, run, o);
+      if (lane >= o) run += v;
+    }
+    if (lane == 31) misc->wsum[warp] = run;
+    if (blockIdx.x == 0 && d.q_lens != nullptr)
+      for (int b = threadIdx.x; b < d.B; b += kThreads)
+        if (d.q_lens[b] < 1 || d.q_lens[b] > d.q_len) atomicOr(&misc->err, kErrQLens);
+    __syncthreads();
+    int base = run - sum;
+    W = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) base += misc->wsum[w];
+      W += misc->wsum[w];
+    }
+#pragma unroll
+    for (int k = 0; k < kOwnPerThread; ++k) {
+      if (k < upt && u0 + k < p.units) {
+        misc->prefix[u0 + k] = base;
+        if (blockIdx.x == 0) p.prefix[u0 + k] = base;
+      }
+      base += cost[k];
+    }
+    per = max(kMinTilesPerCta, ceil_div(W, (int)gridDim.x));
+    if (threadIdx.x == 0) {
+      misc->prefix[p.units] = W;
+      if (blockIdx.x == 0) {
+        p.prefix[p.units] = W;
+        p.hdr->total_cost = W;
+        p.hdr->per_cta = per;
+        p.hdr->grid = gridDim.x;
+        p.hdr->num_units = p.units;
+        p.hdr->unit_cost = kUnitCost;
+      }
+    }
+    prefix = misc->prefix;
+    __syncthreads();
+  } else {
+    W = p.hdr->total_cost;
+    per = p.hdr->per_cta;
+  }
+  const int lo = blockIdx.x * per, hi = min(lo + per, W);   // no piece if lo >= W
 
   PieceIter it;
-  it.init_warp(p.prefix, p.hdr->num_units, lo, hi, p.hdr->unit_cost, lane);
+  it.init_warp(prefix, p.units, lo, hi, kUnitCost, lane);
   int armed[kStages];
   for (int st = 0; st < kStages; ++st) armed[st] = -1;
   int unit, t0, t1, slot;
@@ -355,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (j + 1 < t1) next = entry(j + 1);
         const bool there = page >= 0 && page < d.num_pages;
         if (!there) {
-          if (box < nb && x.p0 + j * nb + box < x.npages) atomicOr(&p.hdr->err, kErrBadPage);
+          if (box < nb && x.p0 + j * nb + box < x.npages) atomicOr(&misc->err, kErrBadPage);
           page = d.num_pages;                    // out of the map: TMA fills zeros
         }
         if (round >= 1 && !(ok = wait(&misc->kv_empty[st], (round - 1) & 1))) break;
@@ -482,7 +550,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         *reinterpret_cast<uint2*>(dst + R * kD) =
             make_uint2((sp[0] >> 16) | (sp[1] & 0xFFFF0000u), (sp[2] >> 16) | (sp[3] & 0xFFFF0000u));
         if (c == 0) {
-          if ((mx >> 7) == 255u) atomicOr(&p.hdr->err, kErrQRange);
+          if ((mx >> 7) == 255u) atomicOr(&misc->err, kErrQRange);
           misc->qs[r] = __uint_as_float((e - 7u) << 23);
           if (r < x.rows) misc->orow[r] = (int)out_row(d, x, r);
           misc->lim[r] = d.causal && r < x.live ? x.L - x.qn + x.i0 + r / d.G : INT_MAX - 1;
@@ -803,6 +871,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
   }
+  if (threadIdx.x == 0) p.err[blockIdx.x] = misc->err;
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, S::kTmemCols);
@@ -812,13 +881,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Units not written by the partial kernel: no token in the shard (o = 0, lse =
 // -inf) and units split across CTAs (their pieces merged by LSE).  Block u,
 // warp w handles rows w, w + 4, ...; lane: dims 4 lane .. 4 lane + 3.
-__global__ void __launch_bounds__(128) gqa_fp8_merge_kernel(Desc d, const WsHeader* hdr,
-                                                            const int* prefix, const float* ws_o,
-                                                            const float* ws_lse, float* out,
-                                                            float* lse) {
+__global__ void __launch_bounds__(128) gqa_fp8_merge_kernel(Desc d, WsHeader* hdr,
+                                                            const int* prefix, const unsigned* err,
+                                                            int ctas, const float* ws_o,
+                                                            const float* ws_lse,
+                                                            float* out, float* lse) {
   griddep_wait();
   griddep_launch_dependents();
   const int u = blockIdx.x;
+  if (u == 0 && threadIdx.x < 32) {              // the call's error word
+    unsigned e = 0;
+    for (int c = threadIdx.x; c < ctas; c += 32) e |= err[c];
+    e = __reduce_or_sync(0xffffffffu, e);
+    if (threadIdx.x == 0) hdr->err = e;
+  }
   const Unit x = make_unit(d, u);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int ps = prefix[u], ue = prefix[u + 1];
@@ -896,13 +972,14 @@ Split split_for(const gqa_shape* s, int num_shards, int shard_id) {
 }
 
 struct WsLayout {
-  size_t prefix, ws_o, ws_lse, total;
+  size_t err, prefix, ws_o, ws_lse, total;
 };
 
 WsLayout ws_layout(int num_units, int grid) {
   auto up = [](size_t v) { return (v + 255) & ~static_cast<size_t>(255); };
   WsLayout w;
-  w.prefix = up(sizeof(WsHeader));
+  w.err = up(sizeof(WsHeader));
+  w.prefix = w.err + up(sizeof(unsigned) * (size_t)(grid + 1));   // + the plan kernel's
   w.ws_o = w.prefix + up(sizeof(int) * (size_t)(num_units + 1));
   w.ws_lse = w.ws_o + up(sizeof(float) * (size_t)grid * 2 * kRows * kD);
   w.total = w.ws_lse + up(sizeof(float) * (size_t)grid * 2 * kRows);
@@ -1040,12 +1117,17 @@ mla_status gqa_decode_partial_fp8(const void* q, const gqa_block_pages* cache,
   p.prefix = reinterpret_cast<int*>(ws + wl.prefix);
   p.ws_o = reinterpret_cast<float*>(ws + wl.ws_o);
   p.ws_lse = reinterpret_cast<float*>(ws + wl.ws_lse);
+  p.err = reinterpret_cast<unsigned*>(ws + wl.err);
+  p.units = sp.units;
+  p.own_plan = sp.units <= gqa8::kMaxOwnPlan;
   p.timeout_ns = host::wait_budget_ns(gqa8::kTimeoutNs);
   p.withhold_query = host::g_withhold_query.load();
 
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  gqa8::gqa_fp8_plan_kernel<<<1, 1024, 0, st>>>(d, p.hdr, p.prefix, grid);
-  if (cudaGetLastError() != cudaSuccess) return MLA_ERR_CUDA;
+  if (!p.own_plan) {
+    gqa8::gqa_fp8_plan_kernel<<<1, 1024, 0, st>>>(d, p.hdr, p.prefix, p.err + grid, grid);
+    if (cudaGetLastError() != cudaSuccess) return MLA_ERR_CUDA;
+  }
   void* ev0 = host::g_ev_before.load();
   void* ev1 = host::g_ev_after.load();
   if (ev0 != nullptr && cudaEventRecord(static_cast<cudaEvent_t>(ev0), st) != cudaSuccess)
@@ -1063,8 +1145,9 @@ mla_status gqa_decode_partial_fp8(const void* q, const gqa_block_pages* cache,
   cfg.stream = st;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, gqa8::gqa_fp8_merge_kernel, d, (const WsHeader*)p.hdr,
-                            (const int*)p.prefix, (const float*)p.ws_o, (const float*)p.ws_lse,
+  return cudaLaunchKernelEx(&cfg, gqa8::gqa_fp8_merge_kernel, d, p.hdr,
+                            (const int*)p.prefix, (const unsigned*)p.err,
+                            p.own_plan ? grid : grid + 1, (const float*)p.ws_o, (const float*)p.ws_lse,
                             out_partial, lse_partial) == cudaSuccess
              ? MLA_OK
              : MLA_ERR_CUDA;

@@ -253,3 +253,33 @@ def test_graph_replay_and_streams(mla):
     w["lens"] = torch.tensor([20, 64], dtype=torch.int32)
     for s in range(2):
         check_attention(p[s], l[s], ref(w, 2, s=s))
+
+
+def test_more_units_than_a_cta_plans_for_itself(mla):
+    """1300 requests: the plan kernel's path, errors included."""
+    g = torch.Generator().manual_seed(84)
+    lens = torch.randint(0, 150, (1300,), generator=g).tolist()
+    w = make(lens, 4, 1, 32, q_len=2, seed=85)
+    ql = torch.randint(1, 3, (1300,), generator=g).to(torch.int32)
+    part, lse, st = call(mla, w, causal=True, q_lens=ql)
+    assert st == 0
+    check_attention(part[0], lse[0], ref(w, causal=True, q_lens=ql))
+    ql[1299] = 0
+    assert call(mla, w, causal=True, q_lens=ql)[2] == -1
+
+
+def test_wait_budget_runs_out_and_the_next_call_is_clean(mla):
+    """The queries of each CTA's first piece are withheld, so the waits for
+    them run out after 1 ms: reported, and nothing is left behind."""
+    for H in (8, 32, 64):
+        w = make([3000, 300], H, 1, seed=86)
+        try:
+            mla.mla_set_wait_budget_ns(1_000_000)
+            mla.mla_set_withhold_query(True)
+            assert call(mla, w)[2] == -4
+        finally:
+            mla.mla_set_withhold_query(False)
+            mla.mla_set_wait_budget_ns(0)
+        part, lse, st = call(mla, w)
+        assert st == 0
+        check_attention(part[0], lse[0], ref(w))
