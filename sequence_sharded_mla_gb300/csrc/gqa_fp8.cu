@@ -7,8 +7,7 @@
 // with K_t, V_t the codes' values and sk, sv the scales of t's block.
 //
 // Work unit: (request, shard, KV head, group of up to R query rows), R = 16,
-// 32 or 64 rows (position i_local, head j of the KV head's group G: row
-// i_local * G + j).  Persistent CTAs walk a stream-K list of 128-token tiles.
+// 32 or 48 rows (of the KV head's q_len * G, position by position).  Persistent CTAs walk a stream-K list of 128-token tiles.
 // The kernel is bound by the cache's bytes as long as it feeds the tensor
 // cores from what TMA brings in, so nothing of the cache is expanded: both
 // MMAs take K and V as e4m3 codes from shared memory, as their 128-row A
@@ -76,7 +75,7 @@ constexpr float kMinScale = 8.67361737988403547e-19f;   // 2^-60
 
 struct Desc {
   int B, q_len, H, Hkv, G;
-  int ni, Gq;          // query positions per row group, row groups per (request, KV head)
+  int rg, Gq;          // query rows per group, row groups per (request, KV head)
   int num_shards, shard_first, n_out, layout, local, causal;
   int num_pages, max_pages, lg_block;
   int lg_run;          // log2 of the consecutive slots of a tile that share a scale
@@ -103,7 +102,8 @@ struct Params {
 };
 
 struct Unit {
-  int b, so, s, kh, i0;
+  int b, so, s, kh;
+  int r0;              // first row: row r0 + r is position (r0 + r) / G, head (r0 + r) % G
   int L, qn;
   int rows, live;      // rows of the group in the output; rows that attend
   int tiles, tstart, tend, p0, npages;
@@ -120,9 +120,9 @@ __device__ __forceinline__ Unit make_unit(const Desc& d, int u) {
   x.s = d.shard_first + x.so;
   x.L = max(d.seq_lens[x.b], 0);
   x.qn = d.q_lens ? min(max(d.q_lens[x.b], 0), d.q_len) : d.q_len;
-  x.i0 = g * d.ni;
-  x.rows = min(d.ni, d.q_len - x.i0) * d.G;
-  x.live = min(max(x.qn - x.i0, 0) * d.G, x.rows);
+  x.r0 = g * d.rg;
+  x.rows = min(d.rg, d.q_len * d.G - x.r0);
+  x.live = min(max(x.qn * d.G - x.r0, 0), x.rows);
   x.tstart = x.p0 = 0;
   x.tend = x.L;
   const int L = x.live > 0 ? x.L : 0;
@@ -161,11 +161,11 @@ __device__ __forceinline__ bool slot_valid(const Unit& x, int t) {
 __device__ __forceinline__ bool tile_full(const Desc& d, const Unit& x, int j) {
   const int first = slot_token(d, x, j, 0), last = slot_token(d, x, j, kTok - 1);
   return slot_valid(x, first) && slot_valid(x, last) &&
-         (!d.causal || last <= x.L - x.qn + x.i0);
+         (!d.causal || last <= x.L - x.qn + x.r0 / d.G);
 }
 
 __device__ __forceinline__ size_t out_row(const Desc& d, const Unit& x, int r) {
-  const int i = x.i0 + r / d.G, h = x.kh * d.G + r % d.G;
+  const int i = (x.r0 + r) / d.G, h = x.kh * d.G + (x.r0 + r) % d.G;
   return (((size_t)x.so * d.B + x.b) * d.q_len + i) * d.H + h;
 }
 
@@ -183,6 +183,7 @@ struct Misc {
   alignas(16) float m[2][kRows];      // per group: the rows' references
   alignas(16) float alpha[2][kRows];
   int rmax[2][kRows];
+  int moved[2][kRows / 16];     // per group: a reference of these 16 rows moved
   float lpart[2][4][kRows];     // per group and warp: sums of a piece
   float f[2][kRows];            // per group: the factor of its accumulator
   int nan_from[kD];             // per dim: the first partly seen token whose V is NaN
@@ -196,16 +197,16 @@ struct Misc {
 // logits are there when the group comes back from the one before.
 template <int R>
 struct Smem {
-  static constexpr int kStages = R == 64 ? 4 : R == 32 ? 5 : 6;
-  static constexpr int kSBufs = R == 64 ? 2 : 4;
-  // Q's two terms side by side in one MMA of 2R columns, added when S is read,
-  // or (R = 64: TMEM is full) two chains into the same columns
-  static constexpr bool kPair = R < 64;
-  static constexpr int kSCols = kPair ? 2 * R : R;
-  static constexpr uint32_t kColO = kSBufs * kSCols;            // O^T after the S buffers
+  static constexpr int kStages = R == 16 ? 6 : 5;
+  static constexpr int kSBufs = R == 48 ? 2 : 4;
+  static constexpr uint32_t kColO = kSBufs * 2 * R;         // O^T after the S buffers
   static constexpr uint32_t kTmemCols = R == 16 ? 256 : 512;
-  static constexpr int kQ = 0;                              // [2][R][128]
-  static constexpr int kP = 2 * R * kD;                     // [2 groups][3][128 tokens][R]
+  static_assert(kColO + 6 * R <= kTmemCols, "TMEM columns");
+  // Q: 16 rows' first terms, their second terms, the next 16 rows, ...
+  static constexpr int kQ = 0;                              // [R / 16][2][16][128]
+  // P: blocks of 16 weights (rows of one term), unswizzled
+  static constexpr int kP = 2 * R * kD;                     // [2 groups][3][R / 16][128 tokens][16]
+  static constexpr int kPBlock = 16 * kTok;
   static constexpr int kPGroup = 3 * R * kTok;
   static constexpr int kStage = (kP + 2 * kPGroup + 1023) & ~1023;
   static constexpr int kMisc = kStage + kStages * kStageBytes;
@@ -246,6 +247,35 @@ __device__ __forceinline__ float rcp_approx(float x) {   // within 1 ulp
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+__device__ __forceinline__ float2 as_f2(uint32_t a, uint32_t b) {
+  return make_float2(__uint_as_float(a), __uint_as_float(b));
+}
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mov.b64 c, {%6, %7};\n\tfma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
 }
 
 // Weights of two rows as three e5m2 terms: the top bytes of the fp16 value, of
@@ -453,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ K Q^T
-    const uint32_t id = idesc_e4m3_f32(kTok, S::kSCols, false, false);
+    const uint32_t id = idesc_e4m3_f32(kTok, 2 * R, false, false);
     const uint64_t dk = sw128_desc(sSt, 16, 1024), dq = sw128_desc(sQ, 16, 1024);
     int g = 0, pc = 0;
     while (ok && it.next(unit, t0, t1, whole, slot)) {
@@ -466,11 +496,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
           const uint32_t off = (uint32_t)(st * kStageBytes) >> 4;
 #pragma unroll
-          for (int term = 0; term < (S::kPair ? 1 : 2); ++term)
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma_e4m3_ss(tmem + S::kSCols * sb, dk + off + ((32 * k) >> 4),
-                          dq + (uint32_t)((term * R * kD + 32 * k) >> 4), id, term + k != 0);
+          for (int k = 0; k < 4; ++k)
+            mma_e4m3_ss(tmem + 2 * R * sb, dk + off + ((32 * k) >> 4), dq + ((32 * k) >> 4), id,
+                        k != 0);
           mma_commit(bar(&misc->s_full[sb]));
         }
         __syncwarp();
@@ -481,12 +509,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ V^T P^T
     const uint32_t id = idesc_e4m3_e5m2_f32(kD, 3 * R, true, true);
     const uint64_t dv = sw128_desc(sSt + kHalf, 16, 1024);
-    // P: [term][token][R] bytes, MN-major; 8-token groups 8 R bytes apart
-    auto pdesc = [&](uint32_t a) {
-      if (R == 16) return sw0_desc(a, 8 * R, R * kTok);
-      if (R == 32) return sw32_desc(a, R * kTok, 8 * R);
-      return sw64_desc(a, R * kTok, 8 * R);
-    };
     int g = 0;
     while (ok && it.next(unit, t0, t1, whole, slot)) {
       for (int j = t0; j < t1; ++j, ++g) {
@@ -494,12 +516,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!(ok = wait(&misc->p_full[grp], gr & 1))) break;
         tc_fence_after();
         if (lane == 0) {
-          const uint64_t dp = pdesc(sP + grp * S::kPGroup);
+          // MN-major without swizzling: 8-token groups 128 bytes apart
+          const uint64_t dp = sw0_desc(sP + grp * S::kPGroup, 128, S::kPBlock);
           const uint32_t off = (uint32_t)(st * kStageBytes) >> 4;
 #pragma unroll
           for (int k = 0; k < 4; ++k)   // 32 tokens each
             mma_e4m3_ss(tmem + S::kColO + 3 * R * grp, dv + off + ((k * 4 * 1024) >> 4),
-                        dp + (uint32_t)((k * 32 * R) >> 4), id, (j >= t0 + 2 || k != 0) ? 1u : 0u);
+                        dp + ((k * 32 * 16) >> 4), id, (j >= t0 + 2 || k != 0) ? 1u : 0u);
           mma_commit(bar(&misc->kv_empty[st]));
           mma_commit(bar(&misc->pv_done[grp]));
         }
@@ -525,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int r = r0 + (tid >> 4), c = tid & 15;
         uint4 w = make_uint4(0, 0, 0, 0);
         if (r < x.live) {
-          const int i = x.i0 + r / d.G, h = x.kh * d.G + r % d.G;
+          const int i = (x.r0 + r) / d.G, h = x.kh * d.G + (x.r0 + r) % d.G;
           w = __ldg(reinterpret_cast<const uint4*>(
                         d.q + (((size_t)x.b * d.q_len + i) * d.H + h) * kD) + c);
         }
@@ -544,16 +567,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int k = 0; k < 4; ++k)
           sp[k] = split_e4m3x2(__uint_as_float(ww[k] << 16) * sc,
                                __uint_as_float(ww[k] & 0xFFFF0000u) * sc);
-        uint8_t* dst = smem + S::kQ + r * kD + (((c >> 1) ^ (r & 7)) << 4) + (c & 1) * 8;
+        uint8_t* dst = smem + S::kQ + (2 * r0 + (r & 15)) * kD + (((c >> 1) ^ (r & 7)) << 4) +
+                       (c & 1) * 8;
         *reinterpret_cast<uint2*>(dst) =
             make_uint2((sp[0] & 0xFFFFu) | (sp[1] << 16), (sp[2] & 0xFFFFu) | (sp[3] << 16));
-        *reinterpret_cast<uint2*>(dst + R * kD) =
+        *reinterpret_cast<uint2*>(dst + 16 * kD) =
             make_uint2((sp[0] >> 16) | (sp[1] & 0xFFFF0000u), (sp[2] >> 16) | (sp[3] & 0xFFFF0000u));
         if (c == 0) {
           if ((mx >> 7) == 255u) atomicOr(&misc->err, kErrQRange);
           misc->qs[r] = __uint_as_float((e - 7u) << 23);
           if (r < x.rows) misc->orow[r] = (int)out_row(d, x, r);
-          misc->lim[r] = d.causal && r < x.live ? x.L - x.qn + x.i0 + r / d.G : INT_MAX - 1;
+          misc->lim[r] = d.causal && r < x.live ? x.L - x.qn + (x.r0 + r) / d.G : INT_MAX - 1;
         }
       }
       if (tid < 2 * R) misc->m[tid / R][tid % R] = kNoRef;
@@ -563,24 +587,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0 && !(p.withhold_query && pc == 0)) mbar_arrive(bar(&misc->q_full));
       named_bar_sync(kBarAll, 2 * kGroupThreads);
 
-      // 16 rows' values of a shared array; for R = 16 the query scales and the
-      // references stay in registers
-      auto load16 = [](const float* a, float (&v)[16]) {
+      float2 l[R / 2];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float4 t = reinterpret_cast<const float4*>(a)[k];
-          v[4 * k] = t.x;
-          v[4 * k + 1] = t.y;
-          v[4 * k + 2] = t.z;
-          v[4 * k + 3] = t.w;
-        }
-      };
-      float qs16[16], ref16[16];
-      load16(misc->qs, qs16);
-      load16(ref, ref16);
-      float l[R];
-#pragma unroll
-      for (int r = 0; r < R; ++r) l[r] = 0.0f;
+      for (int r = 0; r < R / 2; ++r) l[r] = make_float2(0.0f, 0.0f);
       bool first = true;                           // the group's first tile of the piece
       for (int j = t0; j < t1; ++j, ++g) {
         if ((g & 1) != grp) continue;
@@ -606,37 +615,51 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ok_s = ok_s && wait(&misc->s_full[sb], (g / kSBufs) & 1);
         const bool scaled = __any_sync(0xffffffffu, fv != 1.0f);
-        // 16 rows' log2 weights (without the reference) of this token
-        auto logits = [&](int r0, float (&b)[16]) {
-          uint32_t sr[16];
-          tmem_ld16(tS + S::kSCols * sb + r0, sr);
-          uint32_t sl[16];
-          if (S::kPair) tmem_ld16(tS + S::kSCols * sb + R + r0, sl);
-          if (R > 16) load16(misc->qs + r0, qs16);
-          tmem_wait_ld();
+        // 16 rows' logits of this token in log2 units, with the V scale: into
+        // b (two rows each), less the references if asked for
+        auto logits = [&](int r0, const uint32_t (&sr)[32], float2* b, bool less) {
+          const float4* q4 = reinterpret_cast<const float4*>(misc->qs + r0);
+          const float4* m4 = reinterpret_cast<const float4*>(ref + r0);
+          const float2 c2 = make_float2(c, c), lv2 = make_float2(lv, lv);
 #pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            float v = __uint_as_float(sr[k]);
-            if (S::kPair) v += __uint_as_float(sl[k]);
-            b[k] = fmaf(v * qs16[k], c, lv);
+          for (int k = 0; k < 4; ++k) {
+            const float4 q = q4[k];
+            float4 m = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (less) m = m4[k];
+            const float2 v0 = add2(as_f2(sr[4 * k], sr[4 * k + 1]), as_f2(sr[16 + 4 * k], sr[17 + 4 * k]));
+            const float2 v1 = add2(as_f2(sr[4 * k + 2], sr[4 * k + 3]), as_f2(sr[18 + 4 * k], sr[19 + 4 * k]));
+            const float2 n0 = add2(lv2, make_float2(-m.x, -m.y)), n1 = add2(lv2, make_float2(-m.z, -m.w));
+            b[2 * k] = fma2(mul2(v0, make_float2(q.x, q.y)), c2, n0);
+            b[2 * k + 1] = fma2(mul2(v1, make_float2(q.z, q.w)), c2, n1);
           }
           if (!full) {
 #pragma unroll
-            for (int k = 0; k < 16; ++k)
-              if (!valid || t > misc->lim[r0 + k]) b[k] = -CUDART_INF_F;
+            for (int k = 0; k < 8; ++k) {
+              if (!valid || t > misc->lim[r0 + 2 * k]) b[k].x = -CUDART_INF_F;
+              if (!valid || t > misc->lim[r0 + 2 * k + 1]) b[k].y = -CUDART_INF_F;
+            }
           }
         };
-        float b[16];
+        const uint32_t tSb = tS + 2 * R * sb;
+        float2 b[R / 2];
         bool over = false;
-        if (ok_s) {
-          tc_fence_after();
+        auto all_logits = [&]() {
+          uint32_t sr[2][32];
+          tmem_ld32(tSb, sr[0]);
 #pragma unroll
           for (int r0 = 0; r0 < R; r0 += 16) {
-            logits(r0, b);
-            if (R > 16) load16(ref + r0, ref16);
-#pragma unroll
-            for (int k = 0; k < 16; ++k) over = over || b[k] - ref16[k] > kMost;
+            tmem_wait_ld();
+            if (r0 + 16 < R) tmem_ld32(tSb + 2 * (r0 + 16), sr[((r0 >> 4) + 1) & 1]);
+            logits(r0, sr[(r0 >> 4) & 1], b + r0 / 2, true);
           }
+        };
+        if (ok_s) {
+          tc_fence_after();
+          all_logits();
+          float mx = -CUDART_INF_F;
+#pragma unroll
+          for (int k = 0; k < R / 2; ++k) mx = fmaxf(mx, fmaxf(b[k].x, b[k].y));
+          over = mx > kMost;
         }
         if (named_bar_or(kBarGroup + grp, kGroupThreads, over || !ok_s)) {
           if (named_bar_or(kBarGroup + grp, kGroupThreads, !ok_s)) {
@@ -645,16 +668,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           // ---------------------------------------------- new references
           if (gtid < R) misc->rmax[grp][gtid] = INT_MIN;
+          if (gtid < R / 16) misc->moved[grp][gtid] = 0;
           named_bar_sync(kBarGroup + grp, kGroupThreads);
 #pragma unroll 1
           for (int r0 = 0; r0 < R; r0 += 16) {
-            logits(r0, b);
+            uint32_t sr[32];
+            float2 y[8];
+            tmem_ld32(tSb + 2 * r0, sr);
+            tmem_wait_ld();
+            logits(r0, sr, y, false);
+            int mine = INT_MIN;
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
-              const int mx = __reduce_max_sync(0xffffffffu,
-                                               b[k] == b[k] ? ordered(b[k]) : INT_MIN);
-              if (lane == 0) atomicMax(&misc->rmax[grp][r0 + k], mx);
+              const float v = (k & 1) ? y[k >> 1].y : y[k >> 1].x;
+              const int mx = __reduce_max_sync(0xffffffffu, v == v ? ordered(v) : INT_MIN);
+              if (lane == k) mine = mx;
             }
+            if (lane < 16) atomicMax(&misc->rmax[grp][r0 + lane], mine);
           }
           named_bar_sync(kBarGroup + grp, kGroupThreads);
           if (gtid < R) {
@@ -662,78 +692,80 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float top = o == INT_MIN ? -CUDART_INF_F : from_ordered(o), old = ref[gtid];
             const bool up = top > old + kMost;
             misc->alpha[grp][gtid] = up ? ex2_approx(old - (top - kTop)) : 1.0f;
-            if (up) ref[gtid] = top - kTop;
+            if (up) {
+              ref[gtid] = top - kTop;
+              misc->moved[grp][gtid >> 4] = 1;
+            }
           }
           const bool ok_pv = first || wait(&misc->pv_done[grp], (gr - 1) & 1);
           if (named_bar_or(kBarGroup + grp, kGroupThreads, !ok_pv)) {
             ok = false;
             break;
           }
-          if (R == 16) load16(ref, ref16);
 #pragma unroll
-          for (int r = 0; r < R; ++r) l[r] *= misc->alpha[grp][r];
+          for (int r = 0; r < R / 2; ++r)
+            l[r] = mul2(l[r], make_float2(misc->alpha[grp][2 * r], misc->alpha[grp][2 * r + 1]));
           if (!first) {
             tc_fence_after();
 #pragma unroll 1
-            for (int c0 = 0; c0 < 3 * R; c0 += 16) {
-              uint32_t v[16];
-              tmem_ld16(tO + 3 * R * grp + c0, v);
+            for (int r0 = 0; r0 < R; r0 += 16) {
+              if (!misc->moved[grp][r0 >> 4]) continue;
+              uint32_t v[3][16];
+#pragma unroll
+              for (int term = 0; term < 3; ++term) tmem_ld16(tO + 3 * R * grp + R * term + r0, v[term]);
               tmem_wait_ld();
 #pragma unroll
-              for (int k = 0; k < 16; ++k)
-                v[k] = __float_as_uint(__uint_as_float(v[k]) * misc->alpha[grp][c0 % R + k]);
-              tmem_st16(tO + 3 * R * grp + c0, v);
+              for (int k = 0; k < 16; ++k) {
+                const float al = misc->alpha[grp][r0 + k];
+#pragma unroll
+                for (int term = 0; term < 3; ++term)
+                  v[term][k] = __float_as_uint(__uint_as_float(v[term][k]) * al);
+              }
+#pragma unroll
+              for (int term = 0; term < 3; ++term) tmem_st16(tO + 3 * R * grp + R * term + r0, v[term]);
             }
             tmem_wait_st();
           }
+          all_logits();
         }
         // ------------------------------------------------------- weights
-        if (R == 16) {                             // the logits are in registers
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(&misc->s_empty[sb]));
-        }
+        tc_fence_before();                         // the logits are in registers
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(&misc->s_empty[sb]));
         // the group's last P V has read the weights' buffer
         if (!first && !wait(&misc->pv_done[grp], (gr - 1) & 1)) {
           ok = false;
           continue;                                // the next reduction ends the piece
         }
-        uint8_t* prow = smem + S::kP + grp * S::kPGroup + gtid * R;
+        uint8_t* prow = smem + S::kP + grp * S::kPGroup + gtid * 16;
+        const float2 inv2 = make_float2(inv, inv);
 #pragma unroll
         for (int r0 = 0; r0 < R; r0 += 16) {
-          if (R > 16) {
-            logits(r0, b);
-            load16(ref + r0, ref16);
-          }
           uint32_t w0[4], w1[4], w2[4];
 #pragma unroll
           for (int q4 = 0; q4 < 4; ++q4) {
-            float pw[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int r = r0 + 4 * q4 + k;
-              pw[k] = ex2_approx(b[4 * q4 + k] - ref16[4 * q4 + k]);
-              l[r] = fmaf(pw[k], inv, l[r]);
-              if (scaled) pw[k] = pw[k] > 0.0f || pw[k] != pw[k] ? pw[k] * fv : 0.0f;
+            const int i = (r0 >> 1) + 2 * q4;
+            float2 pa = make_float2(ex2_approx(b[i].x), ex2_approx(b[i].y));
+            float2 pb = make_float2(ex2_approx(b[i + 1].x), ex2_approx(b[i + 1].y));
+            l[i] = fma2(pa, inv2, l[i]);
+            l[i + 1] = fma2(pb, inv2, l[i + 1]);
+            if (scaled) {                          // a weight of 0 stays 0 under any scale
+              pa.x = pa.x != 0.0f ? pa.x * fv : 0.0f;
+              pa.y = pa.y != 0.0f ? pa.y * fv : 0.0f;
+              pb.x = pb.x != 0.0f ? pb.x * fv : 0.0f;
+              pb.y = pb.y != 0.0f ? pb.y * fv : 0.0f;
             }
             uint32_t a0, a1, a2, b0, b1, b2;
-            split_e5m2(pw[0], pw[1], a0, a1, a2);
-            split_e5m2(pw[2], pw[3], b0, b1, b2);
+            split_e5m2(pa.x, pa.y, a0, a1, a2);
+            split_e5m2(pb.x, pb.y, b0, b1, b2);
             w0[q4] = __byte_perm(a0, b0, 0x7531);
             w1[q4] = __byte_perm(a1, b1, 0x7531);
             w2[q4] = a2 | (b2 << 16);
           }
-          // 16-byte unit r0 / 16 of the token's R bytes, swizzled for R > 16
-          const int u = R == 16 ? 0 : R == 32 ? (r0 >> 4) ^ ((gtid >> 2) & 1)
-                                              : (r0 >> 4) ^ ((gtid >> 1) & 3);
-          *reinterpret_cast<uint4*>(prow + 16 * u) = make_uint4(w0[0], w0[1], w0[2], w0[3]);
-          *reinterpret_cast<uint4*>(prow + R * kTok + 16 * u) = make_uint4(w1[0], w1[1], w1[2], w1[3]);
-          *reinterpret_cast<uint4*>(prow + 2 * R * kTok + 16 * u) = make_uint4(w2[0], w2[1], w2[2], w2[3]);
-        }
-        if (R > 16) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(&misc->s_empty[sb]));
+          uint8_t* pb = prow + (r0 >> 4) * S::kPBlock;
+          *reinterpret_cast<uint4*>(pb) = make_uint4(w0[0], w0[1], w0[2], w0[3]);
+          *reinterpret_cast<uint4*>(pb + R * kTok) = make_uint4(w1[0], w1[1], w1[2], w1[3]);
+          *reinterpret_cast<uint4*>(pb + 2 * R * kTok) = make_uint4(w2[0], w2[1], w2[2], w2[3]);
         }
         if (!full) {
           // V rows of slots without a token become zeros; a NaN code of a token
@@ -774,7 +806,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // sums over the group's threads, then over its warps, in a fixed order
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        float v = l[r];
+        float v = (r & 1) ? l[r >> 1].y : l[r >> 1].x;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
         if (lane == 0) misc->lpart[grp][quad][r] = v;
@@ -955,18 +987,19 @@ bool shards_ok(int num_shards, int shard_id) {
          (shard_id == MLA_ALL_SHARDS || (shard_id >= 0 && shard_id < num_shards));
 }
 
-// Query rows per work unit: the smallest tile that holds a KV head's rows of
-// a request, 64 at most; and the row groups that needs, of even size.
+// Query rows per work unit: the smallest tile that holds a KV head's q_len * G
+// rows of a request, 48 at most; more rows go to several groups of even size,
+// in the smallest tile that holds those.
 struct Split {
-  int R, ni, Gq, units;
+  int R, rg, Gq, units;
 };
 
 Split split_for(const gqa_shape* s, int num_shards, int shard_id) {
-  const int G = s->num_heads / s->num_kv_heads;
+  const int n = s->q_len * (s->num_heads / s->num_kv_heads);
   Split x;
-  x.R = (long long)s->q_len * G <= 16 ? 16 : (long long)s->q_len * G <= 32 ? 32 : 64;
-  x.Gq = ceil_div(s->q_len, x.R / G);
-  x.ni = ceil_div(s->q_len, x.Gq);
+  x.Gq = ceil_div(n, 48);
+  x.rg = ceil_div(n, x.Gq);
+  x.R = ceil_div(x.rg, 16) * 16;
   x.units = s->batch * (shard_id == MLA_ALL_SHARDS ? num_shards : 1) * s->num_kv_heads * x.Gq;
   return x;
 }
@@ -1067,7 +1100,7 @@ mla_status gqa_decode_partial_fp8(const void* q, const gqa_block_pages* cache,
   d.H = shape->num_heads;
   d.Hkv = shape->num_kv_heads;
   d.G = d.H / d.Hkv;
-  d.ni = sp.ni;
+  d.rg = sp.rg;
   d.Gq = sp.Gq;
   d.num_shards = num_shards;
   d.shard_first = shard_id == MLA_ALL_SHARDS ? 0 : shard_id;
@@ -1134,7 +1167,7 @@ mla_status gqa_decode_partial_fp8(const void* q, const gqa_block_pages* cache,
     return MLA_ERR_CUDA;
   const cudaError_t e = sp.R == 16   ? gqa8::launch_partial<16>(tm_k, tm_v, p, grid, st)
                         : sp.R == 32 ? gqa8::launch_partial<32>(tm_k, tm_v, p, grid, st)
-                                     : gqa8::launch_partial<64>(tm_k, tm_v, p, grid, st);
+                                     : gqa8::launch_partial<48>(tm_k, tm_v, p, grid, st);
   if (e != cudaSuccess) return MLA_ERR_CUDA;
   if (ev1 != nullptr && cudaEventRecord(static_cast<cudaEvent_t>(ev1), st) != cudaSuccess)
     return MLA_ERR_CUDA;
