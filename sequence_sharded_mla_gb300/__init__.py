@@ -4,11 +4,13 @@ Thin Python binding of the C ABI in ``include/mla_dcp.h``: it checks tensor
 dtypes/devices, allocates outputs and workspace with PyTorch and passes raw
 pointers and the current CUDA stream to ``libmla_dcp.so``.  Every step of
 the computation runs in the library's CUDA kernels; there is no fallback.
-If the library cannot be built or loaded, every call raises.
+If the library cannot be built or loaded, every call raises.  The calls of a
+few microseconds do the same in C++ (csrc/binding.cpp).
 """
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import math
 from typing import Optional
 
@@ -155,18 +157,29 @@ def lib():
     return _LIB
 
 
+_BINDING = None
+
+
+def _binding():
+    """The compiled binding (``_lib/_binding.so``) of the calls whose checks in
+    Python would take longer than their work."""
+    global _BINDING
+    if _BINDING is None:
+        lib()
+        spec = importlib.util.spec_from_file_location("_binding", _build.BINDING)
+        m = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(m)
+        m.set_error(MLAError)
+        _BINDING = m
+    return _BINDING
+
+
 def _shape(batch, q_len, num_heads, causal, softmax_scale, q_lens=None):
     return mla_shape(int(batch), int(q_len), int(num_heads), int(bool(causal)),
                      float(softmax_scale), None if q_lens is None else q_lens.data_ptr())
 
 
-# handle of a device's current stream (torch.cuda.current_stream builds an object)
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-
-
 def _stream_ptr(stream):
-    if stream is None and _raw_stream is not None:
-        return ctypes.c_void_p(_raw_stream(torch.cuda.current_device()))
     s = torch.cuda.current_stream() if stream is None else stream
     return ctypes.c_void_p(s.cuda_stream)
 
@@ -548,90 +561,13 @@ def gqa_decode_partial(q, k_cache, v_cache, block_table, seq_lens, num_shards,
 def gqa_shard_combine(partials, lses, out=None, lse_out=None, stream=None):
     """LSE combine of GQA shard partials fp32 [N, B, q_len, H, D] -> bf16
     [B, q_len, H, D] and fp32 lse [B, q_len, H]."""
-    _check(partials, "partials", (torch.float32,), 5)
-    dev = partials.device
-    N, B, q_len, H, D = partials.shape
-    _check(lses, "lses", (torch.float32,), 4, dev)
-    if out is None:
-        out = torch.empty((B, q_len, H, D), dtype=torch.bfloat16, device=dev)
-    if lse_out is None:
-        lse_out = torch.empty((B, q_len, H), dtype=torch.float32, device=dev)
-    sh = _gqa_shape(B, q_len, H, 1, D, False, 1.0)
-    st = lib().gqa_shard_combine(_ptr(partials), _ptr(lses), int(N), ctypes.byref(sh), _ptr(out),
-                                 _ptr(lse_out), _stream_ptr(stream))
-    if st != 0:
-        raise MLAError(st, "gqa_shard_combine")
-    return out, lse_out
+    return _binding().shard_combine(partials, lses, out, lse_out, stream)
 
 
 def gqa_fp8_workspace_size(batch, q_len, num_heads, num_kv_heads, num_shards,
                            shard_id=ALL_SHARDS, head_dim=128, causal=False) -> int:
     sh = _gqa_shape(batch, q_len, num_heads, num_kv_heads, head_dim, causal, 1.0)
     return int(lib().gqa_fp8_workspace_size(ctypes.byref(sh), int(num_shards), int(shard_id)))
-
-
-def _fp8_types():
-    return (torch.uint8, getattr(torch, "float8_e4m3fn", torch.uint8))
-
-
-def _shape_is(t, name, shape):
-    if t.shape != shape:
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-
-
-def _block_pages(k_cache, v_cache, k_scale, v_scale, dev):
-    """The gqa_block_pages descriptor of an e4m3 (or bf16, without scales) cache."""
-    if k_cache.dtype == torch.bfloat16:
-        types, kv_dtype, block = (torch.bfloat16,), KV_BF16, 0
-        if k_scale is not None or v_scale is not None:
-            raise ValueError("k_scale and v_scale are only for fp8 caches")
-    else:
-        types, kv_dtype, block = _fp8_types(), KV_FP8, 0
-    _check(k_cache, "k_cache", types, 4, dev)
-    _check(v_cache, "v_cache", (k_cache.dtype,), 4, dev)
-    _shape_is(v_cache, "v_cache", k_cache.shape)
-    P, page, Hkv, D = k_cache.shape
-    if D != 128:
-        raise ValueError("k_cache and v_cache must be [P, 64, Hkv, 128]")
-    if kv_dtype == KV_FP8:
-        if k_scale is None or v_scale is None:
-            raise ValueError("fp8 caches need k_scale and v_scale")
-        _check(k_scale, "k_scale", (torch.float32,), 3, dev)
-        _check(v_scale, "v_scale", (torch.float32,), 3, dev)
-        n = k_scale.shape[1]
-        if n < 1 or page % n != 0:
-            raise ValueError("k_scale must be [P, 64 / block, Hkv]")
-        block = page // n
-        _shape_is(k_scale, "k_scale", (P, n, Hkv))
-        _shape_is(v_scale, "v_scale", (P, n, Hkv))
-    return gqa_block_pages(k_cache.data_ptr(), v_cache.data_ptr(),
-                           None if k_scale is None else k_scale.data_ptr(),
-                           None if v_scale is None else v_scale.data_ptr(),
-                           kv_dtype, block, P, page, Hkv)
-
-
-def _on(dev, stream):
-    """The stream handle of a call on `dev`: the given stream's, else that of
-    dev's current one."""
-    if stream is not None:
-        return stream.cuda_stream
-    if _raw_stream is not None:
-        return _raw_stream(dev.index)
-    return torch.cuda.current_stream(dev).cuda_stream
-
-
-def _enter(dev):
-    """Makes `dev` the current device; the index to go back to, or -1."""
-    current = torch.cuda.current_device()
-    if current == dev.index:
-        return -1
-    torch.cuda.set_device(dev)
-    return current
-
-
-def _leave(previous):
-    if previous >= 0:
-        torch.cuda.set_device(previous)
 
 
 def gqa_decode_partial_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens,
@@ -648,54 +584,9 @@ def gqa_decode_partial_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, s
     out_partial: fp32 [n_out, B, q_len, H, 128]; lse_partial: fp32 [n_out, B,
     q_len, H].  softmax_scale defaults to 1/sqrt(128).
     """
-    _check(q, "q", (torch.bfloat16,), 4)
-    dev = q.device
-    B, q_len, H, D = q.shape
-    if k_cache.dtype == torch.bfloat16:
-        raise TypeError("k_cache must hold e4m3 codes; gqa_decode_partial takes bf16 caches")
-    pages = _block_pages(k_cache, v_cache, k_scale, v_scale, dev)
-    _check(block_table, "block_table", (torch.int32,), 2, dev)
-    _check(seq_lens, "seq_lens", (torch.int32,), 1, dev)
-    if block_table.shape[0] != B or seq_lens.shape[0] != B:
-        raise ValueError("q, block_table and seq_lens disagree on the number of requests")
-    if q_lens is not None:
-        _check(q_lens, "q_lens", (torch.int32,), 1, dev)
-        _shape_is(q_lens, "q_lens", (B,))
-    scale = 1.0 / math.sqrt(D) if softmax_scale is None else softmax_scale
-    n_out = num_shards if shard_id == ALL_SHARDS else 1
-    sh = _gqa_shape(B, q_len, H, pages.num_kv_heads, D, causal, scale)
-    rows = (max(n_out, 1), B, q_len, H)
-    if out_partial is None:
-        out_partial = torch.empty(rows + (D,), dtype=torch.float32, device=dev)
-    else:
-        _check(out_partial, "out_partial", (torch.float32,), 5, dev)
-        _shape_is(out_partial, "out_partial", rows + (D,))
-    if lse_partial is None:
-        lse_partial = torch.empty(rows, dtype=torch.float32, device=dev)
-    else:
-        _check(lse_partial, "lse_partial", (torch.float32,), 4, dev)
-        _shape_is(lse_partial, "lse_partial", rows)
-    previous = _enter(dev)
-    try:
-        if workspace is None:
-            need = int(lib().gqa_fp8_workspace_size(ctypes.byref(sh), int(num_shards),
-                                                    int(shard_id)))
-            workspace = torch.empty((max(need, 256),), dtype=torch.uint8, device=dev)
-        else:
-            _check(workspace, "workspace", (torch.uint8,), 1, dev)
-        st = lib().gqa_decode_partial_fp8(q.data_ptr(), ctypes.byref(pages),
-                                          block_table.data_ptr(), block_table.shape[1],
-                                          seq_lens.data_ptr(),
-                                          None if q_lens is None else q_lens.data_ptr(),
-                                          ctypes.byref(sh), int(shard_id), int(num_shards),
-                                          LAYOUTS[layout], out_partial.data_ptr(),
-                                          lse_partial.data_ptr(), workspace.data_ptr(),
-                                          workspace.numel(), _on(dev, stream))
-    finally:
-        _leave(previous)
-    if st != 0:
-        raise MLAError(st, "gqa_decode_partial_fp8")
-    return out_partial, lse_partial, workspace
+    return _binding().attend_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens,
+                                 num_shards, LAYOUTS[layout], shard_id, causal, softmax_scale,
+                                 out_partial, lse_partial, workspace, stream, q_lens)
 
 
 # ------------------------------------------------- rotary positions and append
@@ -704,15 +595,12 @@ class Rope:
     token, e.g. from mla_rope_frequencies), the first rotated dim of a head,
     the pair layout and the factor on the rotated values."""
 
+    __slots__ = ("inv_freq", "first_dim", "interleaved", "attention_factor")
+
     def __init__(self, inv_freq, first_dim=0, interleaved=False, attention_factor=1.0):
-        _check(inv_freq, "inv_freq", (torch.float64,), 1)
+        _binding().check_frequencies(inv_freq)
         self.inv_freq, self.first_dim = inv_freq, int(first_dim)
         self.interleaved, self.attention_factor = bool(interleaved), float(attention_factor)
-
-    def _args(self, dev):
-        _check(self.inv_freq, "rope.inv_freq", (torch.float64,), 1, dev)
-        return mla_rope(self.inv_freq.data_ptr(), 2 * self.inv_freq.numel(), self.first_dim,
-                        int(self.interleaved), self.attention_factor)
 
 
 def mla_rope_frequencies(rot_dim, theta=10000.0, scaling=None, device="cuda"):
@@ -777,78 +665,6 @@ def mla_rope_frequencies(rot_dim, theta=10000.0, scaling=None, device="cuda"):
     return inv.to(device), attention_factor
 
 
-def _token_stride(t, name, dims):
-    """Elements between the tokens of t [B, q_len, ...] whose last `dims`
-    dimensions are contiguous (a view of a wider projection output will do)."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{name}: dtype {t.dtype} is not bfloat16")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be on a CUDA device")
-    if t.dim() != 2 + dims:
-        raise ValueError(f"{name} must have {2 + dims} dims, got {t.dim()}")
-    shape = t.shape
-    if t.is_contiguous():
-        return shape[2] if dims == 1 else shape[2] * shape[3]
-    width = 1
-    for d in range(t.dim() - 1, 1, -1):
-        if shape[d] != 1 and t.stride(d) != width:
-            raise ValueError(f"{name}: a token's values must be contiguous")
-        width *= shape[d]
-    B, q_len = shape[:2]
-    if q_len > 1:
-        step = t.stride(1)
-        if B > 1 and t.stride(0) != q_len * step:
-            raise ValueError(f"{name}: tokens must be evenly spaced")
-    else:
-        step = t.stride(0) if B > 1 else width
-    if t.numel() and step < width:
-        raise ValueError(f"{name}: tokens overlap")
-    return step
-
-
-def _tokens(B, q_len, seq_lens, q_lens, positions, dev):
-    if seq_lens is not None:
-        _check(seq_lens, "seq_lens", (torch.int32,), 1, dev)
-        _shape_is(seq_lens, "seq_lens", (B,))
-    if q_lens is not None:
-        _check(q_lens, "q_lens", (torch.int32,), 1, dev)
-        _shape_is(q_lens, "q_lens", (B,))
-    if positions is not None:
-        _check(positions, "positions", (torch.int32,), 2, dev)
-        _shape_is(positions, "positions", (B, q_len))
-    return mla_tokens(B, q_len, None if seq_lens is None else seq_lens.data_ptr(),
-                      None if q_lens is None else q_lens.data_ptr(),
-                      None if positions is None else positions.data_ptr())
-
-
-def _out_rows(x, out, name, dims):
-    """The output of a rotation of x: `out` checked (x itself, or memory of its
-    own), or a new tensor; and the two token strides."""
-    xs = _token_stride(x, name, dims)
-    if out is x:
-        return x, xs, xs
-    if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        return out, xs, _token_stride(out, name, dims)
-    ys = _token_stride(out, name + "_out", dims)
-    if out.shape != x.shape:
-        _shape_is(out, name + "_out", x.shape)
-    if out.device != x.device:
-        raise ValueError(f"{name}_out is on {out.device}, expected {x.device}")
-    a, b = x.data_ptr(), out.data_ptr()
-    if a == b:
-        if xs != ys:
-            raise ValueError(f"{name}_out overlaps {name} with other strides")
-    else:
-        # the bytes from the first token to the end of the last
-        tokens, width = x.shape[0] * x.shape[1] - 1, x.numel() // max(x.shape[0] * x.shape[1], 1)
-        if a < b + 2 * (tokens * ys + width) and b < a + 2 * (tokens * xs + width):
-            raise ValueError(f"{name}_out overlaps {name}")
-    return out, xs, ys
-
-
 def mla_rope_apply(x, rope, seq_lens=None, q_lens=None, positions=None, out=None, stream=None):
     """Rotates heads by their tokens' positions; returns out.
 
@@ -859,46 +675,7 @@ def mla_rope_apply(x, rope, seq_lens=None, q_lens=None, positions=None, out=None
     rotated dims move), memory of its own, or None for a new tensor.  Rows
     i >= n_b are left as they were.
     """
-    out, xs, ys = _out_rows(x, out, "x", 2)
-    dev = x.device
-    B, q_len, H, D = x.shape
-    if seq_lens is None and positions is None:
-        raise ValueError("give seq_lens or positions")
-    tok = _tokens(B, q_len, seq_lens, q_lens, positions, dev)
-    r = rope._args(dev)
-    previous = _enter(dev)
-    try:
-        st = lib().mla_rope_apply(x.data_ptr(), xs, out.data_ptr(), ys, ctypes.byref(tok), H, D,
-                                  ctypes.byref(r), _on(dev, stream))
-    finally:
-        _leave(previous)
-    if st != 0:
-        raise MLAError(st, "mla_rope_apply")
-    return out
-
-
-def _append_query(q, q_out, B, q_len, width, dev):
-    if q is None:
-        if q_out is not None:
-            raise ValueError("q_out without q")
-        return None, 0, 0, 0
-    q_out, qs, ys = _out_rows(q, q_out, "q", 2)
-    if q.device != dev:
-        raise ValueError(f"q is on {q.device}, expected {dev}")
-    _shape_is(q, "q", (B, q_len, q.shape[2], width))
-    return q_out, qs, ys, q.shape[2]
-
-
-def _append_table(block_table, seq_lens, workspace, B, dev):
-    _check(block_table, "block_table", (torch.int32,), 2, dev)
-    if seq_lens is None:
-        raise TypeError("seq_lens must be a torch.Tensor")
-    if block_table.shape[0] != B:
-        raise ValueError("block_table and the new tokens disagree on the number of requests")
-    if workspace is None:
-        return torch.zeros((256,), dtype=torch.uint8, device=dev)
-    _check(workspace, "workspace", (torch.uint8,), 1, dev)
-    return workspace
+    return _binding().rope_apply(x, rope, seq_lens, q_lens, positions, out, stream)
 
 
 def mla_cache_append(latent, kv, block_table, seq_lens, rope=None, q=None, q_out=None,
@@ -916,33 +693,8 @@ def mla_cache_append(latent, kv, block_table, seq_lens, rope=None, q=None, q_out
     workspace: 256 bytes, zeroed before its first use; mla_get_device_error
     reads its errors.
     """
-    ls = _token_stride(latent, "latent", 1)
-    dev = latent.device
-    B, q_len, d = latent.shape
-    if d != D_QK:
-        raise ValueError("latent must be [B, q_len, 576]")
-    pages = _kv_pages(kv, kv_scale, dev)
-    if kv.shape[1:] != (PAGE, D_QK):
-        raise ValueError("kv must be [P, 64, 576]")
-    if kv_scale is not None:
-        _shape_is(kv_scale, "kv_scale", kv.shape[:2])
-    workspace = _append_table(block_table, seq_lens, workspace, B, dev)
-    tok = _tokens(B, q_len, seq_lens, q_lens, positions, dev)
-    q_out, qs, ys, H = _append_query(q, q_out, B, q_len, D_QK, dev)
-    r = None if rope is None else ctypes.byref(rope._args(dev))
-    previous = _enter(dev)
-    try:
-        st = lib().mla_cache_append(latent.data_ptr(), ls, ctypes.byref(pages),
-                                    block_table.data_ptr(), block_table.shape[1],
-                                    ctypes.byref(tok), r, None if q is None else q.data_ptr(), qs,
-                                    None if q is None else q_out.data_ptr(), ys, H, int(shard_id),
-                                    int(num_shards), workspace.data_ptr(), workspace.numel(),
-                                    _on(dev, stream))
-    finally:
-        _leave(previous)
-    if st != 0:
-        raise MLAError(st, "mla_cache_append")
-    return q_out, workspace
+    return _binding().latent_append(latent, kv, kv_scale, block_table, seq_lens, rope, q, q_out,
+                                    q_lens, positions, shard_id, num_shards, workspace, stream)
 
 
 def gqa_cache_append(k, v, k_cache, v_cache, block_table, seq_lens, rope=None, q=None, q_out=None,
@@ -956,29 +708,6 @@ def gqa_cache_append(k, v, k_cache, v_cache, block_table, seq_lens, rope=None, q
     [P, 64 / block, Hkv] (written) for codes.  q: bf16 [B, q_len, H, 128] or
     None.  The rest as for mla_cache_append.
     """
-    ks = _token_stride(k, "k", 2)
-    vs = _token_stride(v, "v", 2)
-    dev = k.device
-    B, q_len, Hkv, _ = k.shape
-    if v.device != dev:
-        raise ValueError(f"v is on {v.device}, expected {dev}")
-    _shape_is(v, "v", k.shape)
-    pages = _block_pages(k_cache, v_cache, k_scale, v_scale, dev)
-    _shape_is(k, "k", (B, q_len, pages.num_kv_heads, 128))
-    workspace = _append_table(block_table, seq_lens, workspace, B, dev)
-    tok = _tokens(B, q_len, seq_lens, q_lens, positions, dev)
-    q_out, qs, ys, H = _append_query(q, q_out, B, q_len, 128, dev)
-    r = None if rope is None else ctypes.byref(rope._args(dev))
-    previous = _enter(dev)
-    try:
-        st = lib().gqa_cache_append(k.data_ptr(), ks, v.data_ptr(), vs, ctypes.byref(pages),
-                                    block_table.data_ptr(), block_table.shape[1],
-                                    ctypes.byref(tok), r, None if q is None else q.data_ptr(), qs,
-                                    None if q is None else q_out.data_ptr(), ys, H, int(shard_id),
-                                    int(num_shards), workspace.data_ptr(), workspace.numel(),
-                                    _on(dev, stream))
-    finally:
-        _leave(previous)
-    if st != 0:
-        raise MLAError(st, "gqa_cache_append")
-    return q_out, workspace
+    return _binding().heads_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens,
+                                   rope, q, q_out, q_lens, positions, shard_id, num_shards,
+                                   workspace, stream)
