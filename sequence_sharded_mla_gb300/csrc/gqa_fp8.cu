@@ -94,34 +94,43 @@ struct Params {
   int* prefix;
   float* ws_o;         // [grid * 2, 64, 128]
   float* ws_lse;       // [grid * 2, 64]
-  unsigned* err;       // [grid] error bits of each CTA; the merge kernel joins them
+  int4* rec;           // [grid] what each CTA leaves for the merge kernel (make_record)
   int units;
-  int own_plan;        // 1: every CTA plans, CTA 0 leaves the plan for the merge kernel
+  int own_plan;        // 1: every CTA plans for itself
   unsigned long long timeout_ns;
   int withhold_query;
 };
 
-struct Unit {
-  int b, so, s, kh;
+struct Rows {
+  int b, so, kh;
   int r0;              // first row: row r0 + r is position (r0 + r) / G, head (r0 + r) % G
-  int L, qn;
-  int rows, live;      // rows of the group in the output; rows that attend
+  int rows;            // rows of the group in the output
+};
+
+struct Unit : Rows {
+  int s, L, qn;
+  int live;            // rows that attend
   int tiles, tstart, tend, p0, npages;
 };
 
-__device__ __forceinline__ Unit make_unit(const Desc& d, int u) {
-  Unit x;
-  const int g = u % d.Gq;
+__device__ __forceinline__ Rows make_rows(const Desc& d, int u) {
+  Rows x;
+  x.r0 = u % d.Gq * d.rg;
   int t = u / d.Gq;
   x.kh = t % d.Hkv;
   t /= d.Hkv;
   x.so = t % d.n_out;
   x.b = t / d.n_out;
+  x.rows = min(d.rg, d.q_len * d.G - x.r0);
+  return x;
+}
+
+__device__ __forceinline__ Unit make_unit(const Desc& d, int u) {
+  Unit x;
+  static_cast<Rows&>(x) = make_rows(d, u);
   x.s = d.shard_first + x.so;
   x.L = max(d.seq_lens[x.b], 0);
   x.qn = d.q_lens ? min(max(d.q_lens[x.b], 0), d.q_len) : d.q_len;
-  x.r0 = g * d.rg;
-  x.rows = min(d.rg, d.q_len * d.G - x.r0);
   x.live = min(max(x.qn * d.G - x.r0, 0), x.rows);
   x.tstart = x.p0 = 0;
   x.tend = x.L;
@@ -164,7 +173,7 @@ __device__ __forceinline__ bool tile_full(const Desc& d, const Unit& x, int j) {
          (!d.causal || last <= x.L - x.qn + x.r0 / d.G);
 }
 
-__device__ __forceinline__ size_t out_row(const Desc& d, const Unit& x, int r) {
+__device__ __forceinline__ size_t out_row(const Desc& d, const Rows& x, int r) {
   const int i = (x.r0 + r) / d.G, h = x.kh * d.G + (x.r0 + r) % d.G;
   return (((size_t)x.so * d.B + x.b) * d.q_len + i) * d.H + h;
 }
@@ -188,8 +197,24 @@ struct Misc {
   float f[2][kRows];            // per group: the factor of its accumulator
   int nan_from[kD];             // per dim: the first partly seen token whose V is NaN
   float ksc[kMaxStages][kTok], vsc[kMaxStages][kTok];   // by run of slots with one scale
+  int4 rec;
   int prefix[kMaxOwnPlan + 1];
 };
+
+// A CTA whose first tile is not its unit's first: (unit, 2 c0 + slot of c0's
+// piece, pieces, error bits), c0 being the CTA of the unit's first piece; CTA
+// c0 + k holds piece k, in slot 0.  Other CTAs: unit -1.
+__device__ __forceinline__ int4 make_record(const int* prefix, int u, int lo, int hi, int per) {
+  int4 r = make_int4(-1, 0, 0, 0);
+  if (lo >= hi) return r;
+  const int us = unit_tile_start(prefix, u, kUnitCost), ue = prefix[u + 1];
+  if (lo <= us || lo >= ue) return r;
+  const int c0 = us / per;
+  r.x = u;
+  r.y = 2 * c0 + (c0 * per < prefix[u] ? 1 : 0);
+  r.z = (ue - 1) / per - c0 + 1;
+  return r;
+}
 
 // Stages: what fits beside the weights.  A stage lives for its load, the
 // logits, the softmax and the P V of its tile, so more of them hide more of
@@ -215,7 +240,7 @@ struct Smem {
 };
 
 __global__ void __launch_bounds__(1024) gqa_fp8_plan_kernel(Desc d, WsHeader* hdr, int* prefix,
-                                                            unsigned* err, int grid) {
+                                                            int4* rec, int grid) {
   griddep_launch_dependents();
   __shared__ unsigned bad;
   if (threadIdx.x == 0) bad = 0;
@@ -226,7 +251,7 @@ __global__ void __launch_bounds__(1024) gqa_fp8_plan_kernel(Desc d, WsHeader* hd
   __syncthreads();
   plan_units(d.B * d.n_out * d.Hkv * d.Gq, [&](int u) { return make_unit(d, u).tiles; }, hdr,
              prefix, grid, kMinTilesPerCta, kUnitCost, 0u);
-  if (threadIdx.x == 0) *err = bad;
+  if (threadIdx.x == 0) *rec = make_int4(-1, 0, 0, (int)bad);
 }
 
 __device__ __forceinline__ int ordered(float x) {   // float order as int order
@@ -396,22 +421,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int k = 0; k < kOwnPerThread; ++k) {
       if (k < upt && u0 + k < p.units) {
         misc->prefix[u0 + k] = base;
-        if (blockIdx.x == 0) p.prefix[u0 + k] = base;
       }
       base += cost[k];
     }
     per = max(kMinTilesPerCta, ceil_div(W, (int)gridDim.x));
-    if (threadIdx.x == 0) {
-      misc->prefix[p.units] = W;
-      if (blockIdx.x == 0) {
-        p.prefix[p.units] = W;
-        p.hdr->total_cost = W;
-        p.hdr->per_cta = per;
-        p.hdr->grid = gridDim.x;
-        p.hdr->num_units = p.units;
-        p.hdr->unit_cost = kUnitCost;
-      }
-    }
+    if (threadIdx.x == 0) misc->prefix[p.units] = W;
     prefix = misc->prefix;
     __syncthreads();
   } else {
@@ -529,7 +543,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
       }
     }
-  } else if (warp >= 4) {
+  } else if (warp == 3) {
+    // ------------------------------------------------ record, empty units
+    if (lane == 0) misc->rec = make_record(prefix, it.u, lo, hi, per);
+    for (int u = blockIdx.x; u < p.units; u += gridDim.x) {
+      if (prefix[u + 1] > prefix[u]) continue;
+      const Unit x = make_unit(d, u);            // no token in the shard: o = 0, lse = -inf
+      for (int r = 0; r < x.rows; ++r) {
+        const size_t row = out_row(d, x, r);
+        reinterpret_cast<float4*>(p.out + row * kD)[lane] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (lane == 0) p.lse[row] = -CUDART_INF_F;
+      }
+    }
+  } else {
     // ------------------------------------------------------------ softmax
     const int grp = (warp - 4) >> 2, quad = warp & 3;
     const int gtid = (threadIdx.x - 128) & 127;    // 0..127 in the group: its token of a tile
@@ -903,68 +929,110 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
   }
-  if (threadIdx.x == 0) p.err[blockIdx.x] = misc->err;
+  if (threadIdx.x == 0)
+    p.rec[blockIdx.x] = make_int4(misc->rec.x, misc->rec.y, misc->rec.z, (int)misc->err);
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, S::kTmemCols);
   }
 }
 
-// Units not written by the partial kernel: no token in the shard (o = 0, lse =
-// -inf) and units split across CTAs (their pieces merged by LSE).  Block u,
-// warp w handles rows w, w + 4, ...; lane: dims 4 lane .. 4 lane + 3.
-__global__ void __launch_bounds__(128) gqa_fp8_merge_kernel(Desc d, WsHeader* hdr,
-                                                            const int* prefix, const unsigned* err,
-                                                            int ctas, const float* ws_o,
-                                                            const float* ws_lse,
-                                                            float* out, float* lse) {
+// Joins the pieces of units that CTAs share, by LSE.  A unit of np pieces has
+// np - 1 CTAs that begin inside it; block c stands for CTA c, and those of a
+// unit take its rows in turn, so that one long request over all CTAs is joined
+// by as many blocks as it has rows.  A block's warps split its rows and, where
+// there are fewer rows than warps, a row's pieces; sums go in a fixed order.
+// (One block per unit took 180 of 361 us for one request of 4M tokens over
+// one KV head, 152 pieces.)  Block 0 joins the error bits.
+constexpr int kMergeWarps = 16;
+
+__global__ void __launch_bounds__(32 * kMergeWarps)
+    gqa_fp8_merge_kernel(Desc d, WsHeader* hdr, const int4* rec, int records, const float* ws_o,
+                         const float* ws_lse, float* out, float* lse) {
+  __shared__ float4 part[kMergeWarps][32];
+  __shared__ float psum[kMergeWarps];
+  const int c = blockIdx.x;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   griddep_wait();
   griddep_launch_dependents();
-  const int u = blockIdx.x;
-  if (u == 0 && threadIdx.x < 32) {              // the call's error word
+  if (c == 0) {
+    if (warp != 0) return;
     unsigned e = 0;
-    for (int c = threadIdx.x; c < ctas; c += 32) e |= err[c];
+    for (int k = lane; k < records; k += 32) e |= (unsigned)rec[k].w;
     e = __reduce_or_sync(0xffffffffu, e);
-    if (threadIdx.x == 0) hdr->err = e;
+    if (lane == 0) hdr->err = e;
+    return;
   }
-  const Unit x = make_unit(d, u);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int ps = prefix[u], ue = prefix[u + 1];
-  const int us = unit_tile_start(prefix, u, hdr->unit_cost);
-  const int per = hdr->per_cta;
-  const bool empty = us == ue;
-  const int c0 = empty ? 0 : us / per, c1 = empty ? 0 : (ue - 1) / per;
-  if (!empty && c0 == c1) return;   // written by the partial kernel
-  auto slot_of = [&](int c) -> size_t {
-    return (c == c0 && c0 * per < ps) ? 2 * (size_t)c + 1 : 2 * (size_t)c;
-  };
-  const int np = c1 - c0 + 1;
-  for (int r = warp; r < x.rows; r += 4) {
-    const size_t row = out_row(d, x, r);
+  const int4 rc = rec[c];
+  if (rc.x < 0) return;
+  const int c0 = rc.y >> 1, np = rc.z, turn = c - c0 - 1;
+  const Rows x = make_rows(d, rc.x);
+  const int mine = turn < x.rows ? (x.rows - 1 - turn) / (np - 1) + 1 : 0;
+  int wpr = 1;                                   // warps per row
+  while (2 * wpr * mine <= kMergeWarps && 2 * wpr <= np) wpr *= 2;
+  const int sub = warp % wpr;
+  for (int i0 = 0; i0 < mine; i0 += kMergeWarps / wpr) {
+    const int i = i0 + warp / wpr;
+    const int r = turn + min(i, mine - 1) * (np - 1);
+    auto slot_row = [&](int k) -> size_t {       // row r of piece k
+      return (size_t)(k == 0 ? rc.y : 2 * (c0 + k)) * kRows + r;
+    };
+    constexpr int kBatch = 4;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     float M = -CUDART_INF_F, wsum = 0.f;
-    if (!empty) {
-      for (int k = lane; k < np; k += 32) M = fmaxf(M, ws_lse[slot_of(c0 + k) * kRows + r]);
+    for (int k0 = sub; k0 < np; k0 += kBatch * wpr) {
+      float e[kBatch];
+      float4 o[kBatch];
 #pragma unroll
-      for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-      for (int k = 0; k < np; ++k) {
-        const size_t s = slot_of(c0 + k);
-        const float e = ws_lse[s * kRows + r];
-        if (e == -CUDART_INF_F) continue;   // a NaN goes on
-        const float w = __expf(e - M);
+      for (int k = 0; k < kBatch; ++k) {
+        const int at = k0 + k * wpr;
+        e[k] = -CUDART_INF_F;
+        if (at < np) {
+          const size_t s = slot_row(at);
+          e[k] = ws_lse[s];
+          o[k] = reinterpret_cast<const float4*>(ws_o + s * kD)[lane];
+        }
+      }
+      if (k0 == sub) {
+        for (int k = lane; k < np; k += 32) M = fmaxf(M, ws_lse[slot_row(k)]);
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1)
+          M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+      }
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        if (e[k] == -CUDART_INF_F) continue;     // a NaN goes on
+        const float w = __expf(e[k] - M);
         wsum += w;
-        const float4 o = reinterpret_cast<const float4*>(ws_o + (s * kRows + r) * kD)[lane];
-        acc.x += w * o.x;
-        acc.y += w * o.y;
-        acc.z += w * o.z;
-        acc.w += w * o.w;
+        acc.x = fmaf(w, o[k].x, acc.x);
+        acc.y = fmaf(w, o[k].y, acc.y);
+        acc.z = fmaf(w, o[k].z, acc.z);
+        acc.w = fmaf(w, o[k].w, acc.w);
       }
     }
-    const bool none = wsum == 0.f;
-    const float inv = none ? 0.f : 1.0f / wsum;
-    reinterpret_cast<float4*>(out + row * kD)[lane] =
-        make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-    if (lane == 0) lse[row] = none ? -CUDART_INF_F : M + logf(wsum);
+    if (wpr > 1) {
+      part[warp][lane] = acc;
+      if (lane == 0) psum[warp] = wsum;
+      __syncthreads();
+      if (sub == 0) {
+        for (int k = 1; k < wpr; ++k) {
+          const float4 a = part[warp + k][lane];
+          acc.x += a.x;
+          acc.y += a.y;
+          acc.z += a.z;
+          acc.w += a.w;
+          wsum += psum[warp + k];
+        }
+      }
+    }
+    if (sub == 0 && i < mine) {
+      const size_t row = out_row(d, x, r);
+      const bool none = wsum == 0.f;
+      const float inv = none ? 0.f : 1.0f / wsum;
+      reinterpret_cast<float4*>(out + row * kD)[lane] =
+          make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+      if (lane == 0) lse[row] = none ? -CUDART_INF_F : M + logf(wsum);
+    }
   }
 }
 
@@ -1005,14 +1073,14 @@ Split split_for(const gqa_shape* s, int num_shards, int shard_id) {
 }
 
 struct WsLayout {
-  size_t err, prefix, ws_o, ws_lse, total;
+  size_t rec, prefix, ws_o, ws_lse, total;
 };
 
 WsLayout ws_layout(int num_units, int grid) {
   auto up = [](size_t v) { return (v + 255) & ~static_cast<size_t>(255); };
   WsLayout w;
-  w.err = up(sizeof(WsHeader));
-  w.prefix = w.err + up(sizeof(unsigned) * (size_t)(grid + 1));   // + the plan kernel's
+  w.rec = up(sizeof(WsHeader));
+  w.prefix = w.rec + up(sizeof(int4) * (size_t)(grid + 1));       // + the plan kernel's
   w.ws_o = w.prefix + up(sizeof(int) * (size_t)(num_units + 1));
   w.ws_lse = w.ws_o + up(sizeof(float) * (size_t)grid * 2 * kRows * kD);
   w.total = w.ws_lse + up(sizeof(float) * (size_t)grid * 2 * kRows);
@@ -1150,7 +1218,7 @@ mla_status gqa_decode_partial_fp8(const void* q, const gqa_block_pages* cache,
   p.prefix = reinterpret_cast<int*>(ws + wl.prefix);
   p.ws_o = reinterpret_cast<float*>(ws + wl.ws_o);
   p.ws_lse = reinterpret_cast<float*>(ws + wl.ws_lse);
-  p.err = reinterpret_cast<unsigned*>(ws + wl.err);
+  p.rec = reinterpret_cast<int4*>(ws + wl.rec);
   p.units = sp.units;
   p.own_plan = sp.units <= gqa8::kMaxOwnPlan;
   p.timeout_ns = host::wait_budget_ns(gqa8::kTimeoutNs);
@@ -1158,7 +1226,7 @@ mla_status gqa_decode_partial_fp8(const void* q, const gqa_block_pages* cache,
 
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (!p.own_plan) {
-    gqa8::gqa_fp8_plan_kernel<<<1, 1024, 0, st>>>(d, p.hdr, p.prefix, p.err + grid, grid);
+    gqa8::gqa_fp8_plan_kernel<<<1, 1024, 0, st>>>(d, p.hdr, p.prefix, p.rec + grid, grid);
     if (cudaGetLastError() != cudaSuccess) return MLA_ERR_CUDA;
   }
   void* ev0 = host::g_ev_before.load();
@@ -1173,15 +1241,14 @@ mla_status gqa_decode_partial_fp8(const void* q, const gqa_block_pages* cache,
     return MLA_ERR_CUDA;
   cudaLaunchAttribute attr = pdl_attribute();
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(sp.units);
-  cfg.blockDim = dim3(128);
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(32 * gqa8::kMergeWarps);
   cfg.stream = st;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, gqa8::gqa_fp8_merge_kernel, d, p.hdr,
-                            (const int*)p.prefix, (const unsigned*)p.err,
-                            p.own_plan ? grid : grid + 1, (const float*)p.ws_o, (const float*)p.ws_lse,
-                            out_partial, lse_partial) == cudaSuccess
+                            (const int4*)p.rec, p.own_plan ? grid : grid + 1,
+                            (const float*)p.ws_o, (const float*)p.ws_lse, out_partial, lse_partial) == cudaSuccess
              ? MLA_OK
              : MLA_ERR_CUDA;
 }
