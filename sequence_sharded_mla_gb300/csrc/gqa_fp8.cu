@@ -35,10 +35,10 @@
 // reference and O^T accumulator, joined by their references at the end of a
 // piece.  The groups never wait for one another inside a piece.
 //
-// Warps: 0 producer (block table, TMA boxes of K and V, cp.async of the
-// tokens' scales); 1 issues K Q^T; 2 issues V^T P^T; 4..7 and 8..11 the
-// softmax groups (TMEM lane quadrant = warp % 4), which also load and split
-// the piece's query rows and write its outputs.
+// Warps: 0 and 3 producers (block table, TMA boxes of K or V, cp.async of the
+// tokens' scales); 1 loads and splits each piece's query rows, a piece ahead
+// of the softmax, and issues K Q^T; 2 issues V^T P^T; 4..7 and 8..11 the
+// softmax groups (TMEM lane quadrant = warp % 4), which write the outputs.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math_constants.h>
@@ -58,14 +58,15 @@ namespace gqa8 {
 constexpr int kD = 128;                    // head width
 constexpr int kTok = 128;                  // tokens of a tile
 constexpr int kHalf = kTok * kD;           // 16384 bytes: K or V of a tile
-constexpr int kMaxStages = 6, kMaxS = 4;
+constexpr int kMaxStages = 6, kSBufs = 4;
 constexpr int kStageBytes = 2 * kHalf;
 constexpr int kThreads = 384;
 constexpr int kGroupThreads = 128;
 constexpr uint32_t kBarAll = 1, kBarGroup = 2;   // group g: kBarGroup + g
 constexpr int kMinTilesPerCta = 2;
 constexpr int kUnitCost = 2;
-constexpr int kMaxOwnPlan = 1024;          // units that every CTA plans for itself
+constexpr int kMaxR = 48;                  // query rows of the largest work unit
+constexpr int kMaxOwnPlan = 768;           // units that every CTA plans for itself
 constexpr int kOwnPerThread = (kMaxOwnPlan + kThreads - 1) / kThreads;
 constexpr unsigned long long kTimeoutNs = 2000000000ull;
 constexpr float kTop = 12.0f;              // log2 of the largest weight at a new reference
@@ -155,22 +156,15 @@ __device__ __forceinline__ Unit make_unit(const Desc& d, int u) {
   return x;
 }
 
-// Position of slot a of tile j.
-__device__ __forceinline__ int slot_token(const Desc& d, const Unit& x, int j, int a) {
-  const int p = j * kTok + a;
-  if (d.layout == kInterleaved) return p * d.num_shards + x.s;
-  return (d.local ? x.tstart : x.p0 * kPage) + p;
-}
+// Slot a of tile j holds position base + (128 j + a) step, if that is in
+// [tstart, tend).
+struct Slots {
+  int base, step;
+};
 
-__device__ __forceinline__ bool slot_valid(const Unit& x, int t) {
-  return t >= x.tstart && t < x.tend;
-}
-
-// Every slot of tile j holds a token that every row of the unit sees.
-__device__ __forceinline__ bool tile_full(const Desc& d, const Unit& x, int j) {
-  const int first = slot_token(d, x, j, 0), last = slot_token(d, x, j, kTok - 1);
-  return slot_valid(x, first) && slot_valid(x, last) &&
-         (!d.causal || last <= x.L - x.qn + x.r0 / d.G);
+__device__ __forceinline__ Slots make_slots(const Desc& d, const Unit& x) {
+  if (d.layout == kInterleaved) return Slots{x.s, d.num_shards};
+  return Slots{d.local ? x.tstart : x.p0 * kPage, 1};
 }
 
 __device__ __forceinline__ size_t out_row(const Desc& d, const Rows& x, int r) {
@@ -178,24 +172,31 @@ __device__ __forceinline__ size_t out_row(const Desc& d, const Rows& x, int r) {
   return (((size_t)x.so * d.B + x.b) * d.q_len + i) * d.H + h;
 }
 
+// A piece's query, by row.
+struct Query {
+  alignas(16) float qs[kMaxR];  // 1 / the row's query scale
+  int lim[kMaxR];               // last position the row sees
+  int orow[kMaxR];              // its output row
+};
+
 struct Misc {
-  uint64_t kv_full[kMaxStages], kv_empty[kMaxStages];
-  uint64_t s_full[kMaxS], s_empty[kMaxS], p_full[2], pv_done[2];
-  uint64_t q_full, drain;
+  uint64_t k_full[kMaxStages], v_full[kMaxStages], kv_empty[kMaxStages];
+  uint64_t s_full[kSBufs], s_empty[kSBufs], p_full[2], pv_done[2];
+  uint64_t q_full[2], q_empty[2], drain;
   uint32_t tmem_base;
   int abort;
   unsigned err;
   int wsum[kThreads / 32];      // planning: the warps' sums
-  int lim[kRows];               // last position a row sees
-  int orow[kRows];              // the row's output row
-  alignas(16) float qs[kRows];        // 1 / the row's query scale
-  alignas(16) float m[2][kRows];      // per group: the rows' references
-  alignas(16) float alpha[2][kRows];
-  int rmax[2][kRows];
-  int moved[2][kRows / 16];     // per group: a reference of these 16 rows moved
-  float lpart[2][4][kRows];     // per group and warp: sums of a piece
-  float f[2][kRows];            // per group: the factor of its accumulator
-  int nan_from[kD];             // per dim: the first partly seen token whose V is NaN
+  Query query[2];               // of this piece and the next
+  alignas(16) float m[2][kMaxR];      // per group: the rows' references, negated
+  // per group, by row: the factor of what has been summed so far when the
+  // references move, and of the group's accumulator at the end of a piece
+  alignas(16) float f[2][kMaxR];
+  // per group, warp and row: the largest logits when the references move, and
+  // the sums at the end of a piece
+  float part[2][4][kMaxR];
+  int moved[2][kMaxR / 16];     // per group: a reference of these 16 rows moved
+  int nan_from[2][kD];          // this piece, the next; per dim: the first partly seen token whose V is NaN
   float ksc[kMaxStages][kTok], vsc[kMaxStages][kTok];   // by run of slots with one scale
   int4 rec;
   int prefix[kMaxOwnPlan + 1];
@@ -218,19 +219,28 @@ __device__ __forceinline__ int4 make_record(const int* prefix, int u, int lo, in
 
 // Stages: what fits beside the weights.  A stage lives for its load, the
 // logits, the softmax and the P V of its tile, so more of them hide more of
-// that chain.  S buffers: two per group where TMEM has room, so that a tile's
-// logits are there when the group comes back from the one before.
+// that chain.  Two S buffers per group, so that a tile's logits are there when
+// the group comes back from the one before.
 template <int R>
 struct Smem {
-  static constexpr int kStages = R == 16 ? 6 : 5;
-  static constexpr int kSBufs = R == 48 ? 2 : 4;
-  static constexpr uint32_t kColO = kSBufs * 2 * R;         // O^T after the S buffers
+  static constexpr int kStages = R == 16 ? 6 : R == 32 ? 5 : 4;
+  // The query's two terms side by side as 2R columns of one MMA chain, added
+  // by the softmax, or (no columns left) as two chains into the same R.  Half
+  // the MMAs to issue, about 100 cycles each, against an addition per logit:
+  // 32 requests x 20000 tokens x 4 heads, R = 16: 137.6 against 139.5 us.
+  static constexpr bool kSplit = R <= 32;
+  static constexpr uint32_t kSCols = kSplit ? 2 * R : R;
+  static constexpr uint32_t kColO = kSBufs * kSCols;        // O^T after the S buffers
   static constexpr uint32_t kTmemCols = R == 16 ? 256 : 512;
   static_assert(kColO + 6 * R <= kTmemCols, "TMEM columns");
-  // Q: 16 rows' first terms, their second terms, the next 16 rows, ...
-  static constexpr int kQ = 0;                              // [R / 16][2][16][128]
+  static constexpr int kQBuf = 2 * R * kD;
+  static constexpr int kQ = 0;                              // two buffers
+  // term `term` of row r within a buffer
+  static __device__ __forceinline__ int q_row(int r, int term) {
+    return (kSplit ? 2 * (r & ~15) + 16 * term + (r & 15) : term * R + r) * kD;
+  }
   // P: blocks of 16 weights (rows of one term), unswizzled
-  static constexpr int kP = 2 * R * kD;                     // [2 groups][3][R / 16][128 tokens][16]
+  static constexpr int kP = 2 * kQBuf;                      // [2 groups][3][R / 16][128 tokens][16]
   static constexpr int kPBlock = 16 * kTok;
   static constexpr int kPGroup = 3 * R * kTok;
   static constexpr int kStage = (kP + 2 * kPGroup + 1023) & ~1023;
@@ -254,12 +264,24 @@ __global__ void __launch_bounds__(1024) gqa_fp8_plan_kernel(Desc d, WsHeader* hd
   if (threadIdx.x == 0) *rec = make_int4(-1, 0, 0, (int)bad);
 }
 
-__device__ __forceinline__ int ordered(float x) {   // float order as int order
-  const int i = __float_as_int(x);
-  return i ^ ((i >> 31) & 0x7fffffff);
+// Largest of the lanes' values that are not NaN.
+__device__ __forceinline__ float warp_max(float x) {
+  float y;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
 }
-__device__ __forceinline__ float from_ordered(int i) {
-  return __int_as_float(i ^ ((i >> 31) & 0x7fffffff));
+
+// Sums of 16 values over the warp: lane k, and lane 16 + k, gets that of v[k].
+__device__ __forceinline__ float warp_sums(float (&v)[16], int lane) {
+#pragma unroll
+  for (int s = 8; s > 0; s >>= 1) {
+    const bool upper = lane & s;
+#pragma unroll
+    for (int k = 0; k < s; ++k)
+      v[k] = (upper ? v[k + s] : v[k]) +
+             __shfl_xor_sync(0xffffffffu, upper ? v[k] : v[k + s], s);
+  }
+  return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 16);
 }
 
 __device__ __forceinline__ float lg2_approx(float x) {
@@ -325,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     gqa_fp8_partial_kernel(const __grid_constant__ CUtensorMap tm_k,
                            const __grid_constant__ CUtensorMap tm_v, Params p) {
   using S = Smem<R>;
-  constexpr int kStages = S::kStages, kSBufs = S::kSBufs;
+  constexpr int kStages = S::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   Misc* misc = reinterpret_cast<Misc*>(smem + S::kMisc);
@@ -349,7 +371,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int st = 0; st < kStages; ++st) {
-      mbar_init(bar(&misc->kv_full[st]), 1 + 32);   // expect_tx + one cp.async arrival per lane
+      mbar_init(bar(&misc->k_full[st]), 1 + 32);   // expect_tx + one cp.async arrival per lane
+      mbar_init(bar(&misc->v_full[st]), 1);
       mbar_init(bar(&misc->kv_empty[st]), 1);
     }
     for (int k = 0; k < kSBufs; ++k) {
@@ -360,7 +383,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar(&misc->p_full[g]), 4);
       mbar_init(bar(&misc->pv_done[g]), 1);
     }
-    mbar_init(bar(&misc->q_full), 8);
+    for (int k = 0; k < 2; ++k) {
+      mbar_init(bar(&misc->q_full[k]), 1);
+      mbar_init(bar(&misc->q_empty[k]), 8);
+    }
     mbar_init(bar(&misc->drain), 2);
     misc->abort = 0;
     misc->err = 0;
@@ -374,6 +400,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
   }
+  if (threadIdx.x < 2 * kMaxR) misc->m[threadIdx.x / kMaxR][threadIdx.x % kMaxR] = -kNoRef;
+  if (threadIdx.x < 2 * kD) misc->nan_from[threadIdx.x / kD][threadIdx.x % kD] = INT_MAX;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -441,14 +469,30 @@ __global__ void __launch_bounds__(kThreads, 1)
   int unit, t0, t1, slot;
   bool whole, ok = true;
 
-  if (warp == 0) {
-    // ------------------------------------------------------------ producer
+  if (warp == 0 || warp == 3) {
+    // ------------------------------------------------------------ producers
+    // warp 0 loads K and the scales, warp 3 loads V: with 8 shards a
+    // tile is 2 x 16 boxes of 1 KB, and one warp that issued all of them
+    // bounded the kernel (1 GB over 8 shards 320 us, two warps XXX us)
+    const bool is_v = warp == 3;
+    if (is_v) {
+      if (lane == 0) misc->rec = make_record(prefix, it.u, lo, hi, per);
+      for (int u = blockIdx.x; u < p.units; u += gridDim.x) {
+        if (prefix[u + 1] > prefix[u]) continue;
+        const Rows x = make_rows(d, u);          // no token in the shard: o = 0, lse = -inf
+        for (int r = 0; r < x.rows; ++r) {
+          const size_t row = out_row(d, x, r);
+          reinterpret_cast<float4*>(p.out + row * kD)[lane] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (lane == 0) p.lse[row] = -CUDART_INF_F;
+        }
+      }
+    }
     const int nb = 2 * d.nv;                     // page boxes per tile
     const int rp = kPage / d.nv;                 // slots per box
     const int lg_rp = 31 - __clz(rp);
-    const int box = lane & 15;                   // lanes 0..15 load K, 16..31 V
-    const CUtensorMap* tm = lane < 16 ? &tm_k : &tm_v;
-    const uint32_t dst0 = sSt + (lane < 16 ? 0 : kHalf) + box * (rp * kD);
+    const CUtensorMap* tm = is_v ? &tm_v : &tm_k;
+    const uint64_t* full_bars = is_v ? misc->v_full : misc->k_full;
+    const uint32_t dst0 = sSt + (is_v ? kHalf : 0);
     const int lg_sub = 6 - d.lg_block;           // scales per page and head
     const int runs = kTok >> d.lg_run;
     int g = 0;
@@ -457,8 +501,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int32_t* bt = d.block_table + (size_t)x.b * d.max_pages;
       const int res = d.nv > 1 ? x.s : 0;
       auto entry = [&](int j) {                  // page of this lane's box of tile j, or -1
-        const int idx = x.p0 + j * nb + box;
-        return (box < nb && idx < x.npages && idx < d.max_pages) ? __ldg(bt + idx) : -1;
+        const int idx = x.p0 + j * nb + lane;
+        return (lane < nb && idx < x.npages && idx < d.max_pages) ? __ldg(bt + idx) : -1;
       };
       int next = entry(t0);
       for (int j = t0; j < t1; ++j, ++g) {
@@ -467,19 +511,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (j + 1 < t1) next = entry(j + 1);
         const bool there = page >= 0 && page < d.num_pages;
         if (!there) {
-          if (box < nb && x.p0 + j * nb + box < x.npages) atomicOr(&misc->err, kErrBadPage);
+          if (lane < nb && x.p0 + j * nb + lane < x.npages) atomicOr(&misc->err, kErrBadPage);
           page = d.num_pages;                    // out of the map: TMA fills zeros
         }
         if (round >= 1 && !(ok = wait(&misc->kv_empty[st], (round - 1) & 1))) break;
-        const uint32_t full = bar(&misc->kv_full[st]);
+        const uint32_t full = bar(&full_bars[st]);
         if (lane == 0) {
-          mbar_arrive_expect_tx(full, kStageBytes);
+          mbar_arrive_expect_tx(full, kHalf);
           armed[st] = g;
         }
         __syncwarp();
-        if (box < nb)
-          tma_load_3d(dst0 + st * kStageBytes, tm, full, 0, 0, (page * kPage + res) * d.Hkv + x.kh);
-        for (int h = 0; h < runs; h += 32) {
+        if (lane < nb)
+          tma_load_3d(dst0 + st * kStageBytes + lane * (rp * kD), tm, full, 0, 0,
+                      (page * kPage + res) * d.Hkv + x.kh);
+        for (int h = 0; !is_v && h < runs; h += 32) {
           const int e = h + lane, a = min(e << d.lg_run, kTok - 1);
           const int pg = __shfl_sync(0xffffffffu, page, a >> lg_rp);
           const int row = res + (a & (rp - 1)) * d.nv;
@@ -491,28 +536,86 @@ __global__ void __launch_bounds__(kThreads, 1)
             cp_async_4_zfill(smem_u32(&misc->vsc[st][e]), d.vs + si, ok_pg);
           }
         }
-        cp_async_mbar_arrive_noinc(full);
+        if (!is_v) cp_async_mbar_arrive_noinc(full);
         __syncwarp();
       }
     }
   } else if (warp == 1) {
-    // ------------------------------------------------------------ K Q^T
-    const uint32_t id = idesc_e4m3_f32(kTok, 2 * R, false, false);
-    const uint64_t dk = sw128_desc(sSt, 16, 1024), dq = sw128_desc(sQ, 16, 1024);
+    // ------------------------------------------------- the query, K Q^T
+    const uint32_t id = idesc_e4m3_f32(kTok, S::kSCols, false, false);
+    const uint64_t dk = sw128_desc(sSt, 16, 1024);
+    const uint32_t rows_of_all = d.B * d.q_len * d.H;
     int g = 0, pc = 0;
     while (ok && it.next(unit, t0, t1, whole, slot)) {
-      if (!(ok = wait(&misc->q_full, pc & 1))) break;
+      const Rows x = make_rows(d, unit);
+      const int L = max(d.seq_lens[x.b], 0);
+      const int qn = d.q_lens ? min(max(d.q_lens[x.b], 0), d.q_len) : d.q_len;
+      const int live = min(qn * d.G - x.r0, x.rows);
+      const int buf = pc & 1;
+      Query& query = misc->query[buf];
+      if (pc >= 2 && !(ok = wait(&misc->q_empty[buf], ((pc >> 1) - 1) & 1))) break;
+      // 16 lanes a row, 8 values each; the loads of 16 rows are in flight together
+#pragma unroll 1
+      for (int r0 = 0; r0 < R; r0 += 16) {
+        const int c = lane & 15;
+        uint4 w[8];
+        int src[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int r = r0 + 2 * k + (lane >> 4);
+          const int i = (x.r0 + r) / d.G;
+          src[k] = (x.b * d.q_len + i) * d.H + x.kh * d.G + (x.r0 + r) - i * d.G;
+          w[k] = make_uint4(0, 0, 0, 0);
+          if (r < live) w[k] = __ldg(reinterpret_cast<const uint4*>(d.q + (size_t)src[k] * kD) + c);
+          if (c == 0) {
+            query.orow[r] = (int)(x.so * rows_of_all) + src[k];
+            query.lim[r] = d.causal && r < live ? L - qn + i : INT_MAX - 1;
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int r = r0 + 2 * k + (lane >> 4);
+          const uint32_t ww[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+          uint32_t mx = 0;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mx = max(mx, max(ww[e] & 0x7FFFu, (ww[e] >> 16) & 0x7FFFu));
+#pragma unroll
+          for (int o = 8; o > 0; o >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+          // s_r = 2^(134 - e) puts max|q| (exponent e) in [128, 256); clamped so
+          // that it and its inverse are normal
+          const uint32_t e = min(max(mx >> 7, 8u), 254u);
+          const float sc = __uint_as_float((261u - e) << 23);
+          uint32_t sp[4];
+#pragma unroll
+          for (int h = 0; h < 4; ++h)
+            sp[h] = split_e4m3x2(__uint_as_float(ww[h] << 16) * sc,
+                                 __uint_as_float(ww[h] & 0xFFFF0000u) * sc);
+          uint8_t* dst = smem + S::kQ + buf * S::kQBuf + (((c >> 1) ^ (r & 7)) << 4) + (c & 1) * 8;
+          *reinterpret_cast<uint2*>(dst + S::q_row(r, 0)) =
+              make_uint2((sp[0] & 0xFFFFu) | (sp[1] << 16), (sp[2] & 0xFFFFu) | (sp[3] << 16));
+          *reinterpret_cast<uint2*>(dst + S::q_row(r, 1)) =
+              make_uint2((sp[0] >> 16) | (sp[1] & 0xFFFF0000u), (sp[2] >> 16) | (sp[3] & 0xFFFF0000u));
+          if (c == 0) {
+            if ((mx >> 7) == 255u) atomicOr(&misc->err, kErrQRange);
+            query.qs[r] = __uint_as_float((e - 7u) << 23);
+          }
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0 && !(p.withhold_query && pc == 0)) mbar_arrive(bar(&misc->q_full[buf]));
+      const uint64_t dq = sw128_desc(sQ + buf * S::kQBuf, 16, 1024);
       for (int j = t0; j < t1; ++j, ++g) {
         const int st = g % kStages, round = g / kStages, sb = g % kSBufs, sr = g / kSBufs;
-        if (!(ok = wait(&misc->kv_full[st], round & 1))) break;
+        if (!(ok = wait(&misc->k_full[st], round & 1))) break;
         if (sr >= 1 && !(ok = wait(&misc->s_empty[sb], (sr - 1) & 1))) break;
         tc_fence_after();
         if (lane == 0) {
           const uint32_t off = (uint32_t)(st * kStageBytes) >> 4;
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mma_e4m3_ss(tmem + 2 * R * sb, dk + off + ((32 * k) >> 4), dq + ((32 * k) >> 4), id,
-                        k != 0);
+          for (int k = 0; k < (S::kSplit ? 4 : 8); ++k)   // 32 dims each
+            mma_e4m3_ss(tmem + S::kSCols * sb, dk + off + ((32 * (k & 3)) >> 4),
+                        dq + (((k >> 2) * R * kD + 32 * (k & 3)) >> 4), id, k != 0);
           mma_commit(bar(&misc->s_full[sb]));
         }
         __syncwarp();
@@ -527,6 +630,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (ok && it.next(unit, t0, t1, whole, slot)) {
       for (int j = t0; j < t1; ++j, ++g) {
         const int st = g % kStages, grp = g & 1, gr = g >> 1;
+        if (!(ok = wait(&misc->v_full[st], (g / kStages) & 1))) break;
         if (!(ok = wait(&misc->p_full[grp], gr & 1))) break;
         tc_fence_after();
         if (lane == 0) {
@@ -543,18 +647,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
       }
     }
-  } else if (warp == 3) {
-    // ------------------------------------------------ record, empty units
-    if (lane == 0) misc->rec = make_record(prefix, it.u, lo, hi, per);
-    for (int u = blockIdx.x; u < p.units; u += gridDim.x) {
-      if (prefix[u + 1] > prefix[u]) continue;
-      const Unit x = make_unit(d, u);            // no token in the shard: o = 0, lse = -inf
-      for (int r = 0; r < x.rows; ++r) {
-        const size_t row = out_row(d, x, r);
-        reinterpret_cast<float4*>(p.out + row * kD)[lane] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (lane == 0) p.lse[row] = -CUDART_INF_F;
-      }
-    }
   } else {
     // ------------------------------------------------------------ softmax
     const int grp = (warp - 4) >> 2, quad = warp & 3;
@@ -563,68 +655,38 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_off = (uint32_t)(32 * quad) << 16;
     const uint32_t tS = tmem + lane_off, tO = tmem + lane_off + S::kColO;
     float* ref = misc->m[grp];
-    int g = 0, pc = 0;
+    // A thread's own wait; the lanes' answers are joined before they matter.
+    auto poll = [&](const uint64_t* b, int parity) {
+      const bool k = mbar_wait(bar(b), parity, tmo, abort_flag);
+      if (!k) fail();
+      return k;
+    };
+    int g = 0, pc = 0;                             // tiles and pieces so far
+    int st = grp, phase = 0, gr = 0;               // the group's next tile: stage, its phase, number
     while (ok && it.next(unit, t0, t1, whole, slot)) {
       const Unit x = make_unit(d, unit);
-      // ------------------------------------------------- the piece's query
-      // 16 lanes a row, 8 values each; the previous piece's MMAs have read the
-      // old rows, since all of its S has been consumed
-#pragma unroll
-      for (int r0 = 0; r0 < R; r0 += 16) {
-        const int r = r0 + (tid >> 4), c = tid & 15;
-        uint4 w = make_uint4(0, 0, 0, 0);
-        if (r < x.live) {
-          const int i = (x.r0 + r) / d.G, h = x.kh * d.G + (x.r0 + r) % d.G;
-          w = __ldg(reinterpret_cast<const uint4*>(
-                        d.q + (((size_t)x.b * d.q_len + i) * d.H + h) * kD) + c);
-        }
-        const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-        uint32_t mx = 0;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) mx = max(mx, max(ww[e] & 0x7FFFu, (ww[e] >> 16) & 0x7FFFu));
-#pragma unroll
-        for (int o = 8; o > 0; o >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        // s_r = 2^(134 - e) puts max|q| (exponent e) in [128, 256); clamped so
-        // that it and its inverse are normal
-        const uint32_t e = min(max(mx >> 7, 8u), 254u);
-        const float sc = __uint_as_float((261u - e) << 23);
-        uint32_t sp[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          sp[k] = split_e4m3x2(__uint_as_float(ww[k] << 16) * sc,
-                               __uint_as_float(ww[k] & 0xFFFF0000u) * sc);
-        uint8_t* dst = smem + S::kQ + (2 * r0 + (r & 15)) * kD + (((c >> 1) ^ (r & 7)) << 4) +
-                       (c & 1) * 8;
-        *reinterpret_cast<uint2*>(dst) =
-            make_uint2((sp[0] & 0xFFFFu) | (sp[1] << 16), (sp[2] & 0xFFFFu) | (sp[3] << 16));
-        *reinterpret_cast<uint2*>(dst + 16 * kD) =
-            make_uint2((sp[0] >> 16) | (sp[1] & 0xFFFF0000u), (sp[2] >> 16) | (sp[3] & 0xFFFF0000u));
-        if (c == 0) {
-          if ((mx >> 7) == 255u) atomicOr(&misc->err, kErrQRange);
-          misc->qs[r] = __uint_as_float((e - 7u) << 23);
-          if (r < x.rows) misc->orow[r] = (int)out_row(d, x, r);
-          misc->lim[r] = d.causal && r < x.live ? x.L - x.qn + (x.r0 + r) / d.G : INT_MAX - 1;
-        }
-      }
-      if (tid < 2 * R) misc->m[tid / R][tid % R] = kNoRef;
-      if (tid < kD) misc->nan_from[tid] = INT_MAX;
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0 && !(p.withhold_query && pc == 0)) mbar_arrive(bar(&misc->q_full));
-      named_bar_sync(kBarAll, 2 * kGroupThreads);
+      const Slots slots = make_slots(d, x);
+      // tiles whose first position is in [tstart, last_full] hold a token that
+      // every row sees in every slot
+      const int last_full = min(x.tend - 1, d.causal ? x.L - x.qn + x.r0 / d.G : INT_MAX) -
+                            (kTok - 1) * slots.step;
+      const Query& query = misc->query[pc & 1];
+      int* nan_from = misc->nan_from[pc & 1];
+      // the end of the previous piece, or the kernel's start, has set the references
+      ok = __all_sync(0xffffffffu, poll(&misc->q_full[pc & 1], (pc >> 1) & 1));
 
       float2 l[R / 2];
 #pragma unroll
       for (int r = 0; r < R / 2; ++r) l[r] = make_float2(0.0f, 0.0f);
       bool first = true;                           // the group's first tile of the piece
-      for (int j = t0; j < t1; ++j, ++g) {
-        if ((g & 1) != grp) continue;
-        const int st = g % kStages, gr = g >> 1, sb = g % kSBufs;
+      for (int j = t0 + ((g ^ grp) & 1); j < t1; j += 2) {
         // -------------------------------------------------------- logits
-        const bool full = tile_full(d, x, j);
-        const int t = slot_token(d, x, j, gtid);
-        const bool valid = full || slot_valid(x, t);
-        bool ok_s = ok && wait(&misc->kv_full[st], (g / kStages) & 1);
+        const int sb = kSBufs == 4 ? 2 * (gr & 1) + grp : grp;
+        const int s_phase = (kSBufs == 4 ? gr >> 1 : gr) & 1;
+        const int tok0 = slots.base + j * kTok * slots.step, t = tok0 + gtid * slots.step;
+        const bool full = tok0 >= x.tstart && tok0 <= last_full;
+        const bool valid = full || (t >= x.tstart && t < x.tend);
+        bool ok_s = ok && poll(&misc->k_full[st], phase);
         float c = 0.0f, lv = 0.0f, inv = 0.0f, fv = 1.0f;
         if (ok_s && valid) {
           c = misc->ksc[st][gtid >> d.lg_run] * d.scale_log2;
@@ -639,43 +701,54 @@ __global__ void __launch_bounds__(kThreads, 1)
           lv = lg2_approx(ve);
           inv = rcp_approx(ve);
         }
-        ok_s = ok_s && wait(&misc->s_full[sb], (g / kSBufs) & 1);
         const bool scaled = __any_sync(0xffffffffu, fv != 1.0f);
+        ok_s = __all_sync(0xffffffffu, ok_s && poll(&misc->s_full[sb], s_phase));
         // 16 rows' logits of this token in log2 units, with the V scale: into
         // b (two rows each), less the references if asked for
-        auto logits = [&](int r0, const uint32_t (&sr)[32], float2* b, bool less) {
-          const float4* q4 = reinterpret_cast<const float4*>(misc->qs + r0);
+        auto logits = [&](int r0, const uint32_t (&sr)[S::kSplit ? 32 : 16], float2* b, bool less) {
+          const float4* q4 = reinterpret_cast<const float4*>(query.qs + r0);
           const float4* m4 = reinterpret_cast<const float4*>(ref + r0);
           const float2 c2 = make_float2(c, c), lv2 = make_float2(lv, lv);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const float4 q = q4[k];
-            float4 m = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (less) m = m4[k];
-            const float2 v0 = add2(as_f2(sr[4 * k], sr[4 * k + 1]), as_f2(sr[16 + 4 * k], sr[17 + 4 * k]));
-            const float2 v1 = add2(as_f2(sr[4 * k + 2], sr[4 * k + 3]), as_f2(sr[18 + 4 * k], sr[19 + 4 * k]));
-            const float2 n0 = add2(lv2, make_float2(-m.x, -m.y)), n1 = add2(lv2, make_float2(-m.z, -m.w));
+            float2 n0 = lv2, n1 = lv2;
+            if (less) {
+              const float4 m = m4[k];
+              n0 = add2(lv2, make_float2(m.x, m.y));
+              n1 = add2(lv2, make_float2(m.z, m.w));
+            }
+            float2 v0 = as_f2(sr[4 * k], sr[4 * k + 1]), v1 = as_f2(sr[4 * k + 2], sr[4 * k + 3]);
+            if constexpr (S::kSplit) {
+              v0 = add2(v0, as_f2(sr[16 + 4 * k], sr[17 + 4 * k]));
+              v1 = add2(v1, as_f2(sr[18 + 4 * k], sr[19 + 4 * k]));
+            }
             b[2 * k] = fma2(mul2(v0, make_float2(q.x, q.y)), c2, n0);
             b[2 * k + 1] = fma2(mul2(v1, make_float2(q.z, q.w)), c2, n1);
           }
           if (!full) {
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-              if (!valid || t > misc->lim[r0 + 2 * k]) b[k].x = -CUDART_INF_F;
-              if (!valid || t > misc->lim[r0 + 2 * k + 1]) b[k].y = -CUDART_INF_F;
+              if (!valid || t > query.lim[r0 + 2 * k]) b[k].x = -CUDART_INF_F;
+              if (!valid || t > query.lim[r0 + 2 * k + 1]) b[k].y = -CUDART_INF_F;
             }
           }
         };
-        const uint32_t tSb = tS + 2 * R * sb;
+        // 16 rows' columns of the tile's S
+        auto load_s = [&](int r0, uint32_t (&sr)[S::kSplit ? 32 : 16]) {
+          const uint32_t a = tS + S::kSCols * sb + (S::kSplit ? 2 * r0 : r0);
+          if constexpr (S::kSplit) tmem_ld32(a, sr);
+          else tmem_ld16(a, sr);
+        };
         float2 b[R / 2];
         bool over = false;
         auto all_logits = [&]() {
-          uint32_t sr[2][32];
-          tmem_ld32(tSb, sr[0]);
+          uint32_t sr[2][S::kSplit ? 32 : 16];
+          load_s(0, sr[0]);
 #pragma unroll
           for (int r0 = 0; r0 < R; r0 += 16) {
             tmem_wait_ld();
-            if (r0 + 16 < R) tmem_ld32(tSb + 2 * (r0 + 16), sr[((r0 >> 4) + 1) & 1]);
+            if (r0 + 16 < R) load_s(r0 + 16, sr[((r0 >> 4) + 1) & 1]);
             logits(r0, sr[(r0 >> 4) & 1], b + r0 / 2, true);
           }
         };
@@ -688,49 +761,47 @@ __global__ void __launch_bounds__(kThreads, 1)
           over = mx > kMost;
         }
         if (named_bar_or(kBarGroup + grp, kGroupThreads, over || !ok_s)) {
+          // ---------------------------------------------- new references
+          if (ok_s) {
+#pragma unroll 1
+            for (int r0 = 0; r0 < R; r0 += 16) {
+              uint32_t sr[S::kSplit ? 32 : 16];
+              float2 y[8];
+              load_s(r0, sr);
+              tmem_wait_ld();
+              logits(r0, sr, y, false);
+              float mine = 0.0f;
+#pragma unroll
+              for (int k = 0; k < 16; ++k) {
+                const float mx = warp_max((k & 1) ? y[k >> 1].y : y[k >> 1].x);
+                if (lane == k) mine = mx;
+              }
+              if (lane < 16) misc->part[grp][quad][r0 + lane] = mine;
+            }
+          }
           if (named_bar_or(kBarGroup + grp, kGroupThreads, !ok_s)) {
             ok = false;
             break;
           }
-          // ---------------------------------------------- new references
-          if (gtid < R) misc->rmax[grp][gtid] = INT_MIN;
-          if (gtid < R / 16) misc->moved[grp][gtid] = 0;
-          named_bar_sync(kBarGroup + grp, kGroupThreads);
-#pragma unroll 1
-          for (int r0 = 0; r0 < R; r0 += 16) {
-            uint32_t sr[32];
-            float2 y[8];
-            tmem_ld32(tSb + 2 * r0, sr);
-            tmem_wait_ld();
-            logits(r0, sr, y, false);
-            int mine = INT_MIN;
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              const float v = (k & 1) ? y[k >> 1].y : y[k >> 1].x;
-              const int mx = __reduce_max_sync(0xffffffffu, v == v ? ordered(v) : INT_MIN);
-              if (lane == k) mine = mx;
-            }
-            if (lane < 16) atomicMax(&misc->rmax[grp][r0 + lane], mine);
-          }
-          named_bar_sync(kBarGroup + grp, kGroupThreads);
+          bool up = false;
           if (gtid < R) {
-            const int o = misc->rmax[grp][gtid];
-            const float top = o == INT_MIN ? -CUDART_INF_F : from_ordered(o), old = ref[gtid];
-            const bool up = top > old + kMost;
-            misc->alpha[grp][gtid] = up ? ex2_approx(old - (top - kTop)) : 1.0f;
-            if (up) {
-              ref[gtid] = top - kTop;
-              misc->moved[grp][gtid >> 4] = 1;
-            }
+            float top = misc->part[grp][0][gtid];  // NaN loses to any number
+            for (int k = 1; k < 4; ++k) top = fmaxf(top, misc->part[grp][k][gtid]);
+            const float old = -ref[gtid];
+            up = top > old + kMost;
+            misc->f[grp][gtid] = up ? ex2_approx(old - (top - kTop)) : 1.0f;
+            if (up) ref[gtid] = kTop - top;
           }
-          const bool ok_pv = first || wait(&misc->pv_done[grp], (gr - 1) & 1);
+          const uint32_t ups = __ballot_sync(0xffffffffu, up);
+          if (gtid < R && (lane & 15) == 0) misc->moved[grp][gtid >> 4] = (ups >> lane) & 0xFFFFu;
+          const bool ok_pv = first || poll(&misc->pv_done[grp], (gr - 1) & 1);
           if (named_bar_or(kBarGroup + grp, kGroupThreads, !ok_pv)) {
             ok = false;
             break;
           }
 #pragma unroll
           for (int r = 0; r < R / 2; ++r)
-            l[r] = mul2(l[r], make_float2(misc->alpha[grp][2 * r], misc->alpha[grp][2 * r + 1]));
+            l[r] = mul2(l[r], make_float2(misc->f[grp][2 * r], misc->f[grp][2 * r + 1]));
           if (!first) {
             tc_fence_after();
 #pragma unroll 1
@@ -742,7 +813,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               tmem_wait_ld();
 #pragma unroll
               for (int k = 0; k < 16; ++k) {
-                const float al = misc->alpha[grp][r0 + k];
+                const float al = misc->f[grp][r0 + k];
 #pragma unroll
                 for (int term = 0; term < 3; ++term)
                   v[term][k] = __float_as_uint(__uint_as_float(v[term][k]) * al);
@@ -759,7 +830,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(&misc->s_empty[sb]));
         // the group's last P V has read the weights' buffer
-        if (!first && !wait(&misc->pv_done[grp], (gr - 1) & 1)) {
+        if (!first && !__all_sync(0xffffffffu, poll(&misc->pv_done[grp], (gr - 1) & 1))) {
           ok = false;
           continue;                                // the next reduction ends the piece
         }
@@ -797,12 +868,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           // V rows of slots without a token become zeros; a NaN code of a token
           // that not every row sees is taken out too and comes back in the
           // epilogue for the rows that see it (rows see a prefix)
+          if (!__all_sync(0xffffffffu, poll(&misc->v_full[st], phase))) {
+            ok = false;
+            continue;
+          }
           uint8_t* vt = smem + S::kStage + st * kStageBytes + kHalf;
           for (int e = gtid; e < kTok * (kD / 16); e += kGroupThreads) {
             const int a = e >> 3, u = e & 7;
-            const int ta = slot_token(d, x, j, a);
+            const int ta = tok0 + a * slots.step;
             uint4* v = reinterpret_cast<uint4*>(vt + a * kD + ((u ^ (a & 7)) << 4));
-            if (!slot_valid(x, ta)) {
+            if (ta < x.tstart || ta >= x.tend) {
               *v = make_uint4(0, 0, 0, 0);
               continue;
             }
@@ -816,7 +891,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               const int sh = 8 * (k & 3);
               if (((ww[k >> 2] >> sh) & 0x7Fu) == 0x7Fu) {
                 ww[k >> 2] &= ~(0xFFu << sh);
-                atomicMin(&misc->nan_from[16 * u + k], ta);
+                atomicMin(&nan_from[16 * u + k], ta);
               }
             }
             *v = make_uint4(ww[0], ww[1], ww[2], ww[3]);
@@ -827,22 +902,33 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(&misc->p_full[grp]));
+        st += 2;
+        if (st >= kStages) {
+          st -= kStages;
+          phase ^= 1;
+        }
+        ++gr;
       }
+      g += t1 - t0;
       // ------------------------------------------------------------ epilogue
       // sums over the group's threads, then over its warps, in a fixed order
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        float v = (r & 1) ? l[r >> 1].y : l[r >> 1].x;
+      for (int r0 = 0; r0 < R; r0 += 16) {
+        float v[16];
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-        if (lane == 0) misc->lpart[grp][quad][r] = v;
+        for (int k = 0; k < 8; ++k) {
+          v[2 * k] = l[r0 / 2 + k].x;
+          v[2 * k + 1] = l[r0 / 2 + k].y;
+        }
+        const float sum = warp_sums(v, lane);
+        if (lane < 16) misc->part[grp][quad][r0 + lane] = sum;
       }
-      // g is now the number of tiles so far; the groups' shares of them
+      // the groups' shares of the tiles so far, and of this piece
       const int n0 = (g + 1) >> 1, n1 = g >> 1;
       const int has0 = t1 - t0 > 1 || (g & 1), has1 = t1 - t0 > 1 || !(g & 1);
       bool ok_e = ok;
-      if (ok_e && has0) ok_e = wait(&misc->pv_done[0], (n0 - 1) & 1);
-      if (ok_e && has1) ok_e = wait(&misc->pv_done[1], (n1 - 1) & 1);
+      if (ok_e && has0) ok_e = poll(&misc->pv_done[0], (n0 - 1) & 1);
+      if (ok_e && has1) ok_e = poll(&misc->pv_done[1], (n1 - 1) & 1);
       if (named_bar_or(kBarAll, 2 * kGroupThreads, !ok_e)) {
         ok = false;
         break;
@@ -853,11 +939,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int r = tid;
         float lg[2], M = kNoRef;
         for (int k = 0; k < 2; ++k) {
-          lg[k] = (misc->lpart[k][0][r] + misc->lpart[k][1][r]) +
-                  (misc->lpart[k][2][r] + misc->lpart[k][3][r]);
-          M = fmaxf(M, misc->m[k][r]);
+          lg[k] = (misc->part[k][0][r] + misc->part[k][1][r]) +
+                  (misc->part[k][2][r] + misc->part[k][3][r]);
+          M = fmaxf(M, -misc->m[k][r]);
         }
-        const float w0 = ex2_approx(misc->m[0][r] - M), w1 = ex2_approx(misc->m[1][r] - M);
+        const float w0 = ex2_approx(-misc->m[0][r] - M), w1 = ex2_approx(-misc->m[1][r] - M);
         const float tot = w0 * lg[0] + w1 * lg[1];
         const bool none = tot == 0.0f || r >= x.live;   // not NaN
         const float it_ = none ? 0.0f : 1.0f / tot;
@@ -865,7 +951,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         misc->f[1][r] = w1 * it_;
         if (r < x.rows) {
           const float v = none ? -CUDART_INF_F : (M + log2f(tot)) * 0.69314718055994530942f;
-          if (whole) p.lse[misc->orow[r]] = v;
+          if (whole) p.lse[query.orow[r]] = v;
           else p.ws_lse[sl * kRows + r] = v;
         }
       }
@@ -873,7 +959,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // thread (quad, lane) holds dim 32 quad + lane of every row; the groups
       // take turns over 16 rows
       const int dim = 32 * quad + lane;
-      const int nan_from = misc->nan_from[dim];
+      const int nf = nan_from[dim];
 #pragma unroll 1
       for (int r0 = 16 * grp; r0 < x.rows; r0 += 32) {
         float o[16];
@@ -882,31 +968,34 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
         for (int gg = 0; gg < 2; ++gg) {
           if (!(gg ? has1 : has0)) continue;       // its accumulator holds nothing of this piece
-          float a[16];
+          uint32_t v[3][16];
 #pragma unroll
-          for (int k = 0; k < 16; ++k) a[k] = 0.0f;
+          for (int term = 0; term < 3; ++term) tmem_ld16(tO + 3 * R * gg + R * term + r0, v[term]);
+          tmem_wait_ld();
+          const float4* f4 = reinterpret_cast<const float4*>(misc->f[gg] + r0);
 #pragma unroll
-          for (int term = 0; term < 3; ++term) {
-            uint32_t v[16];
-            tmem_ld16(tO + 3 * R * gg + R * term + r0, v);
-            tmem_wait_ld();
-#pragma unroll
-            for (int k = 0; k < 16; ++k) a[k] += __uint_as_float(v[k]);
+          for (int k = 0; k < 16; ++k) {
+            const float4 f = f4[k >> 2];
+            const float a = (__uint_as_float(v[0][k]) + __uint_as_float(v[1][k])) +
+                            __uint_as_float(v[2][k]);
+            o[k] = fmaf(a, (k & 3) == 0 ? f.x : (k & 3) == 1 ? f.y : (k & 3) == 2 ? f.z : f.w, o[k]);
           }
-#pragma unroll
-          for (int k = 0; k < 16; ++k) o[k] = fmaf(a[k], misc->f[gg][r0 + k], o[k]);
         }
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
           const int r = r0 + k;
           if (r >= x.rows) break;
-          float v = misc->lim[r] >= nan_from ? CUDART_NAN_F : o[k];
+          float v = query.lim[r] >= nf ? CUDART_NAN_F : o[k];
           if (r >= x.live) v = 0.0f;
-          (whole ? p.out + (size_t)misc->orow[r] * kD : p.ws_o + (sl * kRows + r) * kD)[dim] = v;
+          (whole ? p.out + (size_t)query.orow[r] * kD : p.ws_o + (sl * kRows + r) * kD)[dim] = v;
         }
       }
+      // for the next piece
+      if (gtid < R) ref[gtid] = -kNoRef;
+      if (tid < kD) misc->nan_from[(pc + 1) & 1][tid] = INT_MAX;
       tc_fence_before();
       named_bar_sync(kBarAll, 2 * kGroupThreads);  // accumulators and exchange are free again
+      if (lane == 0) mbar_arrive(bar(&misc->q_empty[pc & 1]));
       ++pc;
     }
   }
@@ -922,10 +1011,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       mma_commit(bar(&misc->drain));
       mbar_wait(bar(&misc->drain), 0, kDrainNs, &never);
     }
-    if (warp == 0 && lane == 0)
+    if ((warp == 0 || warp == 3) && lane == 0)
       for (int st = 0; st < kStages; ++st)
         if (armed[st] >= 0)
-          mbar_wait(bar(&misc->kv_full[st]), (armed[st] / kStages) & 1, kDrainNs, &never);
+          mbar_wait(bar(warp == 0 ? &misc->k_full[st] : &misc->v_full[st]),
+                    (armed[st] / kStages) & 1, kDrainNs, &never);
     tc_fence_before();
     __syncthreads();
   }

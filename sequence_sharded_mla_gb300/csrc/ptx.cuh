@@ -93,11 +93,12 @@ __device__ __forceinline__ bool mbar_try_wait_hint(uint32_t bar, uint32_t parity
 // Wait for the phase with the given parity to complete.  Returns false if
 // `limit_ns` elapsed first or if *abort became non-zero (another role gave up).
 // The waiting thread sleeps in the barrier (up to 0.2 ms per probe) instead
-// of spinning, so it does not take issue slots from the warps doing work.
+// of spinning, so it does not take issue slots from the warps doing work; the
+// clock is read after the first probe, off the path of a wait that succeeds.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns,
                                           volatile int* abort) {
-  if (mbar_try_wait(bar, parity)) return true;
-  uint64_t t0 = globaltimer_ns();
+  if (mbar_try_wait(bar, parity) || mbar_try_wait_hint(bar, parity, 200000u)) return true;
+  const uint64_t t0 = globaltimer_ns();
   while (true) {
     if (mbar_try_wait_hint(bar, parity, 200000u)) return true;
     if (*abort) return false;
