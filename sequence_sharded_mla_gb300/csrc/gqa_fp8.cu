@@ -70,6 +70,7 @@ constexpr int kMaxOwnPlan = 768;           // units that every CTA plans for its
 constexpr int kOwnPerThread = (kMaxOwnPlan + kThreads - 1) / kThreads;
 constexpr unsigned long long kTimeoutNs = 2000000000ull;
 constexpr float kTop = 12.0f;              // log2 of the largest weight at a new reference
+constexpr float kTopFirst = 10.0f;         // and at a piece's first, which grows more often
 constexpr float kMost = 15.0f;             // log2 of the largest weight that fits fp16
 constexpr float kNoRef = -1.0e38f;         // reference of a row that has seen nothing
 constexpr float kMinScale = 8.67361737988403547e-19f;   // 2^-60
@@ -176,7 +177,7 @@ __device__ __forceinline__ size_t out_row(const Desc& d, const Rows& x, int r) {
 struct Query {
   alignas(16) float qs[kMaxR];  // 1 / the row's query scale
   int lim[kMaxR];               // last position the row sees
-  int orow[kMaxR];              // its output row
+  alignas(16) int orow[kMaxR];              // its output row
 };
 
 struct Misc {
@@ -544,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------- the query, K Q^T
     const uint32_t id = idesc_e4m3_f32(kTok, S::kSCols, false, false);
     const uint64_t dk = sw128_desc(sSt, 16, 1024);
-    const uint32_t rows_of_all = d.B * d.q_len * d.H;
+    const int rows_of_all = d.B * d.q_len * d.H;
     int g = 0, pc = 0;
     while (ok && it.next(unit, t0, t1, whole, slot)) {
       const Rows x = make_rows(d, unit);
@@ -554,49 +555,57 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int buf = pc & 1;
       Query& query = misc->query[buf];
       if (pc >= 2 && !(ok = wait(&misc->q_empty[buf], ((pc >> 1) - 1) & 1))) break;
-      // 16 lanes a row, 8 values each; the loads of 16 rows are in flight together
+      // The rows come in by cp.async, half a row to each of the places of its
+      // two terms, and are split in place a row at a time.  The loops stay
+      // rolled: code that runs once a piece costs its own fetch (unrolled over
+      // 48 rows, 38000 cycles).
+      uint8_t* const sq = smem + S::kQ + buf * S::kQBuf;
 #pragma unroll 1
-      for (int r0 = 0; r0 < R; r0 += 16) {
-        const int c = lane & 15;
-        uint4 w[8];
-        int src[8];
+      for (int r = lane; r < R; r += 32) {
+        const int i = (x.r0 + r) / d.G;
+        const int src = (x.b * d.q_len + i) * d.H + x.kh * d.G + (x.r0 + r) - i * d.G;
+        query.orow[r] = x.so * rows_of_all + src;
+        query.lim[r] = d.causal && r < live ? L - qn + i : INT_MAX - 1;
+      }
+      __syncwarp();
+#pragma unroll 2
+      for (int r0 = 0; r0 < R; r0 += 2) {
+        const int r = r0 + (lane >> 4), c = lane & 15;
+        const bool there = r < live;
+        const size_t src = there ? (size_t)(query.orow[r] - x.so * rows_of_all) * kD + 8 * c : 0;
+        cp_async_16_zfill(smem_u32(sq + S::q_row(r, c >> 3) + 16 * (c & 7)), d.q + src, there);
+      }
+      cp_async_commit();
+      cp_async_wait_all();
+      __syncwarp();
+#pragma unroll 1
+      for (int r0 = 0; r0 < R; r0 += 8) {
+        uint2 w[8];
+        uint32_t mx[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          w[k] = *reinterpret_cast<const uint2*>(sq + S::q_row(r0 + k, lane >> 4) + 8 * (lane & 15));
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          mx[k] = __reduce_max_sync(0xffffffffu,
+                                    max(max(w[k].x & 0x7FFFu, (w[k].x >> 16) & 0x7FFFu),
+                                        max(w[k].y & 0x7FFFu, (w[k].y >> 16) & 0x7FFFu)));
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          const int r = r0 + 2 * k + (lane >> 4);
-          const int i = (x.r0 + r) / d.G;
-          src[k] = (x.b * d.q_len + i) * d.H + x.kh * d.G + (x.r0 + r) - i * d.G;
-          w[k] = make_uint4(0, 0, 0, 0);
-          if (r < live) w[k] = __ldg(reinterpret_cast<const uint4*>(d.q + (size_t)src[k] * kD) + c);
-          if (c == 0) {
-            query.orow[r] = (int)(x.so * rows_of_all) + src[k];
-            query.lim[r] = d.causal && r < live ? L - qn + i : INT_MAX - 1;
-          }
-        }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int r = r0 + 2 * k + (lane >> 4);
-          const uint32_t ww[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
-          uint32_t mx = 0;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) mx = max(mx, max(ww[e] & 0x7FFFu, (ww[e] >> 16) & 0x7FFFu));
-#pragma unroll
-          for (int o = 8; o > 0; o >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+          const int r = r0 + k;
           // s_r = 2^(134 - e) puts max|q| (exponent e) in [128, 256); clamped so
           // that it and its inverse are normal
-          const uint32_t e = min(max(mx >> 7, 8u), 254u);
+          const uint32_t e = min(max(mx[k] >> 7, 8u), 254u);
           const float sc = __uint_as_float((261u - e) << 23);
-          uint32_t sp[4];
-#pragma unroll
-          for (int h = 0; h < 4; ++h)
-            sp[h] = split_e4m3x2(__uint_as_float(ww[h] << 16) * sc,
-                                 __uint_as_float(ww[h] & 0xFFFF0000u) * sc);
-          uint8_t* dst = smem + S::kQ + buf * S::kQBuf + (((c >> 1) ^ (r & 7)) << 4) + (c & 1) * 8;
-          *reinterpret_cast<uint2*>(dst + S::q_row(r, 0)) =
-              make_uint2((sp[0] & 0xFFFFu) | (sp[1] << 16), (sp[2] & 0xFFFFu) | (sp[3] << 16));
-          *reinterpret_cast<uint2*>(dst + S::q_row(r, 1)) =
-              make_uint2((sp[0] >> 16) | (sp[1] & 0xFFFF0000u), (sp[2] >> 16) | (sp[3] & 0xFFFF0000u));
-          if (c == 0) {
-            if ((mx >> 7) == 255u) atomicOr(&misc->err, kErrQRange);
+          const uint32_t s0 = split_e4m3x2(__uint_as_float(w[k].x << 16) * sc,
+                                           __uint_as_float(w[k].x & 0xFFFF0000u) * sc);
+          const uint32_t s1 = split_e4m3x2(__uint_as_float(w[k].y << 16) * sc,
+                                           __uint_as_float(w[k].y & 0xFFFF0000u) * sc);
+          uint8_t* dst = sq + (((lane >> 2) ^ k) << 4) + (lane & 3) * 4;
+          *reinterpret_cast<uint32_t*>(dst + S::q_row(r, 0)) = __byte_perm(s0, s1, 0x5410);
+          *reinterpret_cast<uint32_t*>(dst + S::q_row(r, 1)) = __byte_perm(s0, s1, 0x7632);
+          if (lane == k) {
+            if ((mx[k] >> 7) == 255u) atomicOr(&misc->err, kErrQRange);
             query.qs[r] = __uint_as_float((e - 7u) << 23);
           }
         }
@@ -704,27 +713,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool scaled = __any_sync(0xffffffffu, fv != 1.0f);
         ok_s = __all_sync(0xffffffffu, ok_s && poll(&misc->s_full[sb], s_phase));
         // 16 rows' logits of this token in log2 units, with the V scale: into
-        // b (two rows each), less the references if asked for
-        auto logits = [&](int r0, const uint32_t (&sr)[S::kSplit ? 32 : 16], float2* b, bool less) {
+        // b (two rows each), less the references (or, less = 0, without)
+        auto logits = [&](int r0, const uint32_t (&sr)[S::kSplit ? 32 : 16], float2* b, float less) {
           const float4* q4 = reinterpret_cast<const float4*>(query.qs + r0);
           const float4* m4 = reinterpret_cast<const float4*>(ref + r0);
           const float2 c2 = make_float2(c, c), lv2 = make_float2(lv, lv);
+          const float2 less2 = make_float2(less, less);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const float4 q = q4[k];
-            float2 n0 = lv2, n1 = lv2;
-            if (less) {
-              const float4 m = m4[k];
-              n0 = add2(lv2, make_float2(m.x, m.y));
-              n1 = add2(lv2, make_float2(m.z, m.w));
-            }
+            const float4 q = q4[k], m = m4[k];
             float2 v0 = as_f2(sr[4 * k], sr[4 * k + 1]), v1 = as_f2(sr[4 * k + 2], sr[4 * k + 3]);
             if constexpr (S::kSplit) {
               v0 = add2(v0, as_f2(sr[16 + 4 * k], sr[17 + 4 * k]));
               v1 = add2(v1, as_f2(sr[18 + 4 * k], sr[19 + 4 * k]));
             }
-            b[2 * k] = fma2(mul2(v0, make_float2(q.x, q.y)), c2, n0);
-            b[2 * k + 1] = fma2(mul2(v1, make_float2(q.z, q.w)), c2, n1);
+            b[2 * k] = fma2(mul2(v0, make_float2(q.x, q.y)), c2, fma2(make_float2(m.x, m.y), less2, lv2));
+            b[2 * k + 1] =
+                fma2(mul2(v1, make_float2(q.z, q.w)), c2, fma2(make_float2(m.z, m.w), less2, lv2));
           }
           if (!full) {
 #pragma unroll
@@ -741,42 +746,46 @@ __global__ void __launch_bounds__(kThreads, 1)
           else tmem_ld16(a, sr);
         };
         float2 b[R / 2];
-        bool over = false;
-        auto all_logits = [&]() {
+        auto all_logits = [&](float less) {
           uint32_t sr[2][S::kSplit ? 32 : 16];
           load_s(0, sr[0]);
 #pragma unroll
           for (int r0 = 0; r0 < R; r0 += 16) {
             tmem_wait_ld();
             if (r0 + 16 < R) load_s(r0 + 16, sr[((r0 >> 4) + 1) & 1]);
-            logits(r0, sr[(r0 >> 4) & 1], b + r0 / 2, true);
+            logits(r0, sr[(r0 >> 4) & 1], b + r0 / 2, less);
           }
         };
-        if (ok_s) {
-          tc_fence_after();
-          all_logits();
+        if (ok_s) tc_fence_after();
+        bool move = first;                         // a piece's first tile has no references yet
+        if (!first) {
           float mx = -CUDART_INF_F;
+          if (ok_s) {
+            all_logits(1.0f);
 #pragma unroll
-          for (int k = 0; k < R / 2; ++k) mx = fmaxf(mx, fmaxf(b[k].x, b[k].y));
-          over = mx > kMost;
+            for (int k = 0; k < R / 2; ++k) mx = fmaxf(mx, fmaxf(b[k].x, b[k].y));
+          }
+          move = named_bar_or(kBarGroup + grp, kGroupThreads, mx > kMost || !ok_s);
         }
-        if (named_bar_or(kBarGroup + grp, kGroupThreads, over || !ok_s)) {
+        // A weight would pass 2^kMost: the logits without references, for new
+        // ones, then against those (one body for both: it runs seldom, and
+        // code that runs seldom costs its own fetch).
+        for (bool raw = true; move;) {
+          if (ok_s) all_logits(raw ? 0.0f : 1.0f);
+          if (!raw) break;
+          raw = false;
           // ---------------------------------------------- new references
           if (ok_s) {
-#pragma unroll 1
-            for (int r0 = 0; r0 < R; r0 += 16) {
-              uint32_t sr[S::kSplit ? 32 : 16];
-              float2 y[8];
-              load_s(r0, sr);
-              tmem_wait_ld();
-              logits(r0, sr, y, false);
+#pragma unroll
+            for (int r0 = 0; r0 < R; r0 += 32) {
               float mine = 0.0f;
 #pragma unroll
-              for (int k = 0; k < 16; ++k) {
-                const float mx = warp_max((k & 1) ? y[k >> 1].y : y[k >> 1].x);
+              for (int k = 0; k < 32 && r0 + k < R; ++k) {
+                const float2 v = b[(r0 + k) >> 1];
+                const float mx = warp_max((k & 1) ? v.y : v.x);
                 if (lane == k) mine = mx;
               }
-              if (lane < 16) misc->part[grp][quad][r0 + lane] = mine;
+              if (r0 + lane < R) misc->part[grp][quad][r0 + lane] = mine;
             }
           }
           if (named_bar_or(kBarGroup + grp, kGroupThreads, !ok_s)) {
@@ -789,8 +798,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int k = 1; k < 4; ++k) top = fmaxf(top, misc->part[grp][k][gtid]);
             const float old = -ref[gtid];
             up = top > old + kMost;
-            misc->f[grp][gtid] = up ? ex2_approx(old - (top - kTop)) : 1.0f;
-            if (up) ref[gtid] = kTop - top;
+            const float now = top - (first ? kTopFirst : kTop);
+            misc->f[grp][gtid] = up ? ex2_approx(old - now) : 1.0f;
+            if (up) ref[gtid] = -now;
           }
           const uint32_t ups = __ballot_sync(0xffffffffu, up);
           if (gtid < R && (lane & 15) == 0) misc->moved[grp][gtid >> 4] = (ups >> lane) & 0xFFFFu;
@@ -799,32 +809,34 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = false;
             break;
           }
+          if (first) continue;
+          tc_fence_after();
 #pragma unroll
           for (int r = 0; r < R / 2; ++r)
             l[r] = mul2(l[r], make_float2(misc->f[grp][2 * r], misc->f[grp][2 * r + 1]));
-          if (!first) {
-            tc_fence_after();
 #pragma unroll 1
-            for (int r0 = 0; r0 < R; r0 += 16) {
-              if (!misc->moved[grp][r0 >> 4]) continue;
-              uint32_t v[3][16];
-#pragma unroll
-              for (int term = 0; term < 3; ++term) tmem_ld16(tO + 3 * R * grp + R * term + r0, v[term]);
+          for (int r0 = 0; r0 < R; r0 += 16) {
+            if (!misc->moved[grp][r0 >> 4]) continue;
+            const float4* f4 = reinterpret_cast<const float4*>(misc->f[grp] + r0);
+#pragma unroll 1
+            for (int term = 0; term < 3; ++term) {
+              uint32_t v[16];
+              tmem_ld16(tO + 3 * R * grp + R * term + r0, v);
               tmem_wait_ld();
 #pragma unroll
-              for (int k = 0; k < 16; ++k) {
-                const float al = misc->f[grp][r0 + k];
-#pragma unroll
-                for (int term = 0; term < 3; ++term)
-                  v[term][k] = __float_as_uint(__uint_as_float(v[term][k]) * al);
+              for (int k = 0; k < 4; ++k) {
+                const float4 f = f4[k];
+                v[4 * k] = __float_as_uint(__uint_as_float(v[4 * k]) * f.x);
+                v[4 * k + 1] = __float_as_uint(__uint_as_float(v[4 * k + 1]) * f.y);
+                v[4 * k + 2] = __float_as_uint(__uint_as_float(v[4 * k + 2]) * f.z);
+                v[4 * k + 3] = __float_as_uint(__uint_as_float(v[4 * k + 3]) * f.w);
               }
-#pragma unroll
-              for (int term = 0; term < 3; ++term) tmem_st16(tO + 3 * R * grp + R * term + r0, v[term]);
+              tmem_st16(tO + 3 * R * grp + R * term + r0, v);
             }
-            tmem_wait_st();
           }
-          all_logits();
+          tmem_wait_st();
         }
+        if (!ok) break;
         // ------------------------------------------------------- weights
         tc_fence_before();                         // the logits are in registers
         __syncwarp();
@@ -981,13 +993,30 @@ __global__ void __launch_bounds__(kThreads, 1)
             o[k] = fmaf(a, (k & 3) == 0 ? f.x : (k & 3) == 1 ? f.y : (k & 3) == 2 ? f.z : f.w, o[k]);
           }
         }
+        if (nf != INT_MAX || r0 + 16 > x.live) {
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const int r = r0 + k;
-          if (r >= x.rows) break;
-          float v = query.lim[r] >= nf ? CUDART_NAN_F : o[k];
-          if (r >= x.live) v = 0.0f;
-          (whole ? p.out + (size_t)query.orow[r] * kD : p.ws_o + (sl * kRows + r) * kD)[dim] = v;
+          for (int k = 0; k < 16; ++k) {
+            if (query.lim[r0 + k] >= nf) o[k] = CUDART_NAN_F;
+            if (r0 + k >= x.live) o[k] = 0.0f;
+          }
+        }
+        const int n = x.rows - r0;
+        if (whole) {
+          const int4* o4 = reinterpret_cast<const int4*>(query.orow + r0);
+          float* dst = p.out + dim;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int4 at = o4[k];
+            if (4 * k < n) dst[(size_t)at.x * kD] = o[4 * k];
+            if (4 * k + 1 < n) dst[(size_t)at.y * kD] = o[4 * k + 1];
+            if (4 * k + 2 < n) dst[(size_t)at.z * kD] = o[4 * k + 2];
+            if (4 * k + 3 < n) dst[(size_t)at.w * kD] = o[4 * k + 3];
+          }
+        } else {
+          float* dst = p.ws_o + (sl * kRows + r0) * kD + dim;
+#pragma unroll
+          for (int k = 0; k < 16; ++k)
+            if (k < n) dst[k * kD] = o[k];
         }
       }
       // for the next piece
@@ -1001,7 +1030,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   // ---------------------------------------------------------------- teardown
-  if (warp == 0) cp_async_wait_all();
+  if (warp == 0) {
+    cp_async_commit();
+    cp_async_wait_all();
+  }
   tc_fence_before();
   __syncthreads();
   if (*abort_flag) {
