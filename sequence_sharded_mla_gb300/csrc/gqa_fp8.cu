@@ -36,8 +36,8 @@
 // piece.  The groups never wait for one another inside a piece.
 //
 // Warps: 0 and 3 producers (block table, TMA boxes of K or V, cp.async of the
-// tokens' scales); 1 loads and splits each piece's query rows, a piece ahead
-// of the softmax, and issues K Q^T; 2 issues V^T P^T; 4..7 and 8..11 the
+// tokens' scales); 1 loads and splits each piece's query rows but
+// the first's, a piece ahead of the softmax, and issues K Q^T; 2 issues V^T P^T; 4..7 and 8..11 the
 // softmax groups (TMEM lane quadrant = warp % 4), which write the outputs.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -75,10 +75,37 @@ constexpr float kMost = 15.0f;             // log2 of the largest weight that fi
 constexpr float kNoRef = -1.0e38f;         // reference of a row that has seen nothing
 constexpr float kMinScale = 8.67361737988403547e-19f;   // 2^-60
 
+// A divisor of numbers 0 <= n < 2^31 that is fixed for a call: n / d is (n +
+// the high word of n m) >> s with m = floor(2^32 (2^s - d) / d) + 1, s =
+// ceil(log2 d) (Granlund and Montgomery, 1994), a fifth of the instructions
+// of a division.
+struct Div {
+  int d;
+  uint32_t m;
+  int s;
+  __host__ __device__ operator int() const { return d; }
+};
+__device__ __forceinline__ int operator/(int n, const Div& v) {
+  return (int)((__umulhi((uint32_t)n, v.m) + (uint32_t)n) >> v.s);
+}
+__device__ __forceinline__ int operator%(int n, const Div& v) { return n - n / v * v.d; }
+
+Div make_div(int d) {
+  Div v{d, 0, 0};
+  while (v.s < 31 && (1u << v.s) < (uint32_t)d) ++v.s;
+  v.m = (uint32_t)((((1ull << v.s) - (unsigned)d) << 32) / (unsigned)d) + 1;
+  return v;
+}
+
 struct Desc {
-  int B, q_len, H, Hkv, G;
-  int rg, Gq;          // query rows per group, row groups per (request, KV head)
-  int num_shards, shard_first, n_out, layout, local, causal;
+  int B, q_len, H;
+  Div Hkv, G;
+  int rg;              // query rows per group
+  Div Gq;              // row groups per (request, KV head)
+  Div num_shards;
+  int shard_first;
+  Div n_out;
+  int layout, local, causal;
   int num_pages, max_pages, lg_block;
   int lg_run;          // log2 of the consecutive slots of a tile that share a scale
   int nv;              // page boxes per 64 slots: shards of a whole-request interleaved cache, else 1
@@ -117,12 +144,12 @@ struct Unit : Rows {
 
 __device__ __forceinline__ Rows make_rows(const Desc& d, int u) {
   Rows x;
-  x.r0 = u % d.Gq * d.rg;
   int t = u / d.Gq;
-  x.kh = t % d.Hkv;
-  t /= d.Hkv;
-  x.so = t % d.n_out;
-  x.b = t / d.n_out;
+  x.r0 = (u - t * d.Gq) * d.rg;
+  int v = t / d.Hkv;
+  x.kh = t - v * d.Hkv;
+  x.b = v / d.n_out;
+  x.so = v - x.b * d.n_out;
   x.rows = min(d.rg, d.q_len * d.G - x.r0);
   return x;
 }
@@ -142,7 +169,7 @@ __device__ __forceinline__ Unit make_unit(const Desc& d, int u) {
     n = L > x.s ? (L - 1 - x.s) / d.num_shards + 1 : 0;
     x.tiles = ceil_div(n, kTok);
   } else {
-    const int c = ceil_div(L, d.num_shards);
+    const int c = L / d.num_shards + (L % d.num_shards != 0);
     x.tstart = min(x.s * c, L);
     x.tend = min(x.tstart + c, L);
     n = x.tend - x.tstart;
@@ -169,7 +196,7 @@ __device__ __forceinline__ Slots make_slots(const Desc& d, const Unit& x) {
 }
 
 __device__ __forceinline__ size_t out_row(const Desc& d, const Rows& x, int r) {
-  const int i = (x.r0 + r) / d.G, h = x.kh * d.G + (x.r0 + r) % d.G;
+  const int i = (x.r0 + r) / d.G, h = x.kh * d.G + (x.r0 + r) - i * d.G;
   return (((size_t)x.so * d.B + x.b) * d.q_len + i) * d.H + h;
 }
 
@@ -385,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar(&misc->pv_done[g]), 1);
     }
     for (int k = 0; k < 2; ++k) {
-      mbar_init(bar(&misc->q_full[k]), 1);
+      mbar_init(bar(&misc->q_full[k]), 8);
       mbar_init(bar(&misc->q_empty[k]), 8);
     }
     mbar_init(bar(&misc->drain), 2);
@@ -470,6 +497,68 @@ __global__ void __launch_bounds__(kThreads, 1)
   int unit, t0, t1, slot;
   bool whole, ok = true;
 
+  // Rows [ra, rb) of a piece's query, by a warp: they come in by cp.async, half
+  // a row to each of the places of its two terms, and are split in place.  The
+  // loops stay rolled: code that runs once a piece costs its own fetch
+  // (unrolled over 48 rows, 38000 cycles).
+  auto split_query = [&](const Rows& x, int buf, int ra, int rb) {
+    const int L = max(d.seq_lens[x.b], 0);
+    const int qn = d.q_lens ? min(max(d.q_lens[x.b], 0), d.q_len) : d.q_len;
+    const int live = min(qn * d.G - x.r0, x.rows);
+    Query& query = misc->query[buf];
+    uint8_t* const sq = smem + S::kQ + buf * S::kQBuf;
+    const int first_src = (x.b * d.q_len) * d.H + x.kh * d.G + x.r0;
+    const int step = d.H - d.G;                  // between a position's heads and the next's
+#pragma unroll 2
+    for (int r0 = ra; r0 < rb; r0 += 2) {
+      const int r = r0 + (lane >> 4), c = lane & 15;
+      const int i = (x.r0 + r) / d.G, src = first_src + r + i * step;
+      const bool there = r < live;
+      cp_async_16_zfill(smem_u32(sq + S::q_row(r, c >> 3) + 16 * (c & 7)),
+                        d.q + (there ? (size_t)src * kD + 8 * c : 0), there);
+      if (c == 0) {
+        query.orow[r] = x.so * (d.B * d.q_len * d.H) + src;
+        query.lim[r] = d.causal && there ? L - qn + i : INT_MAX - 1;
+      }
+    }
+    cp_async_commit();
+    cp_async_wait_all();
+    __syncwarp();
+#pragma unroll 1
+    for (int r0 = ra; r0 < rb; r0 += 2) {
+      uint2 w[2];
+      uint32_t mx[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        w[k] = *reinterpret_cast<const uint2*>(sq + S::q_row(r0 + k, lane >> 4) + 8 * (lane & 15));
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        mx[k] = __reduce_max_sync(0xffffffffu,
+                                  max(max(w[k].x & 0x7FFFu, (w[k].x >> 16) & 0x7FFFu),
+                                      max(w[k].y & 0x7FFFu, (w[k].y >> 16) & 0x7FFFu)));
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        // s_r = 2^(134 - e) puts max|q| (exponent e) in [128, 256); clamped so
+        // that it and its inverse are normal
+        const uint32_t e = min(max(mx[k] >> 7, 8u), 254u);
+        const float sc = __uint_as_float((261u - e) << 23);
+        const uint32_t s0 = split_e4m3x2(__uint_as_float(w[k].x << 16) * sc,
+                                         __uint_as_float(w[k].x & 0xFFFF0000u) * sc);
+        const uint32_t s1 = split_e4m3x2(__uint_as_float(w[k].y << 16) * sc,
+                                         __uint_as_float(w[k].y & 0xFFFF0000u) * sc);
+        uint8_t* dst = sq + (((lane >> 2) ^ ((r0 + k) & 7)) << 4) + (lane & 3) * 4;
+        *reinterpret_cast<uint32_t*>(dst + S::q_row(r0 + k, 0)) = __byte_perm(s0, s1, 0x5410);
+        *reinterpret_cast<uint32_t*>(dst + S::q_row(r0 + k, 1)) = __byte_perm(s0, s1, 0x7632);
+        if (lane == k) {
+          if ((mx[k] >> 7) == 255u) atomicOr(&misc->err, kErrQRange);
+          query.qs[r0 + k] = __uint_as_float((e - 7u) << 23);
+        }
+      }
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+  };
+
   if (warp == 0 || warp == 3) {
     // ------------------------------------------------------------ producers
     // warp 0 loads K and the scales, warp 3 loads V: with 8 shards a
@@ -545,74 +634,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------- the query, K Q^T
     const uint32_t id = idesc_e4m3_f32(kTok, S::kSCols, false, false);
     const uint64_t dk = sw128_desc(sSt, 16, 1024);
-    const int rows_of_all = d.B * d.q_len * d.H;
     int g = 0, pc = 0;
     while (ok && it.next(unit, t0, t1, whole, slot)) {
-      const Rows x = make_rows(d, unit);
-      const int L = max(d.seq_lens[x.b], 0);
-      const int qn = d.q_lens ? min(max(d.q_lens[x.b], 0), d.q_len) : d.q_len;
-      const int live = min(qn * d.G - x.r0, x.rows);
       const int buf = pc & 1;
-      Query& query = misc->query[buf];
-      if (pc >= 2 && !(ok = wait(&misc->q_empty[buf], ((pc >> 1) - 1) & 1))) break;
-      // The rows come in by cp.async, half a row to each of the places of its
-      // two terms, and are split in place a row at a time.  The loops stay
-      // rolled: code that runs once a piece costs its own fetch (unrolled over
-      // 48 rows, 38000 cycles).
-      uint8_t* const sq = smem + S::kQ + buf * S::kQBuf;
-#pragma unroll 1
-      for (int r = lane; r < R; r += 32) {
-        const int i = (x.r0 + r) / d.G;
-        const int src = (x.b * d.q_len + i) * d.H + x.kh * d.G + (x.r0 + r) - i * d.G;
-        query.orow[r] = x.so * rows_of_all + src;
-        query.lim[r] = d.causal && r < live ? L - qn + i : INT_MAX - 1;
+      if (pc == 0) {
+        if (!(ok = wait(&misc->q_full[0], 0))) break;
+      } else {
+        const Rows x = make_rows(d, unit);
+        if (pc >= 2 && !(ok = wait(&misc->q_empty[buf], ((pc >> 1) - 1) & 1))) break;
+        split_query(x, buf, 0, R);
+        if (lane < 8) mbar_arrive(bar(&misc->q_full[buf]));
       }
-      __syncwarp();
-#pragma unroll 2
-      for (int r0 = 0; r0 < R; r0 += 2) {
-        const int r = r0 + (lane >> 4), c = lane & 15;
-        const bool there = r < live;
-        const size_t src = there ? (size_t)(query.orow[r] - x.so * rows_of_all) * kD + 8 * c : 0;
-        cp_async_16_zfill(smem_u32(sq + S::q_row(r, c >> 3) + 16 * (c & 7)), d.q + src, there);
-      }
-      cp_async_commit();
-      cp_async_wait_all();
-      __syncwarp();
-#pragma unroll 1
-      for (int r0 = 0; r0 < R; r0 += 8) {
-        uint2 w[8];
-        uint32_t mx[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          w[k] = *reinterpret_cast<const uint2*>(sq + S::q_row(r0 + k, lane >> 4) + 8 * (lane & 15));
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          mx[k] = __reduce_max_sync(0xffffffffu,
-                                    max(max(w[k].x & 0x7FFFu, (w[k].x >> 16) & 0x7FFFu),
-                                        max(w[k].y & 0x7FFFu, (w[k].y >> 16) & 0x7FFFu)));
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int r = r0 + k;
-          // s_r = 2^(134 - e) puts max|q| (exponent e) in [128, 256); clamped so
-          // that it and its inverse are normal
-          const uint32_t e = min(max(mx[k] >> 7, 8u), 254u);
-          const float sc = __uint_as_float((261u - e) << 23);
-          const uint32_t s0 = split_e4m3x2(__uint_as_float(w[k].x << 16) * sc,
-                                           __uint_as_float(w[k].x & 0xFFFF0000u) * sc);
-          const uint32_t s1 = split_e4m3x2(__uint_as_float(w[k].y << 16) * sc,
-                                           __uint_as_float(w[k].y & 0xFFFF0000u) * sc);
-          uint8_t* dst = sq + (((lane >> 2) ^ k) << 4) + (lane & 3) * 4;
-          *reinterpret_cast<uint32_t*>(dst + S::q_row(r, 0)) = __byte_perm(s0, s1, 0x5410);
-          *reinterpret_cast<uint32_t*>(dst + S::q_row(r, 1)) = __byte_perm(s0, s1, 0x7632);
-          if (lane == k) {
-            if ((mx[k] >> 7) == 255u) atomicOr(&misc->err, kErrQRange);
-            query.qs[r] = __uint_as_float((e - 7u) << 23);
-          }
-        }
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0 && !(p.withhold_query && pc == 0)) mbar_arrive(bar(&misc->q_full[buf]));
       const uint64_t dq = sw128_desc(sQ + buf * S::kQBuf, 16, 1024);
       for (int j = t0; j < t1; ++j, ++g) {
         const int st = g % kStages, round = g / kStages, sb = g % kSBufs, sr = g / kSBufs;
@@ -681,6 +713,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                             (kTok - 1) * slots.step;
       const Query& query = misc->query[pc & 1];
       int* nan_from = misc->nan_from[pc & 1];
+      if (pc == 0) {
+        split_query(x, 0, (warp - 4) * (R / 8), (warp - 3) * (R / 8));
+        if (lane == 0 && !p.withhold_query) mbar_arrive(bar(&misc->q_full[0]));
+      }
       // the end of the previous piece, or the kernel's start, has set the references
       ok = __all_sync(0xffffffffu, poll(&misc->q_full[pc & 1], (pc >> 1) & 1));
 
@@ -1288,13 +1324,13 @@ mla_status gqa_decode_partial_fp8(const void* q, const gqa_block_pages* cache,
   d.B = shape->batch;
   d.q_len = shape->q_len;
   d.H = shape->num_heads;
-  d.Hkv = shape->num_kv_heads;
-  d.G = d.H / d.Hkv;
+  d.Hkv = gqa8::make_div(shape->num_kv_heads);
+  d.G = gqa8::make_div(shape->num_heads / shape->num_kv_heads);
   d.rg = sp.rg;
-  d.Gq = sp.Gq;
-  d.num_shards = num_shards;
+  d.Gq = gqa8::make_div(sp.Gq);
+  d.num_shards = gqa8::make_div(num_shards);
   d.shard_first = shard_id == MLA_ALL_SHARDS ? 0 : shard_id;
-  d.n_out = shard_id == MLA_ALL_SHARDS ? num_shards : 1;
+  d.n_out = gqa8::make_div(shard_id == MLA_ALL_SHARDS ? num_shards : 1);
   d.layout = (layout & 1) ? kContiguous : kInterleaved;
   d.local = local;
   d.causal = shape->causal;
