@@ -46,6 +46,7 @@
 #include <algorithm>
 #include <climits>
 #include <cmath>
+#include <type_traits>
 
 #include "common.cuh"
 #include "host_util.h"
@@ -57,9 +58,8 @@ namespace gqa8 {
 
 constexpr int kD = 128;                    // head width
 constexpr int kTok = 128;                  // tokens of a tile
-constexpr int kHalf = kTok * kD;           // 16384 bytes: K or V of a tile
+constexpr int kStageBytes = kTok * kD;     // 16384: K or V of a tile
 constexpr int kMaxStages = 6, kSBufs = 4;
-constexpr int kStageBytes = 2 * kHalf;
 constexpr int kThreads = 384;
 constexpr int kGroupThreads = 128;
 constexpr uint32_t kBarAll = 1, kBarGroup = 2;   // group g: kBarGroup + g
@@ -208,7 +208,7 @@ struct Query {
 };
 
 struct Misc {
-  uint64_t k_full[kMaxStages], v_full[kMaxStages], kv_empty[kMaxStages];
+  uint64_t k_full[kMaxStages], k_empty[kMaxStages], v_full[kMaxStages], v_empty[kMaxStages];
   uint64_t s_full[kSBufs], s_empty[kSBufs], p_full[2], pv_done[2];
   uint64_t q_full[2], q_empty[2], drain;
   uint32_t tmem_base;
@@ -245,13 +245,17 @@ __device__ __forceinline__ int4 make_record(const int* prefix, int u, int lo, in
   return r;
 }
 
-// Stages: what fits beside the weights.  A stage lives for its load, the
-// logits, the softmax and the P V of its tile, so more of them hide more of
-// that chain.  Two S buffers per group, so that a tile's logits are there when
-// the group comes back from the one before.
+// Stages: what fits beside the weights and the queries.  A tile's V is held
+// until its P V; where fewer than six of both fit, K is let go after the
+// logits, has fewer of them, and the scales come with V (9-token verify over 8
+// heads 136 -> 123 us; the same at R = 16: 132 -> 137 us, as the logits then
+// wait for V).  Two S buffers per group, so that a tile's logits are there
+// when the group comes back from the one before.
 template <int R>
 struct Smem {
-  static constexpr int kStages = R == 16 ? 6 : R == 32 ? 5 : 4;
+  static constexpr bool kEarlyK = R > 16;
+  static constexpr int kKStages = kEarlyK ? 4 : 6;
+  static constexpr int kVStages = R == 48 ? 5 : 6;
   // The query's two terms side by side as 2R columns of one MMA chain, added
   // by the softmax, or (no columns left) as two chains into the same R.  Half
   // the MMAs to issue, about 100 cycles each, against an addition per logit:
@@ -271,8 +275,9 @@ struct Smem {
   static constexpr int kP = 2 * kQBuf;                      // [2 groups][3][R / 16][128 tokens][16]
   static constexpr int kPBlock = 16 * kTok;
   static constexpr int kPGroup = 3 * R * kTok;
-  static constexpr int kStage = (kP + 2 * kPGroup + 1023) & ~1023;
-  static constexpr int kMisc = kStage + kStages * kStageBytes;
+  static constexpr int kK = (kP + 2 * kPGroup + 1023) & ~1023;
+  static constexpr int kV = kK + kKStages * kStageBytes;
+  static constexpr int kMisc = kV + kVStages * kStageBytes;
   static constexpr int kBytes = kMisc + (int)sizeof(Misc) + 1024;   // + alignment slack
   static_assert(kBytes <= 232448, "shared memory budget");
 };
@@ -375,14 +380,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     gqa_fp8_partial_kernel(const __grid_constant__ CUtensorMap tm_k,
                            const __grid_constant__ CUtensorMap tm_v, Params p) {
   using S = Smem<R>;
-  constexpr int kStages = S::kStages;
+  constexpr int kKStages = S::kKStages, kVStages = S::kVStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   Misc* misc = reinterpret_cast<Misc*>(smem + S::kMisc);
   const Desc& d = p.d;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t sQ = smem_u32(smem + S::kQ), sP = smem_u32(smem + S::kP);
-  const uint32_t sSt = smem_u32(smem + S::kStage);
+  const uint32_t sK = smem_u32(smem + S::kK), sV = smem_u32(smem + S::kV);
   auto bar = [&](const uint64_t* b) { return smem_u32(b); };
   volatile int* abort_flag = &misc->abort;
   const uint64_t tmo = p.timeout_ns;
@@ -398,10 +403,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
 
   if (threadIdx.x == 0) {
-    for (int st = 0; st < kStages; ++st) {
-      mbar_init(bar(&misc->k_full[st]), 1 + 32);   // expect_tx + one cp.async arrival per lane
-      mbar_init(bar(&misc->v_full[st]), 1);
-      mbar_init(bar(&misc->kv_empty[st]), 1);
+    for (int st = 0; st < kMaxStages; ++st) {
+      // expect_tx, and one cp.async arrival per lane of the producer of the scales
+      mbar_init(bar(&misc->k_full[st]), S::kEarlyK ? 1 : 1 + 32);
+      mbar_init(bar(&misc->v_full[st]), S::kEarlyK ? 1 + 32 : 1);
+      mbar_init(bar(&misc->k_empty[st]), 1);
+      mbar_init(bar(&misc->v_empty[st]), 1);
     }
     for (int k = 0; k < kSBufs; ++k) {
       mbar_init(bar(&misc->s_full[k]), 1);
@@ -492,21 +499,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   PieceIter it;
   it.init_warp(prefix, p.units, lo, hi, kUnitCost, lane);
-  int armed[kStages];
-  for (int st = 0; st < kStages; ++st) armed[st] = -1;
+  int armed[kMaxStages];                         // the round a producer last filled a stage in
+  for (int st = 0; st < kMaxStages; ++st) armed[st] = -1;
   int unit, t0, t1, slot;
   bool whole, ok = true;
 
   // Rows [ra, rb) of a piece's query, by a warp: they come in by cp.async, half
-  // a row to each of the places of its two terms, and are split in place.  The
-  // loops stay rolled: code that runs once a piece costs its own fetch
-  // (unrolled over 48 rows, 38000 cycles).
-  auto split_query = [&](const Rows& x, int buf, int ra, int rb) {
+  // a row to each of the places of its two terms, and are split in place, a few
+  // at a time.  The loops stay rolled: code that runs once a piece costs its
+  // own fetch (unrolled over 48 rows, 38000 cycles).
+  auto fetch_query = [&](const Rows& x, int buf, int ra, int rb) {
     const int L = max(d.seq_lens[x.b], 0);
     const int qn = d.q_lens ? min(max(d.q_lens[x.b], 0), d.q_len) : d.q_len;
     const int live = min(qn * d.G - x.r0, x.rows);
     Query& query = misc->query[buf];
-    uint8_t* const sq = smem + S::kQ + buf * S::kQBuf;
     const int first_src = (x.b * d.q_len) * d.H + x.kh * d.G + x.r0;
     const int step = d.H - d.G;                  // between a position's heads and the next's
 #pragma unroll 2
@@ -514,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int r = r0 + (lane >> 4), c = lane & 15;
       const int i = (x.r0 + r) / d.G, src = first_src + r + i * step;
       const bool there = r < live;
-      cp_async_16_zfill(smem_u32(sq + S::q_row(r, c >> 3) + 16 * (c & 7)),
+      cp_async_16_zfill(sQ + buf * S::kQBuf + S::q_row(r, c >> 3) + 16 * (c & 7),
                         d.q + (there ? (size_t)src * kD + 8 * c : 0), there);
       if (c == 0) {
         query.orow[r] = x.so * (d.B * d.q_len * d.H) + src;
@@ -522,38 +528,40 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     cp_async_commit();
+  };
+  auto split_query = [&](int buf, int r0, auto rows) {   // rows r0 .. r0 + n - 1
+    constexpr int n = decltype(rows)::value;
     cp_async_wait_all();
     __syncwarp();
-#pragma unroll 1
-    for (int r0 = ra; r0 < rb; r0 += 2) {
-      uint2 w[2];
-      uint32_t mx[2];
+    uint8_t* const sq = smem + S::kQ + buf * S::kQBuf;
+    uint2 w[n];
+    uint32_t mx[n];
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
-        w[k] = *reinterpret_cast<const uint2*>(sq + S::q_row(r0 + k, lane >> 4) + 8 * (lane & 15));
+    for (int k = 0; k < n; ++k)
+      w[k] = *reinterpret_cast<const uint2*>(sq + S::q_row(r0 + k, lane >> 4) + 8 * (lane & 15));
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
-        mx[k] = __reduce_max_sync(0xffffffffu,
-                                  max(max(w[k].x & 0x7FFFu, (w[k].x >> 16) & 0x7FFFu),
-                                      max(w[k].y & 0x7FFFu, (w[k].y >> 16) & 0x7FFFu)));
+    for (int k = 0; k < n; ++k)
+      mx[k] = __reduce_max_sync(0xffffffffu,
+                                max(max(w[k].x & 0x7FFFu, (w[k].x >> 16) & 0x7FFFu),
+                                    max(w[k].y & 0x7FFFu, (w[k].y >> 16) & 0x7FFFu)));
+    uint32_t mine = 0;
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        // s_r = 2^(134 - e) puts max|q| (exponent e) in [128, 256); clamped so
-        // that it and its inverse are normal
-        const uint32_t e = min(max(mx[k] >> 7, 8u), 254u);
-        const float sc = __uint_as_float((261u - e) << 23);
-        const uint32_t s0 = split_e4m3x2(__uint_as_float(w[k].x << 16) * sc,
-                                         __uint_as_float(w[k].x & 0xFFFF0000u) * sc);
-        const uint32_t s1 = split_e4m3x2(__uint_as_float(w[k].y << 16) * sc,
-                                         __uint_as_float(w[k].y & 0xFFFF0000u) * sc);
-        uint8_t* dst = sq + (((lane >> 2) ^ ((r0 + k) & 7)) << 4) + (lane & 3) * 4;
-        *reinterpret_cast<uint32_t*>(dst + S::q_row(r0 + k, 0)) = __byte_perm(s0, s1, 0x5410);
-        *reinterpret_cast<uint32_t*>(dst + S::q_row(r0 + k, 1)) = __byte_perm(s0, s1, 0x7632);
-        if (lane == k) {
-          if ((mx[k] >> 7) == 255u) atomicOr(&misc->err, kErrQRange);
-          query.qs[r0 + k] = __uint_as_float((e - 7u) << 23);
-        }
-      }
+    for (int k = 0; k < n; ++k) {
+      // s_r = 2^(134 - e) puts max|q| (exponent e) in [128, 256); clamped so
+      // that it and its inverse are normal
+      const float sc = __uint_as_float((261u - min(max(mx[k] >> 7, 8u), 254u)) << 23);
+      const uint32_t s0 = split_e4m3x2(__uint_as_float(w[k].x << 16) * sc,
+                                       __uint_as_float(w[k].x & 0xFFFF0000u) * sc);
+      const uint32_t s1 = split_e4m3x2(__uint_as_float(w[k].y << 16) * sc,
+                                       __uint_as_float(w[k].y & 0xFFFF0000u) * sc);
+      uint8_t* dst = sq + (((lane >> 2) ^ ((r0 + k) & 7)) << 4) + (lane & 3) * 4;
+      *reinterpret_cast<uint32_t*>(dst + S::q_row(r0 + k, 0)) = __byte_perm(s0, s1, 0x5410);
+      *reinterpret_cast<uint32_t*>(dst + S::q_row(r0 + k, 1)) = __byte_perm(s0, s1, 0x7632);
+      if (lane == k) mine = mx[k] >> 7;
+    }
+    if (lane < n) {
+      if (mine == 255u) atomicOr(&misc->err, kErrQRange);
+      misc->query[buf].qs[r0 + lane] = __uint_as_float((min(max(mine, 8u), 254u) - 7u) << 23);
     }
     fence_proxy_async_smem();
     __syncwarp();
@@ -561,7 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 0 || warp == 3) {
     // ------------------------------------------------------------ producers
-    // warp 0 loads K and the scales, warp 3 loads V: with 8 shards a
+    // warp 0 loads K, warp 3 loads V and the scales: with 8 shards a
     // tile is 2 x 16 boxes of 1 KB, and one warp that issued all of them
     // bounded the kernel (1 GB over 8 shards 320 us, two warps XXX us)
     const bool is_v = warp == 3;
@@ -582,10 +590,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int lg_rp = 31 - __clz(rp);
     const CUtensorMap* tm = is_v ? &tm_v : &tm_k;
     const uint64_t* full_bars = is_v ? misc->v_full : misc->k_full;
-    const uint32_t dst0 = sSt + (is_v ? kHalf : 0);
+    const uint64_t* empty_bars = is_v ? misc->v_empty : misc->k_empty;
+    const int stages = is_v ? kVStages : kKStages;
+    const uint32_t dst0 = is_v ? sV : sK;
     const int lg_sub = 6 - d.lg_block;           // scales per page and head
     const int runs = kTok >> d.lg_run;
-    int g = 0;
+    int st = 0, round = 0;
     while (ok && it.next(unit, t0, t1, whole, slot)) {
       const Unit x = make_unit(d, unit);
       const int32_t* bt = d.block_table + (size_t)x.b * d.max_pages;
@@ -595,8 +605,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         return (lane < nb && idx < x.npages && idx < d.max_pages) ? __ldg(bt + idx) : -1;
       };
       int next = entry(t0);
-      for (int j = t0; j < t1; ++j, ++g) {
-        const int st = g % kStages, round = g / kStages;
+      for (int j = t0; j < t1; ++j) {
         int page = next;
         if (j + 1 < t1) next = entry(j + 1);
         const bool there = page >= 0 && page < d.num_pages;
@@ -604,17 +613,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane < nb && x.p0 + j * nb + lane < x.npages) atomicOr(&misc->err, kErrBadPage);
           page = d.num_pages;                    // out of the map: TMA fills zeros
         }
-        if (round >= 1 && !(ok = wait(&misc->kv_empty[st], (round - 1) & 1))) break;
+        if (round >= 1 && !(ok = wait(&empty_bars[st], (round - 1) & 1))) break;
         const uint32_t full = bar(&full_bars[st]);
         if (lane == 0) {
-          mbar_arrive_expect_tx(full, kHalf);
-          armed[st] = g;
+          mbar_arrive_expect_tx(full, kStageBytes);
+          armed[st] = round;
         }
         __syncwarp();
         if (lane < nb)
           tma_load_3d(dst0 + st * kStageBytes + lane * (rp * kD), tm, full, 0, 0,
                       (page * kPage + res) * d.Hkv + x.kh);
-        for (int h = 0; !is_v && h < runs; h += 32) {
+        for (int h = 0; is_v == S::kEarlyK && h < runs; h += 32) {
           const int e = h + lane, a = min(e << d.lg_run, kTok - 1);
           const int pg = __shfl_sync(0xffffffffu, page, a >> lg_rp);
           const int row = res + (a & (rp - 1)) * d.nv;
@@ -626,29 +635,33 @@ __global__ void __launch_bounds__(kThreads, 1)
             cp_async_4_zfill(smem_u32(&misc->vsc[st][e]), d.vs + si, ok_pg);
           }
         }
-        if (!is_v) cp_async_mbar_arrive_noinc(full);
+        if (is_v == S::kEarlyK) cp_async_mbar_arrive_noinc(full);
         __syncwarp();
+        if (++st == stages) {
+          st = 0;
+          ++round;
+        }
       }
     }
   } else if (warp == 1) {
     // ------------------------------------------------- the query, K Q^T
     const uint32_t id = idesc_e4m3_f32(kTok, S::kSCols, false, false);
-    const uint64_t dk = sw128_desc(sSt, 16, 1024);
-    int g = 0, pc = 0;
+    const uint64_t dk = sw128_desc(sK, 16, 1024);
+    int g = 0, pc = 0, st = 0, phase = 0;
     while (ok && it.next(unit, t0, t1, whole, slot)) {
       const int buf = pc & 1;
       if (pc == 0) {
         if (!(ok = wait(&misc->q_full[0], 0))) break;
       } else {
-        const Rows x = make_rows(d, unit);
         if (pc >= 2 && !(ok = wait(&misc->q_empty[buf], ((pc >> 1) - 1) & 1))) break;
-        split_query(x, buf, 0, R);
+        fetch_query(make_rows(d, unit), buf, 0, R);
+        for (int r0 = 0; r0 < R; r0 += 4) split_query(buf, r0, std::integral_constant<int, 4>());
         if (lane < 8) mbar_arrive(bar(&misc->q_full[buf]));
       }
       const uint64_t dq = sw128_desc(sQ + buf * S::kQBuf, 16, 1024);
       for (int j = t0; j < t1; ++j, ++g) {
-        const int st = g % kStages, round = g / kStages, sb = g % kSBufs, sr = g / kSBufs;
-        if (!(ok = wait(&misc->k_full[st], round & 1))) break;
+        const int sb = g % kSBufs, sr = g / kSBufs;
+        if (!(ok = wait(&misc->k_full[st], phase))) break;
         if (sr >= 1 && !(ok = wait(&misc->s_empty[sb], (sr - 1) & 1))) break;
         tc_fence_after();
         if (lane == 0) {
@@ -658,20 +671,26 @@ __global__ void __launch_bounds__(kThreads, 1)
             mma_e4m3_ss(tmem + S::kSCols * sb, dk + off + ((32 * (k & 3)) >> 4),
                         dq + (((k >> 2) * R * kD + 32 * (k & 3)) >> 4), id, k != 0);
           mma_commit(bar(&misc->s_full[sb]));
+          if (S::kEarlyK) mma_commit(bar(&misc->k_empty[st]));
         }
         __syncwarp();
+        if (++st == kKStages) {
+          st = 0;
+          phase ^= 1;
+        }
       }
       ++pc;
     }
   } else if (warp == 2) {
     // ------------------------------------------------------------ V^T P^T
     const uint32_t id = idesc_e4m3_e5m2_f32(kD, 3 * R, true, true);
-    const uint64_t dv = sw128_desc(sSt + kHalf, 16, 1024);
-    int g = 0;
+    const uint64_t dv = sw128_desc(sV, 16, 1024);
+    int g = 0, st = 0, phase = 0;
     while (ok && it.next(unit, t0, t1, whole, slot)) {
       for (int j = t0; j < t1; ++j, ++g) {
-        const int st = g % kStages, grp = g & 1, gr = g >> 1;
-        if (!(ok = wait(&misc->v_full[st], (g / kStages) & 1))) break;
+        const int grp = g & 1, gr = g >> 1;
+        // with kEarlyK the softmax has waited for V
+        if (!S::kEarlyK && !(ok = wait(&misc->v_full[st], phase))) break;
         if (!(ok = wait(&misc->p_full[grp], gr & 1))) break;
         tc_fence_after();
         if (lane == 0) {
@@ -682,10 +701,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int k = 0; k < 4; ++k)   // 32 tokens each
             mma_e4m3_ss(tmem + S::kColO + 3 * R * grp, dv + off + ((k * 4 * 1024) >> 4),
                         dp + ((k * 32 * 16) >> 4), id, (j >= t0 + 2 || k != 0) ? 1u : 0u);
-          mma_commit(bar(&misc->kv_empty[st]));
+          mma_commit(bar(&misc->v_empty[st]));
+          if (!S::kEarlyK) mma_commit(bar(&misc->k_empty[st]));
           mma_commit(bar(&misc->pv_done[grp]));
         }
         __syncwarp();
+        if (++st == kVStages) {
+          st = 0;
+          phase ^= 1;
+        }
       }
     }
   } else {
@@ -714,7 +738,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Query& query = misc->query[pc & 1];
       int* nan_from = misc->nan_from[pc & 1];
       if (pc == 0) {
-        split_query(x, 0, (warp - 4) * (R / 8), (warp - 3) * (R / 8));
+        const int first_row = 2 * (warp - 4);
+        for (int r0 = first_row; r0 < R; r0 += 16) fetch_query(x, 0, r0, r0 + 2);
+#pragma unroll 1
+        for (int r0 = first_row; r0 < R; r0 += 16)
+          split_query(0, r0, std::integral_constant<int, 2>());
         if (lane == 0 && !p.withhold_query) mbar_arrive(bar(&misc->q_full[0]));
       }
       // the end of the previous piece, or the kernel's start, has set the references
@@ -731,7 +759,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int tok0 = slots.base + j * kTok * slots.step, t = tok0 + gtid * slots.step;
         const bool full = tok0 >= x.tstart && tok0 <= last_full;
         const bool valid = full || (t >= x.tstart && t < x.tend);
-        bool ok_s = ok && poll(&misc->k_full[st], phase);
+        bool ok_s = ok && poll(S::kEarlyK ? &misc->v_full[st] : &misc->k_full[st], phase);
         float c = 0.0f, lv = 0.0f, inv = 0.0f, fv = 1.0f;
         if (ok_s && valid) {
           c = misc->ksc[st][gtid >> d.lg_run] * d.scale_log2;
@@ -913,14 +941,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           *reinterpret_cast<uint4*>(pb + 2 * R * kTok) = make_uint4(w2[0], w2[1], w2[2], w2[3]);
         }
         if (!full) {
-          // V rows of slots without a token become zeros; a NaN code of a token
-          // that not every row sees is taken out too and comes back in the
-          // epilogue for the rows that see it (rows see a prefix)
-          if (!__all_sync(0xffffffffu, poll(&misc->v_full[st], phase))) {
+          if (!S::kEarlyK && !__all_sync(0xffffffffu, poll(&misc->v_full[st], phase))) {
             ok = false;
             continue;
           }
-          uint8_t* vt = smem + S::kStage + st * kStageBytes + kHalf;
+          // V rows of slots without a token become zeros; a NaN code of a token
+          // that not every row sees is taken out too and comes back in the
+          // epilogue for the rows that see it (rows see a prefix)
+          uint8_t* vt = smem + S::kV + st * kStageBytes;
           for (int e = gtid; e < kTok * (kD / 16); e += kGroupThreads) {
             const int a = e >> 3, u = e & 7;
             const int ta = tok0 + a * slots.step;
@@ -951,8 +979,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(&misc->p_full[grp]));
         st += 2;
-        if (st >= kStages) {
-          st -= kStages;
+        if (st >= kVStages) {
+          st -= kVStages;
           phase ^= 1;
         }
         ++gr;
@@ -1066,7 +1094,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   // ---------------------------------------------------------------- teardown
-  if (warp == 0) {
+  if (warp == 0 || warp == 3) {
     cp_async_commit();
     cp_async_wait_all();
   }
@@ -1080,10 +1108,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_wait(bar(&misc->drain), 0, kDrainNs, &never);
     }
     if ((warp == 0 || warp == 3) && lane == 0)
-      for (int st = 0; st < kStages; ++st)
+      for (int st = 0; st < kMaxStages; ++st)
         if (armed[st] >= 0)
-          mbar_wait(bar(warp == 0 ? &misc->k_full[st] : &misc->v_full[st]),
-                    (armed[st] / kStages) & 1, kDrainNs, &never);
+          mbar_wait(bar(warp == 0 ? &misc->k_full[st] : &misc->v_full[st]), armed[st] & 1,
+                    kDrainNs, &never);
     tc_fence_before();
     __syncthreads();
   }
