@@ -7,7 +7,8 @@
 // with K_t, V_t the codes' values and sk, sv the scales of t's block.
 //
 // Work unit: (request, shard, KV head, group of up to R query rows), R = 16,
-// 32 or 48 rows (of the KV head's q_len * G, position by position).  Persistent CTAs walk a stream-K list of 128-token tiles.
+// 32 or 48 rows (of the KV head's q_len * G, position by position).
+// Persistent CTAs walk a stream-K list of 128-token tiles.
 // The kernel is bound by the cache's bytes as long as it feeds the tensor
 // cores from what TMA brings in, so nothing of the cache is expanded: both
 // MMAs take K and V as e4m3 codes from shared memory, as their 128-row A
@@ -1241,9 +1242,12 @@ bool shards_ok(int num_shards, int shard_id) {
          (shard_id == MLA_ALL_SHARDS || (shard_id >= 0 && shard_id < num_shards));
 }
 
-// Query rows per work unit: the smallest tile that holds a KV head's q_len * G
-// rows of a request, 48 at most; more rows go to several groups of even size,
-// in the smallest tile that holds those.
+// Query rows per work unit: all of a KV head's q_len * G rows of a request up
+// to 48, in the smallest tile that holds them; more rows go to groups of even
+// size, 32 at most.  16 requests x 6400 tokens x 4 heads, us with groups of up
+// to 48 and 32 rows: 36 rows 47 and 55, 48 rows 47 and 55, 64 rows 57 and 57,
+// 72 rows 77 and 79, 96 rows 77 and 77, 126 rows 107 and 100; a ragged 9-token
+// verify of up to 72 rows 120 and 111.
 struct Split {
   int R, rg, Gq, units;
 };
@@ -1251,7 +1255,7 @@ struct Split {
 Split split_for(const gqa_shape* s, int num_shards, int shard_id) {
   const int n = s->q_len * (s->num_heads / s->num_kv_heads);
   Split x;
-  x.Gq = ceil_div(n, 48);
+  x.Gq = n <= 48 ? 1 : ceil_div(n, 32);
   x.rg = ceil_div(n, x.Gq);
   x.R = ceil_div(x.rg, 16) * 16;
   x.units = s->batch * (shard_id == MLA_ALL_SHARDS ? num_shards : 1) * s->num_kv_heads * x.Gq;
