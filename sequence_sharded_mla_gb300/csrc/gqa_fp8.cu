@@ -112,6 +112,7 @@ struct Desc {
   int nv;              // page boxes per 64 slots: shards of a whole-request interleaved cache, else 1
   float scale_log2;
   const uint16_t* q;
+  const uint8_t *k, *v;
   const float *ks, *vs;
   const int32_t *block_table, *seq_lens, *q_lens;
 };
@@ -405,9 +406,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int st = 0; st < kMaxStages; ++st) {
-      // expect_tx, and one cp.async arrival per lane of the producer of the scales
-      mbar_init(bar(&misc->k_full[st]), S::kEarlyK ? 1 : 1 + 32);
-      mbar_init(bar(&misc->v_full[st]), S::kEarlyK ? 1 + 32 : 1);
+      // expect_tx, and one cp.async arrival per lane
+      mbar_init(bar(&misc->k_full[st]), 1 + 32);
+      mbar_init(bar(&misc->v_full[st]), 1 + 32);
       mbar_init(bar(&misc->k_empty[st]), 1);
       mbar_init(bar(&misc->v_empty[st]), 1);
     }
@@ -522,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int i = (x.r0 + r) / d.G, src = first_src + r + i * step;
       const bool there = r < live;
       cp_async_16_zfill(sQ + buf * S::kQBuf + S::q_row(r, c >> 3) + 16 * (c & 7),
-                        d.q + (there ? (size_t)src * kD + 8 * c : 0), there);
+                        d.q + (there ? (size_t)src * kD + 8 * c : 0), there ? 16 : 0);
       if (c == 0) {
         query.orow[r] = x.so * (d.B * d.q_len * d.H) + src;
         query.lim[r] = d.causal && there ? L - qn + i : INT_MAX - 1;
@@ -595,6 +596,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int stages = is_v ? kVStages : kKStages;
     const uint32_t dst0 = is_v ? sV : sK;
     const int lg_sub = 6 - d.lg_block;           // scales per page and head
+    // 8 shards: 8 rows, 1 KB, of a page.  A box that small costs TMA about 64
+    // cycles, 32 of them a tile more than the tile's share of HBM; cp.async
+    // takes 8 lanes a row (1M tokens x 8 heads, 422 -> XXX us).
+    const bool by_row = d.nv == 8;
+    const size_t page_bytes = (size_t)kPage * d.Hkv * kD;
+    const uint8_t* row_src = (is_v ? d.v : d.k) + 16 * (lane & 7);
+    const uint32_t row_dst0 = (lane >> 3) * 128 + (((lane & 7) ^ (lane >> 3)) << 4);
+    const uint32_t row_dst1 = row_dst0 + 4 * 128 - 2 * (row_dst0 & 64) + 64;   // row + 4, chunk ^ 4
     const int runs = kTok >> d.lg_run;
     int st = 0, round = 0;
     while (ok && it.next(unit, t0, t1, whole, slot)) {
@@ -616,14 +625,38 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (round >= 1 && !(ok = wait(&empty_bars[st], (round - 1) & 1))) break;
         const uint32_t full = bar(&full_bars[st]);
-        if (lane == 0) {
-          mbar_arrive_expect_tx(full, kStageBytes);
-          armed[st] = round;
+        const uint32_t dst = dst0 + st * kStageBytes;
+        if (by_row) {
+          if (lane == 0) mbar_arrive(full);
+          const uint8_t* src = row_src + (size_t)((res + 8 * (lane >> 3)) * d.Hkv + x.kh) * kD;
+          const size_t off = there ? (size_t)page * page_bytes : 0;
+          const uint32_t off_lo = (uint32_t)off, off_hi = (uint32_t)(off >> 32), bytes = there ? 16 : 0;
+          const int step = 32 * d.Hkv * kD;
+#pragma unroll
+          for (int b0 = 0; b0 < 16; b0 += 8) {
+            uint32_t lo[8], hi[8], s[8];
+#pragma unroll
+            for (int b = 0; b < 8; ++b) {
+              lo[b] = __shfl_sync(0xffffffffu, off_lo, b0 + b);
+              hi[b] = __shfl_sync(0xffffffffu, off_hi, b0 + b);
+              s[b] = __shfl_sync(0xffffffffu, bytes, b0 + b);
+            }
+#pragma unroll
+            for (int b = 0; b < 8; ++b) {
+              const uint8_t* from = src + (((size_t)hi[b] << 32) | lo[b]);
+              cp_async_16_zfill(dst + (b0 + b) * 1024 + row_dst0, from, s[b]);
+              cp_async_16_zfill(dst + (b0 + b) * 1024 + row_dst1, from + step, s[b]);
+            }
+          }
+        } else {
+          if (lane == 0) {
+            mbar_arrive_expect_tx(full, kStageBytes);
+            armed[st] = round;
+          }
+          __syncwarp();
+          if (lane < nb)
+            tma_load_3d(dst + lane * (rp * kD), tm, full, 0, 0, (page * kPage + res) * d.Hkv + x.kh);
         }
-        __syncwarp();
-        if (lane < nb)
-          tma_load_3d(dst0 + st * kStageBytes + lane * (rp * kD), tm, full, 0, 0,
-                      (page * kPage + res) * d.Hkv + x.kh);
         for (int h = 0; is_v == S::kEarlyK && h < runs; h += 32) {
           const int e = h + lane, a = min(e << d.lg_run, kTok - 1);
           const int pg = __shfl_sync(0xffffffffu, page, a >> lg_rp);
@@ -636,7 +669,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             cp_async_4_zfill(smem_u32(&misc->vsc[st][e]), d.vs + si, ok_pg);
           }
         }
-        if (is_v == S::kEarlyK) cp_async_mbar_arrive_noinc(full);
+        cp_async_mbar_arrive_noinc(full);
         __syncwarp();
         if (++st == stages) {
           st = 0;
@@ -663,6 +696,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = t0; j < t1; ++j, ++g) {
         const int sb = g % kSBufs, sr = g / kSBufs;
         if (!(ok = wait(&misc->k_full[st], phase))) break;
+        if (d.nv == 8) fence_proxy_async_smem();   // K came by cp.async
         if (sr >= 1 && !(ok = wait(&misc->s_empty[sb], (sr - 1) & 1))) break;
         tc_fence_after();
         if (lane == 0) {
@@ -690,9 +724,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (ok && it.next(unit, t0, t1, whole, slot)) {
       for (int j = t0; j < t1; ++j, ++g) {
         const int grp = g & 1, gr = g >> 1;
-        // with kEarlyK the softmax has waited for V
-        if (!S::kEarlyK && !(ok = wait(&misc->v_full[st], phase))) break;
+        if (!(ok = wait(&misc->v_full[st], phase))) break;
         if (!(ok = wait(&misc->p_full[grp], gr & 1))) break;
+        if (d.nv == 8) fence_proxy_async_smem();
         tc_fence_after();
         if (lane == 0) {
           // MN-major without swizzling: 8-token groups 128 bytes apart
@@ -1372,6 +1406,8 @@ mla_status gqa_decode_partial_fp8(const void* q, const gqa_block_pages* cache,
   while ((1 << d.lg_block) < cache->block) ++d.lg_block;
   d.scale_log2 = shape->softmax_scale * 1.4426950408889634f;
   d.q = static_cast<const uint16_t*>(q);
+  d.k = static_cast<const uint8_t*>(cache->k);
+  d.v = static_cast<const uint8_t*>(cache->v);
   d.ks = cache->k_scale;
   d.vs = cache->v_scale;
   d.block_table = block_table;
