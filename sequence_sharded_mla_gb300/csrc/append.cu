@@ -38,7 +38,8 @@ struct Rows {
   uint16_t* y;
   long long xs, ys;    // elements between tokens
   int heads, D;
-  int split;           // blocks a token's heads are spread over
+  Div split;           // blocks a token's heads are spread over
+  Div items;           // a head's work items (see turn_heads)
 };
 
 struct Cache {
@@ -49,7 +50,8 @@ struct Cache {
   int fp8, block, num_pages, Hkv;
   const int32_t* bt;
   int max_pages;
-  int shard, num_shards;
+  int shard;
+  Div num_shards;
   unsigned* err;
 };
 
@@ -129,29 +131,48 @@ __device__ __forceinline__ void turn_half(uint4& wa, uint4& wb, const float2* cs
   }
 }
 
+// Work items of a head: a rotation of 8 (interleaved) or 16 dims (half), or,
+// unless in place, a copy of 8.
+__host__ __device__ inline int head_items(int D, int rot, int interleaved, bool inplace) {
+  return (interleaved ? rot / 8 : rot / 16) + (inplace ? 0 : (D - rot) / 8);
+}
+
 // Heads [h0, h1) of one token, D wide, src -> dst, by n threads; in place if
-// src == dst (only the rotated dims move).  rot == 0 copies.
+// src == dst (only the rotated dims move).  rot == 0 copies.  A thread has
+// four items' loads in flight.
 __device__ __forceinline__ void turn_heads(const uint16_t* src, uint16_t* dst, int D, int h0,
-                                           int h1, const RopeArgs& r, const float2* cs, int tid,
-                                           int n) {
-  const bool inplace = src == dst;
+                                           int h1, const RopeArgs& r, const Div& items,
+                                           const float2* cs, int tid, int n) {
   const int f8 = r.first >> 3, r8 = r.rot >> 3;
-  const int turns = r.interleaved ? r8 : r8 >> 1;          // work items that rotate
-  const int items = turns + (inplace ? 0 : (D >> 3) - r8);
-  for (int x = tid; x < (h1 - h0) * items; x += n) {
-    const int h = x / items, it = x - h * items;
-    const uint4* s = reinterpret_cast<const uint4*>(src + (size_t)(h0 + h) * D);
-    uint4* d = reinterpret_cast<uint4*>(dst + (size_t)(h0 + h) * D);
-    if (it >= turns) {
-      const int c = it - turns, v = c < f8 ? c : c + r8;
-      d[v] = s[v];
-    } else if (r.interleaved) {
-      d[f8 + it] = turn_interleaved(s[f8 + it], cs + 4 * it);
-    } else {
-      uint4 a = s[f8 + it], b = s[f8 + turns + it];
-      turn_half(a, b, cs + 8 * it);
-      d[f8 + it] = a;
-      d[f8 + turns + it] = b;
+  const int turns = r.interleaved ? r8 : r8 >> 1;
+  const uint4* s = reinterpret_cast<const uint4*>(src + (size_t)h0 * D);
+  uint4* d = reinterpret_cast<uint4*>(dst + (size_t)h0 * D);
+  const int total = (h1 - h0) * items, d8 = D >> 3;
+  for (int x0 = tid; x0 < total; x0 += 4 * n) {
+    uint4 a[4], b[4];
+    int at[4], it[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int x = x0 + k * n;
+      if (x >= total) break;
+      const int h = x / items, i = x - h * items, c = i - turns;
+      it[k] = i;
+      at[k] = h * d8 + (i < turns ? f8 + i : c < f8 ? c : c + r8);
+      a[k] = s[at[k]];
+      if (!r.interleaved && i < turns) b[k] = s[at[k] + turns];
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (x0 + k * n >= total) break;
+      if (it[k] < turns) {
+        if (r.interleaved) {
+          a[k] = turn_interleaved(a[k], cs + 4 * it[k]);
+        } else {
+          turn_half(a[k], b[k], cs + 8 * it[k]);
+          d[at[k] + turns] = b[k];
+        }
+      }
+      d[at[k]] = a[k];
     }
   }
 }
@@ -159,20 +180,22 @@ __device__ __forceinline__ void turn_heads(const uint16_t* src, uint16_t* dst, i
 // Block `blk` of the query rotation: token blk / split, a share of its heads.
 __device__ __forceinline__ void query_block(const Rows& q, const Tokens& t, const RopeArgs& r,
                                             int blk, float2* cs) {
-  const int tok = blk / q.split, part = blk - tok * q.split;
+  const int tok = blk / q.split, part = blk % q.split;
   const int b = tok / t.q_len, i = tok - b * t.q_len;
   const int n = new_count(t, b, nullptr);
   if (i >= n) return;
   const int stand = t.seq_lens != nullptr ? t.seq_lens[b] - n + i : 0;
   fill_cs(r, rope_pos(t, b, i, stand), cs, threadIdx.x, blockDim.x);
   __syncthreads();
-  const int per = ceil_div(q.heads, q.split);
+  const int per = (q.heads - 1) / q.split + 1;
   turn_heads(q.x + tok * q.xs, q.y + tok * q.ys, q.D, part * per, min(q.heads, (part + 1) * per), r,
-             cs, threadIdx.x, blockDim.x);
+             q.items, cs, threadIdx.x, blockDim.x);
 }
 
 __global__ void __launch_bounds__(kThreads) rope_kernel(Rows q, Tokens t, RopeArgs r) {
   __shared__ float2 cs[kMaxPairs];
+  griddep_wait();
+  griddep_launch_dependents();
   query_block(q, t, r, blockIdx.x, cs);
 }
 
@@ -185,6 +208,8 @@ __global__ void __launch_bounds__(kThreads) latent_append_kernel(const uint16_t*
   __shared__ float2 cs[kDqk / 2];
   __shared__ float row[kDqk];
   __shared__ float red[kThreads / 32];
+  griddep_wait();
+  griddep_launch_dependents();
   if ((int)blockIdx.x >= cache_blocks) {
     query_block(q, t, r, blockIdx.x - cache_blocks, cs);
     return;
@@ -240,8 +265,11 @@ __global__ void __launch_bounds__(kThreads) latent_append_kernel(const uint16_t*
 __global__ void __launch_bounds__(kThreads) gqa_append_kernel(const uint16_t* k, long long ks,
                                                               const uint16_t* v, long long vs,
                                                               Cache c, Tokens t, RopeArgs r,
-                                                              Rows q, int cache_blocks) {
+                                                              Rows q, int cache_blocks,
+                                                              Div items) {
   __shared__ float2 cs[kGD / 2];
+  griddep_wait();
+  griddep_launch_dependents();
   if ((int)blockIdx.x >= cache_blocks) {
     query_block(q, t, r, blockIdx.x - cache_blocks, cs);
     return;
@@ -260,121 +288,194 @@ __global__ void __launch_bounds__(kThreads) gqa_append_kernel(const uint16_t* k,
   const size_t dst = ((size_t)page * kPage + lp % kPage) * c.Hkv * kGD;
   fill_cs(r, rope_pos(t, b, i, p), cs, threadIdx.x, kThreads);
   __syncthreads();
-  turn_heads(k + tok * ks, reinterpret_cast<uint16_t*>(c.k) + dst, kGD, 0, c.Hkv, r, cs,
-             threadIdx.x, kThreads);
+  turn_heads(k + tok * ks, reinterpret_cast<uint16_t*>(c.k) + dst, kGD, 0, c.Hkv, r, items,
+             cs, threadIdx.x, kThreads);
   const uint4* s = reinterpret_cast<const uint4*>(v + tok * vs);
   uint4* d = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(c.v) + dst);
   for (int e = threadIdx.x; e < c.Hkv * (kGD / 8); e += kThreads) d[e] = s[e];
 }
 
 // --------------------------------------------------------------- K/V, e4m3
-// One block per (request, touched block of token slots, KV head, K or V): the
-// new tokens' rotated values in shared memory as fp32, their largest, the
-// scale, then the codes (and, if the scale grew, the earlier codes again).
-__global__ void __launch_bounds__(kThreads) gqa_append_fp8_kernel(const uint16_t* k, long long ks,
-                                                                  const uint16_t* v, long long vs,
-                                                                  Cache c, Tokens t, RopeArgs r,
-                                                                  Rows q, int cache_blocks,
-                                                                  int nblk) {
-  __shared__ float2 cs[kGD / 2];
-  __shared__ float4 val[kPage * (kGD / 4)];
-  __shared__ float red[kThreads / 32];
+// A block takes one block of token slots of a request that the new tokens
+// touch, K or V, and as many KV heads as its eight warps hold: a warp has 16
+// tokens of a head (8 dims a lane, two tokens a load) in registers, from the
+// one read to the codes, so a head takes block / 16 warps.  The block's warps
+// share one table of its tokens' sines and cosines: computed for every head
+// again (one head a block), they cost more than the memory does (2 x 4099
+// tokens x 8 heads, 23.5 against XXX us).
+constexpr int kF8Warps = 8;
+
+__global__ void __launch_bounds__(32 * kF8Warps, 2)
+    gqa_append_fp8_kernel(const uint16_t* k, long long ks, const uint16_t* v, long long vs, Cache c,
+                          Tokens t, RopeArgs r, Rows q, int cache_blocks, Div nblk, Div hgroups,
+                          Div wph) {
+  // per token: (cos, sin) of two pairs, those of the 16 (or 8) lanes that turn
+  // them side by side
+  __shared__ float4 cs[kPage][kGD / 4];
+  __shared__ float red[kF8Warps];
+  griddep_wait();
+  griddep_launch_dependents();
   if ((int)blockIdx.x >= cache_blocks) {
-    query_block(q, t, r, blockIdx.x - cache_blocks, cs);
+    query_block(q, t, r, blockIdx.x - cache_blocks, reinterpret_cast<float2*>(cs));
     return;
   }
   int u = blockIdx.x;
   const bool is_v = u & 1;
   u >>= 1;
-  const int kh = u % c.Hkv;
-  u /= c.Hkv;
+  const int hg = u % hgroups;
+  u = u / hgroups;
   const int j = u % nblk, b = u / nblk;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n = new_count(t, b, c.err);
-  const int L = t.seq_lens[b], N = c.num_shards;
+  const int L = t.seq_lens[b], N = c.num_shards, lg_block = 31 - __clz(c.block);
   if (L < n && threadIdx.x == 0) atomicOr(c.err, kErrQLens);
   // local slots [p0, p1) of this shard are new: positions max(L - n, 0) .. L - 1
   const int first_new = max(L - n, 0);
-  const int p0 = first_new > c.shard ? (first_new - c.shard + N - 1) / N : 0;
-  const int p1 = L > c.shard ? (L - 1 - c.shard) / N + 1 : 0;
-  const int blk = p0 / c.block + j;
-  const int lo = max(p0, blk * c.block), hi = min(p1, (blk + 1) * c.block);
-  if (lo >= hi) return;
+  const int p0 = first_new > c.shard ? (first_new - c.shard - 1) / c.num_shards + 1 : 0;
+  const int p1 = L > c.shard ? (L - 1 - c.shard) / c.num_shards + 1 : 0;
+  const int blk = (p0 >> lg_block) + j;
+  const int lo = max(p0, blk * c.block), hi = min(p1, (blk + 1) * c.block), nt = hi - lo;
+  if (nt <= 0) return;
   const int page = page_of(c, b, blk * c.block);
   if (page < 0) return;
   const int row0 = (blk * c.block) % kPage;
-  const uint16_t* x = is_v ? v : k;
+  const int W = wph, wh = warp % wph;            // warps of a head, and this one among them
+  const int kh = hg * (kF8Warps / W) + warp / wph;
+  const bool live = kh < c.Hkv;
+  const int half = lane >> 4, l16 = lane & 15;
+  auto token = [&](int p) { return p * N + c.shard - (L - n); };   // its place in the new ones
+
+  // the warp's tokens: lo + 2 (i W + wh) + half for i < 8
+  uint4 w[8];
+  const uint16_t* x = (is_v ? v : k) + (size_t)kh * kGD + 8 * l16;
   const long long xs = is_v ? vs : ks;
-  // a lane holds dims 4 lane .. 4 lane + 3 of a token
-  const int f4 = r.first >> 2, r4 = r.rot >> 2;
-  const int li = lane - f4;                       // the lane's place in the rotated dims
-  const bool turns = !is_v && li >= 0 && li < r4;
-  const bool upper = !r.interleaved && 2 * li >= r4;
-  const int pair0 = r.interleaved ? 2 * li : 4 * (upper ? li - r4 / 2 : li);
-  const int partner = (turns && !r.interleaved) ? (upper ? lane - r4 / 2 : lane + r4 / 2) : lane;
-  unsigned long long rate[4] = {0, 0, 0, 0};
-  if (turns)
-    for (int e = 0; e < (r.interleaved ? 2 : 4); ++e) rate[e] = turn_rate(__ldg(r.inv_freq + pair0 + e));
-  float amax = 0.0f;
-  for (int p = lo + warp; p < hi; p += kThreads / 32) {
-    const int i = p * N + c.shard - (L - n);
-    const size_t tok = (size_t)b * t.q_len + i;
-    const uint2 w = __ldg(reinterpret_cast<const uint2*>(x + tok * xs + (size_t)kh * kGD) + lane);
-    float a[4] = {bf_lo(w.x), bf_hi(w.x), bf_lo(w.y), bf_hi(w.y)};
-    if (!is_v && r4 > 0) {
-      float o[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[e] = __shfl_sync(0xffffffffu, a[e], partner);
-      if (turns) {
-        const int pos = rope_pos(t, b, i, L - n + i);
-        if (r.interleaved) {
-          turn_pair(a[0], a[1], turn_cs(rate[0], pos, r.factor));
-          turn_pair(a[2], a[3], turn_cs(rate[1], pos, r.factor));
-        } else {
+  for (int i = 0; i < 8; ++i) {
+    const int tt = 2 * (i * W + wh) + half;
+    w[i] = make_uint4(0, 0, 0, 0);
+    if (live && tt < nt)
+      w[i] = __ldg(reinterpret_cast<const uint4*>(x + ((size_t)b * t.q_len + token(lo + tt)) * xs));
+  }
+  const bool had = lo > blk * c.block;
+  float* sp = (is_v ? c.vs : c.ks) + (((size_t)page * kPage + row0) >> lg_block) * c.Hkv + kh;
+  const float old = had && live ? *sp : 0.0f;
+
+  const bool turn = !is_v && r.rot > 0;
+  // lanes that turn a pair's side: 8 dims each, all pairs' (interleaved) or
+  // the lower sides' first (half)
+  const int r8 = r.rot >> 3, nl = r.interleaved ? r8 : r8 >> 1;
+  if (turn) {
+    const int lg = r.interleaved ? 2 : 3;        // log2 of a lane's pairs
+    for (int p = lane; p < r.rot / 2; p += 32) {
+      const unsigned long long rate = turn_rate(__ldg(r.inv_freq + p));
+      const int at = ((p & ((1 << lg) - 1)) >> 1) * nl + (p >> lg);
+      for (int tt = warp; tt < nt; tt += kF8Warps) {
+        const int i = token(lo + tt);
+        reinterpret_cast<float2*>(&cs[tt][at])[p & 1] =
+            turn_cs(rate, rope_pos(t, b, i, L - n + i), r.factor);
+      }
+    }
+    __syncthreads();
+  }
+  const int li = l16 - (r.first >> 3);           // the lane's place in the rotated dims
+  const bool turns = turn && li >= 0 && li < r8;
+  const bool upper = !r.interleaved && li >= nl;
+  const int lc = upper ? li - nl : li;
+  const int partner = turns && !r.interleaved ? (upper ? lane - nl : lane + nl) : lane;
+  float f[8][8];
+  float amax = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int tt = 2 * (i * W + wh) + half;
+    const uint32_t* p = &w[i].x;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      f[i][2 * e] = bf_lo(p[e]);
+      f[i][2 * e + 1] = bf_hi(p[e]);
+    }
+    if (2 * (i * W + wh) < nt && turn) {
+      if (r.interleaved) {
+        if (turns) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float4 z = cs[tt][e * nl + lc];
+            turn_pair(f[i][4 * e], f[i][4 * e + 1], make_float2(z.x, z.y));
+            turn_pair(f[i][4 * e + 2], f[i][4 * e + 3], make_float2(z.z, z.w));
+          }
+        }
+      } else {
+        uint32_t o[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] = __shfl_sync(0xffffffffu, p[e], partner);
+        if (turns) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float2 z = turn_cs(rate[e], pos, r.factor);
-            if (upper) turn_pair(o[e], a[e], z);
-            else turn_pair(a[e], o[e], z);
+            const float4 z = cs[tt][e * nl + lc];
+            float o0 = bf_lo(o[e]), o1 = bf_hi(o[e]);
+            float &a0 = f[i][2 * e], &a1 = f[i][2 * e + 1];
+            if (upper) {
+              turn_pair(o0, a0, make_float2(z.x, z.y));
+              turn_pair(o1, a1, make_float2(z.z, z.w));
+            } else {
+              turn_pair(a0, o0, make_float2(z.x, z.y));
+              turn_pair(a1, o1, make_float2(z.z, z.w));
+            }
           }
         }
       }
     }
+    if (tt < nt) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) amax = fmaxf(amax, finite_abs(a[e]));
-    val[(p - lo) * (kGD / 4) + lane] = make_float4(a[0], a[1], a[2], a[3]);
+      for (int e = 0; e < 8; ++e) amax = fmaxf(amax, finite_abs(f[i][e]));
+    }
   }
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
   if (lane == 0) red[warp] = amax;
-  __syncthreads();
-  amax = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-  float* sp = (is_v ? c.vs : c.ks) + ((size_t)page * (kPage / c.block) + row0 / c.block) * c.Hkv + kh;
+  __syncthreads();                               // every warp has read the old scale too
+  if (!live) return;
+  amax = 0.0f;
+  for (int e = 0; e < W; ++e) amax = fmaxf(amax, red[warp - wh + e]);
   const float need = pow2_scale(amax);
-  const bool had = lo > blk * c.block;
-  const float was = had ? *sp : need;
-  const bool grow = had && fabsf(was) < need;
-  const float s = grow ? need : was;
-  uint8_t* base = (is_v ? c.v : c.k) + (((size_t)page * kPage + row0) * c.Hkv + kh) * kGD;
+  const bool grow = had && fabsf(old) < need;
+  const float s = had && !grow ? old : need;
+  uint8_t* base = (is_v ? c.v : c.k) + (((size_t)page * kPage + row0) * c.Hkv + kh) * kGD + 8 * l16;
   const size_t rs = (size_t)c.Hkv * kGD;
   if (grow) {
-    const float f = was / s;    // s is a power of two: exact
-    for (int p = blk * c.block + warp; p < lo; p += kThreads / 32) {
-      uint32_t* d = reinterpret_cast<uint32_t*>(base + (p - blk * c.block) * rs) + lane;
-      const uint32_t w = *d;
-      float y[4];
-      e4m3x2_to_f32x2(w, y[0], y[1]);
-      e4m3x2_to_f32x2(w >> 16, y[2], y[3]);
-      *d = codes2(y[0] * f, y[1] * f) | (codes2(y[2] * f, y[3] * f) << 16);
+    const float g = old / s;                     // s is a power of two: exact
+    for (int p = 2 * wh + half; p < lo - blk * c.block; p += 2 * W) {
+      uint2* d = reinterpret_cast<uint2*>(base + p * rs);
+      uint32_t z[2] = {d->x, d->y};
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float y[4];
+        e4m3x2_to_f32x2(z[e], y[0], y[1]);
+        e4m3x2_to_f32x2(z[e] >> 16, y[2], y[3]);
+        z[e] = codes2(y[0] * g, y[1] * g) | (codes2(y[2] * g, y[3] * g) << 16);
+      }
+      *d = make_uint2(z[0], z[1]);
     }
   }
-  for (int p = lo + warp; p < hi; p += kThreads / 32) {
-    const float4 a = val[(p - lo) * (kGD / 4) + lane];
-    reinterpret_cast<uint32_t*>(base + (p - blk * c.block) * rs)[lane] =
-        codes2(a.x / s, a.y / s) | (codes2(a.z / s, a.w / s) << 16);
+  // a power of two, as this kernel writes them, has an exact inverse
+  const uint32_t sb = __float_as_uint(s);
+  const bool exact = (sb & 0x807FFFFFu) == 0 && sb >= (1u << 23) && sb <= (253u << 23);
+  const float inv = exact ? __uint_as_float((254u << 23) - sb) : 1.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int tt = 2 * (i * W + wh) + half;
+    if (tt >= nt) break;
+    if (exact) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[i][e] *= inv;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[i][e] /= s;
+    }
+    *reinterpret_cast<uint2*>(base + (lo - blk * c.block + tt) * rs) =
+        make_uint2(codes2(f[i][0], f[i][1]) | (codes2(f[i][2], f[i][3]) << 16),
+                   codes2(f[i][4], f[i][5]) | (codes2(f[i][6], f[i][7]) << 16));
   }
-  __syncthreads();   // every thread has read the old scale
-  if (threadIdx.x == 0) *sp = s;
+  if (wh == 0 && lane == 0) *sp = s;
 }
 
 // ------------------------------------------------------------------ host side
@@ -410,14 +511,15 @@ bool rows_ok(const void* x, long long xs, long long width) {
 
 // Query rows to rotate in an append call: checked, `out` filled.
 mla_status make_rows(const void* q, long long qs, void* y, long long ys, int heads, int D,
-                     const mla_tokens* t, Rows& out) {
+                     const mla_tokens* t, const mla_rope* r, Rows& out) {
   if (heads < 1 || heads > (1 << 16)) return MLA_ERR_INVALID;
   const long long width = (long long)heads * D;
   if (!rows_ok(q, qs, width) || !rows_ok(y, ys, width)) return MLA_ERR_INVALID;
   if (q == y && qs != ys) return MLA_ERR_INVALID;
-  out = Rows{static_cast<const uint16_t*>(q), static_cast<uint16_t*>(y), qs, ys, heads, D, 1};
-  // about 16 KB of a token's heads to a block
-  out.split = std::min(heads, std::max(1, heads * D / 8192));
+  // about 8 KB of a token's heads to a block
+  out = Rows{static_cast<const uint16_t*>(q), static_cast<uint16_t*>(y), qs, ys, heads, D,
+             make_div(std::min(heads, std::max(1, heads * D / 4096))),
+             make_div(head_items(D, r->rot_dim, r->interleaved, q == y))};
   if ((long long)t->batch * t->q_len * out.split >= (1LL << 30)) return MLA_ERR_INVALID;
   return MLA_OK;
 }
@@ -435,10 +537,10 @@ mla_status append_args(const int32_t* block_table, int max_pages, const mla_toke
   if (rope != nullptr && !rope_ok(rope, D)) return MLA_ERR_INVALID;
   if (rope != nullptr && !rope_supported(rope)) return MLA_ERR_UNSUPPORTED;
   if (page_size != kPage) return MLA_ERR_UNSUPPORTED;
-  rows = Rows{nullptr, nullptr, 0, 0, 0, D, 1};
+  rows = Rows{nullptr, nullptr, 0, 0, 0, D, make_div(1), make_div(1)};
   if (q != nullptr) {
     if (rope == nullptr) return MLA_ERR_INVALID;
-    const mla_status st = make_rows(q, qs, q_out, qos, heads, D, tokens, rows);
+    const mla_status st = make_rows(q, qs, q_out, qos, heads, D, tokens, rope, rows);
     if (st != MLA_OK) return st;
   }
   if (workspace == nullptr || !host::aligned16(workspace) || workspace_bytes < sizeof(WsHeader))
@@ -446,7 +548,20 @@ mla_status append_args(const int32_t* block_table, int max_pages, const mla_toke
   return MLA_OK;
 }
 
-mla_status launched() { return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA; }
+// Launches that may begin while the kernel before them ends (their
+// griddep_wait() waits for its results).
+template <class... P, class... A>
+mla_status launch(void (*kernel)(P...), unsigned blocks, unsigned threads, void* stream, A... args) {
+  cudaLaunchAttribute attr = pdl_attribute();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(threads);
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...) == cudaSuccess ? MLA_OK
+                                                                                  : MLA_ERR_CUDA;
+}
 
 }  // namespace append
 }  // namespace mla
@@ -463,12 +578,12 @@ mla_status mla_rope_apply(const void* x, long long x_stride, void* out, long lon
   if (head_dim % 8 != 0 || head_dim > 2 * append::kMaxPairs || !append::rope_supported(rope))
     return MLA_ERR_UNSUPPORTED;
   append::Rows q;
-  const mla_status st = append::make_rows(x, x_stride, out, out_stride, num_heads, head_dim, tokens, q);
+  const mla_status st =
+      append::make_rows(x, x_stride, out, out_stride, num_heads, head_dim, tokens, rope, q);
   if (st != MLA_OK) return st;
-  append::rope_kernel<<<tokens->batch * tokens->q_len * q.split, append::kThreads, 0,
-                        static_cast<cudaStream_t>(stream)>>>(q, append::make_tokens(tokens),
-                                                             append::make_rope(rope));
-  return append::launched();
+  return append::launch(append::rope_kernel, tokens->batch * tokens->q_len * q.split,
+                        append::kThreads, stream, q, append::make_tokens(tokens),
+                        append::make_rope(rope));
 }
 
 mla_status mla_cache_append(const void* latent, long long latent_stride, const mla_kv_pages* kv,
@@ -490,14 +605,13 @@ mla_status mla_cache_append(const void* latent, long long latent_stride, const m
   if (st != MLA_OK) return st;
   const append::Cache c{static_cast<uint8_t*>(const_cast<void*>(kv->data)), nullptr,
                         const_cast<float*>(kv->scale), nullptr, kv->dtype == MLA_KV_FP8_E4M3, 1,
-                        kv->num_pages, 1, block_table, max_pages_per_req, shard_id, num_shards,
+                        kv->num_pages, 1, block_table, max_pages_per_req, shard_id, make_div(num_shards),
                         &static_cast<WsHeader*>(workspace)->err};
   const int n = tokens->batch * tokens->q_len;
-  append::latent_append_kernel<<<n + (rows.heads ? n * rows.split : 0), append::kThreads, 0,
-                                 static_cast<cudaStream_t>(stream)>>>(
-      static_cast<const uint16_t*>(latent), latent_stride, c, append::make_tokens(tokens),
-      append::make_rope(rope), rows, n);
-  return append::launched();
+  return append::launch(append::latent_append_kernel, n + (rows.heads ? n * rows.split : 0),
+                        append::kThreads, stream, static_cast<const uint16_t*>(latent),
+                        latent_stride, c, append::make_tokens(tokens), append::make_rope(rope),
+                        rows, n);
 }
 
 mla_status gqa_cache_append(const void* k, long long k_stride, const void* v, long long v_stride,
@@ -530,25 +644,26 @@ mla_status gqa_cache_append(const void* k, long long k_stride, const void* v, lo
   const append::Cache c{static_cast<uint8_t*>(cache->k), static_cast<uint8_t*>(cache->v),
                         cache->k_scale, cache->v_scale, fp8, fp8 ? cache->block : kPage,
                         cache->num_pages, cache->num_kv_heads, block_table, max_pages_per_req,
-                        shard_id, num_shards, &static_cast<WsHeader*>(workspace)->err};
+                        shard_id, make_div(num_shards), &static_cast<WsHeader*>(workspace)->err};
   const int n = tokens->batch * tokens->q_len;
   const int qb = rows.heads ? n * rows.split : 0;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (!fp8) {
-    append::gqa_append_kernel<<<n + qb, append::kThreads, 0, s>>>(
-        static_cast<const uint16_t*>(k), k_stride, static_cast<const uint16_t*>(v), v_stride, c,
-        append::make_tokens(tokens), append::make_rope(rope), rows, n);
-    return append::launched();
-  }
+  const uint16_t *kp = static_cast<const uint16_t*>(k), *vp = static_cast<const uint16_t*>(v);
+  const RopeArgs r = append::make_rope(rope);
+  if (!fp8)
+    return append::launch(append::gqa_append_kernel, n + qb, append::kThreads, stream, kp, k_stride,
+                          vp, v_stride, c, append::make_tokens(tokens), r, rows, n,
+                          make_div(append::head_items(kGD, r.rot, r.interleaved, false)));
   // blocks that ceil(q_len / N) consecutive local slots can touch
   const int local = ceil_div(tokens->q_len, num_shards);
   const int nblk = (local + cache->block - 2) / cache->block + 1;
-  const long long blocks = 2LL * tokens->batch * nblk * cache->num_kv_heads;
+  const int wph = std::max(1, cache->block / 16);
+  const int hgroups = ceil_div(cache->num_kv_heads, append::kF8Warps / wph);
+  const long long blocks = 2LL * tokens->batch * nblk * hgroups;
   if (blocks + qb >= (1LL << 31)) return MLA_ERR_INVALID;
-  append::gqa_append_fp8_kernel<<<(unsigned)(blocks + qb), append::kThreads, 0, s>>>(
-      static_cast<const uint16_t*>(k), k_stride, static_cast<const uint16_t*>(v), v_stride, c,
-      append::make_tokens(tokens), append::make_rope(rope), rows, (int)blocks, nblk);
-  return append::launched();
+  return append::launch(append::gqa_append_fp8_kernel, (unsigned)(blocks + qb),
+                        32 * append::kF8Warps, stream, kp, k_stride, vp, v_stride, c,
+                        append::make_tokens(tokens), r, rows, (int)blocks, make_div(nblk),
+                        make_div(hgroups), make_div(wph));
 }
 
 }  // extern "C"

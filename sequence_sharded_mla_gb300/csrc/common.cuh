@@ -120,6 +120,28 @@ struct Unit {
 
 __host__ __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
+// A divisor of numbers 0 <= n < 2^31 that is fixed for a call: n / d is (n +
+// the high word of n m) >> s with m = floor(2^32 (2^s - d) / d) + 1, s =
+// ceil(log2 d) (Granlund and Montgomery, 1994), a fifth of the instructions
+// of a division.
+struct Div {
+  int d;
+  uint32_t m;
+  int s;
+  __host__ __device__ operator int() const { return d; }
+};
+__device__ __forceinline__ int operator/(int n, const Div& v) {
+  return (int)((__umulhi((uint32_t)n, v.m) + (uint32_t)n) >> v.s);
+}
+__device__ __forceinline__ int operator%(int n, const Div& v) { return n - n / v * v.d; }
+
+inline Div make_div(int d) {
+  Div v{d, 0, 0};
+  while (v.s < 31 && (1u << v.s) < (uint32_t)d) ++v.s;
+  v.m = (uint32_t)((((1ull << v.s) - (unsigned)d) << 32) / (unsigned)d) + 1;
+  return v;
+}
+
 // Walks the work pieces of one persistent CTA: the units whose tile positions
 // intersect the CTA's range [lo, hi) of work positions.
 struct PieceIter {

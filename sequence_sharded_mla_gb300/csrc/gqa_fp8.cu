@@ -76,28 +76,6 @@ constexpr float kMost = 15.0f;             // log2 of the largest weight that fi
 constexpr float kNoRef = -1.0e38f;         // reference of a row that has seen nothing
 constexpr float kMinScale = 8.67361737988403547e-19f;   // 2^-60
 
-// A divisor of numbers 0 <= n < 2^31 that is fixed for a call: n / d is (n +
-// the high word of n m) >> s with m = floor(2^32 (2^s - d) / d) + 1, s =
-// ceil(log2 d) (Granlund and Montgomery, 1994), a fifth of the instructions
-// of a division.
-struct Div {
-  int d;
-  uint32_t m;
-  int s;
-  __host__ __device__ operator int() const { return d; }
-};
-__device__ __forceinline__ int operator/(int n, const Div& v) {
-  return (int)((__umulhi((uint32_t)n, v.m) + (uint32_t)n) >> v.s);
-}
-__device__ __forceinline__ int operator%(int n, const Div& v) { return n - n / v * v.d; }
-
-Div make_div(int d) {
-  Div v{d, 0, 0};
-  while (v.s < 31 && (1u << v.s) < (uint32_t)d) ++v.s;
-  v.m = (uint32_t)((((1ull << v.s) - (unsigned)d) << 32) / (unsigned)d) + 1;
-  return v;
-}
-
 struct Desc {
   int B, q_len, H;
   Div Hkv, G;
@@ -1390,13 +1368,13 @@ mla_status gqa_decode_partial_fp8(const void* q, const gqa_block_pages* cache,
   d.B = shape->batch;
   d.q_len = shape->q_len;
   d.H = shape->num_heads;
-  d.Hkv = gqa8::make_div(shape->num_kv_heads);
-  d.G = gqa8::make_div(shape->num_heads / shape->num_kv_heads);
+  d.Hkv = make_div(shape->num_kv_heads);
+  d.G = make_div(shape->num_heads / shape->num_kv_heads);
   d.rg = sp.rg;
-  d.Gq = gqa8::make_div(sp.Gq);
-  d.num_shards = gqa8::make_div(num_shards);
+  d.Gq = make_div(sp.Gq);
+  d.num_shards = make_div(num_shards);
   d.shard_first = shard_id == MLA_ALL_SHARDS ? 0 : shard_id;
-  d.n_out = gqa8::make_div(shard_id == MLA_ALL_SHARDS ? num_shards : 1);
+  d.n_out = make_div(shard_id == MLA_ALL_SHARDS ? num_shards : 1);
   d.layout = (layout & 1) ? kContiguous : kInterleaved;
   d.local = local;
   d.causal = shape->causal;

@@ -31,13 +31,22 @@ __device__ __forceinline__ unsigned long long turn_rate(double w) {
 
 // (f cos, f sin) of position pos at `rate`.  The turn is split into the
 // nearest quarter and a rest of at most an eighth, which is exact in integers;
-// the rest goes to sincospif with the error of one fp32 rounding.
+// the rest's sine and cosine are their Taylor sums, which end below 2^-25 for
+// |x| <= pi / 4.
 __device__ __forceinline__ float2 turn_cs(unsigned long long rate, int pos, float f) {
   const unsigned long long u = rate * (unsigned long long)(long long)pos;
   const unsigned q = (unsigned)((u + (1ull << 61)) >> 62);
   const long long r = (long long)(u - ((unsigned long long)q << 62));
-  float s, c;
-  sincospif((float)(int)(r >> 30) * 1.16415321826934814453125e-10f, &s, &c);   // 2^-33
+  const float x = (float)(int)(r >> 30) * 3.657295198e-10f;   // 2 pi 2^-34
+  const float y = x * x;
+  float s = fmaf(y, 1.0f / 362880.0f, -1.0f / 5040.0f);
+  s = fmaf(y, s, 1.0f / 120.0f);
+  s = fmaf(y, s, -1.0f / 6.0f);
+  s = fmaf(x * y, s, x);
+  float c = fmaf(y, 1.0f / 40320.0f, -1.0f / 720.0f);
+  c = fmaf(y, c, 1.0f / 24.0f);
+  c = fmaf(y, c, -0.5f);
+  c = fmaf(y, c, 1.0f);
   if (q & 1) {
     const float t = c;
     c = -s;
