@@ -139,7 +139,7 @@ __host__ __device__ inline int head_items(int D, int rot, int interleaved, bool 
 
 // Heads [h0, h1) of one token, D wide, src -> dst, by n threads; in place if
 // src == dst (only the rotated dims move).  rot == 0 copies.  A thread has
-// four items' loads in flight.
+// two items' loads in flight.
 __device__ __forceinline__ void turn_heads(const uint16_t* src, uint16_t* dst, int D, int h0,
                                            int h1, const RopeArgs& r, const Div& items,
                                            const float2* cs, int tid, int n) {
@@ -148,11 +148,11 @@ __device__ __forceinline__ void turn_heads(const uint16_t* src, uint16_t* dst, i
   const uint4* s = reinterpret_cast<const uint4*>(src + (size_t)h0 * D);
   uint4* d = reinterpret_cast<uint4*>(dst + (size_t)h0 * D);
   const int total = (h1 - h0) * items, d8 = D >> 3;
-  for (int x0 = tid; x0 < total; x0 += 4 * n) {
-    uint4 a[4], b[4];
-    int at[4], it[4];
+  for (int x0 = tid; x0 < total; x0 += 2 * n) {
+    uint4 a[2], b[2];
+    int at[2], it[2];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < 2; ++k) {
       const int x = x0 + k * n;
       if (x >= total) break;
       const int h = x / items, i = x - h * items, c = i - turns;
@@ -162,7 +162,7 @@ __device__ __forceinline__ void turn_heads(const uint16_t* src, uint16_t* dst, i
       if (!r.interleaved && i < turns) b[k] = s[at[k] + turns];
     }
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < 2; ++k) {
       if (x0 + k * n >= total) break;
       if (it[k] < turns) {
         if (r.interleaved) {
@@ -192,7 +192,7 @@ __device__ __forceinline__ void query_block(const Rows& q, const Tokens& t, cons
              q.items, cs, threadIdx.x, blockDim.x);
 }
 
-__global__ void __launch_bounds__(kThreads) rope_kernel(Rows q, Tokens t, RopeArgs r) {
+__global__ void __launch_bounds__(kThreads, 12) rope_kernel(Rows q, Tokens t, RopeArgs r) {
   __shared__ float2 cs[kMaxPairs];
   griddep_wait();
   griddep_launch_dependents();
@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(Rows q, Tokens t, RopeAr
 // ----------------------------------------------------------- latent rows
 // One block per new token: the 576 values in shared memory as fp32, rotated
 // there, then rounded (bf16) or scaled by the row's power of two (e4m3).
-__global__ void __launch_bounds__(kThreads) latent_append_kernel(const uint16_t* x, long long xs,
+__global__ void __launch_bounds__(kThreads, 16) latent_append_kernel(const uint16_t* x, long long xs,
                                                                  Cache c, Tokens t, RopeArgs r,
                                                                  Rows q, int cache_blocks) {
   __shared__ float2 cs[kDqk / 2];
@@ -262,7 +262,7 @@ __global__ void __launch_bounds__(kThreads) latent_append_kernel(const uint16_t*
 
 // --------------------------------------------------------------- K/V, bf16
 // One block per new token: K heads rotated into their page, V heads copied.
-__global__ void __launch_bounds__(kThreads) gqa_append_kernel(const uint16_t* k, long long ks,
+__global__ void __launch_bounds__(kThreads, 12) gqa_append_kernel(const uint16_t* k, long long ks,
                                                               const uint16_t* v, long long vs,
                                                               Cache c, Tokens t, RopeArgs r,
                                                               Rows q, int cache_blocks,
