@@ -426,8 +426,19 @@ __global__ void __launch_bounds__(32 * kF8Warps, 2)
     }
     if (tt < nt) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) amax = fmaxf(amax, finite_abs(f[i][e]));
+      for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(f[i][e]));   // skips NaN
     }
+  }
+  // an infinity sets no scale, and its code is NaN
+  if (__any_sync(0xffffffffu, amax == INFINITY)) {
+    amax = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        if (fabsf(f[i][e]) == INFINITY) f[i][e] = __int_as_float(0x7fffffff);
+        if (2 * (i * W + wh) + half < nt) amax = fmaxf(amax, fabsf(f[i][e]));
+      }
   }
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
@@ -472,8 +483,8 @@ __global__ void __launch_bounds__(32 * kF8Warps, 2)
       for (int e = 0; e < 8; ++e) f[i][e] /= s;
     }
     *reinterpret_cast<uint2*>(base + (lo - blk * c.block + tt) * rs) =
-        make_uint2(codes2(f[i][0], f[i][1]) | (codes2(f[i][2], f[i][3]) << 16),
-                   codes2(f[i][4], f[i][5]) | (codes2(f[i][6], f[i][7]) << 16));
+        make_uint2(f32x2_to_e4m3x2(f[i][0], f[i][1]) | (f32x2_to_e4m3x2(f[i][2], f[i][3]) << 16),
+                   f32x2_to_e4m3x2(f[i][4], f[i][5]) | (f32x2_to_e4m3x2(f[i][6], f[i][7]) << 16));
   }
   if (wh == 0 && lane == 0) *sp = s;
 }

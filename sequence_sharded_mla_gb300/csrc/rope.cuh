@@ -8,8 +8,8 @@
 // the half layout.  Only p * w_i modulo one turn matters.  w_i / 2 pi is held
 // as a 64-bit fraction of a turn, so the product with the integer position
 // wraps by itself: the angle of a far position is as exact as that of a near
-// one (2^-53 of w_i per token, 2^-34 of a turn in the reduction), without
-// 64-bit floating point per position.
+// one (2^-62 of w_i and 2^-64 of a turn per token, 2^-34 of a turn in the
+// reduction), without 64-bit floating point.
 #pragma once
 #include <cstdint>
 
@@ -23,10 +23,20 @@ struct RopeArgs {
   float factor;            // on the rotated values
 };
 
-// Radians per token -> 2^64ths of a turn per token.
+// Radians per token -> 2^64ths of a turn per token, modulo a turn: the product
+// of w's 53 bits with those of 1 / 2 pi, in integers (64-bit floating point is
+// 1/64 of the 32-bit rate here).
 __device__ __forceinline__ unsigned long long turn_rate(double w) {
-  const double t = w * 0.15915494309189533577;   // 1 / (2 pi)
-  return __double2ull_rn((t - floor(t)) * 18446744073709551616.0);
+  const unsigned long long bits = (unsigned long long)__double_as_longlong(w);
+  const int e = (int)((bits >> 52) & 0x7FFu) - 1024;        // w = 1.m 2^(e + 1)
+  if (e < -1000) return 0;
+  // w / 2 pi = hi 2^(e - 64) turns
+  const unsigned long long hi =
+      __umul64hi(((bits << 11) | (1ull << 63)), 0xa2f9836e4e441529ull);   // 2^66 / 2 pi
+  unsigned long long r;
+  if (e >= 0) r = e < 64 ? hi << e : 0;
+  else r = e >= -64 ? ((hi >> (-e - 1)) + 1) >> 1 : 0;
+  return (bits >> 63) ? 0 - r : r;
 }
 
 // (f cos, f sin) of position pos at `rate`.  The turn is split into the
