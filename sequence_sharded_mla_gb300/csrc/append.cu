@@ -192,7 +192,7 @@ __device__ __forceinline__ void query_block(const Rows& q, const Tokens& t, cons
              q.items, cs, threadIdx.x, blockDim.x);
 }
 
-__global__ void __launch_bounds__(kThreads, 12) rope_kernel(Rows q, Tokens t, RopeArgs r) {
+__global__ void __launch_bounds__(kThreads, 10) rope_kernel(Rows q, Tokens t, RopeArgs r) {
   __shared__ float2 cs[kMaxPairs];
   griddep_wait();
   griddep_launch_dependents();
@@ -262,7 +262,7 @@ __global__ void __launch_bounds__(kThreads, 16) latent_append_kernel(const uint1
 
 // --------------------------------------------------------------- K/V, bf16
 // One block per new token: K heads rotated into their page, V heads copied.
-__global__ void __launch_bounds__(kThreads, 12) gqa_append_kernel(const uint16_t* k, long long ks,
+__global__ void __launch_bounds__(kThreads, 10) gqa_append_kernel(const uint16_t* k, long long ks,
                                                               const uint16_t* v, long long vs,
                                                               Cache c, Tokens t, RopeArgs r,
                                                               Rows q, int cache_blocks,
