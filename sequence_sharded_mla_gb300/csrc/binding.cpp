@@ -9,6 +9,8 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/EmptyTensor.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -136,8 +138,11 @@ struct Place {
   }
 };
 
-at::Tensor make(at::IntArrayRef sizes, at::ScalarType t, const c10::Device& dev) {
-  return at::empty(sizes, at::TensorOptions().dtype(t).device(dev));
+// A new tensor on the current device and stream (a Place's), without the
+// dispatcher: half of torch.empty's 1.5 us.
+at::Tensor make(at::IntArrayRef sizes, at::ScalarType t) {
+  return at::detail::empty_generic(sizes, c10::cuda::CUDACachingAllocator::get(),
+                                   c10::DispatchKeySet(c10::DispatchKey::CUDA), t, std::nullopt);
 }
 
 // `given` if it is not None, else the wrapped `t`: a new reference.
@@ -389,7 +394,7 @@ PyObject* run_append(Append& p, const c10::Device& dev, const char* where, F&& c
   at::Tensor ws;
   if (p.pws != Py_None) ws = THPVariable_Unpack(p.pws);
   else ws = at::zeros({256}, at::TensorOptions().dtype(at::kByte).device(dev));
-  if (p.q.x != nullptr && !p.q.out.defined()) p.q.out = make(p.q.x->sizes(), at::kBFloat16, dev);
+  if (p.q.x != nullptr && !p.q.out.defined()) p.q.out = make(p.q.x->sizes(), at::kBFloat16);
   const void* q = p.q.x != nullptr ? p.q.x->const_data_ptr() : nullptr;
   void* q_out = p.q.x != nullptr ? p.q.out.mutable_data_ptr() : nullptr;
   void* wp = ws.mutable_data_ptr();
@@ -416,7 +421,7 @@ PyObject* rope_apply(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const RopeArg rope = rope_arg(a[1], dev);
     const int H = small(r.x->size(2), "x"), D = small(r.x->size(3), "x");
     const Place place(dev, a[6]);
-    if (!r.out.defined()) r.out = make(r.x->sizes(), at::kBFloat16, dev);
+    if (!r.out.defined()) r.out = make(r.x->sizes(), at::kBFloat16);
     const void* x = r.x->const_data_ptr();
     void* y = r.out.mutable_data_ptr();
     status(unlocked([&] {
@@ -533,12 +538,12 @@ PyObject* attend_fp8(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Place place(dev, a[15]);
     if (!ws.defined()) {
       const size_t need = gqa_fp8_workspace_size(&sh, num_shards, shard_id);
-      ws = make({(int64_t)std::max(need, (size_t)256)}, at::kByte, dev);
+      ws = make({(int64_t)std::max(need, (size_t)256)}, at::kByte);
     }
     // refused shapes come back as a status before anything is written
     if (num_shards <= 8) {
-      if (!out.defined()) out = make({n_out, B, q_len, H, D}, at::kFloat, dev);
-      if (!lse.defined()) lse = make({n_out, B, q_len, H}, at::kFloat, dev);
+      if (!out.defined()) out = make({n_out, B, q_len, H, D}, at::kFloat);
+      if (!lse.defined()) lse = make({n_out, B, q_len, H}, at::kFloat);
     }
     const void* qp = q.const_data_ptr();
     const int32_t *btp = bt.const_data_ptr<int32_t>(), *slp = sl.const_data_ptr<int32_t>();
@@ -578,8 +583,8 @@ PyObject* shard_combine(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (a[2] != Py_None) out = tensor(a[2], "out");
     if (a[3] != Py_None) lse = tensor(a[3], "lse_out");
     const Place place(dev, a[4]);
-    if (!out.defined()) out = make({B, q_len, H, D}, at::kBFloat16, dev);
-    if (!lse.defined()) lse = make({B, q_len, H}, at::kFloat, dev);
+    if (!out.defined()) out = make({B, q_len, H, D}, at::kBFloat16);
+    if (!lse.defined()) lse = make({B, q_len, H}, at::kFloat);
     const float *pp = p.const_data_ptr<float>(), *lp = l.const_data_ptr<float>();
     void* op = out.mutable_data_ptr();
     float* lo = static_cast<float*>(lse.mutable_data_ptr());
