@@ -302,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, 10) gqa_append_kernel(const uint16_t
 // one read to the codes, so a head takes block / 16 warps.  The block's warps
 // share one table of its tokens' sines and cosines: computed for every head
 // again (one head a block), they cost more than the memory does (2 x 4099
-// tokens x 8 heads, 23.5 against XXX us).
+// tokens x 8 heads, 23.5 us against 12.7, and 10.7 with fewer operations a value).
 constexpr int kF8Warps = 8;
 
 __global__ void __launch_bounds__(32 * kF8Warps, 2)

@@ -580,8 +580,17 @@ PyObject* shard_combine(PyObject*, PyObject* const* a, Py_ssize_t n) {
     sh.softmax_scale = 1.0f;
     const int N = small(p.size(0), "partials");
     at::Tensor out, lse;
-    if (a[2] != Py_None) out = tensor(a[2], "out");
-    if (a[3] != Py_None) lse = tensor(a[3], "lse_out");
+    if (l.numel() != N * B * q_len * H) value_error("lses and partials disagree");
+    if (a[2] != Py_None) {
+      out = tensor(a[2], "out");
+      on_device(out, "out", &dev);
+      if ((int64_t)out.nbytes() < B * q_len * H * D * 2) value_error("out is too small");
+    }
+    if (a[3] != Py_None) {
+      lse = tensor(a[3], "lse_out");
+      on_device(lse, "lse_out", &dev);
+      if ((int64_t)lse.nbytes() < B * q_len * H * 4) value_error("lse_out is too small");
+    }
     const Place place(dev, a[4]);
     if (!out.defined()) out = make({B, q_len, H, D}, at::kBFloat16);
     if (!lse.defined()) lse = make({B, q_len, H}, at::kFloat);

@@ -27,10 +27,11 @@
 //      largest weight at 2^12 and moves (rescaling O) once one passes 2^15.
 //      P goes to fp16 and from there to three e5m2 terms that add up to it
 //      within 2^-9 of its value, down to 2^-17: a token 2^-29 below the row's
-//      largest weight still counts.  (Two e4m3 terms end 2^-18 below it, and a
-//      million such tokens are not nothing.)  The terms are three blocks of
-//      the MMA's columns, so V is read once for all three; the epilogue adds
-//      their sums.
+//      largest weight (2^-27 below that of the first tile, whose references
+//      are likely to grow) still counts.  (Two e4m3 terms end 2^-18 below it,
+//      and a million such tokens are not nothing.)  The terms are three blocks
+//      of the MMA's columns, so V is read once for all three; the epilogue
+//      adds their sums.
 //
 // Tile g belongs to softmax group g & 1, each with its own S buffer, weights,
 // reference and O^T accumulator, joined by their references at the end of a
@@ -75,7 +76,8 @@ constexpr int kMaxOwnPlan = 768;           // units that every CTA plans for its
 constexpr int kOwnPerThread = (kMaxOwnPlan + kThreads - 1) / kThreads;
 constexpr unsigned long long kTimeoutNs = 2000000000ull;
 constexpr float kTop = 12.0f;              // log2 of the largest weight at a new reference
-constexpr float kTopFirst = 10.0f;         // and at a piece's first, which grows more often
+constexpr float kTopFirst = 10.0f;         // and at a piece's first (verify of 48 rows a unit: 8 of
+                                           // 8 tiles moved a reference at 12, 2 of 8 at 10)
 constexpr float kMost = 15.0f;             // log2 of the largest weight that fits fp16
 constexpr float kNoRef = -1.0e38f;         // reference of a row that has seen nothing
 constexpr float kMinScale = 8.67361737988403547e-19f;   // 2^-60
@@ -90,6 +92,7 @@ struct Desc {
   Div n_out;
   int layout, local, causal;
   int num_pages, max_pages, lg_block;
+  int room;            // tokens of a context that its block-table row has pages for
   int lg_run;          // log2 of the consecutive slots of a tile that share a scale
   int nv;              // page boxes per 64 slots: shards of a whole-request interleaved cache, else 1
   float scale_log2;
@@ -145,9 +148,10 @@ __device__ __forceinline__ Unit make_unit(const Desc& d, int u) {
   x.L = max(d.seq_lens[x.b], 0);
   x.qn = d.q_lens ? min(max(d.q_lens[x.b], 0), d.q_len) : d.q_len;
   x.live = min(max(x.qn * d.G - x.r0, 0), x.rows);
+  const int room = min(x.L, d.room);           // a longer context is cut there and reported
   x.tstart = x.p0 = 0;
-  x.tend = x.L;
-  const int L = x.live > 0 ? x.L : 0;
+  x.tend = room;
+  const int L = x.live > 0 ? room : 0;
   int n;                                       // the shard's tokens
   if (d.layout == kInterleaved) {
     n = L > x.s ? (L - 1 - x.s) / d.num_shards + 1 : 0;
@@ -240,6 +244,7 @@ struct Smem {
   static constexpr bool kEarlyK = R > 16;
   static constexpr int kKStages = kEarlyK ? 4 : 6;
   static constexpr int kVStages = R == 48 ? 5 : 6;
+  static_assert(kEarlyK || kKStages == kVStages, "one ring");
   // The query's two terms side by side as 2R columns of one MMA chain, added
   // by the softmax, or (no columns left) as two chains into the same R.  Half
   // the MMAs to issue, about 100 cycles each, against an addition per logit:
@@ -553,22 +558,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 0 || warp == 3) {
     // ------------------------------------------------------------ producers
-    // warp 0 loads K, warp 3 loads V and the scales: with 8 shards a
-    // tile is 2 x 16 boxes of 1 KB, and one warp that issued all of them
-    // bounded the kernel (1 GB over 8 shards 320 us, two warps XXX us)
+    // warp 0 loads K, warp 3 V: a box costs the warp that issues it 100 cycles
+    // and more (1 GB over 8 shards, 2 x 16 boxes a tile: one warp 320 us, two
+    // 222 us)
     const bool is_v = warp == 3;
-    if (is_v) {
-      if (lane == 0) misc->rec = make_record(prefix, it.u, lo, hi, per);
-      for (int u = blockIdx.x; u < p.units; u += gridDim.x) {
-        if (prefix[u + 1] > prefix[u]) continue;
-        const Rows x = make_rows(d, u);          // no token in the shard: o = 0, lse = -inf
-        for (int r = 0; r < x.rows; ++r) {
-          const size_t row = out_row(d, x, r);
-          reinterpret_cast<float4*>(p.out + row * kD)[lane] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (lane == 0) p.lse[row] = -CUDART_INF_F;
-        }
-      }
-    }
+    if (is_v && lane == 0) misc->rec = make_record(prefix, it.u, lo, hi, per);
     const int nb = 2 * d.nv;                     // page boxes per tile
     const int rp = kPage / d.nv;                 // slots per box
     const int lg_rp = 31 - __clz(rp);
@@ -577,10 +571,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t* empty_bars = is_v ? misc->v_empty : misc->k_empty;
     const int stages = is_v ? kVStages : kKStages;
     const uint32_t dst0 = is_v ? sV : sK;
-    const int lg_sub = 6 - d.lg_block;           // scales per page and head
-    // 8 shards: 8 rows, 1 KB, of a page.  A box that small costs TMA about 64
-    // cycles, 32 of them a tile more than the tile's share of HBM; cp.async
-    // takes 8 lanes a row (1M tokens x 8 heads, 422 -> XXX us).
+    const int lg_sub = 6 - d.lg_block;           // log2 of the scales per page and head
+    // 8 shards: 8 rows, 1 KB, of a page.  32 such boxes take longer than the
+    // tile's share of HBM; cp.async takes 8 lanes a row instead (one request of
+    // 1M tokens x 8 heads: 422 us by boxes, 355 us by rows).
     const bool by_row = d.nv == 8;
     const size_t page_bytes = (size_t)kPage * d.Hkv * kD;
     const uint8_t* row_src = (is_v ? d.v : d.k) + 16 * (lane & 7);
@@ -590,6 +584,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int st = 0, round = 0;
     while (ok && it.next(unit, t0, t1, whole, slot)) {
       const Unit x = make_unit(d, unit);
+      if (x.L > d.room) atomicOr(&misc->err, kErrBadPage);
       const int32_t* bt = d.block_table + (size_t)x.b * d.max_pages;
       const int res = d.nv > 1 ? x.s : 0;
       auto entry = [&](int j) {                  // page of this lane's box of tile j, or -1
@@ -657,6 +652,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           st = 0;
           ++round;
         }
+      }
+    }
+    for (int u = blockIdx.x; is_v && u < p.units; u += gridDim.x) {
+      if (prefix[u + 1] > prefix[u]) continue;
+      const Rows x = make_rows(d, u);            // no token in the shard: o = 0, lse = -inf
+      for (int r = 0; r < x.rows; ++r) {
+        const size_t row = out_row(d, x, r);
+        reinterpret_cast<float4*>(p.out + row * kD)[lane] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (lane == 0) p.lse[row] = -CUDART_INF_F;
       }
     }
   } else if (warp == 1) {
@@ -1043,7 +1047,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         misc->f[0][r] = w0 * it_;
         misc->f[1][r] = w1 * it_;
         if (r < x.rows) {
-          const float v = none ? -CUDART_INF_F : (M + log2f(tot)) * 0.69314718055994530942f;
+          // the reference and the sum's exponent nearly cancel where V's scales are
+          // far from 1 (M = -70, tot = 2^73 under a scale of 0): exact first
+          const int e = tot < INFINITY ? (__float_as_int(tot) >> 23) - 127 : 0;
+          const float lg = (M + (float)e) + log2f(ldexpf(tot, -e));
+          const float v = none ? -CUDART_INF_F : lg * 0.69314718055994530942f;
           if (whole) p.lse[query.orow[r]] = v;
           else p.ws_lse[sl * kRows + r] = v;
         }
@@ -1368,6 +1376,12 @@ mla_status gqa_decode_partial_fp8(const void* q, const gqa_block_pages* cache,
   host::EncodeTiledFn encode = host::encode_fn();
   if (encode == nullptr) return MLA_ERR_CUDA;
 
+  // work positions are 31-bit numbers
+  const long long slots = (long long)max_pages_per_req * kPage;
+  const long long room = std::min((local ? num_shards : 1) * slots, (long long)INT_MAX);
+  const long long tiles = (local ? slots : slots / num_shards) / gqa8::kTok + 3;
+  if (sp.units * (tiles + gqa8::kUnitCost) >= (1LL << 31)) return MLA_ERR_UNSUPPORTED;
+
   gqa8::Desc d;
   d.B = shape->batch;
   d.q_len = shape->q_len;
@@ -1384,6 +1398,7 @@ mla_status gqa_decode_partial_fp8(const void* q, const gqa_block_pages* cache,
   d.causal = shape->causal;
   d.num_pages = cache->num_pages;
   d.max_pages = max_pages_per_req;
+  d.room = (int)room;
   d.lg_block = 0;
   while ((1 << d.lg_block) < cache->block) ++d.lg_block;
   d.scale_log2 = shape->softmax_scale * 1.4426950408889634f;

@@ -408,22 +408,11 @@ __host__ __device__ __forceinline__ uint64_t sw64_desc(uint32_t saddr, uint32_t 
   return d;
 }
 
-// The same with 32-byte swizzling (MN-major: LBO between 32-byte MN blocks,
-// SBO between 8-row K groups), and without swizzling (MN-major: SBO between
-// 16-byte MN blocks, LBO between 8-row K groups).
-__host__ __device__ __forceinline__ uint64_t sw32_desc(uint32_t saddr, uint32_t lbo,
-                                                       uint32_t sbo) {
-  uint64_t d = 0;
-  d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
-  d |= (uint64_t)((lbo >> 4) & 0x3FFFu) << 16;
-  d |= (uint64_t)((sbo >> 4) & 0x3FFFu) << 32;
-  d |= (uint64_t)1 << 46;   // descriptor version for tcgen05
-  d |= (uint64_t)6 << 61;   // 32-byte swizzle
-  return d;
-}
+// The same without swizzling (MN-major: SBO between 16-byte MN blocks, LBO
+// between 8-row K groups).
 __host__ __device__ __forceinline__ uint64_t sw0_desc(uint32_t saddr, uint32_t lbo,
                                                       uint32_t sbo) {
-  return sw32_desc(saddr, lbo, sbo) & ~((uint64_t)7 << 61);
+  return sw128_desc(saddr, lbo, sbo) & ~((uint64_t)7 << 61);
 }
 
 // Instruction descriptor, kind::f16 with bf16 A/B and fp32 D.

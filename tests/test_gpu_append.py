@@ -556,3 +556,102 @@ def test_append_and_attention_in_one_graph(mla):
         torch.cuda.synchronize()
         assert torch.equal(out[0], eager[t][0]) and torch.equal(out[1], eager[t][1])
     assert all(torch.equal(dg[n], d[n]) for n in d)
+
+
+@pytest.mark.parametrize("positions", [[3], [-70000], [1000003]])
+def test_frequencies_of_every_size(mla, positions):
+    """Zero, negative, above a turn per token, far below any angle."""
+    w = torch.tensor([0.0, -0.3, 100.0, 2 * math.pi, 1e-300, 1e-12, 7.0, 0.5], dtype=torch.float64)
+    rope = mla.Rope(w.cuda(), 8, True, 1.25)
+    x = bf((1, 1, 3, 32), 50)
+    got = mla.mla_rope_apply(x.cuda(), rope, positions=i32([positions]).cuda())
+    v = x[0, 0].double()
+    y = turn(v, positions[0], w, 8, True, 1.25)
+    # the 64-bit reference's own angle is off by 2^-53 of up to 2^26.6 rad
+    e = turn_error(v, 8, 8, True, 1.25) * (1 + 2.0 ** -4)
+    assert bool(((got[0, 0].cpu().double() - y).abs() <= y.abs() * 2.0 ** -8 * (e > 0) + e).all())
+
+
+@pytest.mark.parametrize("Hkv,block", [(1, 64), (5, 32), (9, 16), (9, 2), (3, 8), (2, 4)])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_gqa_append_of_part_of_the_head(mla, Hkv, block, interleaved):
+    """Heads that do not fill a block's warps, dims 16..111 turned, appends
+    that end, start and stay inside blocks of scales."""
+    lens, q_lens, q_len = [130, 67, 40, 64, 65], [130, 3, 40, 1, 33], 130
+    P, bt = table(lens, seed=Hkv)
+    c = pool(P, Hkv, block, True, 51)
+    k, v = bf((5, q_len, Hkv, 128), 52), bf((5, q_len, Hkv, 128), 53, 0.01)
+    rope = rope_of(mla, 96, 16, interleaved)
+    got, _ = run_gqa(mla, c, k, v, bt, lens, q_lens, rope, True)
+    check_gqa(got, c, expect_gqa(c, k, v, bt, lens, q_lens, rope, block, True), block, True)
+
+
+def test_infinities_beside_wide_foreign_scales(mla):
+    """An infinity among values under a scale that is kept, and in another
+    head's tokens only."""
+    P, bt = table([70])
+    c = pool(P, 2, 64, True, 54)
+    pg = int(bt[0, 1])
+    for n in "kv":
+        c[n + "s"][pg] = 1000.0
+    x = bf((1, 3, 2, 128), 55)
+    x[0, 1, 0, 7], x[0, 2, 0, 100], x[0, 0, 0, 8] = math.inf, -math.inf, math.nan
+    got, _ = run_gqa(mla, c, x, x, bt, [69], None, None, True)
+    check_gqa(got, c, expect_gqa(c, x, x, bt, [69], None, None, 64, True), 64, True)
+
+
+def test_appends_on_a_given_stream(mla):
+    """The workspace and q_out that a call allocates belong to its stream."""
+    lens = [30, 90]
+    P, bt = table(lens)
+    c = pool(P, 2, 32, True, 56)
+    k, q = bf((2, 3, 2, 128), 57), bf((2, 3, 4, 128), 58)
+    rope = rope_of(mla, 128)
+    want, q_want = run_gqa(mla, c, k, k, bt, lens, None, rope, True, q=q)
+    d = {n: t.clone().cuda() for n, t in c.items()}
+    dk, dq, dbt, dl = k.cuda(), q.cuda(), bt.cuda(), i32(lens).cuda()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    q_out, ws = mla.gqa_cache_append(dk, dk, d["k"], d["v"], dbt, dl, rope, q=dq, k_scale=d["ks"],
+                                     v_scale=d["vs"], stream=side)
+    q_two = mla.mla_rope_apply(dq, rope, dl, stream=side)
+    side.synchronize()
+    assert mla.mla_get_device_error(ws) == 0
+    assert all(torch.equal(d[n].cpu(), want[n]) for n in d)
+    assert torch.equal(q_out.cpu(), q_want) and torch.equal(q_two.cpu(), q_want)
+
+
+def test_append_binding_refusals(mla):
+    P, bt = table([30, 90])
+    c = {n: t.cuda() for n, t in pool(P, 2, 32, True, 59).items()}
+    k, q = bf((2, 3, 2, 128), 60).cuda(), bf((2, 3, 4, 128), 61).cuda()
+    bt, lens, rope = bt.cuda(), i32([30, 90]).cuda(), rope_of(mla, 128)
+
+    def heads(**kw):
+        a = dict(k=k, v=k, k_cache=c["k"], v_cache=c["v"], block_table=bt, seq_lens=lens, rope=rope,
+                 q=q, k_scale=c["ks"], v_scale=c["vs"])
+        return mla.gqa_cache_append(**{**a, **kw})
+
+    for kw in (dict(k=k[..., :64]), dict(v=k[:1]), dict(k=k.float()), dict(k=k.transpose(1, 2)),
+               dict(q=q[:, :1]), dict(q=q[..., :64]), dict(q=None, q_out=q), dict(q_out=q[:, :, :2]),
+               dict(q_out=q.flatten()[128:].expand(2, 3, 4, -1)), dict(block_table=bt[:1]),
+               dict(seq_lens=None), dict(seq_lens=lens.long()), dict(k_scale=None),
+               dict(k_scale=c["ks"][:, :1]), dict(v_cache=c["v"][:1]),
+               dict(positions=i32([[1, 2, 3]]).cuda()), dict(workspace=torch.zeros(300, device="cuda"))):
+        with pytest.raises((TypeError, ValueError)):
+            heads(**kw)
+    wide = torch.zeros(2, 3, 5, 128, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(ValueError):            # shifted by one head
+        mla.mla_rope_apply(wide[:, :, :4], rope, lens, out=wide[:, :, 1:])
+    with pytest.raises(ValueError):
+        mla.mla_rope_apply(q, rope)
+    with pytest.raises(TypeError):
+        mla.mla_rope_apply(q, None, lens)
+    with pytest.raises(mla.MLAError):
+        heads(rope=None)                       # a query without a rotation
+    with pytest.raises(mla.MLAError):
+        heads(shard_id=2, num_shards=2)
+    with pytest.raises(ValueError):
+        mla.Rope(rope.inv_freq[::2])
+    with pytest.raises(TypeError):
+        mla.Rope(rope.inv_freq.float())

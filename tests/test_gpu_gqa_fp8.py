@@ -283,3 +283,127 @@ def test_wait_budget_runs_out_and_the_next_call_is_clean(mla):
         part, lse, st = call(mla, w)
         assert st == 0
         check_attention(part[0], lse[0], ref(w))
+
+
+@pytest.mark.parametrize("H,N", [(1, 1), (16, 1), (48, 1), (2, 8)])
+def test_one_request_over_every_cta(mla, H, N):
+    """20000 tokens over one KV head: about 80 pieces to a unit, more than it
+    has rows, joined by the blocks of all the CTAs that share it."""
+    check(mla, make([20000], H, 1, seed=87 + H), N)
+
+
+def test_a_long_context_among_short_ones(mla):
+    """Units of many pieces, of one and of none side by side."""
+    check(mla, make([3, 15000, 0, 700, 129], 12, 2, 32, q_len=4, seed=91), 2, causal=True)
+
+
+def test_bad_pages_at_eight_shards(mla):
+    w = make([300, 70], 8, 2, 32, seed=92)
+    w["bt"][0, 2] = w["k"].shape[0]
+    w["bt"][1, 0] = -1
+    part, lse, st = call(mla, w, 8)
+    assert st == -5
+    for s in range(8):
+        o, l, spread, err = ref(w, 8, s=s)
+        # a token of a missing page has V scale 0, which stands as lv = -60 in
+        # its weight's exponent s + lv - m (log2 units); here |lv - m| < 64, so
+        # lv - m and the exponent are each rounded by up to 2^-19: 2^-18 ln 2
+        check_attention(part[s], lse[s], (o, l, spread, err + 2.0 ** -18 * math.log(2.0)))
+
+
+def test_eight_shards_of_many_rows(mla):
+    check(mla, make([400, 7, 1300], 40, 1, 16, seed=93), 8)
+    check(mla, make([500, 90], 16, 2, 64, q_len=9, seed=94), 8, causal=True)
+
+
+def test_context_longer_than_its_table(mla):
+    """It is cut at its last page and reported; the others are whole."""
+    w = make([200, 300], 8, 2, seed=95)
+    w["bt"] = w["bt"][:, :4].contiguous()
+    w["lens"] = torch.tensor([200, 2 ** 31 - 1], dtype=torch.int32)
+    part, lse, st = call(mla, w)
+    assert st == -5
+    w["lens"] = torch.tensor([200, 256], dtype=torch.int32)
+    check_attention(part[0], lse[0], ref(w))
+
+
+def test_work_that_passes_31_bits_is_refused(mla):
+    w = make([20] * 64, 64, 64, seed=96)
+    w["bt"] = torch.zeros(64, 1 << 20, dtype=torch.int32)
+    with pytest.raises(mla.MLAError) as e:
+        call(mla, w, 2)
+    assert e.value.status == -2
+
+
+def test_memory_of_a_call_on_a_given_stream(mla):
+    """Outputs and workspace that a call allocates belong to its stream."""
+    w = make([900, 333], 16, 2, seed=97)
+    d = {n: t.cuda() for n, t in w.items()}
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    part, lse, ws = mla.gqa_decode_partial_fp8(d["q"], d["k"], d["v"], d["ks"], d["vs"], d["bt"],
+                                               d["lens"], 2, stream=side)
+    out, lse_out = mla.gqa_shard_combine(part, lse, stream=side)
+    assert torch.cuda.current_stream() != side
+    side.synchronize()
+    assert mla.mla_get_device_error(ws) == 0
+    check_attention(out, lse_out, ref(w, 1, "interleaved", -1), out_rel=2.0 ** -8)
+
+
+def test_two_graphs_with_one_workspace(mla):
+    """Replayed in turn, over a workspace of arbitrary bytes."""
+    ws = torch.full((mla.gqa_fp8_workspace_size(2, 2, 48, 1, 2),), 0xFF, dtype=torch.uint8,
+                    device="cuda")
+    runs = []
+    for seed, lens in ((98, [3000, 5]), (99, [64, 1700])):
+        w = make(lens, 48, 1, q_len=2, seed=seed)
+        d = {n: t.cuda() for n, t in w.items()}
+
+        def go():
+            return mla.gqa_decode_partial_fp8(d["q"], d["k"], d["v"], d["ks"], d["vs"], d["bt"],
+                                              d["lens"], 2, causal=True, workspace=ws)
+
+        go()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            part, lse, _ = go()
+        runs.append((w, d, g, part, lse))
+    for _ in range(2):
+        for w, d, g, part, lse in runs:
+            part.fill_(float("nan"))
+            g.replay()
+    torch.cuda.synchronize()
+    for w, d, g, part, lse in runs:
+        for s in range(2):
+            check_attention(part[s], lse[s], ref(w, 2, s=s, causal=True))
+
+
+def test_binding_refusals(mla):
+    w = {n: t.cuda() for n, t in make([100, 40], 8, 2, seed=100).items()}
+    args = lambda **k: [{**w, **k}[n] for n in ("q", "k", "v", "ks", "vs", "bt", "lens")]
+    bad = [dict(q=w["q"].float()), dict(k=w["k"][..., :64]), dict(v=w["v"][:1]),
+           dict(ks=w["ks"].double()), dict(vs=w["vs"][:, :, :1]), dict(bt=w["bt"].cpu()),
+           dict(lens=w["lens"].long()), dict(lens=w["lens"][:1]), dict(bt=w["bt"][:1]),
+           dict(q=w["q"].transpose(1, 2)), dict(k=w["k"].view(torch.int8))]
+    for k in bad:      # (the transposed q is [2, 8, 1, 128]: one head for two KV heads)
+        with pytest.raises((TypeError, ValueError, mla.MLAError)):
+            mla.gqa_decode_partial_fp8(*args(**k), 1)
+    for k in (dict(out_partial=torch.empty(1, 2, 1, 8, 64, device="cuda")),
+              dict(lse_partial=torch.empty(2, 2, 1, 8, device="cuda")),
+              dict(workspace=torch.empty(16, device="cuda")), dict(q_lens=w["lens"][:1])):
+        with pytest.raises((TypeError, ValueError)):
+            mla.gqa_decode_partial_fp8(*args(), 1, **k)
+    with pytest.raises(KeyError):
+        mla.gqa_decode_partial_fp8(*args(), 1, "diagonal")
+    with pytest.raises(mla.MLAError):
+        mla.gqa_decode_partial_fp8(*args(), 9)
+    with pytest.raises(mla.MLAError):
+        mla.gqa_decode_partial_fp8(*args(), 1, workspace=torch.empty(64, dtype=torch.uint8,
+                                                                     device="cuda"))
+    part, lse, _ = mla.gqa_decode_partial_fp8(*args(), 2)
+    for k in (dict(lses=lse[:1]), dict(out=torch.empty(2, 1, 8, 64, dtype=torch.bfloat16, device="cuda")),
+              dict(out=torch.empty(2, 1, 8, 128, dtype=torch.bfloat16)),
+              dict(lse_out=torch.empty(2, 1, 4, device="cuda"))):
+        with pytest.raises(ValueError):
+            mla.gqa_shard_combine(part, k.pop("lses", lse), **k)
