@@ -1267,11 +1267,12 @@ bool shards_ok(int num_shards, int shard_id) {
 }
 
 // Query rows per work unit: all of a KV head's q_len * G rows of a request up
-// to 48, in the smallest tile that holds them; more rows go to groups of even
-// size, 32 at most.  16 requests x 6400 tokens x 4 heads, us with groups of up
-// to 48 and 32 rows: 36 rows 47 and 55, 48 rows 47 and 55, 64 rows 57 and 57,
-// 72 rows 77 and 79, 96 rows 77 and 77, 126 rows 107 and 100; a ragged 9-token
-// verify of up to 72 rows 120 and 111.
+// to 48, in the smallest tile that holds them; more rows go to groups of 32.
+// 16 requests x 6400 tokens x 4 heads, us with groups of up to 48 and 32 rows:
+// 36 rows 50 and 55, 48 rows 52 and 55, 64 rows 80 and 58, 72 rows 83 and 81,
+// 96 rows 83 and 80, 126 rows 115 and 103.  Full groups and a rest, not groups
+// of even size, as a padded batch's requests often need no rest: a ragged
+// verify of up to 72 rows 93 us, in three groups of 24 rows 110.
 struct Split {
   int R, rg, Gq, units;
 };
@@ -1280,7 +1281,7 @@ Split split_for(const gqa_shape* s, int num_shards, int shard_id) {
   const int n = s->q_len * (s->num_heads / s->num_kv_heads);
   Split x;
   x.Gq = n <= 48 ? 1 : ceil_div(n, 32);
-  x.rg = ceil_div(n, x.Gq);
+  x.rg = x.Gq == 1 ? n : 32;
   x.R = ceil_div(x.rg, 16) * 16;
   x.units = s->batch * (shard_id == MLA_ALL_SHARDS ? num_shards : 1) * s->num_kv_heads * x.Gq;
   return x;
