@@ -297,15 +297,15 @@ __global__ void __launch_bounds__(kThreads, 10) gqa_append_kernel(const uint16_t
 
 // --------------------------------------------------------------- K/V, e4m3
 // A block takes one block of token slots of a request that the new tokens
-// touch, K or V, and as many KV heads as its eight warps hold: a warp has 16
+// touch, K or V, and as many KV heads as its four warps hold: a warp has 16
 // tokens of a head (8 dims a lane, two tokens a load) in registers, from the
 // one read to the codes, so a head takes block / 16 warps.  The block's warps
 // share one table of its tokens' sines and cosines: computed for every head
 // again (one head a block), they cost more than the memory does (2 x 4099
 // tokens x 8 heads, 23.5 us against 12.7, and 10.7 with fewer operations a value).
-constexpr int kF8Warps = 8;
+constexpr int kF8Warps = 4;
 
-__global__ void __launch_bounds__(32 * kF8Warps, 2)
+__global__ void __launch_bounds__(32 * kF8Warps, 4)
     gqa_append_fp8_kernel(const uint16_t* k, long long ks, const uint16_t* v, long long vs, Cache c,
                           Tokens t, RopeArgs r, Rows q, int cache_blocks, Div nblk, Div hgroups,
                           Div wph) {
