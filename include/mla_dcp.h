@@ -514,7 +514,11 @@ size_t gqa_fp8_workspace_size(const gqa_shape* shape, int num_shards, int shard_
  * -inf, and with causal query i sees t <= L_b - q_lens[b] + i.  With
  * INTERLEAVED num_shards must divide 64.  An inf or NaN query value of a row
  * that attends is reported as MLA_ERR_RANGE; a block-table entry out of range
- * reads as zeros and is reported as MLA_ERR_DEVICE_BOUNDS.
+ * reads as zeros, and a context longer than its block-table row is cut at the
+ * row's end, both reported as MLA_ERR_DEVICE_BOUNDS.  Shapes whose work could
+ * pass 2^31 tiles (units times pages per row) are MLA_ERR_UNSUPPORTED.
+ * The workspace may hold anything before a call, and serves one call at a
+ * time; mla_get_device_error reads the last call's errors from it.
  */
 mla_status gqa_decode_partial_fp8(const void* q, const gqa_block_pages* cache,
                                   const int32_t* block_table, int max_pages_per_req,
