@@ -328,7 +328,7 @@ def test_context_longer_than_its_table(mla):
 
 
 def test_work_that_passes_31_bits_is_refused(mla):
-    w = make([20] * 64, 64, 64, seed=96)
+    w = make([20] * 64, 65, 65, seed=96)      # (an odd number of heads: no teams)
     w["bt"] = torch.zeros(64, 1 << 20, dtype=torch.int32)
     with pytest.raises(mla.MLAError) as e:
         call(mla, w, 2)
