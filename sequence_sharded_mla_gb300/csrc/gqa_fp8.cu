@@ -594,7 +594,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // tile's share of HBM; cp.async takes 8 lanes a row instead (one request of
     // 1M tokens x 8 heads: 422 us by boxes, 355 us by rows).
     const bool by_row = d.nv == 8;
-    const size_t page_bytes = (size_t)kPage * d.Hkv * kD;
+    const unsigned page_bytes = kPage * d.Hkv * kD;
     const uint8_t* row_src = (is_v ? d.v : d.k) + 16 * (lane & 7);
     const uint32_t row_dst0 = (lane >> 3) * 128 + (((lane & 7) ^ (lane >> 3)) << 4);
     const uint32_t row_dst1 = row_dst0 + 4 * 128 - 2 * (row_dst0 & 64) + 64;   // row + 4, chunk ^ 4
@@ -624,23 +624,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (by_row) {
           if (lane == 0) mbar_arrive(full);
           const uint8_t* src = row_src + (size_t)((res + 8 * (lane >> 3)) * d.Hkv + x.kh) * kD;
-          const size_t off = there ? (size_t)page * page_bytes : 0;
-          const uint32_t off_lo = (uint32_t)off, off_hi = (uint32_t)(off >> 32), bytes = there ? 16 : 0;
           const int step = 32 * d.Hkv * kD;
 #pragma unroll
           for (int b0 = 0; b0 < 16; b0 += 8) {
-            uint32_t lo[8], hi[8], s[8];
+            int pg[8];
+#pragma unroll
+            for (int b = 0; b < 8; ++b) pg[b] = __shfl_sync(0xffffffffu, page, b0 + b);
 #pragma unroll
             for (int b = 0; b < 8; ++b) {
-              lo[b] = __shfl_sync(0xffffffffu, off_lo, b0 + b);
-              hi[b] = __shfl_sync(0xffffffffu, off_hi, b0 + b);
-              s[b] = __shfl_sync(0xffffffffu, bytes, b0 + b);
-            }
-#pragma unroll
-            for (int b = 0; b < 8; ++b) {
-              const uint8_t* from = src + (((size_t)hi[b] << 32) | lo[b]);
-              cp_async_16_zfill(dst + (b0 + b) * 1024 + row_dst0, from, s[b]);
-              cp_async_16_zfill(dst + (b0 + b) * 1024 + row_dst1, from + step, s[b]);
+              const uint8_t* from = src + (size_t)(unsigned)pg[b] * page_bytes;
+              const uint32_t bytes = pg[b] < d.num_pages ? 16 : 0;
+              cp_async_16_zfill(dst + (b0 + b) * 1024 + row_dst0, from, bytes);
+              cp_async_16_zfill(dst + (b0 + b) * 1024 + row_dst1, from + step, bytes);
             }
           }
         } else {
