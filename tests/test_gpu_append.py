@@ -655,3 +655,50 @@ def test_append_binding_refusals(mla):
         mla.Rope(rope.inv_freq[::2])
     with pytest.raises(TypeError):
         mla.Rope(rope.inv_freq.float())
+
+
+def test_a_graph_with_copies_and_fills_between_the_calls(mla):
+    """Launches that may begin early, behind a copy and behind the clearing of
+    the workspace that the call allocates."""
+    lens, H, Hkv = [30, 90], 4, 2
+    P, bt = table([x + 8 for x in lens])
+    c = pool(P, Hkv, 32, True, 62)
+    steps = [(bf((2, 1, Hkv, 128), 63 + i), bf((2, 1, H, 128), 73 + i)) for i in range(3)]
+    rope = rope_of(mla, 128)
+    dbt, dl = bt.cuda(), i32(lens).cuda()
+    d = {n: t.clone().cuda() for n, t in c.items()}
+    k, q, src_k, src_q = (t.clone().cuda() for t in (*steps[0], *steps[0]))
+
+    def step():
+        k.copy_(src_k)
+        q.copy_(src_q)
+        dl.add_(1)
+        q_out, ws = mla.gqa_cache_append(k, k, d["k"], d["v"], dbt, dl, rope, q=q, k_scale=d["ks"],
+                                         v_scale=d["vs"])
+        part, lse, ws2 = mla.gqa_decode_partial_fp8(q_out, d["k"], d["v"], d["ks"], d["vs"], dbt, dl, 2)
+        return mla.gqa_shard_combine(part, lse), ws, ws2
+
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        step()
+    side.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        (out, lse_out), ws, ws2 = step()
+    for n, t in c.items():
+        d[n].copy_(t)
+    dl.copy_(i32(lens))
+    for i, (dk, dq) in enumerate(steps):
+        src_k.copy_(dk)
+        src_q.copy_(dq)
+        g.replay()
+        torch.cuda.synchronize()
+        assert mla.mla_get_device_error(ws) == 0 and mla.mla_get_device_error(ws2) == 0
+        now = [x + i + 1 for x in lens]
+        before = {n: t.clone() for n, t in c.items()}
+        c, q_want = run_gqa(mla, c, dk, dk, bt, now, None, rope, True, q=dq)
+        check_gqa(c, before, expect_gqa(before, dk, dk, bt, now, None, rope, 32, True), 32, True)
+        assert all(torch.equal(d[n].cpu(), c[n]) for n in c)
+        ref = attend(q_want, c["k"], c["v"], c["ks"], c["vs"], bt, now, None, False, 128 ** -0.5, 1, -1,
+                     "interleaved")
+        check_attention(out, lse_out, ref, out_rel=2.0 ** -8)

@@ -407,3 +407,19 @@ def test_binding_refusals(mla):
               dict(lse_out=torch.empty(2, 1, 4, device="cuda"))):
         with pytest.raises(ValueError):
             mla.gqa_shard_combine(part, k.pop("lses", lse), **k)
+
+
+def test_teams_behind_the_plan_kernel(mla):
+    """800 requests over two heads: a plan of 800 units for teams of two."""
+    g = torch.Generator().manual_seed(101)
+    lens = torch.randint(0, 200, (800,), generator=g).tolist()
+    w = make(lens, 6, 2, 16, seed=102)
+    part, lse, st = call(mla, w)
+    assert st == 0
+    check_attention(part[0], lse[0], ref(w))
+
+
+@pytest.mark.parametrize("Hkv", [1, 2, 3, 4, 6, 8, 12, 16])
+def test_teams_of_every_size(mla, Hkv):
+    """Split, whole and empty units of 1, 2, 4 and 8 CTAs a team."""
+    check(mla, make([2500, 0, 31, 200], 2 * Hkv, Hkv, 32, q_len=2, seed=103 + Hkv), 2, causal=True)
