@@ -688,7 +688,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else {
         if (pc >= 2 && !(ok = wait(&misc->q_empty[buf], ((pc >> 1) - 1) & 1))) break;
         fetch_query(make_rows(d, unit, member), buf, 0, R);
-        for (int r0 = 0; r0 < R; r0 += 4) split_query(buf, r0, std::integral_constant<int, 4>());
+        #pragma unroll 1
+        for (int r0 = 0; r0 < R; r0 += 8) split_query(buf, r0, std::integral_constant<int, 8>());
         if (lane < 8) mbar_arrive(bar(&misc->q_full[buf]));
       }
       const uint64_t dq = sw128_desc(sQ + buf * S::kQBuf, 16, 1024);
@@ -866,12 +867,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           move = named_bar_or(kBarGroup + grp, kGroupThreads, mx > kMost || !ok_s);
         }
         // A weight would pass 2^kMost: the logits without references, for new
-        // ones, then against those (one body for both: it runs seldom, and
-        // code that runs seldom costs its own fetch).
-        for (bool raw = true; move;) {
-          if (ok_s) all_logits(raw ? 0.0f : 1.0f);
-          if (!raw) break;
-          raw = false;
+        // ones, which are then taken off them.
+        if (move) {
+          if (ok_s) all_logits(0.0f);
           // ---------------------------------------------- new references
           if (ok_s) {
 #pragma unroll
@@ -907,34 +905,40 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = false;
             break;
           }
-          if (first) continue;
-          tc_fence_after();
+          if (!first) {
+            tc_fence_after();
 #pragma unroll
-          for (int r = 0; r < R / 2; ++r)
-            l[r] = mul2(l[r], make_float2(misc->f[grp][2 * r], misc->f[grp][2 * r + 1]));
+            for (int r = 0; r < R / 2; ++r)
+              l[r] = mul2(l[r], make_float2(misc->f[grp][2 * r], misc->f[grp][2 * r + 1]));
 #pragma unroll 1
-          for (int r0 = 0; r0 < R; r0 += 16) {
-            if (!misc->moved[grp][r0 >> 4]) continue;
-            const float4* f4 = reinterpret_cast<const float4*>(misc->f[grp] + r0);
+            for (int r0 = 0; r0 < R; r0 += 16) {
+              if (!misc->moved[grp][r0 >> 4]) continue;
+              const float4* f4 = reinterpret_cast<const float4*>(misc->f[grp] + r0);
 #pragma unroll 1
-            for (int term = 0; term < 3; ++term) {
-              uint32_t v[16];
-              tmem_ld16(tO + 3 * R * grp + R * term + r0, v);
-              tmem_wait_ld();
+              for (int term = 0; term < 3; ++term) {
+                uint32_t v[16];
+                tmem_ld16(tO + 3 * R * grp + R * term + r0, v);
+                tmem_wait_ld();
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const float4 f = f4[k];
-                v[4 * k] = __float_as_uint(__uint_as_float(v[4 * k]) * f.x);
-                v[4 * k + 1] = __float_as_uint(__uint_as_float(v[4 * k + 1]) * f.y);
-                v[4 * k + 2] = __float_as_uint(__uint_as_float(v[4 * k + 2]) * f.z);
-                v[4 * k + 3] = __float_as_uint(__uint_as_float(v[4 * k + 3]) * f.w);
+                for (int k = 0; k < 4; ++k) {
+                  const float4 f = f4[k];
+                  v[4 * k] = __float_as_uint(__uint_as_float(v[4 * k]) * f.x);
+                  v[4 * k + 1] = __float_as_uint(__uint_as_float(v[4 * k + 1]) * f.y);
+                  v[4 * k + 2] = __float_as_uint(__uint_as_float(v[4 * k + 2]) * f.z);
+                  v[4 * k + 3] = __float_as_uint(__uint_as_float(v[4 * k + 3]) * f.w);
+                }
+                tmem_st16(tO + 3 * R * grp + R * term + r0, v);
               }
-              tmem_st16(tO + 3 * R * grp + R * term + r0, v);
             }
+            tmem_wait_st();
           }
-          tmem_wait_st();
+#pragma unroll
+          for (int k = 0; k < R / 4; ++k) {
+            const float4 m = reinterpret_cast<const float4*>(ref)[k];
+            b[2 * k] = add2(b[2 * k], make_float2(m.x, m.y));
+            b[2 * k + 1] = add2(b[2 * k + 1], make_float2(m.z, m.w));
+          }
         }
-        if (!ok) break;
         // ------------------------------------------------------- weights
         tc_fence_before();                         // the logits are in registers
         __syncwarp();
