@@ -80,10 +80,10 @@ constexpr int kGroupThreads = 128;
 constexpr uint32_t kBarAll = 1, kBarGroup = 2;   // group g: kBarGroup + g
 constexpr int kMinTilesPerCta = 2;
 // Tiles that a unit's start and end are worth when units are shared out; us at
-// 2, 4, 6, 8: 32 requests x 20000 tokens x 4 heads 117, -, 113, 116; a ragged
-// 9-token verify 113, -, 109, 111; seven requests of up to 5000 tokens, one row
-// a head 16.9, 14.0, 14.7, 15.1.
-constexpr int kUnitCost = 6;
+// 3, 4, 5, 6: 32 requests x 20000 tokens x 4 heads 112.7, 112.4, 113.5, 113.5; a
+// ragged 9-token verify 81.8, 82.1, 82.3, 82.0; seven requests of up to 5000
+// tokens, one row a head 15.7, 14.3, 14.6, 14.6.
+constexpr int kUnitCost = 4;
 constexpr int kMaxR = 48;                  // query rows of the largest work unit
 constexpr int kMaxOwnPlan = 768;           // units that every CTA plans for itself
 constexpr int kOwnPerThread = (kMaxOwnPlan + kThreads - 1) / kThreads;
