@@ -79,11 +79,6 @@ constexpr int kThreads = 384;
 constexpr int kGroupThreads = 128;
 constexpr uint32_t kBarAll = 1, kBarGroup = 2;   // group g: kBarGroup + g
 constexpr int kMinTilesPerCta = 2;
-// Tiles that a unit's start and end are worth when units are shared out; us at
-// 3, 4, 5, 6: 32 requests x 20000 tokens x 4 heads 112.7, 112.4, 113.5, 113.5; a
-// ragged 9-token verify 81.8, 82.1, 82.3, 82.0; seven requests of up to 5000
-// tokens, one row a head 15.7, 14.3, 14.6, 14.6.
-constexpr int kUnitCost = 4;
 constexpr int kMaxR = 48;                  // query rows of the largest work unit
 constexpr int kMaxOwnPlan = 768;           // units that every CTA plans for itself
 constexpr int kOwnPerThread = (kMaxOwnPlan + kThreads - 1) / kThreads;
@@ -101,6 +96,7 @@ struct Desc {
   Div Hg;              // teams' worth of KV heads: Hkv >> lg_team
   Div G;
   int rg;              // query rows per group
+  int unit_cost;       // tiles that a unit's start and end are worth
   Div Gq;              // row groups per (request, KV head)
   Div num_shards;
   int shard_first;
@@ -237,10 +233,11 @@ struct Misc {
 // A CTA whose first tile is not its unit's first: (unit, 2 c0 + slot of c0's
 // piece, pieces, error bits), c0 being the team of the unit's first piece; team
 // c0 + k holds piece k, in slot 0.  Other CTAs: unit -1.
-__device__ __forceinline__ int4 make_record(const int* prefix, int u, int lo, int hi, int per) {
+__device__ __forceinline__ int4 make_record(const int* prefix, int u, int lo, int hi, int per,
+                                            int unit_cost) {
   int4 r = make_int4(-1, 0, 0, 0);
   if (lo >= hi) return r;
-  const int us = unit_tile_start(prefix, u, kUnitCost), ue = prefix[u + 1];
+  const int us = unit_tile_start(prefix, u, unit_cost), ue = prefix[u + 1];
   if (lo <= us || lo >= ue) return r;
   const int c0 = us / per;
   r.x = u;
@@ -298,7 +295,7 @@ __global__ void __launch_bounds__(1024) gqa_fp8_plan_kernel(Desc d, WsHeader* hd
       if (d.q_lens[b] < 1 || d.q_lens[b] > d.q_len) atomicOr(&bad, kErrQLens);
   __syncthreads();
   plan_units(d.B * d.n_out * d.Hg * d.Gq, [&](int u) { return make_unit(d, u, 0).tiles; }, hdr,
-             prefix, teams, kMinTilesPerCta, kUnitCost, 0u);
+             prefix, teams, kMinTilesPerCta, d.unit_cost, 0u);
   if (threadIdx.x == 0) *rec = make_int4(-1, 0, 0, (int)bad);
 }
 
@@ -465,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       cost[k] = 0;
       if (k < upt && u0 + k < p.units) {
         const int t = make_unit(d, u0 + k, 0).tiles;
-        cost[k] = t > 0 ? t + kUnitCost : 0;
+        cost[k] = t > 0 ? t + d.unit_cost : 0;
       }
       sum += cost[k];
     }
@@ -505,7 +502,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int lo = team * per, hi = min(lo + per, W);   // no piece if lo >= W
 
   PieceIter it;
-  it.init_warp(prefix, p.units, lo, hi, kUnitCost, lane);
+  it.init_warp(prefix, p.units, lo, hi, d.unit_cost, lane);
   int armed[kMaxStages];                         // the round a producer last filled a stage in
   for (int st = 0; st < kMaxStages; ++st) armed[st] = -1;
   int unit, t0, t1, slot;
@@ -580,7 +577,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // and more (1 GB over 8 shards, 2 x 16 boxes a tile: one warp 320 us, two
     // 222 us)
     const bool is_v = warp == 3;
-    if (is_v && lane == 0) misc->rec = make_record(prefix, it.u, lo, hi, per);
+    if (is_v && lane == 0) misc->rec = make_record(prefix, it.u, lo, hi, per, d.unit_cost);
     const int nb = 2 * d.nv;                     // page boxes per tile
     const int rp = kPage / d.nv;                 // slots per box
     const int lg_rp = 31 - __clz(rp);
@@ -1292,8 +1289,14 @@ bool shards_ok(int num_shards, int shard_id) {
 // 96 rows 83 and 80, 126 rows 115 and 103.  Full groups and a rest, not groups
 // of even size, as a padded batch's requests often need no rest: a ragged
 // verify of up to 72 rows 93 us, in three groups of 24 rows 110.
+//
+// Work shared out by tiles: a unit's start and end are worth 4 tiles at 16 rows,
+// 6 above (us at 4 and 6: seven requests of up to 5000 tokens, one row a head,
+// 14.3 and 14.6; 32 requests x 20000 tokens x 4 heads, 16 rows, 112.4 and
+// 113.5; 16 requests x 6400 tokens x 4 heads of 48, 72 and 96 rows, 46 and 44.5,
+// 71 and 68, 71 and 68).
 struct Split {
-  int R, rg, Gq;
+  int R, rg, Gq, unit_cost;
   int lg_team, units;   // units a team
 };
 
@@ -1303,6 +1306,7 @@ Split split_for(const gqa_shape* s, int num_shards, int shard_id, int grid) {
   x.Gq = n <= 48 ? 1 : ceil_div(n, 32);
   x.rg = x.Gq == 1 ? n : 32;
   x.R = ceil_div(x.rg, 16) * 16;
+  x.unit_cost = x.R == 16 ? 4 : 6;
   x.lg_team = 0;
   while (x.lg_team < 3 && ((s->num_kv_heads | grid) & (1 << x.lg_team)) == 0) ++x.lg_team;
   x.units = s->batch * (shard_id == MLA_ALL_SHARDS ? num_shards : 1) *
@@ -1404,7 +1408,7 @@ mla_status gqa_decode_partial_fp8(const void* q, const gqa_block_pages* cache,
   const long long slots = (long long)max_pages_per_req * kPage;
   const long long room = std::min((local ? num_shards : 1) * slots, (long long)INT_MAX);
   const long long tiles = (local ? slots : slots / num_shards) / gqa8::kTok + 3;
-  if (sp.units * (tiles + gqa8::kUnitCost) >= (1LL << 31)) return MLA_ERR_UNSUPPORTED;
+  if (sp.units * (tiles + sp.unit_cost) >= (1LL << 31)) return MLA_ERR_UNSUPPORTED;
 
   gqa8::Desc d;
   d.B = shape->batch;
@@ -1415,6 +1419,7 @@ mla_status gqa_decode_partial_fp8(const void* q, const gqa_block_pages* cache,
   d.Hg = make_div(shape->num_kv_heads >> sp.lg_team);
   d.G = make_div(shape->num_heads / shape->num_kv_heads);
   d.rg = sp.rg;
+  d.unit_cost = sp.unit_cost;
   d.Gq = make_div(sp.Gq);
   d.num_shards = make_div(num_shards);
   d.shard_first = shard_id == MLA_ALL_SHARDS ? 0 : shard_id;
