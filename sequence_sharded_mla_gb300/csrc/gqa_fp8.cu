@@ -203,9 +203,9 @@ __device__ __forceinline__ size_t out_row(const Desc& d, const Rows& x, int r) {
 
 // A piece's query, by row.
 struct Query {
-  alignas(16) float qs[kMaxR];  // 1 / the row's query scale
-  int lim[kMaxR];               // last position the row sees
-  alignas(16) int orow[kMaxR];              // its output row
+  alignas(16) float qs[kMaxR];   // 1 / the row's query scale
+  int lim[kMaxR];                // last position the row sees
+  alignas(16) int orow[kMaxR];   // its output row
 };
 
 struct Misc {
@@ -225,7 +225,8 @@ struct Misc {
   // the sums at the end of a piece
   float part[2][4][kMaxR];
   int moved[2][kMaxR / 16];     // per group: a reference of these 16 rows moved
-  int nan_from[2][kD];          // this piece, the next; per dim: the first partly seen token whose V is NaN
+  // this piece, the next; per dim: the first partly seen token whose V is NaN
+  int nan_from[2][kD];
   float ksc[kMaxStages][kTok], vsc[kMaxStages][kTok];   // by run of slots with one scale
   int4 rec;
   int prefix[kMaxOwnPlan + 1];
@@ -487,9 +488,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 #pragma unroll
     for (int k = 0; k < kOwnPerThread; ++k) {
-      if (k < upt && u0 + k < p.units) {
-        misc->prefix[u0 + k] = base;
-      }
+      if (k < upt && u0 + k < p.units) misc->prefix[u0 + k] = base;
       base += cost[k];
     }
     per = max(kMinTilesPerCta, ceil_div(W, teams));
@@ -686,7 +685,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else {
         if (pc >= 2 && !(ok = wait(&misc->q_empty[buf], ((pc >> 1) - 1) & 1))) break;
         fetch_query(make_rows(d, unit, member), buf, 0, R);
-        #pragma unroll 1
+#pragma unroll 1
         for (int r0 = 0; r0 < R; r0 += 8) split_query(buf, r0, std::integral_constant<int, 8>());
         if (lane < 8) mbar_arrive(bar(&misc->q_full[buf]));
       }
