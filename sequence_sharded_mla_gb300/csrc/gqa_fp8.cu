@@ -765,8 +765,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Slots slots = make_slots(d, x);
       // tiles whose first position is in [tstart, last_full] hold a token that
       // every row sees in every slot
-      const int last_full = min(x.tend - 1, d.causal ? x.L - x.qn + x.r0 / d.G : INT_MAX) -
-                            (kTok - 1) * slots.step;
+      const int last_all = d.causal ? x.L - x.qn + x.r0 / d.G : INT_MAX;   // that every row sees
+      const int last_full = min(x.tend - 1, last_all) - (kTok - 1) * slots.step;
       const Query& query = misc->query[pc & 1];
       int* nan_from = misc->nan_from[pc & 1];
       if (pc == 0) {
@@ -983,29 +983,29 @@ __global__ void __launch_bounds__(kThreads, 1)
           // V rows of slots without a token become zeros; a NaN code of a token
           // that not every row sees is taken out too and comes back in the
           // epilogue for the rows that see it (rows see a prefix)
+          const int u = gtid & 7;
           uint8_t* vt = smem + S::kV + st * kStageBytes;
-          for (int e = gtid; e < kTok * (kD / 16); e += kGroupThreads) {
-            const int a = e >> 3, u = e & 7;
+#pragma unroll 1
+          for (int a = gtid >> 3; a < kTok; a += 16) {
             const int ta = tok0 + a * slots.step;
             uint4* v = reinterpret_cast<uint4*>(vt + a * kD + ((u ^ (a & 7)) << 4));
             if (ta < x.tstart || ta >= x.tend) {
               *v = make_uint4(0, 0, 0, 0);
-              continue;
-            }
-            uint4 w = *v;
-            uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-            uint32_t any = 0;
+            } else if (ta > last_all) {
+              const uint4 w = *v;
+              uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+              uint32_t any = 0;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) any |= ((ww[k] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
-            if (any == 0) continue;
-            for (int k = 0; k < 16; ++k) {
-              const int sh = 8 * (k & 3);
-              if (((ww[k >> 2] >> sh) & 0x7Fu) == 0x7Fu) {
-                ww[k >> 2] &= ~(0xFFu << sh);
-                atomicMin(&nan_from[16 * u + k], ta);
+              for (int k = 0; k < 4; ++k) {
+                // 1 in each byte that is a NaN, whose low seven bits are all ones
+                const uint32_t nan = (((ww[k] & 0x7F7F7F7Fu) + 0x01010101u) >> 7) & 0x01010101u;
+                any |= nan;
+                ww[k] &= ~(nan * 0xFFu);
+                for (uint32_t left = nan; left != 0; left &= left - 1)
+                  atomicMin(&nan_from[16 * u + 4 * k + ((__ffs(left) - 1) >> 3)], ta);
               }
+              if (any) *v = make_uint4(ww[0], ww[1], ww[2], ww[3]);
             }
-            *v = make_uint4(ww[0], ww[1], ww[2], ww[3]);
           }
         }
         first = false;
@@ -1046,8 +1046,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc_fence_after();
       const size_t sl = 2 * (size_t)blockIdx.x + slot;
-      if (tid < R) {
-        const int r = tid;
+      if (gtid < R) {                              // group 0: factors; group 1: lse
+        const int r = gtid;
         float lg[2], M = kNoRef;
         for (int k = 0; k < 2; ++k) {
           lg[k] = (misc->part[k][0][r] + misc->part[k][1][r]) +
@@ -1057,15 +1057,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float w0 = ex2_approx(-misc->m[0][r] - M), w1 = ex2_approx(-misc->m[1][r] - M);
         const float tot = w0 * lg[0] + w1 * lg[1];
         const bool none = tot == 0.0f || r >= x.live;   // not NaN
-        const float it_ = none ? 0.0f : 1.0f / tot;
-        misc->f[0][r] = w0 * it_;
-        misc->f[1][r] = w1 * it_;
-        if (r < x.rows) {
+        if (grp == 0) {
+          const float it_ = none ? 0.0f : 1.0f / tot;
+          misc->f[0][r] = w0 * it_;
+          misc->f[1][r] = w1 * it_;
+        } else if (r < x.rows) {
           // the reference and the sum's exponent nearly cancel where V's scales are
           // far from 1 (M = -70, tot = 2^73 under a scale of 0): exact first
-          const int e = tot < INFINITY ? (__float_as_int(tot) >> 23) - 127 : 0;
-          const float lg = (M + (float)e) + log2f(ldexpf(tot, -e));
-          const float v = none ? -CUDART_INF_F : lg * 0.69314718055994530942f;
+          const uint32_t bits = __float_as_uint(tot);
+          const bool normal = bits >= (1u << 23) && bits < (255u << 23);
+          const int e = normal ? (int)(bits >> 23) - 127 : 0;
+          const float one = normal ? __uint_as_float((bits & 0x7FFFFFu) | (127u << 23)) : tot;
+          const float v = none ? -CUDART_INF_F
+                               : ((M + (float)e) + log2f(one)) * 0.69314718055994530942f;
           if (whole) p.lse[query.orow[r]] = v;
           else p.ws_lse[sl * kRows + r] = v;
         }
