@@ -53,7 +53,7 @@
 // 4 heads, 16 rows a unit, 112 us (5.8 TB/s; the partial kernel 6.0, of 6.5
 // that it reaches where nothing is ragged); one request of 1M tokens x 8 heads
 // in 8 shards 363 us (5.9 TB/s, the producers' cp.async); a ragged verify of up
-// to 9 tokens over 16 x 6600 tokens x 8 heads, 32 rows a unit, 82 us (the
+// to 9 tokens over 16 x 6600 tokens x 8 heads, 32 rows a unit, 81 us (the
 // softmax groups: 2900 cycles a tile each); 1024 tokens 11.5 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -1289,7 +1289,7 @@ bool shards_ok(int num_shards, int shard_id) {
 // Query rows per work unit: all of a KV head's q_len * G rows of a request up
 // to 48, in the smallest tile that holds them; more rows go to groups of 32.
 // 16 requests x 6400 tokens x 4 heads, us with groups of up to 48 and 32 rows:
-// 36 rows 45 and 50, 48 rows 44 and 50, 64 rows 65 and 52, 72 rows 70 and 69,
+// 36 rows 46 and 50, 48 rows 46 and 50, 64 rows 65 and 52, 72 rows 70 and 69,
 // 96 rows 69 and 69, 126 rows 93 and 88; a ragged verify of up to 72 rows 90
 // and 82.  Full groups and a rest, not groups of even size, as a padded batch's
 // requests often need no rest (that verify in three groups of 24 rows: 110
