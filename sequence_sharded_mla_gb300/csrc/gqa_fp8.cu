@@ -945,6 +945,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = false;
           continue;                                // the next reduction ends the piece
         }
+        // before the next wait that may give up in some warps only: they all
+        // have to meet the others in the same reductions of the next tile
+        first = false;
         uint8_t* prow = smem + S::kP + grp * S::kPGroup + gtid * 16;
         const float2 inv2 = make_float2(inv, inv);
 #pragma unroll
@@ -1008,7 +1011,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        first = false;
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
