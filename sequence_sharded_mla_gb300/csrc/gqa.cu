@@ -618,13 +618,21 @@ __global__ void __launch_bounds__(256) gqa_combine_kernel(const float* __restric
   const int row = blockIdx.x * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   if (row >= rows) return;
+  // a shard without a token (lse -inf) counts for nothing; a NaN one makes the
+  // row NaN, although fmaxf passes over it
   float M = -CUDART_INF_F;
-  for (int s = 0; s < num_shards; ++s) M = fmaxf(M, __ldg(lses + (size_t)s * rows + row));
+  bool seen = false;
+  for (int s = 0; s < num_shards; ++s) {
+    const float l = __ldg(lses + (size_t)s * rows + row);
+    M = fmaxf(M, l);
+    seen |= l != -CUDART_INF_F;
+  }
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   float wsum = 0.f;
-  if (M > -CUDART_INF_F) {
+  if (seen) {
     for (int s = 0; s < num_shards; ++s) {
-      const float w = __expf(__ldg(lses + (size_t)s * rows + row) - M);
+      const float l = __ldg(lses + (size_t)s * rows + row);
+      const float w = l == -CUDART_INF_F ? 0.f : __expf(l - M);
       wsum += w;
       const float4 o = __ldg(reinterpret_cast<const float4*>(partials + ((size_t)s * rows + row) * kD) + lane);
       acc.x += w * o.x;
@@ -633,11 +641,10 @@ __global__ void __launch_bounds__(256) gqa_combine_kernel(const float* __restric
       acc.w += w * o.w;
     }
   }
-  const float inv = wsum > 0.f ? 1.0f / wsum : 0.f;
+  const float inv = seen ? 1.0f / wsum : 0.f;
   uint2 packed = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
   reinterpret_cast<uint2*>(out + (size_t)row * kD)[lane] = packed;
-  if (lse_out != nullptr && lane == 0)
-    lse_out[row] = M > -CUDART_INF_F ? M + __logf(wsum) : -CUDART_INF_F;
+  if (lse_out != nullptr && lane == 0) lse_out[row] = seen ? M + __logf(wsum) : -CUDART_INF_F;
 }
 
 // ------------------------------------------------------------------ host side
