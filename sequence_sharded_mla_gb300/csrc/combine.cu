@@ -186,7 +186,9 @@ __device__ __forceinline__ void merge_pieces_ctx(const Src& src, const typename 
         ws *= sc;
         M = mb;
       }
-      if (M == -CUDART_INF_F) continue;   // nothing seen yet: every lse so far is -inf
+      // every lse so far is -inf: nothing seen yet.  (A NaN one, which fmaxf
+      // passes over, counts as seen and makes the row NaN.)
+      if (M == -CUDART_INF_F && !__any_sync(0xffffffffu, l != l)) continue;
 #pragma unroll
       for (int jj = 0; jj < kB; ++jj) {
         const float w = __expf(__shfl_sync(0xffffffffu, l, j + jj) - M);
@@ -227,14 +229,14 @@ __global__ void __launch_bounds__(256, kMinB) mla_combine_kernel(Src src, int ro
   const typename Src::Ctx ctx = src.prepare(row, lane);
   merge_pieces_staged<kVec, kB>(src, ctx, lane, 32 * kVec * part,
                                 combine_stage + warp * (kB * 32 * kVec), acc, M, wsum);
-  const float inv = wsum > 0.f ? 1.0f / wsum : 0.f;
+  const float inv = wsum != 0.f ? 1.0f / wsum : 0.f;   // or NaN
   uint2* dst = reinterpret_cast<uint2*>(out + (size_t)row * kDv);
 #pragma unroll
   for (int v = 0; v < kVec; ++v)
     dst[32 * kVec * part + lane + 32 * v] = make_uint2(pack2(acc[v].x * inv, acc[v].y * inv),
                                                      pack2(acc[v].z * inv, acc[v].w * inv));
   if (lse_out != nullptr && part == 0 && lane == 0)
-    lse_out[row] = wsum > 0.f ? M + __logf(wsum) : -CUDART_INF_F;
+    lse_out[row] = wsum != 0.f ? M + __logf(wsum) : -CUDART_INF_F;
 }
 
 // Fused combine + W_UV, as a cluster of four CTAs that split the 512 latent
@@ -324,13 +326,16 @@ __global__ void __cluster_dims__(kWuvSplit, 1, 1) __launch_bounds__(256, 2)
     const int r = warp;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
     if (r < nr) {
-      float M = -CUDART_INF_F;
-      for (int w = 0; w < 8; ++w) M = fmaxf(M, sm.rmax[w][r]);
+      float M = -CUDART_INF_F, nan = 0.f;
+      for (int w = 0; w < 8; ++w) {
+        M = fmaxf(M, sm.rmax[w][r]);
+        nan += sm.rsum[w][r];    // NaN if a piece's lse is
+      }
       float ws = 0.f;
-      if (M > -CUDART_INF_F) {
+      if (M > -CUDART_INF_F || nan != nan) {
         for (int w = 0; w < 8; ++w) {
           const float mp = sm.rmax[w][r];
-          if (mp == -CUDART_INF_F) continue;
+          if (mp == -CUDART_INF_F && nan == nan) continue;
           const float sc = __expf(mp - M);
           const float4 a = *reinterpret_cast<const float4*>(&sm.red[w][r][4 * lane]);
           v.x = fmaf(sc, a.x, v.x);
@@ -340,10 +345,10 @@ __global__ void __cluster_dims__(kWuvSplit, 1, 1) __launch_bounds__(256, 2)
           ws = fmaf(sc, sm.rsum[w][r], ws);
         }
       }
-      const float inv = ws > 0.f ? 1.0f / ws : 0.f;
+      const float inv = ws != 0.f ? 1.0f / ws : 0.f;
       v = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
       if (lse_out != nullptr && q == 0 && lane == 0)
-        lse_out[(bi0 + r) * H + h] = ws > 0.f ? M + __logf(ws) : -CUDART_INF_F;
+        lse_out[(bi0 + r) * H + h] = ws != 0.f ? M + __logf(ws) : -CUDART_INF_F;
     }
     *reinterpret_cast<float4*>(&sm.so[r][4 * lane]) = v;
   }

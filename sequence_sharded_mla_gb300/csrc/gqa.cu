@@ -485,9 +485,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const size_t sl = 2 * (size_t)blockIdx.x + slot;
       const float l_tot = l_run + __shfl_xor_sync(0xffffffffu, l_run, 16);
       if (owner && half == 0) {
-        const float lse = (l_tot > 0.0f) ? (m_run + __log2f(l_tot)) * 0.69314718055994530942f
-                                         : -CUDART_INF_F;
-        misc->inv_l[r] = (l_tot > 0.0f) ? 1.0f / l_tot : 0.0f;
+        const float lse = (l_tot != 0.0f) ? (m_run + __log2f(l_tot)) * 0.69314718055994530942f   // or NaN
+                                          : -CUDART_INF_F;
+        misc->inv_l[r] = (l_tot != 0.0f) ? 1.0f / l_tot : 0.0f;
         if (whole) p.lse_partial[out_row(d, x, r)] = lse;
         else p.ws_lse[sl * kRows + r] = lse;
       }
@@ -585,15 +585,21 @@ __global__ void __launch_bounds__(128) gqa_merge_kernel(Desc d, const WsHeader* 
       continue;
     }
     float M = -CUDART_INF_F;
-    for (int k = lane; k < np; k += 32) M = fmaxf(M, ws_lse[slot_of(c0 + k) * kRows + r]);
+    bool seen = false;                             // a piece with a token, NaN ones among them
+    for (int k = lane; k < np; k += 32) {
+      const float l = ws_lse[slot_of(c0 + k) * kRows + r];
+      M = fmaxf(M, l);
+      seen |= l != -CUDART_INF_F;
+    }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
     float wsum = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (M > -CUDART_INF_F) {
+    if (__any_sync(0xffffffffu, seen)) {
       for (int k = 0; k < np; ++k) {
         const size_t s = slot_of(c0 + k);
-        const float w = __expf(ws_lse[s * kRows + r] - M);
+        const float l = ws_lse[s * kRows + r];
+        const float w = l == -CUDART_INF_F ? 0.f : __expf(l - M);
         wsum += w;
         const float4 o = reinterpret_cast<const float4*>(ws_o + (s * kRows + r) * kD)[lane];
         acc.x += w * o.x;
@@ -602,9 +608,9 @@ __global__ void __launch_bounds__(128) gqa_merge_kernel(Desc d, const WsHeader* 
         acc.w += w * o.w;
       }
     }
-    const float inv = wsum > 0.f ? 1.0f / wsum : 0.f;
+    const float inv = wsum != 0.f ? 1.0f / wsum : 0.f;
     dst[lane] = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-    if (lane == 0) lse_partial[out_row(d, x, r)] = wsum > 0.f ? M + __logf(wsum) : -CUDART_INF_F;
+    if (lane == 0) lse_partial[out_row(d, x, r)] = wsum != 0.f ? M + __logf(wsum) : -CUDART_INF_F;
   }
 }
 

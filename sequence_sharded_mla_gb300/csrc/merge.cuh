@@ -70,7 +70,9 @@ __device__ __forceinline__ void merge_pieces_staged(const Src& src, const typena
         ws *= sc;
         M = mb;
       }
-      if (M == -CUDART_INF_F) continue;   // nothing seen yet: every lse so far is -inf
+      // every lse so far is -inf: nothing seen yet.  (A NaN one, which fmaxf
+      // passes over, counts as seen and makes the row NaN.)
+      if (M == -CUDART_INF_F && !__any_sync(0xffffffffu, l != l)) continue;
 #pragma unroll
       for (int jj = 0; jj < kB; ++jj) {
         const float w = __expf(__shfl_sync(0xffffffffu, l, j + jj) - M);

@@ -615,9 +615,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (kRankIo && tid < kRows) misc->orow[tid] = (uint32_t)dst_row(tid);
       const float l_tot = l_run + __shfl_xor_sync(0xffffffffu, l_run, 16);
       if (owner && half == 0) {
-        float lse = (l_tot > 0.0f) ? (m_run + __log2f(l_tot)) * 0.69314718055994530942f
-                                   : -CUDART_INF_F;
-        misc->inv_l[r] = (l_tot > 0.0f) ? 1.0f / l_tot : 0.0f;
+        float lse = (l_tot != 0.0f) ? (m_run + __log2f(l_tot)) * 0.69314718055994530942f   // or NaN
+                                    : -CUDART_INF_F;
+        misc->inv_l[r] = (l_tot != 0.0f) ? 1.0f / l_tot : 0.0f;
         lbase[dst_row(r)] = lse;
       }
       if (whole) {

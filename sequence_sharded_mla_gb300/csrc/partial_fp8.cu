@@ -787,9 +787,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (kRankIo && tid < kRows) misc->orow[tid] = (uint32_t)dst_row(tid);
       if (grp == 0 && owner && half == 0) {
         const float l_tot = misc->xl[0][r] + misc->xl[1][r];
-        float lse = (l_tot > 0.0f) ? (m_run + __log2f(l_tot)) * 0.69314718055994530942f
-                                   : -CUDART_INF_F;
-        misc->inv_l[r] = (l_tot > 0.0f) ? 1.0f / l_tot : 0.0f;
+        float lse = (l_tot != 0.0f) ? (m_run + __log2f(l_tot)) * 0.69314718055994530942f   // or NaN
+                                    : -CUDART_INF_F;
+        misc->inv_l[r] = (l_tot != 0.0f) ? 1.0f / l_tot : 0.0f;
         lbase[dst_row(r)] = lse;
       }
       if (whole) {

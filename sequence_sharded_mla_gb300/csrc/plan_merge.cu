@@ -93,9 +93,9 @@ __global__ void __launch_bounds__(256, 4) mla_merge_kernel(
   float M, wsum;
   merge_pieces_staged<1, kMergeBatch>(src, ctx, lane, 32 * part,
                                       merge_stage + warp * (kMergeBatch * 32), acc, M, wsum);
-  const float inv = wsum > 0.f ? 1.0f / wsum : 0.f;
+  const float inv = wsum != 0.f ? 1.0f / wsum : 0.f;   // or NaN
   dst[lane] = make_float4(acc[0].x * inv, acc[0].y * inv, acc[0].z * inv, acc[0].w * inv);
-  if (part == 0 && lane == 0) lse_partial[orow] = wsum > 0.f ? M + __logf(wsum) : -CUDART_INF_F;
+  if (part == 0 && lane == 0) lse_partial[orow] = wsum != 0.f ? M + __logf(wsum) : -CUDART_INF_F;
 }
 
 cudaError_t launch_plan(const ProblemDesc& pd, WsHeader* hdr, int* prefix, int grid,
