@@ -25,8 +25,8 @@
 //      m), and the normaliser sums P_t / |sv| = 2^(s_t log2(e) - m), so one
 //      running reference m serves rows whose scales lie far apart.  m puts the
 //      largest weight at 2^12 and moves (rescaling O) once one passes 2^15.
-//      P goes to fp16 and from there to three e5m2 terms that add up to it
-//      within 2^-9 of its value, down to 2^-17: a token 2^-29 below the row's
+//      P goes to fp16, off by 2^-11 of its value, and from there without loss
+//      to three e5m2 terms, down to 2^-17: a token 2^-29 below the row's
 //      largest weight (2^-27 below that of the first tile, whose references
 //      are likely to grow) still counts.  (Two e4m3 terms end 2^-18 below it,
 //      and a million such tokens are not nothing.)  The terms are three blocks
@@ -362,17 +362,23 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return d;
 }
 
-// Weights of two rows as three e5m2 terms: the top bytes of the fp16 value, of
-// what that leaves, and of what is left then rounded to nearest.  Returns the
-// first two terms in the top bytes of t0, t1 and the third as a byte pair.
+// Weights of two rows as three e5m2 terms, which are the top bytes of fp16
+// values: of the weight in fp16, of what that leaves, and of what is left then,
+// each rounded to nearest (half a last place added to the bits).  The first
+// term leaves at most 2^-3 of the value's power of two, the second 2^-7; that
+// is a multiple of fp16's last place, 2^-10, of three bits: the third is exact,
+// down to e5m2's least value 2^-16.  Returns the first two terms in the top
+// bytes of t0, t1 and the third as a byte pair.  (A NaN's first two terms come
+// out as zeros, its third as NaN.)
 __device__ __forceinline__ void split_e5m2(float a, float b, uint32_t& t0, uint32_t& t1,
                                            uint32_t& t2) {
+  constexpr uint32_t kHalf = 0x00800080u, kTopBytes = 0xFF00FF00u;
   __half2 x = __floats2half2_rn(a, b);
-  t0 = *reinterpret_cast<uint32_t*>(&x);
-  uint32_t h = t0 & 0xFF00FF00u;
+  t0 = *reinterpret_cast<uint32_t*>(&x) + kHalf;
+  uint32_t h = t0 & kTopBytes;
   __half2 y = __hsub2(x, *reinterpret_cast<__half2*>(&h));
-  t1 = *reinterpret_cast<uint32_t*>(&y);
-  h = t1 & 0xFF00FF00u;
+  t1 = *reinterpret_cast<uint32_t*>(&y) + kHalf;
+  h = t1 & kTopBytes;
   y = __hsub2(y, *reinterpret_cast<__half2*>(&h));
   unsigned short c;
   asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(c) : "r"(*reinterpret_cast<uint32_t*>(&y)));
