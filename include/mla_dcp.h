@@ -57,7 +57,8 @@ typedef enum mla_status {
   MLA_ERR_TIMEOUT = -4,       /* a device-side wait gave up (from mla_get_device_error) */
   MLA_ERR_DEVICE_BOUNDS = -5, /* a block-table entry was outside [0, num_pages) */
   MLA_ERR_WORKSPACE = -6,     /* workspace missing or smaller than mla_workspace_size() */
-  MLA_ERR_RANGE = -7          /* fp8 cache: an inf or NaN query value in a row that attends */
+  MLA_ERR_RANGE = -7          /* fp8 cache: an inf or NaN query value in a row that attends,
+                                 or a finite V scale of a block above 2^120 */
 } mla_status;
 
 /* Which token positions of a request belong to shard s of N
@@ -464,9 +465,9 @@ mla_status mla_cache_append(const void* latent, long long latent_stride, const m
  *   k, v              e4m3 (or bf16) [num_pages, 64, Hkv, 128]
  *   k_scale, v_scale  fp32 [num_pages, 64 / block, Hkv]: value of row r, head h
  *                     = code * scale[page][r / block][h]
- * Scales written by gqa_cache_append are powers of two; the attention takes
- * any finite scale (a V scale below 2^-60 in magnitude weighs its block with
- * that much less precision, 0 is exact).
+ * Scales written by gqa_cache_append are powers of two between 2^-60 and
+ * 2^120.  The attention takes any finite K scale, and V scales as
+ * gqa_decode_partial_fp8 says.
  */
 typedef struct gqa_block_pages {
   void* k;
@@ -517,6 +518,20 @@ size_t gqa_fp8_workspace_size(const gqa_shape* shape, int num_shards, int shard_
  * reads as zeros, and a context longer than its block-table row is cut at the
  * row's end, both reported as MLA_ERR_DEVICE_BOUNDS.  Shapes whose work could
  * pass 2^31 tiles (units times pages per row) are MLA_ERR_UNSUPPORTED.
+ *
+ * Accuracy.  A query value is held to 2^-18 of its row's largest or better.  A
+ * token's weight p_t carries its V scale sv_t, and one reference serves a row:
+ * p_t sv_t is off by up to 2^-11 of itself and 2^-27 max_u (p_u |sv_u|), the
+ * row's largest.  So where one seen block's V scale is S times another's, the
+ * other's weights have log2 S fewer of these 27 bits, whatever the wide block's
+ * codes are: at S = 2^16 a token with the same p is still held to 2^-10, at
+ * S = 2^28 it is gone.  (Scales follow the largest value of their block, so a
+ * wide one goes with large outputs, but a dim that has zeros there has them
+ * too.)  The lse does not depend on this while the row's V scales lie within
+ * 2^100 of one another; one below 2^-60 in magnitude counts as 2^-60 in this,
+ * and weighs its block with that much less precision (0 is exact).  A finite V
+ * scale above 2^120 of a token in the context is reported as MLA_ERR_RANGE.
+ *
  * The workspace may hold anything before a call, and serves one call at a
  * time; mla_get_device_error reads the last call's errors from it.
  */

@@ -106,7 +106,7 @@ const char* mla_status_string(mla_status st) {
     case MLA_ERR_TIMEOUT: return "device wait timed out";
     case MLA_ERR_DEVICE_BOUNDS: return "block-table entry out of range";
     case MLA_ERR_WORKSPACE: return "workspace missing or too small";
-    case MLA_ERR_RANGE: return "non-finite query value (fp8 cache)";
+    case MLA_ERR_RANGE: return "non-finite query value or V scale out of range (fp8 cache)";
   }
   return "unknown status";
 }

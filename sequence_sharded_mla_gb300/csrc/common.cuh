@@ -28,7 +28,7 @@ constexpr unsigned long long kDrainNs = 2000000000ull;
 // Error bits written to the workspace error word.
 constexpr unsigned kErrTimeout = 1u;
 constexpr unsigned kErrBadPage = 2u;
-constexpr unsigned kErrQRange = 4u;   // fp8 caches: a non-finite query value
+constexpr unsigned kErrQRange = 4u;   // fp8 caches: a non-finite query value, a V scale above 2^120
 constexpr unsigned kErrQLens = 8u;    // a per-request query count outside [1, q_len]
 
 enum Layout : int { kInterleaved = 0, kContiguous = 1 };

@@ -90,6 +90,7 @@ constexpr float kTopFirst = 10.0f;         // and at a piece's first (verify of 
 constexpr float kMost = 15.0f;             // log2 of the largest weight that fits fp16
 constexpr float kNoRef = -1.0e38f;         // reference of a row that has seen nothing
 constexpr float kMinScale = 8.67361737988403547e-19f;   // 2^-60
+constexpr float kMaxScale = 1.32922799578491587e36f;    // 2^120
 
 struct Desc {
   int B, q_len, H;
@@ -803,11 +804,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           c = misc->ksc[st][gtid >> d.lg_run] * d.scale_log2;
           const float sv = misc->vsc[st][gtid >> d.lg_run];
           // |sv| below 2^-60 counts as 2^-60 in the reference and as itself in
-          // the product; a scale that is not finite goes to the product alone
+          // the product; a scale that is not finite goes to the product alone;
+          // one above 2^120, whose inverse may be no normal number, is reported
           float ve = sv;
-          if (!(sv >= kMinScale && sv < INFINITY)) {
+          if (!(sv >= kMinScale && sv <= kMaxScale)) {
             ve = fabsf(sv) < INFINITY ? fmaxf(fabsf(sv), kMinScale) : 1.0f;
             fv = sv / ve;
+            if (ve > kMaxScale) atomicOr(&misc->err, kErrQRange);
           }
           lv = lg2_approx(ve);
           inv = rcp_approx(ve);
