@@ -559,8 +559,12 @@ def gqa_decode_partial(q, k_cache, v_cache, block_table, seq_lens, num_shards,
 
 
 def gqa_shard_combine(partials, lses, out=None, lse_out=None, stream=None):
-    """LSE combine of GQA shard partials fp32 [N, B, q_len, H, D] -> bf16
-    [B, q_len, H, D] and fp32 lse [B, q_len, H]."""
+    """LSE combine of GQA shard partials fp32 [N, B, q_len, H, D] and lses fp32
+    [N, B, q_len, H] -> bf16 [B, q_len, H, D] and fp32 lse [B, q_len, H].
+
+    out, lse_out: contiguous tensors of these types with room for the result
+    (any number of dims; with 4 and 3, all but the first as above), or None.
+    """
     return _binding().shard_combine(partials, lses, out, lse_out, stream)
 
 

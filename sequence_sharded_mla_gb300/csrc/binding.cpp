@@ -75,6 +75,24 @@ void shape_is(const at::Tensor& t, const char* name, at::IntArrayRef want) {
     value_error(std::string(name) + " must be " + dims_of(want) + ", got " + dims_of(t.sizes()));
 }
 
+// Contiguous memory of `type` that holds a tensor of shape `want`: one of that
+// shape, or with more entries in front, or of another number of dimensions.
+const at::Tensor& room(PyObject* o, const char* name, at::ScalarType type, at::IntArrayRef want,
+                       const c10::Device& dev) {
+  const at::Tensor& t = tensor(o, name);
+  if (t.scalar_type() != type)
+    type_error(std::string(name) + ": dtype " + c10::toString(t.scalar_type()) + " is not " +
+               c10::toString(type));
+  on_device(t, name, &dev);
+  if (!t.is_contiguous()) value_error(std::string(name) + " must be contiguous");
+  int64_t need = 1;
+  for (int64_t n : want) need *= n;
+  if (t.numel() < need) value_error(std::string(name) + " is too small");
+  if (t.dim() == (int64_t)want.size() && t.sizes().slice(1) != want.slice(1))
+    value_error(std::string(name) + " must be " + dims_of(want) + ", got " + dims_of(t.sizes()));
+  return t;
+}
+
 int to_int(PyObject* o, const char* name) {
   const long v = PyLong_AsLong(o);
   if (v == -1 && PyErr_Occurred()) throw Raised{};
@@ -580,17 +598,9 @@ PyObject* shard_combine(PyObject*, PyObject* const* a, Py_ssize_t n) {
     sh.softmax_scale = 1.0f;
     const int N = small(p.size(0), "partials");
     at::Tensor out, lse;
-    if (l.numel() != N * B * q_len * H) value_error("lses and partials disagree");
-    if (a[2] != Py_None) {
-      out = tensor(a[2], "out");
-      on_device(out, "out", &dev);
-      if ((int64_t)out.nbytes() < B * q_len * H * D * 2) value_error("out is too small");
-    }
-    if (a[3] != Py_None) {
-      lse = tensor(a[3], "lse_out");
-      on_device(lse, "lse_out", &dev);
-      if ((int64_t)lse.nbytes() < B * q_len * H * 4) value_error("lse_out is too small");
-    }
+    shape_is(l, "lses", {N, B, q_len, H});
+    if (a[2] != Py_None) out = room(a[2], "out", at::kBFloat16, {B, q_len, H, D}, dev);
+    if (a[3] != Py_None) lse = room(a[3], "lse_out", at::kFloat, {B, q_len, H}, dev);
     const Place place(dev, a[4]);
     if (!out.defined()) out = make({B, q_len, H, D}, at::kBFloat16);
     if (!lse.defined()) lse = make({B, q_len, H}, at::kFloat);
