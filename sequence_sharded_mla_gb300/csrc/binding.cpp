@@ -140,19 +140,31 @@ struct Place {
       stream = c10::cuda::getCurrentCUDAStream(dev.index()).stream();
       return;
     }
-    static PyObject* const kId = name_of("stream_id");
-    static PyObject* const kIndex = name_of("device_index");
-    static PyObject* const kType = name_of("device_type");
-    const Ref id(PyObject_GetAttr(s, kId)), index(PyObject_GetAttr(s, kIndex)),
-        type(PyObject_GetAttr(s, kType));
-    const long long i = PyLong_AsLongLong(id.p);
-    if (i == -1 && PyErr_Occurred()) throw Raised{};
-    const auto cs = c10::cuda::CUDAStream::unpack3(
-        i, (c10::DeviceIndex)to_int(index.p, "stream"), (c10::DeviceType)to_int(type.p, "stream"));
+    const c10::cuda::CUDAStream cs = stream_of(dev, s);
     if (cs.device() != dev)
       value_error("stream is on " + cs.device().str() + ", expected " + dev.str());
     given.reset_stream(cs);
     stream = cs.stream();
+  }
+  // A torch stream, or any object with the CUDA handle of a stream of the
+  // device as `cuda_stream`.
+  static c10::cuda::CUDAStream stream_of(const c10::Device& dev, PyObject* s) {
+    static PyObject* const kId = name_of("stream_id");
+    static PyObject* const kIndex = name_of("device_index");
+    static PyObject* const kType = name_of("device_type");
+    static PyObject* const kHandle = name_of("cuda_stream");
+    if (!PyObject_HasAttr(s, kId)) {
+      const Ref handle(PyObject_GetAttr(s, kHandle));
+      void* const h = PyLong_AsVoidPtr(handle.p);
+      if (h == nullptr && PyErr_Occurred()) throw Raised{};
+      return c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(h), dev.index());
+    }
+    const Ref id(PyObject_GetAttr(s, kId)), index(PyObject_GetAttr(s, kIndex)),
+        type(PyObject_GetAttr(s, kType));
+    const long long i = PyLong_AsLongLong(id.p);
+    if (i == -1 && PyErr_Occurred()) throw Raised{};
+    return c10::cuda::CUDAStream::unpack3(i, (c10::DeviceIndex)to_int(index.p, "stream"),
+                                          (c10::DeviceType)to_int(type.p, "stream"));
   }
 };
 

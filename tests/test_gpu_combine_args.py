@@ -56,3 +56,42 @@ def test_outputs_with_room(mla, parts):
         assert torch.equal(l.flatten()[:want_lse.numel()], want_lse.flatten())
         assert bool((out.flatten()[want.numel():] == 7).all())
         assert bool((l.flatten()[want_lse.numel():] == 7).all())
+
+
+class Handle:
+    """A stream of another library: all it has is the CUDA handle."""
+
+    def __init__(self, handle):
+        self.cuda_stream = handle
+
+
+def test_streams_known_by_their_handle(mla, parts):
+    part, lse = parts
+    want = mla.gqa_shard_combine(part, lse)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for s in (side, Handle(side.cuda_stream), torch.cuda.ExternalStream(side.cuda_stream),
+              Handle(torch.cuda.default_stream().cuda_stream), torch.cuda.default_stream()):
+        got = mla.gqa_shard_combine(part, lse, stream=s)
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert torch.cuda.current_stream() == torch.cuda.default_stream()
+    for s in (3, "stream", object()):
+        with pytest.raises(AttributeError):
+            mla.gqa_shard_combine(part, lse, stream=s)
+
+
+def test_work_is_on_the_stream_of_the_handle(mla, parts):
+    """The call is captured into a graph of the handle's stream."""
+    part, lse = parts
+    want = mla.gqa_shard_combine(part, lse)
+    out, l = torch.zeros_like(want[0]), torch.zeros_like(want[1])
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        mla.gqa_shard_combine(part, lse, out=out, lse_out=l, stream=Handle(side.cuda_stream))
+    assert bool((out == 0).all())
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want[0]) and torch.equal(l, want[1])
