@@ -165,8 +165,7 @@ def _binding():
     Python would take longer than their work."""
     global _BINDING
     if _BINDING is None:
-        lib()
-        spec = importlib.util.spec_from_file_location("_binding", _build.BINDING)
+        spec = importlib.util.spec_from_file_location("_binding", _build.build_binding())
         m = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(m)
         m.set_error(MLAError)

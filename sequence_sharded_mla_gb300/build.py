@@ -5,12 +5,14 @@ Each translation unit is compiled in parallel with one ``-gencode`` and the
 objects are linked into one shared library with the CUDA runtime linked
 statically, so the library loads on a machine without a GPU driver (the
 driver is looked up at first use).  The module is host code against PyTorch's
-C++ headers; it finds the library beside itself.
+C++ headers; it finds the library beside itself.  The library is built and
+loaded without it: what breaks the module's build takes only its own calls.
 """
 import concurrent.futures as cf
 import os
 import shutil
 import subprocess
+import sys
 import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -21,6 +23,7 @@ SOURCES = ["partial.cu", "partial_fp8.cu", "wuv_gemm.cu", "plan_merge.cu", "comb
            "gqa_fp8.cu", "append.cu"]
 HEADERS = ["common.cuh", "merge.cuh", "ptx.cuh", "host_util.h", "rope.cuh"]
 BINDING = os.path.join(OUT_DIR, "_binding.so")
+BINDING_STAMP = os.path.join(OUT_DIR, "_binding.built-for")
 BINDING_SOURCE = os.path.join(CSRC, "binding.cpp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -35,6 +38,7 @@ def nvcc():
 
 
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
+API_HEADER = os.path.join(INCLUDE, "mla_dcp.h")
 
 
 def flags(extra=()):
@@ -42,17 +46,33 @@ def flags(extra=()):
                    "--expt-relaxed-constexpr", "-I" + INCLUDE, *extra]
 
 
-def _inputs():
-    root = os.path.dirname(HERE)
-    return ([os.path.join(CSRC, s) for s in SOURCES + HEADERS] + [BINDING_SOURCE] +
-            [os.path.join(root, "include", "mla_dcp.h")])
+def _newer_than(t, paths):
+    return any(os.path.getmtime(p) > t for p in paths)
 
 
 def needs_build():
-    if not (os.path.exists(LIB) and os.path.exists(BINDING)):
+    """Whether the library is missing or older than one of its sources."""
+    if not os.path.exists(LIB):
         return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
-    return any(os.path.getmtime(p) > t for p in _inputs())
+    return _newer_than(os.path.getmtime(LIB),
+                       [os.path.join(CSRC, s) for s in SOURCES + HEADERS] + [API_HEADER])
+
+
+def _binding_for():
+    """What the Python module is compiled against besides its sources."""
+    import torch
+    return f"torch {torch.__version__} at {os.path.dirname(torch.__file__)}, python {sys.version}"
+
+
+def needs_binding():
+    """Whether the Python module is missing, older than one of its sources or
+    compiled against another torch or Python."""
+    if not (os.path.exists(BINDING) and os.path.exists(BINDING_STAMP)):
+        return True
+    with open(BINDING_STAMP) as f:
+        if f.read() != _binding_for():
+            return True
+    return _newer_than(os.path.getmtime(BINDING), [BINDING_SOURCE, API_HEADER])
 
 
 def _binding_object(obj):
@@ -85,11 +105,8 @@ def build(force=False, verbose=False, extra_flags=()):
             raise RuntimeError(f"nvcc failed for {src}:\n{r.stdout}\n{r.stderr}")
         return r.stdout + r.stderr
 
-    binding_obj = os.path.join(OUT_DIR, "binding.o")
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        torch_lib = ex.submit(_binding_object, binding_obj)
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
         logs = list(ex.map(compile_one, SOURCES, objs))
-        torch_lib = torch_lib.result()
     if verbose:
         for log in logs:
             if log.strip():
@@ -98,16 +115,34 @@ def build(force=False, verbose=False, extra_flags=()):
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    cmd = [shutil.which("g++") or "c++", "-shared", "-o", BINDING, binding_obj, "-L" + OUT_DIR,
+    return LIB
+
+
+def build_binding(force=False):
+    """Builds the Python module, and the library if that is not up to date."""
+    if not (force or needs_binding()):
+        build()
+        return BINDING
+    os.makedirs(OUT_DIR, exist_ok=True)
+    obj = os.path.join(OUT_DIR, "binding.o")
+    with cf.ThreadPoolExecutor(max_workers=1) as ex:
+        torch_lib = ex.submit(_binding_object, obj)
+        build(force)
+        torch_lib = torch_lib.result()
+    if os.path.exists(BINDING_STAMP):
+        os.remove(BINDING_STAMP)
+    cmd = [shutil.which("g++") or "c++", "-shared", "-o", BINDING, obj, "-L" + OUT_DIR,
            "-l:" + os.path.basename(LIB), "-L" + torch_lib, "-lc10", "-lc10_cuda", "-ltorch_cpu",
            "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link of the Python module failed:\n{r.stdout}\n{r.stderr}")
-    return LIB
+    with open(BINDING_STAMP, "w") as f:
+        f.write(_binding_for())
+    return BINDING
 
 
 if __name__ == "__main__":
-    import sys
     extra = ["-Xptxas", "-v"] if "-v" in sys.argv else []
     print(build(force=True, verbose=bool(extra), extra_flags=extra))
+    print(build_binding())
