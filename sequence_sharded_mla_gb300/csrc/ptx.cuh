@@ -95,6 +95,8 @@ __device__ __forceinline__ bool mbar_try_wait_hint(uint32_t bar, uint32_t parity
 // The waiting thread sleeps in the barrier (up to 0.2 ms per probe) instead
 // of spinning, so it does not take issue slots from the warps doing work; the
 // clock is read after the first probe, off the path of a wait that succeeds.
+// (The hardware ends a probe long before its hint: waits with a limit of 0.05,
+// 0.2, 1 and 3 ms gave up 6 to 10 us after it.)
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns,
                                           volatile int* abort) {
   if (mbar_try_wait(bar, parity) || mbar_try_wait_hint(bar, parity, 200000u)) return true;
