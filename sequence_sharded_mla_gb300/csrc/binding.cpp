@@ -331,10 +331,14 @@ RowsArg rows_arg(PyObject* px, PyObject* pout, const char* name) {
       value_error(oname + " overlaps " + name + " with other strides");
     r.ys = r.xs;
   } else if (r.x->numel() > 0) {
-    // the bytes from the first token to the end of the last
+    // the bytes from the first token to the end of the last; with equal strides
+    // they may be columns of one tensor, apart in every token
     const int64_t last = r.x->size(0) * r.x->size(1) - 1, width = r.x->size(2) * r.x->size(3);
-    if (a < b + 2 * (last * r.ys + width) && b < a + 2 * (last * r.xs + width))
-      value_error(oname + " overlaps " + name);
+    if (a < b + 2 * (last * r.ys + width) && b < a + 2 * (last * r.xs + width)) {
+      const int64_t step = 2 * r.xs, gap = (int64_t)(a < b ? b - a : a - b) % step;
+      if (r.xs != r.ys || gap < 2 * width || step - gap < 2 * width)
+        value_error(oname + " overlaps " + name);
+    }
   }
   return r;
 }
