@@ -339,12 +339,14 @@ __global__ void __launch_bounds__(32 * kF8Warps, 4)
   const int first_new = max(L - n, 0);
   const int p0 = first_new > c.shard ? (first_new - c.shard - 1) / c.num_shards + 1 : 0;
   const int p1 = L > c.shard ? (L - 1 - c.shard) / c.num_shards + 1 : 0;
-  const int blk = (p0 >> lg_block) + j;
-  const int lo = max(p0, blk * c.block), hi = min(p1, (blk + 1) * c.block), nt = hi - lo;
+  // counted from the first touched block's start: slots go up to 2^31 - 2
+  const int start = p0 & ~(c.block - 1), off = j * c.block;
+  const int nt = min(p1 - start, off + c.block) - max(p0 - start, off);
   if (nt <= 0) return;
-  const int page = page_of(c, b, blk * c.block);
+  const int slot0 = start + off, lo = max(p0, slot0);
+  const int page = page_of(c, b, slot0);
   if (page < 0) return;
-  const int row0 = (blk * c.block) % kPage;
+  const int row0 = slot0 % kPage;
   const int W = wph, wh = warp % wph;            // warps of a head, and this one among them
   const int kh = hg * (kF8Warps / W) + warp / wph;
   const bool live = kh < c.Hkv;
@@ -362,7 +364,7 @@ __global__ void __launch_bounds__(32 * kF8Warps, 4)
     if (live && tt < nt)
       w[i] = __ldg(reinterpret_cast<const uint4*>(x + ((size_t)b * t.q_len + token(lo + tt)) * xs));
   }
-  const bool had = lo > blk * c.block;
+  const bool had = lo > slot0;
   float* sp = (is_v ? c.vs : c.ks) + (((size_t)page * kPage + row0) >> lg_block) * c.Hkv + kh;
   const float old = had && live ? *sp : 0.0f;
 
@@ -460,7 +462,7 @@ __global__ void __launch_bounds__(32 * kF8Warps, 4)
   const size_t rs = (size_t)c.Hkv * kGD;
   if (grow) {
     const float g = old / s;                     // s is a power of two: exact
-    for (int p = 2 * wh + half; p < lo - blk * c.block; p += 2 * W) {
+    for (int p = 2 * wh + half; p < lo - slot0; p += 2 * W) {
       uint2* d = reinterpret_cast<uint2*>(base + p * rs);
       uint32_t z[2] = {d->x, d->y};
 #pragma unroll
@@ -488,7 +490,7 @@ __global__ void __launch_bounds__(32 * kF8Warps, 4)
 #pragma unroll
       for (int e = 0; e < 8; ++e) f[i][e] /= s;
     }
-    *reinterpret_cast<uint2*>(base + (lo - blk * c.block + tt) * rs) =
+    *reinterpret_cast<uint2*>(base + (lo - slot0 + tt) * rs) =
         make_uint2(f32x2_to_e4m3x2(f[i][0], f[i][1]) | (f32x2_to_e4m3x2(f[i][2], f[i][3]) << 16),
                    f32x2_to_e4m3x2(f[i][4], f[i][5]) | (f32x2_to_e4m3x2(f[i][6], f[i][7]) << 16));
   }
