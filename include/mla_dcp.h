@@ -371,7 +371,10 @@ size_t gqa_workspace_size(const gqa_shape* shape, int num_shards, int shard_id);
  * computed shard s, over the shard's visible tokens T_s:
  *   s_t = softmax_scale * q[b,i,h,:] . K_t[kh,:],  kh = h / (H / Hkv)
  *   lse_partial = ln sum exp(s_t)  (-inf if empty);
- *   out_partial = sum exp(s_t - lse) V_t[kh,:]  (0 if empty). */
+ *   out_partial = sum exp(s_t - lse) V_t[kh,:]  (0 if empty).
+ * A NaN key makes its rows NaN.  There is no q_lens here and no *_LOCAL layout:
+ * of what gqa_cache_append writes to bf16 caches this call attends to whole
+ * requests with q_len new tokens each. */
 mla_status gqa_decode_partial(const void* q, const gqa_kv_pages* kv, const int32_t* block_table,
                               int max_pages_per_req, const int32_t* seq_lens,
                               const gqa_shape* shape, int shard_id, int num_shards,
@@ -379,7 +382,8 @@ mla_status gqa_decode_partial(const void* q, const gqa_kv_pages* kv, const int32
                               void* workspace, size_t workspace_bytes, void* stream);
 
 /* LSE combine of N GQA shard partials (head_dim wide) into bf16 out
- * [B, q_len, H, D] and lse_out (may be NULL). */
+ * [B, q_len, H, D] and lse_out (may be NULL).  A shard with lse -inf counts for
+ * nothing; one with lse NaN makes the row NaN. */
 mla_status gqa_shard_combine(const float* partials, const float* lses, int num_shards,
                              const gqa_shape* shape, void* out, float* lse_out, void* stream);
 
@@ -518,6 +522,10 @@ size_t gqa_fp8_workspace_size(const gqa_shape* shape, int num_shards, int shard_
  * reads as zeros, and a context longer than its block-table row is cut at the
  * row's end, both reported as MLA_ERR_DEVICE_BOUNDS.  Shapes whose work could
  * pass 2^31 tiles (units times pages per row) are MLA_ERR_UNSUPPORTED.
+ *
+ * Made for decode and verify steps.  A prompt chunk's many queries are answered
+ * rightly, but K and V are read and multiplied once for every 32 rows of a KV
+ * head, those behind the rows' last visible token too.
  *
  * Accuracy.  A query value is held to 2^-18 of its row's largest or better.  A
  * token's weight p_t carries its V scale sv_t, and one reference serves a row:

@@ -53,7 +53,7 @@
 // 4 heads, 16 rows a unit, 112 us (5.8 TB/s; the partial kernel 6.0, of 6.5
 // that it reaches where nothing is ragged); one request of 1M tokens x 8 heads
 // in 8 shards 363 us (5.9 TB/s, the producers' cp.async); a ragged verify of up
-// to 9 tokens over 16 x 6600 tokens x 8 heads, 32 rows a unit, 81 us (the
+// to 9 tokens over 16 x 6600 tokens x 8 heads, 32 rows a unit, 83 us (the
 // softmax groups: 2900 cycles a tile each); 1024 tokens 11.5 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
