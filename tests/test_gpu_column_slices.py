@@ -60,11 +60,11 @@ def test_other_overlaps_are_refused(mla):
     flat = bf((8192,), 193).cuda()
     lens, rope = i32([5]).cuda(), rope_of(mla, 64, 0, True)
     x = flat[:1536].view(1, 3, 512).unflatten(-1, (4, 128))
-    for y in (flat[512:2048].view(1, 3, 512), flat[:3 * 1024].view(1, 3, 1024)[..., 512:],
+    for y in (flat[512:2048].view(1, 3, 512), flat[:3 * 1032].view(1, 3, 1032)[..., 512:1024],
               flat[1024:1024 + 3 * 520].view(1, 3, 520)[..., :512]):
         with pytest.raises(ValueError):
             mla.mla_rope_apply(x, rope, lens, out=y.unflatten(-1, (4, 128)))
-    y = flat[1536:3072].view(1, 3, 512).unflatten(-1, (4, 128))
+    y = flat[1600:3136].view(1, 3, 512).unflatten(-1, (4, 128))
     mla.mla_rope_apply(x, rope, lens, out=y)
     assert torch.equal(y, mla.mla_rope_apply(x, rope, lens))
     # one row of tokens shifted by a token: the same columns
