@@ -23,19 +23,23 @@ def codes_of(x):
     return x.float().to(FP8).view(torch.uint8)
 
 
-def expected(cache, scale, x, bt, lens, q_lens, block):
+def expected(cache, scale, x, bt, lens, q_lens, block, N=1, s_id=0):
     """The cache and scales [P, 64 / block, Hkv] that appending x leaves, by the
     rule: one pass over requests, blocks and heads.  Also which rows may change
     at all, and how many blocks with earlier tokens keep their scale or not."""
     cache, scale, written = cache.clone(), scale.clone(), torch.zeros(cache.shape[:3], dtype=torch.bool)
     seen = dict(kept=0, grown=0, new=0)
     for b, (L, n) in enumerate(zip(lens, q_lens)):
-        first = L - n
-        for blk in range(first // block, (L - 1) // block + 1):
+        mine = [p for p in range(L - n, L) if p % N == s_id]     # new tokens of this shard
+        if not mine:
+            continue
+        first, end = mine[0] // N, mine[-1] // N + 1             # their slots
+        rows = torch.tensor(mine) - (L - n)
+        for blk in range(first // block, (end - 1) // block + 1):
             page, row0 = int(bt[b, blk * block // PAGE]), blk * block % PAGE
             for h in range(cache.shape[2]):
-                lo, hi = max(first, blk * block), min(L, (blk + 1) * block)
-                new = x[b, lo - first:hi - first, h].double()
+                lo, hi = max(first, blk * block), min(end, (blk + 1) * block)
+                new = x[b, rows[lo - first:hi - first], h].double()
                 fin = torch.where(torch.isfinite(new), new.abs(), torch.zeros_like(new))
                 need = pow2_scale(float(fin.max()))
                 s = float(scale[page, row0 // block, h])
@@ -99,3 +103,30 @@ def test_every_byte(mla, block, Hkv, size):
         assert torch.equal(d[n].cpu()[~written], c[n][~written])
         if block > 1 and size != 1.0:
             assert seen["kept" if size < 1.0 else "grown"] > 0
+
+
+@pytest.mark.parametrize("N", [2, 3, 8])
+@pytest.mark.parametrize("block", [64, 8])
+def test_every_byte_of_a_slice(mla, N, block):
+    """A ragged batch into each rank's interleaved slice; some requests bring it
+    no token."""
+    g = torch.Generator().manual_seed(240 + N + block)
+    lens, q_lens, q_len = [70, 2, 64, 131, 900], [3, 1, 1, 70, 5], 70
+    P = 5 * 8
+    table = torch.randperm(P, generator=g).to(torch.int32).view(5, 8)
+    x = {n: bf((5, q_len, 2, 128), 250 + i, 3.0) for i, n in enumerate("kv")}
+    c = {n: torch.randint(0, 256, (P, PAGE, 2, 128), generator=g).to(torch.uint8) for n in "kv"}
+    sc = {n: torch.exp2(torch.randint(-12, -3, (P, PAGE // block, 2), generator=g).float())
+          for n in "kv"}
+    for s in range(N):
+        d = {n: t.clone().cuda() for n, t in c.items()}
+        ds = {n: t.clone().cuda() for n, t in sc.items()}
+        _, ws = mla.gqa_cache_append(x["k"].cuda(), x["v"].cuda(), d["k"], d["v"], table.cuda(),
+                                     i32(lens).cuda(), k_scale=ds["k"], v_scale=ds["v"],
+                                     q_lens=i32(q_lens).cuda(), shard_id=s, num_shards=N)
+        assert mla.mla_get_device_error(ws) == 0
+        for n in "kv":
+            want, want_s, written, _ = expected(c[n], sc[n], x[n], table, lens, q_lens, block, N, s)
+            assert torch.equal(ds[n].cpu(), want_s)
+            same_bits(d[n], want, f"{n} of shard {s}")
+            assert torch.equal(d[n].cpu()[~written], c[n][~written])
