@@ -139,6 +139,9 @@ size_t mla_workspace_size(const mla_shape* shape, int num_shards, int shard_id);
  *     s_t = softmax_scale * q[b,i,h,:] . K_t            (K_t = cache row, 576 wide)
  *     lse_partial = ln sum_{t in T_s} exp(s_t)           (-inf if T_s is empty)
  *     out_partial = sum_{t in T_s} exp(s_t - lse) * K_t[0:512]   (0 if empty)
+ * A NaN in a cache row makes the query rows that see it NaN; with causal, one
+ * among the step's own tokens reaches the outputs of the rows before it too
+ * (0 x NaN).
  * shard_id = MLA_ALL_SHARDS computes all N shards (out_partial holds N
  * slices, shard-major); shard_id in [0, N) computes that shard only
  * (n_out = 1), which is the per-GPU call of a multi-GPU deployment.
@@ -372,7 +375,9 @@ size_t gqa_workspace_size(const gqa_shape* shape, int num_shards, int shard_id);
  *   s_t = softmax_scale * q[b,i,h,:] . K_t[kh,:],  kh = h / (H / Hkv)
  *   lse_partial = ln sum exp(s_t)  (-inf if empty);
  *   out_partial = sum exp(s_t - lse) V_t[kh,:]  (0 if empty).
- * A NaN key makes its rows NaN.  There is no q_lens here and no *_LOCAL layout:
+ * A NaN key makes the rows that see it NaN, a NaN value one dim; with causal, a
+ * NaN value among the step's own tokens reaches the rows before it too (0 x NaN;
+ * not so in gqa_decode_partial_fp8).  There is no q_lens here and no *_LOCAL layout:
  * of what gqa_cache_append writes to bf16 caches this call attends to whole
  * requests with q_len new tokens each. */
 mla_status gqa_decode_partial(const void* q, const gqa_kv_pages* kv, const int32_t* block_table,
