@@ -555,6 +555,53 @@ mla_status gqa_decode_partial_fp8(const void* q, const gqa_block_pages* cache,
                                   mla_layout layout, float* out_partial, float* lse_partial,
                                   void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * Eviction from a paged latent cache by accumulated attention weight.  Request
+ * b keeps n_b = min(seq_lens[b], keep[b]) of its tokens:
+ *   - the first f_b = min(keep_first[b], n_b) (keep_first NULL: none): attention
+ *     sinks, or a prefix that it shares with other requests;
+ *   - the newest r_b = min(recent, n_b - f_b);
+ *   - of the others the n_b - f_b - r_b with the largest weights; equal ones
+ *     from the lowest position on.  NaN counts as larger than everything, the
+ *     two zeros as equal.
+ * They move in order: token kept[b][j] becomes row j of the new context, whose
+ * pages are new_block_table[b].  Rotary positions are in the rows and do not
+ * change; later appends give theirs in mla_tokens.positions.
+ *
+ *   kv               the cache, with its scales (both written; the new pages
+ *                    are pages of the same pool)
+ *   weights          fp32 [B, weights_width], weights_stride floats between
+ *                    requests (weights_width at most 2^30, at least seq_lens)
+ *   keep             int32 [B], 0 .. max_keep; keep_first int32 [B] or NULL
+ *   new_block_table  int32 [B, new_max_pages], new_max_pages >= ceil(max_keep / 64);
+ *                    entries behind a request's new pages are not read
+ *   new_seq_lens     int32 [B]: n_b; not seq_lens itself
+ *   kept             int32 [B, max_keep]: positions in the old context, ascending;
+ *                    -1 from n_b on
+ *   weights_out      fp32 [B, max_keep] or NULL: the kept tokens' weights; entries
+ *                    from n_b on are left as they were; not in weights
+ * The new pages are pages that no context uses, each in one place of
+ * new_block_table, but for leading ones: where new_block_table[b][i] is
+ * block_table[b][i] and the rows of page i all keep their place (a kept
+ * prefix), the page is left as it is and may be shared.  The same page with
+ * rows that would move is reported as MLA_ERR_INVALID and not written.  Rows
+ * behind a new context's end are left as they were, and so are the old pages.
+ *
+ * workspace: 256 bytes of device memory, zeroed once before its first use:
+ * MLA_ERR_DEVICE_BOUNDS (a page outside [0, num_pages): its rows are not moved)
+ * and MLA_ERR_INVALID (a seq_lens entry below 0, above weights_width or beyond
+ * the block table's row, a keep entry outside [0, max_keep], all clamped; a
+ * page that would be overwritten) stay there until mla_get_device_error reads
+ * them.
+ */
+mla_status mla_cache_evict(const mla_kv_pages* kv, const int32_t* block_table,
+                           int max_pages_per_req, const int32_t* seq_lens, int batch,
+                           const float* weights, long long weights_stride, int weights_width,
+                           const int32_t* keep, const int32_t* keep_first, int recent,
+                           const int32_t* new_block_table, int new_max_pages,
+                           int32_t* new_seq_lens, int32_t* kept, int max_keep, float* weights_out,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
 /* Static description of a status code. */
 const char* mla_status_string(mla_status status);
 

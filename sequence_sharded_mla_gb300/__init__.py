@@ -84,7 +84,7 @@ EXPORTS = ("mla_decode_partial", "mla_decode_partial_noalloc", "mla_decode_parti
            "mla_status_string",
            "mla_version", "gqa_workspace_size", "gqa_decode_partial", "gqa_shard_combine",
            "mla_rope_apply", "mla_cache_append", "gqa_cache_append", "gqa_fp8_workspace_size",
-           "gqa_decode_partial_fp8")
+           "gqa_decode_partial_fp8", "mla_cache_evict")
 
 
 def lib():
@@ -153,6 +153,9 @@ def lib():
         L.gqa_decode_partial_fp8.argtypes = [vp, ptr(gqa_block_pages), vp, i32, vp, vp,
                                              ptr(gqa_shape), i32, i32, i32, vp, vp, vp, sz, vp]
         L.gqa_decode_partial_fp8.restype = i32
+        L.mla_cache_evict.argtypes = [ptr(mla_kv_pages), vp, i32, vp, i32, vp, i64, i32, vp, vp, i32,
+                                      vp, i32, vp, vp, i32, vp, vp, sz, vp]
+        L.mla_cache_evict.restype = i32
         _LIB = L
     return _LIB
 
@@ -714,3 +717,29 @@ def gqa_cache_append(k, v, k_cache, v_cache, block_table, seq_lens, rope=None, q
     return _binding().heads_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens,
                                    rope, q, q_out, q_lens, positions, shard_id, num_shards,
                                    workspace, stream)
+
+
+# ------------------------------------------------------------------- eviction
+def mla_cache_evict(kv, block_table, seq_lens, weights, keep, new_block_table, keep_first=None,
+                    recent=0, kv_scale=None, kept=None, new_seq_lens=None, weights_out=None,
+                    workspace=None, stream=None):
+    """Cuts contexts of a latent cache to budgets by accumulated attention
+    weight; returns (new_seq_lens, kept, weights_out, workspace).
+
+    Request b keeps min(seq_lens[b], keep[b]) tokens: its first keep_first[b],
+    its `recent` newest, and the others with the largest weights (equal ones
+    from the lowest position on).  Their rows move in order to the pages of
+    new_block_table, which no context uses yet; leading pages of which every
+    row stays (a kept, shared prefix) may be those of block_table.
+
+    kv: bf16 or e4m3 codes [P, 64, 576] (written), with kv_scale fp32 [P, 64]
+    (written) for codes.  weights: fp32 [B, W], W at least every context (rows
+    may be further apart).  keep, keep_first: int32 [B] (device).  kept: int32
+    [B, max_keep], the kept tokens' old positions, -1 behind them (default:
+    room for new_block_table's pages); weights_out: fp32 [B, max_keep], their
+    weights; new_seq_lens: int32 [B].  workspace: 256 bytes, zeroed before its
+    first use; mla_get_device_error reads its errors.
+    """
+    return _binding().cache_evict(kv, kv_scale, block_table, seq_lens, weights, keep,
+                                  new_block_table, keep_first, recent, kept, new_seq_lens,
+                                  weights_out, workspace, stream)

@@ -1,5 +1,5 @@
-// Python entry of the rotary, cache-append and e4m3 grouped-query calls (and
-// the combine that follows them): argument checks, output allocation and the
+// Python entry of the rotary, cache-append, eviction and e4m3 grouped-query
+// calls (and the combine that follows them): argument checks, output allocation and the
 // C call, without a Python object per pointer.  A decode step's calls are a
 // few microseconds of GPU work each, so checks written in Python (10 to 30 us
 // a call on the Grace host) would be what bounds them.
@@ -379,6 +379,46 @@ gqa_block_pages block_pages(PyObject* pk, PyObject* pv, PyObject* pks, PyObject*
   return p;
 }
 
+// The mla_kv_pages descriptor of a bf16 or e4m3 latent cache.
+mla_kv_pages latent_pages(PyObject* pkv, PyObject* pscale, const c10::Device& dev) {
+  const at::Tensor& kv = tensor(pkv, "kv");
+  mla_kv_pages pages{};
+  if (kv.scalar_type() == at::kBFloat16) {
+    if (pscale != Py_None) value_error("kv_scale is only for fp8 caches");
+    pages.dtype = MLA_KV_BF16;
+  } else if (kv.scalar_type() == at::kByte || kv.scalar_type() == at::kFloat8_e4m3fn) {
+    if (pscale == Py_None) value_error("fp8 caches need kv_scale");
+    pages.dtype = MLA_KV_FP8_E4M3;
+  } else {
+    type_error(std::string("kv dtype ") + c10::toString(kv.scalar_type()) + " unsupported");
+  }
+  check(pkv, "kv", {kv.scalar_type()}, 3, &dev);
+  if (kv.size(1) != 64 || kv.size(2) != 576) value_error("kv must be [P, 64, 576]");
+  pages.data = kv.mutable_data_ptr();
+  pages.num_pages = small(kv.size(0), "kv");
+  pages.page_size = 64;
+  if (pscale != Py_None) {
+    const at::Tensor& sc = check(pscale, "kv_scale", {at::kFloat}, 2, &dev);
+    shape_is(sc, "kv_scale", {kv.size(0), kv.size(1)});
+    pages.scale = sc.mutable_data_ptr<float>();
+  }
+  return pages;
+}
+
+// fp32 rows [B, width] whose values are contiguous; floats between rows.
+int64_t row_stride(const at::Tensor& t, const char* name, int64_t B, const c10::Device& dev) {
+  if (t.scalar_type() != at::kFloat)
+    type_error(std::string(name) + ": dtype " + c10::toString(t.scalar_type()) + " is not Float");
+  on_device(t, name, &dev);
+  if (t.dim() != 2 || t.size(0) != B)
+    value_error(std::string(name) + " must be [B, width] with the batch of seq_lens");
+  if (t.size(1) > 1 && t.stride(1) != 1)
+    value_error(std::string(name) + ": a request's values must be contiguous");
+  const int64_t step = B > 1 ? t.stride(0) : t.size(1);
+  if (step < t.size(1)) value_error(std::string(name) + ": rows overlap");
+  return step;
+}
+
 // What both cache appends take besides the cache and the new rows.
 struct Append {
   const int32_t* block_table;
@@ -474,27 +514,7 @@ PyObject* latent_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t xs = token_stride(x, "latent", 1);
     const c10::Device dev = x.device();
     if (x.size(2) != 576) value_error("latent must be [B, q_len, 576]");
-    const at::Tensor& kv = tensor(a[1], "kv");
-    mla_kv_pages pages{};
-    if (kv.scalar_type() == at::kBFloat16) {
-      if (a[2] != Py_None) value_error("kv_scale is only for fp8 caches");
-      pages.dtype = MLA_KV_BF16;
-    } else if (kv.scalar_type() == at::kByte || kv.scalar_type() == at::kFloat8_e4m3fn) {
-      if (a[2] == Py_None) value_error("fp8 caches need kv_scale");
-      pages.dtype = MLA_KV_FP8_E4M3;
-    } else {
-      type_error(std::string("kv dtype ") + c10::toString(kv.scalar_type()) + " unsupported");
-    }
-    check(a[1], "kv", {kv.scalar_type()}, 3, &dev);
-    if (kv.size(1) != 64 || kv.size(2) != 576) value_error("kv must be [P, 64, 576]");
-    pages.data = kv.mutable_data_ptr();
-    pages.num_pages = small(kv.size(0), "kv");
-    pages.page_size = 64;
-    if (a[2] != Py_None) {
-      const at::Tensor& sc = check(a[2], "kv_scale", {at::kFloat}, 2, &dev);
-      shape_is(sc, "kv_scale", {kv.size(0), kv.size(1)});
-      pages.scale = sc.mutable_data_ptr<float>();
-    }
+    const mla_kv_pages pages = latent_pages(a[1], a[2], dev);
     Append p = append_arg(a + 3, x.size(0), x.size(1), 576, dev);
     const void* xp = x.const_data_ptr();
     return run_append(p, dev, "mla_cache_append",
@@ -630,6 +650,66 @@ PyObject* shard_combine(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// kv, kv_scale, block_table, seq_lens, weights, keep, new_block_table,
+// keep_first, recent, kept, new_seq_lens, weights_out, workspace, stream
+PyObject* cache_evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!want_args("cache_evict", n, 14)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    on_device(tensor(a[0], "kv"), "kv", nullptr);
+    const c10::Device dev = THPVariable_Unpack(a[0]).device();
+    const mla_kv_pages pages = latent_pages(a[0], a[1], dev);
+    const at::Tensor& sl = check(a[3], "seq_lens", {at::kInt}, 1, &dev);
+    const int64_t B = sl.size(0);
+    const at::Tensor& bt = check(a[2], "block_table", {at::kInt}, 2, &dev);
+    const at::Tensor& nbt = check(a[6], "new_block_table", {at::kInt}, 2, &dev);
+    if (bt.size(0) != B || nbt.size(0) != B)
+      value_error("block_table, new_block_table and seq_lens disagree on the number of requests");
+    const at::Tensor& w = tensor(a[4], "weights");
+    const int64_t step = row_stride(w, "weights", B, dev);
+    if (a[5] == Py_None) type_error("keep must be a torch.Tensor");
+    const int32_t* keep = ints(a[5], "keep", {B}, dev);
+    const int32_t* first = ints(a[7], "keep_first", {B}, dev);
+    const int recent = to_int(a[8], "recent");
+    at::Tensor kept, lens, wo, ws;
+    if (a[9] != Py_None) {
+      kept = check(a[9], "kept", {at::kInt}, 2, &dev);
+      if (kept.size(0) != B) value_error("kept must have a row for every request");
+    }
+    const int64_t max_keep = kept.defined() ? kept.size(1) : nbt.size(1) * 64;
+    if (a[10] != Py_None) {
+      lens = check(a[10], "new_seq_lens", {at::kInt}, 1, &dev);
+      shape_is(lens, "new_seq_lens", {B});
+    }
+    if (a[11] != Py_None) {
+      wo = check(a[11], "weights_out", {at::kFloat}, 2, &dev);
+      shape_is(wo, "weights_out", {B, max_keep});
+    }
+    if (a[12] != Py_None) ws = check(a[12], "workspace", {at::kByte}, 1, &dev);
+    const int batch = small(B, "seq_lens"), mk = small(max_keep, "kept");
+    const int width = small(w.size(1), "weights"), mp = small(bt.size(1), "block_table");
+    const int nmp = small(nbt.size(1), "new_block_table");
+    const Place place(dev, a[13]);
+    if (!ws.defined()) ws = at::zeros({256}, at::TensorOptions().dtype(at::kByte).device(dev));
+    if (!kept.defined()) kept = make({B, max_keep}, at::kInt);
+    if (!lens.defined()) lens = make({B}, at::kInt);
+    if (!wo.defined()) wo = make({B, max_keep}, at::kFloat);
+    const int32_t *btp = bt.const_data_ptr<int32_t>(), *nbp = nbt.const_data_ptr<int32_t>();
+    const int32_t* slp = sl.const_data_ptr<int32_t>();
+    const float* wp = w.const_data_ptr<float>();
+    int32_t *lp = lens.mutable_data_ptr<int32_t>(), *kp = kept.mutable_data_ptr<int32_t>();
+    float* wop = wo.mutable_data_ptr<float>();
+    void* wsp = ws.mutable_data_ptr();
+    const size_t wb = (size_t)ws.numel();
+    status(unlocked([&] {
+             return mla_cache_evict(&pages, btp, mp, slp, batch, wp, step, width, keep, first,
+                                    recent, nbp, nmp, lp, kp, mk, wop, wsp, wb, place.stream);
+           }),
+           "mla_cache_evict");
+    const Ref r0(give(a[10], lens)), r1(give(a[9], kept)), r2(give(a[11], wo)), r3(give(a[12], ws));
+    return PyTuple_Pack(4, r0.p, r1.p, r2.p, r3.p);
+  });
+}
+
 // inv_freq of a Rope: float64, one dimension, contiguous, on a CUDA device
 PyObject* check_frequencies(PyObject*, PyObject* o) {
   return guarded([&]() -> PyObject* {
@@ -656,6 +736,7 @@ PyMethodDef kMethods[] = {
     {"heads_append", fast(&heads_append), METH_FASTCALL, nullptr},
     {"attend_fp8", fast(&attend_fp8), METH_FASTCALL, nullptr},
     {"shard_combine", fast(&shard_combine), METH_FASTCALL, nullptr},
+    {"cache_evict", fast(&cache_evict), METH_FASTCALL, nullptr},
     {"check_frequencies", check_frequencies, METH_O, nullptr},
     {"set_error", set_error, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr}};

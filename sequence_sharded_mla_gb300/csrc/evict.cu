@@ -1,0 +1,436 @@
+// Eviction from the paged latent cache by accumulated attention weight: which
+// tokens of a context stay, and the move of their rows to new pages.
+//
+// A context of L tokens with a budget of K keeps its `first` leading tokens,
+// its `recent` newest ones and, of the candidates between, the k = K - first -
+// recent with the largest weights, the lowest index first among equals.
+//
+// evict_select_kernel  one cluster of CTAs per request.  A weight becomes a
+//     32-bit key whose unsigned order is the weights' order; three passes of
+//     11, 11 and 10 bits histogram the keys that match the digits chosen so
+//     far and descend into the bin that holds the k-th largest, which leaves
+//     its key T and how many of the candidates equal to T are kept.  Then
+//     every warp counts the keys above and equal to T in its slice, and with
+//     the counts before it writes its kept positions in order.  Counts are
+//     integers: the order of the shared-memory atomics cannot change them.
+// evict_copy_kernel    one block per new page: 64 rows of the source pages to
+//     one page, 16 bytes a thread and load, with their scales and weights.
+//
+// What bounds them: the copy, memory bandwidth (2 x 1152 or 2 x 580 bytes a
+// kept token); the selection of a short context, its chain of cluster
+// barriers; of a long one, five reads of the weights out of L2.
+#include <cooperative_groups.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "common.cuh"
+#include "host_util.h"
+#include "mla_dcp.h"
+#include "ptx.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace mla {
+namespace evict {
+
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
+constexpr int kBins = 2048;
+constexpr int kCopyThreads = 256;
+constexpr int kUnroll = 8;            // weights in flight per thread
+
+struct Select {
+  const int32_t* seq_lens;
+  const float* weights;
+  long long stride;                   // floats between requests' weights
+  int width;                          // weights per request
+  const int32_t* keep;
+  const int32_t* keep_first;          // or null
+  int recent;
+  int max_pages;
+  int32_t* new_lens;
+  int32_t* kept;
+  int max_keep;
+  int cluster;                        // CTAs per request
+  unsigned* err;
+};
+
+struct Copy {
+  uint8_t* data;
+  float* scale;                       // e4m3 only
+  int num_pages;
+  const int32_t* seq_lens;
+  const int32_t* block_table;
+  int max_pages;
+  const int32_t* new_block_table;
+  int new_max_pages;
+  const float* weights;
+  long long stride;
+  int width;
+  float* weights_out;                 // or null
+  const int32_t* new_lens;
+  const int32_t* kept;
+  int max_keep;
+  Div pages;                          // blocks per request
+  unsigned* err;
+};
+
+// Unsigned key in the order of the weights: -inf first, both zeros alike, NaN
+// above everything.
+__device__ __forceinline__ uint32_t key_of(float w) {
+  const uint32_t u = __float_as_uint(w);
+  if (w != w) return 0xFFFFFFFFu;
+  if (w == 0.0f) return 0x80000000u;
+  return (u >> 31) ? ~u : u | 0x80000000u;
+}
+
+struct alignas(16) Shared {
+  uint32_t hist[kBins];
+  uint32_t warp_sum[kWarps];
+  uint32_t gt[kWarps], eq[kWarps];    // per warp's slice: keys above, equal to T
+  uint32_t total_gt, total_eq;        // the CTA's
+  uint32_t bin, above;                // the descent's choice
+};
+
+// Adds to hist the digit of each of the CTA's candidates [a, b) whose upper
+// bits are `match`.  Lanes with the same digit add once between them: weights
+// crowd into few exponents, and many are zero together.
+__device__ __forceinline__ void count_digits(const float* w, int a, int b, uint32_t* hist,
+                                             uint32_t match, int upper, int shift,
+                                             uint32_t mask) {
+  const int lane = threadIdx.x & 31;
+  for (int i0 = a + (int)(threadIdx.x & ~31u); i0 < b; i0 += kThreads * kUnroll) {
+    float v[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int i = i0 + u * kThreads + lane;
+      v[u] = i < b ? __ldg(w + i) : 0.0f;
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int i = i0 + u * kThreads + lane;
+      const uint32_t k = key_of(v[u]);
+      // upper = 32 on the first pass: everything matches
+      const bool in = i < b && (upper >= 32 || (k >> upper) == match);
+      const uint32_t d = in ? (k >> shift) & mask : 0xFFFFFFFFu;
+      const uint32_t same = __match_any_sync(0xFFFFFFFFu, d);
+      if (in && lane == __ffs(same) - 1) atomicAdd(&hist[d], (uint32_t)__popc(same));
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kThreads) evict_select_kernel(Select p) {
+  __shared__ Shared sm;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int C = p.cluster, rank = (int)(blockIdx.x % C), b = (int)(blockIdx.x / C);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  griddep_wait();
+  griddep_launch_dependents();
+  const int given = p.seq_lens[b], budget = p.keep[b];
+  const int L = (int)max(0LL, min((long long)given, min((long long)p.width,
+                                                        (long long)p.max_pages * kPage)));
+  const int K = max(0, min(budget, p.max_keep));
+  if (rank == 0 && tid == 0 && (L != given || K != budget)) atomicOr(p.err, kErrQLens);
+  const int n_new = min(L, K);
+  const int first = p.keep_first != nullptr ? max(0, min(p.keep_first[b], n_new)) : 0;
+  const int recent = min(p.recent, n_new - first);
+  int32_t* out = p.kept + (size_t)b * p.max_keep;
+  if (rank == 0 && tid == 0) p.new_lens[b] = n_new;
+  const int gid = rank * kThreads + tid, step = C * kThreads;
+  const bool cut = n_new < L;
+  const int head = cut ? first : n_new;
+  for (int j = gid; j < head; j += step) out[j] = j;
+  for (int j = n_new + gid; j < p.max_keep; j += step) out[j] = -1;
+  if (cut)
+    for (int i = gid; i < recent; i += step) out[n_new - recent + i] = L - recent + i;
+  const int k = n_new - first - recent;       // candidates to keep
+  if (!cut || k == 0) return;                 // uniform over the cluster
+
+  const float* w = p.weights + (size_t)b * p.stride + first;
+  const int n = L - recent - first;           // candidates, more than k
+  // slices in whole warps of 32; CTA `rank` holds candidates [a, z)
+  const int per_warp = ((n + C * kWarps - 1) / (C * kWarps) + 31) & ~31;
+  const int a = min(n, rank * kWarps * per_warp), z = min(n, a + kWarps * per_warp);
+
+  uint32_t match = 0, left = (uint32_t)k;     // digits so far; still to take below them
+  int upper = 32;
+#pragma unroll 1
+  for (int pass = 0; pass < 3; ++pass) {
+    const int bits = pass < 2 ? 11 : 10;
+    const int shift = upper - bits;
+    const uint32_t mask = (1u << bits) - 1;
+    for (int i = tid; i < kBins; i += kThreads) sm.hist[i] = 0;
+    __syncthreads();
+    count_digits(w, a, z, sm.hist, match, upper, shift, mask);
+    cluster.sync();
+    // thread t sums bins 4t .. 4t + 3 over the cluster
+    uint32_t c[4] = {0, 0, 0, 0};
+    for (int r = 0; r < C; ++r) {
+      const uint4 v = *reinterpret_cast<const uint4*>(
+          C == 1 ? &sm.hist[4 * tid] : cluster.map_shared_rank(&sm.hist[4 * tid], r));
+      c[0] += v.x;
+      c[1] += v.y;
+      c[2] += v.z;
+      c[3] += v.w;
+    }
+    // keys in bins above this thread's: a suffix sum over the threads
+    const uint32_t own = c[0] + c[1] + c[2] + c[3];
+    uint32_t suf = own;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const uint32_t o = __shfl_down_sync(0xFFFFFFFFu, suf, off);
+      if (lane + off < 32) suf += o;
+    }
+    if (lane == 0) sm.warp_sum[warp] = suf;
+    __syncthreads();
+    uint32_t above = suf - own;
+    for (int v = warp + 1; v < kWarps; ++v) above += sm.warp_sum[v];
+#pragma unroll
+    for (int j = 3; j >= 0; --j) {
+      if (above < left && left <= above + c[j]) {   // one bin of one thread
+        sm.bin = 4 * tid + j;
+        sm.above = above;
+      }
+      above += c[j];
+    }
+    cluster.sync();              // sm.bin is there, and no peer reads hist any more
+    match = (match << bits) | sm.bin;
+    left -= sm.above;
+    upper = shift;
+  }
+  const uint32_t T = match;      // the k-th largest key; `left` of its equals stay
+
+  // each warp's slice, in order
+  const int wa = min(z, a + warp * per_warp), wz = min(z, wa + per_warp);
+  uint32_t gt = 0, eq = 0;
+  for (int i0 = wa; i0 < wz; i0 += 32 * kUnroll) {
+    float v[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int i = i0 + 32 * u + lane;
+      v[u] = i < wz ? __ldg(w + i) : 0.0f;
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const uint32_t key = key_of(v[u]);
+      const bool in = i0 + 32 * u + lane < wz;
+      gt += __popc(__ballot_sync(0xFFFFFFFFu, in && key > T));
+      eq += __popc(__ballot_sync(0xFFFFFFFFu, in && key == T));
+    }
+  }
+  if (lane == 0) {
+    sm.gt[warp] = gt;
+    sm.eq[warp] = eq;
+  }
+  __syncthreads();
+  uint32_t gt0 = 0, eq0 = 0;     // before this warp's slice
+  for (int v = 0; v < warp; ++v) {
+    gt0 += sm.gt[v];
+    eq0 += sm.eq[v];
+  }
+  if (tid == kThreads - 1) {     // the last warp's: the CTA's totals
+    sm.total_gt = gt0 + gt;
+    sm.total_eq = eq0 + eq;
+  }
+  cluster.sync();
+  for (int r = 0; r < rank; ++r) {
+    gt0 += *cluster.map_shared_rank(&sm.total_gt, r);
+    eq0 += *cluster.map_shared_rank(&sm.total_eq, r);
+  }
+  const uint32_t below = (1u << lane) - 1;
+  for (int i0 = wa; i0 < wz; i0 += 32 * kUnroll) {
+    float v[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int i = i0 + 32 * u + lane;
+      v[u] = i < wz ? __ldg(w + i) : 0.0f;
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int i = i0 + 32 * u + lane;
+      const uint32_t key = key_of(v[u]);
+      const bool in = i < wz;
+      const uint32_t mg = __ballot_sync(0xFFFFFFFFu, in && key > T);
+      const uint32_t me = __ballot_sync(0xFFFFFFFFu, in && key == T);
+      const uint32_t g = gt0 + __popc(mg & below), e = eq0 + __popc(me & below);
+      if (in && (key > T || (key == T && e < left)))
+        out[first + g + min(e, left)] = first + i;
+      gt0 += __popc(mg);
+      eq0 += __popc(me);
+    }
+  }
+  cluster.sync();                // peers have read this CTA's totals
+}
+
+// Block: one new page of one request.  kVec 16-byte pieces per row.
+template <int kVec>
+__global__ void __launch_bounds__(kCopyThreads) evict_copy_kernel(Copy p) {
+  __shared__ long long src[kPage];    // first row's byte / 16 .. of each row, -1: not moved
+  __shared__ int bad;
+  const int b = (int)blockIdx.x / p.pages, pg = (int)blockIdx.x - b * p.pages.d;
+  const int tid = threadIdx.x;
+  if (tid == 0) bad = 0;
+  griddep_wait();
+  griddep_launch_dependents();
+  const int n = p.new_lens[b], j0 = pg * kPage;
+  if (j0 >= n) return;
+  const int rows = min(kPage, n - j0);
+  const int page = p.new_block_table[(size_t)b * p.new_max_pages + pg];
+  const bool page_ok = page >= 0 && page < p.num_pages;
+  if (!page_ok) {
+    if (tid == 0) atomicOr(p.err, kErrBadPage);
+  }
+  __syncthreads();
+  const int32_t* bt = p.block_table + (size_t)b * p.max_pages;
+  float w = 0.f, sc = 0.f;
+  bool move = false;
+  if (tid < kPage) {
+    long long at = -1;
+    if (tid < rows) {
+      const int j = j0 + tid;
+      const int t = p.kept[(size_t)b * p.max_keep + j];
+      const int sp = bt[t / kPage];
+      const bool ok = sp >= 0 && sp < p.num_pages;
+      if (!ok) atomicOr(p.err, kErrBadPage);
+      if (p.weights_out != nullptr) w = p.weights[(size_t)b * p.stride + t];
+      // a row that stays where it is; any other into the request's own page of
+      // that index would overwrite rows that other blocks still read
+      const bool stays = page == sp && t == j;
+      if (!stays && page_ok && pg < p.max_pages && j0 < p.seq_lens[b] && bt[pg] == page) bad = 1;
+      if (ok && page_ok && !stays) {
+        at = (long long)sp * kPage + t % kPage;
+        move = true;
+        if (p.scale != nullptr) sc = p.scale[at];
+      }
+      if (p.weights_out != nullptr) p.weights_out[(size_t)b * p.max_keep + j] = w;
+    }
+    src[tid] = at;
+  }
+  __syncthreads();
+  if (bad) {
+    if (tid == 0) atomicOr(p.err, kErrQLens);
+    return;
+  }
+  if (p.scale != nullptr && move) p.scale[(size_t)page * kPage + tid] = sc;
+  if (!page_ok) return;
+  const uint4* from = reinterpret_cast<const uint4*>(p.data);
+  uint4* to = reinterpret_cast<uint4*>(p.data) + (size_t)page * kPage * kVec;
+  constexpr int kItems = kPage * kVec / kCopyThreads;   // 18 (bf16), 9 (e4m3)
+  constexpr int kBatch = 9;
+  static_assert(kItems % kBatch == 0, "whole batches");
+#pragma unroll 1
+  for (int i0 = 0; i0 < kItems; i0 += kBatch) {
+    uint4 v[kBatch];
+    bool live[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int e = (i0 + i) * kCopyThreads + tid, r = e / kVec, c = e - r * kVec;
+      const long long s = src[r];
+      live[i] = s >= 0;
+      if (live[i]) v[i] = from[s * kVec + c];
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int e = (i0 + i) * kCopyThreads + tid;
+      if (live[i]) to[e] = v[i];
+    }
+  }
+}
+
+// Whether the bytes [a, a + n) and [b, b + m) meet.
+inline bool overlap(const void* a, size_t n, const void* b, size_t m) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + m && y < x + n;
+}
+
+// A context is cut by a cluster of this many CTAs: one where 16 elements a
+// thread hold the longest, else eight.
+inline int cluster_size(int width) { return width <= 16 * kThreads ? 1 : 8; }
+
+}  // namespace evict
+}  // namespace mla
+
+using namespace mla;
+
+extern "C" mla_status mla_cache_evict(const mla_kv_pages* kv, const int32_t* block_table,
+                                      int max_pages_per_req, const int32_t* seq_lens, int batch,
+                                      const float* weights, long long weights_stride,
+                                      int weights_width, const int32_t* keep,
+                                      const int32_t* keep_first, int recent,
+                                      const int32_t* new_block_table, int new_max_pages,
+                                      int32_t* new_seq_lens, int32_t* kept, int max_keep,
+                                      float* weights_out, void* workspace, size_t workspace_bytes,
+                                      void* stream) {
+  using host::aligned4;
+  if (kv == nullptr || kv->data == nullptr || !host::aligned16(kv->data) || kv->num_pages < 1)
+    return MLA_ERR_INVALID;
+  if (kv->dtype != MLA_KV_BF16 && kv->dtype != MLA_KV_FP8_E4M3) return MLA_ERR_INVALID;
+  const bool fp8 = kv->dtype == MLA_KV_FP8_E4M3;
+  if (fp8 != (kv->scale != nullptr) || !aligned4(kv->scale)) return MLA_ERR_INVALID;
+  if (!block_table || !seq_lens || !weights || !keep || !new_block_table || !new_seq_lens || !kept)
+    return MLA_ERR_INVALID;
+  if (!aligned4(block_table) || !aligned4(seq_lens) || !aligned4(weights) || !aligned4(keep) ||
+      !aligned4(keep_first) || !aligned4(new_block_table) || !aligned4(new_seq_lens) ||
+      !aligned4(kept) || !aligned4(weights_out))
+    return MLA_ERR_INVALID;
+  if (batch < 1 || max_pages_per_req < 1 || new_max_pages < 1 || recent < 0 || max_keep < 1 ||
+      weights_width < 1 || weights_stride < weights_width)
+    return MLA_ERR_INVALID;
+  const int pages = (max_keep - 1) / kPage + 1;
+  if (new_max_pages < pages) return MLA_ERR_INVALID;
+  if (kv->page_size != kPage) return MLA_ERR_UNSUPPORTED;
+  if (workspace == nullptr || !host::aligned16(workspace) || workspace_bytes < sizeof(WsHeader))
+    return MLA_ERR_WORKSPACE;
+  // candidates are indexed in 32 bits, with a cluster's rounding behind them
+  if (weights_width > (1 << 30)) return MLA_ERR_UNSUPPORTED;
+  // read by every CTA while another writes
+  if (evict::overlap(seq_lens, sizeof(int32_t) * batch, new_seq_lens, sizeof(int32_t) * batch) ||
+      (weights_out != nullptr &&
+       evict::overlap(weights, sizeof(float) * ((batch - 1) * (size_t)weights_stride + weights_width),
+                      weights_out, sizeof(float) * (size_t)batch * max_keep)))
+    return MLA_ERR_INVALID;
+  const int C = evict::cluster_size(weights_width);
+  if ((long long)batch * pages >= (1LL << 31) || (long long)batch * C >= (1LL << 31))
+    return MLA_ERR_INVALID;
+  unsigned* err = &static_cast<WsHeader*>(workspace)->err;
+  const evict::Select s{seq_lens,   weights,           weights_stride, weights_width, keep,
+                        keep_first, recent,            max_pages_per_req, new_seq_lens, kept,
+                        max_keep,   C,                 err};
+  const evict::Copy c{static_cast<uint8_t*>(const_cast<void*>(kv->data)),
+                      const_cast<float*>(kv->scale),
+                      kv->num_pages,
+                      seq_lens,
+                      block_table,
+                      max_pages_per_req,
+                      new_block_table,
+                      new_max_pages,
+                      weights,
+                      weights_stride,
+                      weights_width,
+                      weights_out,
+                      new_seq_lens,
+                      kept,
+                      max_keep,
+                      make_div(pages),
+                      err};
+  cudaLaunchAttribute attr[2];
+  attr[0] = pdl_attribute();
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = C;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  cfg.gridDim = dim3((unsigned)(batch * C));
+  cfg.blockDim = dim3(evict::kThreads);
+  if (cudaLaunchKernelEx(&cfg, evict::evict_select_kernel, s) != cudaSuccess) return MLA_ERR_CUDA;
+  cfg.numAttrs = 1;
+  cfg.gridDim = dim3((unsigned)(batch * pages));
+  cfg.blockDim = dim3(evict::kCopyThreads);
+  const cudaError_t e =
+      fp8 ? cudaLaunchKernelEx(&cfg, evict::evict_copy_kernel<kDqk / 16>, c)
+          : cudaLaunchKernelEx(&cfg, evict::evict_copy_kernel<2 * kDqk / 16>, c);
+  return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+}

@@ -1,0 +1,41 @@
+"""Host-side checks of the calls for long, shared and bounded latent caches,
+which answer without a GPU."""
+import ctypes
+
+import pytest
+
+import sequence_sharded_mla_gb300 as mla
+
+INVALID, UNSUPPORTED, WORKSPACE = -1, -2, -6
+
+
+def p(x):
+    return None if x is None else ctypes.c_void_p(x)
+
+
+def evict(data=512, scale=None, dtype=0, pages=4, page=64, bt=512, mp=4, sl=512, B=2, w=1024, ws_=300,
+          width=256, keep=512, first=None, recent=0, nbt=512, nmp=2, new=8192, kept=512, mk=128,
+          wo=65536, ws=512, wb=256):
+    kv = mla.mla_kv_pages(data, scale, dtype, pages, page)
+    return mla.lib().mla_cache_evict(ctypes.byref(kv), p(bt), mp, p(sl), B, p(w), ws_, width, p(keep),
+                                     p(first), recent, p(nbt), nmp, p(new), p(kept), mk, p(wo), p(ws),
+                                     wb, None)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(data=None), INVALID), (dict(data=520), INVALID), (dict(dtype=2), INVALID),
+    (dict(dtype=1), INVALID), (dict(scale=512), INVALID), (dict(dtype=1, scale=514), INVALID),
+    (dict(pages=0), INVALID), (dict(page=32), UNSUPPORTED), (dict(bt=None), INVALID),
+    (dict(bt=514), INVALID), (dict(mp=0), INVALID), (dict(sl=None), INVALID), (dict(sl=513), INVALID),
+    (dict(B=0), INVALID), (dict(w=None), INVALID), (dict(w=1026), INVALID), (dict(ws_=255), INVALID),
+    (dict(width=0), INVALID), (dict(width=(1 << 30) + 1, ws_=1 << 31), UNSUPPORTED),
+    (dict(keep=None), INVALID), (dict(keep=514), INVALID), (dict(first=514), INVALID),
+    (dict(recent=-1), INVALID), (dict(nbt=None), INVALID), (dict(nbt=514), INVALID),
+    (dict(nmp=0), INVALID), (dict(nmp=1), INVALID), (dict(new=None), INVALID), (dict(new=512), INVALID),
+    (dict(new=516), INVALID), (dict(new=514), INVALID), (dict(kept=None), INVALID),
+    (dict(kept=514), INVALID), (dict(mk=0), INVALID), (dict(mk=129), INVALID), (dict(wo=65538), INVALID),
+    (dict(wo=1024), INVALID), (dict(wo=512), INVALID), (dict(B=1 << 30, mk=256, nmp=4), INVALID),
+    (dict(ws=None), WORKSPACE), (dict(ws=520), WORKSPACE), (dict(wb=255), WORKSPACE),
+])
+def test_eviction_refusals(kw, want):
+    assert evict(**kw) == want
