@@ -555,6 +555,46 @@ mla_status gqa_decode_partial_fp8(const void* q, const gqa_block_pages* cache,
                                   mla_layout layout, float* out_partial, float* lse_partial,
                                   void* workspace, size_t workspace_bytes, void* stream);
 
+/* Workspace bytes mla_attention_weights needs (0 for invalid shapes). */
+size_t mla_attention_weights_workspace_size(const mla_shape* shape, mla_kv_dtype dtype);
+
+/*
+ * The attention weight that a step gives to every cached token, summed over
+ * its query rows and added to what earlier steps gave -- what mla_cache_evict
+ * selects by.  For request b with n_b = q_lens[b] (or q_len) query tokens:
+ *   w[t] = sum over i < n_b, h, with t visible to i, of
+ *          exp(softmax_scale * q[b,i,h,:] . K_t - lse[b,i,h])
+ *   out[b,t] = w[t] + (before[b,t] if before != NULL and t < L_b - n_b, else 0)
+ * for t < L_b: the last n_b tokens, which the step appended, start from 0.
+ * Entries from L_b on are left as they were.  Visibility is that of the
+ * attention calls (causal: t <= L_b - n_b + i; else every t < L_b).
+ *
+ *   lse     fp32 [B, q_len, H]: the whole contexts' log-sum-exps, the lse_out of
+ *           mla_shard_combine or mla_decode_step for the same step; a row at
+ *           -inf gives nothing
+ *   before  fp32 [B, width], before_stride floats between requests, or NULL
+ *   out     fp32 [B, width], out_stride floats between requests; before itself
+ *           (with its stride), or apart from it
+ * Whole-request caches of either type, every num_heads that is a multiple of
+ * 16; width at least every L_b, at most 2^30.  Sums are fp32 in a fixed order.
+ * A NaN in a cache row makes that token's weight NaN, a NaN lse every weight
+ * of its request.  With an e4m3 cache the query is held as in
+ * mla_decode_partial, and an inf or NaN query value of a row i < n_b is
+ * reported as MLA_ERR_RANGE.
+ *
+ * workspace: mla_attention_weights_workspace_size bytes, which may hold
+ * anything and serve one call at a time; mla_get_device_error reads the last
+ * call's errors: MLA_ERR_DEVICE_BOUNDS (a page out of range, its rows count as
+ * zeros), MLA_ERR_INVALID (a seq_lens entry below 0, above width or beyond the
+ * block table's row, or a q_lens entry outside [1, q_len], clamped),
+ * MLA_ERR_RANGE, MLA_ERR_TIMEOUT.
+ */
+mla_status mla_attention_weights(const void* q, const mla_kv_pages* kv, const int32_t* block_table,
+                                 int max_pages_per_req, const int32_t* seq_lens,
+                                 const mla_shape* shape, const float* lse, const float* before,
+                                 long long before_stride, float* out, long long out_stride,
+                                 int width, void* workspace, size_t workspace_bytes, void* stream);
+
 /*
  * Eviction from a paged latent cache by accumulated attention weight.  Request
  * b keeps n_b = min(seq_lens[b], keep[b]) of its tokens:

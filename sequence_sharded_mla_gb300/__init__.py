@@ -84,7 +84,8 @@ EXPORTS = ("mla_decode_partial", "mla_decode_partial_noalloc", "mla_decode_parti
            "mla_status_string",
            "mla_version", "gqa_workspace_size", "gqa_decode_partial", "gqa_shard_combine",
            "mla_rope_apply", "mla_cache_append", "gqa_cache_append", "gqa_fp8_workspace_size",
-           "gqa_decode_partial_fp8", "mla_cache_evict")
+           "gqa_decode_partial_fp8", "mla_cache_evict",
+           "mla_attention_weights", "mla_attention_weights_workspace_size")
 
 
 def lib():
@@ -156,6 +157,11 @@ def lib():
         L.mla_cache_evict.argtypes = [ptr(mla_kv_pages), vp, i32, vp, i32, vp, i64, i32, vp, vp, i32,
                                       vp, i32, vp, vp, i32, vp, vp, sz, vp]
         L.mla_cache_evict.restype = i32
+        L.mla_attention_weights.argtypes = [vp, ptr(mla_kv_pages), vp, i32, vp, ptr(mla_shape), vp, vp,
+                                            i64, vp, i64, i32, vp, sz, vp]
+        L.mla_attention_weights.restype = i32
+        L.mla_attention_weights_workspace_size.argtypes = [ptr(mla_shape), i32]
+        L.mla_attention_weights_workspace_size.restype = sz
         _LIB = L
     return _LIB
 
@@ -719,7 +725,29 @@ def gqa_cache_append(k, v, k_cache, v_cache, block_table, seq_lens, rope=None, q
                                    workspace, stream)
 
 
-# ------------------------------------------------------------------- eviction
+# ----------------------------------------------------- weights and eviction
+def mla_attention_weights_workspace_size(batch, q_len, num_heads, fp8=False) -> int:
+    sh = _shape(batch, q_len, num_heads, False, DEFAULT_SCALE)
+    return int(lib().mla_attention_weights_workspace_size(ctypes.byref(sh), KV_FP8 if fp8 else KV_BF16))
+
+
+def mla_attention_weights(q, kv, block_table, seq_lens, lse, weights=None, out=None, kv_scale=None,
+                          causal=False, softmax_scale=DEFAULT_SCALE, workspace=None, stream=None,
+                          q_lens=None):
+    """The attention weight that a step gives to every cached token, summed
+    over its query rows and added to `weights`; returns (out, workspace).
+
+    q, kv, kv_scale, block_table, seq_lens, causal, softmax_scale, q_lens: the
+    step's, as for mla_decode_step; lse: its lse_out, fp32 [B, q_len, H].
+    weights: fp32 [B, W] of earlier steps (W at least every context; rows may be
+    further apart), or None; the tokens that the step appended start from 0.
+    out: weights itself, memory of its own of that shape, or None for a new
+    tensor with zeros behind the contexts.
+    """
+    return _binding().attention_weights(q, kv, kv_scale, block_table, seq_lens, lse, weights, out,
+                                        causal, softmax_scale, q_lens, workspace, stream)
+
+
 def mla_cache_evict(kv, block_table, seq_lens, weights, keep, new_block_table, keep_first=None,
                     recent=0, kv_scale=None, kept=None, new_seq_lens=None, weights_out=None,
                     workspace=None, stream=None):

@@ -1,5 +1,5 @@
-// Python entry of the rotary, cache-append, eviction and e4m3 grouped-query
-// calls (and the combine that follows them): argument checks, output allocation and the
+// Python entry of the rotary, cache-append, attention-weight, eviction and
+// e4m3 grouped-query calls (and the combine that follows them): argument checks, output allocation and the
 // C call, without a Python object per pointer.  A decode step's calls are a
 // few microseconds of GPU work each, so checks written in Python (10 to 30 us
 // a call on the Grace host) would be what bounds them.
@@ -650,6 +650,75 @@ PyObject* shard_combine(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// A latent step's shape from q [B, q_len, H, 576].
+mla_shape latent_shape(const at::Tensor& q, PyObject* causal, PyObject* scale, const int32_t* q_lens) {
+  if (q.size(3) != 576) value_error("q must be [B, q_len, H, 576]");
+  mla_shape sh{};
+  sh.batch = small(q.size(0), "q");
+  sh.q_len = small(q.size(1), "q");
+  sh.num_heads = small(q.size(2), "q");
+  sh.causal = to_bool(causal);
+  sh.softmax_scale = (float)to_double(scale);
+  sh.q_lens = q_lens;
+  return sh;
+}
+
+// q, kv, kv_scale, block_table, seq_lens, lse, weights, out, causal,
+// softmax_scale, q_lens, workspace, stream
+PyObject* attention_weights(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!want_args("attention_weights", n, 13)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    const at::Tensor& q = check(a[0], "q", {at::kBFloat16}, 4, nullptr);
+    const c10::Device dev = q.device();
+    const int64_t B = q.size(0);
+    const mla_kv_pages pages = latent_pages(a[1], a[2], dev);
+    const at::Tensor& bt = check(a[3], "block_table", {at::kInt}, 2, &dev);
+    const at::Tensor& sl = check(a[4], "seq_lens", {at::kInt}, 1, &dev);
+    if (bt.size(0) != B || sl.size(0) != B)
+      value_error("q, block_table and seq_lens disagree on the number of requests");
+    const mla_shape sh = latent_shape(q, a[8], a[9], ints(a[10], "q_lens", {B}, dev));
+    const at::Tensor& lse = check(a[5], "lse", {at::kFloat}, 3, &dev);
+    shape_is(lse, "lse", q.sizes().slice(0, 3));
+    at::Tensor before, out, ws;
+    int64_t bs = 0, os = 0;
+    if (a[6] != Py_None) {
+      before = tensor(a[6], "weights");
+      bs = row_stride(before, "weights", B, dev);
+    }
+    if (a[7] != Py_None) {
+      out = tensor(a[7], "out");
+      os = row_stride(out, "out", B, dev);
+      if (before.defined()) shape_is(before, "weights", out.sizes());
+    }
+    const int64_t width = out.defined() ? out.size(1) : before.defined() ? before.size(1) : bt.size(1) * 64;
+    if (a[11] != Py_None) ws = check(a[11], "workspace", {at::kByte}, 1, &dev);
+    const int w = small(width, "weights"), mp = small(bt.size(1), "block_table");
+    const Place place(dev, a[12]);
+    if (!ws.defined()) {
+      const size_t need = mla_attention_weights_workspace_size(&sh, pages.dtype);
+      ws = make({(int64_t)std::max(need, (size_t)256)}, at::kByte);
+    }
+    if (!out.defined()) {
+      out = at::zeros({B, width}, at::TensorOptions().dtype(at::kFloat).device(dev));
+      os = width;
+    }
+    const void* qp = q.const_data_ptr();
+    const int32_t *btp = bt.const_data_ptr<int32_t>(), *slp = sl.const_data_ptr<int32_t>();
+    const float* lp = lse.const_data_ptr<float>();
+    const float* bp = before.defined() ? before.const_data_ptr<float>() : nullptr;
+    float* op = out.mutable_data_ptr<float>();
+    void* wp = ws.mutable_data_ptr();
+    const size_t wb = (size_t)ws.numel();
+    status(unlocked([&] {
+             return mla_attention_weights(qp, &pages, btp, mp, slp, &sh, lp, bp, bs, op, os, w, wp,
+                                          wb, place.stream);
+           }),
+           "mla_attention_weights");
+    const Ref r0(give(a[7], out)), r1(give(a[11], ws));
+    return PyTuple_Pack(2, r0.p, r1.p);
+  });
+}
+
 // kv, kv_scale, block_table, seq_lens, weights, keep, new_block_table,
 // keep_first, recent, kept, new_seq_lens, weights_out, workspace, stream
 PyObject* cache_evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
@@ -736,6 +805,7 @@ PyMethodDef kMethods[] = {
     {"heads_append", fast(&heads_append), METH_FASTCALL, nullptr},
     {"attend_fp8", fast(&attend_fp8), METH_FASTCALL, nullptr},
     {"shard_combine", fast(&shard_combine), METH_FASTCALL, nullptr},
+    {"attention_weights", fast(&attention_weights), METH_FASTCALL, nullptr},
     {"cache_evict", fast(&cache_evict), METH_FASTCALL, nullptr},
     {"check_frequencies", check_frequencies, METH_O, nullptr},
     {"set_error", set_error, METH_O, nullptr},

@@ -39,3 +39,40 @@ def evict(data=512, scale=None, dtype=0, pages=4, page=64, bt=512, mp=4, sl=512,
 ])
 def test_eviction_refusals(kw, want):
     assert evict(**kw) == want
+
+
+def weights(q=512, data=512, scale=None, dtype=0, pages=4, page=64, bt=512, mp=4, sl=512,
+            shape=(2, 1, 16, 0, 0.07, None), lse=512, before=None, bs=0, out=65536, os_=256, width=256,
+            ws=512, wb=1 << 30):
+    kv = mla.mla_kv_pages(data, scale, dtype, pages, page)
+    sh = mla.mla_shape(*shape)
+    return mla.lib().mla_attention_weights(p(q), ctypes.byref(kv), p(bt), mp, p(sl), ctypes.byref(sh),
+                                           p(lse), p(before), bs, p(out), os_, width, p(ws), wb, None)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(q=None), INVALID), (dict(q=520), INVALID), (dict(data=None), INVALID), (dict(data=520), INVALID),
+    (dict(dtype=2), INVALID), (dict(dtype=1), INVALID), (dict(scale=512), INVALID),
+    (dict(pages=0), INVALID), (dict(pages=(1 << 24) + 1), UNSUPPORTED), (dict(page=32), UNSUPPORTED),
+    (dict(bt=None), INVALID), (dict(bt=514), INVALID), (dict(mp=0), INVALID), (dict(sl=None), INVALID),
+    (dict(sl=514), INVALID), (dict(lse=None), INVALID), (dict(lse=514), INVALID), (dict(out=None), INVALID),
+    (dict(out=514), INVALID), (dict(os_=255), INVALID), (dict(width=0), INVALID),
+    (dict(before=514, bs=256), INVALID), (dict(before=1024, bs=255), INVALID),
+    (dict(before=65540, bs=256), INVALID), (dict(before=65536, bs=300), INVALID),
+    (dict(shape=(0, 1, 16, 0, 0.07, None)), INVALID), (dict(shape=(2, 0, 16, 0, 0.07, None)), INVALID),
+    (dict(shape=(2, 1, 16, 2, 0.07, None)), INVALID), (dict(shape=(2, 1, 16, 0, 0.0, None)), INVALID),
+    (dict(shape=(2, 1, 16, 0, 0.07, 514)), INVALID), (dict(shape=(2, 1, 24, 0, 0.07, None)), UNSUPPORTED),
+    (dict(shape=(1 << 15, 256, 64, 0, 0.07, None)), UNSUPPORTED),
+    (dict(width=(1 << 30) + 1, os_=1 << 31), UNSUPPORTED),
+    (dict(shape=(1 << 10, 1, 16, 0, 0.07, None), width=1 << 30, os_=1 << 30, mp=1 << 24), UNSUPPORTED),
+    (dict(ws=None), WORKSPACE), (dict(ws=520), WORKSPACE), (dict(wb=255), WORKSPACE),
+])
+def test_weights_refusals(kw, want):
+    assert weights(**kw) == want
+
+
+def test_weights_workspace():
+    size = mla.mla_attention_weights_workspace_size
+    assert 0 < size(3, 1, 16) <= 1024
+    assert size(3, 2, 16, fp8=True) >= 96 * (1152 + 4)
+    assert size(0, 1, 16) == 0 and size(1, 0, 16) == 0
