@@ -555,6 +555,47 @@ mla_status gqa_decode_partial_fp8(const void* q, const gqa_block_pages* cache,
                                   mla_layout layout, float* out_partial, float* lse_partial,
                                   void* workspace, size_t workspace_bytes, void* stream);
 
+/* Workspace bytes mla_prefix_partial needs on the current device (0 for invalid
+ * shapes). */
+size_t mla_prefix_workspace_size(const mla_shape* shape, int num_groups, int max_pages_per_req,
+                                 mla_kv_dtype dtype);
+
+/*
+ * Partial attention of a batch whose requests share prefixes, each prefix read
+ * and multiplied once for all the query rows that share it.  Group g is the
+ * consecutive requests [group_starts[g], group_starts[g + 1]); the first
+ * prefix_lens[g] tokens of their contexts are the same, and their block-table
+ * rows name the same pages for them.  Two partials, as of two shards:
+ *   out_partial fp32 [2, B, q_len, H, 512], lse_partial fp32 [2, B, q_len, H]
+ * which mla_shard_combine (num_shards 2, with or without w_uv) turns into the
+ * attention of every request over its whole context.  Slice 0 is over shared
+ * pages, slice 1 over the rest; what falls into which is the library's choice:
+ * whole pages of a prefix that every row of the group sees are shared, a group
+ * of at most 64 rows (requests x q_len x H) shares none, and one whose
+ * prefix_lens is below a page, 0 or negative neither.
+ *
+ *   block_table, seq_lens, shape (q_lens, causal)  as in mla_decode_partial:
+ *                 whole contexts, the prefix among them
+ *   group_starts  device int32 [num_groups + 1]: from 0 to B, ascending (empty
+ *                 groups allowed); num_groups 1 .. B
+ *   prefix_lens   device int32 [num_groups]
+ * Whole-request caches; a DCP rank passes its slice's own lengths, with causal
+ * 0 (one query token).
+ *
+ * workspace: mla_prefix_workspace_size bytes, which may hold anything and serve
+ * one call at a time.  mla_get_device_error reads the last call's errors: as
+ * for mla_decode_partial, and MLA_ERR_INVALID for group_starts that are not
+ * such ranges (no prefix is shared then, the result is right all the same),
+ * MLA_ERR_DEVICE_BOUNDS for a context longer than its block-table row (cut at
+ * the row's end).
+ */
+mla_status mla_prefix_partial(const void* q, const mla_kv_pages* kv, const int32_t* block_table,
+                              int max_pages_per_req, const int32_t* seq_lens,
+                              const mla_shape* shape, const int32_t* group_starts,
+                              const int32_t* prefix_lens, int num_groups, float* out_partial,
+                              float* lse_partial, void* workspace, size_t workspace_bytes,
+                              void* stream);
+
 /* Workspace bytes mla_attention_weights needs (0 for invalid shapes). */
 size_t mla_attention_weights_workspace_size(const mla_shape* shape, mla_kv_dtype dtype);
 

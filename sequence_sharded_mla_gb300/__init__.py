@@ -85,7 +85,8 @@ EXPORTS = ("mla_decode_partial", "mla_decode_partial_noalloc", "mla_decode_parti
            "mla_version", "gqa_workspace_size", "gqa_decode_partial", "gqa_shard_combine",
            "mla_rope_apply", "mla_cache_append", "gqa_cache_append", "gqa_fp8_workspace_size",
            "gqa_decode_partial_fp8", "mla_cache_evict",
-           "mla_attention_weights", "mla_attention_weights_workspace_size")
+           "mla_attention_weights", "mla_attention_weights_workspace_size", "mla_prefix_partial",
+           "mla_prefix_workspace_size")
 
 
 def lib():
@@ -162,6 +163,11 @@ def lib():
         L.mla_attention_weights.restype = i32
         L.mla_attention_weights_workspace_size.argtypes = [ptr(mla_shape), i32]
         L.mla_attention_weights_workspace_size.restype = sz
+        L.mla_prefix_partial.argtypes = [vp, ptr(mla_kv_pages), vp, i32, vp, ptr(mla_shape), vp, vp, i32,
+                                         vp, vp, vp, sz, vp]
+        L.mla_prefix_partial.restype = i32
+        L.mla_prefix_workspace_size.argtypes = [ptr(mla_shape), i32, i32, i32]
+        L.mla_prefix_workspace_size.restype = sz
         _LIB = L
     return _LIB
 
@@ -723,6 +729,32 @@ def gqa_cache_append(k, v, k_cache, v_cache, block_table, seq_lens, rope=None, q
     return _binding().heads_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens,
                                    rope, q, q_out, q_lens, positions, shard_id, num_shards,
                                    workspace, stream)
+
+
+# ------------------------------------------------------------ shared prefixes
+def mla_prefix_workspace_size(batch, q_len, num_heads, num_groups, max_pages_per_req, fp8=False) -> int:
+    sh = _shape(batch, q_len, num_heads, False, DEFAULT_SCALE)
+    return int(lib().mla_prefix_workspace_size(ctypes.byref(sh), int(num_groups), int(max_pages_per_req),
+                                               KV_FP8 if fp8 else KV_BF16))
+
+
+def mla_prefix_partial(q, kv, block_table, seq_lens, group_starts, prefix_lens, kv_scale=None,
+                       causal=False, softmax_scale=DEFAULT_SCALE, out_partial=None, lse_partial=None,
+                       workspace=None, stream=None, q_lens=None):
+    """Partial attention of a batch whose requests share prefixes, each prefix
+    attended once for all the requests that share it; returns (out_partial,
+    lse_partial, workspace) of two partials for mla_shard_combine.
+
+    q, kv, kv_scale, block_table, seq_lens, causal, softmax_scale, q_lens: as
+    for mla_decode_partial, the contexts whole.  group_starts: int32 [G + 1]
+    (device), group g is requests group_starts[g] .. group_starts[g + 1] - 1;
+    prefix_lens: int32 [G] (device), the leading tokens that the group's
+    contexts have in common, in the same pages of their block-table rows.
+    out_partial: fp32 [2, B, q_len, H, 512]; lse_partial: fp32 [2, B, q_len, H].
+    """
+    return _binding().prefix_partial(q, kv, kv_scale, block_table, seq_lens, group_starts, prefix_lens,
+                                     causal, softmax_scale, out_partial, lse_partial, workspace, stream,
+                                     q_lens)
 
 
 # ----------------------------------------------------- weights and eviction

@@ -20,8 +20,10 @@ CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_lib")
 LIB = os.path.join(OUT_DIR, "libmla_dcp.so")
 SOURCES = ["partial.cu", "partial_fp8.cu", "wuv_gemm.cu", "plan_merge.cu", "combine.cu", "capi.cu", "noalloc.cu", "gqa.cu",
-           "gqa_fp8.cu", "append.cu", "evict.cu", "weights.cu"]
-HEADERS = ["common.cuh", "merge.cuh", "ptx.cuh", "host_util.h", "rope.cuh", "qterms.cuh"]
+           "gqa_fp8.cu", "append.cu", "evict.cu", "weights.cu",
+           "prefix.cu"]
+HEADERS = ["common.cuh", "merge.cuh", "ptx.cuh", "host_util.h", "rope.cuh", "qterms.cuh",
+           "pair.cuh", "prefix.h"]
 BINDING = os.path.join(OUT_DIR, "_binding.so")
 BINDING_STAMP = os.path.join(OUT_DIR, "_binding.built-for")
 BINDING_SOURCE = os.path.join(CSRC, "binding.cpp")

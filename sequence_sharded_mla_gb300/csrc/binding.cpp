@@ -1,5 +1,5 @@
-// Python entry of the rotary, cache-append, attention-weight, eviction and
-// e4m3 grouped-query calls (and the combine that follows them): argument checks, output allocation and the
+// Python entry of the rotary, cache-append, shared-prefix, attention-weight,
+// eviction and e4m3 grouped-query calls (and the combine that follows them): argument checks, output allocation and the
 // C call, without a Python object per pointer.  A decode step's calls are a
 // few microseconds of GPU work each, so checks written in Python (10 to 30 us
 // a call on the Grace host) would be what bounds them.
@@ -663,6 +663,58 @@ mla_shape latent_shape(const at::Tensor& q, PyObject* causal, PyObject* scale, c
   return sh;
 }
 
+// q, kv, kv_scale, block_table, seq_lens, group_starts, prefix_lens, causal,
+// softmax_scale, out_partial, lse_partial, workspace, stream, q_lens
+PyObject* prefix_partial(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!want_args("prefix_partial", n, 14)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    const at::Tensor& q = check(a[0], "q", {at::kBFloat16}, 4, nullptr);
+    const c10::Device dev = q.device();
+    const int64_t B = q.size(0);
+    const mla_kv_pages pages = latent_pages(a[1], a[2], dev);
+    const at::Tensor& bt = check(a[3], "block_table", {at::kInt}, 2, &dev);
+    const at::Tensor& sl = check(a[4], "seq_lens", {at::kInt}, 1, &dev);
+    if (bt.size(0) != B || sl.size(0) != B)
+      value_error("q, block_table and seq_lens disagree on the number of requests");
+    const mla_shape sh = latent_shape(q, a[7], a[8], ints(a[13], "q_lens", {B}, dev));
+    const at::Tensor& pl = check(a[6], "prefix_lens", {at::kInt}, 1, &dev);
+    const at::Tensor& gs = check(a[5], "group_starts", {at::kInt}, 1, &dev);
+    shape_is(gs, "group_starts", {pl.size(0) + 1});
+    at::Tensor out, lse, ws;
+    const int64_t ql = q.size(1), H = q.size(2);
+    if (a[9] != Py_None) {
+      out = check(a[9], "out_partial", {at::kFloat}, 5, &dev);
+      shape_is(out, "out_partial", {2, B, ql, H, 512});
+    }
+    if (a[10] != Py_None) {
+      lse = check(a[10], "lse_partial", {at::kFloat}, 4, &dev);
+      shape_is(lse, "lse_partial", {2, B, ql, H});
+    }
+    if (a[11] != Py_None) ws = check(a[11], "workspace", {at::kByte}, 1, &dev);
+    const int groups = small(pl.size(0), "prefix_lens"), mp = small(bt.size(1), "block_table");
+    const Place place(dev, a[12]);
+    if (!ws.defined()) {
+      const size_t need = mla_prefix_workspace_size(&sh, groups, mp, pages.dtype);
+      ws = make({(int64_t)std::max(need, (size_t)256)}, at::kByte);
+    }
+    if (!out.defined()) out = make({2, B, ql, H, 512}, at::kFloat);
+    if (!lse.defined()) lse = make({2, B, ql, H}, at::kFloat);
+    const void* qp = q.const_data_ptr();
+    const int32_t *btp = bt.const_data_ptr<int32_t>(), *slp = sl.const_data_ptr<int32_t>();
+    const int32_t *gp = gs.const_data_ptr<int32_t>(), *pp = pl.const_data_ptr<int32_t>();
+    float *op = out.mutable_data_ptr<float>(), *lp = lse.mutable_data_ptr<float>();
+    void* wp = ws.mutable_data_ptr();
+    const size_t wb = (size_t)ws.numel();
+    status(unlocked([&] {
+             return mla_prefix_partial(qp, &pages, btp, mp, slp, &sh, gp, pp, groups, op, lp, wp, wb,
+                                       place.stream);
+           }),
+           "mla_prefix_partial");
+    const Ref r0(give(a[9], out)), r1(give(a[10], lse)), r2(give(a[11], ws));
+    return PyTuple_Pack(3, r0.p, r1.p, r2.p);
+  });
+}
+
 // q, kv, kv_scale, block_table, seq_lens, lse, weights, out, causal,
 // softmax_scale, q_lens, workspace, stream
 PyObject* attention_weights(PyObject*, PyObject* const* a, Py_ssize_t n) {
@@ -805,6 +857,7 @@ PyMethodDef kMethods[] = {
     {"heads_append", fast(&heads_append), METH_FASTCALL, nullptr},
     {"attend_fp8", fast(&attend_fp8), METH_FASTCALL, nullptr},
     {"shard_combine", fast(&shard_combine), METH_FASTCALL, nullptr},
+    {"prefix_partial", fast(&prefix_partial), METH_FASTCALL, nullptr},
     {"attention_weights", fast(&attention_weights), METH_FASTCALL, nullptr},
     {"cache_evict", fast(&cache_evict), METH_FASTCALL, nullptr},
     {"check_frequencies", check_frequencies, METH_O, nullptr},

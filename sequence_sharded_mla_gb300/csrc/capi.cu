@@ -12,6 +12,7 @@
 #include "mla_dcp.h"
 #include "common.cuh"
 #include "host_util.h"
+#include "prefix.h"
 
 namespace mla {
 int partial_smem_bytes();
@@ -413,6 +414,41 @@ StepLayout step_layout(const mla_shape* shape, int num_shards) {
   return s;
 }
 
+// Workspace of the shared-prefix attention: the per-request kernel's, then the
+// own tokens' lengths and tables, the units and their split, the query's terms
+// (e4m3) and the pieces of split units.
+struct PrefixLayout {
+  size_t partial_ws, own_lens, own_table, group_pages, units, positions, work, terms, inv_scale, ws_o, ws_lse, total;
+  int max_units;
+};
+
+// false: the sizes pass what the kernels index with 32 bits
+bool prefix_layout(const mla_shape* s, int groups, int max_pages, bool fp8, int pairs,
+                   PrefixLayout* l) {
+  auto up = [](size_t v) { return (v + 255) & ~static_cast<size_t>(255); };
+  const size_t rows = (size_t)s->batch * s->q_len * s->num_heads;
+  const long long units = (long long)(rows / prefix::kPairRows) + groups;
+  if (units * (max_pages / 2 + 8LL) >= (1LL << 31)) return false;
+  l->max_units = (int)units;
+  l->partial_ws = up(mla_workspace_size(s, 1, 0));
+  l->own_lens = l->partial_ws;
+  l->own_table = l->own_lens + up(sizeof(int32_t) * (size_t)s->batch);
+  l->group_pages = l->own_table + up(sizeof(int32_t) * (size_t)s->batch * max_pages);
+  l->units = l->group_pages + up(sizeof(int32_t) * (size_t)groups);
+  l->positions = l->units + up(sizeof(int4) * (size_t)units);
+  l->work = l->positions + up(sizeof(int) * ((size_t)units + 1));
+  l->terms = l->work + up(sizeof(WsHeader));
+  l->inv_scale = l->terms + (fp8 ? up(rows * 2 * kDqk) : 0);
+  l->ws_o = l->inv_scale + (fp8 ? up(rows * sizeof(float)) : 0);
+  l->ws_lse = l->ws_o + up(sizeof(float) * (size_t)pairs * 2 * prefix::kPairRows * kDv);
+  l->total = l->ws_lse + up(sizeof(float) * (size_t)pairs * 2 * prefix::kPairRows);
+  return true;
+}
+
+bool prefix_shape_ok(const mla_shape* s, int groups, int max_pages) {
+  return shape_ok(s) && groups >= 1 && groups <= s->batch && max_pages >= 1;
+}
+
 // Rows per head from which the fused W_UV projection runs as a tensor-core
 // GEMM per head (after a combine that writes O) instead of on the CUDA cores
 // inside the combine.
@@ -537,6 +573,96 @@ mla_status mla_shard_combine(const float* partials, const float* lses, int num_s
                            shape->num_heads, static_cast<const uint16_t*>(w_uv),
                            static_cast<uint16_t*>(out), lse_out, st);
   return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+}
+
+size_t mla_prefix_workspace_size(const mla_shape* shape, int num_groups, int max_pages_per_req,
+                                 mla_kv_dtype dtype) {
+  if (!prefix_shape_ok(shape, num_groups, max_pages_per_req)) return 0;
+  if (dtype != MLA_KV_BF16 && dtype != MLA_KV_FP8_E4M3) return 0;
+  if (mla_workspace_size(shape, 1, 0) == 0) return 0;
+  const int pairs = prefix::max_pairs();
+  PrefixLayout l;
+  if (pairs <= 0 || !prefix_layout(shape, num_groups, max_pages_per_req, dtype == MLA_KV_FP8_E4M3,
+                                   pairs, &l))
+    return 0;
+  return l.total;
+}
+
+mla_status mla_prefix_partial(const void* q, const mla_kv_pages* kv, const int32_t* block_table,
+                              int max_pages_per_req, const int32_t* seq_lens,
+                              const mla_shape* shape, const int32_t* group_starts,
+                              const int32_t* prefix_lens, int num_groups, float* out_partial,
+                              float* lse_partial, void* workspace, size_t workspace_bytes,
+                              void* stream) {
+  if (!q || !kv || !block_table || !seq_lens || !group_starts || !prefix_lens || !out_partial ||
+      !lse_partial || !prefix_shape_ok(shape, num_groups, max_pages_per_req))
+    return MLA_ERR_INVALID;
+  if (kv->data == nullptr || kv->num_pages < 1) return MLA_ERR_INVALID;
+  if (kv->dtype != MLA_KV_BF16 && kv->dtype != MLA_KV_FP8_E4M3) return MLA_ERR_INVALID;
+  const bool fp8 = kv->dtype == MLA_KV_FP8_E4M3;
+  if (fp8 != (kv->scale != nullptr) || !aligned16(kv->scale)) return MLA_ERR_INVALID;
+  if (!aligned16(q) || !aligned16(kv->data) || !aligned16(out_partial) ||
+      !aligned16(lse_partial) || !aligned4(block_table) || !aligned4(seq_lens) ||
+      !aligned4(shape->q_lens) || !aligned4(group_starts) || !aligned4(prefix_lens))
+    return MLA_ERR_INVALID;
+  if (kv->page_size != kPage || kv->num_pages > (1 << 24) || shape->num_heads % 16 != 0)
+    return MLA_ERR_UNSUPPORTED;
+  if (workspace == nullptr || !aligned16(workspace)) return MLA_ERR_WORKSPACE;
+  const int pairs = prefix::max_pairs();
+  if (pairs <= 0) return MLA_ERR_CUDA;
+  PrefixLayout l;
+  if (!prefix_layout(shape, num_groups, max_pages_per_req, fp8, pairs, &l))
+    return MLA_ERR_UNSUPPORTED;
+  if (workspace_bytes < l.total) return MLA_ERR_WORKSPACE;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  const size_t rows = (size_t)shape->batch * shape->q_len * shape->num_heads;
+  prefix::Params p;
+  p.B = shape->batch;
+  p.q_len = shape->q_len;
+  p.H = shape->num_heads;
+  p.R = shape->q_len * shape->num_heads;
+  p.causal = shape->causal;
+  p.num_pages = kv->num_pages;
+  p.max_pages = max_pages_per_req;
+  p.groups = num_groups;
+  p.max_units = l.max_units;
+  p.scale_log2 = shape->softmax_scale * 1.4426950408889634f;
+  p.block_table = block_table;
+  p.seq_lens = seq_lens;
+  p.q_lens = shape->q_lens;
+  p.group_starts = group_starts;
+  p.prefix_lens = prefix_lens;
+  p.q = static_cast<const uint16_t*>(q);
+  p.kv_scale = kv->scale;
+  p.terms = ws + l.terms;
+  p.inv_scale = reinterpret_cast<float*>(ws + l.inv_scale);
+  p.own_lens = reinterpret_cast<int32_t*>(ws + l.own_lens);
+  p.own_table = reinterpret_cast<int32_t*>(ws + l.own_table);
+  p.group_pages = reinterpret_cast<int32_t*>(ws + l.group_pages);
+  p.units = reinterpret_cast<int4*>(ws + l.units);
+  p.positions = reinterpret_cast<int*>(ws + l.positions);
+  p.work = reinterpret_cast<WsHeader*>(ws + l.work);
+  p.err = &reinterpret_cast<WsHeader*>(ws)->err;   // reset by the per-request kernel's plan
+  p.ws_o = reinterpret_cast<float*>(ws + l.ws_o);
+  p.ws_lse = reinterpret_cast<float*>(ws + l.ws_lse);
+  p.out = out_partial;
+  p.lse = lse_partial;
+  p.timeout_ns = host::wait_budget_ns(kTimeoutNs);
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  if (prefix::launch_prep(p, fp8, pairs, cs) != cudaSuccess) return MLA_ERR_CUDA;
+  float* own_out = out_partial + rows * kDv;
+  float* own_lse = lse_partial + rows;
+  Launched L;
+  const mla_status st =
+      partial_launch(q, kv, p.own_table, max_pages_per_req, p.own_lens, shape, 0, 1,
+                     MLA_LAYOUT_INTERLEAVED, own_out, own_lse, workspace, l.partial_ws, stream, &L);
+  if (st != MLA_OK) return st;
+  if (launch_merge(L.pd, L.hdr, L.prefix, L.ws_o, L.ws_lse, own_out, own_lse, L.num_units, cs) !=
+          cudaSuccess ||
+      prefix::launch_attend(p, kv->data, fp8, pairs, cs) != cudaSuccess ||
+      prefix::launch_join(p, cs) != cudaSuccess)
+    return MLA_ERR_CUDA;
+  return MLA_OK;
 }
 
 mla_status mla_set_profile_events(void* before_partial, void* after_partial) {

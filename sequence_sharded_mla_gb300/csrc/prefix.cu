@@ -1,0 +1,1010 @@
+// Attention of a batch over long prefixes that its requests share: the shared
+// pages are attended once for all the rows of a group of requests, in tiles of
+// 128 rows, instead of once per request.
+//
+//   o = sum_t exp(s_t - lse) c_t,  lse = ln sum_t exp(s_t),  s_t = scale q . K_t
+//
+// over the group's shared pages, for every query row of its requests.  What
+// lies behind them (the requests' own tokens) the per-request kernel attends;
+// the two partials meet in the LSE combine, as two shards do.
+//
+// A group of many rows is bounded by the tensor cores, not by memory: 128 rows
+// do 242 operations for every byte of a bf16 row.  An accumulator of 128 rows x
+// 512 dims would fill a CTA's tensor memory, so two CTAs (a cluster of two, one
+// per SM) hold it between them, 64 rows each, and their tensor cores work
+// together (cta_group::2, M = 128): each CTA gives the MMAs its 64 rows of A
+// and half of B.
+//
+//   S = Q K^T   N = 128 tokens: CTA r gives page 2j + r (all 576 dims)
+//   O += P V    K = 128 tokens, N = 256 dims, twice: CTA r gives the dims
+//               256 r .. 256 r + 255 of both pages
+//
+// Both descriptors mean the same offset in both CTAs, which fixes the tile's
+// place in shared memory: the nine 64-dim chunks of the CTA's own page, A =
+// chunks 0-3, B = chunks 4-7, C = chunk 8 (rope).  P V reads page 2j at A and
+// page 2j + 1 at B.  CTA 0 keeps its A (its dims of its page) and, once S is
+// done, loads its dims of page 2j + 1 over B; CTA 1 keeps B and loads over A.
+// So a tile costs a CTA 13 chunks of loads and 9 of space.
+//
+//   warp 0      producer: K of the tiles ahead, V of the current one
+//   warp 1      S issue (leader only)
+//   warps 2..5  softmax: a thread has one row and 64 tokens; the two threads of
+//               a row exchange their maxima; O is rescaled only when a running
+//               maximum grows by more than 2^8; the epilogue
+//   warp 6      P V issue (leader only)
+//   warp 7      e4m3: the tile's token scales, split into mantissa and exponent
+//
+// e4m3 caches: the MMAs take the codes as they are, the query and the
+// probabilities as two-term e4m3 sums, as in the per-request kernel; three
+// stages.  bf16: two stages, probabilities in the stage's rope chunk (tokens
+// 0-63) and one chunk of their own (64-127).
+//
+// Work is (group, 128 rows, tile of 128 tokens), split evenly over the pairs;
+// pieces of a unit that was split are joined by their LSEs.
+#include <cuda_bf16.h>
+#include <math_constants.h>
+
+#include <algorithm>
+#include <cstddef>
+
+#include "common.cuh"
+#include "host_util.h"
+#include "merge.cuh"
+#include "pair.cuh"
+#include "prefix.h"
+#include "ptx.cuh"
+#include "qterms.cuh"
+
+namespace mla {
+namespace prefix {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kHalf = 64;                    // rows, and tokens of a tile, per CTA
+constexpr int kPrepThreads = 1024;
+// Work positions charged to a unit for its fixed costs (query load, pipeline
+// refill, the epilogue's 256 KB of output).
+constexpr int kUnitCost = 3;
+constexpr int kMinTiles = 2;
+constexpr uint32_t kBarPair = 2;             // named barriers 2, 3: the warps of the same rows
+constexpr float kRescale = 8.0f;             // log2 units
+constexpr uint32_t kTmemCols = 512, kColS = 0, kColO = 128;
+constexpr int kQBytes = kTileBytes;          // 73728, either type
+
+// ------------------------------------------------------------------ planning
+__device__ __forceinline__ int queries(const Params& p, int b) {
+  return p.q_lens != nullptr ? min(max(p.q_lens[b], 0), p.q_len) : p.q_len;
+}
+
+// Whether the groups are consecutive ranges that cover the batch (whole block).
+__device__ __forceinline__ bool groups_ok(const Params& p) {
+  bool ok = true;
+  for (int g = threadIdx.x; g <= p.groups; g += blockDim.x) {
+    const int s = p.group_starts[g];
+    if (g == 0) ok &= s == 0;
+    if (g == p.groups) ok &= s == p.B;
+    else ok &= s >= 0 && s <= p.group_starts[g + 1];
+  }
+  return __syncthreads_and(ok) != 0;
+}
+
+// Requests of group g; one group of everything if the groups are no ranges.
+__device__ __forceinline__ void group_range(const Params& p, bool ok, int g, int& b0, int& b1) {
+  b0 = ok ? p.group_starts[g] : 0;
+  b1 = ok ? p.group_starts[g + 1] : g == 0 ? p.B : 0;
+  b1 = max(b0, b1);
+}
+
+// Whole shared pages of group g that every query row of it sees (whole warp).  A
+// group of at most 64 rows has none: the per-request kernel reads its pages
+// once already.
+__device__ __forceinline__ int shared_pages(const Params& p, bool ok, int g, int b0, int b1) {
+  if (!ok || (long long)(b1 - b0) * p.R <= kRows) return 0;
+  int n = min(p.prefix_lens[g] / kPage, p.max_pages);
+  for (int b = b0 + (int)(threadIdx.x & 31); b < b1; b += 32) {
+    const int L = p.seq_lens[b], seen = p.causal ? L - queries(p, b) + 1 : L;
+    n = min(n, seen / kPage);
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) n = min(n, __shfl_xor_sync(0xFFFFFFFFu, n, off));
+  return max(n, 0);
+}
+
+// Block 0: units and their split.  Blocks 1 .. B: a request's own tokens.  The
+// others (e4m3): a query row per warp.
+__global__ void __launch_bounds__(kPrepThreads) prefix_prep_kernel(Params p, int pairs) {
+  griddep_wait();
+  griddep_launch_dependents();
+  if (blockIdx.x > (unsigned)p.B) {
+    const int row = ((int)blockIdx.x - 1 - p.B) * (kPrepThreads / 32) + (threadIdx.x >> 5);
+    if (row >= p.B * p.R) return;
+    const int b = row / p.R;
+    split_query_row(p.q + (size_t)row * kDqk, row - b * p.R < queries(p, b) * p.H,
+                    p.terms + (size_t)row * 2 * kDqk, p.inv_scale + row, threadIdx.x & 31);
+    return;
+  }
+  const bool ok = groups_ok(p);
+  if (blockIdx.x > 0) {
+    const int b = (int)blockIdx.x - 1;
+    // its group: the last one that starts at or before it
+    int lo = 0, hi = p.groups - 1;
+    while (ok && lo < hi) {
+      const int m = (lo + hi + 1) >> 1;
+      if (p.group_starts[m] <= b) lo = m;
+      else hi = m - 1;
+    }
+    int b0, b1;
+    group_range(p, ok, lo, b0, b1);
+    __shared__ int shared_n;
+    if (threadIdx.x < 32) {
+      const int n = shared_pages(p, ok, lo, b0, b1);
+      if (threadIdx.x == 0) shared_n = n;
+    }
+    __syncthreads();
+    const int n = shared_n;
+    // a context longer than its table is cut at the table's end
+    const int L = (int)min((long long)p.seq_lens[b], (long long)p.max_pages * kPage);
+    if (threadIdx.x == 0) p.own_lens[b] = L - n * kPage;
+    const int32_t* from = p.block_table + (size_t)b * p.max_pages + n;
+    int32_t* to = p.own_table + (size_t)b * p.max_pages;
+    const int live = ceil_div(max(L, 0), kPage) - n;
+    for (int i = threadIdx.x; i < live; i += kPrepThreads) to[i] = from[i];
+    return;
+  }
+  __shared__ int part[kPrepThreads];
+  const int tid = threadIdx.x;
+  bool fits = true;
+  for (int b = tid; b < p.B; b += kPrepThreads)
+    fits &= p.seq_lens[b] <= (long long)p.max_pages * kPage;
+  const unsigned bad = (ok ? 0u : kErrQLens) | (__syncthreads_and(fits) ? 0u : kErrBadPage);
+  for (int g = tid >> 5; g < p.groups; g += kPrepThreads / 32) {
+    int b0, b1;
+    group_range(p, ok, g, b0, b1);
+    const int n = shared_pages(p, ok, g, b0, b1);
+    if ((tid & 31) == 0) p.group_pages[g] = n;
+  }
+  const int per = ceil_div(p.groups, kPrepThreads), g0 = min(p.groups, tid * per);
+  const int g1 = min(p.groups, g0 + per);
+  auto tiles_of_rows = [&](int g) {
+    int b0, b1;
+    group_range(p, ok, g, b0, b1);
+    return (int)(((long long)(b1 - b0) * p.R + kPairRows - 1) / kPairRows);
+  };
+  int sum = 0;
+  for (int g = g0; g < g1; ++g) sum += tiles_of_rows(g);
+  part[tid] = sum;
+  __syncthreads();
+  for (int off = 1; off < kPrepThreads; off <<= 1) {
+    const int v = tid >= off ? part[tid - off] : 0;
+    __syncthreads();
+    part[tid] += v;
+    __syncthreads();
+  }
+  int u = part[tid] - sum;
+  for (int g = g0; g < g1; ++g) {
+    int b0, b1;
+    group_range(p, ok, g, b0, b1);
+    const int n = p.group_pages[g];
+    for (int r = b0 * p.R; r < b1 * p.R; r += kPairRows) p.units[u++] = make_int4(r, b1 * p.R, b0, n);
+  }
+  const int total = part[kPrepThreads - 1];
+  for (int v = total + tid; v < p.max_units; v += kPrepThreads) p.units[v] = make_int4(0, 0, 0, 0);
+  __syncthreads();
+  plan_units(p.max_units, [&](int v) { return (p.units[v].w + 1) / 2; }, p.work, p.positions,
+             pairs, kMinTiles, kUnitCost, bad);
+}
+
+// ------------------------------------------------------------------ attention
+enum Part { kA = 0, kB = 1, kC = 2, kV = 3 };   // of a tile's loads
+
+template <bool kFp8>
+struct Cfg {
+  static constexpr int kStages = kFp8 ? 3 : 2;
+  static constexpr int kLine = kFp8 ? 64 : 128;          // bytes of a chunk's row
+  static constexpr int kSlot = kHalf * kLine;            // a page's chunk
+  static constexpr int kTile = kChunks * kSlot;
+  static constexpr int kGroup = 8 * kLine;               // eight rows of a chunk
+  static constexpr int kSmemKV = kQBytes;
+  static constexpr int kSmemP = kSmemKV + kStages * kTile;
+  // bf16: the second half's probabilities; e4m3: two buffers of both terms
+  static constexpr int kSmemMisc = kSmemP + (kFp8 ? 2 * 4 * kSlot : kSlot);
+};
+
+template <bool kFp8>
+struct Misc {
+  static constexpr int kStages = Cfg<kFp8>::kStages;
+  uint64_t full[kStages][4];     // leader: loads of both CTAs landed
+  uint64_t a_free[kStages];      // P V has read A
+  uint64_t pv_done[kStages];     // P V has read everything
+  uint64_t s_full[2];
+  uint64_t s_empty[2], p_full[2], o_free;   // leader: the softmax warps of both
+  uint64_t q_full, q_empty;
+  uint64_t drain;
+  uint64_t sc_full[kFp8 ? kStages : 1], sc_ready[kFp8 ? kStages : 1];
+  uint32_t tmem_base;
+  int abort;
+  uint32_t armed[kStages][4];    // loads announced on full, for a teardown
+  uint32_t armed_q;
+  float xmax[2][2][kHalf];       // by tile parity and half of the tokens
+  // token scales (copied in 16-byte units, read as float4) and their exponents
+  alignas(16) float sigma[kFp8 ? kStages : 1][kFp8 ? 128 : 4];
+  alignas(16) float lge[kFp8 ? kStages : 1][kFp8 ? 128 : 4];
+};
+static_assert(offsetof(Misc<true>, sigma) % 16 == 0 && offsetof(Misc<true>, lge) % 16 == 0,
+              "16-byte units");
+static_assert(Cfg<true>::kSmemMisc % 1024 == 0 && Cfg<false>::kSmemMisc % 1024 == 0,
+              "swizzle atoms and 16-byte units");
+
+template <bool kFp8>
+constexpr int smem_bytes() {
+  return Cfg<kFp8>::kSmemMisc + (int)sizeof(Misc<kFp8>) + 1024;
+}
+static_assert(smem_bytes<false>() <= 232448 && smem_bytes<true>() <= 232448, "shared memory");
+
+// One role's walk over the pair's tiles.
+struct Walk {
+  PieceIter it;
+  const int4* units;
+  int4 u;                        // the unit: first row, end row, table row, pages
+  int j, t1;                     // the tile, the piece's end
+  int g;                         // tiles before this one
+  bool whole, first;             // the piece is the whole unit; its first tile
+  int slot;
+  __device__ void init(const Params& p, int lo, int hi) {
+    it.init(p.positions, p.work->num_units, lo, hi, p.work->unit_cost);
+    units = p.units;
+    j = t1 = 0;
+    g = -1;
+  }
+  __device__ bool next() {
+    first = ++j >= t1;
+    if (first) {
+      int unit;
+      if (!it.next(unit, j, t1, whole, slot)) return false;
+      u = units[unit];
+    }
+    ++g;
+    return true;
+  }
+};
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<uint32_t*>(&h);
+}
+
+template <bool kFp8>
+__global__ void __launch_bounds__(kThreads, 1)
+    prefix_kernel(const __grid_constant__ CUtensorMap tm_q,
+                  const __grid_constant__ CUtensorMap tm_kv4,
+                  const __grid_constant__ CUtensorMap tm_kv1, Params p) {
+  using C = Cfg<kFp8>;
+  constexpr int kStages = C::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  Misc<kFp8>* misc = reinterpret_cast<Misc<kFp8>*>(smem + C::kSmemMisc);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const bool leader = rank == 0;
+  griddep_wait();                // the work list, the query's terms
+  griddep_launch_dependents();
+
+  const int W = p.work->total_cost, per = p.work->per_cta;
+  const int pair = (int)blockIdx.x >> 1;
+  const int lo = (int)min((long long)W, (long long)pair * per);
+  if (lo >= W) return;           // both CTAs of the pair
+  const int hi = (int)min((long long)W, (long long)lo + per);
+
+  volatile int* abort_flag = &misc->abort;
+  const uint64_t tmo = p.timeout_ns;
+  const uint32_t peer_abort = map_rank(smem_u32(&misc->abort), rank ^ 1);
+  auto fail = [&]() {            // one thread: both CTAs leave their loops
+    atomicOr(p.err, kErrTimeout);
+    *(volatile int*)&misc->abort = 1;
+    st_cluster(peer_abort, 1);
+  };
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_wait_cluster(smem_u32(bar), parity, tmo, abort_flag));
+  };
+  auto at_leader = [&](uint64_t* bar) { return map_rank(smem_u32(bar), 0); };
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      for (int k = 0; k < 4; ++k) {
+        mbar_init(smem_u32(&misc->full[s][k]), 2);
+        misc->armed[s][k] = 0;
+      }
+      mbar_init(smem_u32(&misc->a_free[s]), 1);
+      mbar_init(smem_u32(&misc->pv_done[s]), 1);
+      if (kFp8) {
+        mbar_init(smem_u32(&misc->sc_full[s]), 1);
+        mbar_init(smem_u32(&misc->sc_ready[s]), 1);
+      }
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&misc->s_full[i]), 1);
+      mbar_init(smem_u32(&misc->s_empty[i]), 8);
+      mbar_init(smem_u32(&misc->p_full[i]), 8);
+    }
+    mbar_init(smem_u32(&misc->o_free), 8);
+    mbar_init(smem_u32(&misc->q_full), 2);
+    mbar_init(smem_u32(&misc->q_empty), 1);
+    mbar_init(smem_u32(&misc->drain), 2);
+    misc->armed_q = 0;
+    misc->abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) tmem_alloc_pair(smem_u32(&misc->tmem_base), kTmemCols);
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tm_q);
+    tma_prefetch_desc(&tm_kv4);
+    tma_prefetch_desc(&tm_kv1);
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();            // the peer's barriers and tensor memory are there
+  tc_fence_after();
+  const uint32_t tmem = misc->tmem_base;
+  const uint32_t sQ = smem_u32(smem), sKV = smem_u32(smem + C::kSmemKV);
+  const uint32_t sP = smem_u32(smem + C::kSmemP);
+
+  Walk w;
+  w.init(p, lo, hi);
+  bool ok = true;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    // Announces `bytes` of a part of a stage on the leader's barrier.
+    auto arm = [&](int s, int part, uint32_t bytes) {
+      misc->armed[s][part]++;
+      mbar_arrive_expect_tx_cluster(at_leader(&misc->full[s][part]), bytes);
+    };
+    // Page `i` of the walk's prefix; one behind it or out of range lies behind
+    // the pool, where loads give zeros.
+    auto page_of = [&](const Walk& x, int i) {
+      int page = p.num_pages;
+      if (i < x.u.w) {
+        page = __ldg(p.block_table + (size_t)x.u.z * p.max_pages + i);
+        if (page < 0 || page >= p.num_pages) {
+          if (lane == 0) atomicOr(p.err, kErrBadPage);
+          page = p.num_pages;
+        }
+      }
+      return page;
+    };
+    int pieces = 0;              // pieces whose query was loaded
+    auto load_k = [&](const Walk& x) {
+      const int s = x.g % kStages, use = x.g / kStages;
+      const uint32_t st = sKV + s * C::kTile;
+      const int row = page_of(x, 2 * x.j + (int)rank) * kPage;
+      if (x.first) {
+        if (pieces > 0) ok = wait(&misc->q_empty, (pieces - 1) & 1);
+        if (!ok) return;
+        if (lane == 0) {
+          misc->armed_q++;
+          mbar_arrive_expect_tx_cluster(at_leader(&misc->q_full), kQBytes);
+          const int r0 = x.u.x + (int)rank * kHalf;
+          if (kFp8) {
+            tma_load_4d_pair(sQ, &tm_q, at_leader(&misc->q_full), 0, r0, 0, 0);
+            tma_load_4d_pair(sQ + kQBytes / 2, &tm_q, at_leader(&misc->q_full), 0, r0, 0, 1);
+          } else {
+            tma_load_3d_pair(sQ, &tm_q, at_leader(&misc->q_full), 0, r0, 0);
+          }
+        }
+        __syncwarp();
+        ++pieces;
+      }
+      if (use > 0) ok = wait(&misc->a_free[s], (use - 1) & 1);
+      if (!ok) return;
+      if (lane == 0) {
+        arm(s, kA, 4 * C::kSlot);
+        tma_load_3d_pair(st, &tm_kv4, at_leader(&misc->full[s][kA]), 0, row, 0);
+      }
+      __syncwarp();
+      if (use > 0) ok = wait(&misc->pv_done[s], (use - 1) & 1);
+      if (!ok) return;
+      if (lane == 0) {
+        arm(s, kB, 4 * C::kSlot);
+        tma_load_3d_pair(st + 4 * C::kSlot, &tm_kv4, at_leader(&misc->full[s][kB]), 0, row, 4);
+        arm(s, kC, C::kSlot);
+        tma_load_3d_pair(st + 8 * C::kSlot, &tm_kv1, at_leader(&misc->full[s][kC]), 0, row, 8);
+      }
+      __syncwarp();
+      if (kFp8) {
+        // both pages' token scales; 1 where there is no page (its codes are 0)
+        uint32_t bytes = 0;
+        const float* src[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int page = page_of(x, 2 * x.j + h);
+          src[h] = page < p.num_pages ? p.kv_scale + (size_t)page * kPage : nullptr;
+          if (src[h] != nullptr) bytes += kPage * 4;
+          else misc->sigma[s][64 * h + lane] = misc->sigma[s][64 * h + 32 + lane] = 1.0f;
+        }
+        __syncwarp();
+        if (lane == 0) {
+          const uint32_t bar = smem_u32(&misc->sc_full[s]);
+          mbar_arrive_expect_tx(bar, bytes);
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            if (src[h] != nullptr)
+              bulk_load(smem_u32(&misc->sigma[s][64 * h]), src[h], kPage * 4, bar);
+        }
+        __syncwarp();
+      }
+    };
+    // The CTA's dims of the other CTA's page, over what S has read.
+    auto load_v = [&](const Walk& x) {
+      const int s = x.g % kStages;
+      const int row = page_of(x, 2 * x.j + (int)(rank ^ 1)) * kPage;
+      ok = wait(&misc->s_full[x.g & 1], (x.g >> 1) & 1);
+      if (!ok) return;
+      if (lane == 0) {
+        arm(s, kV, 4 * C::kSlot);
+        tma_load_3d_pair(sKV + s * C::kTile + (leader ? 4 : 0) * C::kSlot, &tm_kv4,
+                         at_leader(&misc->full[s][kV]), 0, row, leader ? 0 : 4);
+      }
+      __syncwarp();
+    };
+    // K runs ahead of V: two tiles first, then after V of tile g the K of tile
+    // g + stages - 1, which waits for P V of tile g - 1 (V of tile g waits for
+    // its S only).  K of tile g + 2 never goes out before V of tile g: S of tile
+    // g + 2 would end a second phase of the barrier that V of tile g waits on.
+    Walk k;
+    k.init(p, lo, hi);
+    bool more = true;
+    for (int i = 0; i < 2 && ok && more; ++i) {
+      more = k.next();
+      if (more) load_k(k);
+    }
+    while (ok && w.next()) {
+      load_v(w);
+      if (ok && more && (kStages > 2 || w.g > 0)) {
+        more = k.next();
+        if (more) load_k(k);
+      }
+    }
+    if (!ok && lane == 0) fail();
+  } else if (warp == 1 && leader) {
+    // ------------------------------------------------------------ S issue
+    constexpr uint32_t id = kFp8 ? idesc_e4m3_f32(128, 128, false, false)
+                                 : idesc_bf16_f32(128, 128, false, false);
+    int pieces = 0;
+    Walk n = w;                  // the next tile: is this one its piece's last?
+    n.next();
+    while (ok && w.next()) {
+      const int s = w.g % kStages, sb = w.g & 1;
+      if (w.first) {
+        ok = wait(&misc->q_full, pieces & 1);
+        ++pieces;
+      }
+      if (ok && w.g >= 2) ok = wait(&misc->s_empty[sb], ((w.g >> 1) - 1) & 1);
+      const bool last = !n.next() || n.first;
+      const uint32_t d = tmem + kColS + 64 * sb;
+#pragma unroll
+      for (int part = 0; part < 3; ++part) {
+        if (ok) ok = wait(&misc->full[s][part], (w.g / kStages) & 1);
+        if (!ok) break;
+        tc_fence_after();
+        if (lane == 0) {
+#pragma unroll
+          for (int c = 4 * part; c < (part == kC ? 9 : 4 * part + 4); ++c) {
+            const uint32_t k0 = sKV + s * C::kTile + c * C::kSlot, q0 = sQ + c * C::kSlot;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t acc = (c > 0 || k > 0) ? 1u : 0u;
+              if (kFp8)          // k: 32-dim step k / 2, term k % 2 of the query
+                mma_e4m3_pair(d, sw64_desc(q0 + (k & 1) * (kQBytes / 2) + 32 * (k >> 1), 16, C::kGroup),
+                              sw64_desc(k0 + 32 * (k >> 1), 16, C::kGroup), id, acc);
+              else
+                mma_bf16_pair(d, sw128_desc(q0 + 32 * k, 16, C::kGroup),
+                              sw128_desc(k0 + 32 * k, 16, C::kGroup), id, acc);
+            }
+          }
+          if (part == kC) {
+            mma_commit_pair(smem_u32(&misc->s_full[sb]));
+            if (last) mma_commit_pair(smem_u32(&misc->q_empty));
+          }
+        }
+        __syncwarp();
+      }
+    }
+    if (!ok && lane == 0) fail();
+  } else if (warp == 6 && leader) {
+    // ------------------------------------------------------------ P V issue
+    constexpr uint32_t id = kFp8 ? idesc_e4m3_f32(128, 256, false, true)
+                                 : idesc_bf16_f32(128, 256, false, true);
+    int pieces = 0;
+    while (ok && w.next()) {
+      const int s = w.g % kStages;
+      ok = wait(&misc->p_full[w.g & 1], (w.g >> 1) & 1);
+      if (ok) ok = wait(&misc->full[s][kV], (w.g / kStages) & 1);
+      if (w.first) {
+        if (ok && pieces > 0) ok = wait(&misc->o_free, (pieces - 1) & 1);
+        ++pieces;
+      }
+      if (!ok) break;
+      tc_fence_after();
+      if (lane == 0) {
+        const uint32_t st = sKV + s * C::kTile;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {             // tokens 64 half ..
+          const uint32_t p0 = kFp8 ? sP + (w.g & 1) * 4 * C::kSlot + half * C::kSlot
+                                   : half == 0 ? st + 8 * C::kSlot : sP;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            // bf16: 16 tokens; e4m3: 32 tokens k / 2, term k % 2
+            const uint32_t a = kFp8 ? p0 + (k & 1) * 2 * C::kSlot + 32 * (k >> 1) : p0 + 32 * k;
+            const uint32_t v = st + 4 * half * C::kSlot + 2048 * (kFp8 ? k >> 1 : k);
+#pragma unroll
+            for (int nb = 0; nb < 2; ++nb) {               // 128 dims of each CTA
+              const uint32_t d = tmem + kColO + 128 * nb, b = v + 2 * nb * C::kSlot;
+              const uint32_t acc = (w.first && half == 0 && k == 0) ? 0u : 1u;
+              if (kFp8)
+                mma_e4m3_pair(d, sw64_desc(a, 16, C::kGroup), sw64_desc(b, C::kSlot, C::kGroup), id, acc);
+              else
+                mma_bf16_pair(d, sw128_desc(a, 16, C::kGroup), sw128_desc(b, C::kSlot, C::kGroup), id,
+                              acc);
+            }
+          }
+          mma_commit_pair(smem_u32(half == 0 ? &misc->a_free[s] : &misc->pv_done[s]));
+        }
+      }
+      __syncwarp();
+    }
+    if (!ok && lane == 0) fail();
+  } else if (warp == 7 && kFp8) {
+    // ------------------------------------------------------- token scales
+    // sigma = mant 2^E with mant in [0.5, 1): sigma sanitised in place, E apart
+    while (ok && w.next()) {
+      const int s = w.g % kStages;
+      ok = wait(&misc->sc_full[s], (w.g / kStages) & 1);
+      if (!ok) break;
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        const int a = lane + 32 * h;
+        float sg = misc->sigma[s][a];
+        uint32_t eb = (__float_as_uint(sg) >> 23) & 0xFFu;
+        if (eb < 27u) {
+          // zero, subnormal or below 2^-100: as 2^-60
+          sg = copysignf(8.6736174e-19f, sg);
+          eb = (__float_as_uint(sg) >> 23) & 0xFFu;
+        }
+        misc->sigma[s][a] = sg;
+        // inf, NaN or >= 2^126: exponent 0, and the value itself propagates
+        misc->lge[s][a] = eb >= 253u ? 0.0f : (float)((int)eb - 126);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&misc->sc_ready[s]));
+    }
+    if (!ok && lane == 0) fail();
+  } else if (warp >= 2 && warp < 6) {
+    // ------------------------------------------------------------ softmax
+    const int quad = warp & 3, half = quad >> 1;           // TMEM lanes 32 quad ..
+    const int r = 32 * (quad & 1) + lane;                  // the thread's row of the CTA
+    const uint32_t bar = kBarPair + (quad & 1);            // the two warps of these rows
+    const uint32_t lanes = (uint32_t)(32 * quad) << 16;
+    while (w.next()) {
+      // one piece; `w` is at its first tile
+      const int gr = w.u.x + (int)rank * kHalf + r;        // global row
+      const bool mine = gr < w.u.y;
+      bool live = false;
+      if (mine) {
+        const int b = gr / p.R;
+        live = gr - b * p.R < queries(p, b) * p.H;
+      }
+      float qs = p.scale_log2;
+      if (kFp8) {
+        const float f = mine ? p.inv_scale[gr] : 1.0f;
+        if (live && f != f) atomicOr(p.err, kErrQRange);
+        qs *= f;
+      }
+      float m_run = -CUDART_INF_F, l_run = 0.0f;           // l_run: this thread's tokens
+      while (true) {
+        const int s = w.g % kStages, sb = w.g & 1;
+        ok = ok && wait(&misc->s_full[sb], (w.g >> 1) & 1);
+        if (kFp8) ok = ok && wait(&misc->sc_ready[s], (w.g / kStages) & 1);
+        float a[64];
+        float mx = -CUDART_INF_F;
+        // the last tile of an odd number of pages has no second page
+        const bool there = 2 * w.j + half < w.u.w;
+        if (ok) {
+          tc_fence_after();
+          uint32_t v0[32], v1[32];
+          tmem_ld32(tmem + lanes + kColS + 64 * sb, v0);
+          tmem_ld32(tmem + lanes + kColS + 64 * sb + 32, v1);
+          tmem_wait_ld();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(at_leader(&misc->s_empty[sb]));
+          float m4[4] = {mx, mx, mx, mx};
+#pragma unroll
+          for (int i4 = 0; i4 < 16; ++i4) {
+            float sg[4], eg[4];
+            if (kFp8) {
+              const float4 x = *reinterpret_cast<const float4*>(&misc->sigma[s][64 * half + 4 * i4]);
+              const float4 y = *reinterpret_cast<const float4*>(&misc->lge[s][64 * half + 4 * i4]);
+              sg[0] = x.x, sg[1] = x.y, sg[2] = x.z, sg[3] = x.w;
+              eg[0] = y.x, eg[1] = y.y, eg[2] = y.z, eg[3] = y.w;
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int i = 4 * i4 + e;
+              const float x = __uint_as_float(i < 32 ? v0[i & 31] : v1[i & 31]);
+              a[i] = kFp8 ? x * sg[e] * qs : x;
+              m4[e] = fmaxf(m4[e], kFp8 ? a[i] + eg[e] : a[i]);
+            }
+          }
+          mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+          if (!kFp8) mx *= p.scale_log2;
+          if (!there) mx = -CUDART_INF_F;
+          misc->xmax[sb][half][r] = mx;
+        }
+        if (named_bar_or(bar, 64, !ok)) {
+          ok = false;
+          break;
+        }
+        const float m_new = fmaxf(m_run, fmaxf(mx, misc->xmax[sb][half ^ 1][r]));
+        float alpha = 1.0f;
+        bool rescale = false;
+        if (m_new > m_run + kRescale || (w.first && m_new > -CUDART_INF_F)) {
+          alpha = m_run == -CUDART_INF_F ? 0.0f : ex2_approx(m_run - m_new);
+          l_run *= alpha;
+          m_run = m_new;
+          rescale = live && !w.first;
+        }
+        const float m_use = m_run == -CUDART_INF_F ? 0.0f : m_run;
+        // P V of the tile before: O is rescaled behind it, and it has read the
+        // probabilities that are written over
+        const int gp = w.g - 1, ga = kFp8 ? w.g - 2 : w.g - 1;
+        auto pv_of = [&](int g) {
+          return wait(&misc->pv_done[g % kStages], (g / kStages) & 1);
+        };
+        if (__any_sync(0xffffffffu, rescale)) {
+          ok = pv_of(gp);
+          tc_fence_after();
+          if (ok) {
+#pragma unroll 1
+            for (int c = 0; c < 256; c += 32) {
+              uint32_t v[32];
+              tmem_ld32(tmem + lanes + kColO + c, v);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * alpha);
+              tmem_st32(tmem + lanes + kColO + c, v);
+            }
+            tmem_wait_st();
+          }
+        }
+        float ls[4] = {0.f, 0.f, 0.f, 0.f};
+        if (kFp8) {
+          uint32_t hi4[16], lo4[16];
+#pragma unroll
+          for (int i4 = 0; i4 < 16; ++i4) {
+            const float4 x = *reinterpret_cast<const float4*>(&misc->sigma[s][64 * half + 4 * i4]);
+            const float sg[4] = {x.x, x.y, x.z, x.w};
+            float pv[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float u = there ? ex2_approx(a[4 * i4 + e] - m_use) : 0.0f;
+              ls[e] += u;
+              pv[e] = there ? u * sg[e] : 0.0f;
+            }
+            const uint32_t s01 = split_e4m3x2(pv[0], pv[1]), s23 = split_e4m3x2(pv[2], pv[3]);
+            hi4[i4] = (s01 & 0xFFFFu) | (s23 << 16);
+            lo4[i4] = (s01 >> 16) | (s23 & 0xFFFF0000u);
+          }
+          if (ok && ga >= 0) ok = pv_of(ga);
+          if (ok) {
+            // 64-byte rows, 16-byte units under a 64-byte swizzle
+            uint8_t* row = smem + C::kSmemP + (w.g & 1) * 4 * C::kSlot + half * C::kSlot + r * 64;
+            const int sw = (r >> 1) & 3;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              *reinterpret_cast<uint4*>(row + ((c ^ sw) << 4)) =
+                  make_uint4(hi4[4 * c], hi4[4 * c + 1], hi4[4 * c + 2], hi4[4 * c + 3]);
+              *reinterpret_cast<uint4*>(row + 2 * C::kSlot + ((c ^ sw) << 4)) =
+                  make_uint4(lo4[4 * c], lo4[4 * c + 1], lo4[4 * c + 2], lo4[4 * c + 3]);
+            }
+          }
+        } else {
+          uint32_t pk[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            // bf16: P is rounded to 8 bits, relative 2^-9, as in the
+            // per-request kernel; its sum is taken before the rounding
+            const float x = there ? ex2_approx(fmaf(a[2 * i], p.scale_log2, -m_use)) : 0.0f;
+            const float y = there ? ex2_approx(fmaf(a[2 * i + 1], p.scale_log2, -m_use)) : 0.0f;
+            pk[i] = pack_bf16(x, y);
+            ls[i & 3] += x + y;
+          }
+          // tokens 0-63 go into the stage's rope chunk, which S has read;
+          // tokens 64-127 into the one chunk that every tile uses
+          if (ok && half == 1 && ga >= 0) ok = pv_of(ga);
+          if (ok) {
+            uint8_t* row = smem + (half == 0 ? C::kSmemKV + s * C::kTile + 8 * C::kSlot : C::kSmemP) +
+                           r * 128;
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+              *reinterpret_cast<uint4*>(row + ((c ^ (r & 7)) << 4)) =
+                  make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
+          }
+        }
+        l_run += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        // a failed wait is seen by both warps at the next reduction
+        if (ok && lane == 0) mbar_arrive_cluster(at_leader(&misc->p_full[sb]));
+        if (w.j + 1 >= w.t1) break;
+        w.next();
+      }
+      // ---------------------------------------------------------- epilogue
+      ok = ok && wait(&misc->pv_done[w.g % kStages], (w.g / kStages) & 1);
+      // (the other buffer of xmax: this tile's may still be read)
+      misc->xmax[(w.g & 1) ^ 1][half][r] = l_run;
+      if (named_bar_or(bar, 64, !ok)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const float l = l_run + misc->xmax[(w.g & 1) ^ 1][half ^ 1][r];
+      const size_t at = w.whole ? (size_t)gr
+                                : ((size_t)2 * pair + w.slot) * kPairRows + rank * kHalf + r;
+      float* const orow = (w.whole ? p.out : p.ws_o) + at * kDv + 256 * half;
+      // pieces of split units: the join writes rows without a query
+      const bool store = w.whole ? mine : live;
+      const float inv = (live && l != 0.0f) ? 1.0f / l : 0.0f;            // or NaN
+      if (store && half == 0)
+        (w.whole ? p.lse : p.ws_lse)[at] =
+            live && l != 0.0f ? (m_run + __log2f(l)) * 0.69314718055994530942f : -CUDART_INF_F;
+      auto put = [&](int c, const uint32_t (&v)[32]) {
+        if (!store) return;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (live)
+            x = make_float4(__uint_as_float(v[4 * i]) * inv, __uint_as_float(v[4 * i + 1]) * inv,
+                            __uint_as_float(v[4 * i + 2]) * inv, __uint_as_float(v[4 * i + 3]) * inv);
+          reinterpret_cast<float4*>(orow + c)[i] = x;
+        }
+      };
+      {
+        uint32_t va[32], vb[32];
+        tmem_ld32(tmem + lanes + kColO, va);
+#pragma unroll
+        for (int c = 0; c < 256; c += 64) {
+          tmem_wait_ld();
+          tmem_ld32(tmem + lanes + kColO + c + 32, vb);
+          put(c, va);
+          tmem_wait_ld();
+          if (c + 64 < 256) tmem_ld32(tmem + lanes + kColO + c + 64, va);
+          put(c + 32, vb);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(at_leader(&misc->o_free));
+      // xmax is written again by the next piece's first tile
+      named_bar_sync(bar, 64);
+    }
+    if (!ok && lane == 0) fail();
+  }
+
+  // ---------------------------------------------------------------- teardown
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();            // nothing is issued any more, by either CTA
+  const bool failed = *abort_flag != 0 || ld_cluster(peer_abort) != 0;
+  if (failed) {
+    // after a failure, the MMAs and copies in flight land before tensor and
+    // shared memory are given back
+    int never = 0;
+    if (leader && (warp == 1 || warp == 6) && lane == 0) {
+      asm volatile(
+          "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+              smem_u32(&misc->drain))
+          : "memory");
+      mbar_wait_cluster(smem_u32(&misc->drain), 0, kDrainNs, &never);
+    }
+    if (leader && warp == 0 && lane == 0) {
+      // a load that one CTA announced and the other never did: the missing
+      // arrival is made up, then the phase ends with the announced bytes
+      bool good = true;
+      auto settle = [&](uint64_t* bar, uint32_t mine_n, uint32_t theirs) {
+        if (mine_n != theirs) mbar_arrive(smem_u32(bar));
+        const uint32_t n = max(mine_n, theirs);
+        if (n > 0 && good) good = mbar_wait_cluster(smem_u32(bar), (n - 1) & 1, kDrainNs, &never);
+      };
+      for (int s = 0; s < kStages; ++s)
+        for (int k = 0; k < 4; ++k)
+          settle(&misc->full[s][k], misc->armed[s][k],
+                 ld_cluster(map_rank(smem_u32(&misc->armed[s][k]), 1)));
+      settle(&misc->q_full, misc->armed_q, ld_cluster(map_rank(smem_u32(&misc->armed_q), 1)));
+    }
+    if (kFp8 && warp == 0 && lane == 0) {
+      // the scales of a stage are announced behind its chunk C
+      for (int s = 0; s < kStages; ++s) {
+        const uint32_t n = misc->armed[s][kC];
+        if (n > 0) mbar_wait(smem_u32(&misc->sc_full[s]), (n - 1) & 1, kDrainNs, &never);
+      }
+    }
+    tc_fence_before();
+    __syncthreads();
+  }
+  cluster_sync_all();            // the peer reads this CTA no more
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, kTmemCols);
+  }
+}
+
+// ------------------------------------------------------------ joining pieces
+struct UnitPieces {
+  const float* ws_o;
+  const float* ws_lse;
+  struct Ctx {
+    int c0, count, r, first_in_slot1;
+  };
+  __device__ void piece(const Ctx& c, int k, const float*& src, float& lse) const {
+    const size_t cc = (size_t)(c.c0 + k);
+    const size_t slot = (k == 0 && c.first_in_slot1) ? 2 * cc + 1 : 2 * cc;
+    src = ws_o + (slot * kPairRows + c.r) * kDv;
+    lse = ws_lse[slot * kPairRows + c.r];
+  }
+};
+
+constexpr int kJoinRows = 2, kJoinBatch = 12;
+constexpr int kJoinSmem = 8 * kJoinBatch * 32 * (int)sizeof(float4);
+
+// Rows of units that no pair computed whole: without a shared page 0 and -inf,
+// else the LSE join of their pieces.  Four warps per row, 128 dims each.
+__global__ void __launch_bounds__(256, 4) prefix_join_kernel(Params p) {
+  extern __shared__ __align__(16) float4 join_stage[];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int u = blockIdx.x;
+  if (u == 0 && blockIdx.y == 0 && threadIdx.x == 0 && p.work->err != 0) atomicOr(p.err, p.work->err);
+  const int4 x = p.units[u];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int r = blockIdx.y * kJoinRows + (warp >> 2), part = warp & 3;
+  const int gr = x.x + r;
+  if (gr >= x.y) return;
+  const int ps = p.positions[u], ue = p.positions[u + 1];
+  const int us = unit_tile_start(p.positions, u, p.work->unit_cost);
+  const int per = p.work->per_cta;
+  const int b = gr / p.R;
+  const bool live = gr - b * p.R < queries(p, b) * p.H;
+  const bool split = us < ue && us / per != (ue - 1) / per;
+  if (us < ue && !split) return;               // written by the pair that computed it
+  float4* dst = reinterpret_cast<float4*>(p.out + (size_t)gr * kDv) + 32 * part;
+  if (us == ue || !live) {
+    dst[lane] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (part == 0 && lane == 0) p.lse[gr] = -CUDART_INF_F;
+    return;
+  }
+  const int c0 = us / per, c1 = (ue - 1) / per;
+  const UnitPieces src{p.ws_o, p.ws_lse};
+  const UnitPieces::Ctx ctx{c0, c1 - c0 + 1, r, c0 * per < ps ? 1 : 0};
+  float4 acc[1];
+  float M, wsum;
+  merge_pieces_staged<1, kJoinBatch>(src, ctx, lane, 32 * part, join_stage + warp * (kJoinBatch * 32),
+                                     acc, M, wsum);
+  const float inv = wsum != 0.f ? 1.0f / wsum : 0.f;   // or NaN
+  dst[lane] = make_float4(acc[0].x * inv, acc[0].y * inv, acc[0].z * inv, acc[0].w * inv);
+  if (part == 0 && lane == 0) p.lse[gr] = wsum != 0.f ? M + __logf(wsum) : -CUDART_INF_F;
+}
+
+// ------------------------------------------------------------------ launches
+bool encode(CUtensorMap* m, bool fp8, int rank, const void* base, const cuuint64_t* dims,
+            const cuuint64_t* strides, const cuuint32_t* box) {
+  const cuuint32_t es[4] = {1, 1, 1, 1};
+  return host::encode_fn()(m, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                           rank, const_cast<void*>(base), dims, strides, box, es,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE,
+                           fp8 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                           fp8 ? CU_TENSOR_MAP_L2_PROMOTION_NONE : CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool kFp8>
+cudaError_t attend(const Params& p, const void* kv, int pairs, cudaStream_t stream) {
+  if (host::encode_fn() == nullptr) return cudaErrorInitializationError;
+  const cuuint64_t e = kFp8 ? 1 : 2;
+  CUtensorMap tm_q, tm_kv4, tm_kv1;
+  bool ok;
+  if (kFp8) {
+    // (64 dims, row, chunk, term) of the terms [rows, 2, 576]
+    const cuuint64_t d[4] = {64, (cuuint64_t)p.B * p.R, (cuuint64_t)kChunks, 2};
+    const cuuint64_t s[3] = {2 * kDqk, 64, kDqk};
+    const cuuint32_t b[4] = {64, (cuuint32_t)kHalf, (cuuint32_t)kChunks, 1};
+    ok = encode(&tm_q, true, 4, p.terms, d, s, b);
+  } else {
+    const cuuint64_t d[3] = {64, (cuuint64_t)p.B * p.R, (cuuint64_t)kChunks};
+    const cuuint64_t s[2] = {2 * kDqk, 128};
+    const cuuint32_t b[3] = {64, (cuuint32_t)kHalf, (cuuint32_t)kChunks};
+    ok = encode(&tm_q, false, 3, p.q, d, s, b);
+  }
+  // (64 dims, cache row, chunk): a page's chunks as [chunk][row][64 dims]
+  const cuuint64_t d[3] = {64, (cuuint64_t)p.num_pages * kPage, (cuuint64_t)kChunks};
+  const cuuint64_t s[2] = {kDqk * e, 64 * e};
+  const cuuint32_t b4[3] = {64, (cuuint32_t)kPage, 4}, b1[3] = {64, (cuuint32_t)kPage, 1};
+  ok = ok && encode(&tm_kv4, kFp8, 3, kv, d, s, b4) && encode(&tm_kv1, kFp8, 3, kv, d, s, b1);
+  if (!ok) return cudaErrorInvalidValue;
+  const cudaError_t err = host::ensure_dynamic_smem(
+      reinterpret_cast<const void*>(&prefix_kernel<kFp8>), smem_bytes<kFp8>());
+  if (err != cudaSuccess) return err;
+  cudaLaunchAttribute attr[2];
+  attr[0] = pdl_attribute();
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * pairs);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem_bytes<kFp8>();
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, prefix_kernel<kFp8>, tm_q, tm_kv4, tm_kv1, p);
+}
+
+}  // namespace
+
+int max_pairs() {
+  // CTA pairs that the device runs at once (its GPCs may leave SMs without a
+  // partner): one wave of them, asked once per context
+  static host::PerContext<int> known;
+  int n = 0;
+  const void* kernel = reinterpret_cast<const void*>(&prefix_kernel<false>);
+  if (!known.get(kernel, n, [&](int& v) {
+        if (host::ensure_dynamic_smem(kernel, smem_bytes<false>()) != cudaSuccess) return false;
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = 2;
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(2);
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = smem_bytes<false>();
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        return cudaOccupancyMaxActiveClusters(&v, kernel, &cfg) == cudaSuccess && v > 0;
+      }))
+    return 0;
+  return std::min(n, 256);
+}
+
+cudaError_t launch_prep(const Params& p, bool fp8, int pairs, cudaStream_t stream) {
+  cudaLaunchAttribute attr = pdl_attribute();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(1 + p.B + (fp8 ? ceil_div(p.B * p.R, kPrepThreads / 32) : 0));
+  cfg.blockDim = dim3(kPrepThreads);
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, prefix_prep_kernel, p, pairs);
+}
+
+cudaError_t launch_attend(const Params& p, const void* kv, bool fp8, int pairs, cudaStream_t stream) {
+  return fp8 ? attend<true>(p, kv, pairs, stream) : attend<false>(p, kv, pairs, stream);
+}
+
+cudaError_t launch_join(const Params& p, cudaStream_t stream) {
+  const cudaError_t e =
+      host::ensure_dynamic_smem(reinterpret_cast<const void*>(&prefix_join_kernel), kJoinSmem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr = pdl_attribute();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.max_units, kPairRows / kJoinRows);
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = kJoinSmem;
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, prefix_join_kernel, p);
+}
+
+}  // namespace prefix
+}  // namespace mla

@@ -1,0 +1,45 @@
+// What the C entry of the shared-prefix attention hands its kernels.
+#pragma once
+
+#include "common.cuh"
+
+namespace mla {
+namespace prefix {
+
+constexpr int kPairRows = 128;   // query rows of a CTA pair (64 per CTA)
+
+struct Params {
+  int B, q_len, H, R;            // R = q_len * H rows per request
+  int causal, num_pages, max_pages, groups;
+  int max_units;
+  float scale_log2;
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  const int32_t* q_lens;         // or null
+  const int32_t* group_starts;   // [groups + 1]
+  const int32_t* prefix_lens;    // [groups]
+  const uint16_t* q;             // [B * R, 576]
+  const float* kv_scale;         // e4m3: [num_pages * 64]
+  uint8_t* terms;                // e4m3: the query's two terms [B * R, 2, 576]
+  float* inv_scale;              // e4m3: [B * R]
+  int32_t* own_lens;             // [B] tokens behind the shared pages
+  int32_t* own_table;            // [B, max_pages] their pages
+  int32_t* group_pages;          // [groups] their shared pages
+  int4* units;                   // [max_units] first row, end row, table row, shared pages
+  int* positions;                // [max_units + 1] work positions before each unit
+  WsHeader* work;                // the work list's header
+  unsigned* err;                 // the call's error word
+  float* ws_o;                   // [pairs * 2, 128, 512] pieces of split units
+  float* ws_lse;                 // [pairs * 2, 128]
+  float* out;                    // [B * R, 512]: slice 0 of the outputs
+  float* lse;                    // [B * R]
+  unsigned long long timeout_ns;
+};
+
+int max_pairs();                 // CTA pairs that can run at once; 0 on an error
+cudaError_t launch_prep(const Params& p, bool fp8, int pairs, cudaStream_t stream);
+cudaError_t launch_attend(const Params& p, const void* kv, bool fp8, int pairs, cudaStream_t stream);
+cudaError_t launch_join(const Params& p, cudaStream_t stream);
+
+}  // namespace prefix
+}  // namespace mla
