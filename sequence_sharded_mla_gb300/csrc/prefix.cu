@@ -26,13 +26,13 @@
 // done, loads its dims of page 2j + 1 over B; CTA 1 keeps B and loads over A.
 // So a tile costs a CTA 13 chunks of loads and 9 of space.
 //
-//   warp 0      producer: K of the tiles ahead, V of the current one
-//   warp 1      S issue (leader only)
-//   warps 2..5  softmax: a thread has one row and 64 tokens; the two threads of
+//   warp 0      K producer: the query, and the tiles ahead
+//   warps 1, 2  S issue, P V issue (leader only)
+//   warp 3      V producer; e4m3: the tile's token scales, split into mantissa
+//               and exponent
+//   warps 4..11 softmax: a thread has one row and 32 tokens; the four threads of
 //               a row exchange their maxima; O is rescaled only when a running
 //               maximum grows by more than 2^8; the epilogue
-//   warp 6      P V issue (leader only)
-//   warp 7      e4m3: the tile's token scales, split into mantissa and exponent
 //
 // e4m3 caches: the MMAs take the codes as they are, the query and the
 // probabilities as two-term e4m3 sums, as in the per-request kernel; three
@@ -60,14 +60,15 @@ namespace prefix {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kSoftmaxWarps = 8;             // warps 4 .. 11
+constexpr int kThreads = 128 + 32 * kSoftmaxWarps;
 constexpr int kHalf = 64;                    // rows, and tokens of a tile, per CTA
 constexpr int kPrepThreads = 1024;
 // Work positions charged to a unit for its fixed costs (query load, pipeline
 // refill, the epilogue's 256 KB of output).
 constexpr int kUnitCost = 3;
 constexpr int kMinTiles = 2;
-constexpr uint32_t kBarPair = 2;             // named barriers 2, 3: the warps of the same rows
+constexpr uint32_t kBarRows = 2;             // named barriers 2, 3: the warps of the same rows
 constexpr float kRescale = 8.0f;             // log2 units
 constexpr uint32_t kTmemCols = 512, kColS = 0, kColO = 128;
 constexpr int kQBytes = kTileBytes;          // 73728, either type
@@ -218,6 +219,7 @@ struct Misc {
   uint64_t a_free[kStages];      // P V has read A
   uint64_t pv_done[kStages];     // P V has read everything
   uint64_t s_full[2];
+  uint64_t k_read[kStages];      // S is done: V goes over half of K
   uint64_t s_empty[2], p_full[2], o_free;   // leader: the softmax warps of both
   uint64_t q_full, q_empty;
   uint64_t drain;
@@ -226,7 +228,7 @@ struct Misc {
   int abort;
   uint32_t armed[kStages][4];    // loads announced on full, for a teardown
   uint32_t armed_q;
-  float xmax[2][2][kHalf];       // by tile parity and half of the tokens
+  float xmax[2][4][kHalf];       // by tile parity and quarter of the tokens
   // token scales (copied in 16-byte units, read as float4) and their exponents
   alignas(16) float sigma[kFp8 ? kStages : 1][kFp8 ? 128 : 4];
   alignas(16) float lge[kFp8 ? kStages : 1][kFp8 ? 128 : 4];
@@ -238,7 +240,7 @@ static_assert(Cfg<true>::kSmemMisc % 1024 == 0 && Cfg<false>::kSmemMisc % 1024 =
 
 template <bool kFp8>
 constexpr int smem_bytes() {
-  return Cfg<kFp8>::kSmemMisc + (int)sizeof(Misc<kFp8>) + 1024;
+  return Cfg<kFp8>::kSmemMisc + (int)sizeof(Misc<kFp8>);
 }
 static_assert(smem_bytes<false>() <= 232448 && smem_bytes<true>() <= 232448, "shared memory");
 
@@ -269,6 +271,33 @@ struct Walk {
   }
 };
 
+// The pages of a walk's tiles: lane l holds entries base + l and base + 32 + l of
+// the table row, the second half on its way while the first is used.
+struct Pages {
+  const int32_t* row;
+  int base, count, cur, ahead;
+  __device__ int entry(int i) const { return i < count ? __ldg(row + i) : -1; }
+  __device__ void move_to(const Params& p, const Walk& w, int lane) {
+    if (w.first) {
+      row = p.block_table + (size_t)w.u.z * p.max_pages;
+      count = w.u.w;
+      base = (2 * w.j) & ~31;
+      cur = entry(base + lane);
+      ahead = entry(base + 32 + lane);
+    } else if (2 * w.j >= base + 32) {
+      base += 32;
+      cur = ahead;
+      ahead = entry(base + 32 + lane);
+    }
+  }
+  // Entry i of the tile; one behind the prefix or out of range gives num_pages,
+  // which lies behind the pool, where loads give zeros.
+  __device__ int at(const Params& p, int i) const {
+    const int v = __shfl_sync(0xffffffffu, cur, i & 31);
+    return i < count && v >= 0 && v < p.num_pages ? v : p.num_pages;
+  }
+};
+
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<uint32_t*>(&h);
@@ -281,8 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                   const __grid_constant__ CUtensorMap tm_kv1, Params p) {
   using C = Cfg<kFp8>;
   constexpr int kStages = C::kStages;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  extern __shared__ __align__(1024) uint8_t smem[];   // whole swizzle atoms
   Misc<kFp8>* misc = reinterpret_cast<Misc<kFp8>*>(smem + C::kSmemMisc);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
@@ -296,6 +324,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (lo >= W) return;           // both CTAs of the pair
   const int hi = (int)min((long long)W, (long long)lo + per);
 
+  if ((smem_u32(smem) & 1023u) != 0) {   // never: its alignment is declared
+    if (threadIdx.x == 0) atomicOr(p.err, kErrTimeout);
+    return;
+  }
+
   volatile int* abort_flag = &misc->abort;
   const uint64_t tmo = p.timeout_ns;
   const uint32_t peer_abort = map_rank(smem_u32(&misc->abort), rank ^ 1);
@@ -305,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     st_cluster(peer_abort, 1);
   };
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, mbar_wait_cluster(smem_u32(bar), parity, tmo, abort_flag));
+    return __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), parity, tmo, abort_flag));
   };
   auto at_leader = [&](uint64_t* bar) { return map_rank(smem_u32(bar), 0); };
 
@@ -316,6 +349,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         misc->armed[s][k] = 0;
       }
       mbar_init(smem_u32(&misc->a_free[s]), 1);
+      mbar_init(smem_u32(&misc->k_read[s]), 1);
       mbar_init(smem_u32(&misc->pv_done[s]), 1);
       if (kFp8) {
         mbar_init(smem_u32(&misc->sc_full[s]), 1);
@@ -324,10 +358,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&misc->s_full[i]), 1);
-      mbar_init(smem_u32(&misc->s_empty[i]), 8);
-      mbar_init(smem_u32(&misc->p_full[i]), 8);
+      mbar_init(smem_u32(&misc->s_empty[i]), 2 * kSoftmaxWarps);
+      mbar_init(smem_u32(&misc->p_full[i]), 2 * kSoftmaxWarps);
     }
-    mbar_init(smem_u32(&misc->o_free), 8);
+    mbar_init(smem_u32(&misc->o_free), 2 * kSoftmaxWarps);
     mbar_init(smem_u32(&misc->q_full), 2);
     mbar_init(smem_u32(&misc->q_empty), 1);
     mbar_init(smem_u32(&misc->drain), 2);
@@ -349,61 +383,40 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t sQ = smem_u32(smem), sKV = smem_u32(smem + C::kSmemKV);
   const uint32_t sP = smem_u32(smem + C::kSmemP);
 
+  // Announces `bytes` of a part of a stage on the leader's barrier.
+  auto arm = [&](int s, int part, uint32_t bytes) {
+    misc->armed[s][part]++;
+    mbar_arrive_expect_tx_pair(at_leader(&misc->full[s][part]), bytes);
+  };
+  // descriptors of the buffers' starts; an offset adds its sixteenth
+  auto desc = [&](uint32_t at, uint32_t lbo) {
+    return kFp8 ? sw64_desc(at, lbo, C::kGroup) : sw128_desc(at, lbo, C::kGroup);
+  };
+
   Walk w;
   w.init(p, lo, hi);
   bool ok = true;
 
   if (warp == 0) {
-    // ------------------------------------------------------------ producer
-    // Announces `bytes` of a part of a stage on the leader's barrier.
-    auto arm = [&](int s, int part, uint32_t bytes) {
-      misc->armed[s][part]++;
-      mbar_arrive_expect_tx_cluster(at_leader(&misc->full[s][part]), bytes);
-    };
-    // Page `i` of the walk's prefix; one behind it or out of range lies behind
-    // the pool, where loads give zeros.
-    auto page_of = [&](const Walk& x, int i) {
-      int page = p.num_pages;
-      if (i < x.u.w) {
-        page = __ldg(p.block_table + (size_t)x.u.z * p.max_pages + i);
-        if (page < 0 || page >= p.num_pages) {
-          if (lane == 0) atomicOr(p.err, kErrBadPage);
-          page = p.num_pages;
-        }
-      }
-      return page;
-    };
-    int pieces = 0;              // pieces whose query was loaded
-    auto load_k = [&](const Walk& x) {
-      const int s = x.g % kStages, use = x.g / kStages;
+    // ---------------------------------------------------------- K producer
+    Pages pages;
+    int pieces = 0;
+    while (ok && w.next()) {
+      const int s = w.g % kStages, use = w.g / kStages;
       const uint32_t st = sKV + s * C::kTile;
-      const int row = page_of(x, 2 * x.j + (int)rank) * kPage;
-      if (x.first) {
-        if (pieces > 0) ok = wait(&misc->q_empty, (pieces - 1) & 1);
-        if (!ok) return;
-        if (lane == 0) {
-          misc->armed_q++;
-          mbar_arrive_expect_tx_cluster(at_leader(&misc->q_full), kQBytes);
-          const int r0 = x.u.x + (int)rank * kHalf;
-          if (kFp8) {
-            tma_load_4d_pair(sQ, &tm_q, at_leader(&misc->q_full), 0, r0, 0, 0);
-            tma_load_4d_pair(sQ + kQBytes / 2, &tm_q, at_leader(&misc->q_full), 0, r0, 0, 1);
-          } else {
-            tma_load_3d_pair(sQ, &tm_q, at_leader(&misc->q_full), 0, r0, 0);
-          }
-        }
-        __syncwarp();
-        ++pieces;
-      }
+      pages.move_to(p, w, lane);
+      const int i = 2 * w.j + (int)rank;
+      const int page = pages.at(p, i), row = page * kPage;
+      if (lane == 0 && page == p.num_pages && i < w.u.w) atomicOr(p.err, kErrBadPage);
       if (use > 0) ok = wait(&misc->a_free[s], (use - 1) & 1);
-      if (!ok) return;
+      if (!ok) break;
       if (lane == 0) {
         arm(s, kA, 4 * C::kSlot);
         tma_load_3d_pair(st, &tm_kv4, at_leader(&misc->full[s][kA]), 0, row, 0);
       }
       __syncwarp();
       if (use > 0) ok = wait(&misc->pv_done[s], (use - 1) & 1);
-      if (!ok) return;
+      if (!ok) break;
       if (lane == 0) {
         arm(s, kB, 4 * C::kSlot);
         tma_load_3d_pair(st + 4 * C::kSlot, &tm_kv4, at_leader(&misc->full[s][kB]), 0, row, 4);
@@ -417,8 +430,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float* src[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int page = page_of(x, 2 * x.j + h);
-          src[h] = page < p.num_pages ? p.kv_scale + (size_t)page * kPage : nullptr;
+          const int pg = pages.at(p, 2 * w.j + h);
+          src[h] = pg < p.num_pages ? p.kv_scale + (size_t)pg * kPage : nullptr;
           if (src[h] != nullptr) bytes += kPage * 4;
           else misc->sigma[s][64 * h + lane] = misc->sigma[s][64 * h + 32 + lane] = 1.0f;
         }
@@ -433,43 +446,74 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
       }
-    };
-    // The CTA's dims of the other CTA's page, over what S has read.
-    auto load_v = [&](const Walk& x) {
-      const int s = x.g % kStages;
-      const int row = page_of(x, 2 * x.j + (int)(rank ^ 1)) * kPage;
-      ok = wait(&misc->s_full[x.g & 1], (x.g >> 1) & 1);
-      if (!ok) return;
+      if (w.first) {
+        // the piece's query, once S of the piece before is done
+        if (pieces > 0) ok = wait(&misc->q_empty, (pieces - 1) & 1);
+        if (!ok) break;
+        if (lane == 0) {
+          misc->armed_q++;
+          mbar_arrive_expect_tx_pair(at_leader(&misc->q_full), kQBytes);
+          const int r0 = w.u.x + (int)rank * kHalf;
+          if (kFp8) {
+            tma_load_4d_pair(sQ, &tm_q, at_leader(&misc->q_full), 0, r0, 0, 0);
+            tma_load_4d_pair(sQ + kQBytes / 2, &tm_q, at_leader(&misc->q_full), 0, r0, 0, 1);
+          } else {
+            tma_load_3d_pair(sQ, &tm_q, at_leader(&misc->q_full), 0, r0, 0);
+          }
+        }
+        __syncwarp();
+        ++pieces;
+      }
+    }
+    if (!ok && lane == 0) fail();
+  } else if (warp == 3) {
+    // ---------------------------------------------------------- V producer
+    // The CTA's dims of the other CTA's page, over what S has read; e4m3: before
+    // that the tile's token scales.
+    Pages pages;
+    while (ok && w.next()) {
+      const int s = w.g % kStages;
+      pages.move_to(p, w, lane);
+      const int i = 2 * w.j + (int)(rank ^ 1);
+      const int page = pages.at(p, i), row = page * kPage;
+      if (lane == 0 && page == p.num_pages && i < w.u.w) atomicOr(p.err, kErrBadPage);
+      if (kFp8) {
+        // token scales sigma = mant 2^E with mant in [0.5, 1): sigma sanitised
+        // in place, E apart
+        ok = wait(&misc->sc_full[s], (w.g / kStages) & 1);
+        if (!ok) break;
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          const int a = lane + 32 * h;
+          float sg = misc->sigma[s][a];
+          uint32_t eb = (__float_as_uint(sg) >> 23) & 0xFFu;
+          if (eb < 27u) {
+            // zero, subnormal or below 2^-100: as 2^-60
+            sg = copysignf(8.6736174e-19f, sg);
+            eb = (__float_as_uint(sg) >> 23) & 0xFFu;
+          }
+          misc->sigma[s][a] = sg;
+          // inf, NaN or >= 2^126: exponent 0, and the value itself propagates
+          misc->lge[s][a] = eb >= 253u ? 0.0f : (float)((int)eb - 126);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&misc->sc_ready[s]));
+      }
+      ok = wait(&misc->k_read[s], (w.g / kStages) & 1);
+      if (!ok) break;
       if (lane == 0) {
         arm(s, kV, 4 * C::kSlot);
         tma_load_3d_pair(sKV + s * C::kTile + (leader ? 4 : 0) * C::kSlot, &tm_kv4,
                          at_leader(&misc->full[s][kV]), 0, row, leader ? 0 : 4);
       }
       __syncwarp();
-    };
-    // K runs ahead of V: two tiles first, then after V of tile g the K of tile
-    // g + stages - 1, which waits for P V of tile g - 1 (V of tile g waits for
-    // its S only).  K of tile g + 2 never goes out before V of tile g: S of tile
-    // g + 2 would end a second phase of the barrier that V of tile g waits on.
-    Walk k;
-    k.init(p, lo, hi);
-    bool more = true;
-    for (int i = 0; i < 2 && ok && more; ++i) {
-      more = k.next();
-      if (more) load_k(k);
-    }
-    while (ok && w.next()) {
-      load_v(w);
-      if (ok && more && (kStages > 2 || w.g > 0)) {
-        more = k.next();
-        if (more) load_k(k);
-      }
     }
     if (!ok && lane == 0) fail();
   } else if (warp == 1 && leader) {
     // ------------------------------------------------------------ S issue
     constexpr uint32_t id = kFp8 ? idesc_e4m3_f32(128, 128, false, false)
                                  : idesc_bf16_f32(128, 128, false, false);
+    const uint64_t dq = desc(sQ, 16);
     int pieces = 0;
     Walk n = w;                  // the next tile: is this one its piece's last?
     n.next();
@@ -482,6 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ok && w.g >= 2) ok = wait(&misc->s_empty[sb], ((w.g >> 1) - 1) & 1);
       const bool last = !n.next() || n.first;
       const uint32_t d = tmem + kColS + 64 * sb;
+      const uint64_t dk = desc(sKV + s * C::kTile, 16);
 #pragma unroll
       for (int part = 0; part < 3; ++part) {
         if (ok) ok = wait(&misc->full[s][part], (w.g / kStages) & 1);
@@ -490,20 +535,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
 #pragma unroll
           for (int c = 4 * part; c < (part == kC ? 9 : 4 * part + 4); ++c) {
-            const uint32_t k0 = sKV + s * C::kTile + c * C::kSlot, q0 = sQ + c * C::kSlot;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const uint32_t acc = (c > 0 || k > 0) ? 1u : 0u;
-              if (kFp8)          // k: 32-dim step k / 2, term k % 2 of the query
-                mma_e4m3_pair(d, sw64_desc(q0 + (k & 1) * (kQBytes / 2) + 32 * (k >> 1), 16, C::kGroup),
-                              sw64_desc(k0 + 32 * (k >> 1), 16, C::kGroup), id, acc);
-              else
-                mma_bf16_pair(d, sw128_desc(q0 + 32 * k, 16, C::kGroup),
-                              sw128_desc(k0 + 32 * k, 16, C::kGroup), id, acc);
+              // e4m3: 32-dim step k / 2, term k % 2 of the query
+              const uint32_t oq = c * C::kSlot + (kFp8 ? (k & 1) * (kQBytes / 2) + 32 * (k >> 1) : 32 * k);
+              const uint32_t ok16 = c * C::kSlot + 32 * (kFp8 ? k >> 1 : k);
+              if (kFp8) mma_e4m3_pair(d, dq + (oq >> 4), dk + (ok16 >> 4), id, acc);
+              else mma_bf16_pair(d, dq + (oq >> 4), dk + (ok16 >> 4), id, acc);
             }
           }
           if (part == kC) {
             mma_commit_pair(smem_u32(&misc->s_full[sb]));
+            mma_commit_pair(smem_u32(&misc->k_read[s]));
             if (last) mma_commit_pair(smem_u32(&misc->q_empty));
           }
         }
@@ -511,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     if (!ok && lane == 0) fail();
-  } else if (warp == 6 && leader) {
+  } else if (warp == 2 && leader) {
     // ------------------------------------------------------------ P V issue
     constexpr uint32_t id = kFp8 ? idesc_e4m3_f32(128, 256, false, true)
                                  : idesc_bf16_f32(128, 256, false, true);
@@ -527,25 +571,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       tc_fence_after();
       if (lane == 0) {
-        const uint32_t st = sKV + s * C::kTile;
+        const uint64_t dv = desc(sKV + s * C::kTile, C::kSlot);
+        const uint64_t dp0 = kFp8 ? desc(sP + (w.g & 1) * 4 * C::kSlot, 16)
+                                  : desc(sKV + s * C::kTile + 8 * C::kSlot, 16);
+        const uint64_t dp1 = kFp8 ? dp0 + (C::kSlot >> 4) : desc(sP, 16);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {             // tokens 64 half ..
-          const uint32_t p0 = kFp8 ? sP + (w.g & 1) * 4 * C::kSlot + half * C::kSlot
-                                   : half == 0 ? st + 8 * C::kSlot : sP;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             // bf16: 16 tokens; e4m3: 32 tokens k / 2, term k % 2
-            const uint32_t a = kFp8 ? p0 + (k & 1) * 2 * C::kSlot + 32 * (k >> 1) : p0 + 32 * k;
-            const uint32_t v = st + 4 * half * C::kSlot + 2048 * (kFp8 ? k >> 1 : k);
+            const uint32_t oa = kFp8 ? (k & 1) * 2 * C::kSlot + 32 * (k >> 1) : 32 * k;
+            const uint32_t ov = 4 * half * C::kSlot + 2048 * (kFp8 ? k >> 1 : k);
+            const uint64_t a = (half == 0 ? dp0 : dp1) + (oa >> 4);
 #pragma unroll
             for (int nb = 0; nb < 2; ++nb) {               // 128 dims of each CTA
-              const uint32_t d = tmem + kColO + 128 * nb, b = v + 2 * nb * C::kSlot;
+              const uint32_t d = tmem + kColO + 128 * nb;
+              const uint64_t b = dv + ((ov + 2 * nb * C::kSlot) >> 4);
               const uint32_t acc = (w.first && half == 0 && k == 0) ? 0u : 1u;
-              if (kFp8)
-                mma_e4m3_pair(d, sw64_desc(a, 16, C::kGroup), sw64_desc(b, C::kSlot, C::kGroup), id, acc);
-              else
-                mma_bf16_pair(d, sw128_desc(a, 16, C::kGroup), sw128_desc(b, C::kSlot, C::kGroup), id,
-                              acc);
+              if (kFp8) mma_e4m3_pair(d, a, b, id, acc);
+              else mma_bf16_pair(d, a, b, id, acc);
             }
           }
           mma_commit_pair(smem_u32(half == 0 ? &misc->a_free[s] : &misc->pv_done[s]));
@@ -554,36 +598,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     }
     if (!ok && lane == 0) fail();
-  } else if (warp == 7 && kFp8) {
-    // ------------------------------------------------------- token scales
-    // sigma = mant 2^E with mant in [0.5, 1): sigma sanitised in place, E apart
-    while (ok && w.next()) {
-      const int s = w.g % kStages;
-      ok = wait(&misc->sc_full[s], (w.g / kStages) & 1);
-      if (!ok) break;
-#pragma unroll
-      for (int h = 0; h < 4; ++h) {
-        const int a = lane + 32 * h;
-        float sg = misc->sigma[s][a];
-        uint32_t eb = (__float_as_uint(sg) >> 23) & 0xFFu;
-        if (eb < 27u) {
-          // zero, subnormal or below 2^-100: as 2^-60
-          sg = copysignf(8.6736174e-19f, sg);
-          eb = (__float_as_uint(sg) >> 23) & 0xFFu;
-        }
-        misc->sigma[s][a] = sg;
-        // inf, NaN or >= 2^126: exponent 0, and the value itself propagates
-        misc->lge[s][a] = eb >= 253u ? 0.0f : (float)((int)eb - 126);
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&misc->sc_ready[s]));
-    }
-    if (!ok && lane == 0) fail();
-  } else if (warp >= 2 && warp < 6) {
+  } else if (warp >= 4) {
     // ------------------------------------------------------------ softmax
     const int quad = warp & 3, half = quad >> 1;           // TMEM lanes 32 quad ..
+    const int grp = (warp - 4) >> 2;                       // tokens 64 half + 32 grp ..
     const int r = 32 * (quad & 1) + lane;                  // the thread's row of the CTA
-    const uint32_t bar = kBarPair + (quad & 1);            // the two warps of these rows
+    const int part = 2 * half + grp;
+    const uint32_t bar = kBarRows + (quad & 1);            // the four warps of these rows
     const uint32_t lanes = (uint32_t)(32 * quad) << 16;
     while (w.next()) {
       // one piece; `w` is at its first tile
@@ -605,33 +626,32 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int s = w.g % kStages, sb = w.g & 1;
         ok = ok && wait(&misc->s_full[sb], (w.g >> 1) & 1);
         if (kFp8) ok = ok && wait(&misc->sc_ready[s], (w.g / kStages) & 1);
-        float a[64];
+        float a[32];
         float mx = -CUDART_INF_F;
         // the last tile of an odd number of pages has no second page
         const bool there = 2 * w.j + half < w.u.w;
         if (ok) {
           tc_fence_after();
-          uint32_t v0[32], v1[32];
-          tmem_ld32(tmem + lanes + kColS + 64 * sb, v0);
-          tmem_ld32(tmem + lanes + kColS + 64 * sb + 32, v1);
+          uint32_t v[32];
+          tmem_ld32(tmem + lanes + kColS + 64 * sb + 32 * grp, v);
           tmem_wait_ld();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(at_leader(&misc->s_empty[sb]));
+          if (lane == 0) mbar_arrive_pair(at_leader(&misc->s_empty[sb]));
           float m4[4] = {mx, mx, mx, mx};
 #pragma unroll
-          for (int i4 = 0; i4 < 16; ++i4) {
+          for (int i4 = 0; i4 < 8; ++i4) {
             float sg[4], eg[4];
             if (kFp8) {
-              const float4 x = *reinterpret_cast<const float4*>(&misc->sigma[s][64 * half + 4 * i4]);
-              const float4 y = *reinterpret_cast<const float4*>(&misc->lge[s][64 * half + 4 * i4]);
+              const float4 x = *reinterpret_cast<const float4*>(&misc->sigma[s][32 * part + 4 * i4]);
+              const float4 y = *reinterpret_cast<const float4*>(&misc->lge[s][32 * part + 4 * i4]);
               sg[0] = x.x, sg[1] = x.y, sg[2] = x.z, sg[3] = x.w;
               eg[0] = y.x, eg[1] = y.y, eg[2] = y.z, eg[3] = y.w;
             }
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const int i = 4 * i4 + e;
-              const float x = __uint_as_float(i < 32 ? v0[i & 31] : v1[i & 31]);
+              const float x = __uint_as_float(v[i]);
               a[i] = kFp8 ? x * sg[e] * qs : x;
               m4[e] = fmaxf(m4[e], kFp8 ? a[i] + eg[e] : a[i]);
             }
@@ -639,13 +659,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
           if (!kFp8) mx *= p.scale_log2;
           if (!there) mx = -CUDART_INF_F;
-          misc->xmax[sb][half][r] = mx;
+          misc->xmax[sb][part][r] = mx;
         }
-        if (named_bar_or(bar, 64, !ok)) {
+        if (named_bar_or(bar, 128, !ok)) {
           ok = false;
           break;
         }
-        const float m_new = fmaxf(m_run, fmaxf(mx, misc->xmax[sb][half ^ 1][r]));
+        const float m_new =
+            fmaxf(fmaxf(m_run, fmaxf(mx, misc->xmax[sb][part ^ 1][r])),
+                  fmaxf(misc->xmax[sb][part ^ 2][r], misc->xmax[sb][part ^ 3][r]));
         float alpha = 1.0f;
         bool rescale = false;
         if (m_new > m_run + kRescale || (w.first && m_new > -CUDART_INF_F)) {
@@ -666,7 +688,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
           if (ok) {
 #pragma unroll 1
-            for (int c = 0; c < 256; c += 32) {
+            for (int c = 128 * grp; c < 128 * grp + 128; c += 32) {
               uint32_t v[32];
               tmem_ld32(tmem + lanes + kColO + c, v);
               tmem_wait_ld();
@@ -679,10 +701,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         float ls[4] = {0.f, 0.f, 0.f, 0.f};
         if (kFp8) {
-          uint32_t hi4[16], lo4[16];
+          uint32_t hi4[8], lo4[8];
 #pragma unroll
-          for (int i4 = 0; i4 < 16; ++i4) {
-            const float4 x = *reinterpret_cast<const float4*>(&misc->sigma[s][64 * half + 4 * i4]);
+          for (int i4 = 0; i4 < 8; ++i4) {
+            const float4 x = *reinterpret_cast<const float4*>(&misc->sigma[s][32 * part + 4 * i4]);
             const float sg[4] = {x.x, x.y, x.z, x.w};
             float pv[4];
 #pragma unroll
@@ -701,17 +723,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint8_t* row = smem + C::kSmemP + (w.g & 1) * 4 * C::kSlot + half * C::kSlot + r * 64;
             const int sw = (r >> 1) & 3;
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              *reinterpret_cast<uint4*>(row + ((c ^ sw) << 4)) =
+            for (int c = 0; c < 2; ++c) {
+              const int at = ((2 * grp + c) ^ sw) << 4;
+              *reinterpret_cast<uint4*>(row + at) =
                   make_uint4(hi4[4 * c], hi4[4 * c + 1], hi4[4 * c + 2], hi4[4 * c + 3]);
-              *reinterpret_cast<uint4*>(row + 2 * C::kSlot + ((c ^ sw) << 4)) =
+              *reinterpret_cast<uint4*>(row + 2 * C::kSlot + at) =
                   make_uint4(lo4[4 * c], lo4[4 * c + 1], lo4[4 * c + 2], lo4[4 * c + 3]);
             }
           }
         } else {
-          uint32_t pk[32];
+          uint32_t pk[16];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
+          for (int i = 0; i < 16; ++i) {
             // bf16: P is rounded to 8 bits, relative 2^-9, as in the
             // per-request kernel; its sum is taken before the rounding
             const float x = there ? ex2_approx(fmaf(a[2 * i], p.scale_log2, -m_use)) : 0.0f;
@@ -726,8 +749,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint8_t* row = smem + (half == 0 ? C::kSmemKV + s * C::kTile + 8 * C::kSlot : C::kSmemP) +
                            r * 128;
 #pragma unroll
-            for (int c = 0; c < 8; ++c)
-              *reinterpret_cast<uint4*>(row + ((c ^ (r & 7)) << 4)) =
+            for (int c = 0; c < 4; ++c)
+              *reinterpret_cast<uint4*>(row + (((4 * grp + c) ^ (r & 7)) << 4)) =
                   make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
           }
         }
@@ -735,28 +758,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
-        // a failed wait is seen by both warps at the next reduction
-        if (ok && lane == 0) mbar_arrive_cluster(at_leader(&misc->p_full[sb]));
+        // a failed wait is seen by all four warps at the next reduction
+        if (ok && lane == 0) mbar_arrive_pair(at_leader(&misc->p_full[sb]));
         if (w.j + 1 >= w.t1) break;
         w.next();
       }
       // ---------------------------------------------------------- epilogue
       ok = ok && wait(&misc->pv_done[w.g % kStages], (w.g / kStages) & 1);
       // (the other buffer of xmax: this tile's may still be read)
-      misc->xmax[(w.g & 1) ^ 1][half][r] = l_run;
-      if (named_bar_or(bar, 64, !ok)) {
+      misc->xmax[(w.g & 1) ^ 1][part][r] = l_run;
+      if (named_bar_or(bar, 128, !ok)) {
         ok = false;
         break;
       }
       tc_fence_after();
-      const float l = l_run + misc->xmax[(w.g & 1) ^ 1][half ^ 1][r];
+      // the four sums in one order for all of the row's threads
+      const float* ls = &misc->xmax[(w.g & 1) ^ 1][0][r];
+      const float l = (ls[0] + ls[kHalf]) + (ls[2 * kHalf] + ls[3 * kHalf]);
       const size_t at = w.whole ? (size_t)gr
                                 : ((size_t)2 * pair + w.slot) * kPairRows + rank * kHalf + r;
-      float* const orow = (w.whole ? p.out : p.ws_o) + at * kDv + 256 * half;
+      float* const orow = (w.whole ? p.out : p.ws_o) + at * kDv + 128 * part;
       // pieces of split units: the join writes rows without a query
       const bool store = w.whole ? mine : live;
       const float inv = (live && l != 0.0f) ? 1.0f / l : 0.0f;            // or NaN
-      if (store && half == 0)
+      if (store && part == 0)
         (w.whole ? p.lse : p.ws_lse)[at] =
             live && l != 0.0f ? (m_run + __log2f(l)) * 0.69314718055994530942f : -CUDART_INF_F;
       auto put = [&](int c, const uint32_t (&v)[32]) {
@@ -772,22 +797,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       {
         uint32_t va[32], vb[32];
-        tmem_ld32(tmem + lanes + kColO, va);
+        const uint32_t o = tmem + lanes + kColO + 128 * grp;
+        tmem_ld32(o, va);
 #pragma unroll
-        for (int c = 0; c < 256; c += 64) {
+        for (int c = 0; c < 128; c += 64) {
           tmem_wait_ld();
-          tmem_ld32(tmem + lanes + kColO + c + 32, vb);
+          tmem_ld32(o + c + 32, vb);
           put(c, va);
           tmem_wait_ld();
-          if (c + 64 < 256) tmem_ld32(tmem + lanes + kColO + c + 64, va);
+          if (c + 64 < 128) tmem_ld32(o + c + 64, va);
           put(c + 32, vb);
         }
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(at_leader(&misc->o_free));
+      if (lane == 0) mbar_arrive_pair(at_leader(&misc->o_free));
       // xmax is written again by the next piece's first tile
-      named_bar_sync(bar, 64);
+      named_bar_sync(bar, 128);
     }
     if (!ok && lane == 0) fail();
   }
@@ -801,12 +827,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     // after a failure, the MMAs and copies in flight land before tensor and
     // shared memory are given back
     int never = 0;
-    if (leader && (warp == 1 || warp == 6) && lane == 0) {
+    if (leader && (warp == 1 || warp == 2) && lane == 0) {
       asm volatile(
           "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
               smem_u32(&misc->drain))
           : "memory");
-      mbar_wait_cluster(smem_u32(&misc->drain), 0, kDrainNs, &never);
+      mbar_wait(smem_u32(&misc->drain), 0, kDrainNs, &never);
     }
     if (leader && warp == 0 && lane == 0) {
       // a load that one CTA announced and the other never did: the missing
@@ -815,7 +841,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto settle = [&](uint64_t* bar, uint32_t mine_n, uint32_t theirs) {
         if (mine_n != theirs) mbar_arrive(smem_u32(bar));
         const uint32_t n = max(mine_n, theirs);
-        if (n > 0 && good) good = mbar_wait_cluster(smem_u32(bar), (n - 1) & 1, kDrainNs, &never);
+        if (n > 0 && good) good = mbar_wait(smem_u32(bar), (n - 1) & 1, kDrainNs, &never);
       };
       for (int s = 0; s < kStages; ++s)
         for (int k = 0; k < 4; ++k)
