@@ -34,11 +34,9 @@ namespace cg = cooperative_groups;
 namespace mla {
 namespace evict {
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kCopyThreads = 256;
-constexpr int kUnroll = 8;            // weights in flight per thread
+constexpr int kHold = 16;             // weights per thread in registers
 
 struct Select {
   const int32_t* seq_lens;
@@ -52,7 +50,6 @@ struct Select {
   int32_t* new_lens;
   int32_t* kept;
   int max_keep;
-  int cluster;                        // CTAs per request
   unsigned* err;
 };
 
@@ -85,45 +82,27 @@ __device__ __forceinline__ uint32_t key_of(float w) {
   return (u >> 31) ? ~u : u | 0x80000000u;
 }
 
-struct alignas(16) Shared {
-  uint32_t hist[kBins];
+template <int kWarps>
+struct Shared {
+  uint32_t hist[kBins];               // this CTA's digits
+  uint32_t total[3][kBins];           // rank 0: the cluster's, by pass
   uint32_t warp_sum[kWarps];
   uint32_t gt[kWarps], eq[kWarps];    // per warp's slice: keys above, equal to T
   uint32_t total_gt, total_eq;        // the CTA's
-  uint32_t bin, above;                // the descent's choice
+  uint32_t bin[3], above[3];          // the descent's choices
 };
 
-// Adds to hist the digit of each of the CTA's candidates [a, b) whose upper
-// bits are `match`.  Lanes with the same digit add once between them: weights
-// crowd into few exponents, and many are zero together.
-__device__ __forceinline__ void count_digits(const float* w, int a, int b, uint32_t* hist,
-                                             uint32_t match, int upper, int shift,
-                                             uint32_t mask) {
-  const int lane = threadIdx.x & 31;
-  for (int i0 = a + (int)(threadIdx.x & ~31u); i0 < b; i0 += kThreads * kUnroll) {
-    float v[kUnroll];
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int i = i0 + u * kThreads + lane;
-      v[u] = i < b ? __ldg(w + i) : 0.0f;
-    }
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int i = i0 + u * kThreads + lane;
-      const uint32_t k = key_of(v[u]);
-      // upper = 32 on the first pass: everything matches
-      const bool in = i < b && (upper >= 32 || (k >> upper) == match);
-      const uint32_t d = in ? (k >> shift) & mask : 0xFFFFFFFFu;
-      const uint32_t same = __match_any_sync(0xFFFFFFFFu, d);
-      if (in && lane == __ffs(same) - 1) atomicAdd(&hist[d], (uint32_t)__popc(same));
-    }
-  }
-}
-
+// C: CTAs per request (a cluster of them).
+template <int C, int kThreads>
 __global__ void __launch_bounds__(kThreads) evict_select_kernel(Select p) {
-  __shared__ Shared sm;
+  constexpr int kWarps = kThreads / 32, kOwn = kBins / kThreads;   // bins per thread
+  __shared__ Shared<kWarps> sm;
   cg::cluster_group cluster = cg::this_cluster();
-  const int C = p.cluster, rank = (int)(blockIdx.x % C), b = (int)(blockIdx.x / C);
+  auto sync = [&]() {
+    if (C == 1) __syncthreads();
+    else cluster.sync();
+  };
+  const int rank = (int)(blockIdx.x % C), b = (int)(blockIdx.x / C);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   griddep_wait();
   griddep_launch_dependents();
@@ -149,10 +128,35 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(Select p) {
 
   const float* w = p.weights + (size_t)b * p.stride + first;
   const int n = L - recent - first;           // candidates, more than k
-  // slices in whole warps of 32; CTA `rank` holds candidates [a, z)
+  // each warp has a slice [wa, wz) of whole groups of 32; its keys stay in
+  // registers if there are at most kHold a thread, else every pass reads them
   const int per_warp = ((n + C * kWarps - 1) / (C * kWarps) + 31) & ~31;
-  const int a = min(n, rank * kWarps * per_warp), z = min(n, a + kWarps * per_warp);
+  const int wa = (int)min((long long)n, (long long)(rank * kWarps + warp) * per_warp);
+  const int wz = min(n, wa + per_warp);
+  const bool held = per_warp <= 32 * kHold;
+  uint32_t key[kHold];
+  auto load = [&](int i0) {
+    float v[kHold];
+#pragma unroll
+    for (int u = 0; u < kHold; ++u) {
+      const int i = i0 + 32 * u + lane;
+      v[u] = i < wz ? __ldg(w + i) : 0.0f;
+    }
+#pragma unroll
+    for (int u = 0; u < kHold; ++u) key[u] = key_of(v[u]);
+  };
+  // f(key, candidate) in every lane for 32 candidates at a time, in order
+  auto each = [&](auto&& f) {
+    for (int i0 = wa; i0 < wz; i0 += 32 * kHold) {
+      if (!held) load(i0);
+#pragma unroll
+      for (int u = 0; u < kHold; ++u)
+        if (i0 + 32 * u < wz) f(key[u], i0 + 32 * u + lane);
+    }
+  };
+  if (held) load(wa);
 
+  for (int i = tid; i < 3 * kBins; i += kThreads) (&sm.total[0][0])[i] = 0;
   uint32_t match = 0, left = (uint32_t)k;     // digits so far; still to take below them
   int upper = 32;
 #pragma unroll 1
@@ -160,65 +164,73 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(Select p) {
     const int bits = pass < 2 ? 11 : 10;
     const int shift = upper - bits;
     const uint32_t mask = (1u << bits) - 1;
-    for (int i = tid; i < kBins; i += kThreads) sm.hist[i] = 0;
+    // one CTA counts straight into the totals
+    uint32_t* hist = C == 1 ? sm.total[pass] : sm.hist;
+    if (C > 1)
+      for (int i = tid; i < kBins; i += kThreads) hist[i] = 0;
+    if (C > 1 && pass == 0) cluster.sync();   // rank 0's totals are zero
+    else __syncthreads();
+    // The lanes that have the first such lane's digit add once between them:
+    // weights crowd into few exponents, and many are zero together.
+    each([&](uint32_t x, int i) {
+      // upper = 32 on the first pass: everything matches
+      const bool in = i < wz && (upper >= 32 || (x >> upper) == match);
+      const uint32_t live = __ballot_sync(0xFFFFFFFFu, in);
+      if (live == 0) return;
+      const uint32_t d = (x >> shift) & mask;
+      const int lead = __ffs(live) - 1;
+      const uint32_t d0 = __shfl_sync(0xFFFFFFFFu, d, lead);
+      const bool same = in && d == d0;
+      const uint32_t m = __popc(__ballot_sync(0xFFFFFFFFu, same));
+      if (in && (!same || lane == lead)) atomicAdd(&hist[d], same ? m : 1u);
+    });
     __syncthreads();
-    count_digits(w, a, z, sm.hist, match, upper, shift, mask);
-    cluster.sync();
-    // thread t sums bins 4t .. 4t + 3 over the cluster
-    uint32_t c[4] = {0, 0, 0, 0};
-    for (int r = 0; r < C; ++r) {
-      const uint4 v = *reinterpret_cast<const uint4*>(
-          C == 1 ? &sm.hist[4 * tid] : cluster.map_shared_rank(&sm.hist[4 * tid], r));
-      c[0] += v.x;
-      c[1] += v.y;
-      c[2] += v.z;
-      c[3] += v.w;
+    if (C > 1) {
+      // the few digits that occur go to rank 0 (every CTA reading all of the
+      // others' bins took 15 us a pass)
+      uint32_t* total = cluster.map_shared_rank(sm.total[pass], 0);
+      for (int i = tid; i < kBins; i += kThreads)
+        if (hist[i] != 0) atomicAdd(total + i, hist[i]);
+      cluster.sync();
     }
-    // keys in bins above this thread's: a suffix sum over the threads
-    const uint32_t own = c[0] + c[1] + c[2] + c[3];
-    uint32_t suf = own;
+    if (rank == 0) {
+      uint32_t c[kOwn], own = 0;
 #pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const uint32_t o = __shfl_down_sync(0xFFFFFFFFu, suf, off);
-      if (lane + off < 32) suf += o;
-    }
-    if (lane == 0) sm.warp_sum[warp] = suf;
-    __syncthreads();
-    uint32_t above = suf - own;
-    for (int v = warp + 1; v < kWarps; ++v) above += sm.warp_sum[v];
+      for (int j = 0; j < kOwn; ++j) own += c[j] = sm.total[pass][kOwn * tid + j];
+      // keys in bins above this thread's: a suffix sum over the threads
+      uint32_t suf = own;
 #pragma unroll
-    for (int j = 3; j >= 0; --j) {
-      if (above < left && left <= above + c[j]) {   // one bin of one thread
-        sm.bin = 4 * tid + j;
-        sm.above = above;
+      for (int off = 1; off < 32; off <<= 1) {
+        const uint32_t o = __shfl_down_sync(0xFFFFFFFFu, suf, off);
+        if (lane + off < 32) suf += o;
       }
-      above += c[j];
+      if (lane == 0) sm.warp_sum[warp] = suf;
+      __syncthreads();
+      uint32_t above = suf - own;
+      for (int v = warp + 1; v < kWarps; ++v) above += sm.warp_sum[v];
+#pragma unroll
+      for (int j = kOwn - 1; j >= 0; --j) {
+        if (above < left && left <= above + c[j])   // one bin of one thread
+          for (int r = 0; r < C; ++r) {
+            *(C == 1 ? &sm.bin[pass] : cluster.map_shared_rank(&sm.bin[pass], r)) = kOwn * tid + j;
+            *(C == 1 ? &sm.above[pass] : cluster.map_shared_rank(&sm.above[pass], r)) = above;
+          }
+        above += c[j];
+      }
     }
-    cluster.sync();              // sm.bin is there, and no peer reads hist any more
-    match = (match << bits) | sm.bin;
-    left -= sm.above;
+    sync();
+    match = (match << bits) | sm.bin[pass];
+    left -= sm.above[pass];
     upper = shift;
   }
   const uint32_t T = match;      // the k-th largest key; `left` of its equals stay
 
   // each warp's slice, in order
-  const int wa = min(z, a + warp * per_warp), wz = min(z, wa + per_warp);
   uint32_t gt = 0, eq = 0;
-  for (int i0 = wa; i0 < wz; i0 += 32 * kUnroll) {
-    float v[kUnroll];
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int i = i0 + 32 * u + lane;
-      v[u] = i < wz ? __ldg(w + i) : 0.0f;
-    }
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const uint32_t key = key_of(v[u]);
-      const bool in = i0 + 32 * u + lane < wz;
-      gt += __popc(__ballot_sync(0xFFFFFFFFu, in && key > T));
-      eq += __popc(__ballot_sync(0xFFFFFFFFu, in && key == T));
-    }
-  }
+  each([&](uint32_t x, int i) {
+    gt += __popc(__ballot_sync(0xFFFFFFFFu, i < wz && x > T));
+    eq += __popc(__ballot_sync(0xFFFFFFFFu, i < wz && x == T));
+  });
   if (lane == 0) {
     sm.gt[warp] = gt;
     sm.eq[warp] = eq;
@@ -233,34 +245,21 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(Select p) {
     sm.total_gt = gt0 + gt;
     sm.total_eq = eq0 + eq;
   }
-  cluster.sync();
+  if (C > 1) cluster.sync();
   for (int r = 0; r < rank; ++r) {
     gt0 += *cluster.map_shared_rank(&sm.total_gt, r);
     eq0 += *cluster.map_shared_rank(&sm.total_eq, r);
   }
   const uint32_t below = (1u << lane) - 1;
-  for (int i0 = wa; i0 < wz; i0 += 32 * kUnroll) {
-    float v[kUnroll];
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int i = i0 + 32 * u + lane;
-      v[u] = i < wz ? __ldg(w + i) : 0.0f;
-    }
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int i = i0 + 32 * u + lane;
-      const uint32_t key = key_of(v[u]);
-      const bool in = i < wz;
-      const uint32_t mg = __ballot_sync(0xFFFFFFFFu, in && key > T);
-      const uint32_t me = __ballot_sync(0xFFFFFFFFu, in && key == T);
-      const uint32_t g = gt0 + __popc(mg & below), e = eq0 + __popc(me & below);
-      if (in && (key > T || (key == T && e < left)))
-        out[first + g + min(e, left)] = first + i;
-      gt0 += __popc(mg);
-      eq0 += __popc(me);
-    }
-  }
-  cluster.sync();                // peers have read this CTA's totals
+  each([&](uint32_t x, int i) {
+    const uint32_t mg = __ballot_sync(0xFFFFFFFFu, i < wz && x > T);
+    const uint32_t me = __ballot_sync(0xFFFFFFFFu, i < wz && x == T);
+    const uint32_t g = gt0 + __popc(mg & below), e = eq0 + __popc(me & below);
+    if (i < wz && (x > T || (x == T && e < left))) out[first + g + min(e, left)] = first + i;
+    gt0 += __popc(mg);
+    eq0 += __popc(me);
+  });
+  if (C > 1) cluster.sync();     // peers have read this CTA's totals
 }
 
 // Block: one new page of one request.  kVec 16-byte pieces per row.
@@ -344,9 +343,36 @@ inline bool overlap(const void* a, size_t n, const void* b, size_t m) {
   return x < y + m && y < x + n;
 }
 
-// A context is cut by a cluster of this many CTAs: one where 16 elements a
-// thread hold the longest, else eight.
-inline int cluster_size(int width) { return width <= 16 * kThreads ? 1 : 8; }
+// A context is cut by a cluster whose CTAs have 8192 weights each at most, or
+// 16384 of up to 262144, or by 16 CTAs.  (One CTA for 32768 weights took
+// MEASURE us, eight 15; eight for a million 66, sixteen 42.)
+template <int C, int kThreads>
+cudaError_t select(const Select& s, int batch, cudaStream_t stream) {
+  const void* kernel = reinterpret_cast<const void*>(&evict_select_kernel<C, kThreads>);
+  if (C > 8) {
+    // beyond the portable cluster size: allowed once per context
+    static host::PerContext<int> done;
+    int ok = 0;
+    if (!done.get(kernel, ok, [&](int& v) {
+          v = 1;
+          return cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) ==
+                 cudaSuccess;
+        }))
+      return cudaErrorInitializationError;
+  }
+  cudaLaunchAttribute attr[2];
+  attr[0] = pdl_attribute();
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = C;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = C > 1 ? 2 : 1;
+  cfg.gridDim = dim3((unsigned)(batch * C));
+  cfg.blockDim = dim3(kThreads);
+  return cudaLaunchKernelEx(&cfg, evict_select_kernel<C, kThreads>, s);
+}
 
 }  // namespace evict
 }  // namespace mla
@@ -390,13 +416,12 @@ extern "C" mla_status mla_cache_evict(const mla_kv_pages* kv, const int32_t* blo
        evict::overlap(weights, sizeof(float) * ((batch - 1) * (size_t)weights_stride + weights_width),
                       weights_out, sizeof(float) * (size_t)batch * max_keep)))
     return MLA_ERR_INVALID;
-  const int C = evict::cluster_size(weights_width);
-  if ((long long)batch * pages >= (1LL << 31) || (long long)batch * C >= (1LL << 31))
+  if ((long long)batch * pages >= (1LL << 31) || (long long)batch * 16 >= (1LL << 31))
     return MLA_ERR_INVALID;
   unsigned* err = &static_cast<WsHeader*>(workspace)->err;
   const evict::Select s{seq_lens,   weights,           weights_stride, weights_width, keep,
                         keep_first, recent,            max_pages_per_req, new_seq_lens, kept,
-                        max_keep,   C,                 err};
+                        max_keep,   err};
   const evict::Copy c{static_cast<uint8_t*>(const_cast<void*>(kv->data)),
                       const_cast<float*>(kv->scale),
                       kv->num_pages,
@@ -414,18 +439,15 @@ extern "C" mla_status mla_cache_evict(const mla_kv_pages* kv, const int32_t* blo
                       max_keep,
                       make_div(pages),
                       err};
-  cudaLaunchAttribute attr[2];
-  attr[0] = pdl_attribute();
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = C;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t se = weights_width <= 8192     ? evict::select<1, 512>(s, batch, st)
+                         : weights_width <= 262144 ? evict::select<8, 1024>(s, batch, st)
+                                                   : evict::select<16, 1024>(s, batch, st);
+  if (se != cudaSuccess) return MLA_ERR_CUDA;
+  cudaLaunchAttribute attr = pdl_attribute();
   cudaLaunchConfig_t cfg = {};
-  cfg.stream = static_cast<cudaStream_t>(stream);
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  cfg.gridDim = dim3((unsigned)(batch * C));
-  cfg.blockDim = dim3(evict::kThreads);
-  if (cudaLaunchKernelEx(&cfg, evict::evict_select_kernel, s) != cudaSuccess) return MLA_ERR_CUDA;
+  cfg.stream = st;
+  cfg.attrs = &attr;
   cfg.numAttrs = 1;
   cfg.gridDim = dim3((unsigned)(batch * pages));
   cfg.blockDim = dim3(evict::kCopyThreads);

@@ -27,7 +27,10 @@
 // So a tile costs a CTA 13 chunks of loads and 9 of space.
 //
 //   warp 0      K producer: the query, and the tiles ahead
-//   warps 1, 2  S issue, P V issue (leader only)
+//   warps 1, 2  S issue (leader only): half of every chunk's products each, into an
+//               accumulator each -- one thread issues an MMA every 44 cycles or
+//               so, and one of M = 128, N = 128 takes 33
+//   warp 12     P V issue (leader only)
 //   warp 3      V producer; e4m3: the tile's token scales, split into mantissa
 //               and exponent
 //   warps 4..11 softmax: a thread has one row and 32 tokens; the four threads of
@@ -61,7 +64,7 @@ namespace prefix {
 namespace {
 
 constexpr int kSoftmaxWarps = 8;             // warps 4 .. 11
-constexpr int kThreads = 128 + 32 * kSoftmaxWarps;
+constexpr int kThreads = 32 * (4 + kSoftmaxWarps + 1);
 constexpr int kHalf = 64;                    // rows, and tokens of a tile, per CTA
 constexpr int kPrepThreads = 1024;
 // Work positions charged to a unit for its fixed costs (query load, pipeline
@@ -70,7 +73,7 @@ constexpr int kUnitCost = 3;
 constexpr int kMinTiles = 2;
 constexpr uint32_t kBarRows = 2;             // named barriers 2, 3: the warps of the same rows
 constexpr float kRescale = 8.0f;             // log2 units
-constexpr uint32_t kTmemCols = 512, kColS = 0, kColO = 128;
+constexpr uint32_t kTmemCols = 512, kColS = 0, kColO = 256;
 constexpr int kQBytes = kTileBytes;          // 73728, either type
 
 // ------------------------------------------------------------------ planning
@@ -218,7 +221,7 @@ struct Misc {
   uint64_t full[kStages][4];     // leader: loads of both CTAs landed
   uint64_t a_free[kStages];      // P V has read A
   uint64_t pv_done[kStages];     // P V has read everything
-  uint64_t s_full[2];
+  uint64_t s_full[2];            // both S issuers
   uint64_t k_read[kStages];      // S is done: V goes over half of K
   uint64_t s_empty[2], p_full[2], o_free;   // leader: the softmax warps of both
   uint64_t q_full, q_empty;
@@ -349,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         misc->armed[s][k] = 0;
       }
       mbar_init(smem_u32(&misc->a_free[s]), 1);
-      mbar_init(smem_u32(&misc->k_read[s]), 1);
+      mbar_init(smem_u32(&misc->k_read[s]), 2);
       mbar_init(smem_u32(&misc->pv_done[s]), 1);
       if (kFp8) {
         mbar_init(smem_u32(&misc->sc_full[s]), 1);
@@ -357,14 +360,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&misc->s_full[i]), 1);
+      mbar_init(smem_u32(&misc->s_full[i]), 2);
       mbar_init(smem_u32(&misc->s_empty[i]), 2 * kSoftmaxWarps);
       mbar_init(smem_u32(&misc->p_full[i]), 2 * kSoftmaxWarps);
     }
     mbar_init(smem_u32(&misc->o_free), 2 * kSoftmaxWarps);
     mbar_init(smem_u32(&misc->q_full), 2);
-    mbar_init(smem_u32(&misc->q_empty), 1);
-    mbar_init(smem_u32(&misc->drain), 2);
+    mbar_init(smem_u32(&misc->q_empty), 2);
+    mbar_init(smem_u32(&misc->drain), 3);
     misc->armed_q = 0;
     misc->abort = 0;
     fence_mbar_init();
@@ -509,11 +512,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     }
     if (!ok && lane == 0) fail();
-  } else if (warp == 1 && leader) {
+  } else if ((warp == 1 || warp == 2) && leader) {
     // ------------------------------------------------------------ S issue
     constexpr uint32_t id = kFp8 ? idesc_e4m3_f32(128, 128, false, false)
                                  : idesc_bf16_f32(128, 128, false, false);
-    const uint64_t dq = desc(sQ, 16);
+    // bf16: issuer i takes the 16-dim steps 2 i, 2 i + 1 of every chunk; e4m3: the
+    // query's term i
+    const int i = warp - 1;
+    const uint64_t dq = desc(sQ + i * (kFp8 ? kQBytes / 2 : 64), 16);
     int pieces = 0;
     Walk n = w;                  // the next tile: is this one its piece's last?
     n.next();
@@ -525,8 +531,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (ok && w.g >= 2) ok = wait(&misc->s_empty[sb], ((w.g >> 1) - 1) & 1);
       const bool last = !n.next() || n.first;
-      const uint32_t d = tmem + kColS + 64 * sb;
-      const uint64_t dk = desc(sKV + s * C::kTile, 16);
+      const uint32_t d = tmem + kColS + 128 * sb + 64 * i;
+      const uint64_t dk = desc(sKV + s * C::kTile + (kFp8 ? 0 : 64 * i), 16);
 #pragma unroll
       for (int part = 0; part < 3; ++part) {
         if (ok) ok = wait(&misc->full[s][part], (w.g / kStages) & 1);
@@ -536,13 +542,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int c = 4 * part; c < (part == kC ? 9 : 4 * part + 4); ++c) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint32_t acc = (c > 0 || k > 0) ? 1u : 0u;
-              // e4m3: 32-dim step k / 2, term k % 2 of the query
-              const uint32_t oq = c * C::kSlot + (kFp8 ? (k & 1) * (kQBytes / 2) + 32 * (k >> 1) : 32 * k);
-              const uint32_t ok16 = c * C::kSlot + 32 * (kFp8 ? k >> 1 : k);
-              if (kFp8) mma_e4m3_pair(d, dq + (oq >> 4), dk + (ok16 >> 4), id, acc);
-              else mma_bf16_pair(d, dq + (oq >> 4), dk + (ok16 >> 4), id, acc);
+            for (int k = 0; k < 2; ++k) {
+              const uint32_t acc = (c > 0 || k > 0) ? 1u : 0u, o = (c * C::kSlot + 32 * k) >> 4;
+              if (kFp8) mma_e4m3_pair(d, dq + o, dk + o, id, acc);
+              else mma_bf16_pair(d, dq + o, dk + o, id, acc);
             }
           }
           if (part == kC) {
@@ -555,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     if (!ok && lane == 0) fail();
-  } else if (warp == 2 && leader) {
+  } else if (warp == 12 && leader) {
     // ------------------------------------------------------------ P V issue
     constexpr uint32_t id = kFp8 ? idesc_e4m3_f32(128, 256, false, true)
                                  : idesc_bf16_f32(128, 256, false, true);
@@ -598,7 +601,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     }
     if (!ok && lane == 0) fail();
-  } else if (warp >= 4) {
+  } else if (warp >= 4 && warp < 12) {
     // ------------------------------------------------------------ softmax
     const int quad = warp & 3, half = quad >> 1;           // TMEM lanes 32 quad ..
     const int grp = (warp - 4) >> 2;                       // tokens 64 half + 32 grp ..
@@ -632,9 +635,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool there = 2 * w.j + half < w.u.w;
         if (ok) {
           tc_fence_after();
+          // both issuers' accumulators (the second in two parts, for registers)
           uint32_t v[32];
-          tmem_ld32(tmem + lanes + kColS + 64 * sb + 32 * grp, v);
-          tmem_wait_ld();
+          const uint32_t s0 = tmem + lanes + kColS + 128 * sb + 32 * grp;
+          tmem_ld32(s0, v);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t u[16];
+            tmem_ld16(s0 + 64 + 16 * h, u);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              a[16 * h + i] = __uint_as_float(v[16 * h + i]) + __uint_as_float(u[i]);
+          }
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_pair(at_leader(&misc->s_empty[sb]));
@@ -651,8 +664,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const int i = 4 * i4 + e;
-              const float x = __uint_as_float(v[i]);
-              a[i] = kFp8 ? x * sg[e] * qs : x;
+              if (kFp8) a[i] = a[i] * sg[e] * qs;
               m4[e] = fmaxf(m4[e], kFp8 ? a[i] + eg[e] : a[i]);
             }
           }
@@ -676,7 +688,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           m_run = m_new;
           rescale = live && !w.first;
         }
-        const float m_use = m_run == -CUDART_INF_F ? 0.0f : m_run;
+        // (a page that is not there has keys of 0: finite logits, and weights of 0)
+        const float m_use = !there ? CUDART_INF_F : m_run == -CUDART_INF_F ? 0.0f : m_run;
         // P V of the tile before: O is rescaled behind it, and it has read the
         // probabilities that are written over
         const int gp = w.g - 1, ga = kFp8 ? w.g - 2 : w.g - 1;
@@ -709,9 +722,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             float pv[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const float u = there ? ex2_approx(a[4 * i4 + e] - m_use) : 0.0f;
+              const float u = ex2_approx(a[4 * i4 + e] - m_use);
               ls[e] += u;
-              pv[e] = there ? u * sg[e] : 0.0f;
+              pv[e] = u * sg[e];
             }
             const uint32_t s01 = split_e4m3x2(pv[0], pv[1]), s23 = split_e4m3x2(pv[2], pv[3]);
             hi4[i4] = (s01 & 0xFFFFu) | (s23 << 16);
@@ -737,8 +750,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < 16; ++i) {
             // bf16: P is rounded to 8 bits, relative 2^-9, as in the
             // per-request kernel; its sum is taken before the rounding
-            const float x = there ? ex2_approx(fmaf(a[2 * i], p.scale_log2, -m_use)) : 0.0f;
-            const float y = there ? ex2_approx(fmaf(a[2 * i + 1], p.scale_log2, -m_use)) : 0.0f;
+            const float x = ex2_approx(fmaf(a[2 * i], p.scale_log2, -m_use));
+            const float y = ex2_approx(fmaf(a[2 * i + 1], p.scale_log2, -m_use));
             pk[i] = pack_bf16(x, y);
             ls[i & 3] += x + y;
           }
@@ -827,7 +840,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // after a failure, the MMAs and copies in flight land before tensor and
     // shared memory are given back
     int never = 0;
-    if (leader && (warp == 1 || warp == 2) && lane == 0) {
+    if (leader && (warp == 1 || warp == 2 || warp == 12) && lane == 0) {
       asm volatile(
           "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
               smem_u32(&misc->drain))

@@ -12,8 +12,9 @@
 // the rows, so the sum over rows stays inside a thread (fixed order, nothing
 // to exchange) and every thread ends with one token's weight.
 //
-//   warp 0      K producer: per tile nine chunks of 64 dims (two pages, one
-//               TMA box each) into a ring of nine (bf16) or eighteen (e4m3)
+//   warp 0      K producer: per tile three groups of three 64-dim chunks (two
+//               pages, one TMA box each) into a ring of three (bf16) or six
+//               (e4m3)
 //   warp 1      MMA issue
 //   warps 2..5  one token a thread: exp2 of every column, summed
 //   warp 6      Q producer: a group's nine chunks.  A request of one group of
@@ -44,7 +45,7 @@ namespace weights {
 
 constexpr int kThreads = 224;
 constexpr int kTokens = 128;               // tokens per tile: MMA M
-constexpr int kMaxDepth = 18;
+constexpr int kMaxDepth = 6;
 constexpr uint32_t kBarSum = 1;            // named barrier of the summing warps
 constexpr int kSumThreads = 128;
 constexpr uint32_t kTmemCols = 512;        // two accumulators of up to 256 columns
@@ -130,9 +131,11 @@ template <bool kFp8, int kRowsN>
 struct Cfg {
   static constexpr int kN = kFp8 ? 2 * kRowsN : kRowsN;
   static constexpr int kLine = kFp8 ? 64 : 128;            // bytes of a chunk's row
-  static constexpr int kKBytes = kTokens * kLine;          // K chunk: 8 or 16 KB
+  // a slot of K: [16 groups of 8 tokens][3 chunks][8 tokens][64 dims]
+  static constexpr int kKGroup = kCgChunks * 8 * kLine;
+  static constexpr int kKBytes = kTokens / 8 * kKGroup;    // 24 or 48 KB
   static constexpr int kQBytes = kN * kLine;               // Q chunk: 8 or 16 KB
-  static constexpr int kKDepth = kFp8 ? 18 : 9;
+  static constexpr int kKDepth = kFp8 ? 6 : 3;
   static constexpr int kQDepth = kRowsN == 64 ? 9 : 4;
   static constexpr int kSmemQ = kKDepth * kKBytes;
   static constexpr int kSmemMisc = kSmemQ + kQDepth * kQBytes;
@@ -180,8 +183,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     atomicOr(&p.hdr->err, kErrTimeout);
     *(volatile int*)&misc->abort = 1;
   };
+  // one thread's wait: a warp whose 32 lanes poll takes a few times as long
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), parity, tmo, abort_flag));
+    return mbar_wait(smem_u32(bar), parity, tmo, abort_flag);
   };
 
   if (threadIdx.x == 0) {
@@ -227,92 +231,108 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     // ---------------------------------------------------------- K producer
-    while (ok && walk.next<kRowsN>(p, b, L, rows, groups, t0, t1)) {
-      const int npages = ceil_div(L, kPage);
-      const int32_t* bt = p.block_table + (size_t)b * p.max_pages;
-      for (int t = t0; ok && t < t1; ++t) {
-        // lane k < 2: page k of the tile; past the context or out of range it
-        // lies behind the pool, and its rows are zeros
-        int page = p.num_pages;
-        if (lane < 2 && 2 * t + lane < npages) {
-          page = __ldg(bt + 2 * t + lane);
-          if (page < 0 || page >= p.num_pages) {
-            atomicOr(&p.hdr->err, kErrBadPage);
-            page = p.num_pages;
+    // (one thread; so are the other producer and the issuer)
+    if (lane == 0) {
+      while (ok && walk.next<kRowsN>(p, b, L, rows, groups, t0, t1)) {
+        const int npages = ceil_div(L, kPage);
+        const int32_t* bt = p.block_table + (size_t)b * p.max_pages;
+        // the table's entries are read a tile ahead
+        int e[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) e[h] = 2 * t0 + h < npages ? __ldg(bt + 2 * t0 + h) : -1;
+        for (int t = t0; ok && t < t1; ++t) {
+          // a page past the context or out of range lies behind the pool, and its
+          // rows are zeros
+          int group[2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const bool valid = e[h] >= 0 && e[h] < p.num_pages;
+            if (2 * t + h < npages && !valid) atomicOr(&p.hdr->err, kErrBadPage);
+            group[h] = (valid ? e[h] : p.num_pages) * (kPage / 8);
+            const int i = 2 * t + 2 + h;
+            e[h] = i < npages ? __ldg(bt + i) : -1;
+          }
+#pragma unroll
+          for (int c = 0; c < kChunks / kCgChunks; ++c, ++armed) {
+            const int s = armed % C::kKDepth, use = armed / C::kKDepth;
+            if (use > 0) ok = wait(&misc->ke[s], (use - 1) & 1);
+            if (!ok) break;
+            const uint32_t bar = smem_u32(&misc->kf[s]);
+            mbar_arrive_expect_tx(bar, C::kKBytes);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              tma_load_4d(sK + s * C::kKBytes + h * (C::kKBytes / 2), &tm_k, bar, 0, 0,
+                          kCgChunks * c, group[h]);
           }
         }
-        for (int c = 0; c < kChunks; ++c, ++armed) {
-          const int s = armed % C::kKDepth, use = armed / C::kKDepth;
-          if (use > 0) ok = wait(&misc->ke[s], (use - 1) & 1);
-          if (!ok) break;
-          if (lane == 0) mbar_arrive_expect_tx(smem_u32(&misc->kf[s]), C::kKBytes);
-          __syncwarp();
-          if (lane < 2)
-            tma_load_2d(sK + s * C::kKBytes + lane * (C::kKBytes / 2), &tm_k,
-                        smem_u32(&misc->kf[s]), 64 * c, page * kPage);
-        }
       }
+      if (!ok) fail();
     }
-    if (!ok && lane == 0) fail();
   } else if (warp == 6) {
     // ---------------------------------------------------------- Q producer
-    while (ok && walk.next<kRowsN>(p, b, L, rows, groups, t0, t1)) {
-      for (int t = t0; ok && t < (stay ? t0 + 1 : t1); ++t)
-        for (int g = 0; ok && g < groups; ++g)
-          for (int c = 0; c < kChunks; ++c, ++armed) {
-            const int s = armed % C::kQDepth, use = armed / C::kQDepth;
-            if (use > 0) ok = wait(&misc->qe[s], (use - 1) & 1);
-            if (!ok) break;
-            if (lane == 0) {
+    if (lane == 0) {
+      while (ok && walk.next<kRowsN>(p, b, L, rows, groups, t0, t1)) {
+        for (int t = t0; ok && t < (stay ? t0 + 1 : t1); ++t)
+          for (int g = 0; ok && g < groups; ++g)
+            for (int c = 0; c < kChunks; ++c, ++armed) {
+              const int s = armed % C::kQDepth, use = armed / C::kQDepth;
+              if (use > 0) ok = wait(&misc->qe[s], (use - 1) & 1);
+              if (!ok) break;
               mbar_arrive_expect_tx(smem_u32(&misc->qf[s]), C::kQBytes);
               tma_load_2d(sQ + s * C::kQBytes, &tm_q, smem_u32(&misc->qf[s]), 64 * c,
                           (b * p.R + g * kRowsN) * (kFp8 ? 2 : 1));
             }
-            __syncwarp();
-          }
+      }
+      if (!ok) fail();
     }
-    if (!ok && lane == 0) fail();
   } else if (warp == 1) {
     // ----------------------------------------------------------- MMA issue
-    constexpr uint32_t id = kFp8 ? idesc_e4m3_f32(kTokens, C::kN, false, false)
-                                 : idesc_bf16_f32(kTokens, C::kN, false, false);
-    constexpr uint32_t kGroup = 8 * C::kLine;              // eight rows
-    constexpr int kSteps = kFp8 ? 2 : 4;                   // 32-byte steps of a chunk
-    int nk = 0, nq = 0, nd = 0;
-    while (ok && walk.next<kRowsN>(p, b, L, rows, groups, t0, t1)) {
-      for (int t = t0; ok && t < t1; ++t) {
-        for (int g = 0; ok && g < groups; ++g, ++nd) {
-          const int buf = nd & 1;
-          if (nd >= 2) ok = wait(&misc->de[buf], ((nd >> 1) - 1) & 1);
-          for (int c = 0; ok && c < kChunks; ++c) {
-            const int ks = (nk + c) % C::kKDepth, qs = (nq + c) % C::kQDepth;
-            if (g == 0) ok = wait(&misc->kf[ks], ((nk + c) / C::kKDepth) & 1);
-            if (ok && (!stay || t == t0)) ok = wait(&misc->qf[qs], ((nq + c) / C::kQDepth) & 1);
-            if (!ok) break;
-            tc_fence_after();
-            if (lane == 0) {
+    if (lane == 0) {
+      constexpr uint32_t id = kFp8 ? idesc_e4m3_f32(kTokens, C::kN, false, false)
+                                   : idesc_bf16_f32(kTokens, C::kN, false, false);
+      constexpr uint32_t kQGroup = 8 * C::kLine;           // eight rows
+      constexpr int kSteps = kFp8 ? 2 : 4;                 // 32-byte steps of a chunk
+      const uint64_t dk0 = kFp8 ? sw64_desc(sK, 16, C::kKGroup) : sw128_desc(sK, 16, C::kKGroup);
+      const uint64_t dq0 = kFp8 ? sw64_desc(sQ, 16, kQGroup) : sw128_desc(sQ, 16, kQGroup);
+      int nk = 0, nq = 0, nd = 0;                          // loads and sums so far
+      while (ok && walk.next<kRowsN>(p, b, L, rows, groups, t0, t1)) {
+        for (int t = t0; ok && t < t1; ++t) {
+          for (int g = 0; ok && g < groups; ++g, ++nd) {
+            const int buf = nd & 1;
+            if (nd >= 2) ok = wait(&misc->de[buf], ((nd >> 1) - 1) & 1);
+            const uint32_t d = tmem + 256 * buf;
+#pragma unroll 1
+            for (int cg = 0; ok && cg < kChunks / kCgChunks; ++cg) {
+              const int ks = (nk + cg) % C::kKDepth;
+              if (g == 0) ok = wait(&misc->kf[ks], ((nk + cg) / C::kKDepth) & 1);
+              const uint64_t dk = dk0 + ((ks * C::kKBytes) >> 4);
 #pragma unroll
-              for (int k = 0; k < kSteps; ++k) {
-                const uint32_t a = sK + ks * C::kKBytes + 32 * k, q = sQ + qs * C::kQBytes + 32 * k;
-                const uint32_t d = tmem + 256 * buf, acc = (c > 0 || k > 0) ? 1u : 0u;
-                if (kFp8)
-                  mma_e4m3_ss(d, sw64_desc(a, 16, kGroup), sw64_desc(q, 16, kGroup), id, acc);
-                else
-                  mma_bf16_ss(d, sw128_desc(a, 16, kGroup), sw128_desc(q, 16, kGroup), id, acc);
+              for (int c = 0; c < kCgChunks; ++c) {
+                const int i = nq + cg * kCgChunks + c, qs = i % C::kQDepth;
+                if (ok && (!stay || t == t0)) ok = wait(&misc->qf[qs], (i / C::kQDepth) & 1);
+                if (!ok) break;
+                tc_fence_after();
+                const uint64_t dq = dq0 + ((qs * C::kQBytes) >> 4);
+#pragma unroll
+                for (int k = 0; k < kSteps; ++k) {
+                  const uint64_t a = dk + ((c * 8 * C::kLine + 32 * k) >> 4), q = dq + ((32 * k) >> 4);
+                  const uint32_t acc = (cg > 0 || c > 0 || k > 0) ? 1u : 0u;
+                  if (kFp8) mma_e4m3_ss(d, a, q, id, acc);
+                  else mma_bf16_ss(d, a, q, id, acc);
+                }
+                if (!stay || t == t1 - 1) mma_commit(smem_u32(&misc->qe[qs]));
               }
-              if (g == groups - 1) mma_commit(smem_u32(&misc->ke[ks]));
-              if (!stay || t == t1 - 1) mma_commit(smem_u32(&misc->qe[qs]));
-              if (c == kChunks - 1) mma_commit(smem_u32(&misc->df[buf]));
+              if (ok && g == groups - 1) mma_commit(smem_u32(&misc->ke[ks]));
             }
-            __syncwarp();
+            if (ok) mma_commit(smem_u32(&misc->df[buf]));
+            if (!stay) nq += kChunks;
           }
-          if (!stay) nq += kChunks;
+          nk += kChunks / kCgChunks;
         }
-        nk += kChunks;
+        if (stay) nq += kChunks;
       }
-      if (stay) nq += kChunks;
+      if (!ok) fail();
     }
-    if (!ok && lane == 0) fail();
   } else {
     // ---------------------------------------------------------- summing
     const int quad = warp & 3, tid = 32 * quad + lane;     // the thread's token of a tile
@@ -357,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             named_bar_sync(kBarSum, kSumThreads);
           }
           const int buf = nd & 1;
-          ok = wait(&misc->df[buf], (nd >> 1) & 1);
+          ok = __all_sync(0xffffffffu, wait(&misc->df[buf], (nd >> 1) & 1));
           if (named_bar_or(kBarSum, kSumThreads, !ok)) {
             ok = false;
             break;
@@ -407,6 +427,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   // ---------------------------------------------------------------- teardown
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
   if (*abort_flag) {
@@ -452,13 +473,11 @@ bool shape_ok(const mla_shape* s) {
          s->softmax_scale > 0.f && (long long)s->batch * s->q_len * s->num_heads < (1LL << 30);
 }
 
-bool encode2d(CUtensorMap* m, bool fp8, const void* base, uint64_t rows, uint32_t box_rows) {
-  const uint64_t e = fp8 ? 1 : 2;
-  cuuint64_t dims[2] = {(cuuint64_t)kDqk, rows};
-  cuuint64_t strides[1] = {kDqk * e};
-  cuuint32_t box[2] = {64, box_rows}, es[2] = {1, 1};
+bool encode(CUtensorMap* m, bool fp8, const void* base, int rank, const cuuint64_t* dims,
+            const cuuint64_t* strides, const cuuint32_t* box) {
+  const cuuint32_t es[4] = {1, 1, 1, 1};
   return host::encode_fn()(m, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                           2, const_cast<void*>(base), dims, strides, box, es,
+                           rank, const_cast<void*>(base), dims, strides, box, es,
                            CU_TENSOR_MAP_INTERLEAVE_NONE,
                            fp8 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
                            fp8 ? CU_TENSOR_MAP_L2_PROMOTION_NONE : CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
@@ -471,8 +490,14 @@ mla_status run(const Params& p, const void* kv, int grid, cudaStream_t st) {
   CUtensorMap tm_k, tm_q;
   const void* q = kFp8 ? static_cast<const void*>(p.terms) : p.q;
   const uint64_t rows = (uint64_t)p.B * p.R * (kFp8 ? 2 : 1);
-  if (!encode2d(&tm_k, kFp8, kv, (uint64_t)p.num_pages * kPage, kPage) ||
-      !encode2d(&tm_q, kFp8, q, rows, C::kN))
+  const cuuint64_t e = kFp8 ? 1 : 2;
+  // cache: (64 dims, row of 8, chunk, 8-row group); query: (dim, row)
+  const cuuint64_t kd[4] = {64, 8, (cuuint64_t)kChunks, (cuuint64_t)p.num_pages * (kPage / 8)};
+  const cuuint64_t ks[3] = {kDqk * e, 64 * e, 8 * kDqk * e};
+  const cuuint32_t kb[4] = {64, 8, (cuuint32_t)kCgChunks, (cuuint32_t)(kPage / 8)};
+  const cuuint64_t qd[2] = {(cuuint64_t)kDqk, rows}, qs[1] = {kDqk * e};
+  const cuuint32_t qb[2] = {64, (cuuint32_t)C::kN};
+  if (!encode(&tm_k, kFp8, kv, 4, kd, ks, kb) || !encode(&tm_q, kFp8, q, 2, qd, qs, qb))
     return MLA_ERR_CUDA;
   cudaLaunchAttribute attr = pdl_attribute();
   cudaLaunchConfig_t cfg = {};
