@@ -73,12 +73,14 @@ struct Copy {
   unsigned* err;
 };
 
+constexpr uint32_t kZero = 0x80000000u;   // key of 0
+
 // Unsigned key in the order of the weights: -inf first, both zeros alike, NaN
 // above everything.
 __device__ __forceinline__ uint32_t key_of(float w) {
   const uint32_t u = __float_as_uint(w);
   if (w != w) return 0xFFFFFFFFu;
-  if (w == 0.0f) return 0x80000000u;
+  if (w == 0.0f) return kZero;
   return (u >> 31) ? ~u : u | 0x80000000u;
 }
 
@@ -170,20 +172,18 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(Select p) {
       for (int i = tid; i < kBins; i += kThreads) hist[i] = 0;
     if (C > 1 && pass == 0) cluster.sync();   // rank 0's totals are zero
     else __syncthreads();
-    // The lanes that have the first such lane's digit add once between them:
-    // weights crowd into few exponents, and many are zero together.
+    // Weights of zero, often many, are counted by ballot; the others spread over
+    // enough digits (an exponent has four) for atomics of their own.  Grouping
+    // equal digits first took 2.5 times as long on a long-tailed row.
+    uint32_t zeros = 0;
     each([&](uint32_t x, int i) {
       // upper = 32 on the first pass: everything matches
       const bool in = i < wz && (upper >= 32 || (x >> upper) == match);
-      const uint32_t live = __ballot_sync(0xFFFFFFFFu, in);
-      if (live == 0) return;
-      const uint32_t d = (x >> shift) & mask;
-      const int lead = __ffs(live) - 1;
-      const uint32_t d0 = __shfl_sync(0xFFFFFFFFu, d, lead);
-      const bool same = in && d == d0;
-      const uint32_t m = __popc(__ballot_sync(0xFFFFFFFFu, same));
-      if (in && (!same || lane == lead)) atomicAdd(&hist[d], same ? m : 1u);
+      const bool zero = in && x == kZero;
+      zeros += __popc(__ballot_sync(0xFFFFFFFFu, zero));
+      if (in && !zero) atomicAdd(&hist[(x >> shift) & mask], 1u);
     });
+    if (lane == 0 && zeros != 0) atomicAdd(&hist[(kZero >> shift) & mask], zeros);
     __syncthreads();
     if (C > 1) {
       // the few digits that occur go to rank 0 (every CTA reading all of the
@@ -343,9 +343,13 @@ inline bool overlap(const void* a, size_t n, const void* b, size_t m) {
   return x < y + m && y < x + n;
 }
 
-// A context is cut by a cluster whose CTAs have 8192 weights each at most, or
-// 16384 of up to 262144, or by 16 CTAs.  (One CTA for 32768 weights took
-// MEASURE us, eight 15; eight for a million 66, sixteen 42.)
+// CTAs per request, by the width of the weights.  A whole eviction to a quarter
+// (e4m3) with one CTA of 512 threads, and clusters of 4, 8 and 16 of 1024:
+//   4 x 777      11.3,  16.2,  16.3,  18.2 us
+//   16 x 8000    18.0,  19.9,  32.0,  48.3
+//   16 x 40000    117,  52.3,  64.5,  82.7
+//   4 x 131000    279,  68.6,  49.8,  49.1
+//   1 x 1048576  1443,   278,   174,   124
 template <int C, int kThreads>
 cudaError_t select(const Select& s, int batch, cudaStream_t stream) {
   const void* kernel = reinterpret_cast<const void*>(&evict_select_kernel<C, kThreads>);
@@ -441,6 +445,7 @@ extern "C" mla_status mla_cache_evict(const mla_kv_pages* kv, const int32_t* blo
                       err};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const cudaError_t se = weights_width <= 8192     ? evict::select<1, 512>(s, batch, st)
+                         : weights_width <= 65536  ? evict::select<4, 1024>(s, batch, st)
                          : weights_width <= 262144 ? evict::select<8, 1024>(s, batch, st)
                                                    : evict::select<16, 1024>(s, batch, st);
   if (se != cudaSuccess) return MLA_ERR_CUDA;
