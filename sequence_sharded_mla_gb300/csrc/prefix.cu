@@ -274,30 +274,26 @@ struct Walk {
   }
 };
 
-// The pages of a walk's tiles: lane l holds entries base + l and base + 32 + l of
-// the table row, the second half on its way while the first is used.
+// The two pages of a walk's tiles, read a tile ahead by one thread.
 struct Pages {
   const int32_t* row;
-  int base, count, cur, ahead;
+  int count, ahead[2];
   __device__ int entry(int i) const { return i < count ? __ldg(row + i) : -1; }
-  __device__ void move_to(const Params& p, const Walk& w, int lane) {
+  // The tile's pages; one behind the prefix or out of range gives num_pages,
+  // which lies behind the pool, where loads give zeros.
+  __device__ void next(const Params& p, const Walk& w, int (&page)[2]) {
     if (w.first) {
       row = p.block_table + (size_t)w.u.z * p.max_pages;
       count = w.u.w;
-      base = (2 * w.j) & ~31;
-      cur = entry(base + lane);
-      ahead = entry(base + 32 + lane);
-    } else if (2 * w.j >= base + 32) {
-      base += 32;
-      cur = ahead;
-      ahead = entry(base + 32 + lane);
+      ahead[0] = entry(2 * w.j);
+      ahead[1] = entry(2 * w.j + 1);
     }
-  }
-  // Entry i of the tile; one behind the prefix or out of range gives num_pages,
-  // which lies behind the pool, where loads give zeros.
-  __device__ int at(const Params& p, int i) const {
-    const int v = __shfl_sync(0xffffffffu, cur, i & 31);
-    return i < count && v >= 0 && v < p.num_pages ? v : p.num_pages;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int e = ahead[h];
+      page[h] = e >= 0 && e < p.num_pages ? e : p.num_pages;
+      ahead[h] = entry(2 * w.j + 2 + h);
+    }
   }
 };
 
@@ -340,8 +336,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     *(volatile int*)&misc->abort = 1;
     st_cluster(peer_abort, 1);
   };
+  // one thread's wait, and a warp's
+  auto wait1 = [&](uint64_t* bar, uint32_t parity) {
+    return mbar_wait(smem_u32(bar), parity, tmo, abort_flag);
+  };
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), parity, tmo, abort_flag));
+    return __all_sync(0xffffffffu, wait1(bar, parity)) != 0;
   };
   auto at_leader = [&](uint64_t* bar) { return map_rank(smem_u32(bar), 0); };
 
@@ -402,58 +402,48 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     // ---------------------------------------------------------- K producer
-    Pages pages;
-    int pieces = 0;
-    while (ok && w.next()) {
-      const int s = w.g % kStages, use = w.g / kStages;
-      const uint32_t st = sKV + s * C::kTile;
-      pages.move_to(p, w, lane);
-      const int i = 2 * w.j + (int)rank;
-      const int page = pages.at(p, i), row = page * kPage;
-      if (lane == 0 && page == p.num_pages && i < w.u.w) atomicOr(p.err, kErrBadPage);
-      if (use > 0) ok = wait(&misc->a_free[s], (use - 1) & 1);
-      if (!ok) break;
-      if (lane == 0) {
+    // (one thread; so are the other producer and the issuers)
+    if (lane == 0) {
+      Pages pages;
+      int pieces = 0;
+      while (ok && w.next()) {
+        const int s = w.g % kStages, use = w.g / kStages;
+        const uint32_t st = sKV + s * C::kTile;
+        int page[2];
+        pages.next(p, w, page);
+        const int mine = leader ? page[0] : page[1], row = mine * kPage;
+        if (mine == p.num_pages && 2 * w.j + (int)rank < w.u.w) atomicOr(p.err, kErrBadPage);
+        if (use > 0) ok = wait1(&misc->a_free[s], (use - 1) & 1);
+        if (!ok) break;
         arm(s, kA, 4 * C::kSlot);
         tma_load_3d_pair(st, &tm_kv4, at_leader(&misc->full[s][kA]), 0, row, 0);
-      }
-      __syncwarp();
-      if (use > 0) ok = wait(&misc->pv_done[s], (use - 1) & 1);
-      if (!ok) break;
-      if (lane == 0) {
+        if (use > 0) ok = wait1(&misc->pv_done[s], (use - 1) & 1);
+        if (!ok) break;
         arm(s, kB, 4 * C::kSlot);
         tma_load_3d_pair(st + 4 * C::kSlot, &tm_kv4, at_leader(&misc->full[s][kB]), 0, row, 4);
         arm(s, kC, C::kSlot);
         tma_load_3d_pair(st + 8 * C::kSlot, &tm_kv1, at_leader(&misc->full[s][kC]), 0, row, 8);
-      }
-      __syncwarp();
-      if (kFp8) {
-        // both pages' token scales; 1 where there is no page (its codes are 0)
-        uint32_t bytes = 0;
-        const float* src[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int pg = pages.at(p, 2 * w.j + h);
-          src[h] = pg < p.num_pages ? p.kv_scale + (size_t)pg * kPage : nullptr;
-          if (src[h] != nullptr) bytes += kPage * 4;
-          else misc->sigma[s][64 * h + lane] = misc->sigma[s][64 * h + 32 + lane] = 1.0f;
-        }
-        __syncwarp();
-        if (lane == 0) {
+        if (kFp8) {
+          // both pages' token scales; 1 where there is no page (its codes are 0)
           const uint32_t bar = smem_u32(&misc->sc_full[s]);
+          uint32_t bytes = 0;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (page[h] < p.num_pages) bytes += kPage * 4;
+            else
+              for (int a = 0; a < kPage; ++a) misc->sigma[s][64 * h + a] = 1.0f;
+          }
           mbar_arrive_expect_tx(bar, bytes);
 #pragma unroll
           for (int h = 0; h < 2; ++h)
-            if (src[h] != nullptr)
-              bulk_load(smem_u32(&misc->sigma[s][64 * h]), src[h], kPage * 4, bar);
+            if (page[h] < p.num_pages)
+              bulk_load(smem_u32(&misc->sigma[s][64 * h]), p.kv_scale + (size_t)page[h] * kPage,
+                        kPage * 4, bar);
         }
-        __syncwarp();
-      }
-      if (w.first) {
-        // the piece's query, once S of the piece before is done
-        if (pieces > 0) ok = wait(&misc->q_empty, (pieces - 1) & 1);
-        if (!ok) break;
-        if (lane == 0) {
+        if (w.first) {
+          // the piece's query, once S of the piece before is done
+          if (pieces > 0) ok = wait1(&misc->q_empty, (pieces - 1) & 1);
+          if (!ok) break;
           misc->armed_q++;
           mbar_arrive_expect_tx_pair(at_leader(&misc->q_full), kQBytes);
           const int r0 = w.u.x + (int)rank * kHalf;
@@ -463,23 +453,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           } else {
             tma_load_3d_pair(sQ, &tm_q, at_leader(&misc->q_full), 0, r0, 0);
           }
+          ++pieces;
         }
-        __syncwarp();
-        ++pieces;
       }
+      if (!ok) fail();
     }
-    if (!ok && lane == 0) fail();
   } else if (warp == 3) {
     // ---------------------------------------------------------- V producer
     // The CTA's dims of the other CTA's page, over what S has read; e4m3: before
-    // that the tile's token scales.
+    // that the tile's token scales, by the whole warp.
     Pages pages;
     while (ok && w.next()) {
       const int s = w.g % kStages;
-      pages.move_to(p, w, lane);
-      const int i = 2 * w.j + (int)(rank ^ 1);
-      const int page = pages.at(p, i), row = page * kPage;
-      if (lane == 0 && page == p.num_pages && i < w.u.w) atomicOr(p.err, kErrBadPage);
       if (kFp8) {
         // token scales sigma = mant 2^E with mant in [0.5, 1): sigma sanitised
         // in place, E apart
@@ -502,43 +487,49 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&misc->sc_ready[s]));
       }
-      ok = wait(&misc->k_read[s], (w.g / kStages) & 1);
-      if (!ok) break;
       if (lane == 0) {
-        arm(s, kV, 4 * C::kSlot);
-        tma_load_3d_pair(sKV + s * C::kTile + (leader ? 4 : 0) * C::kSlot, &tm_kv4,
-                         at_leader(&misc->full[s][kV]), 0, row, leader ? 0 : 4);
+        int page[2];
+        pages.next(p, w, page);
+        const int other = leader ? page[1] : page[0], row = other * kPage;
+        if (other == p.num_pages && 2 * w.j + (int)(rank ^ 1) < w.u.w)
+          atomicOr(p.err, kErrBadPage);
+        ok = wait1(&misc->k_read[s], (w.g / kStages) & 1);
+        if (ok) {
+          arm(s, kV, 4 * C::kSlot);
+          tma_load_3d_pair(sKV + s * C::kTile + (leader ? 4 : 0) * C::kSlot, &tm_kv4,
+                           at_leader(&misc->full[s][kV]), 0, row, leader ? 0 : 4);
+        }
       }
-      __syncwarp();
+      ok = __shfl_sync(0xffffffffu, ok, 0) != 0;
     }
     if (!ok && lane == 0) fail();
   } else if ((warp == 1 || warp == 2) && leader) {
     // ------------------------------------------------------------ S issue
     constexpr uint32_t id = kFp8 ? idesc_e4m3_f32(128, 128, false, false)
                                  : idesc_bf16_f32(128, 128, false, false);
-    // bf16: issuer i takes the 16-dim steps 2 i, 2 i + 1 of every chunk; e4m3: the
-    // query's term i
-    const int i = warp - 1;
-    const uint64_t dq = desc(sQ + i * (kFp8 ? kQBytes / 2 : 64), 16);
-    int pieces = 0;
-    Walk n = w;                  // the next tile: is this one its piece's last?
-    n.next();
-    while (ok && w.next()) {
-      const int s = w.g % kStages, sb = w.g & 1;
-      if (w.first) {
-        ok = wait(&misc->q_full, pieces & 1);
-        ++pieces;
-      }
-      if (ok && w.g >= 2) ok = wait(&misc->s_empty[sb], ((w.g >> 1) - 1) & 1);
-      const bool last = !n.next() || n.first;
-      const uint32_t d = tmem + kColS + 128 * sb + 64 * i;
-      const uint64_t dk = desc(sKV + s * C::kTile + (kFp8 ? 0 : 64 * i), 16);
+    if (lane == 0) {
+      // bf16: issuer i takes the 16-dim steps 2 i, 2 i + 1 of every chunk; e4m3:
+      // the query's term i
+      const int i = warp - 1;
+      const uint64_t dq = desc(sQ + i * (kFp8 ? kQBytes / 2 : 64), 16);
+      int pieces = 0;
+      Walk n = w;                // the next tile: is this one its piece's last?
+      n.next();
+      while (ok && w.next()) {
+        const int s = w.g % kStages, sb = w.g & 1;
+        if (w.first) {
+          ok = wait1(&misc->q_full, pieces & 1);
+          ++pieces;
+        }
+        if (ok && w.g >= 2) ok = wait1(&misc->s_empty[sb], ((w.g >> 1) - 1) & 1);
+        const bool last = !n.next() || n.first;
+        const uint32_t d = tmem + kColS + 128 * sb + 64 * i;
+        const uint64_t dk = desc(sKV + s * C::kTile + (kFp8 ? 0 : 64 * i), 16);
 #pragma unroll
-      for (int part = 0; part < 3; ++part) {
-        if (ok) ok = wait(&misc->full[s][part], (w.g / kStages) & 1);
-        if (!ok) break;
-        tc_fence_after();
-        if (lane == 0) {
+        for (int part = 0; part < 3; ++part) {
+          if (ok) ok = wait1(&misc->full[s][part], (w.g / kStages) & 1);
+          if (!ok) break;
+          tc_fence_after();
 #pragma unroll
           for (int c = 4 * part; c < (part == kC ? 9 : 4 * part + 4); ++c) {
 #pragma unroll
@@ -548,32 +539,30 @@ __global__ void __launch_bounds__(kThreads, 1)
               else mma_bf16_pair(d, dq + o, dk + o, id, acc);
             }
           }
-          if (part == kC) {
-            mma_commit_pair(smem_u32(&misc->s_full[sb]));
-            mma_commit_pair(smem_u32(&misc->k_read[s]));
-            if (last) mma_commit_pair(smem_u32(&misc->q_empty));
-          }
         }
-        __syncwarp();
+        if (!ok) break;
+        mma_commit_pair(smem_u32(&misc->s_full[sb]));
+        mma_commit_pair(smem_u32(&misc->k_read[s]));
+        if (last) mma_commit_pair(smem_u32(&misc->q_empty));
       }
+      if (!ok) fail();
     }
-    if (!ok && lane == 0) fail();
   } else if (warp == 12 && leader) {
     // ------------------------------------------------------------ P V issue
     constexpr uint32_t id = kFp8 ? idesc_e4m3_f32(128, 256, false, true)
                                  : idesc_bf16_f32(128, 256, false, true);
-    int pieces = 0;
-    while (ok && w.next()) {
-      const int s = w.g % kStages;
-      ok = wait(&misc->p_full[w.g & 1], (w.g >> 1) & 1);
-      if (ok) ok = wait(&misc->full[s][kV], (w.g / kStages) & 1);
-      if (w.first) {
-        if (ok && pieces > 0) ok = wait(&misc->o_free, (pieces - 1) & 1);
-        ++pieces;
-      }
-      if (!ok) break;
-      tc_fence_after();
-      if (lane == 0) {
+    if (lane == 0) {
+      int pieces = 0;
+      while (ok && w.next()) {
+        const int s = w.g % kStages;
+        ok = wait1(&misc->full[s][kV], (w.g / kStages) & 1);
+        if (w.first) {
+          if (ok && pieces > 0) ok = wait1(&misc->o_free, (pieces - 1) & 1);
+          ++pieces;
+        }
+        if (ok) ok = wait1(&misc->p_full[w.g & 1], (w.g >> 1) & 1);
+        if (!ok) break;
+        tc_fence_after();
         const uint64_t dv = desc(sKV + s * C::kTile, C::kSlot);
         const uint64_t dp0 = kFp8 ? desc(sP + (w.g & 1) * 4 * C::kSlot, 16)
                                   : desc(sKV + s * C::kTile + 8 * C::kSlot, 16);
@@ -598,9 +587,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           mma_commit_pair(smem_u32(half == 0 ? &misc->a_free[s] : &misc->pv_done[s]));
         }
       }
-      __syncwarp();
+      if (!ok) fail();
     }
-    if (!ok && lane == 0) fail();
   } else if (warp >= 4 && warp < 12) {
     // ------------------------------------------------------------ softmax
     const int quad = warp & 3, half = quad >> 1;           // TMEM lanes 32 quad ..
@@ -832,6 +820,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   // ---------------------------------------------------------------- teardown
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
   cluster_sync_all();            // nothing is issued any more, by either CTA
