@@ -23,7 +23,7 @@ SOURCES = ["partial.cu", "partial_fp8.cu", "wuv_gemm.cu", "plan_merge.cu", "comb
            "gqa_fp8.cu", "append.cu", "evict.cu", "weights.cu",
            "prefix.cu"]
 HEADERS = ["common.cuh", "merge.cuh", "ptx.cuh", "host_util.h", "rope.cuh", "qterms.cuh",
-           "pair.cuh", "prefix.h"]
+           "pair.cuh", "prefix.h", "unit_merge.cuh"]
 BINDING = os.path.join(OUT_DIR, "_binding.so")
 BINDING_STAMP = os.path.join(OUT_DIR, "_binding.built-for")
 BINDING_SOURCE = os.path.join(CSRC, "binding.cpp")

@@ -147,11 +147,21 @@ struct RankIo {
   int batch_first;  // first of them computed by this call
 };
 
+// The planning kernel on its own; a caller may have one that does more.
+struct PlanOnly {
+  cudaError_t operator()(const ProblemDesc& pd, WsHeader* hdr, int* prefix, int grid, int min_tiles,
+                         int unit_cost, cudaStream_t st) const {
+    return launch_plan(pd, hdr, prefix, grid, min_tiles, unit_cost, st);
+  }
+};
+
+template <class Plan = PlanOnly>
 mla_status partial_launch(const void* q, const mla_kv_pages* kv, const int32_t* block_table,
                           int max_pages_per_req, const int32_t* seq_lens, const mla_shape* shape,
                           int shard_id, int num_shards, mla_layout layout, float* out_partial,
                           float* lse_partial, void* workspace, size_t workspace_bytes,
-                          void* stream, Launched* L, RankIo rio = RankIo{0, 1, 0, 0}) {
+                          void* stream, Launched* L, RankIo rio = RankIo{0, 1, 0, 0},
+                          Plan plan = Plan()) {
   if (!q || !kv || !block_table || !seq_lens || !out_partial || !lse_partial) return MLA_ERR_INVALID;
   if (!shape_ok(shape)) return MLA_ERR_INVALID;
   if (num_shards < 1 || num_shards > kMaxShards) return MLA_ERR_INVALID;
@@ -373,8 +383,8 @@ mla_status partial_launch(const void* q, const mla_kv_pages* kv, const int32_t* 
   p.withhold_query = host::g_withhold_query.load();
 
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (launch_plan(pd, p.hdr, p.prefix, grid, kMinTilesPerCta, fp8 ? kUnitCostFp8 : kUnitCost,
-                  st) != cudaSuccess)
+  if (plan(pd, p.hdr, p.prefix, grid, kMinTilesPerCta, fp8 ? kUnitCostFp8 : kUnitCost, st) !=
+      cudaSuccess)
     return MLA_ERR_CUDA;
   void* ev0 = host::g_ev_before.load();
   void* ev1 = host::g_ev_after.load();
@@ -418,7 +428,7 @@ StepLayout step_layout(const mla_shape* shape, int num_shards) {
 // own tokens' lengths and tables, the units and their split, the query's terms
 // (e4m3) and the pieces of split units.
 struct PrefixLayout {
-  size_t partial_ws, own_lens, own_table, group_pages, units, positions, work, terms, inv_scale, ws_o, ws_lse, total;
+  size_t partial_ws, own_lens, own_table, group_pages, group_pages2, units, positions, work, terms, inv_scale, ws_o, ws_lse, total;
   int max_units;
 };
 
@@ -428,13 +438,18 @@ bool prefix_layout(const mla_shape* s, int groups, int max_pages, bool fp8, int 
   auto up = [](size_t v) { return (v + 255) & ~static_cast<size_t>(255); };
   const size_t rows = (size_t)s->batch * s->q_len * s->num_heads;
   const long long units = (long long)(rows / prefix::kPairRows) + groups;
-  if (units * (max_pages / 2 + 8LL) >= (1LL << 31)) return false;
+  // work positions, and the joining kernel's blocks
+  const long long own = (long long)s->batch * ceil_div(s->q_len * s->num_heads, kRows);
+  if (units * (max_pages / 2 + 8LL) >= (1LL << 31) ||
+      units * (prefix::kPairRows / 2) + own * (kRows / 2) >= (1LL << 31))
+    return false;
   l->max_units = (int)units;
   l->partial_ws = up(mla_workspace_size(s, 1, 0));
   l->own_lens = l->partial_ws;
   l->own_table = l->own_lens + up(sizeof(int32_t) * (size_t)s->batch);
   l->group_pages = l->own_table + up(sizeof(int32_t) * (size_t)s->batch * max_pages);
-  l->units = l->group_pages + up(sizeof(int32_t) * (size_t)groups);
+  l->group_pages2 = l->group_pages + up(sizeof(int32_t) * (size_t)groups);
+  l->units = l->group_pages2 + up(sizeof(int32_t) * (size_t)groups);
   l->positions = l->units + up(sizeof(int4) * (size_t)units);
   l->work = l->positions + up(sizeof(int) * ((size_t)units + 1));
   l->terms = l->work + up(sizeof(WsHeader));
@@ -639,28 +654,32 @@ mla_status mla_prefix_partial(const void* q, const mla_kv_pages* kv, const int32
   p.own_lens = reinterpret_cast<int32_t*>(ws + l.own_lens);
   p.own_table = reinterpret_cast<int32_t*>(ws + l.own_table);
   p.group_pages = reinterpret_cast<int32_t*>(ws + l.group_pages);
+  p.group_pages2 = reinterpret_cast<int32_t*>(ws + l.group_pages2);
   p.units = reinterpret_cast<int4*>(ws + l.units);
   p.positions = reinterpret_cast<int*>(ws + l.positions);
   p.work = reinterpret_cast<WsHeader*>(ws + l.work);
-  p.err = &reinterpret_cast<WsHeader*>(ws)->err;   // reset by the per-request kernel's plan
+  p.err = &reinterpret_cast<WsHeader*>(ws)->err;   // reset by the planning kernel
   p.ws_o = reinterpret_cast<float*>(ws + l.ws_o);
   p.ws_lse = reinterpret_cast<float*>(ws + l.ws_lse);
   p.out = out_partial;
   p.lse = lse_partial;
   p.timeout_ns = host::wait_budget_ns(kTimeoutNs);
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  if (prefix::launch_prep(p, fp8, pairs, cs) != cudaSuccess) return MLA_ERR_CUDA;
   float* own_out = out_partial + rows * kDv;
   float* own_lse = lse_partial + rows;
   Launched L;
-  const mla_status st =
-      partial_launch(q, kv, p.own_table, max_pages_per_req, p.own_lens, shape, 0, 1,
-                     MLA_LAYOUT_INTERLEAVED, own_out, own_lse, workspace, l.partial_ws, stream, &L);
+  const mla_status st = partial_launch(
+      q, kv, p.own_table, max_pages_per_req, p.own_lens, shape, 0, 1, MLA_LAYOUT_INTERLEAVED,
+      own_out, own_lse, workspace, l.partial_ws, stream, &L, RankIo{0, 1, 0, 0},
+      [&](const ProblemDesc& pd, WsHeader* hdr, int* positions, int grid, int min_tiles,
+          int unit_cost, cudaStream_t s) {
+        return prefix::launch_prep(p, fp8, pairs,
+                                   prefix::OwnPlan{pd, hdr, positions, grid, min_tiles, unit_cost}, s);
+      });
   if (st != MLA_OK) return st;
-  if (launch_merge(L.pd, L.hdr, L.prefix, L.ws_o, L.ws_lse, own_out, own_lse, L.num_units, cs) !=
-          cudaSuccess ||
-      prefix::launch_attend(p, kv->data, fp8, pairs, cs) != cudaSuccess ||
-      prefix::launch_join(p, cs) != cudaSuccess)
+  const prefix::OwnPieces own{L.pd, L.hdr, L.prefix, L.ws_o, L.ws_lse, own_out, own_lse, L.num_units};
+  if (prefix::launch_attend(p, kv->data, fp8, pairs, cs) != cudaSuccess ||
+      prefix::launch_join(p, own, cs) != cudaSuccess)
     return MLA_ERR_CUDA;
   return MLA_OK;
 }

@@ -57,6 +57,7 @@
 #include "prefix.h"
 #include "ptx.cuh"
 #include "qterms.cuh"
+#include "unit_merge.cuh"
 
 namespace mla {
 namespace prefix {
@@ -115,13 +116,41 @@ __device__ __forceinline__ int shared_pages(const Params& p, bool ok, int g, int
   return max(n, 0);
 }
 
-// Block 0: units and their split.  Blocks 1 .. B: a request's own tokens.  The
+// The group of request b: the last one that starts at or before it.
+__device__ __forceinline__ int group_of(const Params& p, bool ok, int b) {
+  int lo = 0, hi = ok ? p.groups - 1 : 0;
+  while (lo < hi) {
+    const int m = (lo + hi + 1) >> 1;
+    if (p.group_starts[m] <= b) lo = m;
+    else hi = m - 1;
+  }
+  return lo;
+}
+
+// All groups' shared pages, a warp each (whole block).
+__device__ __forceinline__ void fill_pages(const Params& p, bool ok, int32_t* pages) {
+  for (int g = threadIdx.x >> 5; g < p.groups; g += kPrepThreads / 32) {
+    int b0, b1;
+    group_range(p, ok, g, b0, b1);
+    const int n = shared_pages(p, ok, g, b0, b1);
+    if ((threadIdx.x & 31) == 0) pages[g] = n;
+  }
+  __syncthreads();
+}
+
+// A context longer than its table is cut at the table's end.
+__device__ __forceinline__ int context(const Params& p, int b) {
+  return (int)min((long long)p.seq_lens[b], (long long)p.max_pages * kPage);
+}
+
+// Block 0: units and their split.  Block 1: the own tokens' lengths, and the
+// per-request kernel's plan.  Blocks 2 .. B + 1: a request's own pages.  The
 // others (e4m3): a query row per warp.
-__global__ void __launch_bounds__(kPrepThreads) prefix_prep_kernel(Params p, int pairs) {
+__global__ void __launch_bounds__(kPrepThreads) prefix_prep_kernel(Params p, OwnPlan own, int pairs) {
   griddep_wait();
   griddep_launch_dependents();
-  if (blockIdx.x > (unsigned)p.B) {
-    const int row = ((int)blockIdx.x - 1 - p.B) * (kPrepThreads / 32) + (threadIdx.x >> 5);
+  if (blockIdx.x > (unsigned)p.B + 1) {
+    const int row = ((int)blockIdx.x - 2 - p.B) * (kPrepThreads / 32) + (threadIdx.x >> 5);
     if (row >= p.B * p.R) return;
     const int b = row / p.R;
     split_query_row(p.q + (size_t)row * kDqk, row - b * p.R < queries(p, b) * p.H,
@@ -129,31 +158,34 @@ __global__ void __launch_bounds__(kPrepThreads) prefix_prep_kernel(Params p, int
     return;
   }
   const bool ok = groups_ok(p);
-  if (blockIdx.x > 0) {
-    const int b = (int)blockIdx.x - 1;
-    // its group: the last one that starts at or before it
-    int lo = 0, hi = p.groups - 1;
-    while (ok && lo < hi) {
-      const int m = (lo + hi + 1) >> 1;
-      if (p.group_starts[m] <= b) lo = m;
-      else hi = m - 1;
-    }
-    int b0, b1;
-    group_range(p, ok, lo, b0, b1);
+  if (blockIdx.x > 1) {
+    const int b = (int)blockIdx.x - 2;
     __shared__ int shared_n;
     if (threadIdx.x < 32) {
-      const int n = shared_pages(p, ok, lo, b0, b1);
+      const int g = group_of(p, ok, b);
+      int b0, b1;
+      group_range(p, ok, g, b0, b1);
+      const int n = shared_pages(p, ok, g, b0, b1);
       if (threadIdx.x == 0) shared_n = n;
     }
     __syncthreads();
-    const int n = shared_n;
-    // a context longer than its table is cut at the table's end
-    const int L = (int)min((long long)p.seq_lens[b], (long long)p.max_pages * kPage);
-    if (threadIdx.x == 0) p.own_lens[b] = L - n * kPage;
+    const int n = shared_n, live = ceil_div(max(context(p, b), 0), kPage) - n;
     const int32_t* from = p.block_table + (size_t)b * p.max_pages + n;
     int32_t* to = p.own_table + (size_t)b * p.max_pages;
-    const int live = ceil_div(max(L, 0), kPage) - n;
     for (int i = threadIdx.x; i < live; i += kPrepThreads) to[i] = from[i];
+    return;
+  }
+  if (blockIdx.x == 1) {
+    bool good = true;
+    fill_pages(p, ok, p.group_pages2);
+    for (int b = threadIdx.x; b < p.B; b += kPrepThreads) {
+      p.own_lens[b] = context(p, b) - p.group_pages2[group_of(p, ok, b)] * kPage;
+      good &= p.q_lens == nullptr || (p.q_lens[b] >= 1 && p.q_lens[b] <= p.q_len);
+    }
+    good = __syncthreads_and(good) != 0;
+    plan_units(own.pd.B * own.pd.n_out * own.pd.G,
+               [&](int u) { return make_unit(own.pd, u).tiles; }, own.hdr, own.positions, own.grid,
+               own.min_tiles, own.unit_cost, good ? 0u : kErrQLens);
     return;
   }
   __shared__ int part[kPrepThreads];
@@ -162,12 +194,7 @@ __global__ void __launch_bounds__(kPrepThreads) prefix_prep_kernel(Params p, int
   for (int b = tid; b < p.B; b += kPrepThreads)
     fits &= p.seq_lens[b] <= (long long)p.max_pages * kPage;
   const unsigned bad = (ok ? 0u : kErrQLens) | (__syncthreads_and(fits) ? 0u : kErrBadPage);
-  for (int g = tid >> 5; g < p.groups; g += kPrepThreads / 32) {
-    int b0, b1;
-    group_range(p, ok, g, b0, b1);
-    const int n = shared_pages(p, ok, g, b0, b1);
-    if ((tid & 31) == 0) p.group_pages[g] = n;
-  }
+  fill_pages(p, ok, p.group_pages);
   const int per = ceil_div(p.groups, kPrepThreads), g0 = min(p.groups, tid * per);
   const int g1 = min(p.groups, g0 + per);
   auto tiles_of_rows = [&](int g) {
@@ -869,7 +896,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ------------------------------------------------------------ joining pieces
-struct UnitPieces {
+struct PairPieces {
   const float* ws_o;
   const float* ws_lse;
   struct Ctx {
@@ -885,18 +912,27 @@ struct UnitPieces {
 
 constexpr int kJoinRows = 2, kJoinBatch = 12;
 constexpr int kJoinSmem = 8 * kJoinBatch * 32 * (int)sizeof(float4);
+static_assert(kJoinSmem >= kMergeSmem, "either kind of block");
 
-// Rows of units that no pair computed whole: without a shared page 0 and -inf,
-// else the LSE join of their pieces.  Four warps per row, 128 dims each.
-__global__ void __launch_bounds__(256, 4) prefix_join_kernel(Params p) {
+// Blocks of the shared pages' units: rows that no pair computed whole, without a
+// shared page 0 and -inf, else the LSE join of their pieces, four warps per row
+// of 128 dims each.  The blocks behind them: the same of the own tokens' units.
+__global__ void __launch_bounds__(256, 4) prefix_join_kernel(Params p, OwnPieces own) {
   extern __shared__ __align__(16) float4 join_stage[];
   griddep_wait();
   griddep_launch_dependents();
-  const int u = blockIdx.x;
-  if (u == 0 && blockIdx.y == 0 && threadIdx.x == 0 && p.work->err != 0) atomicOr(p.err, p.work->err);
+  constexpr int kBlocks = kPairRows / kJoinRows, kOwnBlocks = kRows / kMergeRowsPerBlock;
+  const int i = blockIdx.x - p.max_units * kBlocks;
+  if (i >= 0) {
+    merge_unit_rows(own.pd, own.hdr, own.positions, own.ws_o, own.ws_lse, own.out, own.lse,
+                    i / kOwnBlocks, i % kOwnBlocks, join_stage);
+    return;
+  }
+  const int u = blockIdx.x / kBlocks, y = blockIdx.x % kBlocks;
+  if (blockIdx.x == 0 && threadIdx.x == 0 && p.work->err != 0) atomicOr(p.err, p.work->err);
   const int4 x = p.units[u];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int r = blockIdx.y * kJoinRows + (warp >> 2), part = warp & 3;
+  const int r = y * kJoinRows + (warp >> 2), part = warp & 3;
   const int gr = x.x + r;
   if (gr >= x.y) return;
   const int ps = p.positions[u], ue = p.positions[u + 1];
@@ -913,8 +949,8 @@ __global__ void __launch_bounds__(256, 4) prefix_join_kernel(Params p) {
     return;
   }
   const int c0 = us / per, c1 = (ue - 1) / per;
-  const UnitPieces src{p.ws_o, p.ws_lse};
-  const UnitPieces::Ctx ctx{c0, c1 - c0 + 1, r, c0 * per < ps ? 1 : 0};
+  const PairPieces src{p.ws_o, p.ws_lse};
+  const PairPieces::Ctx ctx{c0, c1 - c0 + 1, r, c0 * per < ps ? 1 : 0};
   float4 acc[1];
   float M, wsum;
   merge_pieces_staged<1, kJoinBatch>(src, ctx, lane, 32 * part, join_stage + warp * (kJoinBatch * 32),
@@ -1004,34 +1040,36 @@ int max_pairs() {
   return std::min(n, 256);
 }
 
-cudaError_t launch_prep(const Params& p, bool fp8, int pairs, cudaStream_t stream) {
+cudaError_t launch_prep(const Params& p, bool fp8, int pairs, const OwnPlan& own,
+                        cudaStream_t stream) {
   cudaLaunchAttribute attr = pdl_attribute();
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(1 + p.B + (fp8 ? ceil_div(p.B * p.R, kPrepThreads / 32) : 0));
+  cfg.gridDim = dim3(2 + p.B + (fp8 ? ceil_div(p.B * p.R, kPrepThreads / 32) : 0));
   cfg.blockDim = dim3(kPrepThreads);
   cfg.stream = stream;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, prefix_prep_kernel, p, pairs);
+  return cudaLaunchKernelEx(&cfg, prefix_prep_kernel, p, own, pairs);
 }
 
 cudaError_t launch_attend(const Params& p, const void* kv, bool fp8, int pairs, cudaStream_t stream) {
   return fp8 ? attend<true>(p, kv, pairs, stream) : attend<false>(p, kv, pairs, stream);
 }
 
-cudaError_t launch_join(const Params& p, cudaStream_t stream) {
+cudaError_t launch_join(const Params& p, const OwnPieces& own, cudaStream_t stream) {
   const cudaError_t e =
       host::ensure_dynamic_smem(reinterpret_cast<const void*>(&prefix_join_kernel), kJoinSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr = pdl_attribute();
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.max_units, kPairRows / kJoinRows);
+  cfg.gridDim = dim3(p.max_units * (kPairRows / kJoinRows) +
+                     own.num_units * (kRows / kMergeRowsPerBlock));
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = kJoinSmem;
   cfg.stream = stream;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, prefix_join_kernel, p);
+  return cudaLaunchKernelEx(&cfg, prefix_join_kernel, p, own);
 }
 
 }  // namespace prefix

@@ -25,6 +25,7 @@ struct Params {
   int32_t* own_lens;             // [B] tokens behind the shared pages
   int32_t* own_table;            // [B, max_pages] their pages
   int32_t* group_pages;          // [groups] their shared pages
+  int32_t* group_pages2;         // the same, for the plan of the own tokens
   int4* units;                   // [max_units] first row, end row, table row, shared pages
   int* positions;                // [max_units + 1] work positions before each unit
   WsHeader* work;                // the work list's header
@@ -36,10 +37,29 @@ struct Params {
   unsigned long long timeout_ns;
 };
 
+// The per-request kernel's work over the own tokens: its plan, and what it
+// leaves in pieces.
+struct OwnPlan {
+  ProblemDesc pd;
+  WsHeader* hdr;
+  int* positions;
+  int grid, min_tiles, unit_cost;
+};
+struct OwnPieces {
+  ProblemDesc pd;
+  const WsHeader* hdr;
+  const int* positions;
+  const float* ws_o;
+  const float* ws_lse;
+  float* out;
+  float* lse;
+  int num_units;
+};
+
 int max_pairs();                 // CTA pairs that can run at once; 0 on an error
-cudaError_t launch_prep(const Params& p, bool fp8, int pairs, cudaStream_t stream);
+cudaError_t launch_prep(const Params& p, bool fp8, int pairs, const OwnPlan& own, cudaStream_t stream);
 cudaError_t launch_attend(const Params& p, const void* kv, bool fp8, int pairs, cudaStream_t stream);
-cudaError_t launch_join(const Params& p, cudaStream_t stream);
+cudaError_t launch_join(const Params& p, const OwnPieces& own, cudaStream_t stream);
 
 }  // namespace prefix
 }  // namespace mla
