@@ -283,8 +283,8 @@ struct Walk {
   int g;                         // tiles before this one
   bool whole, first;             // the piece is the whole unit; its first tile
   int slot;
-  __device__ void init(const Params& p, int lo, int hi) {
-    it.init(p.positions, p.work->num_units, lo, hi, p.work->unit_cost);
+  __device__ void init(const Params& p, int lo, int hi, int lane) {   // whole warp
+    it.init_warp(p.positions, p.work->num_units, lo, hi, p.work->unit_cost, lane);
     units = p.units;
     j = t1 = 0;
     g = -1;
@@ -424,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
 
   Walk w;
-  w.init(p, lo, hi);
+  w.init(p, lo, hi, lane);
   bool ok = true;
 
   if (warp == 0) {
@@ -741,9 +741,17 @@ __global__ void __launch_bounds__(kThreads, 1)
               ls[e] += u;
               pv[e] = u * sg[e];
             }
-            const uint32_t s01 = split_e4m3x2(pv[0], pv[1]), s23 = split_e4m3x2(pv[2], pv[3]);
-            hi4[i4] = (s01 & 0xFFFFu) | (s23 << 16);
-            lo4[i4] = (s01 >> 16) | (s23 & 0xFFFF0000u);
+            // two-term sums: hi to 4 significant bits in integers (converting the
+            // code back takes three conversions a pair, at an eighth of the
+            // rate), lo what is left.  Below 2^-6, where codes are multiples of
+            // 2^-9, the sum is off by 2^-9 at most -- 2^-17 of the row's largest.
+            float hi[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              hi[e] = __uint_as_float((__float_as_uint(pv[e]) + 0x80000u) & 0xFFF00000u);
+            hi4[i4] = f32x2_to_e4m3x2(hi[0], hi[1]) | (f32x2_to_e4m3x2(hi[2], hi[3]) << 16);
+            lo4[i4] = f32x2_to_e4m3x2(pv[0] - hi[0], pv[1] - hi[1]) |
+                      (f32x2_to_e4m3x2(pv[2] - hi[2], pv[3] - hi[3]) << 16);
           }
           if (ok && ga >= 0) ok = pv_of(ga);
           if (ok) {
@@ -806,6 +814,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const size_t at = w.whole ? (size_t)gr
                                 : ((size_t)2 * pair + w.slot) * kPairRows + rank * kHalf + r;
       float* const orow = (w.whole ? p.out : p.ws_o) + at * kDv + 128 * part;
+      const bool wide = (reinterpret_cast<uintptr_t>(orow) & 31u) == 0;
       // pieces of split units: the join writes rows without a query
       const bool store = w.whole ? mine : live;
       const float inv = (live && l != 0.0f) ? 1.0f / l : 0.0f;            // or NaN
@@ -815,12 +824,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto put = [&](int c, const uint32_t (&v)[32]) {
         if (!store) return;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (live)
-            x = make_float4(__uint_as_float(v[4 * i]) * inv, __uint_as_float(v[4 * i + 1]) * inv,
-                            __uint_as_float(v[4 * i + 2]) * inv, __uint_as_float(v[4 * i + 3]) * inv);
-          reinterpret_cast<float4*>(orow + c)[i] = x;
+        for (int i = 0; i < 4; ++i) {
+          float x[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] = live ? __uint_as_float(v[8 * i + e]) * inv : 0.0f;
+          float* const to = orow + c + 8 * i;
+          if (wide) {
+            // a sector a lane: the lanes' rows are 2 KB apart
+            st_global_8(to, x);
+          } else {
+            reinterpret_cast<float4*>(to)[0] = make_float4(x[0], x[1], x[2], x[3]);
+            reinterpret_cast<float4*>(to)[1] = make_float4(x[4], x[5], x[6], x[7]);
+          }
         }
       };
       {
