@@ -248,12 +248,12 @@ struct Misc {
   uint64_t full[kStages][4];     // leader: loads of both CTAs landed
   uint64_t a_free[kStages];      // P V has read A
   uint64_t pv_done[kStages];     // P V has read everything
-  uint64_t s_full[2];            // both S issuers
+  uint64_t s_full[2];            // both S issuers; e4m3: the tile's scales
   uint64_t k_read[kStages];      // S is done: V goes over half of K
   uint64_t s_empty[2], p_full[2], o_free;   // leader: the softmax warps of both
   uint64_t q_full, q_empty;
   uint64_t drain;
-  uint64_t sc_full[kFp8 ? kStages : 1], sc_ready[kFp8 ? kStages : 1];
+  uint64_t sc_full[kFp8 ? kStages : 1];
   uint32_t tmem_base;
   int abort;
   uint32_t armed[kStages][4];    // loads announced on full, for a teardown
@@ -383,11 +383,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&misc->pv_done[s]), 1);
       if (kFp8) {
         mbar_init(smem_u32(&misc->sc_full[s]), 1);
-        mbar_init(smem_u32(&misc->sc_ready[s]), 1);
       }
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&misc->s_full[i]), 2);
+      mbar_init(smem_u32(&misc->s_full[i]), kFp8 ? 3 : 2);
       mbar_init(smem_u32(&misc->s_empty[i]), 2 * kSoftmaxWarps);
       mbar_init(smem_u32(&misc->p_full[i]), 2 * kSoftmaxWarps);
     }
@@ -512,7 +511,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           misc->lge[s][a] = eb >= 253u ? 0.0f : (float)((int)eb - 126);
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&misc->sc_ready[s]));
+        // (S of the tile before is done, so the phase of two tiles before has
+        // ended: this arrival counts for this tile)
+        if (lane == 0) mbar_arrive(smem_u32(&misc->s_full[w.g & 1]));
       }
       if (lane == 0) {
         int page[2];
@@ -639,12 +640,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (live && f != f) atomicOr(p.err, kErrQRange);
         qs *= f;
       }
+      const f32x2 qs2 = pack2(qs, qs);                     // logits in log2 units
       float m_run = -CUDART_INF_F, l_run = 0.0f;           // l_run: this thread's tokens
       while (true) {
         const int s = w.g % kStages, sb = w.g & 1;
         ok = ok && wait(&misc->s_full[sb], (w.g >> 1) & 1);
-        if (kFp8) ok = ok && wait(&misc->sc_ready[s], (w.g / kStages) & 1);
-        float a[32];
+        f32x2 a[16];             // bf16: S; e4m3: S sigma
         float mx = -CUDART_INF_F;
         // the last tile of an odd number of pages has no second page
         const bool there = 2 * w.j + half < w.u.w;
@@ -660,30 +661,29 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_ld16(s0 + 64 + 16 * h, u);
             tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              a[16 * h + i] = __uint_as_float(v[16 * h + i]) + __uint_as_float(u[i]);
+            for (int i = 0; i < 8; ++i) {
+              const int k = 16 * h + 2 * i;
+              a[8 * h + i] = add2(pack2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])),
+                                  pack2(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1])));
+            }
           }
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_pair(at_leader(&misc->s_empty[sb]));
           float m4[4] = {mx, mx, mx, mx};
 #pragma unroll
-          for (int i4 = 0; i4 < 8; ++i4) {
-            float sg[4], eg[4];
+          for (int i = 0; i < 16; ++i) {
+            f32x2 b = a[i];
             if (kFp8) {
-              const float4 x = *reinterpret_cast<const float4*>(&misc->sigma[s][32 * part + 4 * i4]);
-              const float4 y = *reinterpret_cast<const float4*>(&misc->lge[s][32 * part + 4 * i4]);
-              sg[0] = x.x, sg[1] = x.y, sg[2] = x.z, sg[3] = x.w;
-              eg[0] = y.x, eg[1] = y.y, eg[2] = y.z, eg[3] = y.w;
+              // b_t = S sigma qs + E_t
+              const int t = 32 * part + 2 * i;
+              a[i] = mul2(a[i], *reinterpret_cast<const f32x2*>(&misc->sigma[s][t]));
+              b = fma2(a[i], qs2, *reinterpret_cast<const f32x2*>(&misc->lge[s][t]));
             }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int i = 4 * i4 + e;
-              if (kFp8) a[i] = a[i] * sg[e] * qs;
-              m4[e] = fmaxf(m4[e], kFp8 ? a[i] + eg[e] : a[i]);
-            }
+            const float2 y = unpack2(b);
+            m4[i & 3] = max3(m4[i & 3], y.x, y.y);
           }
-          mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+          mx = max3(fmaxf(m4[0], m4[1]), m4[2], m4[3]);
           if (!kFp8) mx *= p.scale_log2;
           if (!there) mx = -CUDART_INF_F;
           misc->xmax[sb][part][r] = mx;
@@ -727,31 +727,34 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_wait_st();
           }
         }
-        float ls[4] = {0.f, 0.f, 0.f, 0.f};
+        const f32x2 m2 = pack2(-m_use, -m_use);
+        f32x2 ls[2] = {0, 0};
         if (kFp8) {
+          // two-term sums of P' = u sigma: hi to 4 significant bits in integers
+          // (converting a code back takes three conversions a pair, at an eighth
+          // of the rate; a product and two differences are fused into hi = P'),
+          // lo what is left.  Below 2^-6, where codes are multiples of 2^-9, the
+          // sum is off by 2^-9 at most -- 2^-17 of the row's largest.
           uint32_t hi4[8], lo4[8];
 #pragma unroll
-          for (int i4 = 0; i4 < 8; ++i4) {
-            const float4 x = *reinterpret_cast<const float4*>(&misc->sigma[s][32 * part + 4 * i4]);
-            const float sg[4] = {x.x, x.y, x.z, x.w};
-            float pv[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float u = ex2_approx(a[4 * i4 + e] - m_use);
-              ls[e] += u;
-              pv[e] = u * sg[e];
+          for (int i = 0; i < 16; ++i) {
+            const float2 x = unpack2(fma2(a[i], qs2, m2));
+            const f32x2 u = pack2(ex2_approx(x.x), ex2_approx(x.y));
+            ls[i & 1] = add2(ls[i & 1], u);
+            const f32x2 pv = mul2(u, *reinterpret_cast<const f32x2*>(&misc->sigma[s][32 * part + 2 * i]));
+            const float2 y = unpack2(pv);
+            const float2 h =
+                make_float2(__uint_as_float((__float_as_uint(y.x) + 0x80000u) & 0xFFF00000u),
+                            __uint_as_float((__float_as_uint(y.y) + 0x80000u) & 0xFFF00000u));
+            const float2 l = unpack2(sub2(pv, pack2(h.x, h.y)));
+            const uint32_t ch = f32x2_to_e4m3x2(h.x, h.y), cl = f32x2_to_e4m3x2(l.x, l.y);
+            if (i % 2 == 0) {
+              hi4[i / 2] = ch;
+              lo4[i / 2] = cl;
+            } else {
+              hi4[i / 2] |= ch << 16;
+              lo4[i / 2] |= cl << 16;
             }
-            // two-term sums: hi to 4 significant bits in integers (converting the
-            // code back takes three conversions a pair, at an eighth of the
-            // rate), lo what is left.  Below 2^-6, where codes are multiples of
-            // 2^-9, the sum is off by 2^-9 at most -- 2^-17 of the row's largest.
-            float hi[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              hi[e] = __uint_as_float((__float_as_uint(pv[e]) + 0x80000u) & 0xFFF00000u);
-            hi4[i4] = f32x2_to_e4m3x2(hi[0], hi[1]) | (f32x2_to_e4m3x2(hi[2], hi[3]) << 16);
-            lo4[i4] = f32x2_to_e4m3x2(pv[0] - hi[0], pv[1] - hi[1]) |
-                      (f32x2_to_e4m3x2(pv[2] - hi[2], pv[3] - hi[3]) << 16);
           }
           if (ok && ga >= 0) ok = pv_of(ga);
           if (ok) {
@@ -773,10 +776,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < 16; ++i) {
             // bf16: P is rounded to 8 bits, relative 2^-9, as in the
             // per-request kernel; its sum is taken before the rounding
-            const float x = ex2_approx(fmaf(a[2 * i], p.scale_log2, -m_use));
-            const float y = ex2_approx(fmaf(a[2 * i + 1], p.scale_log2, -m_use));
-            pk[i] = pack_bf16(x, y);
-            ls[i & 3] += x + y;
+            const float2 x = unpack2(fma2(a[i], qs2, m2));
+            const float2 u = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+            pk[i] = pack_bf16(u.x, u.y);
+            ls[i & 1] = add2(ls[i & 1], pack2(u.x, u.y));
           }
           // tokens 0-63 go into the stage's rope chunk, which S has read;
           // tokens 64-127 into the one chunk that every tile uses
@@ -790,7 +793,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                   make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
           }
         }
-        l_run += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+        const float2 lt = unpack2(add2(ls[0], ls[1]));
+        l_run += lt.x + lt.y;
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
