@@ -428,7 +428,7 @@ StepLayout step_layout(const mla_shape* shape, int num_shards) {
 // own tokens' lengths and tables, the units and their split, the query's terms
 // (e4m3) and the pieces of split units.
 struct PrefixLayout {
-  size_t partial_ws, own_lens, own_table, group_pages, group_pages2, units, positions, work, terms, inv_scale, ws_o, ws_lse, total;
+  size_t partial_ws, own_lens, own_table, group_pages, units, positions, work, terms, inv_scale, ws_o, ws_lse, total;
   int max_units;
 };
 
@@ -448,8 +448,7 @@ bool prefix_layout(const mla_shape* s, int groups, int max_pages, bool fp8, int 
   l->own_lens = l->partial_ws;
   l->own_table = l->own_lens + up(sizeof(int32_t) * (size_t)s->batch);
   l->group_pages = l->own_table + up(sizeof(int32_t) * (size_t)s->batch * max_pages);
-  l->group_pages2 = l->group_pages + up(sizeof(int32_t) * (size_t)groups);
-  l->units = l->group_pages2 + up(sizeof(int32_t) * (size_t)groups);
+  l->units = l->group_pages + up(sizeof(int32_t) * (size_t)groups);
   l->positions = l->units + up(sizeof(int4) * (size_t)units);
   l->work = l->positions + up(sizeof(int) * ((size_t)units + 1));
   l->terms = l->work + up(sizeof(WsHeader));
@@ -654,7 +653,6 @@ mla_status mla_prefix_partial(const void* q, const mla_kv_pages* kv, const int32
   p.own_lens = reinterpret_cast<int32_t*>(ws + l.own_lens);
   p.own_table = reinterpret_cast<int32_t*>(ws + l.own_table);
   p.group_pages = reinterpret_cast<int32_t*>(ws + l.group_pages);
-  p.group_pages2 = reinterpret_cast<int32_t*>(ws + l.group_pages2);
   p.units = reinterpret_cast<int4*>(ws + l.units);
   p.positions = reinterpret_cast<int*>(ws + l.positions);
   p.work = reinterpret_cast<WsHeader*>(ws + l.work);
@@ -678,7 +676,9 @@ mla_status mla_prefix_partial(const void* q, const mla_kv_pages* kv, const int32
       });
   if (st != MLA_OK) return st;
   const prefix::OwnPieces own{L.pd, L.hdr, L.prefix, L.ws_o, L.ws_lse, own_out, own_lse, L.num_units};
-  if (prefix::launch_attend(p, kv->data, fp8, pairs, cs) != cudaSuccess ||
+  // (a batch of at most 64 rows has no group that shares pages)
+  if ((rows > (size_t)kRows &&
+       prefix::launch_attend(p, kv->data, fp8, pairs, cs) != cudaSuccess) ||
       prefix::launch_join(p, own, cs) != cudaSuccess)
     return MLA_ERR_CUDA;
   return MLA_OK;

@@ -218,32 +218,47 @@ struct PieceIter {
 template <class TilesFn>
 __device__ void plan_units(int U, TilesFn tiles_of, WsHeader* hdr, int* prefix, int grid,
                            int min_tiles, int unit_cost, unsigned err_bits) {
-  __shared__ int part[1024];
-  const int tid = threadIdx.x;
+  __shared__ int part[32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per_thread = ceil_div(U, 1024);
-  const int u0 = tid * per_thread, u1 = min(U, u0 + per_thread);
+  const int u0 = min(U, tid * per_thread), u1 = min(U, u0 + per_thread);
   auto cost = [&](int u) {
     const int t = tiles_of(u);
     return t > 0 ? t + unit_cost : 0;
   };
-  int sum = 0;
-  for (int u = u0; u < u1; ++u) sum += cost(u);
-  part[tid] = sum;
-  __syncthreads();
-  // inclusive Hillis-Steele scan of the 1024 partial sums
-  for (int off = 1; off < 1024; off <<= 1) {
-    int v = tid >= off ? part[tid - off] : 0;
-    __syncthreads();
-    part[tid] += v;
-    __syncthreads();
+  // the first unit's cost is kept (most often the thread has no other): its
+  // tiles take a few loads
+  const int first = u0 < u1 ? cost(u0) : 0;
+  int sum = first;
+  for (int u = u0 + 1; u < u1; ++u) sum += cost(u);
+  // inclusive scan: within the warp, then over the warps' sums
+  int run = sum;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, run, off);
+    if (lane >= off) run += v;
   }
-  int run = part[tid] - sum;  // exclusive
+  if (lane == 31) part[warp] = run;
+  __syncthreads();
+  if (warp == 0) {
+    int v = part[lane];
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, v, off);
+      if (lane >= off) v += o;
+    }
+    part[lane] = v;
+  }
+  __syncthreads();
+  if (warp > 0) run += part[warp - 1];
+  const int total = part[31];
+  run -= sum;                    // exclusive
   for (int u = u0; u < u1; ++u) {
     prefix[u] = run;
-    run += cost(u);
+    run += u == u0 ? first : cost(u);
   }
   if (tid == 1023) {
-    const int W = part[1023];
+    const int W = total;
     prefix[U] = W;
     hdr->err = err_bits;
     hdr->total_cost = W;

@@ -37,6 +37,7 @@ namespace evict {
 constexpr int kBins = 2048;
 constexpr int kCopyThreads = 256;
 constexpr int kHold = 16;             // weights per thread in registers
+constexpr int kList = 96;             // undecided weights per warp that are listed
 
 struct Select {
   const int32_t* seq_lens;
@@ -92,6 +93,7 @@ struct Shared {
   uint32_t gt[kWarps], eq[kWarps];    // per warp's slice: keys above, equal to T
   uint32_t total_gt, total_eq;        // the CTA's
   uint32_t bin[3], above[3];          // the descent's choices
+  uint32_t list[kWarps][kList];       // keys with the first chosen digit, in order
 };
 
 // C: CTAs per request (a cluster of them).
@@ -158,6 +160,19 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(Select p) {
   };
   if (held) load(wa);
 
+  uint32_t sure = 0, listed = 0;              // above the first digit; sharing it
+  const uint32_t below = (1u << lane) - 1;
+  // f(key, whether there is one) for the weights that share the first digit,
+  // from the list or, if they are too many for it, from all of the slice
+  auto undecided = [&](auto&& f) {
+    if (listed <= kList) {
+      for (uint32_t i0 = 0; i0 < listed; i0 += 32)
+        f(i0 + lane < listed ? sm.list[warp][i0 + lane] : 0u, i0 + lane < listed);
+    } else {
+      each([&](uint32_t x, int i) { f(x, i < wz && (x >> 21) == sm.bin[0]); });
+    }
+  };
+
   for (int i = tid; i < 3 * kBins; i += kThreads) (&sm.total[0][0])[i] = 0;
   uint32_t match = 0, left = (uint32_t)k;     // digits so far; still to take below them
   int upper = 32;
@@ -176,13 +191,30 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(Select p) {
     // enough digits (an exponent has four) for atomics of their own.  Grouping
     // equal digits first took 2.5 times as long on a long-tailed row.
     uint32_t zeros = 0;
-    each([&](uint32_t x, int i) {
-      // upper = 32 on the first pass: everything matches
-      const bool in = i < wz && (upper >= 32 || (x >> upper) == match);
+    auto count = [&](uint32_t x, bool in) {
       const bool zero = in && x == kZero;
       zeros += __popc(__ballot_sync(0xFFFFFFFFu, zero));
       if (in && !zero) atomicAdd(&hist[(x >> shift) & mask], 1u);
-    });
+    };
+    if (pass == 0) {
+      each([&](uint32_t x, int i) { count(x, i < wz); });
+    } else if (pass == 1) {
+      // the weights above the first digit are kept; those that share it are
+      // listed, so that later passes read only them (two of five reads less)
+      each([&](uint32_t x, int i) {
+        const bool in = i < wz && (x >> upper) == match;
+        sure += __popc(__ballot_sync(0xFFFFFFFFu, i < wz && (x >> upper) > match));
+        const uint32_t m = __ballot_sync(0xFFFFFFFFu, in);
+        if (m == 0) return;
+        const uint32_t at = listed + __popc(m & below);
+        if (in && at < kList) sm.list[warp][at] = x;
+        listed += __popc(m);
+        count(x, in);
+      });
+      __syncwarp();
+    } else {
+      undecided([&](uint32_t x, bool in) { count(x, in && (x >> upper) == match); });
+    }
     if (lane == 0 && zeros != 0) atomicAdd(&hist[(kZero >> shift) & mask], zeros);
     __syncthreads();
     if (C > 1) {
@@ -226,10 +258,10 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(Select p) {
   const uint32_t T = match;      // the k-th largest key; `left` of its equals stay
 
   // each warp's slice, in order
-  uint32_t gt = 0, eq = 0;
-  each([&](uint32_t x, int i) {
-    gt += __popc(__ballot_sync(0xFFFFFFFFu, i < wz && x > T));
-    eq += __popc(__ballot_sync(0xFFFFFFFFu, i < wz && x == T));
+  uint32_t gt = sure, eq = 0;
+  undecided([&](uint32_t x, bool in) {
+    gt += __popc(__ballot_sync(0xFFFFFFFFu, in && x > T));
+    eq += __popc(__ballot_sync(0xFFFFFFFFu, in && x == T));
   });
   if (lane == 0) {
     sm.gt[warp] = gt;
@@ -250,7 +282,6 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(Select p) {
     gt0 += *cluster.map_shared_rank(&sm.total_gt, r);
     eq0 += *cluster.map_shared_rank(&sm.total_eq, r);
   }
-  const uint32_t below = (1u << lane) - 1;
   each([&](uint32_t x, int i) {
     const uint32_t mg = __ballot_sync(0xFFFFFFFFu, i < wz && x > T);
     const uint32_t me = __ballot_sync(0xFFFFFFFFu, i < wz && x == T);

@@ -116,24 +116,23 @@ __device__ __forceinline__ int shared_pages(const Params& p, bool ok, int g, int
   return max(n, 0);
 }
 
-// The group of request b: the last one that starts at or before it.
-__device__ __forceinline__ int group_of(const Params& p, bool ok, int b) {
-  int lo = 0, hi = ok ? p.groups - 1 : 0;
-  while (lo < hi) {
-    const int m = (lo + hi + 1) >> 1;
-    if (p.group_starts[m] <= b) lo = m;
-    else hi = m - 1;
-  }
-  return lo;
+// The group of request b (whole block).
+__device__ __forceinline__ int group_of(const Params& p, bool ok, int b, int* found) {
+  if (threadIdx.x == 0) *found = 0;
+  __syncthreads();
+  for (int g = threadIdx.x; ok && g < p.groups; g += kPrepThreads)
+    if (p.group_starts[g] <= b && b < p.group_starts[g + 1]) *found = g;
+  __syncthreads();
+  return *found;
 }
 
-// All groups' shared pages, a warp each (whole block).
-__device__ __forceinline__ void fill_pages(const Params& p, bool ok, int32_t* pages) {
+// f(group, its requests, its shared pages) for every group, a warp each.
+template <class F>
+__device__ __forceinline__ void each_group(const Params& p, bool ok, F&& f) {
   for (int g = threadIdx.x >> 5; g < p.groups; g += kPrepThreads / 32) {
     int b0, b1;
     group_range(p, ok, g, b0, b1);
-    const int n = shared_pages(p, ok, g, b0, b1);
-    if ((threadIdx.x & 31) == 0) pages[g] = n;
+    f(g, b0, b1, shared_pages(p, ok, g, b0, b1));
   }
   __syncthreads();
 }
@@ -160,9 +159,9 @@ __global__ void __launch_bounds__(kPrepThreads) prefix_prep_kernel(Params p, Own
   const bool ok = groups_ok(p);
   if (blockIdx.x > 1) {
     const int b = (int)blockIdx.x - 2;
-    __shared__ int shared_n;
+    __shared__ int found, shared_n;
+    const int g = group_of(p, ok, b, &found);
     if (threadIdx.x < 32) {
-      const int g = group_of(p, ok, b);
       int b0, b1;
       group_range(p, ok, g, b0, b1);
       const int n = shared_pages(p, ok, g, b0, b1);
@@ -177,11 +176,12 @@ __global__ void __launch_bounds__(kPrepThreads) prefix_prep_kernel(Params p, Own
   }
   if (blockIdx.x == 1) {
     bool good = true;
-    fill_pages(p, ok, p.group_pages2);
-    for (int b = threadIdx.x; b < p.B; b += kPrepThreads) {
-      p.own_lens[b] = context(p, b) - p.group_pages2[group_of(p, ok, b)] * kPage;
+    for (int b = threadIdx.x; b < p.B; b += kPrepThreads)
       good &= p.q_lens == nullptr || (p.q_lens[b] >= 1 && p.q_lens[b] <= p.q_len);
-    }
+    each_group(p, ok, [&](int, int b0, int b1, int n) {
+      for (int b = b0 + (int)(threadIdx.x & 31); b < b1; b += 32)
+        p.own_lens[b] = context(p, b) - n * kPage;
+    });
     good = __syncthreads_and(good) != 0;
     plan_units(own.pd.B * own.pd.n_out * own.pd.G,
                [&](int u) { return make_unit(own.pd, u).tiles; }, own.hdr, own.positions, own.grid,
@@ -194,7 +194,9 @@ __global__ void __launch_bounds__(kPrepThreads) prefix_prep_kernel(Params p, Own
   for (int b = tid; b < p.B; b += kPrepThreads)
     fits &= p.seq_lens[b] <= (long long)p.max_pages * kPage;
   const unsigned bad = (ok ? 0u : kErrQLens) | (__syncthreads_and(fits) ? 0u : kErrBadPage);
-  fill_pages(p, ok, p.group_pages);
+  each_group(p, ok, [&](int g, int, int, int n) {
+    if ((tid & 31) == 0) p.group_pages[g] = n;
+  });
   const int per = ceil_div(p.groups, kPrepThreads), g0 = min(p.groups, tid * per);
   const int g1 = min(p.groups, g0 + per);
   auto tiles_of_rows = [&](int g) {

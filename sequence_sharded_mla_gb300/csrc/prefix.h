@@ -25,7 +25,6 @@ struct Params {
   int32_t* own_lens;             // [B] tokens behind the shared pages
   int32_t* own_table;            // [B, max_pages] their pages
   int32_t* group_pages;          // [groups] their shared pages
-  int32_t* group_pages2;         // the same, for the plan of the own tokens
   int4* units;                   // [max_units] first row, end row, table row, shared pages
   int* positions;                // [max_units + 1] work positions before each unit
   WsHeader* work;                // the work list's header

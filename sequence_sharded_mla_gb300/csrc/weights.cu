@@ -12,9 +12,10 @@
 // the rows, so the sum over rows stays inside a thread (fixed order, nothing
 // to exchange) and every thread ends with one token's weight.
 //
-//   warp 0      K producer: per tile three groups of three 64-dim chunks (two
-//               pages, one TMA box each) into a ring of three (bf16) or six
-//               (e4m3)
+//   warp 0      K producer, two pages a tile, by TMA: bf16, three boxes of three
+//               64-dim chunks a page into a ring of three; e4m3, whole pages (in
+//               192-byte pieces of the 576-byte rows a million tokens took 119
+//               instead of 105 us) into two tiles
 //   warp 1      MMA issue
 //   warps 2..5  one token a thread: exp2 of every column, summed
 //   warp 6      Q producer: a group's nine chunks.  A request of one group of
@@ -45,7 +46,7 @@ namespace weights {
 
 constexpr int kThreads = 224;
 constexpr int kTokens = 128;               // tokens per tile: MMA M
-constexpr int kMaxDepth = 6;
+constexpr int kMaxDepth = 3;
 constexpr uint32_t kBarSum = 1;            // named barrier of the summing warps
 constexpr int kSumThreads = 128;
 constexpr uint32_t kTmemCols = 512;        // two accumulators of up to 256 columns
@@ -131,11 +132,12 @@ template <bool kFp8, int kRowsN>
 struct Cfg {
   static constexpr int kN = kFp8 ? 2 * kRowsN : kRowsN;
   static constexpr int kLine = kFp8 ? 64 : 128;            // bytes of a chunk's row
-  // a slot of K: [16 groups of 8 tokens][3 chunks][8 tokens][64 dims]
-  static constexpr int kKGroup = kCgChunks * 8 * kLine;
-  static constexpr int kKBytes = kTokens / 8 * kKGroup;    // 24 or 48 KB
+  // a slot of K: [16 groups of 8 tokens][kCg chunks][8 tokens][64 dims]
+  static constexpr int kCg = kFp8 ? kChunks : 3;
+  static constexpr int kKGroup = kCg * 8 * kLine;
+  static constexpr int kKBytes = kTokens / 8 * kKGroup;    // 72 or 48 KB
   static constexpr int kQBytes = kN * kLine;               // Q chunk: 8 or 16 KB
-  static constexpr int kKDepth = kFp8 ? 6 : 3;
+  static constexpr int kKDepth = kFp8 ? 2 : 3;
   static constexpr int kQDepth = kRowsN == 64 ? 9 : 4;
   static constexpr int kSmemQ = kKDepth * kKBytes;
   static constexpr int kSmemMisc = kSmemQ + kQDepth * kQBytes;
@@ -253,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             e[h] = i < npages ? __ldg(bt + i) : -1;
           }
 #pragma unroll
-          for (int c = 0; c < kChunks / kCgChunks; ++c, ++armed) {
+          for (int c = 0; c < kChunks / C::kCg; ++c, ++armed) {
             const int s = armed % C::kKDepth, use = armed / C::kKDepth;
             if (use > 0) ok = wait(&misc->ke[s], (use - 1) & 1);
             if (!ok) break;
@@ -262,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int h = 0; h < 2; ++h)
               tma_load_4d(sK + s * C::kKBytes + h * (C::kKBytes / 2), &tm_k, bar, 0, 0,
-                          kCgChunks * c, group[h]);
+                          C::kCg * c, group[h]);
           }
         }
       }
@@ -288,8 +290,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 1) {
     // ----------------------------------------------------------- MMA issue
     if (lane == 0) {
-      constexpr uint32_t id = kFp8 ? idesc_e4m3_f32(kTokens, C::kN, false, false)
-                                   : idesc_bf16_f32(kTokens, C::kN, false, false);
       constexpr uint32_t kQGroup = 8 * C::kLine;           // eight rows
       constexpr int kSteps = kFp8 ? 2 : 4;                 // 32-byte steps of a chunk
       const uint64_t dk0 = kFp8 ? sw64_desc(sK, 16, C::kKGroup) : sw128_desc(sK, 16, C::kKGroup);
@@ -301,14 +301,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int buf = nd & 1;
             if (nd >= 2) ok = wait(&misc->de[buf], ((nd >> 1) - 1) & 1);
             const uint32_t d = tmem + 256 * buf;
+            // columns of the group's rows: the last of five groups of a 576-row
+            // step has half
+            const int cols = min(kRowsN, rows - g * kRowsN) * (kFp8 ? 2 : 1);
+            const uint32_t id = kFp8 ? idesc_e4m3_f32(kTokens, cols, false, false)
+                                     : idesc_bf16_f32(kTokens, cols, false, false);
 #pragma unroll 1
-            for (int cg = 0; ok && cg < kChunks / kCgChunks; ++cg) {
+            for (int cg = 0; ok && cg < kChunks / C::kCg; ++cg) {
               const int ks = (nk + cg) % C::kKDepth;
               if (g == 0) ok = wait(&misc->kf[ks], ((nk + cg) / C::kKDepth) & 1);
               const uint64_t dk = dk0 + ((ks * C::kKBytes) >> 4);
 #pragma unroll
-              for (int c = 0; c < kCgChunks; ++c) {
-                const int i = nq + cg * kCgChunks + c, qs = i % C::kQDepth;
+              for (int c = 0; c < C::kCg; ++c) {
+                const int i = nq + cg * C::kCg + c, qs = i % C::kQDepth;
                 if (ok && (!stay || t == t0)) ok = wait(&misc->qf[qs], (i / C::kQDepth) & 1);
                 if (!ok) break;
                 tc_fence_after();
@@ -327,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (ok) mma_commit(smem_u32(&misc->df[buf]));
             if (!stay) nq += kChunks;
           }
-          nk += kChunks / kCgChunks;
+          nk += kChunks / C::kCg;
         }
         if (stay) nq += kChunks;
       }
@@ -494,7 +499,7 @@ mla_status run(const Params& p, const void* kv, int grid, cudaStream_t st) {
   // cache: (64 dims, row of 8, chunk, 8-row group); query: (dim, row)
   const cuuint64_t kd[4] = {64, 8, (cuuint64_t)kChunks, (cuuint64_t)p.num_pages * (kPage / 8)};
   const cuuint64_t ks[3] = {kDqk * e, 64 * e, 8 * kDqk * e};
-  const cuuint32_t kb[4] = {64, 8, (cuuint32_t)kCgChunks, (cuuint32_t)(kPage / 8)};
+  const cuuint32_t kb[4] = {64, 8, (cuuint32_t)C::kCg, (cuuint32_t)(kPage / 8)};
   const cuuint64_t qd[2] = {(cuuint64_t)kDqk, rows}, qs[1] = {kDqk * e};
   const cuuint32_t qb[2] = {64, (cuuint32_t)C::kN};
   if (!encode(&tm_k, kFp8, kv, 4, kd, ks, kb) || !encode(&tm_q, kFp8, q, 2, qd, qs, qb))
