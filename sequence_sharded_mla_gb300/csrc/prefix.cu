@@ -674,16 +674,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) mbar_arrive_pair(at_leader(&misc->s_empty[sb]));
           float m4[4] = {mx, mx, mx, mx};
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            f32x2 b = a[i];
+          for (int i = 0; i < 16; i += 2) {
+            f32x2 b0 = a[i], b1 = a[i + 1];
             if (kFp8) {
               // b_t = S sigma qs + E_t
               const int t = 32 * part + 2 * i;
-              a[i] = mul2(a[i], *reinterpret_cast<const f32x2*>(&misc->sigma[s][t]));
-              b = fma2(a[i], qs2, *reinterpret_cast<const f32x2*>(&misc->lge[s][t]));
+              const ulonglong2 sg = *reinterpret_cast<const ulonglong2*>(&misc->sigma[s][t]);
+              const ulonglong2 eg = *reinterpret_cast<const ulonglong2*>(&misc->lge[s][t]);
+              a[i] = mul2(a[i], sg.x);
+              a[i + 1] = mul2(a[i + 1], sg.y);
+              b0 = fma2(a[i], qs2, eg.x);
+              b1 = fma2(a[i + 1], qs2, eg.y);
             }
-            const float2 y = unpack2(b);
-            m4[i & 3] = max3(m4[i & 3], y.x, y.y);
+            const float2 y0 = unpack2(b0), y1 = unpack2(b1);
+            m4[i & 2] = max3(m4[i & 2], y0.x, y0.y);
+            m4[(i & 2) + 1] = max3(m4[(i & 2) + 1], y1.x, y1.y);
           }
           mx = max3(fmaxf(m4[0], m4[1]), m4[2], m4[3]);
           if (!kFp8) mx *= p.scale_log2;
@@ -737,13 +742,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           // of the rate; a product and two differences are fused into hi = P'),
           // lo what is left.  Below 2^-6, where codes are multiples of 2^-9, the
           // sum is off by 2^-9 at most -- 2^-17 of the row's largest.
+          ulonglong2 sg;
           uint32_t hi4[8], lo4[8];
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             const float2 x = unpack2(fma2(a[i], qs2, m2));
             const f32x2 u = pack2(ex2_approx(x.x), ex2_approx(x.y));
             ls[i & 1] = add2(ls[i & 1], u);
-            const f32x2 pv = mul2(u, *reinterpret_cast<const f32x2*>(&misc->sigma[s][32 * part + 2 * i]));
+            if (i % 2 == 0)
+              sg = *reinterpret_cast<const ulonglong2*>(&misc->sigma[s][32 * part + 2 * i]);
+            const f32x2 pv = mul2(u, i % 2 == 0 ? sg.x : sg.y);
             const float2 y = unpack2(pv);
             const float2 h =
                 make_float2(__uint_as_float((__float_as_uint(y.x) + 0x80000u) & 0xFFF00000u),
