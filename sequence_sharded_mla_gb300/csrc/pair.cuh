@@ -38,6 +38,20 @@ __device__ __forceinline__ void st_cluster(uint32_t addr, uint32_t v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
+// What is left of mbar_wait() after a first probe that failed; a function of its
+// own, off the path of the loops that wait (whose instructions a warp fetches
+// anew every round).
+__device__ __noinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity, uint64_t limit_ns,
+                                            volatile int* abort) {
+  if (mbar_try_wait_hint(bar, parity, 200000u)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (true) {
+    if (mbar_try_wait_hint(bar, parity, 200000u)) return true;
+    if (*abort) return false;
+    if (globaltimer_ns() - t0 > limit_ns) return false;
+  }
+}
+
 // Arrivals on a barrier of either CTA (a map_rank address).  What they order is
 // this CTA's shared and tensor memory for its own asynchronous units (behind a
 // proxy or tcgen05 fence), which the CTA's scope covers; a release of cluster

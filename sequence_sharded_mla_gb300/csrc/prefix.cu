@@ -343,20 +343,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const bool leader = rank == 0;
-  griddep_wait();                // the work list, the query's terms
-  griddep_launch_dependents();
-
-  const int W = p.work->total_cost, per = p.work->per_cta;
-  const int pair = (int)blockIdx.x >> 1;
-  const int lo = (int)min((long long)W, (long long)pair * per);
-  if (lo >= W) return;           // both CTAs of the pair
-  const int hi = (int)min((long long)W, (long long)lo + per);
-
-  if ((smem_u32(smem) & 1023u) != 0) {   // never: its alignment is declared
-    if (threadIdx.x == 0) atomicOr(p.err, kErrTimeout);
-    return;
-  }
-
   volatile int* abort_flag = &misc->abort;
   const uint64_t tmo = p.timeout_ns;
   const uint32_t peer_abort = map_rank(smem_u32(&misc->abort), rank ^ 1);
@@ -367,7 +353,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   // one thread's wait, and a warp's
   auto wait1 = [&](uint64_t* bar, uint32_t parity) {
-    return mbar_wait(smem_u32(bar), parity, tmo, abort_flag);
+    return mbar_try_wait_hint(smem_u32(bar), parity, 200000u) ||
+           mbar_wait_long(smem_u32(bar), parity, tmo, abort_flag);
   };
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     return __all_sync(0xffffffffu, wait1(bar, parity)) != 0;
@@ -410,6 +397,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   cluster_sync_all();            // the peer's barriers and tensor memory are there
   tc_fence_after();
+  griddep_wait();                // the work list, the query's terms
+  griddep_launch_dependents();
+  // (a pair without work falls through to the teardown; so would every pair if
+  // the declared alignment of shared memory did not hold)
+  const bool aligned = (smem_u32(smem) & 1023u) == 0;
+  if (!aligned && threadIdx.x == 0) atomicOr(p.err, kErrTimeout);
+  const int W = aligned ? p.work->total_cost : 0, per = p.work->per_cta;
+  const int pair = (int)blockIdx.x >> 1;
+  const int lo = (int)min((long long)W, (long long)pair * per);
+  const int hi = (int)min((long long)W, (long long)lo + per);
   const uint32_t tmem = misc->tmem_base;
   const uint32_t sQ = smem_u32(smem), sKV = smem_u32(smem + C::kSmemKV);
   const uint32_t sP = smem_u32(smem + C::kSmemP);
@@ -556,18 +553,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t d = tmem + kColS + 128 * sb + 64 * i;
         const uint64_t dk = desc(sKV + s * C::kTile + (kFp8 ? 0 : 64 * i), 16);
 #pragma unroll
-        for (int part = 0; part < 3; ++part) {
-          if (ok) ok = wait1(&misc->full[s][part], (w.g / kStages) & 1);
-          if (!ok) break;
-          tc_fence_after();
+        for (int c = 0; c < kChunks; ++c) {
+          if ((c & 3) == 0) {    // a part's first chunk
+            ok = ok && wait1(&misc->full[s][c >> 2], (w.g / kStages) & 1);
+            if (!ok) break;
+            tc_fence_after();
+          }
 #pragma unroll
-          for (int c = 4 * part; c < (part == kC ? 9 : 4 * part + 4); ++c) {
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const uint32_t acc = (c > 0 || k > 0) ? 1u : 0u, o = (c * C::kSlot + 32 * k) >> 4;
-              if (kFp8) mma_e4m3_pair(d, dq + o, dk + o, id, acc);
-              else mma_bf16_pair(d, dq + o, dk + o, id, acc);
-            }
+          for (int k = 0; k < 2; ++k) {
+            const uint32_t acc = (c > 0 || k > 0) ? 1u : 0u;
+            const uint64_t o = (uint32_t)(c * C::kSlot + 32 * k) >> 4;
+            if (kFp8) mma_e4m3_pair(d, dq + o, dk + o, id, acc);
+            else mma_bf16_pair(d, dq + o, dk + o, id, acc);
           }
         }
         if (!ok) break;
@@ -597,7 +594,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t dp0 = kFp8 ? desc(sP + (w.g & 1) * 4 * C::kSlot, 16)
                                   : desc(sKV + s * C::kTile + 8 * C::kSlot, 16);
         const uint64_t dp1 = kFp8 ? dp0 + (C::kSlot >> 4) : desc(sP, 16);
-#pragma unroll
+        // (rolled: unrolled, the e4m3 kernel waits for instructions, 171 instead
+        // of 161 us over nine prefixes)
+#pragma unroll 1
         for (int half = 0; half < 2; ++half) {             // tokens 64 half ..
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
