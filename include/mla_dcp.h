@@ -569,10 +569,11 @@ size_t mla_prefix_workspace_size(const mla_shape* shape, int num_groups, int max
  *   out_partial fp32 [2, B, q_len, H, 512], lse_partial fp32 [2, B, q_len, H]
  * which mla_shard_combine (num_shards 2, with or without w_uv) turns into the
  * attention of every request over its whole context.  Slice 0 is over shared
- * pages, slice 1 over the rest; what falls into which is the library's choice:
- * whole pages of a prefix that every row of the group sees are shared, a group
- * of at most 64 rows (requests x q_len x H) shares none, and one whose
- * prefix_lens is below a page, 0 or negative neither.
+ * pages, slice 1 over the rest.  What falls into which is the library's choice,
+ * made on the device from the lengths: whole pages of a prefix that every row of
+ * the group sees are shared where that takes less time than attending them per
+ * request (mla_set_prefix_sharing); prefix_lens below a page, 0 or negative share
+ * nothing.
  *
  *   block_table, seq_lens, shape (q_lens, causal)  as in mla_decode_partial:
  *                 whole contexts, the prefix among them
@@ -595,6 +596,14 @@ mla_status mla_prefix_partial(const void* q, const mla_kv_pages* kv, const int32
                               const int32_t* prefix_lens, int num_groups, float* out_partial,
                               float* lse_partial, void* workspace, size_t workspace_bytes,
                               void* stream);
+
+/*
+ * Testing aid (not part of the method): while `always` is non-zero,
+ * mla_prefix_partial calls made from now on share all the pages that can be
+ * shared, also where attending them per request is faster (process-wide).  0
+ * turns it off.  Always MLA_OK.
+ */
+mla_status mla_set_prefix_sharing(int always);
 
 /* Workspace bytes mla_attention_weights needs (0 for invalid shapes). */
 size_t mla_attention_weights_workspace_size(const mla_shape* shape, mla_kv_dtype dtype);

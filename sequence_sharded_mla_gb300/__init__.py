@@ -86,7 +86,7 @@ EXPORTS = ("mla_decode_partial", "mla_decode_partial_noalloc", "mla_decode_parti
            "mla_rope_apply", "mla_cache_append", "gqa_cache_append", "gqa_fp8_workspace_size",
            "gqa_decode_partial_fp8", "mla_cache_evict",
            "mla_attention_weights", "mla_attention_weights_workspace_size", "mla_prefix_partial",
-           "mla_prefix_workspace_size")
+           "mla_prefix_workspace_size", "mla_set_prefix_sharing")
 
 
 def lib():
@@ -166,6 +166,8 @@ def lib():
         L.mla_prefix_partial.argtypes = [vp, ptr(mla_kv_pages), vp, i32, vp, ptr(mla_shape), vp, vp, i32,
                                          vp, vp, vp, sz, vp]
         L.mla_prefix_partial.restype = i32
+        L.mla_set_prefix_sharing.argtypes = [i32]
+        L.mla_set_prefix_sharing.restype = i32
         L.mla_prefix_workspace_size.argtypes = [ptr(mla_shape), i32, i32, i32]
         L.mla_prefix_workspace_size.restype = sz
         _LIB = L
@@ -749,12 +751,19 @@ def mla_prefix_partial(q, kv, block_table, seq_lens, group_starts, prefix_lens, 
     for mla_decode_partial, the contexts whole.  group_starts: int32 [G + 1]
     (device), group g is requests group_starts[g] .. group_starts[g + 1] - 1;
     prefix_lens: int32 [G] (device), the leading tokens that the group's
-    contexts have in common, in the same pages of their block-table rows.
+    contexts have in common, in the same pages of their block-table rows.  Which
+    of them are shared (slice 0) is chosen on the device from the lengths.
     out_partial: fp32 [2, B, q_len, H, 512]; lse_partial: fp32 [2, B, q_len, H].
     """
     return _binding().prefix_partial(q, kv, kv_scale, block_table, seq_lens, group_starts, prefix_lens,
                                      causal, softmax_scale, out_partial, lse_partial, workspace, stream,
                                      q_lens)
+
+
+def mla_set_prefix_sharing(always: bool) -> None:
+    """Testing aid: while on, mla_prefix_partial shares all the pages that can
+    be shared, also where attending them per request is faster."""
+    lib().mla_set_prefix_sharing(int(bool(always)))
 
 
 # ----------------------------------------------------- weights and eviction

@@ -428,7 +428,7 @@ StepLayout step_layout(const mla_shape* shape, int num_shards) {
 // own tokens' lengths and tables, the units and their split, the query's terms
 // (e4m3) and the pieces of split units.
 struct PrefixLayout {
-  size_t partial_ws, own_lens, own_table, group_pages, units, positions, work, terms, inv_scale, ws_o, ws_lse, total;
+  size_t partial_ws, own_lens, own_table, group_info, members, units, runs, where, positions, work, terms, inv_scale, ws_o, ws_lse, total;
   int max_units;
 };
 
@@ -441,15 +441,18 @@ bool prefix_layout(const mla_shape* s, int groups, int max_pages, bool fp8, int 
   // work positions, and the joining kernel's blocks
   const long long own = (long long)s->batch * ceil_div(s->q_len * s->num_heads, kRows);
   if (units * (max_pages / 2 + 8LL) >= (1LL << 31) ||
-      units * (prefix::kPairRows / 2) + own * (kRows / 2) >= (1LL << 31))
+      (long long)rows / 2 + own * (kRows / 2) >= (1LL << 31))
     return false;
   l->max_units = (int)units;
   l->partial_ws = up(mla_workspace_size(s, 1, 0));
   l->own_lens = l->partial_ws;
   l->own_table = l->own_lens + up(sizeof(int32_t) * (size_t)s->batch);
-  l->group_pages = l->own_table + up(sizeof(int32_t) * (size_t)s->batch * max_pages);
-  l->units = l->group_pages + up(sizeof(int32_t) * (size_t)groups);
-  l->positions = l->units + up(sizeof(int4) * (size_t)units);
+  l->group_info = l->own_table + up(sizeof(int32_t) * (size_t)s->batch * max_pages);
+  l->members = l->group_info + up(sizeof(int2) * 2 * (size_t)groups);
+  l->units = l->members + up(sizeof(int2) * (size_t)s->batch);
+  l->runs = l->units + up(sizeof(int4) * (size_t)units);
+  l->where = l->runs + up(sizeof(int32_t) * 8 * (size_t)units);
+  l->positions = l->where + up(sizeof(int32_t) * (rows / 16));
   l->work = l->positions + up(sizeof(int) * ((size_t)units + 1));
   l->terms = l->work + up(sizeof(WsHeader));
   l->inv_scale = l->terms + (fp8 ? up(rows * 2 * kDqk) : 0);
@@ -652,7 +655,10 @@ mla_status mla_prefix_partial(const void* q, const mla_kv_pages* kv, const int32
   p.inv_scale = reinterpret_cast<float*>(ws + l.inv_scale);
   p.own_lens = reinterpret_cast<int32_t*>(ws + l.own_lens);
   p.own_table = reinterpret_cast<int32_t*>(ws + l.own_table);
-  p.group_pages = reinterpret_cast<int32_t*>(ws + l.group_pages);
+  p.group_info = reinterpret_cast<int2*>(ws + l.group_info);
+  p.members = reinterpret_cast<int2*>(ws + l.members);
+  p.runs = reinterpret_cast<int32_t*>(ws + l.runs);
+  p.where = reinterpret_cast<int32_t*>(ws + l.where);
   p.units = reinterpret_cast<int4*>(ws + l.units);
   p.positions = reinterpret_cast<int*>(ws + l.positions);
   p.work = reinterpret_cast<WsHeader*>(ws + l.work);
@@ -662,6 +668,7 @@ mla_status mla_prefix_partial(const void* q, const mla_kv_pages* kv, const int32
   p.out = out_partial;
   p.lse = lse_partial;
   p.timeout_ns = host::wait_budget_ns(kTimeoutNs);
+  p.always = host::g_share_always.load();
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   float* own_out = out_partial + rows * kDv;
   float* own_lse = lse_partial + rows;
@@ -676,8 +683,8 @@ mla_status mla_prefix_partial(const void* q, const mla_kv_pages* kv, const int32
       });
   if (st != MLA_OK) return st;
   const prefix::OwnPieces own{L.pd, L.hdr, L.prefix, L.ws_o, L.ws_lse, own_out, own_lse, L.num_units};
-  // (a batch of at most 64 rows has no group that shares pages)
-  if ((rows > (size_t)kRows &&
+  // (a batch of at most 64 rows gains nothing)
+  if (((rows > (size_t)kRows || p.always) &&
        prefix::launch_attend(p, kv->data, fp8, pairs, cs) != cudaSuccess) ||
       prefix::launch_join(p, own, cs) != cudaSuccess)
     return MLA_ERR_CUDA;
@@ -693,6 +700,11 @@ mla_status mla_set_profile_events(void* before_partial, void* after_partial) {
 
 mla_status mla_set_wait_budget_ns(unsigned long long ns) {
   host::g_wait_budget_ns.store(ns);
+  return MLA_OK;
+}
+
+mla_status mla_set_prefix_sharing(int always) {
+  host::g_share_always.store(always != 0 ? 1 : 0);
   return MLA_OK;
 }
 

@@ -58,6 +58,10 @@ inline unsigned long long wait_budget_ns(unsigned long long dflt) {
 // for them can only run out.
 inline std::atomic<int> g_withhold_query{0};
 
+// Testing aid (mla_set_prefix_sharing): while non-zero, mla_prefix_partial shares
+// whatever can be shared.
+inline std::atomic<int> g_share_always{0};
+
 // Unique id of the CUDA context current on the calling thread (the device's
 // primary context for runtime users), made current first if none is.  Ids
 // are never reused within a process, so per-context state keyed on them

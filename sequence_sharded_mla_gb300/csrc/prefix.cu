@@ -101,40 +101,64 @@ __device__ __forceinline__ void group_range(const Params& p, bool ok, int g, int
   b1 = max(b0, b1);
 }
 
-// Whole shared pages of group g that every query row of it sees (whole warp).  A
-// group of at most 64 rows has none: the per-request kernel reads its pages
-// once already.
-__device__ __forceinline__ int shared_pages(const Params& p, bool ok, int g, int b0, int b1) {
-  if (!ok || (long long)(b1 - b0) * p.R <= kRows) return 0;
-  int n = min(p.prefix_lens[g] / kPage, p.max_pages);
+// What a group would share.
+struct Group {
+  int pages;                     // whole pages that every query row of it sees
+  int runs;                      // its query rows, in runs of 16, padding rows apart
+  int units;                     // 64-row units of the per-request kernel
+};
+
+// (whole warp)
+__device__ __forceinline__ Group measure(const Params& p, bool ok, int g, int b0, int b1) {
+  Group x{ok ? min(p.prefix_lens[g] / kPage, p.max_pages) : 0, 0, 0};
   for (int b = b0 + (int)(threadIdx.x & 31); b < b1; b += 32) {
-    const int L = p.seq_lens[b], seen = p.causal ? L - queries(p, b) + 1 : L;
-    n = min(n, seen / kPage);
+    const int L = p.seq_lens[b], n = queries(p, b), seen = p.causal ? L - n + 1 : L;
+    x.pages = min(x.pages, seen / kPage);
+    x.runs += n * p.H / 16;
+    x.units += ceil_div(n * p.H, kRows);
   }
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) n = min(n, __shfl_xor_sync(0xFFFFFFFFu, n, off));
-  return max(n, 0);
+  for (int off = 16; off > 0; off >>= 1) {
+    x.pages = min(x.pages, __shfl_xor_sync(0xFFFFFFFFu, x.pages, off));
+    x.runs += __shfl_xor_sync(0xFFFFFFFFu, x.runs, off);
+    x.units += __shfl_xor_sync(0xFFFFFFFFu, x.units, off);
+  }
+  x.pages = max(x.pages, 0);
+  return x;
 }
 
-// The group of request b (whole block).
-__device__ __forceinline__ int group_of(const Params& p, bool ok, int b, int* found) {
-  if (threadIdx.x == 0) *found = 0;
-  __syncthreads();
-  for (int g = threadIdx.x; ok && g < p.groups; g += kPrepThreads)
-    if (p.group_starts[g] <= b && b < p.group_starts[g + 1]) *found = g;
-  __syncthreads();
-  return *found;
+// Nanoseconds that a group's sharing saves: the per-request kernel takes 10 ns
+// for every unit and page (a 64 x 64 tile, over all SMs), this one 25 ns for
+// every 128 rows and two pages.  A launch with shared pages costs 12 us more.
+// (Measured with the combine, bf16, 64 heads, one token, 500 own tokens:
+//   4 requests behind 16384 tokens 54 us shared, 47 not; behind 65536 86 and 85;
+//   8 behind 4096 47 and 38, 16384 56 and 54, 65536 107 and 134;
+//   32 behind 4096 69 and 63, 16384 108 and 126, 65536 263 and 368;
+//   e4m3 32 behind 65536 229 and 367.)
+constexpr long long kMinGain = 12000;
+__device__ __forceinline__ long long gain_of(const Group& x) {
+  return 10LL * x.units * x.pages - 25LL * ((x.runs + 7) / 8) * ((x.pages + 1) / 2);
 }
 
-// f(group, its requests, its shared pages) for every group, a warp each.
+// f(group, its requests, what it would share) for every group, a warp each; true
+// if the batch is to share at all (whole block).  A group that gains nothing is
+// handed on without pages.
 template <class F>
-__device__ __forceinline__ void each_group(const Params& p, bool ok, F&& f) {
+__device__ __forceinline__ bool survey(const Params& p, bool ok, F&& f) {
+  __shared__ unsigned long long gain;
+  if (threadIdx.x == 0) gain = 0;
+  __syncthreads();
   for (int g = threadIdx.x >> 5; g < p.groups; g += kPrepThreads / 32) {
     int b0, b1;
     group_range(p, ok, g, b0, b1);
-    f(g, b0, b1, shared_pages(p, ok, g, b0, b1));
+    Group x = measure(p, ok, g, b0, b1);
+    const long long n = gain_of(x);
+    if (n <= 0 && !p.always) x.pages = 0;
+    else if (n > 0 && (threadIdx.x & 31) == 0) atomicAdd(&gain, (unsigned long long)n);
+    f(g, b0, b1, x);
   }
   __syncthreads();
+  return p.always || gain > (unsigned long long)kMinGain;
 }
 
 // A context longer than its table is cut at the table's end.
@@ -157,73 +181,107 @@ __global__ void __launch_bounds__(kPrepThreads) prefix_prep_kernel(Params p, Own
     return;
   }
   const bool ok = groups_ok(p);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (blockIdx.x > 1) {
     const int b = (int)blockIdx.x - 2;
-    __shared__ int found, shared_n;
-    const int g = group_of(p, ok, b, &found);
-    if (threadIdx.x < 32) {
-      int b0, b1;
-      group_range(p, ok, g, b0, b1);
-      const int n = shared_pages(p, ok, g, b0, b1);
-      if (threadIdx.x == 0) shared_n = n;
-    }
-    __syncthreads();
-    const int n = shared_n, live = ceil_div(max(context(p, b), 0), kPage) - n;
+    __shared__ int pages;
+    const bool share = survey(p, ok, [&](int, int b0, int b1, const Group& x) {
+      if (lane == 0 && b0 <= b && b < b1) pages = x.pages;
+    });
+    const int n = share ? pages : 0, live = ceil_div(max(context(p, b), 0), kPage) - n;
     const int32_t* from = p.block_table + (size_t)b * p.max_pages + n;
     int32_t* to = p.own_table + (size_t)b * p.max_pages;
-    for (int i = threadIdx.x; i < live; i += kPrepThreads) to[i] = from[i];
+    for (int i = tid; i < live; i += kPrepThreads) to[i] = from[i];
     return;
   }
+  int2* const info = p.group_info + (size_t)blockIdx.x * p.groups;
   if (blockIdx.x == 1) {
     bool good = true;
-    for (int b = threadIdx.x; b < p.B; b += kPrepThreads)
+    for (int b = tid; b < p.B; b += kPrepThreads)
       good &= p.q_lens == nullptr || (p.q_lens[b] >= 1 && p.q_lens[b] <= p.q_len);
-    each_group(p, ok, [&](int, int b0, int b1, int n) {
-      for (int b = b0 + (int)(threadIdx.x & 31); b < b1; b += 32)
-        p.own_lens[b] = context(p, b) - n * kPage;
+    const bool share = survey(p, ok, [&](int g, int, int, const Group& x) {
+      if (lane == 0) info[g].x = x.pages;
     });
+    for (int g = warp; g < p.groups; g += kPrepThreads / 32) {
+      int b0, b1;
+      group_range(p, ok, g, b0, b1);
+      const int n = share ? info[g].x : 0;
+      for (int b = b0 + lane; b < b1; b += 32) p.own_lens[b] = context(p, b) - n * kPage;
+    }
     good = __syncthreads_and(good) != 0;
     plan_units(own.pd.B * own.pd.n_out * own.pd.G,
                [&](int u) { return make_unit(own.pd, u).tiles; }, own.hdr, own.positions, own.grid,
                own.min_tiles, own.unit_cost, good ? 0u : kErrQLens);
     return;
   }
-  __shared__ int part[kPrepThreads];
-  const int tid = threadIdx.x;
   bool fits = true;
   for (int b = tid; b < p.B; b += kPrepThreads)
     fits &= p.seq_lens[b] <= (long long)p.max_pages * kPage;
   const unsigned bad = (ok ? 0u : kErrQLens) | (__syncthreads_and(fits) ? 0u : kErrBadPage);
-  each_group(p, ok, [&](int g, int, int, int n) {
-    if ((tid & 31) == 0) p.group_pages[g] = n;
+  const bool share = survey(p, ok, [&](int g, int, int, const Group& x) {
+    if (lane == 0) info[g] = make_int2(x.pages, (x.runs + 7) / 8);
   });
+  // first units of the groups that share: a scan over the groups
+  __shared__ int sums[32];
   const int per = ceil_div(p.groups, kPrepThreads), g0 = min(p.groups, tid * per);
   const int g1 = min(p.groups, g0 + per);
-  auto tiles_of_rows = [&](int g) {
-    int b0, b1;
-    group_range(p, ok, g, b0, b1);
-    return (int)(((long long)(b1 - b0) * p.R + kPairRows - 1) / kPairRows);
-  };
+  auto units_of = [&](int g) { return share && info[g].x > 0 ? info[g].y : 0; };
   int sum = 0;
-  for (int g = g0; g < g1; ++g) sum += tiles_of_rows(g);
-  part[tid] = sum;
+  for (int g = g0; g < g1; ++g) sum += units_of(g);
+  int run = sum;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int v = __shfl_up_sync(0xFFFFFFFFu, run, off);
+    if (lane >= off) run += v;
+  }
+  if (lane == 31) sums[warp] = run;
   __syncthreads();
-  for (int off = 1; off < kPrepThreads; off <<= 1) {
-    const int v = tid >= off ? part[tid - off] : 0;
-    __syncthreads();
-    part[tid] += v;
-    __syncthreads();
+  int total = 0;
+  run -= sum;
+  for (int v = 0; v < kPrepThreads / 32; ++v) {
+    if (v < warp) run += sums[v];
+    total += sums[v];
   }
-  int u = part[tid] - sum;
   for (int g = g0; g < g1; ++g) {
-    int b0, b1;
-    group_range(p, ok, g, b0, b1);
-    const int n = p.group_pages[g];
-    for (int r = b0 * p.R; r < b1 * p.R; r += kPairRows) p.units[u++] = make_int4(r, b1 * p.R, b0, n);
+    const int n = units_of(g);
+    info[g].y = n > 0 ? run : -1;
+    run += n;
   }
-  const int total = part[kPrepThreads - 1];
   for (int v = total + tid; v < p.max_units; v += kPrepThreads) p.units[v] = make_int4(0, 0, 0, 0);
   __syncthreads();
+  // a warp per group: its requests' first runs, its units
+  for (int g = warp; g < p.groups; g += kPrepThreads / 32) {
+    int b0, b1;
+    group_range(p, ok, g, b0, b1);
+    const int first = info[g].y, pages = info[g].x;
+    int runs = 0;
+    for (int c = b0; c < b1; c += 32) {
+      const int b = c + lane, n = b < b1 ? queries(p, b) * p.H / 16 : 0;
+      int at = n;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int v = __shfl_up_sync(0xFFFFFFFFu, at, off);
+        if (lane >= off) at += v;
+      }
+      if (b < b1) p.members[b] = make_int2(runs + at - n, first);
+      runs += __shfl_sync(0xFFFFFFFFu, at, 31);
+    }
+    if (first >= 0)
+      for (int u = lane; 8 * u < runs; u += 32)
+        p.units[first + u] = make_int4(min(8, runs - 8 * u), 0, b0, pages);
+  }
+  __syncthreads();
+  // a warp per request: where its rows are
+  const int mine = p.R / 16;
+  for (int b = warp; b < p.B; b += kPrepThreads / 32) {
+    const int2 m = p.members[b];
+    const int live = m.y >= 0 ? queries(p, b) * p.H / 16 : 0;
+    for (int k = lane; k < mine; k += 32) {
+      const int at = k < live ? m.y * 8 + m.x + k : -1;
+      p.where[(size_t)b * mine + k] = at;
+      if (at >= 0) p.runs[at] = b * p.R + 16 * k;
+    }
+  }
   plan_units(p.max_units, [&](int v) { return (p.units[v].w + 1) / 2; }, p.work, p.positions,
              pairs, kMinTiles, kUnitCost, bad);
 }
@@ -238,6 +296,7 @@ struct Cfg {
   static constexpr int kSlot = kHalf * kLine;            // a page's chunk
   static constexpr int kTile = kChunks * kSlot;
   static constexpr int kGroup = 8 * kLine;               // eight rows of a chunk
+  static constexpr int kQGroup = kChunks * kGroup;       // eight query rows: [chunk][8][64]
   static constexpr int kSmemKV = kQBytes;
   static constexpr int kSmemP = kSmemKV + kStages * kTile;
   // bf16: the second half's probabilities; e4m3: two buffers of both terms
@@ -280,7 +339,8 @@ static_assert(smem_bytes<false>() <= 232448 && smem_bytes<true>() <= 232448, "sh
 struct Walk {
   PieceIter it;
   const int4* units;
-  int4 u;                        // the unit: first row, end row, table row, pages
+  int4 u;                        // the unit: runs, -, table row, pages
+  int unit;
   int j, t1;                     // the tile, the piece's end
   int g;                         // tiles before this one
   bool whole, first;             // the piece is the whole unit; its first tile
@@ -294,7 +354,6 @@ struct Walk {
   __device__ bool next() {
     first = ++j >= t1;
     if (first) {
-      int unit;
       if (!it.next(unit, j, t1, whole, slot)) return false;
       u = units[unit];
     }
@@ -471,12 +530,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           misc->armed_q++;
           mbar_arrive_expect_tx_pair(at_leader(&misc->q_full), kQBytes);
-          const int r0 = w.u.x + (int)rank * kHalf;
-          if (kFp8) {
-            tma_load_4d_pair(sQ, &tm_q, at_leader(&misc->q_full), 0, r0, 0, 0);
-            tma_load_4d_pair(sQ + kQBytes / 2, &tm_q, at_leader(&misc->q_full), 0, r0, 0, 1);
-          } else {
-            tma_load_3d_pair(sQ, &tm_q, at_leader(&misc->q_full), 0, r0, 0);
+          // four runs of 16 rows; a run behind the group's last lies behind the
+          // query, where loads give zeros
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int run = 4 * (int)rank + k;
+            const int g8 = (run < w.u.x ? p.runs[8 * w.unit + run] : p.B * p.R) / 8;
+            const uint32_t to = sQ + 2 * k * C::kQGroup, bar = at_leader(&misc->q_full);
+            if (kFp8) {
+              tma_load_5d_pair(to, &tm_q, bar, 0, 0, 0, g8, 0);
+              tma_load_5d_pair(to + kQBytes / 2, &tm_q, bar, 0, 0, 0, g8, 1);
+            } else {
+              tma_load_4d_pair(to, &tm_q, bar, 0, 0, 0, g8);
+            }
           }
           ++pieces;
         }
@@ -538,7 +604,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // bf16: issuer i takes the 16-dim steps 2 i, 2 i + 1 of every chunk; e4m3:
       // the query's term i
       const int i = warp - 1;
-      const uint64_t dq = desc(sQ + i * (kFp8 ? kQBytes / 2 : 64), 16);
+      const uint64_t dq = kFp8 ? sw64_desc(sQ + i * (kQBytes / 2), 16, C::kQGroup)
+                               : sw128_desc(sQ + i * 64, 16, C::kQGroup);
       int pieces = 0;
       Walk n = w;                // the next tile: is this one its piece's last?
       n.next();
@@ -562,9 +629,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             const uint32_t acc = (c > 0 || k > 0) ? 1u : 0u;
-            const uint64_t o = (uint32_t)(c * C::kSlot + 32 * k) >> 4;
-            if (kFp8) mma_e4m3_pair(d, dq + o, dk + o, id, acc);
-            else mma_bf16_pair(d, dq + o, dk + o, id, acc);
+            const uint32_t oq = (c * C::kGroup + 32 * k) >> 4, o = (c * C::kSlot + 32 * k) >> 4;
+            if (kFp8) mma_e4m3_pair(d, dq + oq, dk + o, id, acc);
+            else mma_bf16_pair(d, dq + oq, dk + o, id, acc);
           }
         }
         if (!ok) break;
@@ -628,17 +695,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lanes = (uint32_t)(32 * quad) << 16;
     while (w.next()) {
       // one piece; `w` is at its first tile
-      const int gr = w.u.x + (int)rank * kHalf + r;        // global row
-      const bool mine = gr < w.u.y;
-      bool live = false;
-      if (mine) {
-        const int b = gr / p.R;
-        live = gr - b * p.R < queries(p, b) * p.H;
-      }
+      const int tr = (int)rank * kHalf + r;                // row of the tile
+      const bool live = (tr >> 4) < w.u.x;
+      const int gr = live ? p.runs[8 * w.unit + (tr >> 4)] + (tr & 15) : 0;   // of the query
       float qs = p.scale_log2;
       if (kFp8) {
-        const float f = mine ? p.inv_scale[gr] : 1.0f;
-        if (live && f != f) atomicOr(p.err, kErrQRange);
+        const float f = live ? p.inv_scale[gr] : 1.0f;
+        if (f != f) atomicOr(p.err, kErrQRange);
         qs *= f;
       }
       const f32x2 qs2 = pack2(qs, qs);                     // logits in log2 units
@@ -824,23 +887,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the four sums in one order for all of the row's threads
       const float* ls = &misc->xmax[(w.g & 1) ^ 1][0][r];
       const float l = (ls[0] + ls[kHalf]) + (ls[2 * kHalf] + ls[3 * kHalf]);
-      const size_t at = w.whole ? (size_t)gr
-                                : ((size_t)2 * pair + w.slot) * kPairRows + rank * kHalf + r;
+      const size_t at = w.whole ? (size_t)gr : ((size_t)2 * pair + w.slot) * kPairRows + tr;
       float* const orow = (w.whole ? p.out : p.ws_o) + at * kDv + 128 * part;
       const bool wide = (reinterpret_cast<uintptr_t>(orow) & 31u) == 0;
-      // pieces of split units: the join writes rows without a query
-      const bool store = w.whole ? mine : live;
-      const float inv = (live && l != 0.0f) ? 1.0f / l : 0.0f;            // or NaN
-      if (store && part == 0)
+      const float inv = l != 0.0f ? 1.0f / l : 0.0f;       // or NaN
+      if (live && part == 0)
         (w.whole ? p.lse : p.ws_lse)[at] =
-            live && l != 0.0f ? (m_run + __log2f(l)) * 0.69314718055994530942f : -CUDART_INF_F;
+            l != 0.0f ? (m_run + __log2f(l)) * 0.69314718055994530942f : -CUDART_INF_F;
       auto put = [&](int c, const uint32_t (&v)[32]) {
-        if (!store) return;
+        if (!live) return;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           float x[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = live ? __uint_as_float(v[8 * i + e]) * inv : 0.0f;
+          for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(v[8 * i + e]) * inv;
           float* const to = orow + c + 8 * i;
           if (wide) {
             // a sector a lane: the lanes' rows are 2 KB apart
@@ -942,36 +1002,34 @@ constexpr int kJoinRows = 2, kJoinBatch = 12;
 constexpr int kJoinSmem = 8 * kJoinBatch * 32 * (int)sizeof(float4);
 static_assert(kJoinSmem >= kMergeSmem, "either kind of block");
 
-// Blocks of the shared pages' units: rows that no pair computed whole, without a
-// shared page 0 and -inf, else the LSE join of their pieces, four warps per row
-// of 128 dims each.  The blocks behind them: the same of the own tokens' units.
+// Slice 0, two rows a block: 0 and -inf for rows in no unit, else the LSE join of
+// their pieces unless a pair computed the unit whole; four warps per row of 128
+// dims each.  The blocks behind them: the own tokens' units.
 __global__ void __launch_bounds__(256, 4) prefix_join_kernel(Params p, OwnPieces own) {
   extern __shared__ __align__(16) float4 join_stage[];
   griddep_wait();
   griddep_launch_dependents();
-  constexpr int kBlocks = kPairRows / kJoinRows, kOwnBlocks = kRows / kMergeRowsPerBlock;
-  const int i = blockIdx.x - p.max_units * kBlocks;
+  constexpr int kOwnBlocks = kRows / kMergeRowsPerBlock;
+  const int i = (int)blockIdx.x - p.B * p.R / kJoinRows;
   if (i >= 0) {
     merge_unit_rows(own.pd, own.hdr, own.positions, own.ws_o, own.ws_lse, own.out, own.lse,
                     i / kOwnBlocks, i % kOwnBlocks, join_stage);
     return;
   }
-  const int u = blockIdx.x / kBlocks, y = blockIdx.x % kBlocks;
   if (blockIdx.x == 0 && threadIdx.x == 0 && p.work->err != 0) atomicOr(p.err, p.work->err);
-  const int4 x = p.units[u];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int r = y * kJoinRows + (warp >> 2), part = warp & 3;
-  const int gr = x.x + r;
-  if (gr >= x.y) return;
-  const int ps = p.positions[u], ue = p.positions[u + 1];
-  const int us = unit_tile_start(p.positions, u, p.work->unit_cost);
-  const int per = p.work->per_cta;
-  const int b = gr / p.R;
-  const bool live = gr - b * p.R < queries(p, b) * p.H;
-  const bool split = us < ue && us / per != (ue - 1) / per;
-  if (us < ue && !split) return;               // written by the pair that computed it
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = warp & 3;
+  const int gr = (int)blockIdx.x * kJoinRows + (warp >> 2);
+  const int w = p.where[gr >> 4], u = w >> 3, r = (w & 7) * 16 + (gr & 15);
+  int ps = 0, ue = 0, us = 0, per = 1;
+  if (w >= 0) {
+    ps = p.positions[u];
+    ue = p.positions[u + 1];
+    us = unit_tile_start(p.positions, u, p.work->unit_cost);
+    per = p.work->per_cta;
+    if (us / per == (ue - 1) / per) return;    // written by the pair that computed it
+  }
   float4* dst = reinterpret_cast<float4*>(p.out + (size_t)gr * kDv) + 32 * part;
-  if (us == ue || !live) {
+  if (w < 0) {
     dst[lane] = make_float4(0.f, 0.f, 0.f, 0.f);
     if (part == 0 && lane == 0) p.lse[gr] = -CUDART_INF_F;
     return;
@@ -991,7 +1049,7 @@ __global__ void __launch_bounds__(256, 4) prefix_join_kernel(Params p, OwnPieces
 // ------------------------------------------------------------------ launches
 bool encode(CUtensorMap* m, bool fp8, int rank, const void* base, const cuuint64_t* dims,
             const cuuint64_t* strides, const cuuint32_t* box) {
-  const cuuint32_t es[4] = {1, 1, 1, 1};
+  const cuuint32_t es[5] = {1, 1, 1, 1, 1};
   return host::encode_fn()(m, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
                            rank, const_cast<void*>(base), dims, strides, box, es,
                            CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -1006,18 +1064,12 @@ cudaError_t attend(const Params& p, const void* kv, int pairs, cudaStream_t stre
   const cuuint64_t e = kFp8 ? 1 : 2;
   CUtensorMap tm_q, tm_kv4, tm_kv1;
   bool ok;
-  if (kFp8) {
-    // (64 dims, row, chunk, term) of the terms [rows, 2, 576]
-    const cuuint64_t d[4] = {64, (cuuint64_t)p.B * p.R, (cuuint64_t)kChunks, 2};
-    const cuuint64_t s[3] = {2 * kDqk, 64, kDqk};
-    const cuuint32_t b[4] = {64, (cuuint32_t)kHalf, (cuuint32_t)kChunks, 1};
-    ok = encode(&tm_q, true, 4, p.terms, d, s, b);
-  } else {
-    const cuuint64_t d[3] = {64, (cuuint64_t)p.B * p.R, (cuuint64_t)kChunks};
-    const cuuint64_t s[2] = {2 * kDqk, 128};
-    const cuuint32_t b[3] = {64, (cuuint32_t)kHalf, (cuuint32_t)kChunks};
-    ok = encode(&tm_q, false, 3, p.q, d, s, b);
-  }
+  // query: (64 dims, row of 8, chunk, 8-row group), e4m3 of each term: a run of 16
+  // rows as [group][chunk][8 rows][64 dims]
+  const cuuint64_t qd[5] = {64, 8, (cuuint64_t)kChunks, (cuuint64_t)p.B * p.R / 8, 2};
+  const cuuint64_t qs[4] = {2 * kDqk, 64 * e, 8 * 2 * kDqk, kDqk};
+  const cuuint32_t qb[5] = {64, 8, (cuuint32_t)kChunks, 2, 1};
+  ok = encode(&tm_q, kFp8, kFp8 ? 5 : 4, kFp8 ? static_cast<const void*>(p.terms) : p.q, qd, qs, qb);
   // (64 dims, cache row, chunk): a page's chunks as [chunk][row][64 dims]
   const cuuint64_t d[3] = {64, (cuuint64_t)p.num_pages * kPage, (cuuint64_t)kChunks};
   const cuuint64_t s[2] = {kDqk * e, 64 * e};
@@ -1090,7 +1142,7 @@ cudaError_t launch_join(const Params& p, const OwnPieces& own, cudaStream_t stre
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr = pdl_attribute();
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.max_units * (kPairRows / kJoinRows) +
+  cfg.gridDim = dim3(p.B * p.R / kJoinRows +
                      own.num_units * (kRows / kMergeRowsPerBlock));
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = kJoinSmem;

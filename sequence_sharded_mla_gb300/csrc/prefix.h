@@ -24,8 +24,11 @@ struct Params {
   float* inv_scale;              // e4m3: [B * R]
   int32_t* own_lens;             // [B] tokens behind the shared pages
   int32_t* own_table;            // [B, max_pages] their pages
-  int32_t* group_pages;          // [groups] their shared pages
-  int4* units;                   // [max_units] first row, end row, table row, shared pages
+  int2* group_info;              // [2, groups] shared pages and first unit, a block's each
+  int2* members;                 // [B] a request's first run in its group, the group's first unit
+  int4* units;                   // [max_units] runs, -, table row, shared pages
+  int32_t* runs;                 // [max_units, 8] first row of every 16 rows of a unit
+  int32_t* where;                // [B * R / 16] unit * 8 + run of every 16 rows, -1: in none
   int* positions;                // [max_units + 1] work positions before each unit
   WsHeader* work;                // the work list's header
   unsigned* err;                 // the call's error word
@@ -34,6 +37,7 @@ struct Params {
   float* out;                    // [B * R, 512]: slice 0 of the outputs
   float* lse;                    // [B * R]
   unsigned long long timeout_ns;
+  int always;                    // testing aid: share whatever can be shared
 };
 
 // The per-request kernel's work over the own tokens: its plan, and what it

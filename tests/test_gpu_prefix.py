@@ -16,6 +16,13 @@ PAGE, DEV = 64, "cuda"
 SCALE = mla.DEFAULT_SCALE
 
 
+@pytest.fixture(autouse=True)
+def share_whatever_can_be():
+    mla.mla_set_prefix_sharing(True)
+    yield
+    mla.mla_set_prefix_sharing(False)
+
+
 def i32(x):
     return torch.tensor(x, dtype=torch.int32, device=DEV)
 
@@ -138,8 +145,7 @@ def test_groups_of_odd_sizes_and_lengths(fp8):
     b = Batch(sizes, common, own, H=64, fp8=fp8, seed=3)
     part, lse, _ = check(b)
     got = in_slice_0(lse)
-    # one request of 64 rows, and prefixes below a page, share nothing
-    assert got == [k in (1, 3, 4, 5) for k in b.group]
+    assert got == [k != 2 for k in b.group]    # a prefix below a page
 
 
 @pytest.mark.parametrize("fp8", [False, True])
@@ -365,6 +371,35 @@ def test_a_step_with_weights_and_eviction():
         assert torch.equal(pool.view(-1, 576)[nbt[r, t // 64].long() * 64 + t % 64].view(torch.int16),
                            before[r].view(torch.int16))
     check(b)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_sharing_where_it_takes_less_time(fp8):
+    # many rows behind a long prefix share it; a few behind a short one, and a
+    # request alone, do not
+    mla.mla_set_prefix_sharing(False)
+    own = [5 + 7 * i for i in range(33)]
+    b = Batch([32, 1], [9000, 3000], own, H=64, fp8=fp8, seed=2)
+    _, lse, _ = check(b)
+    assert in_slice_0(lse) == [True] * 32 + [False]
+    b = Batch([4], [1000], own[:4], H=64, fp8=fp8, seed=2)
+    _, lse, _ = check(b)
+    assert not any(in_slice_0(lse))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_padded_requests_side_by_side_in_a_tile(fp8):
+    # 128-row tiles hold rows of many requests, with gaps of padding between
+    rng = random.Random(8)
+    new = [rng.randint(1, 4) for _ in range(40)]
+    b = Batch([23, 17], [700, 333], [4 + rng.randint(0, 90) for _ in range(40)], 4, 16, fp8, q_lens=new,
+              seed=8)
+    for r, n in enumerate(new):
+        b.q[r, n:] = math.inf
+    part, lse, _ = check(b)
+    for r, n in enumerate(new):
+        assert torch.isneginf(lse[:, r, n:]).all() and (part[:, r, n:] == 0).all()
+        assert not torch.isneginf(lse[0, r, :n]).any()
 
 
 def test_refusals_of_the_binding():
