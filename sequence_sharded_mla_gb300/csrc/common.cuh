@@ -104,6 +104,11 @@ struct PartialParams {
   const uint8_t* kv_fp8;  // fp8 caches: [num_pages, 64, 576] codes
   unsigned long long timeout_ns;
   int withhold_query;   // testing aid: 1 = never load the first piece's query rows
+  // e4m3 caches: the softmax's reference lies this far (log2 units, 0 to 7) below
+  // the running maximum that sets it, so that probabilities are up to 2^(this)
+  // there.  Their lower terms are multiples of 2^-9: at 0, one of a tenth of the
+  // largest is off by up to 2^-7 of itself, at 5 by 2^-8 like any other.
+  float ref_shift;
 };
 
 // Geometry of one work unit u = ((b * n_out) + so) * G + g.

@@ -671,9 +671,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         float alpha = 1.0f;
         bool resc = false;
         if (m_new > m_run + kRescaleThreshold || (j == t0 && m_new > -CUDART_INF_F)) {
-          alpha = (m_run == -CUDART_INF_F) ? 0.0f : ex2_approx(m_run - m_new);
+          const float ref = m_new - p.ref_shift;
+          alpha = (m_run == -CUDART_INF_F) ? 0.0f : ex2_approx(m_run - ref);
           l_run *= alpha;
-          m_run = m_new;
+          m_run = ref;
           resc = owner && (j != t0);
         }
         if (owner && half == 0) misc->alpha[grp][r] = alpha;

@@ -767,9 +767,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         float alpha = 1.0f;
         bool rescale = false;
         if (m_new > m_run + kRescale || (w.first && m_new > -CUDART_INF_F)) {
-          alpha = m_run == -CUDART_INF_F ? 0.0f : ex2_approx(m_run - m_new);
+          // (e4m3: P' of 2^5 at the maximum, 2^8 at most)
+          const float ref = kFp8 ? m_new - kRefShift : m_new;
+          alpha = m_run == -CUDART_INF_F ? 0.0f : ex2_approx(m_run - ref);
           l_run *= alpha;
-          m_run = m_new;
+          m_run = ref;
           rescale = live && !w.first;
         }
         // (a page that is not there has keys of 0: finite logits, and weights of 0)
@@ -803,7 +805,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // (converting a code back takes three conversions a pair, at an eighth
           // of the rate; a product and two differences are fused into hi = P'),
           // lo what is left.  Below 2^-6, where codes are multiples of 2^-9, the
-          // sum is off by 2^-9 at most -- 2^-17 of the row's largest.
+          // sum is off by 2^-9 at most -- 2^-14 of the row's largest.
           ulonglong2 sg;
           uint32_t hi4[8], lo4[8];
 #pragma unroll
