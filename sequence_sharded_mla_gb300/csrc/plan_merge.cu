@@ -41,8 +41,8 @@ __global__ void __launch_bounds__(256, 4) mla_merge_kernel(
   extern __shared__ __align__(16) float4 merge_stage[];   // [8 warps][kMergeBatch][32]
   griddep_wait();                // the partial kernel's pieces and outputs
   griddep_launch_dependents();
-  merge_unit_rows(pd, hdr, prefix, ws_o, ws_lse, out_partial, lse_partial, blockIdx.x, blockIdx.y,
-                  merge_stage);
+  merge_unit_rows<1, kMergeBatch>(pd, hdr, prefix, ws_o, ws_lse, out_partial, lse_partial,
+                                  blockIdx.x, blockIdx.y, merge_stage);
 }
 
 cudaError_t launch_plan(const ProblemDesc& pd, WsHeader* hdr, int* prefix, int grid,

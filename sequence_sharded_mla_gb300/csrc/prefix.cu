@@ -1000,27 +1000,36 @@ struct PairPieces {
   }
 };
 
-constexpr int kJoinRows = 2, kJoinBatch = 12;
-constexpr int kJoinSmem = 8 * kJoinBatch * 32 * (int)sizeof(float4);
-static_assert(kJoinSmem >= kMergeSmem, "either kind of block");
+// Few rows, which may have dozens of pieces: four warps a row (kVec 1), twelve
+// pieces in flight; from kManyRows rows, a warp a row (kVec 4) and three, for
+// fewer waves of blocks (joining a ragged verify step of 5120 rows 21.5 -> 12.4 us).
+constexpr int kManyRows = 1024;
+template <int kVec>
+struct Join {
+  static constexpr int kRowsB = 2 * kVec, kBatch = kVec == 1 ? kMergeBatch : 3;
+  static constexpr int kSmem = 8 * kBatch * kVec * 32 * (int)sizeof(float4);
+};
 
-// Slice 0, two rows a block: 0 and -inf for rows in no unit, else the LSE join of
-// their pieces unless a pair computed the unit whole; four warps per row of 128
-// dims each.  The blocks behind them: the own tokens' units.
+// Slice 0, 2 kVec rows a block: 0 and -inf for rows in no unit, else the LSE join
+// of their pieces unless a pair computed the unit whole.  The blocks behind them:
+// the own tokens' units.
+template <int kVec>
 __global__ void __launch_bounds__(256, 4) prefix_join_kernel(Params p, OwnPieces own) {
+  using J = Join<kVec>;
   extern __shared__ __align__(16) float4 join_stage[];
   griddep_wait();
   griddep_launch_dependents();
-  constexpr int kOwnBlocks = kRows / kMergeRowsPerBlock;
-  const int i = (int)blockIdx.x - p.B * p.R / kJoinRows;
+  constexpr int kOwnBlocks = kRows / J::kRowsB;
+  const int i = (int)blockIdx.x - p.B * p.R / J::kRowsB;
   if (i >= 0) {
-    merge_unit_rows(own.pd, own.hdr, own.positions, own.ws_o, own.ws_lse, own.out, own.lse,
-                    i / kOwnBlocks, i % kOwnBlocks, join_stage);
+    merge_unit_rows<kVec, J::kBatch>(own.pd, own.hdr, own.positions, own.ws_o, own.ws_lse, own.out,
+                                     own.lse, i / kOwnBlocks, i % kOwnBlocks, join_stage);
     return;
   }
   if (blockIdx.x == 0 && threadIdx.x == 0 && p.work->err != 0) atomicOr(p.err, p.work->err);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = warp & 3;
-  const int gr = (int)blockIdx.x * kJoinRows + (warp >> 2);
+  constexpr int kWarps = 4 / kVec;               // per row
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = warp % kWarps;
+  const int gr = (int)blockIdx.x * J::kRowsB + warp / kWarps;
   const int w = p.where[gr >> 4], u = w >> 3, r = (w & 7) * 16 + (gr & 15);
   int ps = 0, ue = 0, us = 0, per = 1;
   if (w >= 0) {
@@ -1030,21 +1039,25 @@ __global__ void __launch_bounds__(256, 4) prefix_join_kernel(Params p, OwnPieces
     per = p.work->per_cta;
     if (us / per == (ue - 1) / per) return;    // written by the pair that computed it
   }
-  float4* dst = reinterpret_cast<float4*>(p.out + (size_t)gr * kDv) + 32 * part;
+  float4* dst = reinterpret_cast<float4*>(p.out + (size_t)gr * kDv) + 32 * kVec * part;
   if (w < 0) {
-    dst[lane] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int v = 0; v < kVec; ++v) dst[lane + 32 * v] = make_float4(0.f, 0.f, 0.f, 0.f);
     if (part == 0 && lane == 0) p.lse[gr] = -CUDART_INF_F;
     return;
   }
   const int c0 = us / per, c1 = (ue - 1) / per;
   const PairPieces src{p.ws_o, p.ws_lse};
   const PairPieces::Ctx ctx{c0, c1 - c0 + 1, r, c0 * per < ps ? 1 : 0};
-  float4 acc[1];
+  float4 acc[kVec];
   float M, wsum;
-  merge_pieces_staged<1, kJoinBatch>(src, ctx, lane, 32 * part, join_stage + warp * (kJoinBatch * 32),
-                                     acc, M, wsum);
+  merge_pieces_staged<kVec, J::kBatch>(src, ctx, lane, 32 * kVec * part,
+                                       join_stage + warp * (J::kBatch * kVec * 32), acc, M, wsum);
   const float inv = wsum != 0.f ? 1.0f / wsum : 0.f;   // or NaN
-  dst[lane] = make_float4(acc[0].x * inv, acc[0].y * inv, acc[0].z * inv, acc[0].w * inv);
+#pragma unroll
+  for (int v = 0; v < kVec; ++v)
+    dst[lane + 32 * v] =
+        make_float4(acc[v].x * inv, acc[v].y * inv, acc[v].z * inv, acc[v].w * inv);
   if (part == 0 && lane == 0) p.lse[gr] = wsum != 0.f ? M + __logf(wsum) : -CUDART_INF_F;
 }
 
@@ -1138,20 +1151,25 @@ cudaError_t launch_attend(const Params& p, const void* kv, bool fp8, int pairs, 
   return fp8 ? attend<true>(p, kv, pairs, stream) : attend<false>(p, kv, pairs, stream);
 }
 
-cudaError_t launch_join(const Params& p, const OwnPieces& own, cudaStream_t stream) {
-  const cudaError_t e =
-      host::ensure_dynamic_smem(reinterpret_cast<const void*>(&prefix_join_kernel), kJoinSmem);
+template <int kVec>
+static cudaError_t join(const Params& p, const OwnPieces& own, cudaStream_t stream) {
+  using J = Join<kVec>;
+  const cudaError_t e = host::ensure_dynamic_smem(
+      reinterpret_cast<const void*>(&prefix_join_kernel<kVec>), J::kSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr = pdl_attribute();
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.B * p.R / kJoinRows +
-                     own.num_units * (kRows / kMergeRowsPerBlock));
+  cfg.gridDim = dim3(p.B * p.R / J::kRowsB + own.num_units * (kRows / J::kRowsB));
   cfg.blockDim = dim3(256);
-  cfg.dynamicSmemBytes = kJoinSmem;
+  cfg.dynamicSmemBytes = J::kSmem;
   cfg.stream = stream;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, prefix_join_kernel, p, own);
+  return cudaLaunchKernelEx(&cfg, prefix_join_kernel<kVec>, p, own);
+}
+
+cudaError_t launch_join(const Params& p, const OwnPieces& own, cudaStream_t stream) {
+  return p.B * p.R >= kManyRows ? join<4>(p, own, stream) : join<1>(p, own, stream);
 }
 
 }  // namespace prefix

@@ -34,27 +34,31 @@ constexpr int kMergeRowsPerBlock = 2;
 constexpr int kMergeBatch = 12;
 constexpr int kMergeSmem = 8 * kMergeBatch * 32 * (int)sizeof(float4);
 
-// Rows 2 y and 2 y + 1 of unit u, if the partial kernel left them: 0 and -inf, or
-// the merge of their pieces.  `stage`: kMergeSmem bytes of shared memory.
+// Rows of unit u, block y of 2 * kVec rows, if the partial kernel left them: 0 and
+// -inf, or the merge of their pieces, 4 / kVec warps per row and kB pieces in
+// flight.  `stage`: 8 * kB * kVec * 512 bytes of shared memory.
+template <int kVec, int kB>
 __device__ __forceinline__ void merge_unit_rows(const ProblemDesc& pd, const WsHeader* hdr,
                                                 const int* prefix, const float* ws_o,
                                                 const float* ws_lse, float* out_partial,
                                                 float* lse_partial, int u, int y, float4* stage) {
   const Unit x = make_unit(pd, u);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int r = y * kMergeRowsPerBlock + (warp >> 2), part = warp & 3;
+  constexpr int kWarps = 4 / kVec;               // per row
+  const int r = y * (8 / kWarps) + warp / kWarps, part = warp % kWarps;
   if (r >= x.rows_out) return;
   const int ps = prefix[u], ue = prefix[u + 1];
   const int us = unit_tile_start(prefix, u, hdr->unit_cost);
   const size_t orow = out_row(pd, x, r);
-  float4* dst = reinterpret_cast<float4*>(out_partial + orow * kDv) + 32 * part;
+  float4* dst = reinterpret_cast<float4*>(out_partial + orow * kDv) + 32 * kVec * part;
   const int per = hdr->per_cta;
   const bool split = us < ue && us / per != (ue - 1) / per;
   // rows with no token to see: the shard holds none of the request's
   // positions, or the row is padding of a request with fewer query tokens
   // (a whole unit's padding rows are written by the partial kernel)
   if (us == ue || (split && r >= x.rows)) {
-    dst[lane] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int v = 0; v < kVec; ++v) dst[lane + 32 * v] = make_float4(0.f, 0.f, 0.f, 0.f);
     if (part == 0 && lane == 0) lse_partial[orow] = -CUDART_INF_F;
     return;
   }
@@ -62,12 +66,15 @@ __device__ __forceinline__ void merge_unit_rows(const ProblemDesc& pd, const WsH
   if (c0 == c1) return;  // written directly by the partial kernel
   const UnitPieces src{ws_o, ws_lse};
   const UnitPieces::Ctx ctx{c0, c1 - c0 + 1, r, c0 * per < ps ? 1 : 0};
-  float4 acc[1];
+  float4 acc[kVec];
   float M, wsum;
-  merge_pieces_staged<1, kMergeBatch>(src, ctx, lane, 32 * part,
-                                      stage + warp * (kMergeBatch * 32), acc, M, wsum);
+  merge_pieces_staged<kVec, kB>(src, ctx, lane, 32 * kVec * part, stage + warp * (kB * kVec * 32), acc,
+                                M, wsum);
   const float inv = wsum != 0.f ? 1.0f / wsum : 0.f;   // or NaN
-  dst[lane] = make_float4(acc[0].x * inv, acc[0].y * inv, acc[0].z * inv, acc[0].w * inv);
+#pragma unroll
+  for (int v = 0; v < kVec; ++v)
+    dst[lane + 32 * v] =
+        make_float4(acc[v].x * inv, acc[v].y * inv, acc[v].z * inv, acc[v].w * inv);
   if (part == 0 && lane == 0) lse_partial[orow] = wsum != 0.f ? M + __logf(wsum) : -CUDART_INF_F;
 }
 

@@ -12,10 +12,9 @@
 // the rows, so the sum over rows stays inside a thread (fixed order, nothing
 // to exchange) and every thread ends with one token's weight.
 //
-//   warp 0      K producer, two pages a tile, by TMA: bf16, three boxes of three
-//               64-dim chunks a page into a ring of three; e4m3, whole pages (in
-//               192-byte pieces of the 576-byte rows a million tokens took 119
-//               instead of 105 us) into two tiles
+//   warp 0      K producer, two pages a tile, by TMA: boxes of three 64-dim chunks
+//               a page; e4m3, whole pages (in 192-byte pieces of the
+//               576-byte rows a million tokens took 119 instead of 105 us)
 //   warp 1      MMA issue
 //   warps 2..5  one token a thread: exp2 of every column, summed
 //   warp 6      Q producer: a group's nine chunks.  A request of one group of
@@ -137,7 +136,9 @@ struct Cfg {
   static constexpr int kKGroup = kCg * 8 * kLine;
   static constexpr int kKBytes = kTokens / 8 * kKGroup;    // 72 or 48 KB
   static constexpr int kQBytes = kN * kLine;               // Q chunk: 8 or 16 KB
-  static constexpr int kKDepth = kFp8 ? 2 : 3;
+  // with more than 64 rows the query's chunks stream (one tile of e4m3 keys and
+  // nine chunks of the query in flight took 52 instead of 50 us for a 9-token step)
+  static constexpr int kKDepth = !kFp8 ? 3 : kRowsN == 64 ? 2 : 2;
   static constexpr int kQDepth = kRowsN == 64 ? 9 : 4;
   static constexpr int kSmemQ = kKDepth * kKBytes;
   static constexpr int kSmemMisc = kSmemQ + kQDepth * kQBytes;
@@ -345,6 +346,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     int nd = 0, last_b = -1, have = 0;
     while (ok && walk.next<kRowsN>(p, b, L, rows, groups, t0, t1)) {
       const int before_step = L - new_tokens(p, b);         // tokens of earlier steps
+      // the thread's row of a group
+      float next_l = 0.0f, next_f = 0.0f;
+      auto fetch = [&](int g) {
+        if (g * kRowsN + tid >= min(rows, (g + 1) * kRowsN)) return;
+        const size_t r = (size_t)b * p.R + g * kRowsN + tid;
+        next_l = p.lse[r];
+        if (kFp8) next_f = p.inv_scale[r];
+      };
+      if (groups > 1 || b != last_b) fetch(0);
       for (int t = t0; ok && t < t1; ++t) {
         const int tok = t * kTokens + tid;
         // the token's scale and earlier weight: on their way while the MMAs run
@@ -365,20 +375,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int g = 0; ok && g < groups; ++g, ++nd) {
           const int n = min(kRowsN, rows - g * kRowsN);     // a multiple of 16
           // the rows' log-sum-exps (a row that saw nothing gives nothing) and
-          // query scales, unless the last group's are this group's
+          // query scales, unless the last group's are this group's; the next
+          // group's are on their way meanwhile
           if (groups > 1 || b != last_b) {
             have ^= 1;           // the other buffer: a warp may still read this one
             if (tid < n) {
-              const size_t r = (size_t)b * p.R + g * kRowsN + tid;
-              const float l = p.lse[r];
-              misc->row_lse[have][tid] = l == -CUDART_INF_F ? CUDART_INF_F : l * kLog2e;
+              misc->row_lse[have][tid] = next_l == -CUDART_INF_F ? CUDART_INF_F : next_l * kLog2e;
               if (kFp8) {
-                const float f = p.inv_scale[r];
-                if (f != f) atomicOr(&p.hdr->err, kErrQRange);
-                misc->row_f[have][tid] = f * p.scale_log2;
+                if (next_f != next_f) atomicOr(&p.hdr->err, kErrQRange);
+                misc->row_f[have][tid] = next_f * p.scale_log2;
               }
             }
             last_b = b;
+            if (groups > 1) fetch(g + 1 < groups ? g + 1 : 0);
             named_bar_sync(kBarSum, kSumThreads);
           }
           const int buf = nd & 1;
