@@ -308,7 +308,8 @@ mla_status mla_set_wait_budget_ns(unsigned long long ns);
 
 /*
  * Testing aid (not part of the method): while `on` is non-zero, the
- * partial-attention kernels of mla_decode_partial launched from now on never
+ * partial-attention kernels of mla_decode_partial (and those of
+ * mla_prefix_partial and mla_attention_weights) launched from now on never
  * load the query rows of each CTA's first piece of work (process-wide).  The
  * waits for those rows cannot succeed, so each CTA stops once its wait
  * budget (mla_set_wait_budget_ns) runs out, and mla_get_device_error then

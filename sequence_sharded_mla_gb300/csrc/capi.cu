@@ -670,6 +670,7 @@ mla_status mla_prefix_partial(const void* q, const mla_kv_pages* kv, const int32
   p.lse = lse_partial;
   p.timeout_ns = host::wait_budget_ns(kTimeoutNs);
   p.always = host::g_share_always.load();
+  p.withhold_query = host::g_withhold_query.load();
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   float* own_out = out_partial + rows * kDv;
   float* own_lse = lse_partial + rows;
@@ -685,8 +686,9 @@ mla_status mla_prefix_partial(const void* q, const mla_kv_pages* kv, const int32
       prefix::kRefShift);
   if (st != MLA_OK) return st;
   const prefix::OwnPieces own{L.pd, L.hdr, L.prefix, L.ws_o, L.ws_lse, own_out, own_lse, L.num_units};
-  // (a batch of at most 64 rows gains nothing)
-  if (((rows > (size_t)kRows || p.always) &&
+  // (not where no lengths could make sharing worth it)
+  const long long most = 10LL * shape->batch * ceil_div(p.R, kRows) * max_pages_per_req;
+  if (((most > prefix::kMinGain || p.always) &&
        prefix::launch_attend(p, kv->data, fp8, pairs, cs) != cudaSuccess) ||
       prefix::launch_join(p, own, cs) != cudaSuccess)
     return MLA_ERR_CUDA;

@@ -135,7 +135,6 @@ __device__ __forceinline__ Group measure(const Params& p, bool ok, int g, int b0
 //   8 behind 4096 47 and 38, 16384 56 and 54, 65536 107 and 134;
 //   32 behind 4096 69 and 63, 16384 108 and 126, 65536 263 and 368;
 //   e4m3 32 behind 65536 229 and 367.)
-constexpr long long kMinGain = 12000;
 __device__ __forceinline__ long long gain_of(const Group& x) {
   return 10LL * x.units * x.pages - 25LL * ((x.runs + 7) / 8) * ((x.pages + 1) / 2);
 }
@@ -528,6 +527,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // the piece's query, once S of the piece before is done
           if (pieces > 0) ok = wait1(&misc->q_empty, (pieces - 1) & 1);
           if (!ok) break;
+          if (p.withhold_query && pieces == 0) continue;
           misc->armed_q++;
           mbar_arrive_expect_tx_pair(at_leader(&misc->q_full), kQBytes);
           // four runs of 16 rows; a run behind the group's last lies behind the

@@ -7,6 +7,7 @@ namespace mla {
 namespace prefix {
 
 constexpr int kPairRows = 128;   // query rows of a CTA pair (64 per CTA)
+constexpr long long kMinGain = 12000;   // ns that sharing has to save
 constexpr float kRefShift = 5.0f;   // e4m3: PartialParams::ref_shift
 
 struct Params {
@@ -38,6 +39,7 @@ struct Params {
   float* out;                    // [B * R, 512]: slice 0 of the outputs
   float* lse;                    // [B * R]
   unsigned long long timeout_ns;
+  int withhold_query;            // testing aid: a pair's first query is never loaded
   int always;                    // testing aid: share whatever can be shared
 };
 

@@ -73,6 +73,7 @@ struct Params {
   WsHeader* hdr;
   int* prefix;                             // [B + 1]
   unsigned long long timeout_ns;
+  int withhold_query;                      // testing aid: the query is never loaded
 };
 
 __device__ __forceinline__ int context(const Params& p, int b) {
@@ -273,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 6) {
     // ---------------------------------------------------------- Q producer
-    if (lane == 0) {
+    if (lane == 0 && !p.withhold_query) {
       while (ok && walk.next<kRowsN>(p, b, L, rows, groups, t0, t1)) {
         for (int t = t0; ok && t < (stay ? t0 + 1 : t1); ++t)
           for (int g = 0; ok && g < groups; ++g)
@@ -611,6 +612,7 @@ mla_status mla_attention_weights(const void* q, const mla_kv_pages* kv, const in
   p.hdr = reinterpret_cast<WsHeader*>(ws);
   p.prefix = reinterpret_cast<int*>(ws + l.prefix);
   p.timeout_ns = host::wait_budget_ns(2000000000ull);
+  p.withhold_query = host::g_withhold_query.load();
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (fp8)
     return n == 64 ? weights::run<true, 64>(p, kv->data, grid, st)

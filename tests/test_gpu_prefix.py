@@ -333,16 +333,21 @@ def test_outputs_at_16_byte_addresses():
     check(b, out_partial=out, lse_partial=lse)
 
 
-def test_a_wait_that_runs_out_is_reported_and_leaves_the_gpu_usable():
-    b = Batch([4], [64 * 400], [40, 3, 70, 1], H=64, seed=4)
+@pytest.mark.parametrize("fp8", [False, True])
+def test_waits_that_run_out_are_reported_and_leave_the_gpu_usable(fp8):
+    # the query rows that both CTAs of a pair wait for never come
+    b = Batch([4], [64 * 40], [40, 3, 70, 1], H=64, fp8=fp8, seed=4)
+    want = b.expect()
     try:
-        mla.mla_set_wait_budget_ns(1)
+        mla.mla_set_wait_budget_ns(2_000_000)
+        mla.mla_set_withhold_query(True)
         _, _, ws = b.call()
         got = mla.mla_get_device_error(ws)
     finally:
+        mla.mla_set_withhold_query(False)
         mla.mla_set_wait_budget_ns(0)
-    assert got in (0, -4)
-    check(b)
+    assert got == -4
+    check(b, want=want)
 
 
 def test_a_step_with_weights_and_eviction():
@@ -385,6 +390,14 @@ def test_sharing_where_it_takes_less_time(fp8):
     b = Batch([4], [1000], own[:4], H=64, fp8=fp8, seed=2)
     _, lse, _ = check(b)
     assert not any(in_slice_0(lse))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_few_rows_behind_a_long_prefix_share_it_too(fp8):
+    mla.mla_set_prefix_sharing(False)
+    b = Batch([4], [40000], [5, 1, 70, 200], H=16, fp8=fp8, seed=2)
+    _, lse, _ = check(b)
+    assert all(in_slice_0(lse))
 
 
 @pytest.mark.parametrize("fp8", [False, True])

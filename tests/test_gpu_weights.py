@@ -251,15 +251,19 @@ def test_same_bits_again_and_in_a_graph_on_another_stream():
     assert torch.equal(out, replayed) and not torch.equal(out, first)
 
 
-def test_wait_that_runs_out_is_reported():
-    step = Step([5000], 1, 16, seed=1)
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("q_len", [1, 9])
+def test_waits_that_run_out_are_reported(q_len, fp8):
+    step = Step([5000, 70], q_len, 16, fp8, seed=1)
     try:
-        mla.mla_set_wait_budget_ns(1)
+        mla.mla_set_wait_budget_ns(2_000_000)
+        mla.mla_set_withhold_query(True)
         _, ws = step.call()
         got = mla.mla_get_device_error(ws)
     finally:
+        mla.mla_set_withhold_query(False)
         mla.mla_set_wait_budget_ns(0)
-    assert got in (0, -4)                       # short waits may succeed at once
+    assert got == -4
     check(step)
 
 
