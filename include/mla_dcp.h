@@ -666,7 +666,7 @@ mla_status mla_attention_weights(const void* q, const mla_kv_pages* kv, const in
  *   keep             int32 [B], 0 .. max_keep; keep_first int32 [B] or NULL
  *   new_block_table  int32 [B, new_max_pages], new_max_pages >= ceil(max_keep / 64);
  *                    entries behind a request's new pages are not read
- *   new_seq_lens     int32 [B]: n_b; not seq_lens itself
+ *   new_seq_lens     int32 [B]: n_b; not seq_lens, keep or keep_first itself
  *   kept             int32 [B, max_keep]: positions in the old context, ascending;
  *                    -1 from n_b on
  *   weights_out      fp32 [B, max_keep] or NULL: the kept tokens' weights; entries

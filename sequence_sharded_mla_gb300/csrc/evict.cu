@@ -65,7 +65,6 @@ struct Copy {
   int new_max_pages;
   const float* weights;
   long long stride;
-  int width;
   float* weights_out;                 // or null
   const int32_t* new_lens;
   const int32_t* kept;
@@ -446,7 +445,10 @@ extern "C" mla_status mla_cache_evict(const mla_kv_pages* kv, const int32_t* blo
   // candidates are indexed in 32 bits, with a cluster's rounding behind them
   if (weights_width > (1 << 30)) return MLA_ERR_UNSUPPORTED;
   // read by every CTA while another writes
-  if (evict::overlap(seq_lens, sizeof(int32_t) * batch, new_seq_lens, sizeof(int32_t) * batch) ||
+  const size_t row = sizeof(int32_t) * batch;
+  if (evict::overlap(seq_lens, row, new_seq_lens, row) ||
+      evict::overlap(keep, row, new_seq_lens, row) ||
+      (keep_first != nullptr && evict::overlap(keep_first, row, new_seq_lens, row)) ||
       (weights_out != nullptr &&
        evict::overlap(weights, sizeof(float) * ((batch - 1) * (size_t)weights_stride + weights_width),
                       weights_out, sizeof(float) * (size_t)batch * max_keep)))
@@ -467,7 +469,6 @@ extern "C" mla_status mla_cache_evict(const mla_kv_pages* kv, const int32_t* blo
                       new_max_pages,
                       weights,
                       weights_stride,
-                      weights_width,
                       weights_out,
                       new_seq_lens,
                       kept,

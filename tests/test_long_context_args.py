@@ -32,7 +32,8 @@ def evict(data=512, scale=None, dtype=0, pages=4, page=64, bt=512, mp=4, sl=512,
     (dict(keep=None), INVALID), (dict(keep=514), INVALID), (dict(first=514), INVALID),
     (dict(recent=-1), INVALID), (dict(nbt=None), INVALID), (dict(nbt=514), INVALID),
     (dict(nmp=0), INVALID), (dict(nmp=1), INVALID), (dict(new=None), INVALID), (dict(new=512), INVALID),
-    (dict(new=516), INVALID), (dict(new=514), INVALID), (dict(kept=None), INVALID),
+    (dict(new=516), INVALID), (dict(new=514), INVALID), (dict(keep=8196), INVALID),
+    (dict(first=8188), INVALID), (dict(kept=None), INVALID),
     (dict(kept=514), INVALID), (dict(mk=0), INVALID), (dict(mk=129), INVALID), (dict(wo=65538), INVALID),
     (dict(wo=1024), INVALID), (dict(wo=512), INVALID), (dict(B=1 << 30, mk=256, nmp=4), INVALID),
     (dict(ws=None), WORKSPACE), (dict(ws=520), WORKSPACE), (dict(wb=255), WORKSPACE),
