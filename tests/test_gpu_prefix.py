@@ -379,6 +379,44 @@ def test_a_step_with_weights_and_eviction():
 
 
 @pytest.mark.parametrize("fp8", [False, True])
+def test_pages_whose_offsets_pass_32_bits(fp8):
+    """The same pages at the end of a pool of more than 4 GB: the same bits."""
+    far = (1 << 32) // (PAGE * 576) + 64
+    b = Batch([3], [320], [200, 77, 130], H=64, seed=22, fp8=fp8)
+    n, w0 = b.P, torch.rand((3, b.bt.shape[1] * PAGE), device=DEV)
+    free = i32([b.P + k for k in range(3 * 4)]).view(3, 4)
+
+    def steps(kv, scale, at):
+        table = torch.where(b.bt >= 0, b.bt + at, b.bt)
+        part, lse, ws = mla.mla_prefix_partial(b.q, kv, table, b.seq, b.starts, b.prefix, kv_scale=scale,
+                                               causal=True)
+        _, lse_out = mla.mla_shard_combine(part, lse)
+        w, wws = mla.mla_attention_weights(b.q, kv, table, b.seq, lse_out, w0, torch.zeros_like(w0),
+                                           kv_scale=scale, causal=True)
+        new, kept, wk, ews = mla.mla_cache_evict(kv, table, b.seq, w, i32([200, 256, 130]), free + at,
+                                                 recent=8, kv_scale=scale,
+                                                 weights_out=torch.zeros((3, 256), device=DEV))
+        torch.cuda.synchronize()
+        assert [mla.mla_get_device_error(x) for x in (ws, wws, ews)] == [0, 0, 0]
+        rows = kv[at + n:at + n + 12].reshape(3, -1, 576)
+        moved = [rows[r, :k].clone().view(torch.uint8) for r, k in enumerate((200, 256, 130))]
+        scales = [] if scale is None else [scale[at + n:at + n + 12].reshape(3, -1)[r, :k].clone()
+                                           for r, k in enumerate((200, 256, 130))]
+        return [part, lse, w, new, kept, wk] + moved + scales
+
+    kv = torch.zeros((far + n + 12, PAGE, 576), dtype=b.kv.dtype, device=DEV)
+    scale = None if b.scale is None else torch.zeros((far + n + 12, PAGE), device=DEV)
+    got = []
+    for at in (0, far):
+        kv[at:at + n] = b.kv
+        if fp8:
+            scale[at:at + n] = b.scale
+        got.append(steps(kv, scale, at))
+    for x, y in zip(*got):
+        assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
 def test_sharing_where_it_takes_less_time(fp8):
     # many rows behind a long prefix share it; a few behind a short one, and a
     # request alone, do not
