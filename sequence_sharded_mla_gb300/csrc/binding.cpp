@@ -1,8 +1,9 @@
 // Python entry of the rotary, cache-append, shared-prefix, attention-weight,
-// eviction and e4m3 grouped-query calls (and the combine that follows them): argument checks, output allocation and the
-// C call, without a Python object per pointer.  A decode step's calls are a
-// few microseconds of GPU work each, so checks written in Python (10 to 30 us
-// a call on the Grace host) would be what bounds them.
+// eviction and e4m3 grouped-query calls (and the combine that follows them):
+// argument checks, output allocation and the C call, without a Python object per
+// pointer.  A decode step's calls are a few microseconds of GPU work each, so
+// checks written in Python (10 to 30 us a call on the Grace host) would be what
+// bounds them.
 //
 // Every call runs on the tensors' device, on the given stream or the device's
 // current one; outputs and workspaces that it allocates belong to that stream.

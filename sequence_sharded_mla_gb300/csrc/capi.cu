@@ -429,7 +429,8 @@ StepLayout step_layout(const mla_shape* shape, int num_shards) {
 // own tokens' lengths and tables, the units and their split, the query's terms
 // (e4m3) and the pieces of split units.
 struct PrefixLayout {
-  size_t partial_ws, own_lens, own_table, group_info, members, units, runs, where, positions, work, terms, inv_scale, ws_o, ws_lse, total;
+  size_t partial_ws, own_lens, own_table, group_info, members, units, runs, where, positions,
+      work, terms, inv_scale, ws_o, ws_lse, total;
   int max_units;
 };
 

@@ -139,7 +139,7 @@ struct Cfg {
   static constexpr int kQBytes = kN * kLine;               // Q chunk: 8 or 16 KB
   // with more than 64 rows the query's chunks stream (one tile of e4m3 keys and
   // nine chunks of the query in flight took 52 instead of 50 us for a 9-token step)
-  static constexpr int kKDepth = !kFp8 ? 3 : kRowsN == 64 ? 2 : 2;
+  static constexpr int kKDepth = kFp8 ? 2 : 3;
   static constexpr int kQDepth = kRowsN == 64 ? 9 : 4;
   static constexpr int kSmemQ = kKDepth * kKBytes;
   static constexpr int kSmemMisc = kSmemQ + kQDepth * kQBytes;
