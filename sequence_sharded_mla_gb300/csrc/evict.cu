@@ -18,7 +18,7 @@
 //
 // What bounds them: the copy, memory bandwidth (2 x 1152 or 2 x 580 bytes a
 // kept token); the selection of a short context, its chain of cluster
-// barriers; of a long one, five reads of the weights out of L2.
+// barriers; of a long one, the instructions of three passes over the weights.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -73,15 +73,12 @@ struct Copy {
   unsigned* err;
 };
 
-constexpr uint32_t kZero = 0x80000000u;   // key of 0
-
 // Unsigned key in the order of the weights: -inf first, both zeros alike, NaN
-// above everything.
+// above everything (a sum with 0 makes -0 the other zero, and any NaN the one of
+// all ones behind a sign of 0).
 __device__ __forceinline__ uint32_t key_of(float w) {
-  const uint32_t u = __float_as_uint(w);
-  if (w != w) return 0xFFFFFFFFu;
-  if (w == 0.0f) return kZero;
-  return (u >> 31) ? ~u : u | 0x80000000u;
+  const uint32_t u = __float_as_uint(__fadd_rn(w, 0.0f));
+  return u ^ ((uint32_t)((int)u >> 31) | 0x80000000u);
 }
 
 template <int kWarps>
@@ -95,9 +92,10 @@ struct Shared {
   uint32_t list[kWarps][kList];       // keys with the first chosen digit, in order
 };
 
-// C: CTAs per request (a cluster of them).
+// C: CTAs per request (a cluster of them).  (One CTA per SM: without that bound
+// the 512 threads get 40 registers, spill and take 12.1 instead of 10.7 us.)
 template <int C, int kThreads>
-__global__ void __launch_bounds__(kThreads) evict_select_kernel(Select p) {
+__global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(Select p) {
   constexpr int kWarps = kThreads / 32, kOwn = kBins / kThreads;   // bins per thread
   __shared__ Shared<kWarps> sm;
   cg::cluster_group cluster = cg::this_cluster();
@@ -186,14 +184,11 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(Select p) {
       for (int i = tid; i < kBins; i += kThreads) hist[i] = 0;
     if (C > 1 && pass == 0) cluster.sync();   // rank 0's totals are zero
     else __syncthreads();
-    // Weights of zero, often many, are counted by ballot; the others spread over
-    // enough digits (an exponent has four) for atomics of their own.  Grouping
-    // equal digits first took 2.5 times as long on a long-tailed row.
-    uint32_t zeros = 0;
+    // Equal digits, such as those of many weights of zero, meet in one addition of
+    // the shared-memory atomics.  (Counting zeros by ballot took 104 instead of
+    // 100 us for a million tokens, grouping all equal digits 2.5 times as long.)
     auto count = [&](uint32_t x, bool in) {
-      const bool zero = in && x == kZero;
-      zeros += __popc(__ballot_sync(0xFFFFFFFFu, zero));
-      if (in && !zero) atomicAdd(&hist[(x >> shift) & mask], 1u);
+      if (in) atomicAdd(&hist[(x >> shift) & mask], 1u);
     };
     if (pass == 0) {
       each([&](uint32_t x, int i) { count(x, i < wz); });
@@ -214,7 +209,6 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(Select p) {
     } else {
       undecided([&](uint32_t x, bool in) { count(x, in && (x >> upper) == match); });
     }
-    if (lane == 0 && zeros != 0) atomicAdd(&hist[(kZero >> shift) & mask], zeros);
     __syncthreads();
     if (C > 1) {
       // the few digits that occur go to rank 0 (every CTA reading all of the
@@ -281,13 +275,19 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(Select p) {
     gt0 += *cluster.map_shared_rank(&sm.total_gt, r);
     eq0 += *cluster.map_shared_rank(&sm.total_eq, r);
   }
+  // (at: where the slice's next weight goes, of those above T and the equal ones
+  // that stay)
+  uint32_t at = (uint32_t)first + gt0 + min(eq0, left);
   each([&](uint32_t x, int i) {
-    const uint32_t mg = __ballot_sync(0xFFFFFFFFu, i < wz && x > T);
+    bool stays = i < wz && x > T;
     const uint32_t me = __ballot_sync(0xFFFFFFFFu, i < wz && x == T);
-    const uint32_t g = gt0 + __popc(mg & below), e = eq0 + __popc(me & below);
-    if (i < wz && (x > T || (x == T && e < left))) out[first + g + min(e, left)] = first + i;
-    gt0 += __popc(mg);
-    eq0 += __popc(me);
+    if (me != 0) {
+      stays |= i < wz && x == T && eq0 + __popc(me & below) < left;
+      eq0 += __popc(me);
+    }
+    const uint32_t m = __ballot_sync(0xFFFFFFFFu, stays);
+    if (stays) out[at + __popc(m & below)] = first + i;
+    at += __popc(m);
   });
   if (C > 1) cluster.sync();     // peers have read this CTA's totals
 }
@@ -375,11 +375,11 @@ inline bool overlap(const void* a, size_t n, const void* b, size_t m) {
 
 // CTAs per request, by the width of the weights.  A whole eviction to a quarter
 // (e4m3) with one CTA of 512 threads, and clusters of 4, 8 and 16 of 1024:
-//   4 x 777      11.3,  16.2,  16.3,  18.2 us
-//   16 x 8000    18.0,  19.9,  32.0,  48.3
-//   16 x 40000    117,  52.3,  64.5,  82.7
-//   4 x 131000    279,  68.6,  49.8,  49.1
-//   1 x 1048576  1443,   278,   174,   124
+//   4 x 777       9.0,  14.5,  14.5,  16.6 us
+//   16 x 8000    13.8,  18.1,  28.6,  44.1
+//   16 x 40000   64.3,  50.7,  61.8,  78.4
+//   4 x 131000    154,  54.4,  47.1,  47.5
+//   1 x 1048576  1004,   225,   145,  97.6 (107 if all weights are equal)
 template <int C, int kThreads>
 cudaError_t select(const Select& s, int batch, cudaStream_t stream) {
   const void* kernel = reinterpret_cast<const void*>(&evict_select_kernel<C, kThreads>);

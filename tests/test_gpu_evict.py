@@ -161,6 +161,33 @@ def test_long_contexts_take_a_cluster(kind):
     check(pool, lens, weights_of(kind, 4, max(lens), 7), keeps, [100, 0, 0, 0], 77)
 
 
+@pytest.mark.parametrize("kind", ["tail", "equal", "few", "last", "comb up", "comb down"])
+@pytest.mark.parametrize("L", [524288, 200003])
+def test_selection_of_rows_too_long_for_registers(L, kind):
+    """Weights whose every eighth group of 32 is nothing like the others among
+    them: what a sample of such rows says of them is wrong."""
+    if kind.startswith("comb"):
+        t = torch.arange(L, device=DEV)
+        w = torch.rand((1, L), device=DEV, generator=torch.Generator(device=DEV).manual_seed(5)) + 1
+        w[0, ((t % 256) < 32) == (kind == "comb up")] *= 1000
+    else:
+        w = weights_of(kind, 1, L, 13)
+    pages_old, bt = pages(L), torch.arange(pages(L), dtype=torch.int32, device=DEV)[None]
+    order = torch.argsort(-w[0], stable=True)
+    kv = torch.zeros((2 * pages_old, PAGE, 576), dtype=torch.uint8, device=DEV)
+    scale = torch.arange(2 * pages_old * PAGE, device=DEV, dtype=torch.float32).view(-1, PAGE)
+    ws = torch.zeros(256, dtype=torch.uint8, device=DEV)
+    for keep in (1, 1000, L // 4, L // 2 + 1, L - 1):
+        new, kept, wk, _ = mla.mla_cache_evict(kv, bt, i32([L]), w, i32([keep]), bt + pages_old, kv_scale=scale,
+                                               workspace=ws)
+        want = order[:keep].sort().values
+        torch.cuda.synchronize()
+        assert mla.mla_get_device_error(ws) == 0 and new.tolist() == [keep]
+        assert torch.equal(kept[0, :keep].long(), want) and (kept[0, keep:] == -1).all()
+        assert torch.equal(wk[0, :keep], w[0, want])
+        assert torch.equal(scale.view(-1)[pages_old * PAGE:][:keep].long(), want)
+
+
 def test_a_long_tie_ends_at_the_right_token():
     # every weight equal: the kept ones are the first of the candidates
     L, keep = 70001, 50021
