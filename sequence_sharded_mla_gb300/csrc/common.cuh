@@ -5,6 +5,9 @@
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <math_constants.h>
+
+#include "ptx.cuh"
 
 namespace mla {
 
@@ -110,6 +113,37 @@ struct PartialParams {
   // largest is off by up to 2^-7 of itself, at 5 by 2^-8 like any other.
   float ref_shift;
 };
+
+// The reference of an e4m3 cache's softmax: probabilities 2^(b - ref) times a
+// scale's mantissa are multiplied as sums of two e4m3 terms.  Those overflow from
+// 448 on, are off by 2^-8 of themselves at most down to 2^-1 and by up to 2^-9 below
+// that, and vanish below 2^-10.  So the reference follows what is being added, not
+// only the maximum: a running maximum alone left a tail of 64k tokens 11 nats
+// below one heavy token out of the output altogether, half of its weight, while
+// the sum of the weights had it in.  A tile's largest logit may lie from ref - 2 to
+// ref + 8; outside, the tile's becomes ref + 5, and what was summed up is scaled
+// (in fp32, which has the range).  A tile 2^-30 below the largest logit moves
+// nothing: a million of its tokens weigh 2^-10 of that one.
+// A token is then off by 2^-9 where its tile's largest is 2^-3 at least: what a
+// token far above the others of its tile costs those, 2^-7 of its own weight if
+// all 128 are off one way, is all that is lost.  (Logits of 3 nats' deviation
+// move the reference 18 times in 64k tokens.)
+constexpr float kRefHigh = 8.0f, kRefSet = 5.0f, kRefLow = -2.0f, kRefDeep = 30.0f;
+
+// Takes in a tile whose largest logit is m_tile (log2 units; -inf: none): true if
+// the reference moved, and what was summed up is to be scaled by alpha.  `top`: the
+// largest so far.  Both start at -inf.
+__device__ __forceinline__ bool move_reference(float m_tile, float& ref, float& top, float& alpha) {
+  const bool move =
+      m_tile > ref + kRefHigh || (m_tile < ref + kRefLow && m_tile > top - kRefDeep);
+  top = fmaxf(top, m_tile);
+  alpha = 1.0f;
+  if (move) {
+    alpha = ref == -CUDART_INF_F ? 0.0f : ex2_approx(ref - (m_tile - kRefSet));
+    ref = m_tile - kRefSet;
+  }
+  return move;
+}
 
 // Geometry of one work unit u = ((b * n_out) + so) * G + g.
 struct Unit {

@@ -34,8 +34,8 @@
 //   warp 3      V producer; e4m3: the tile's token scales, split into mantissa
 //               and exponent
 //   warps 4..11 softmax: a thread has one row and 32 tokens; the four threads of
-//               a row exchange their maxima; O is rescaled only when a running
-//               maximum grows by more than 2^8; the epilogue
+//               a row exchange their maxima; O is rescaled only when a tile's is
+//               2^8 above the reference (e4m3: or far below); the epilogue
 //
 // e4m3 caches: the MMAs take the codes as they are, the query and the
 // probabilities as two-term e4m3 sums, as in the per-request kernel; three
@@ -705,7 +705,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         qs *= f;
       }
       const f32x2 qs2 = pack2(qs, qs);                     // logits in log2 units
-      float m_run = -CUDART_INF_F, l_run = 0.0f;           // l_run: this thread's tokens
+      float m_run = -CUDART_INF_F, m_top = -CUDART_INF_F;  // the reference, the largest logit
+      float l_run = 0.0f;                                  // this thread's tokens
       while (true) {
         const int s = w.g % kStages, sb = w.g & 1;
         ok = ok && wait(&misc->s_full[sb], (w.g >> 1) & 1);
@@ -761,19 +762,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = false;
           break;
         }
-        const float m_new =
-            fmaxf(fmaxf(m_run, fmaxf(mx, misc->xmax[sb][part ^ 1][r])),
-                  fmaxf(misc->xmax[sb][part ^ 2][r], misc->xmax[sb][part ^ 3][r]));
+        const float m_tile = fmaxf(fmaxf(mx, misc->xmax[sb][part ^ 1][r]),
+                                   fmaxf(misc->xmax[sb][part ^ 2][r], misc->xmax[sb][part ^ 3][r]));
         float alpha = 1.0f;
         bool rescale = false;
-        if (m_new > m_run + kRescale || (w.first && m_new > -CUDART_INF_F)) {
-          // (e4m3: P' of 2^5 at the maximum, 2^8 at most)
-          const float ref = kFp8 ? m_new - kRefShift : m_new;
-          alpha = m_run == -CUDART_INF_F ? 0.0f : ex2_approx(m_run - ref);
-          l_run *= alpha;
-          m_run = ref;
-          rescale = live && !w.first;
+        if (kFp8) {
+          rescale = move_reference(m_tile, m_run, m_top, alpha);
+        } else if (m_tile > m_run + kRescale) {
+          alpha = m_run == -CUDART_INF_F ? 0.0f : ex2_approx(m_run - m_tile);
+          m_run = m_tile;
+          rescale = true;
         }
+        l_run *= alpha;
+        rescale = rescale && live && !w.first;
         // (a page that is not there has keys of 0: finite logits, and weights of 0)
         const float m_use = !there ? CUDART_INF_F : m_run == -CUDART_INF_F ? 0.0f : m_run;
         // P V of the tile before: O is rescaled behind it, and it has read the
@@ -804,8 +805,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           // two-term sums of P' = u sigma: hi to 4 significant bits in integers
           // (converting a code back takes three conversions a pair, at an eighth
           // of the rate; a product and two differences are fused into hi = P'),
-          // lo what is left.  Below 2^-6, where codes are multiples of 2^-9, the
-          // sum is off by 2^-9 at most -- 2^-14 of the row's largest.
+          // lo what is left.  Off by 2^-8 of P' at most from 2^-1 up, by 2^-9
+          // below, where codes are multiples of that (move_reference).
           ulonglong2 sg;
           uint32_t hi4[8], lo4[8];
 #pragma unroll
