@@ -161,7 +161,7 @@ mla_status partial_launch(const void* q, const mla_kv_pages* kv, const int32_t* 
                           int shard_id, int num_shards, mla_layout layout, float* out_partial,
                           float* lse_partial, void* workspace, size_t workspace_bytes,
                           void* stream, Launched* L, RankIo rio = RankIo{0, 1, 0, 0},
-                          Plan plan = Plan(), float ref_shift = 0.0f) {
+                          Plan plan = Plan()) {
   if (!q || !kv || !block_table || !seq_lens || !out_partial || !lse_partial) return MLA_ERR_INVALID;
   if (!shape_ok(shape)) return MLA_ERR_INVALID;
   if (num_shards < 1 || num_shards > kMaxShards) return MLA_ERR_INVALID;
@@ -381,7 +381,6 @@ mla_status partial_launch(const void* q, const mla_kv_pages* kv, const int32_t* 
   p.q = static_cast<const uint16_t*>(q);
   p.timeout_ns = host::wait_budget_ns(kTimeoutNs);
   p.withhold_query = host::g_withhold_query.load();
-  p.ref_shift = ref_shift;
 
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (plan(pd, p.hdr, p.prefix, grid, kMinTilesPerCta, fp8 ? kUnitCostFp8 : kUnitCost, st) !=
@@ -683,8 +682,7 @@ mla_status mla_prefix_partial(const void* q, const mla_kv_pages* kv, const int32
           int unit_cost, cudaStream_t s) {
         return prefix::launch_prep(p, fp8, pairs,
                                    prefix::OwnPlan{pd, hdr, positions, grid, min_tiles, unit_cost}, s);
-      },
-      prefix::kRefShift);
+      });
   if (st != MLA_OK) return st;
   const prefix::OwnPieces own{L.pd, L.hdr, L.prefix, L.ws_o, L.ws_lse, own_out, own_lse, L.num_units};
   // (not where no lengths could make sharing worth it)

@@ -19,11 +19,12 @@
 //     them exchange halves by shuffle; an M=64 MMA would cost the tensor core
 //     as much as an M=128 one.
 //   - the probabilities: with sigma_t = mant_t * 2^E_t (mant in [0.5, 1)),
-//     the softmax keeps its running max over b_t = a_t + E_t, where a_t is
-//     the log2-domain logit, so that P'_t = 2^(a_t - m) * sigma_t =
-//     2^(b_t - m) * mant_t is at most 2^8; P'_t carries the value scale, and
-//     the normaliser sums u_t = 2^(a_t - m).  P' = hi + lo as above
-//     (relative error about 2^-8, like a bf16 P), and O^T += V^T P'^T is two
+//     the softmax keeps a reference m near the maxima of b_t = a_t + E_t,
+//     where a_t is the log2-domain logit, so that P'_t = 2^(a_t - m) * sigma_t
+//     = 2^(b_t - m) * mant_t is below 448 and a tile's largest 2^-3 or more
+//     (move_reference); P'_t carries the value scale, and the normaliser sums
+//     u_t = 2^(a_t - m).  P' = hi + lo as above: off by 2^-8 of itself at most
+//     from 2^-1 up, like a bf16 P, by 2^-10 below.  O^T += V^T P'^T is two
 //     accumulating MMAs per 32-token step.
 // The tensor cores accumulate in fp32.
 //
@@ -86,7 +87,6 @@ constexpr int kConvThreads = 128;           // softmax group 1 splits the query
 constexpr uint32_t kBarSoftmax = 1;         // all softmax threads
 constexpr uint32_t kBarGroup0 = 2;          // group k: kBarGroup0 + k
 constexpr uint32_t kBarConv = 4;            // the query split (group 1)
-constexpr float kRescaleThreshold = 8.0f;  // log2 units: 2^(b_t - m) <= 2^8 keeps P' inside e4m3
 constexpr int kPrefetch = 2;               // tiles of a piece prefetched into L2 ahead of the loads
 
 struct Misc {
@@ -583,7 +583,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the row's query scale and the softmax scale, in log2 units
       const float qs = misc->qinv[r] * pd.scale_log2;
       int unit_left = 0;   // tiles of the current QK^T unit still to read
-      float m_run = -CUDART_INF_F, l_run = 0.0f;   // l_run: sum of u_t over this thread's tokens
+      float m_run = -CUDART_INF_F, m_top = -CUDART_INF_F;   // the reference, the largest b_t
+      float l_run = 0.0f;                          // sum of u_t over this thread's tokens
       for (int j = t0; j < t1; ++j, ++gt) {
         const int sb = qu & 1, st = gt & (kStages - 1);
         bool ok_s = ok;
@@ -667,21 +668,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         // thread's wait failed
         if (named_bar_or(kBarSoftmax, kSoftmaxThreads, !ok_s)) { ok = false; break; }
         const float m_tile = fmaxf(mx, misc->xmax[gt & 1][grp ^ 1][r]);
-        const float m_new = fmaxf(m_run, m_tile);
-        float alpha = 1.0f;
-        bool resc = false;
-        if (m_new > m_run + kRescaleThreshold || (j == t0 && m_new > -CUDART_INF_F)) {
-          const float ref = m_new - p.ref_shift;
-          alpha = (m_run == -CUDART_INF_F) ? 0.0f : ex2_approx(m_run - ref);
-          l_run *= alpha;
-          m_run = ref;
-          resc = owner && (j != t0);
-        }
+        float alpha;
+        const bool resc = move_reference(m_tile, m_run, m_top, alpha) && owner && j != t0;
+        l_run *= alpha;
         if (owner && half == 0) misc->alpha[grp][r] = alpha;
         bool waited_pv = false;
         // both groups see the same maxima, so they take the same decision
         if (named_bar_or(kBarGroup0 + grp, 128, resc)) {
-          // some row's running max grew: rescale this group's half of O^T
+          // some row's reference moved: rescale this group's half of O^T
           // (latent blocks 2 grp, 2 grp + 1) once the previous P.V landed
           const bool ok_pv = __all_sync(
               0xffffffffu, (gt == 0) || mbar_wait(b_pv_done + 8 * ((gt - 1) & 1),

@@ -8,7 +8,6 @@ namespace prefix {
 
 constexpr int kPairRows = 128;   // query rows of a CTA pair (64 per CTA)
 constexpr long long kMinGain = 12000;   // ns that sharing has to save
-constexpr float kRefShift = 5.0f;   // e4m3: PartialParams::ref_shift
 
 struct Params {
   int B, q_len, H, R;            // R = q_len * H rows per request

@@ -134,3 +134,72 @@ def test_shared_prefix_far_below_its_first_token():
     c = Cache(4096, {0: 970.0}, 0.5, spare=B + 2)
     part, lse = prefix_call(c, c.query(B, Q, H), 1)
     assert (part.double() - 0.5).abs().max().item() <= 2.0 ** -8
+
+
+def decode(c, q, shards=1, layout="interleaved", seq=None, **kw):
+    table = c.table.expand(q.shape[0], -1).contiguous()
+    seq = i32([c.n] * q.shape[0]) if seq is None else seq
+    part, lse, ws = mla.mla_decode_partial(q, c.kv, table, seq, shards, layout, kv_scale=c.scale, **kw)
+    out, lse_out = mla.mla_shard_combine(part, lse)
+    assert mla.mla_get_device_error(ws) == 0
+    return (part[0], lse[0]) if shards == 1 else (out, lse_out)
+
+
+@pytest.mark.parametrize("n,heavy,value", CASES)
+def test_per_request(n, heavy, value):
+    c = Cache(n, heavy, value, seed=n)
+    q = c.query(B, Q, H)
+    part, lse = decode(c, q)
+    close(some(part), some(lse), some(q), c.tokens(), len(heavy))
+
+
+@pytest.mark.parametrize("layout", ["interleaved", "contiguous"])
+def test_a_sharded_step(layout):
+    # four shards of 40 requests; the combine's output is rounded to bf16
+    c = Cache(20000, {0: 11.0, 7000: 10.0}, 0.0, seed=1)
+    q = c.query(40, 1, H)
+    out, lse, ws = mla.mla_decode_step(q, c.kv, c.table.expand(40, -1).contiguous(), i32([c.n] * 40), 4, layout,
+                                       kv_scale=c.scale)
+    assert mla.mla_get_device_error(ws) == 0
+    q, out, lse = (x[:, :, ::24].contiguous() for x in (q, out, lse))
+    close(out, lse, q, c.tokens(), 2)
+
+
+def test_per_request_far_below_its_first_token():
+    c = Cache(4096, {0: 970.0}, 0.5)
+    part, lse = decode(c, c.query(B, Q, H))
+    assert (part.double() - 0.5).abs().max().item() <= 2.0 ** -8
+
+
+def test_masks_that_cut_the_tail():
+    # each query token of a causal step sees its own share of the tail, which
+    # starts inside a tile; the padding rows' requests see nothing
+    c = Cache(16389, {0: 11.0}, 0.0, seed=3)
+    q = c.query(B, Q, H)
+    new = [8, 1, 3, 8, 5, 2, 8, 7, 4, 6]
+    part, lse = decode(c, q, causal=True, q_lens=i32(new))
+    K = c.tokens()
+    for b in (1, 2, 4):
+        for i in range(new[b]):
+            last = c.n - new[b] + i + 1
+            close(part[b, i, 5::24], lse[b, i, 5::24], q[b, i, 5::24], K[:last])
+        assert (part[b, new[b]:] == 0).all() and torch.isneginf(lse[b, new[b]:]).all()
+
+
+def test_logits_of_three_nats_deviation():
+    # wide logits without a heavy token: tiles' maxima go up and down by 2^10.
+    # Values are independent and of mean 0, so |O| is |v| sqrt(sum p^2), and weights
+    # off by 2^-8 of themselves at most turn it by 2^-8 of that; as much again for
+    # the smaller ones of every tile.
+    g = torch.Generator(device=DEV).manual_seed(5)
+    c = Cache(16384, {0: 1.0}, 0.5, seed=5)
+    x = torch.randn(c.kv.shape, device=DEV, generator=g) * 100
+    c.kv = x.clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+    K = c.tokens()
+    q = torch.randn((B, Q, H, 576), device=DEV, generator=g)
+    q = (q * (3 / (SCALE * K.std() * math.sqrt(576)))).to(torch.bfloat16)
+    part, lse = decode(c, q)
+    part, lse, q = some(part), some(lse), some(q)
+    ref, ref_lse = expect(q, K)
+    assert ((part.double() - ref).norm(dim=-1) / ref.norm(dim=-1)).max().item() <= 2.0 ** -7
+    assert (lse.double() - ref_lse).abs().max().item() <= 1e-3
