@@ -82,6 +82,12 @@ __device__ __forceinline__ int queries(const Params& p, int b) {
   return p.q_lens != nullptr ? min(max(p.q_lens[b], 0), p.q_len) : p.q_len;
 }
 
+// A context longer than its table is cut at the table's end, for what is shared as
+// for the own tokens.
+__device__ __forceinline__ int context(const Params& p, int b) {
+  return (int)min((long long)p.seq_lens[b], (long long)p.max_pages * kPage);
+}
+
 // Whether the groups are consecutive ranges that cover the batch (whole block).
 __device__ __forceinline__ bool groups_ok(const Params& p) {
   bool ok = true;
@@ -112,7 +118,7 @@ struct Group {
 __device__ __forceinline__ Group measure(const Params& p, bool ok, int g, int b0, int b1) {
   Group x{ok ? min(p.prefix_lens[g] / kPage, p.max_pages) : 0, 0, 0};
   for (int b = b0 + (int)(threadIdx.x & 31); b < b1; b += 32) {
-    const int L = p.seq_lens[b], n = queries(p, b), seen = p.causal ? L - n + 1 : L;
+    const int L = context(p, b), n = queries(p, b), seen = p.causal ? L - n + 1 : L;
     x.pages = min(x.pages, seen / kPage);
     x.runs += n * p.H / 16;
     x.units += ceil_div(n * p.H, kRows);
@@ -158,11 +164,6 @@ __device__ __forceinline__ bool survey(const Params& p, bool ok, F&& f) {
   }
   __syncthreads();
   return p.always || gain > (unsigned long long)kMinGain;
-}
-
-// A context longer than its table is cut at the table's end.
-__device__ __forceinline__ int context(const Params& p, int b) {
-  return (int)min((long long)p.seq_lens[b], (long long)p.max_pages * kPage);
 }
 
 // Block 0: units and their split.  Block 1: the own tokens' lengths, and the

@@ -270,6 +270,21 @@ def test_bad_pages_and_long_contexts_are_reported():
     assert mla.mla_get_device_error(ws) == -5
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("share", [True, False])
+def test_contexts_longer_than_their_table_are_cut_alike(share, fp8):
+    # what a row sees does not hang on what is shared: the context ends at the
+    # table's end, and with it the rows of a causal step
+    b = Batch([4], [640], [0, 0, 0, 0], q_len=5, H=64, fp8=fp8, seed=4)
+    want = b.expect()
+    b.prefix = i32([900])
+    for seq in ([740] * 4, [645, 640, 1 << 30, 640]):
+        b.seq = i32(seq)
+        mla.mla_set_prefix_sharing(share)
+        _, lse, _ = check(b, error=-5, want=want)
+        assert all(in_slice_0(lse)) == share
+
+
 def test_infinite_query_over_an_e4m3_prefix():
     b = Batch([4], [640], [40, 3, 70, 1], q_len=2, H=64, fp8=True, q_lens=[2, 1, 2, 1], seed=4)
     b.q[1, 1] = math.inf                        # padding
