@@ -668,7 +668,7 @@ mla_status mla_attention_weights(const void* q, const mla_kv_pages* kv, const in
  *                    entries behind a request's new pages are not read
  *   new_seq_lens     int32 [B]: n_b; not seq_lens, keep or keep_first itself
  *   kept             int32 [B, max_keep]: positions in the old context, ascending;
- *                    -1 from n_b on
+ *                    -1 from n_b on (max_keep at most 2^30)
  *   weights_out      fp32 [B, max_keep] or NULL: the kept tokens' weights; entries
  *                    from n_b on are left as they were; not in weights
  * The new pages are pages that no context uses, each in one place of

@@ -442,8 +442,9 @@ extern "C" mla_status mla_cache_evict(const mla_kv_pages* kv, const int32_t* blo
   if (kv->page_size != kPage) return MLA_ERR_UNSUPPORTED;
   if (workspace == nullptr || !host::aligned16(workspace) || workspace_bytes < sizeof(WsHeader))
     return MLA_ERR_WORKSPACE;
-  // candidates are indexed in 32 bits, with a cluster's rounding behind them
-  if (weights_width > (1 << 30)) return MLA_ERR_UNSUPPORTED;
+  // candidates and kept positions are indexed in 32 bits, with a cluster's rounding
+  // behind them
+  if (weights_width > (1 << 30) || max_keep > (1 << 30)) return MLA_ERR_UNSUPPORTED;
   // read by every CTA while another writes
   const size_t row = sizeof(int32_t) * batch;
   if (evict::overlap(seq_lens, row, new_seq_lens, row) ||

@@ -42,6 +42,13 @@ def test_eviction_refusals(kw, want):
     assert evict(**kw) == want
 
 
+@pytest.mark.parametrize("mk", [(1 << 30) + 1, (1 << 31) - 16384, (1 << 31) - 1])
+def test_eviction_refuses_more_positions_than_it_indexes(mk):
+    # a position and a cluster's step have to fit 32 bits
+    assert evict(B=1, mk=mk, nmp=1 << 25, wo=None) == UNSUPPORTED
+    assert evict(B=1, mk=1 << 30, nmp=1 << 25, wo=None, ws=None) == WORKSPACE
+
+
 def weights(q=512, data=512, scale=None, dtype=0, pages=4, page=64, bt=512, mp=4, sl=512,
             shape=(2, 1, 16, 0, 0.07, None), lse=512, before=None, bs=0, out=65536, os_=256, width=256,
             ws=512, wb=1 << 30):
