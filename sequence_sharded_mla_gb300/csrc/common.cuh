@@ -119,24 +119,27 @@ struct PartialParams {
 // ref + 8.75; outside, the reference moves, and what was summed up is scaled (in
 // fp32, which has the range).  A tile 2^-30 below the largest logit moves nothing:
 // a million of its tokens weigh 2^-10 of that one.
-// A token is then off by 2^-9 where its tile's largest is 2^-3 at least: what a
-// token far above the others of its tile costs those, 2^-7 of its own weight if
-// all 128 are off one way, is all that is lost.
+// A token is then off by 2^-9 at most where its tile's largest is 2^-3 at least: a
+// tail of like tokens by 2^-6 of itself at worst, 2^-8 where the reference was set
+// by it.  A token far above the others of its own tile can cost those up to 2^-6
+// of its weight together, if all are off one way.
 // A larger tile moves the reference only as far as it has to (ref + 8): the tiles
 // behind it are smaller again.  (Four requests of up to a million tokens, logits of
 // 1.7 nats' deviation: 0.256 ms, as with a running maximum; 0.260 if every move
 // leads to ref + 5, which some row of 64 then outgrows in a tile out of five.)
-constexpr float kRefHigh = 8.75f, kRefUp = 8.0f, kRefSet = 5.0f, kRefLow = -2.0f, kRefDeep = 30.0f;
+constexpr float kRefHigh = 8.75f, kRefUp = 8.0f, kRefLow = -2.0f, kRefDeep = 30.0f;
 
 // Takes in a tile whose largest logit is m_tile (log2 units; -inf: none): true if
-// the reference moved, and what was summed up is to be scaled by alpha.  `top`: the
-// largest so far.  Both start at -inf.
-__device__ __forceinline__ bool move_reference(float m_tile, float& ref, float& top, float& alpha) {
+// the reference moved, and what was summed up is to be scaled by alpha.  `set`: where
+// the first tile and one that lowers it come to lie.  `top`: the largest so far.
+// Both start at -inf.
+__device__ __forceinline__ bool move_reference(float m_tile, float set, float& ref, float& top,
+                                               float& alpha) {
   const bool up = m_tile > ref + kRefHigh;
   const bool move = up || (m_tile < ref + kRefLow && m_tile > top - kRefDeep);
   alpha = 1.0f;
   if (move) {
-    const float to = m_tile - (up && ref != -CUDART_INF_F ? kRefUp : kRefSet);
+    const float to = m_tile - (up && ref != -CUDART_INF_F ? kRefUp : set);
     alpha = ref == -CUDART_INF_F ? 0.0f : ex2_approx(ref - to);
     ref = to;
   }

@@ -87,6 +87,11 @@ constexpr int kConvThreads = 128;           // softmax group 1 splits the query
 constexpr uint32_t kBarSoftmax = 1;         // all softmax threads
 constexpr uint32_t kBarGroup0 = 2;          // group k: kBarGroup0 + k
 constexpr uint32_t kBarConv = 4;            // the query split (group 1)
+// What a new or lowered reference leaves the tile at: of 64 rows, one outgrows 2^5
+// in many tiles where logits vary (four requests of 256k tokens, logits of 1, 1.7
+// and 2.5 nats' deviation: 182, 201, 231 us; from 2^5 191, 212, 235; a running
+// maximum alone, which loses tails, 181, 183, 197).
+constexpr float kRefSet = 3.0f;
 constexpr int kPrefetch = 2;               // tiles of a piece prefetched into L2 ahead of the loads
 
 struct Misc {
@@ -669,7 +674,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (named_bar_or(kBarSoftmax, kSoftmaxThreads, !ok_s)) { ok = false; break; }
         const float m_tile = fmaxf(mx, misc->xmax[gt & 1][grp ^ 1][r]);
         float alpha;
-        const bool resc = move_reference(m_tile, m_run, m_top, alpha) && owner && j != t0;
+        const bool resc = move_reference(m_tile, kRefSet, m_run, m_top, alpha) && owner && j != t0;
         l_run *= alpha;
         if (owner && half == 0) misc->alpha[grp][r] = alpha;
         bool waited_pv = false;

@@ -74,6 +74,7 @@ constexpr int kUnitCost = 3;
 constexpr int kMinTiles = 2;
 constexpr uint32_t kBarRows = 2;             // named barriers 2, 3: the warps of the same rows
 constexpr float kRescale = 8.0f;             // log2 units
+constexpr float kRefSet = 5.0f;              // e4m3: what a new reference leaves a tile at
 constexpr uint32_t kTmemCols = 512, kColS = 0, kColO = 256;
 constexpr int kQBytes = kTileBytes;          // 73728, either type
 
@@ -768,7 +769,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float alpha = 1.0f;
         bool rescale = false;
         if (kFp8) {
-          rescale = move_reference(m_tile, m_run, m_top, alpha);
+          rescale = move_reference(m_tile, kRefSet, m_run, m_top, alpha);
         } else if (m_tile > m_run + kRescale) {
           alpha = m_run == -CUDART_INF_F ? 0.0f : ex2_approx(m_run - m_tile);
           m_run = m_tile;
