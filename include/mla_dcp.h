@@ -92,6 +92,10 @@ typedef enum mla_kv_dtype { MLA_KV_BF16 = 0, MLA_KV_FP8_E4M3 = 1 } mla_kv_dtype;
  * power-of-two row scale (exact for components within 2^10 of the row's
  * largest; any finite bf16 value is accepted); an inf or NaN component of a
  * row that attends is reported as MLA_ERR_RANGE by mla_get_device_error.
+ * Probabilities times token scales are two-term e4m3 sums as well, under a
+ * reference that follows the logits tile by tile: off by 2^-8 of themselves
+ * near the largest of their tile (64 tokens; 128 behind a shared prefix), and lost
+ * only where they are 2^-7 of that or less at worst, 2^-12 mostly.
  * With causal != 0
  * (a speculative verify step of q_len = 1 + drafts tokens whose KV is the
  * last q_len entries of the cache), query i sees tokens t <= L - q_len + i. */
@@ -574,7 +578,11 @@ size_t mla_prefix_workspace_size(const mla_shape* shape, int num_groups, int max
  * made on the device from the lengths: whole pages of a prefix that every row of
  * the group sees are shared where that takes less time than attending them per
  * request (mla_set_prefix_sharing); prefix_lens below a page, 0 or negative share
- * nothing.
+ * nothing.  The alternative is mla_decode_step, which takes whole contexts and
+ * is a launch or two shorter: it is the faster call for few requests, short
+ * prefixes and verify steps behind some thousand shared tokens (two requests
+ * behind 1024 tokens 35 us, 36 here; 16 of 5 tokens behind three prefixes of
+ * 2000 to 16000 120, 122 here; 32 behind 114k 651, 444 here).
  *
  *   block_table, seq_lens, shape (q_lens, causal)  as in mla_decode_partial:
  *                 whole contexts, the prefix among them
@@ -582,7 +590,7 @@ size_t mla_prefix_workspace_size(const mla_shape* shape, int num_groups, int max
  *                 groups allowed); num_groups 1 .. B
  *   prefix_lens   device int32 [num_groups]
  * Whole-request caches; a DCP rank passes its slice's own lengths, with causal
- * 0 (one query token).
+ * 0 (one query token), and the combine takes two partials from each rank.
  *
  * workspace: mla_prefix_workspace_size bytes, which may hold anything and serve
  * one call at a time.  mla_get_device_error reads the last call's errors: as
@@ -626,7 +634,8 @@ size_t mla_attention_weights_workspace_size(const mla_shape* shape, mla_kv_dtype
  *   before  fp32 [B, width], before_stride floats between requests, or NULL
  *   out     fp32 [B, width], out_stride floats between requests; before itself
  *           (with its stride), or apart from it
- * Whole-request caches of either type, every num_heads that is a multiple of
+ * Whole-request caches of either type, not a rank's slice (whose last n_b
+ * tokens are not the step's new ones), every num_heads that is a multiple of
  * 16; width at least every L_b, at most 2^30.  Sums are fp32 in a fixed order.
  * A NaN in a cache row makes that token's weight NaN, a NaN lse every weight
  * of its request.  With an e4m3 cache the query is held as in
@@ -677,6 +686,13 @@ mla_status mla_attention_weights(const void* q, const mla_kv_pages* kv, const in
  * prefix), the page is left as it is and may be shared.  The same page with
  * rows that would move is reported as MLA_ERR_INVALID and not written.  Rows
  * behind a new context's end are left as they were, and so are the old pages.
+ * Where a new context ends inside such a page, the request's next append writes
+ * behind its last row there: a shared page that can be the last one needs a page
+ * of its own in new_block_table, into which its rows are then copied.
+ *
+ * The selection runs on 1 to 16 SMs a request, chosen by weights_width: rows
+ * much wider than the contexts cost time (16 contexts of 8000 tokens 14 us in
+ * rows of 8192, 44 in rows above 262144); pass the part that contexts reach.
  *
  * workspace: 256 bytes of device memory, zeroed once before its first use:
  * MLA_ERR_DEVICE_BOUNDS (a page outside [0, num_pages): its rows are not moved)

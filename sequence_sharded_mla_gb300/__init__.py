@@ -753,6 +753,9 @@ def mla_prefix_partial(q, kv, block_table, seq_lens, group_starts, prefix_lens, 
     prefix_lens: int32 [G] (device), the leading tokens that the group's
     contexts have in common, in the same pages of their block-table rows.  Which
     of them are shared (slice 0) is chosen on the device from the lengths.
+    mla_decode_step over whole contexts gives the same attention, and is the
+    faster call for few requests, short prefixes and verify steps behind some
+    thousand shared tokens.
     out_partial: fp32 [2, B, q_len, H, 512]; lse_partial: fp32 [2, B, q_len, H].
     """
     return _binding().prefix_partial(q, kv, kv_scale, block_table, seq_lens, group_starts, prefix_lens,
@@ -779,7 +782,8 @@ def mla_attention_weights(q, kv, block_table, seq_lens, lse, weights=None, out=N
     over its query rows and added to `weights`; returns (out, workspace).
 
     q, kv, kv_scale, block_table, seq_lens, causal, softmax_scale, q_lens: the
-    step's, as for mla_decode_step; lse: its lse_out, fp32 [B, q_len, H].
+    step's, as for mla_decode_step, over whole contexts (not a rank's slice);
+    lse: its lse_out, fp32 [B, q_len, H].
     weights: fp32 [B, W] of earlier steps (W at least every context; rows may be
     further apart), or None; the tokens that the step appended start from 0.
     out: weights itself, memory of its own of that shape, or None for a new
@@ -799,11 +803,14 @@ def mla_cache_evict(kv, block_table, seq_lens, weights, keep, new_block_table, k
     its `recent` newest, and the others with the largest weights (equal ones
     from the lowest position on).  Their rows move in order to the pages of
     new_block_table, which no context uses yet; leading pages of which every
-    row stays (a kept, shared prefix) may be those of block_table.
+    row stays (a kept, shared prefix) may be those of block_table.  A context
+    that ends inside such a page goes on in it: give it a page of its own there
+    if the page is shared.
 
     kv: bf16 or e4m3 codes [P, 64, 576] (written), with kv_scale fp32 [P, 64]
     (written) for codes.  weights: fp32 [B, W], W at least every context (rows
-    may be further apart).  keep, keep_first: int32 [B] (device).  kept: int32
+    may be further apart; weights[:, :longest] of a wider tensor takes less time
+    than all of it).  keep, keep_first: int32 [B] (device).  kept: int32
     [B, max_keep], the kept tokens' old positions, -1 behind them (default:
     room for new_block_table's pages); weights_out: fp32 [B, max_keep], their
     weights; new_seq_lens: int32 [B].  workspace: 256 bytes, zeroed before its

@@ -111,7 +111,7 @@ struct PartialParams {
 
 // The reference of an e4m3 cache's softmax: probabilities 2^(b - ref) times a
 // scale's mantissa are multiplied as sums of two e4m3 terms.  Those overflow from
-// 448 on, are off by 2^-8 of themselves at most down to 2^-1 and by up to 2^-9 below
+// 448 on, are off by 2^-8 of themselves at most down to 2^-2 and by up to 2^-9 below
 // that, and vanish below 2^-10.  So the reference follows what is being added, not
 // only the maximum: a running maximum alone left a tail of 64k tokens 11 nats
 // below one heavy token out of the output altogether, half of its weight, while

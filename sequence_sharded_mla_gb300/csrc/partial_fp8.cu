@@ -24,7 +24,7 @@
 //     = 2^(b_t - m) * mant_t is below 448 and a tile's largest 2^-3 or more
 //     (move_reference); P'_t carries the value scale, and the normaliser sums
 //     u_t = 2^(a_t - m).  P' = hi + lo as above: off by 2^-8 of itself at most
-//     from 2^-1 up, like a bf16 P, by 2^-10 below.  O^T += V^T P'^T is two
+//     from 2^-2 up, like a bf16 P, by 2^-10 below.  O^T += V^T P'^T is two
 //     accumulating MMAs per 32-token step.
 // The tensor cores accumulate in fp32.
 //

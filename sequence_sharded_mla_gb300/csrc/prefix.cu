@@ -807,7 +807,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // two-term sums of P' = u sigma: hi to 4 significant bits in integers
           // (converting a code back takes three conversions a pair, at an eighth
           // of the rate; a product and two differences are fused into hi = P'),
-          // lo what is left.  Off by 2^-8 of P' at most from 2^-1 up, by 2^-9
+          // lo what is left.  Off by 2^-8 of P' at most from 2^-2 up, by 2^-9
           // below, where codes are multiples of that (move_reference).
           ulonglong2 sg;
           uint32_t hi4[8], lo4[8];
@@ -851,7 +851,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t pk[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            // bf16: P is rounded to 8 bits, relative 2^-9, as in the
+            // bf16: P is rounded to 8 bits, relative 2^-8, as in the
             // per-request kernel; its sum is taken before the rounding
             const float2 x = unpack2(fma2(a[i], qs2, m2));
             const float2 u = make_float2(ex2_approx(x.x), ex2_approx(x.y));

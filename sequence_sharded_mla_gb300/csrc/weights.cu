@@ -138,7 +138,7 @@ struct Cfg {
   static constexpr int kKBytes = kTokens / 8 * kKGroup;    // 72 or 48 KB
   static constexpr int kQBytes = kN * kLine;               // Q chunk: 8 or 16 KB
   // with more than 64 rows the query's chunks stream (one tile of e4m3 keys and
-  // nine chunks of the query in flight took 52 instead of 50 us for a 9-token step)
+  // nine chunks of the query in flight took 2 us more of a 9-token step's 54)
   static constexpr int kKDepth = kFp8 ? 2 : 3;
   static constexpr int kQDepth = kRowsN == 64 ? 9 : 4;
   static constexpr int kSmemQ = kKDepth * kKBytes;
