@@ -203,3 +203,27 @@ def test_logits_of_three_nats_deviation():
     ref, ref_lse = expect(q, K)
     assert ((part.double() - ref).norm(dim=-1) / ref.norm(dim=-1)).max().item() <= 2.0 ** -7
     assert (lse.double() - ref_lse).abs().max().item() <= 1e-3
+
+
+def test_a_step_behind_a_shared_prefix_is_the_step_alone():
+    # whole contexts, the heavy token in the shared part: both calls' outputs are
+    # rounded to bf16 (2^-8 of values of up to 80 / 64) on top
+    c = Cache(20032, {100: 10.0}, 0.0, spare=B + 2, seed=6)
+    q = c.query(B, Q, H)
+    used = set(c.table[0].tolist())
+    own = i32([p for p in range(c.kv.shape[0]) if p not in used][:B])
+    table = torch.cat((c.table.expand(B, -1), own[:, None]), 1).contiguous()
+    seq = i32([c.n + 9 + 5 * b for b in range(B)])
+    part, plse, ws = mla.mla_prefix_partial(q, c.kv, table, seq, i32([0, B]), i32([c.n]), kv_scale=c.scale)
+    assert mla.mla_get_device_error(ws) == 0 and not torch.isneginf(plse[0]).any()
+    both = [mla.mla_shard_combine(part, plse),
+            mla.mla_decode_step(q, c.kv, table, seq, 1, kv_scale=c.scale)[:2]]
+    for b in (0, 4, 9):
+        rows = torch.cat((c.rows, own[b].long() * PAGE + torch.arange(int(seq[b]) - c.n, device=DEV)))
+        K = c.kv.view(-1, 576)[rows].view(torch.float8_e4m3fn).double() * c.scale.view(-1)[rows].double()[:, None]
+        x = q[b, ::3, 5::24].contiguous()
+        ref, ref_lse = expect(x, K)
+        for out, lse in both:
+            err = (out[b, ::3, 5::24].double() - ref).abs().max().item()
+            assert err <= tolerance(spread(x, K), 1) + 2.0 ** -8 * 80 / 64
+            assert (lse[b, ::3, 5::24].double() - ref_lse).abs().max().item() <= 1e-3
