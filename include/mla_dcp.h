@@ -675,11 +675,13 @@ mla_status mla_attention_weights(const void* q, const mla_kv_pages* kv, const in
  *   keep             int32 [B], 0 .. max_keep; keep_first int32 [B] or NULL
  *   new_block_table  int32 [B, new_max_pages], new_max_pages >= ceil(max_keep / 64);
  *                    entries behind a request's new pages are not read
- *   new_seq_lens     int32 [B]: n_b; not seq_lens, keep or keep_first itself
+ *   new_seq_lens     int32 [B]: n_b
  *   kept             int32 [B, max_keep]: positions in the old context, ascending;
  *                    -1 from n_b on (max_keep at most 2^30)
  *   weights_out      fp32 [B, max_keep] or NULL: the kept tokens' weights; entries
- *                    from n_b on are left as they were; not in weights
+ *                    from n_b on are left as they were
+ * The three outputs share memory with each other and with the other arrays
+ * nowhere (MLA_ERR_INVALID).
  * The new pages are pages that no context uses, each in one place of
  * new_block_table, but for leading ones: where new_block_table[b][i] is
  * block_table[b][i] and the rows of page i all keep their place (a kept

@@ -367,10 +367,14 @@ __global__ void __launch_bounds__(kCopyThreads) evict_copy_kernel(Copy p) {
   }
 }
 
-// Whether the bytes [a, a + n) and [b, b + m) meet.
-inline bool overlap(const void* a, size_t n, const void* b, size_t m) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return x < y + m && y < x + n;
+// Bytes of an array, or null.
+struct Span {
+  const void* p;
+  size_t n;
+};
+inline bool overlap(const Span& a, const Span& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return a.p != nullptr && b.p != nullptr && x < y + b.n && y < x + a.n;
 }
 
 // CTAs per request, by the width of the weights.  A whole eviction to a quarter
@@ -445,15 +449,24 @@ extern "C" mla_status mla_cache_evict(const mla_kv_pages* kv, const int32_t* blo
   // candidates and kept positions are indexed in 32 bits, with a cluster's rounding
   // behind them
   if (weights_width > (1 << 30) || max_keep > (1 << 30)) return MLA_ERR_UNSUPPORTED;
-  // read by every CTA while another writes
-  const size_t row = sizeof(int32_t) * batch;
-  if (evict::overlap(seq_lens, row, new_seq_lens, row) ||
-      evict::overlap(keep, row, new_seq_lens, row) ||
-      (keep_first != nullptr && evict::overlap(keep_first, row, new_seq_lens, row)) ||
-      (weights_out != nullptr &&
-       evict::overlap(weights, sizeof(float) * ((batch - 1) * (size_t)weights_stride + weights_width),
-                      weights_out, sizeof(float) * (size_t)batch * max_keep)))
-    return MLA_ERR_INVALID;
+  // inputs are read by every CTA while another writes, and the copy takes the
+  // lengths and positions of the selection for indexes
+  const size_t row = sizeof(int32_t) * (size_t)batch;   // of 4-byte values, one a request
+  const evict::Span in[] = {
+      {seq_lens, row},
+      {keep, row},
+      {keep_first, row},
+      {weights, sizeof(float) * ((batch - 1) * (size_t)weights_stride + weights_width)},
+      {block_table, row * max_pages_per_req},
+      {new_block_table, row * new_max_pages}};
+  const evict::Span out[] = {
+      {new_seq_lens, row}, {kept, row * max_keep}, {weights_out, row * max_keep}};
+  for (int i = 0; i < 3; ++i) {
+    for (const evict::Span& x : in)
+      if (evict::overlap(out[i], x)) return MLA_ERR_INVALID;
+    for (int j = 0; j < i; ++j)
+      if (evict::overlap(out[i], out[j])) return MLA_ERR_INVALID;
+  }
   if ((long long)batch * pages >= (1LL << 31) || (long long)batch * 16 >= (1LL << 31))
     return MLA_ERR_INVALID;
   unsigned* err = &static_cast<WsHeader*>(workspace)->err;

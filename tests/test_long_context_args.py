@@ -49,6 +49,22 @@ def test_eviction_refuses_more_positions_than_it_indexes(mk):
     assert evict(B=1, mk=1 << 30, nmp=1 << 25, wo=None, ws=None) == WORKSPACE
 
 
+@pytest.mark.parametrize("kw", [
+    dict(kept=8192), dict(kept=8196), dict(kept=8192 - 1020), dict(kept=65536), dict(kept=65536 + 1020),
+    dict(wo=8196), dict(wo=8192 - 1020), dict(kept=512), dict(kept=1024), dict(kept=2000), dict(kept=4096),
+    dict(kept=4096 + 4), dict(wo=4100), dict(new=4096 + 28), dict(wo=600), dict(kept=16384 + 12),
+    dict(wo=16384), dict(new=16384 + 12), dict(first=900000, kept=900000 + 4), dict(kept=3244),
+])
+def test_eviction_refuses_outputs_in_other_arrays(kw):
+    # block_table 4096 .. 4128, new_block_table 16384 .. 16400, weights 1024 .. 3248,
+    # kept and weights_out of 1024 bytes, new_seq_lens 8192 .. 8200
+    apart = dict(bt=4096, nbt=16384, sl=512, keep=520, w=1024, new=8192, kept=32768, wo=65536)
+    assert evict(**{**apart, **kw}) == INVALID
+    # next to each other is apart
+    ends = dict(apart, kept=8200, wo=8200 + 1024, new=8192, ws=None)
+    assert evict(**ends) == WORKSPACE
+
+
 def weights(q=512, data=512, scale=None, dtype=0, pages=4, page=64, bt=512, mp=4, sl=512,
             shape=(2, 1, 16, 0, 0.07, None), lse=512, before=None, bs=0, out=65536, os_=256, width=256,
             ws=512, wb=1 << 30):
